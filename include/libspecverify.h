@@ -20,7 +20,9 @@
  *   sv_adapt_gamma    each request's next draft length from its own
  *                     acceptance history;
  *   sv_select_chunk   the chunk size of least expected cost for the next
- *                     chunked step.
+ *                     chunked step;
+ *   sv_reserve_kv     blocks for a step's rows taken from the pool, their
+ *                     cache slots and positions (sv_commit_kv's counterpart).
  *
  * Sources (pages by title; section names glossed):
  *   [SwiftSpec] "SwiftSpec: 드래프터와 타깃을 서로 다른 GPU에 분리하고 비동기로
@@ -91,6 +93,7 @@ typedef enum {
 #define SV_DEV_BAD_TOKEN 32      /* draft token outside [0, vocab) */
 #define SV_DEV_UNSUPPORTED 64    /* reserved (no longer raised: trees at temperature > 0 are sampled) */
 #define SV_DEV_BAD_LENGTH 128    /* ctx + rows does not fit the block table */
+#define SV_DEV_POOL_EMPTY 256    /* the pool has too few free blocks for a request */
 
 /* Paged KV cache ([SSD] PagedAttention; [SwiftSpec] mechanism 2).
  * k_cache, v_cache: bf16 [num_blocks][n_kv_heads][block_size][head_dim];
@@ -416,6 +419,39 @@ sv_status sv_adapt_gamma(int32_t n_req, const int32_t* accepted_len, const int32
                          double* state, int32_t* gamma_next, double decay, double overhead,
                          int32_t gamma_min, int32_t gamma_max, int32_t* dev_status,
                          void* stream);
+
+/* --------------------------------------------------------------- reserve --
+ * The counterpart of the commit's release ([SwiftSpec] mechanism 2; [SSD]
+ * PagedAttention): before a step's rows are staged, request i needs the
+ * table entries t in [floor(ctx_i / 16), ceil((ctx_i + rows_i) / 16)).  Those
+ * that are -1 are new (they must be the last of the range: entries in use
+ * come first, and the block of a partly filled page must be there).  With n_i
+ * new entries and S_i = n_0 + .. + n_i over the well-formed requests, request
+ * i is served iff n_i == 0 or S_i <= *free_count: requests are served in
+ * order, whole, and once one does not fit no later one takes a block.  New
+ * block k of the call (k from 0, in (request, table index) order) is
+ * free_list[*free_count - 1 - k]; *free_count drops by the blocks taken.
+ * Outputs:
+ *   kv->block_tables: the new entries of served requests;
+ *   taken [n_req]: new blocks of the request, -1 if it was not served;
+ *   slots [total_rows]: cache slot block * 16 + offset of the row's staged
+ *     K/V (slot ctx_i + j), -1 if its request was not served;
+ *   positions (nullable) [total_rows]: ctx_i + pos_offset_i + the node's
+ *     depth (for a tree two siblings share a position, not a slot), -1 where
+ *     slots is -1.  pos_offset (nullable): int32 [n_req].
+ * Packed rows of no request (behind cu_rows[n_req]) get -1 in both.  A
+ * request that is malformed (SV_DEV_BAD_WINDOW, BAD_LENGTH, BAD_BLOCK_ID,
+ * BAD_PARENT) or does not fit (SV_DEV_POOL_EMPTY) is left as it was; a
+ * free-list entry that is no block id is dropped with SV_DEV_BAD_BLOCK_ID
+ * (its table entry stays -1, its rows get slot -1).  Row windows and
+ * verify_len are ignored, as the commit ignores them.
+ * batch->parent may be NULL here: every request is a chain, of any length
+ * (a prompt); max_rows_per_req is then not limited to 128.  batch->tokens and
+ * kv->k_cache / v_cache are not read.
+ * Supported: block_size 16, n_req <= 8192, fewer than 2^27 blocks. */
+sv_status sv_reserve_kv(const sv_paged_kv* kv, const sv_batch* batch, const sv_block_pool* pool,
+                        const int32_t* pos_offset, int32_t* slots, int32_t* positions,
+                        int32_t* taken, int32_t* dev_status, void* stream);
 
 /* ------------------------------------------------------------ self test --
  * Every wait inside the library's kernels (on an mbarrier a TMA copy or a

@@ -1,0 +1,69 @@
+"""CPU oracle of a verification step's two edges: block reservation, in plain Python and numpy fp64, one row after the
+other.  TEST INFRASTRUCTURE ONLY, like the rest of this package.
+"""
+
+from __future__ import annotations
+
+import numpy as np
+
+PAGE = 16
+BAD_BLOCK, BAD_PARENT, BAD_WINDOW, BAD_LENGTH = 1, 2, 8, 128
+POOL_EMPTY, BAD_SLOT, BAD_PARAM, EMPTY_MASK = 256, 512, 1024, 2048
+
+
+def _depths(parent):
+    """Depth of every node, or None if the parents are not topological."""
+    depth = []
+    for j, p in enumerate(parent):
+        if (j == 0 and p != -1) or (j > 0 and not 0 <= p < j):
+            return None
+        depth.append(0 if j == 0 else depth[p] + 1)
+    return depth
+
+
+def reserve(cu, parent, ctx, tables, free_list, free_count, num_blocks, max_rows, total_rows,
+            pos_offset=None):
+    """(err, state) of sv_reserve_kv; the arrays given are not changed."""
+    tables = np.array(tables, dtype=np.int32)
+    R, width = tables.shape
+    slots = np.full(total_rows, -1, np.int32)
+    positions = np.full(total_rows, -1, np.int32)
+    taken = np.full(R, -1, np.int32)
+    err, asked, left = 0, 0, int(free_count)
+    for i in range(R):
+        c0, c1, n = int(cu[i]), int(cu[i + 1]), int(cu[i + 1]) - int(cu[i])
+        if n < 1 or n > max_rows or c0 < 0 or c1 > total_rows:
+            err |= BAD_WINDOW
+            continue
+        if ctx[i] < 0 or ctx[i] + n > width * PAGE:
+            err |= BAD_LENGTH
+            continue
+        depth = list(range(n)) if parent is None else _depths([int(p) for p in parent[c0:c1]])
+        t0, t1 = int(ctx[i]) // PAGE, -(-(int(ctx[i]) + n) // PAGE)
+        part = tables[i, t0:t1]
+        new = [t for t in range(t0, t1) if tables[i, t] == -1]
+        bad = bool((part < -1).any() or (part >= num_blocks).any())
+        bad |= bool(ctx[i] % PAGE and part[0] == -1)
+        bad |= bool(new) and new != list(range(t1 - len(new), t1))
+        err |= BAD_BLOCK if bad else 0
+        err |= BAD_PARENT if depth is None else 0
+        if bad or depth is None:
+            continue
+        asked += len(new)
+        if new and asked > free_count:
+            err |= POOL_EMPTY
+            continue
+        taken[i] = len(new)
+        for t in new:
+            left -= 1
+            if 0 <= free_list[left] < num_blocks:
+                tables[i, t] = free_list[left]
+            else:
+                err |= BAD_BLOCK
+        for j in range(n):
+            block = tables[i, (ctx[i] + j) // PAGE]
+            if block >= 0:
+                slots[c0 + j] = block * PAGE + (ctx[i] + j) % PAGE
+                positions[c0 + j] = ctx[i] + depth[j] + (0 if pos_offset is None else pos_offset[i])
+    return err, {"tables": tables, "count": left, "slots": slots, "positions": positions,
+                 "taken": taken}

@@ -32,6 +32,7 @@ SV_DEV_TIMEOUT = 16
 SV_DEV_BAD_TOKEN = 32
 SV_DEV_UNSUPPORTED = 64
 SV_DEV_BAD_LENGTH = 128
+SV_DEV_POOL_EMPTY = 256
 
 SV_ACCEPT_STATIC_SCRATCH_BYTES = 4 << 20
 
@@ -77,6 +78,7 @@ PROTOTYPES = {
                                       P, P]),
     "sv_select_chunk": (ctypes.c_int, [I32, P, P, P, ctypes.c_double, ctypes.c_double, U64, P, P,
                                        P, P, P]),
+    "sv_reserve_kv": (ctypes.c_int, [P, P, P, P, P, P, P, P, P]),
     "sv_selftest_bounded_wait": (ctypes.c_int, [I32, P, P]),
 }
 

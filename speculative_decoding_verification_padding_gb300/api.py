@@ -31,6 +31,26 @@ def _expect(t: Optional[torch.Tensor], dtype, name):
         raise N.SpecVerifyError(f"{name} must be {dtype}, got {t.dtype}")
 
 
+def _at_least(t: Optional[torch.Tensor], n: int, name):
+    if t is not None and t.numel() < n:
+        raise N.SpecVerifyError(f"{name} must hold at least {n} elements, got {t.numel()}")
+
+
+def _one_device(*tensors) -> torch.device:
+    """The device of all the tensors, which must be the current one: a call
+    is launched there."""
+    devs = {t.device for t in tensors if t is not None}
+    if len(devs) != 1:
+        raise N.SpecVerifyError(f"tensors of one call live on {sorted(map(str, devs))}")
+    dev = devs.pop()
+    if dev.type != "cuda":
+        raise N.SpecVerifyError("libspecverify takes device tensors")
+    if dev.index != torch.cuda.current_device():
+        raise N.SpecVerifyError(f"tensors live on {dev}, the current device is "
+                                f"cuda:{torch.cuda.current_device()}")
+    return dev
+
+
 def _stream(stream) -> int:
     if stream is None:
         return torch.cuda.current_stream().cuda_stream
@@ -42,6 +62,9 @@ def _stream(stream) -> int:
 # The current stream's handle for a device index, without building a Stream
 # object (a few microseconds less per call on the launch path).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _current_stream(device_index: int) -> int:
@@ -62,15 +85,19 @@ class BoundCall:
     Batch / PagedKV / BlockPool objects must keep the same tensors: the
     call reads their pointers as they were when it was bound."""
 
-    __slots__ = ("_f", "_name", "_args", "_dev")
+    __slots__ = ("_f", "_name", "_args", "_dev", "_keep")
 
-    def __init__(self, name: str, args: tuple, device: torch.device):
+    def __init__(self, name: str, args: tuple, device: torch.device, keep=None):
         self._f = getattr(N.lib(), name)
         self._name = name
         self._args = args  # ctypes byref objects keep their structs alive
+        self._keep = keep  # what the call's tensors belong to, where the binder hands it over
         self._dev = device.index if device.index is not None else torch.cuda.current_device()
 
     def __call__(self, stream=None):
+        if _current_device() != self._dev:
+            raise N.SpecVerifyError(f"{self._name} is bound to cuda:{self._dev}, the current device "
+                                    f"is cuda:{_current_device()}")
         st = _current_stream(self._dev) if stream is None else _stream(stream)
         status = self._f(*self._args, st)
         if status != N.SV_OK:
@@ -81,7 +108,7 @@ class BoundCall:
 class Batch:
     """sv_batch: packed draft chains / trees (int32 device tensors)."""
     cu_rows: torch.Tensor
-    parent: torch.Tensor
+    parent: Optional[torch.Tensor]
     tokens: torch.Tensor
     max_rows: int
     row_begin: Optional[torch.Tensor] = None
@@ -94,7 +121,8 @@ class Batch:
 
     @property
     def total_rows(self):
-        return self.parent.shape[0]
+        # sv_reserve_kv takes chains without parents
+        return (self.tokens if self.parent is None else self.parent).shape[0]
 
     def c(self) -> N.SvBatch:
         for name in ("cu_rows", "parent", "tokens", "row_begin", "row_end", "verify_len"):
@@ -433,3 +461,44 @@ def bind_verify_chunked_commit(kv: PagedKV, batch: Batch, q: torch.Tensor, n_q_h
                                           target_logits, draft_logits, vocab, temperature, seed,
                                           chunk_size, accepted_len, accepted_nodes, next_token,
                                           ambiguous, done, pool, ws, dev_status), q.device)
+
+
+# --------------------------------------------------- the step's two edges --
+
+def _reserve_args(kv, batch, pool, slots, positions, taken, pos_offset, dev_status):
+    for name, t in (("slots", slots), ("positions", positions), ("taken", taken),
+                    ("pos_offset", pos_offset), ("dev_status", dev_status)):
+        _expect(t, torch.int32, name)
+    n, rows = batch.n_req, batch.total_rows
+    _at_least(slots, rows, "slots")
+    _at_least(positions, rows, "positions")
+    _at_least(batch.tokens, rows, "tokens")
+    for name, t in (("taken", taken), ("pos_offset", pos_offset), ("cache_lens", kv.cache_lens)):
+        _at_least(t, n, name)
+    if kv.block_tables.shape[0] < n:
+        raise N.SpecVerifyError(f"block_tables has {kv.block_tables.shape[0]} rows for {n} requests")
+    dev = _one_device(batch.cu_rows, batch.parent, kv.block_tables, kv.cache_lens, pool.free_list,
+                      pool.free_count, slots, positions, taken, pos_offset, dev_status)
+    b, k, p = batch.c(), kv.c(), pool.c()
+    return (ctypes.byref(k), ctypes.byref(b), ctypes.byref(p), _ptr(pos_offset), _ptr(slots),
+            _ptr(positions), _ptr(taken), _ptr(dev_status)), dev
+
+
+def sv_reserve_kv(kv: PagedKV, batch: Batch, pool: BlockPool, slots: torch.Tensor,
+                  positions: Optional[torch.Tensor], taken: torch.Tensor,
+                  pos_offset: Optional[torch.Tensor] = None,
+                  dev_status: Optional[torch.Tensor] = None, stream=None):
+    """Blocks for the batch's rows out of the pool: table entries, cache slots
+    and positions.  batch.parent None: chains of any length (prompts)."""
+    args, _ = _reserve_args(kv, batch, pool, slots, positions, taken, pos_offset, dev_status)
+    _call("sv_reserve_kv", args, stream)
+
+
+def bind_reserve_kv(kv: PagedKV, batch: Batch, pool: BlockPool, slots: torch.Tensor,
+                    positions: Optional[torch.Tensor], taken: torch.Tensor,
+                    pos_offset: Optional[torch.Tensor] = None,
+                    dev_status: Optional[torch.Tensor] = None) -> BoundCall:
+    """sv_reserve_kv with its arguments marshalled once (see BoundCall)."""
+    args, dev = _reserve_args(kv, batch, pool, slots, positions, taken, pos_offset, dev_status)
+    return BoundCall("sv_reserve_kv", args, dev,
+                     (kv, batch, pool, slots, positions, taken, pos_offset, dev_status))
