@@ -22,7 +22,9 @@
  *   sv_select_chunk   the chunk size of least expected cost for the next
  *                     chunked step;
  *   sv_reserve_kv     blocks for a step's rows taken from the pool, their
- *                     cache slots and positions (sv_commit_kv's counterpart).
+ *                     cache slots and positions (sv_commit_kv's counterpart);
+ *   sv_stage_qkv      head norms and rotation of the rows' Q and K, K and V
+ *                     written into the cache pages sv_tree_attend reads.
  *
  * Sources (pages by title; section names glossed):
  *   [SwiftSpec] "SwiftSpec: 드래프터와 타깃을 서로 다른 GPU에 분리하고 비동기로
@@ -94,6 +96,8 @@ typedef enum {
 #define SV_DEV_UNSUPPORTED 64    /* reserved (no longer raised: trees at temperature > 0 are sampled) */
 #define SV_DEV_BAD_LENGTH 128    /* ctx + rows does not fit the block table */
 #define SV_DEV_POOL_EMPTY 256    /* the pool has too few free blocks for a request */
+#define SV_DEV_BAD_SLOT 512      /* cache slot outside the cache */
+#define SV_DEV_BAD_PARAM 1024    /* rotation axis out of range */
 
 /* Paged KV cache ([SSD] PagedAttention; [SwiftSpec] mechanism 2).
  * k_cache, v_cache: bf16 [num_blocks][n_kv_heads][block_size][head_dim];
@@ -452,6 +456,49 @@ sv_status sv_adapt_gamma(int32_t n_req, const int32_t* accepted_len, const int32
 sv_status sv_reserve_kv(const sv_paged_kv* kv, const sv_batch* batch, const sv_block_pool* pool,
                         const int32_t* pos_offset, int32_t* slots, int32_t* positions,
                         int32_t* taken, int32_t* dev_status, void* stream);
+
+/* ----------------------------------------------------------------- stage --
+ * Fills what sv_tree_attend reads from the rows' projections: for every row r
+ * with slot s = slots[r] >= 0,
+ *   q_out[r][h]  = turn(norm(q[r][h], q_weight))     h < n_q_heads
+ *   K page of s  = turn(norm(k[r][g], k_weight))     g < kv->n_kv_heads
+ *   V page of s  = v[r][g]
+ * norm(x, w) = x / sqrt(mean(x^2) + eps) * w over the head's head_dim
+ *   elements; w NULL: x itself.  Weights: fp32 [head_dim], 16-byte aligned.
+ * turn: the first rotary_dim elements form rotary_dim / 2 pairs (a, b),
+ *   elements (j, j + rotary_dim / 2), or (2j, 2j + 1) if interleaved;
+ *   (a, b) -> scale * (a cos t - b sin t, b cos t + a sin t) with
+ *   t = position * inv_freq[j] (of the exact product, however far the
+ *   position).  With n_axes > 1, pair j turns by the position on axis
+ *   freq_axis[j] (time, height, width of an image's or video's tokens):
+ *   positions[freq_axis[j] * axis_stride + r]; axis_stride 0 = all axes share
+ *   one position.  rotary NULL or rotary_dim 0: no rotation, positions unused.
+ * All arithmetic is fp32, rounded once to bf16.
+ * q, k, v: bf16, row r at element r * stride, heads and elements dense; strides
+ *   multiples of 8 elements (views of one packed projection output will do).
+ *   q_out: bf16 [n_rows][n_q_heads][head_dim]; it may be q itself, else
+ *   it must not overlap q, k or v.
+ * A row of slot -1 (padding, a request that was not served) is skipped: nothing
+ * of it is read or written; any other slot outside the cache sets
+ * SV_DEV_BAD_SLOT and is skipped too.  Two rows must not name one slot.  An
+ * axis outside [0, n_axes) sets SV_DEV_BAD_PARAM and reads axis 0.
+ * kv->block_tables and cache_lens are not read.
+ * Supported: block_size 16, head_dim 64 or 128, rotary_dim a multiple of 16;
+ * q, k, v, q_out, the caches and the weights 16-byte aligned. */
+typedef struct {
+  const float* inv_freq;     /* fp32 [rotary_dim / 2] */
+  int32_t rotary_dim;
+  int32_t interleaved;
+  int32_t n_axes;            /* 1: one position per row */
+  const int32_t* freq_axis;  /* int32 [rotary_dim / 2]; may be NULL with one axis */
+  float scale;               /* of cosine and sine; 1 = a plain rotation */
+} sv_rotary;
+sv_status sv_stage_qkv(const sv_paged_kv* kv, int32_t n_rows, const void* q, int64_t q_stride,
+                       const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                       int32_t n_q_heads, const int32_t* slots, const int32_t* positions,
+                       int64_t axis_stride, const sv_rotary* rotary, const float* q_weight,
+                       const float* k_weight, float eps, void* q_out, int32_t* dev_status,
+                       void* stream);
 
 /* ------------------------------------------------------------ self test --
  * Every wait inside the library's kernels (on an mbarrier a TMA copy or a

@@ -1,4 +1,5 @@
-"""CPU oracle of a verification step's two edges: block reservation, in plain Python and numpy fp64, one row after the
+"""CPU oracle of a verification step's two edges: block reservation
+and Q / K / V staging, in plain Python and numpy fp64, one row after the
 other.  TEST INFRASTRUCTURE ONLY, like the rest of this package.
 """
 
@@ -67,3 +68,23 @@ def reserve(cu, parent, ctx, tables, free_list, free_count, num_blocks, max_rows
                 positions[c0 + j] = ctx[i] + depth[j] + (0 if pos_offset is None else pos_offset[i])
     return err, {"tables": tables, "count": left, "slots": slots, "positions": positions,
                  "taken": taken}
+
+
+def stage(x, weight, eps, positions, inv_freq, rotary_dim, freq_axis=None, interleaved=False,
+          scale=1.0):
+    """(value, magnitude) fp64 [rows][heads][dim] of normed and rotated heads x;
+    the magnitude is what the two terms of each element add up to in absolute
+    value.  positions: [axes][rows]."""
+    x = np.asarray(x, np.float64)
+    if weight is not None:
+        x = x / np.sqrt((x * x).mean(-1, keepdims=True) + eps) * np.asarray(weight, np.float64)
+    y, mag = x.copy(), np.abs(x)
+    for j in range(rotary_dim // 2):
+        a, b = (2 * j, 2 * j + 1) if interleaved else (j, j + rotary_dim // 2)
+        axis = 0 if freq_axis is None else int(freq_axis[j])
+        t = positions[axis].astype(np.float64) * float(inv_freq[j])
+        c, s = scale * np.cos(t)[:, None], scale * np.sin(t)[:, None]
+        y[..., a] = x[..., a] * c - x[..., b] * s
+        y[..., b] = x[..., b] * c + x[..., a] * s
+        mag[..., a] = mag[..., b] = abs(scale) * (np.abs(x[..., a]) + np.abs(x[..., b]))
+    return y, mag

@@ -16,6 +16,7 @@ P = ctypes.c_void_p
 I32 = ctypes.c_int32
 F32 = ctypes.c_float
 U64 = ctypes.c_uint64
+I64 = ctypes.c_int64
 SZ = ctypes.c_size_t
 
 SV_OK = 0
@@ -33,6 +34,8 @@ SV_DEV_BAD_TOKEN = 32
 SV_DEV_UNSUPPORTED = 64
 SV_DEV_BAD_LENGTH = 128
 SV_DEV_POOL_EMPTY = 256
+SV_DEV_BAD_SLOT = 512
+SV_DEV_BAD_PARAM = 1024
 
 SV_ACCEPT_STATIC_SCRATCH_BYTES = 4 << 20
 
@@ -51,6 +54,11 @@ class SvBatch(ctypes.Structure):
 
 class SvBlockPool(ctypes.Structure):
     _fields_ = [("free_list", P), ("free_count", P), ("capacity", I32)]
+
+
+class SvRotary(ctypes.Structure):
+    _fields_ = [("inv_freq", P), ("rotary_dim", I32), ("interleaved", I32), ("n_axes", I32),
+                ("freq_axis", P), ("scale", F32)]
 
 
 # name -> (restype, argtypes), exactly the functions declared in the header
@@ -79,6 +87,8 @@ PROTOTYPES = {
     "sv_select_chunk": (ctypes.c_int, [I32, P, P, P, ctypes.c_double, ctypes.c_double, U64, P, P,
                                        P, P, P]),
     "sv_reserve_kv": (ctypes.c_int, [P, P, P, P, P, P, P, P, P]),
+    "sv_stage_qkv": (ctypes.c_int, [P, I32, P, I64, P, I64, P, I64, I32, P, P, I64, P, P, P, F32, P,
+                                    P, P]),
     "sv_selftest_bounded_wait": (ctypes.c_int, [I32, P, P]),
 }
 

@@ -51,6 +51,19 @@ def _one_device(*tensors) -> torch.device:
     return dev
 
 
+def _rows_ptr(t: torch.Tensor, name):
+    """Pointer and row stride of a [rows][heads][dim] or [rows][columns] tensor
+    whose rows are dense and may lie apart (a view of a wider tensor)."""
+    if not t.is_cuda:
+        raise N.SpecVerifyError("libspecverify takes device tensors")
+    dense = 1
+    for size, step in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+        if size != 1 and step != dense:
+            raise N.SpecVerifyError(f"{name}: the elements of a row must be dense")
+        dense *= size
+    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else dense)
+
+
 def _stream(stream) -> int:
     if stream is None:
         return torch.cuda.current_stream().cuda_stream
@@ -161,6 +174,27 @@ class BlockPool:
         _expect(self.free_list, torch.int32, "free_list")
         _expect(self.free_count, torch.int32, "free_count")
         return N.SvBlockPool(_ptr(self.free_list), _ptr(self.free_count), self.free_list.shape[0])
+
+
+@dataclass
+class Rotary:
+    """sv_rotary: the rotation of Q and K heads.  inv_freq fp32
+    [rotary_dim / 2]; freq_axis int32 [rotary_dim / 2] names the position axis
+    of each pair (with positions of several axes)."""
+    inv_freq: torch.Tensor
+    rotary_dim: int
+    freq_axis: Optional[torch.Tensor] = None
+    interleaved: bool = False
+    scale: float = 1.0
+
+    def c(self, n_axes: int) -> N.SvRotary:
+        _expect(self.inv_freq, torch.float32, "inv_freq")
+        _expect(self.freq_axis, torch.int32, "freq_axis")
+        half = self.rotary_dim // 2
+        _at_least(self.inv_freq, half, "inv_freq")
+        _at_least(self.freq_axis, half, "freq_axis")
+        return N.SvRotary(_ptr(self.inv_freq), self.rotary_dim, int(self.interleaved), n_axes,
+                          _ptr(self.freq_axis), float(self.scale))
 
 
 def workspace(nbytes: int, device=None) -> torch.Tensor:
@@ -502,3 +536,72 @@ def bind_reserve_kv(kv: PagedKV, batch: Batch, pool: BlockPool, slots: torch.Ten
     args, dev = _reserve_args(kv, batch, pool, slots, positions, taken, pos_offset, dev_status)
     return BoundCall("sv_reserve_kv", args, dev,
                      (kv, batch, pool, slots, positions, taken, pos_offset, dev_status))
+
+
+def _stage_args(kv, q, k, v, slots, positions, rotary, q_out, q_weight, k_weight, eps, dev_status):
+    for name, t in (("q", q), ("k", k), ("v", v), ("q_out", q_out)):
+        _expect(t, torch.bfloat16, name)
+    for name, t in (("slots", slots), ("positions", positions), ("dev_status", dev_status)):
+        _expect(t, torch.int32, name)
+    _expect(q_weight, torch.float32, "q_weight")
+    _expect(k_weight, torch.float32, "k_weight")
+    nb, hkv, bs, d = kv.k_cache.shape
+    if kv.v_cache.shape != kv.k_cache.shape:
+        raise N.SpecVerifyError("k_cache and v_cache differ in shape")
+    if q.dim() != 3 or q.shape[2] != d:
+        raise N.SpecVerifyError(f"q must be [rows][heads][{d}], got {tuple(q.shape)}")
+    rows, heads = q.shape[:2]
+    for name, t, want in (("k", k, (rows, hkv, d)), ("v", v, (rows, hkv, d)),
+                          ("q_out", q_out, (rows, heads, d))):
+        if tuple(t.shape) != want:
+            raise N.SpecVerifyError(f"{name} must be {list(want)}, got {list(t.shape)}")
+    if slots.dim() != 1 or slots.shape[0] != rows:
+        raise N.SpecVerifyError(f"slots must be [{rows}], got {list(slots.shape)}")
+    _at_least(q_weight, d, "q_weight")
+    _at_least(k_weight, d, "k_weight")
+    n_axes, axis_stride = 1, 0
+    if positions is not None:
+        if positions.shape[-1] != rows or positions.dim() not in (1, 2):
+            raise N.SpecVerifyError(f"positions must be [{rows}] or [axes][{rows}], got "
+                                    f"{list(positions.shape)}")
+        if positions.dim() == 2:
+            n_axes, axis_stride = positions.shape[0], positions.shape[1]
+    if rotary is not None and rotary.freq_axis is not None and n_axes == 1:
+        # one position for every axis: the pairs' axes make no difference
+        rotary = Rotary(rotary.inv_freq, rotary.rotary_dim, None, rotary.interleaved, rotary.scale)
+    dev = _one_device(kv.k_cache, kv.v_cache, q, k, v, slots, positions, q_out, q_weight, k_weight,
+                      dev_status, *(() if rotary is None else (rotary.inv_freq, rotary.freq_axis)))
+    c = N.SvPagedKV(_ptr(kv.k_cache), _ptr(kv.v_cache), nb, bs, hkv, d, None, 0, None)
+    _expect(kv.k_cache, torch.bfloat16, "k_cache")
+    _expect(kv.v_cache, torch.bfloat16, "v_cache")
+    (qp, qs), (kp, ks), (vp, vs) = _rows_ptr(q, "q"), _rows_ptr(k, "k"), _rows_ptr(v, "v")
+    r = None if rotary is None else ctypes.byref(rotary.c(n_axes))
+    return (ctypes.byref(c), rows, qp, qs, kp, ks, vp, vs, heads, _ptr(slots), _ptr(positions),
+            axis_stride, r, _ptr(q_weight), _ptr(k_weight), float(eps), _ptr(q_out),
+            _ptr(dev_status)), dev
+
+
+def sv_stage_qkv(kv: PagedKV, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                 slots: torch.Tensor, positions: Optional[torch.Tensor],
+                 rotary: Optional[Rotary], q_out: torch.Tensor,
+                 q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None,
+                 eps: float = 1e-6, dev_status: Optional[torch.Tensor] = None, stream=None):
+    """Head norms and rotation of q and k, q into q_out, k and v into the cache
+    pages of slots.  q, k, v: [rows][heads][dim], views of one packed
+    projection output will do; positions: [rows] or [axes][rows]."""
+    args, _ = _stage_args(kv, q, k, v, slots, positions, rotary, q_out, q_weight, k_weight, eps,
+                          dev_status)
+    _call("sv_stage_qkv", args, stream)
+
+
+def bind_stage_qkv(kv: PagedKV, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                   slots: torch.Tensor, positions: Optional[torch.Tensor],
+                   rotary: Optional[Rotary], q_out: torch.Tensor,
+                   q_weight: Optional[torch.Tensor] = None,
+                   k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                   dev_status: Optional[torch.Tensor] = None) -> BoundCall:
+    """sv_stage_qkv with its arguments marshalled once (see BoundCall)."""
+    args, dev = _stage_args(kv, q, k, v, slots, positions, rotary, q_out, q_weight, k_weight, eps,
+                            dev_status)
+    return BoundCall("sv_stage_qkv", args, dev,
+                     (kv, q, k, v, slots, positions, rotary, q_out, q_weight, k_weight, dev_status))
