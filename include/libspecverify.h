@@ -24,7 +24,9 @@
  *   sv_reserve_kv     blocks for a step's rows taken from the pool, their
  *                     cache slots and positions (sv_commit_kv's counterpart);
  *   sv_stage_qkv      head norms and rotation of the rows' Q and K, K and V
- *                     written into the cache pages sv_tree_attend reads.
+ *                     written into the cache pages sv_tree_attend reads;
+ *   sv_shape_logits   penalties for repeated tokens, biases and grammar masks
+ *                     on the logits sv_accept reads.
  *
  * Sources (pages by title; section names glossed):
  *   [SwiftSpec] "SwiftSpec: 드래프터와 타깃을 서로 다른 GPU에 분리하고 비동기로
@@ -94,10 +96,12 @@ typedef enum {
 #define SV_DEV_TIMEOUT 16        /* reserved: a bounded device wait gave up */
 #define SV_DEV_BAD_TOKEN 32      /* draft token outside [0, vocab) */
 #define SV_DEV_UNSUPPORTED 64    /* reserved (no longer raised: trees at temperature > 0 are sampled) */
-#define SV_DEV_BAD_LENGTH 128    /* ctx + rows does not fit the block table */
+#define SV_DEV_BAD_LENGTH 128    /* ctx + rows does not fit the block table; a history
+                                    length outside the history */
 #define SV_DEV_POOL_EMPTY 256    /* the pool has too few free blocks for a request */
 #define SV_DEV_BAD_SLOT 512      /* cache slot outside the cache */
-#define SV_DEV_BAD_PARAM 1024    /* rotation axis out of range */
+#define SV_DEV_BAD_PARAM 1024    /* penalty, bias range, mask row or rotation axis out of range */
+#define SV_DEV_EMPTY_MASK 2048   /* a mask that permits no token (it is not applied) */
 
 /* Paged KV cache ([SSD] PagedAttention; [SwiftSpec] mechanism 2).
  * k_cache, v_cache: bf16 [num_blocks][n_kv_heads][block_size][head_dim];
@@ -499,6 +503,61 @@ sv_status sv_stage_qkv(const sv_paged_kv* kv, int32_t n_rows, const void* q, int
                        int64_t axis_stride, const sv_rotary* rotary, const float* q_weight,
                        const float* k_weight, float eps, void* q_out, int32_t* dev_status,
                        void* stream);
+
+/* ----------------------------------------------------------------- rules --
+ * The logits of every draft node under its request's rules, ready for
+ * sv_accept (which must test and draw from the distribution the request asked
+ * for: the same rules on target and draft rows keep verification lossless).
+ * For row r = node n of request i inside its window, and token v:
+ *   c(v) = occurrences of v among history entries prompt_len_i ..
+ *          history_len_i - 1 and among the tokens of n and its ancestors (the
+ *          root excepted: its token is the history's last);
+ *   seen(v) = c(v) > 0 or v among the first prompt_len_i entries;
+ *   y = seen(v) ? (x > 0 ? x / repetition_i : x * repetition_i) : x;
+ *   y = y - (frequency_i * c(v) + presence_i * [c(v) > 0]);
+ *   y = y + bias_i(v);
+ *   out[r][v] = y, or -inf if the row's mask has bit v (of word v / 32) zero.
+ * Everything is fp32; out is fp32 [total_rows][vocab].
+ * logits: SV_LOGITS_F32 or SV_LOGITS_BF16, row r at element r * logits_stride
+ *   (a head's padded output will do); out may be the logits themselves (fp32,
+ *   logits_stride == vocab), else the two must not overlap.
+ * Every part may be left out (NULL):
+ *   history int32 [n_req][max_history], history_len, prompt_len (NULL: 0)
+ *     [n_req]: read only with a penalty; tokens outside [0, vocab) are ignored;
+ *   repetition (finite, > 0; 1 = none), frequency, presence (finite; 0 = none):
+ *     fp32 [n_req];
+ *   biases: entries bias_begin[i] .. bias_begin[i + 1] - 1 (of n_bias) of
+ *     bias_token / bias_value are request i's; a token listed twice takes its
+ *     first entry, one outside [0, vocab) is ignored;
+ *   mask: int32 words [n_masks][mask_stride], mask_row [total_rows] = the
+ *     row's mask, -1 for none (NULL: mask r for row r).
+ * A request with a parameter or range out of bounds (SV_DEV_BAD_PARAM,
+ * BAD_LENGTH, BAD_WINDOW, BAD_PARENT) and rows outside the windows are left as
+ * they were.  A mask row outside [0, n_masks) sets SV_DEV_BAD_PARAM, one that
+ * permits no token SV_DEV_EMPTY_MASK; such a mask is not applied.
+ * No workspace; results do not depend on the order of anything. */
+#define SV_LOGITS_F32 0
+#define SV_LOGITS_BF16 1
+typedef struct {
+  const int32_t* history;
+  int32_t max_history;
+  const int32_t* history_len;
+  const int32_t* prompt_len;
+  const float* repetition;
+  const float* frequency;
+  const float* presence;
+  const int32_t* bias_begin; /* int32 [n_req + 1] */
+  const int32_t* bias_token;
+  const float* bias_value;
+  int32_t n_bias;
+  const int32_t* mask;
+  int32_t mask_stride;       /* words per mask row, at least ceil(vocab / 32) */
+  int32_t n_masks;
+  const int32_t* mask_row;
+} sv_logit_rules;
+sv_status sv_shape_logits(const sv_batch* batch, const void* logits, int32_t logits_type,
+                          int64_t logits_stride, int32_t vocab, const sv_logit_rules* rules,
+                          float* out, int32_t* dev_status, void* stream);
 
 /* ------------------------------------------------------------ self test --
  * Every wait inside the library's kernels (on an mbarrier a TMA copy or a

@@ -1,5 +1,5 @@
-"""CPU oracle of a verification step's two edges: block reservation
-and Q / K / V staging, in plain Python and numpy fp64, one row after the
+"""CPU oracle of a verification step's two edges: block reservation, Q / K / V
+staging and logit rules, in plain Python and numpy fp64, one row after the
 other.  TEST INFRASTRUCTURE ONLY, like the rest of this package.
 """
 
@@ -87,4 +87,58 @@ def stage(x, weight, eps, positions, inv_freq, rotary_dim, freq_axis=None, inter
         y[..., a] = x[..., a] * c - x[..., b] * s
         y[..., b] = x[..., b] * c + x[..., a] * s
         mag[..., a] = mag[..., b] = abs(scale) * (np.abs(x[..., a]) + np.abs(x[..., b]))
+    return y, mag
+
+
+def shape_logits(cu, parent, tokens, logits, history=None, history_len=None, prompt_len=None,
+                 repetition=None, frequency=None, presence=None, bias_begin=None, bias_token=None,
+                 bias_value=None, mask=None, mask_row=None):
+    """(value, magnitude) fp64 [rows][vocab] of well-formed requests; the
+    magnitude is the sum of the absolute values of what is added up."""
+    y = np.array(logits, np.float64)
+    V = y.shape[1]
+    mag = np.abs(y)
+    pen = repetition is not None or frequency is not None or presence is not None
+    for i in range(len(cu) - 1):
+        c0, c1 = int(cu[i]), int(cu[i + 1])
+        for r in range(c0, c1):
+            if pen:
+                rho = 1.0 if repetition is None else float(repetition[i])
+                f = 0.0 if frequency is None else float(frequency[i])
+                p = 0.0 if presence is None else float(presence[i])
+                n = 0 if history is None else int(history_len[i])
+                k = 0 if history is None or prompt_len is None else int(prompt_len[i])
+                said, seen = {}, set()
+                for t in range(n):
+                    v = int(history[i][t])
+                    seen.add(v)
+                    if t >= k:
+                        said[v] = said.get(v, 0) + 1
+                node = r - c0
+                while node > 0:
+                    v = int(tokens[c0 + node])
+                    seen.add(v)
+                    said[v] = said.get(v, 0) + 1
+                    node = int(parent[c0 + node])
+                for v in seen:
+                    if not 0 <= v < V:
+                        continue
+                    x, c = y[r, v], said.get(v, 0)
+                    x = x / rho if x > 0 else x * rho
+                    y[r, v] = x - (f * c + p * (c > 0))
+                    mag[r, v] = abs(x) + abs(f) * c + abs(p) * (c > 0)
+            if bias_begin is not None:
+                done = set()
+                for t in range(int(bias_begin[i]), int(bias_begin[i + 1])):
+                    v = int(bias_token[t])
+                    if 0 <= v < V and v not in done:
+                        done.add(v)
+                        y[r, v] += float(bias_value[t])
+                        mag[r, v] += abs(float(bias_value[t]))
+            m = -1 if mask is None else r if mask_row is None else int(mask_row[r])
+            if m >= 0:
+                bits = (np.asarray(mask[m]).astype(np.uint32)[:, None] >> np.arange(32, dtype=np.uint32)) & 1
+                let = bits.reshape(-1)[:V].astype(bool)
+                if let.any():
+                    y[r, ~let] = -np.inf
     return y, mag

@@ -36,6 +36,10 @@ SV_DEV_BAD_LENGTH = 128
 SV_DEV_POOL_EMPTY = 256
 SV_DEV_BAD_SLOT = 512
 SV_DEV_BAD_PARAM = 1024
+SV_DEV_EMPTY_MASK = 2048
+
+SV_LOGITS_F32 = 0
+SV_LOGITS_BF16 = 1
 
 SV_ACCEPT_STATIC_SCRATCH_BYTES = 4 << 20
 
@@ -59,6 +63,13 @@ class SvBlockPool(ctypes.Structure):
 class SvRotary(ctypes.Structure):
     _fields_ = [("inv_freq", P), ("rotary_dim", I32), ("interleaved", I32), ("n_axes", I32),
                 ("freq_axis", P), ("scale", F32)]
+
+
+class SvLogitRules(ctypes.Structure):
+    _fields_ = [("history", P), ("max_history", I32), ("history_len", P), ("prompt_len", P),
+                ("repetition", P), ("frequency", P), ("presence", P), ("bias_begin", P),
+                ("bias_token", P), ("bias_value", P), ("n_bias", I32), ("mask", P),
+                ("mask_stride", I32), ("n_masks", I32), ("mask_row", P)]
 
 
 # name -> (restype, argtypes), exactly the functions declared in the header
@@ -89,6 +100,7 @@ PROTOTYPES = {
     "sv_reserve_kv": (ctypes.c_int, [P, P, P, P, P, P, P, P, P]),
     "sv_stage_qkv": (ctypes.c_int, [P, I32, P, I64, P, I64, P, I64, I32, P, P, I64, P, P, P, F32, P,
                                     P, P]),
+    "sv_shape_logits": (ctypes.c_int, [P, P, I32, I64, I32, P, P, P, P]),
     "sv_selftest_bounded_wait": (ctypes.c_int, [I32, P, P]),
 }
 

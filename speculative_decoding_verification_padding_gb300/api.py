@@ -197,6 +197,52 @@ class Rotary:
                           _ptr(self.freq_axis), float(self.scale))
 
 
+@dataclass
+class LogitRules:
+    """sv_logit_rules: what shapes a request's logits; every part may be left
+    out.  history int32 [n_req][max_history] with history_len / prompt_len
+    int32 [n_req]; repetition, frequency, presence fp32 [n_req]; biases as one
+    packed list with offsets bias_begin [n_req + 1]; mask int32 words
+    [n_masks][words] with mask_row int32 [total_rows]."""
+    history: Optional[torch.Tensor] = None
+    history_len: Optional[torch.Tensor] = None
+    prompt_len: Optional[torch.Tensor] = None
+    repetition: Optional[torch.Tensor] = None
+    frequency: Optional[torch.Tensor] = None
+    presence: Optional[torch.Tensor] = None
+    bias_begin: Optional[torch.Tensor] = None
+    bias_token: Optional[torch.Tensor] = None
+    bias_value: Optional[torch.Tensor] = None
+    mask: Optional[torch.Tensor] = None
+    mask_row: Optional[torch.Tensor] = None
+
+    def c(self, n_req: int, total_rows: int) -> N.SvLogitRules:
+        for name in ("history", "history_len", "prompt_len", "bias_begin", "bias_token", "mask",
+                     "mask_row"):
+            _expect(getattr(self, name), torch.int32, name)
+        for name in ("repetition", "frequency", "presence", "bias_value"):
+            _expect(getattr(self, name), torch.float32, name)
+        for name in ("history_len", "prompt_len", "repetition", "frequency", "presence"):
+            _at_least(getattr(self, name), n_req, name)
+        _at_least(self.bias_begin, n_req + 1, "bias_begin")
+        _at_least(self.mask_row, total_rows, "mask_row")
+        hist, mask = self.history, self.mask
+        if hist is not None and (hist.dim() != 2 or hist.shape[0] < n_req):
+            raise N.SpecVerifyError(f"history must be [{n_req}][max_history], got {tuple(hist.shape)}")
+        if mask is not None and mask.dim() != 2:
+            raise N.SpecVerifyError(f"mask must be [n_masks][words], got {tuple(mask.shape)}")
+        n_bias = 0
+        if self.bias_begin is not None and self.bias_token is not None:
+            n_bias = self.bias_token.numel()
+            _at_least(self.bias_value, n_bias, "bias_value")
+        return N.SvLogitRules(
+            _ptr(hist), 0 if hist is None else hist.shape[1], _ptr(self.history_len),
+            _ptr(self.prompt_len), _ptr(self.repetition), _ptr(self.frequency),
+            _ptr(self.presence), _ptr(self.bias_begin), _ptr(self.bias_token),
+            _ptr(self.bias_value), n_bias, _ptr(mask), 0 if mask is None else mask.shape[1],
+            0 if mask is None else mask.shape[0], _ptr(self.mask_row))
+
+
 def workspace(nbytes: int, device=None) -> torch.Tensor:
     """A 256-byte aligned device buffer of at least nbytes (torch allocations are)."""
     return torch.empty(max(1, nbytes), dtype=torch.uint8, device=device or "cuda")
@@ -605,3 +651,41 @@ def bind_stage_qkv(kv: PagedKV, q: torch.Tensor, k: torch.Tensor, v: torch.Tenso
                             dev_status)
     return BoundCall("sv_stage_qkv", args, dev,
                      (kv, q, k, v, slots, positions, rotary, q_out, q_weight, k_weight, dev_status))
+
+
+_LOGIT_TYPES = {torch.float32: N.SV_LOGITS_F32, torch.bfloat16: N.SV_LOGITS_BF16}
+
+
+def _shape_args(batch, logits, rules, out, dev_status):
+    _expect(out, torch.float32, "out")
+    _expect(dev_status, torch.int32, "dev_status")
+    if logits.dtype not in _LOGIT_TYPES:
+        raise N.SpecVerifyError(f"logits must be float32 or bfloat16, got {logits.dtype}")
+    n, rows = batch.n_req, batch.total_rows
+    if logits.dim() != 2 or logits.shape != out.shape or out.shape[0] != rows:
+        raise N.SpecVerifyError(f"logits and out must be [{rows}][vocab], got {list(logits.shape)} "
+                                f"and {list(out.shape)}")
+    _at_least(batch.tokens, rows, "tokens")
+    for name in ("row_begin", "row_end", "verify_len"):
+        _at_least(getattr(batch, name), n, name)
+    dev = _one_device(batch.cu_rows, batch.parent, batch.tokens, batch.row_begin, batch.row_end,
+                      batch.verify_len, logits, out, dev_status, *vars(rules).values())
+    b, r = batch.c(), rules.c(n, rows)
+    lp, stride = _rows_ptr(logits, "logits")
+    return (ctypes.byref(b), lp, _LOGIT_TYPES[logits.dtype], stride, out.shape[1], ctypes.byref(r),
+            _ptr(out), _ptr(dev_status)), dev
+
+
+def sv_shape_logits(batch: Batch, logits: torch.Tensor, rules: LogitRules, out: torch.Tensor,
+                    dev_status: Optional[torch.Tensor] = None, stream=None):
+    """The logits [rows][vocab] (fp32 or bf16; rows may lie apart) under each
+    request's penalties, biases and masks, into out (fp32; may be logits)."""
+    args, _ = _shape_args(batch, logits, rules, out, dev_status)
+    _call("sv_shape_logits", args, stream)
+
+
+def bind_shape_logits(batch: Batch, logits: torch.Tensor, rules: LogitRules, out: torch.Tensor,
+                      dev_status: Optional[torch.Tensor] = None) -> BoundCall:
+    """sv_shape_logits with its arguments marshalled once (see BoundCall)."""
+    args, dev = _shape_args(batch, logits, rules, out, dev_status)
+    return BoundCall("sv_shape_logits", args, dev, (batch, logits, rules, out, dev_status))
