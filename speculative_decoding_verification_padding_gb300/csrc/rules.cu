@@ -31,11 +31,12 @@ namespace sv {
 namespace rul {
 
 constexpr int kThreads = 256;
+constexpr int kCtasPerSm = 4;
 constexpr int kWarps = kThreads / 32;
 constexpr int kSlice = 4096;    // vocabulary entries of a CTA
 constexpr int kWords = kSlice / 32;
 constexpr int kQuads = kSlice / (4 * kThreads);
-constexpr int kMaxChunk = 32;   // rows of a CTA at most
+constexpr int kMaxChunk = 9;    // rows of a CTA at most: a root and eight drafts
 constexpr int kHistVecs = 2;    // vectors of four history tokens a thread has in flight
 
 struct Args {
@@ -53,9 +54,10 @@ struct Args {
 
 struct Smem {
   union {
-    unsigned cnt[kSlice];      // first occurrences, kSeen and kDraft,
+    unsigned cnt[kSlice];      // first occurrences and kDraft,
     float add[kSlice];         // then the addend
   };
+  uint8_t asked[kSlice];       // 1: the token is in the prompt
   unsigned hit[kWords + 1];    // touched entries, a bit each (and a word for a look past the end)
   unsigned seen[kWords + 1];   // entries that the repetition penalty takes
   int tok[kMaxRows];
@@ -63,13 +65,13 @@ struct Smem {
   unsigned mine[kMaxRows / 32];             // nodes whose token is in the slice
   unsigned path[kMaxChunk][kMaxRows / 32];  // of those, the nodes on the row's path
   int masked[kMaxChunk];                    // the row's mask row, -1: none
+  unsigned words[kMaxChunk][kWords + 1];    // that mask's bits of the slice
 };
 // Behind it, with biases: the lowest list position of each token.
 constexpr size_t kBiasAt = (sizeof(Smem) + 15) / 16 * 16;
 constexpr size_t kBiasBytes = kSlice * sizeof(unsigned);
 
-constexpr unsigned kSeen = 0x80000000u;   // the token is in the prompt
-constexpr unsigned kDraft = 0x40000000u;  // the token is some draft's
+constexpr unsigned kDraft = 0x80000000u;  // the token is some draft's
 
 __device__ __forceinline__ float load1(const float* p) { return *p; }
 __device__ __forceinline__ float load1(const __nv_bfloat16* p) { return __bfloat162float(*p); }
@@ -82,29 +84,31 @@ struct Quad32 {
     if (alike) x = *reinterpret_cast<const float4*>(p);
     else x = make_float4(p[0], p[1], p[2], p[3]);
   }
-  __device__ __forceinline__ float4 get() const { return x; }
+  __device__ __forceinline__ float4 get(bool) const { return x; }
 };
 struct Quad16 {
-  uint32_t w0, w1;
-  // alike: they lie together in 8 bytes; else the aligned words around them
-  // are shifted into place (entry by entry where those reach past the input)
+  uint32_t w[3];
+  // alike: they lie together in 8 bytes; else the aligned words around them,
+  // shifted into place when they are used (a shift here would wait for them).
+  // A first half word before the input lies in the same four bytes as its
+  // first entry; a last one behind it is not read.
   __device__ __forceinline__ void load(const __nv_bfloat16* p, bool alike, const void* end) {
     if (alike) {
       const uint2 u = *reinterpret_cast<const uint2*>(p);
-      w0 = u.x;
-      w1 = u.y;
+      w[0] = u.x;
+      w[1] = u.y;
       return;
     }
-    const uintptr_t at = (uintptr_t)p, lo = at & ~(uintptr_t)3;
-    const uint32_t* w = reinterpret_cast<const uint32_t*>(lo);
-    w0 = w[0];
-    w1 = w[1];
-    if (at == lo) return;
-    const uint32_t w2 = lo + 12 <= (uintptr_t)end ? w[2] : *reinterpret_cast<const uint16_t*>(w + 2);
-    w0 = __funnelshift_r(w0, w1, 16);
-    w1 = __funnelshift_r(w1, w2, 16);
+    const uintptr_t lo = (uintptr_t)p & ~(uintptr_t)3;
+    const uint32_t* q = reinterpret_cast<const uint32_t*>(lo);
+    w[0] = q[0];
+    w[1] = q[1];
+    if ((uintptr_t)p & 2) w[2] = lo + 12 <= (uintptr_t)end ? q[2] : *reinterpret_cast<const uint16_t*>(q + 2);
   }
-  __device__ __forceinline__ float4 get() const {
+  // odd: they start in the upper half of a word
+  __device__ __forceinline__ float4 get(bool odd) const {
+    const uint32_t w0 = odd ? __funnelshift_r(w[0], w[1], 16) : w[0];
+    const uint32_t w1 = odd ? __funnelshift_r(w[1], w[2], 16) : w[1];
     return make_float4(__uint_as_float(w0 << 16), __uint_as_float(w0 & 0xffff0000u),
                        __uint_as_float(w1 << 16), __uint_as_float(w1 & 0xffff0000u));
   }
@@ -114,19 +118,19 @@ struct QuadOf { using type = Quad32; };
 template <>
 struct QuadOf<__nv_bfloat16> { using type = Quad16; };
 
-// Does mask row m permit any of the entries [lo, lo + n)?  By one warp; bits
-// past the vocabulary do not count.
-__device__ __forceinline__ bool any_permitted(const int32_t* m, int lo, int n, int V) {
+// Does mask row m permit anything?  By one warp; bits past the vocabulary do
+// not count.
+__device__ __forceinline__ bool any_permitted(const int32_t* m, int V) {
   const int lane = threadIdx.x & 31;
-  const int w1 = (lo + n + 31) >> 5, last = (V - 1) >> 5;
-  for (int w = lo >> 5; w < w1; w += 32 * 8) {
+  const int words = (V + 31) >> 5;
+  for (int w = 0; w < words; w += 32 * 8) {
     unsigned x = 0;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const int at = w + 32 * k + lane;
-      if (at < w1) {
+      if (at < words) {
         unsigned b = (unsigned)__ldg(m + at);
-        if (at == last && (V & 31)) b &= (1u << (V & 31)) - 1u;
+        if (at == words - 1 && (V & 31)) b &= (1u << (V & 31)) - 1u;
         x |= b;
       }
     }
@@ -144,7 +148,7 @@ __device__ __forceinline__ unsigned nibble(const unsigned* bits, int o) {
 
 // EVEN: every row of the output starts on 16 bytes.
 template <typename T, bool EVEN>
-__global__ void __launch_bounds__(kThreads, 4) rules_kernel(Args a) {
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) rules_kernel(Args a) {
   griddep_entry();
   extern __shared__ __align__(16) uint8_t s_raw[];
   Smem& sm = *reinterpret_cast<Smem*>(s_raw);
@@ -225,10 +229,13 @@ __global__ void __launch_bounds__(kThreads, 4) rules_kernel(Args a) {
     }
     sm.masked[tid] = m;
   }
-  auto mine = [&](int v) { return v >= 0 && (unsigned)(v - lo) < (unsigned)n; };
+  // (a negative token is a large offset)
+  auto mine = [&](int v) { return (unsigned)(v - lo) < (unsigned)n; };
   if (rules) {
-    for (int o = tid; o < kSlice / 4; o += kThreads)
+    for (int o = tid; o < kSlice / 4; o += kThreads) {
       reinterpret_cast<uint4*>(sm.cnt)[o] = make_uint4(0u, 0u, 0u, 0u);
+      reinterpret_cast<uint32_t*>(sm.asked)[o] = 0u;
+    }
     if (b1 > b0)
       for (int o = tid; o < kSlice / 4; o += kThreads)
         reinterpret_cast<uint4*>(s_first)[o] =
@@ -236,7 +243,7 @@ __global__ void __launch_bounds__(kThreads, 4) rules_kernel(Args a) {
     if (tid < kMaxRows) {
       sm.tok[tid] = node_t;
       sm.par[tid] = (int8_t)(bad ? 0 : node_p);
-      const unsigned m = __ballot_sync(0xffffffffu, tid > 0 && mine(node_t));
+      const unsigned m = __ballot_sync(0xffffffffu, tid > 0 && tid < w.rows && mine(node_t));
       if (lane == 0) sm.mine[wid] = m;
     }
   }
@@ -245,13 +252,22 @@ __global__ void __launch_bounds__(kThreads, 4) rules_kernel(Args a) {
     return;
   }
   if (ru.mask) {
-    // a warp for each row: a mask that lets nothing through would leave no
-    // distribution
-    for (int k = wid; k < rows; k += kWarps) {
+    for (int k = wid; k < rows; k += kWarps) {  // a warp for each row
       const int m = sm.masked[k];
       if (m < 0) continue;
-      const int32_t* words = ru.mask + (size_t)m * ru.mask_stride;
-      if (!any_permitted(words, lo, n, a.V) && !any_permitted(words, 0, a.V, a.V) && lane == 0) {
+      const int32_t* mask = ru.mask + (size_t)m * ru.mask_stride;
+      unsigned any = 0;
+#pragma unroll
+      for (int q = 0; q < kWords / 32; ++q) {
+        const int at = 32 * q + lane;
+        unsigned b = 32 * at < n ? (unsigned)__ldg(mask + (lo >> 5) + at) : 0u;
+        if (n - 32 * at < 32 && 32 * at < n) b &= (1u << (n & 31)) - 1u;
+        sm.words[k][at] = b;
+        any |= b;
+      }
+      if (lane == 0) sm.words[k][kWords] = 0;
+      // a mask that lets nothing through would leave no distribution
+      if (!__any_sync(0xffffffffu, any != 0) && !any_permitted(mask, a.V) && lane == 0) {
         flag(a.dev_status, SV_DEV_EMPTY_MASK);
         sm.masked[k] = -1;
       }
@@ -263,11 +279,13 @@ __global__ void __launch_bounds__(kThreads, 4) rules_kernel(Args a) {
   float node_bias = 0.f;  // bias
   if (rules) {
     if (pen) {
+      // a prompt's token leaves a mark (a plain store: all write the same),
+      // an output's is counted
+      auto mark = [&](int v) { if (mine(v)) sm.asked[v - lo] = 1; };
+      auto count = [&](int v) { if (mine(v)) atomicAdd(&sm.cnt[v - lo], 1u); };
       auto take = [&](int t, int v) {
-        if (mine(v)) {
-          if (t < plen) atomicOr(&sm.cnt[v - lo], kSeen);
-          else atomicAdd(&sm.cnt[v - lo], 1u);
-        }
+        if (t < plen) mark(v);
+        else count(v);
       };
       for (int t0 = 0; t0 < hvecs; t0 += kThreads * kHistVecs) {
         int4 next[kHistVecs];
@@ -279,11 +297,23 @@ __global__ void __launch_bounds__(kThreads, 4) rules_kernel(Args a) {
 #pragma unroll
         for (int q = 0; q < kHistVecs; ++q) {
           const int t = t0 + q * kThreads + tid;
-          if (t < hvecs) {
-            take(hhead + 4 * t, hv[q].x);
-            take(hhead + 4 * t + 1, hv[q].y);
-            take(hhead + 4 * t + 2, hv[q].z);
-            take(hhead + 4 * t + 3, hv[q].w);
+          const int at = hhead + 4 * t;
+          if (t >= hvecs) {
+          } else if (at >= plen) {
+            count(hv[q].x);
+            count(hv[q].y);
+            count(hv[q].z);
+            count(hv[q].w);
+          } else if (at + 4 <= plen) {
+            mark(hv[q].x);
+            mark(hv[q].y);
+            mark(hv[q].z);
+            mark(hv[q].w);
+          } else {
+            take(at, hv[q].x);
+            take(at + 1, hv[q].y);
+            take(at + 2, hv[q].z);
+            take(at + 3, hv[q].w);
           }
           hv[q] = next[q];
         }
@@ -295,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 4) rules_kernel(Args a) {
       // the path of every row of this CTA, its nodes in the slice only
       paths = (sm.mine[0] | sm.mine[1] | sm.mine[2] | sm.mine[3]) != 0;
       if (paths) {
-        if (tid > 0 && mine(node_t)) atomicOr(&sm.cnt[node_t - lo], kDraft);
+        if (tid > 0 && tid < w.rows && mine(node_t)) atomicOr(&sm.cnt[node_t - lo], kDraft);
         if (tid < rows) {
           unsigned m[kMaxRows / 32] = {};
           for (int p = j0 + tid; p > 0; p = sm.par[p]) {  // parents lie before their children
@@ -315,25 +345,40 @@ __global__ void __launch_bounds__(kThreads, 4) rules_kernel(Args a) {
     }
     __syncthreads();
     if (paths) {
-      if (tid > 0 && mine(node_t)) {
-        const unsigned c = sm.cnt[node_t - lo];
-        node_n = (int)(c & ~(kSeen | kDraft));
-        node_seen = node_n > 0 || (c & kSeen);
+      if (tid > 0 && tid < w.rows && mine(node_t)) {
+        node_n = (int)(sm.cnt[node_t - lo] & ~kDraft);
+        node_seen = node_n > 0 || sm.asked[node_t - lo];
         const unsigned f = b1 > b0 ? s_first[node_t - lo] : 0xffffffffu;
         if (f != 0xffffffffu) node_bias = ru.bias_value[b0 + (int)f];
       }
       __syncthreads();  // the counts become addends
     }
 #pragma unroll
-    for (int q = 0; q < kSlice / kThreads; ++q) {
-      const int o = q * kThreads + tid;
-      const unsigned c = sm.cnt[o];
-      const int m = (int)(c & ~(kSeen | kDraft));
-      const bool biased = b1 > b0 && s_first[o] != 0xffffffffu;
-      sm.add[o] = m ? -(freq * (float)m + pres) : 0.f;
-      const unsigned seen = __ballot_sync(0xffffffffu, m > 0 || (c & kSeen));
-      const unsigned hit = __ballot_sync(0xffffffffu, c != 0u || biased);
-      if (lane == 0) {
+    for (int q = 0; q < kQuads; ++q) {
+      const int o = 4 * (q * kThreads + tid);
+      const uint4 c = *reinterpret_cast<const uint4*>(sm.cnt + o);
+      const uint32_t asked = *reinterpret_cast<const uint32_t*>(sm.asked + o);
+      const auto addend = [&](unsigned m) { return m ? -(freq * (float)m + pres) : 0.f; };
+      const unsigned m[4] = {c.x & ~kDraft, c.y & ~kDraft, c.z & ~kDraft, c.w & ~kDraft};
+      *reinterpret_cast<float4*>(sm.add + o) =
+          make_float4(addend(m[0]), addend(m[1]), addend(m[2]), addend(m[3]));
+      unsigned seen = (m[0] || (asked & 0xffu) ? 1u : 0u) | (m[1] || (asked & 0xff00u) ? 2u : 0u) |
+                      (m[2] || (asked & 0xff0000u) ? 4u : 0u) | (m[3] || (asked >> 24) ? 8u : 0u);
+      unsigned hit = seen | (c.x ? 1u : 0u) | (c.y ? 2u : 0u) | (c.z ? 4u : 0u) | (c.w ? 8u : 0u);
+      if (b1 > b0) {
+        const uint4 f = *reinterpret_cast<const uint4*>(s_first + o);
+        hit |= (f.x != ~0u ? 1u : 0u) | (f.y != ~0u ? 2u : 0u) | (f.z != ~0u ? 4u : 0u) |
+               (f.w != ~0u ? 8u : 0u);
+      }
+      // eight lanes' nibbles make a word
+      seen <<= 4 * (lane & 7);
+      hit <<= 4 * (lane & 7);
+#pragma unroll
+      for (int d = 1; d < 8; d <<= 1) {
+        seen |= __shfl_xor_sync(0xffffffffu, seen, d);
+        hit |= __shfl_xor_sync(0xffffffffu, hit, d);
+      }
+      if ((lane & 7) == 0) {
         sm.seen[o >> 5] = seen;
         sm.hit[o >> 5] = hit;
       }
@@ -359,11 +404,20 @@ __global__ void __launch_bounds__(kThreads, 4) rules_kernel(Args a) {
     const float y = x * (x > 0.f ? inv : rho);
     return (seen ? y : x) + add;
   };
-  unsigned hits[kQuads] = {};  // EVEN: this thread's touched entries, the same in every row
-  if (EVEN && rules) {
+  // This thread's touched entries, four bits a quad: sixteen bits for each
+  // place that a row can start at.
+  static_assert(kQuads == 4, "");
+  uint64_t hits4 = 0;
+  if (rules) {
 #pragma unroll
-    for (int q = 0; q < kQuads; ++q) hits[q] = nibble(sm.hit, 4 * (q * kThreads + tid));
+    for (int e = 0; e < (EVEN ? 1 : 4); ++e)
+#pragma unroll
+      for (int q = 0; q < kQuads; ++q) {
+        const int o = e + 4 * (q * kThreads + tid);
+        if (o < n) hits4 |= (uint64_t)nibble(sm.hit, o) << (16 * e + 4 * q);
+      }
   }
+  auto hits_at = [&](int head, int q) { return (unsigned)(hits4 >> (16 * head + 4 * q)) & 15u; };
 
   // ---- the rows ----
   // Each row is loaded (its mask's bits first) before the row before it is
@@ -371,39 +425,40 @@ __global__ void __launch_bounds__(kThreads, 4) rules_kernel(Args a) {
   using Quad = typename QuadOf<T>::type;
   struct Row {
     Quad x[kQuads];
-    unsigned let;  // permitted entries, four bits a quad
+    unsigned let;  // permitted entries, four bits a quad; the top bit: the edge
+    float edge;    // !EVEN: one of the entries that no 16 bytes of the output hold
   };
-  auto words_of = [&](int k) {
-    const int m = ru.mask ? sm.masked[k] : -1;
-    return m >= 0 ? ru.mask + (size_t)m * ru.mask_stride + (lo >> 5) : nullptr;
+  auto words_of = [&](int k) -> const unsigned* {
+    return ru.mask && sm.masked[k] >= 0 ? sm.words[k] : nullptr;
   };
   // entries [head, head + mid) of the row at d start on 16 bytes of the output
   auto head_of = [&](const float* d) {
     return EVEN ? 0 : min(n, (int)((0u - (unsigned)((uintptr_t)d >> 2)) & 3u));
   };
   auto fetch = [&](int k, const T* s, const float* d, Row& row) {
-    const int32_t* words = words_of(k);
+    const unsigned* words = words_of(k);
     const int head = head_of(d), end = EVEN ? n : head + ((n - head) & ~3);
     row.let = 0xffffffffu;
     if (words) {
-      row.let = 0;
+      row.let = 1u << 31;
 #pragma unroll
       for (int q = 0; q < kQuads; ++q) {
         const int o = head + 4 * (q * kThreads + tid);
-        if (o < end) {
-          const int wd = o >> 5;
-          unsigned b = (unsigned)__ldg(words + wd) >> (o & 31);
-          if (!EVEN && (o & 31) > 28) b |= (unsigned)__ldg(words + wd + 1) << (32 - (o & 31));
-          row.let |= (b & 15u) << (4 * q);
-        }
+        if (o < end) row.let |= nibble(words, o) << (4 * q);
       }
     }
 #pragma unroll
     for (int q = 0; q < kQuads; ++q) {
       const int o = head + 4 * (q * kThreads + tid);
       bool want = o < end && (row.let >> (4 * q) & 15u);
-      if (a.in_place && !words) want = want && rules && (EVEN ? hits[q] : nibble(sm.hit, o));
+      if (a.in_place && !words) want = want && hits_at(head, q);
       if (want) row.x[q].load(s + o, a.alike, a.logits_end);
+    }
+    if (!EVEN && tid < n - (end - head)) {
+      const int o = tid < head ? tid : end - head + tid;
+      const bool may = !words || (words[o >> 5] >> (o & 31) & 1u);
+      if (may) row.edge = load1(s + o);
+      else row.let &= ~(1u << 31);
     }
   };
   bool added = false;  // some row's path is in the addends
@@ -412,14 +467,15 @@ __global__ void __launch_bounds__(kThreads, 4) rules_kernel(Args a) {
   for (int k = 0; k < rows; ++k, src += a.stride, dst += a.V) {
     Row row = next;
     if (k + 1 < rows) fetch(k + 1, src + a.stride, dst + a.V, next);
-    const int32_t* words = words_of(k);
+    const unsigned* words = words_of(k);
     const bool sparse = a.in_place && !words;  // only touched entries change
     const int head = head_of(dst), end = EVEN ? n : head + ((n - head) & ~3);
+    const bool odd = sizeof(T) == 2 && !a.alike && ((uintptr_t)(src + head) & 2);
     if (paths) {
       const bool some = on_path(k);
       if (some || added) {  // the same for the whole CTA
         __syncthreads();
-        if (tid > 0 && mine(node_t)) {
+        if (tid > 0 && tid < w.rows && mine(node_t)) {
           // (nodes with the same token write the same)
           int c = node_n;
           for (int q = 0; q < kMaxRows / 32; ++q)
@@ -438,8 +494,8 @@ __global__ void __launch_bounds__(kThreads, 4) rules_kernel(Args a) {
     for (int q = 0; q < kQuads; ++q) {
       const int o = head + 4 * (q * kThreads + tid);
       const unsigned let = row.let >> (4 * q) & 15u;
-      const unsigned hit = !rules ? 0u : EVEN ? hits[q] : o < end ? nibble(sm.hit, o) : 0u;
-      float4 x = row.x[q].get();
+      const unsigned hit = hits_at(head, q);
+      float4 x = row.x[q].get(odd);
       if (__any_sync(0xffffffffu, hit & let)) {
         if (o < end) {
           const unsigned seen = nibble(sm.seen, o);
@@ -461,12 +517,9 @@ __global__ void __launch_bounds__(kThreads, 4) rules_kernel(Args a) {
     const int rest = n - (end - head);
     if (!EVEN && tid < rest) {  // what no 16 bytes of the output hold
       const int o = tid < head ? tid : end - head + tid;
-      const bool may = !words || ((unsigned)__ldg(words + (o >> 5)) >> (o & 31) & 1u);
-      float y = -INFINITY;
-      if (may) {
-        y = load1(src + o);
-        if (rules) y = shaped(y, sm.add[o], sm.seen[o >> 5] >> (o & 31) & 1u);
-      }
+      float y = row.edge;
+      if (rules) y = shaped(y, sm.add[o], sm.seen[o >> 5] >> (o & 31) & 1u);
+      if (!(row.let >> 31)) y = -INFINITY;
       dst[o] = y;
     }
   }
@@ -526,10 +579,13 @@ extern "C" sv_status sv_shape_logits(const sv_batch* bt, const void* logits, int
   const int nsm = num_sms();
   if (nsm < 1) return SV_ERR_CUDA;
   const int slices = (vocab + rul::kSlice - 1) / rul::kSlice;
-  // rows of a CTA: all of a request's, unless that leaves room for more CTAs
-  const long fair = (long)bt->total_rows * slices / ((long)nsm * 6);
-  a.chunk = (int)max(1L, min((long)rul::kMaxChunk, fair));
-  a.chunks = (bt->max_rows_per_req + a.chunk - 1) / a.chunk;
+  // rows of a CTA: all of a request's, unless that leaves places for CTAs
+  // empty: a CTA's rows follow one another, its rules cost a few rows' time
+  const long room = (long)nsm * rul::kCtasPerSm;
+  const long fair = ((long)bt->total_rows * slices + room - 1) / room;
+  const int most = (int)max(1L, min((long)rul::kMaxChunk, fair));
+  a.chunks = (bt->max_rows_per_req + most - 1) / most;
+  a.chunk = (bt->max_rows_per_req + a.chunks - 1) / a.chunks;
   const long units = (long)bt->n_req * a.chunks, ctas = units * slices;
   if (ctas > 0x7fffffffL) return SV_ERR_UNSUPPORTED_SHAPE;
   a.units = (int)units;
