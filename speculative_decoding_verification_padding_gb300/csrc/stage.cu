@@ -14,16 +14,24 @@
 // of itself, 0.06 rad at a million.  The turn inv_freq / (2 pi) is kept as a
 // 64-bit binary fraction instead, and position * turn modulo one turn is a
 // 64-bit integer product: what wraps away is whole turns.  The fraction is
-// good to 2^-53 of a turn of inv_freq / (2 pi), so a position of 2^31 still
-// has an angle good to 2^-20; fp64 is used once per thread, not per row.
+// the fp32 mantissa times 2^64 / (2 pi), shifted by the exponent, good to a
+// few units of 2^-64 for frequencies up to 1; no fp64, which this GPU has
+// little of (it cost a quarter of a microsecond per row of a CTA).
 //
 // Bound: HBM for many rows (each element read once and written once), launch
-// and one load latency for few.  A CTA takes whole rows, so that the row's
-// sines are computed once for all its heads; a thread holds up to kVecs
-// 16-byte vectors of the row, all loaded before the sines are computed.
-// Eight or sixteen neighbouring lanes hold one head (64 or 128 elements), so
-// a norm is three or four shuffles, and a pair's partner is in another lane
-// of the same head (halves) or in the same vector (pairs side by side).
+// and one load latency for few.  A piece is 16 elements of a head, two 16-byte
+// vectors chosen so that both elements of every pair are the same thread's (8
+// elements of the first half and their 8 partners of the second, or 16
+// neighbours), and it lies at the same place of every head a thread works on:
+// the rotation needs no exchange between lanes, and a row's sine and cosine
+// are read from shared memory once for all its heads.  (With 8 elements per
+// lane and shuffles for the partners, shared-memory and shuffle traffic
+// bounded the kernel at 43 % of HBM.)  A norm is two or three shuffles.
+// Many rows: each goes to a warp, which loads kVecs pieces per lane ahead of
+// the kVecs it works on, over the end of the row; the next row's sines are
+// computed under its last loads.  Few: a CTA for each, all its loads at once.
+// 20000 rows of 80 heads of 128: 133 us, 6.15 TB/s, 0.91 of the measured copy
+// rate; six rows of 48 heads: 3.0 us.
 
 #include <limits.h>
 
@@ -49,156 +57,299 @@ struct Args {
   float eps, scale;
 };
 
-constexpr int kVecs = 4;          // vectors of a row in flight per thread
-constexpr int kMaxThreads = 320;
+constexpr int kVecs = 3;          // pieces of a thread's round; two rounds are in flight
+constexpr int kMaxThreads = 512;
+// Rows per SM from which a warp takes whole rows (56 heads of 128: 2000 rows
+// 13.5 us in stream_kernel and 16.2 in row_kernel, 300 rows 8.5 and 4.5, 1280
+// rows 12.4 and 11.9).
+constexpr int kStreamRows = 12;
 constexpr int kMaxHalf = 64;      // rotated pairs of a head at most
 
-// inv_freq / (2 pi) modulo one turn, in units of 2^-64 of a turn.
+// f / (2 pi) modulo one turn, in units of 2^-64 of a turn.
 __device__ __forceinline__ unsigned long long turn_fraction(float f) {
-  const double t = (double)f * 0.15915494309189533577;  // 1 / (2 pi)
-  const double frac = t - floor(t);
-  return (unsigned long long)(frac * 18446744073709551616.0);  // 2^64; frac <= 1 - 2^-53
+  const unsigned long long kInv2Pi = 2935890503282001226ull;  // floor(2^64 / (2 pi))
+  const uint32_t u = __float_as_uint(f);
+  const int ex = (int)(u >> 23 & 255u);
+  const unsigned long long m = (u & 0x7fffffu) | (ex ? 0x800000u : 0u);
+  const int s = 150 - (ex ? ex : 1);  // f = m 2^-s
+  const unsigned long long lo = m * kInv2Pi, hi = __umul64hi(m, kInv2Pi);
+  unsigned long long t;
+  if (s <= 0) t = s > -64 ? lo << -s : 0ull;
+  else if (s < 64) t = lo >> s | hi << (64 - s);
+  else t = s < 128 ? hi >> (s - 64) : 0ull;
+  return u >> 31 ? 0ull - t : t;
 }
 
 __device__ __forceinline__ float lo_f(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float hi_f(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
 
+// Head h of row r: queries, then keys, then values.
 template <int D>
-__global__ void __launch_bounds__(kMaxThreads) stage_kernel(Args a) {
-  griddep_entry();
-  constexpr int kLanes = D / 8;  // lanes of a head
-  __shared__ float2 s_cs[2][kMaxHalf];  // (cos, sin) of this row and the next
-  const int tid = threadIdx.x, nt = blockDim.x;
-  const int half = a.rd >> 1;
-  const int heads = a.Hq + 2 * a.Hkv;
-  const int nvec = heads * kLanes;
-  // the frequency this thread turns every row's position by
-  unsigned long long frac = 0;
-  int axis = 0;
-  if (tid < half) {
-    frac = turn_fraction(a.inv_freq[tid]);
-    if (a.freq_axis) {
-      axis = a.freq_axis[tid];
-      if (axis < 0 || axis >= a.n_axes) {
-        flag(a.dev_status, SV_DEV_BAD_PARAM);
-        axis = 0;
+__device__ __forceinline__ const __nv_bfloat16* piece_of(const Args& a, long r, int h) {
+  if (h < a.Hq) return a.q + (size_t)r * a.q_stride + (size_t)h * D;
+  if (h < a.Hq + a.Hkv) return a.k + (size_t)r * a.k_stride + (size_t)(h - a.Hq) * D;
+  return a.v + (size_t)r * a.v_stride + (size_t)(h - a.Hq - a.Hkv) * D;
+}
+
+// (cos, sin) of pos turns of frac, times the scale.
+__device__ __forceinline__ float2 turn_by(const Args& a, int pos, unsigned long long frac) {
+  const long long turn = (long long)((unsigned long long)(long)pos * frac);
+  float sn, co;
+  sincospif((float)turn * 0x1p-63f, &sn, &co);  // signed: +- half a turn
+  return make_float2(co * a.scale, sn * a.scale);
+}
+
+// An axis that there is.
+__device__ __forceinline__ int checked_axis(const Args& a, int axis, bool used) {
+  if (!used || (axis >= 0 && axis < a.n_axes)) return used ? axis : 0;
+  flag(a.dev_status, SV_DEV_BAD_PARAM);
+  return 0;
+}
+
+// Piece c of head h of row r (its elements at g0 and g1 of the head): norm,
+// rotation, store.  Every lane of the warp calls it; `live` ones store.
+template <int D>
+__device__ __forceinline__ void finish(const Args& a, uint4 y0, uint4 y1, int h, bool live, int g0,
+                                       int g1, bool rot, const float4 (&cs)[4], long r,
+                                       size_t page) {
+  constexpr int kLanes = D / 16;
+  float f[16] = {lo_f(y0.x), hi_f(y0.x), lo_f(y0.y), hi_f(y0.y), lo_f(y0.z), hi_f(y0.z),
+                 lo_f(y0.w), hi_f(y0.w), lo_f(y1.x), hi_f(y1.x), lo_f(y1.y), hi_f(y1.y),
+                 lo_f(y1.z), hi_f(y1.z), lo_f(y1.w), hi_f(y1.w)};
+  const bool turns = h < a.Hq + a.Hkv;
+  const float* w = h < a.Hq ? a.qw : a.kw;
+  if (a.qw || a.kw) {
+    // (a head's lanes share a warp; those of V heads and past the row
+    // take part in the shuffles and keep their elements)
+    float ss = 0.f;
+#pragma unroll
+    for (int t = 0; t < 16; ++t) ss = fmaf(f[t], f[t], ss);
+#pragma unroll
+    for (int o = kLanes >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    if (turns && w) {
+      const float rs = rsqrtf(ss * (1.f / D) + a.eps);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const float4 ww = __ldg(reinterpret_cast<const float4*>(w + (t < 2 ? g0 : g1)) + (t & 1));
+        f[4 * t] *= rs * ww.x;
+        f[4 * t + 1] *= rs * ww.y;
+        f[4 * t + 2] *= rs * ww.z;
+        f[4 * t + 3] *= rs * ww.w;
       }
     }
   }
-  int par = 0;
-  for (int r = blockIdx.x; r < a.N; r += gridDim.x) {
-    const long slot = a.slots[r];
-    if (slot < 0 || slot >= a.n_slots) {  // the same for the whole CTA
-      if (slot != -1 && tid == 0) flag(a.dev_status, SV_DEV_BAD_SLOT);
-      continue;
-    }
-    const __nv_bfloat16* src[3] = {a.q + (size_t)r * a.q_stride, a.k + (size_t)r * a.k_stride,
-                                   a.v + (size_t)r * a.v_stride};
-    bool turned = half == 0;
-    for (int v0 = 0; v0 < nvec; v0 += kVecs * nt) {
-      uint4 x[kVecs];
+  if (rot && turns) {
 #pragma unroll
-      for (int u = 0; u < kVecs; ++u) {
-        const int vec = v0 + u * nt + tid;
-        x[u] = make_uint4(0u, 0u, 0u, 0u);
-        if (vec < nvec) {
-          int h = vec / kLanes, which = 0;
-          if (h >= a.Hq) { h -= a.Hq; which = 1; }
-          if (which && h >= a.Hkv) { h -= a.Hkv; which = 2; }
-          const __nv_bfloat16* p = which == 0 ? src[0] : which == 1 ? src[1] : src[2];
-          x[u] = *reinterpret_cast<const uint4*>(p + (size_t)h * D + (vec % kLanes) * 8);
-        }
-      }
-      if (!turned) {
-        // the row's sines, behind the loads; two rows' tables alternate, so
-        // one barrier per row is enough
-        if (tid < half) {
-          const long pos = a.positions[(size_t)axis * a.axis_stride + r];
-          const long long turn = (long long)((unsigned long long)pos * frac);  // signed: +- half a turn
-          float s, c;
-          sincospif((float)turn * 0x1p-63f, &s, &c);
-          s_cs[par][tid] = make_float2(c * a.scale, s * a.scale);
-        }
-        __syncthreads();
-        turned = true;
-      }
-#pragma unroll
-      for (int u = 0; u < kVecs; ++u) {
-        const int vec = v0 + u * nt + tid;
-        if (v0 + u * nt >= nvec) break;  // the same for the whole CTA
-        const int c = vec % kLanes;      // this lane's eighth of the head
-        int h = vec / kLanes, which = 0;
-        if (h >= a.Hq) { h -= a.Hq; which = 1; }
-        if (which && h >= a.Hkv) { h -= a.Hkv; which = 2; }
-        uint4 y = x[u];
-        float f[8] = {lo_f(y.x), hi_f(y.x), lo_f(y.y), hi_f(y.y),
-                      lo_f(y.z), hi_f(y.z), lo_f(y.w), hi_f(y.w)};
-        const float* w = which == 0 ? a.qw : a.kw;
-        // (a head's lanes always share a warp; lanes of V heads and past the
-        // row take part in the shuffles and keep their elements)
-        float ss = 0.f;
-#pragma unroll
-        for (int t = 0; t < 8; ++t) ss = fmaf(f[t], f[t], ss);
-#pragma unroll
-        for (int o = kLanes >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        if (w && which < 2) {
-          const float rs = rsqrtf(ss * (1.f / D) + a.eps);
-          const float4 w0 = *reinterpret_cast<const float4*>(w + c * 8);
-          const float4 w1 = *reinterpret_cast<const float4*>(w + c * 8 + 4);
-          f[0] = f[0] * rs * w0.x; f[1] = f[1] * rs * w0.y;
-          f[2] = f[2] * rs * w0.z; f[3] = f[3] * rs * w0.w;
-          f[4] = f[4] * rs * w1.x; f[5] = f[5] * rs * w1.y;
-          f[6] = f[6] * rs * w1.z; f[7] = f[7] * rs * w1.w;
-        }
-        if (half) {
-          if (a.inter) {
-            if (c * 8 < a.rd && which < 2) {
-#pragma unroll
-              for (int t = 0; t < 4; ++t) {
-                const float2 cs = s_cs[par][c * 4 + t];
-                const float p0 = f[2 * t], p1 = f[2 * t + 1];
-                f[2 * t] = p0 * cs.x - p1 * cs.y;
-                f[2 * t + 1] = p1 * cs.x + p0 * cs.y;
-              }
-            }
-          } else {
-            // element e < half pairs with e + half, half a multiple of 8:
-            // the partner is the same element of the lane half / 8 away
-            const int hl = half >> 3;
-            const int lane0 = (tid & 31) - c;
-            const int mate = c < hl ? c + hl : c < 2 * hl ? c - hl : c;
-            const float sgn = c < hl ? -1.f : 1.f;
-            const bool rot = c < 2 * hl && which < 2;
-            const int j0 = (c < hl ? c : c - hl) * 8;
-#pragma unroll
-            for (int t = 0; t < 8; ++t) {
-              const float o = __shfl_sync(0xffffffffu, f[t], lane0 + mate);
-              if (rot) {
-                const float2 cs = s_cs[par][j0 + t];
-                f[t] = f[t] * cs.x + sgn * o * cs.y;
-              }
-            }
-          }
-        }
-        if (which < 2) {
-          y.x = pack_bf16(f[0], f[1]);
-          y.y = pack_bf16(f[2], f[3]);
-          y.z = pack_bf16(f[4], f[5]);
-          y.w = pack_bf16(f[6], f[7]);
-        }
-        if (vec < nvec) {
-          __nv_bfloat16* dst;
-          if (which == 0) {
-            dst = a.out + ((size_t)r * a.Hq + h) * D;
-          } else {
-            const size_t page = (size_t)(slot / kBlockSize) * a.Hkv + h;
-            dst = (which == 1 ? a.kc : a.vc) + (page * kBlockSize + (size_t)(slot % kBlockSize)) * D;
-          }
-          *reinterpret_cast<uint4*>(dst + c * 8) = y;
-        }
+    for (int t = 0; t < 8; ++t) {
+      const float co = t & 1 ? cs[t >> 1].z : cs[t >> 1].x;
+      const float sn = t & 1 ? cs[t >> 1].w : cs[t >> 1].y;
+      if (a.inter) {
+        const float p0 = f[2 * t], p1 = f[2 * t + 1];
+        f[2 * t] = p0 * co - p1 * sn;
+        f[2 * t + 1] = p1 * co + p0 * sn;
+      } else {
+        const float p0 = f[t], p1 = f[t + 8];
+        f[t] = p0 * co - p1 * sn;
+        f[t + 8] = p1 * co + p0 * sn;
       }
     }
-    par ^= 1;
+  }
+  if (turns) {
+    y0 = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]),
+                    pack_bf16(f[6], f[7]));
+    y1 = make_uint4(pack_bf16(f[8], f[9]), pack_bf16(f[10], f[11]), pack_bf16(f[12], f[13]),
+                    pack_bf16(f[14], f[15]));
+  }
+  if (live) {
+    __nv_bfloat16* d;
+    if (h < a.Hq) d = a.out + ((size_t)r * a.Hq + h) * D;
+    else if (turns) d = a.kc + (page + (size_t)(h - a.Hq) * kBlockSize) * D;
+    else d = a.vc + (page + (size_t)(h - a.Hq - a.Hkv) * kBlockSize) * D;
+    *reinterpret_cast<uint4*>(d + g0) = y0;
+    *reinterpret_cast<uint4*>(d + g1) = y1;
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(32) stream_kernel(Args a) {
+  griddep_entry();
+  constexpr int kLanes = D / 16;  // lanes of a head
+  __shared__ __align__(16) float2 s_cs[2][kMaxHalf];  // (cos, sin) of this row and the next
+  const int tid = threadIdx.x;
+  constexpr int nt = 32;
+  const int half = a.rd >> 1;
+  const int heads = a.Hq + 2 * a.Hkv;
+  const int c = tid % kLanes, hs = tid / kLanes, hstep = nt / kLanes;
+  const bool rot = 16 * c < a.rd;  // rotary_dim is a multiple of 16: whole pieces
+  const int g0 = rot && !a.inter ? 8 * c : 16 * c;
+  const int g1 = rot && !a.inter ? half + 8 * c : 16 * c + 8;
+  // The frequencies this lane turns every row's position by, as loaded; what
+  // they make is computed behind the first row's loads.
+  constexpr int kFreqs = kMaxHalf / 32;
+  float freq[kFreqs];
+  int axis[kFreqs];
+#pragma unroll
+  for (int i = 0; i < kFreqs; ++i) {
+    const int j = tid + i * nt;
+    freq[i] = j < half ? a.inv_freq[j] : 0.f;
+    axis[i] = j < half && a.freq_axis ? a.freq_axis[j] : 0;
+  }
+  // Row r's slot and the positions its angles need, as loaded.
+  struct Ahead {
+    int slot;
+    int pos[kFreqs];
+  };
+  unsigned long long frac[kFreqs];
+  auto look = [&](long r, Ahead& n) {
+    n.slot = -1;
+    if (r < a.N) {
+      n.slot = a.slots[r];
+#pragma unroll
+      for (int i = 0; i < kFreqs; ++i)
+        if (tid + i * nt < half) n.pos[i] = a.positions[(size_t)axis[i] * a.axis_stride + r];
+    }
+  };
+  // The first row from r on (in steps of the grid) that is not skipped.
+  auto settle = [&](long& r, Ahead& n) {
+    while (r < a.N && (n.slot < 0 || n.slot >= a.n_slots)) {  // the same for the whole CTA
+      if (n.slot != -1 && tid == 0) flag(a.dev_status, SV_DEV_BAD_SLOT);
+      r += gridDim.x;
+      look(r, n);
+    }
+  };
+  auto turn_table = [&](const Ahead& n, float2* table) {
+#pragma unroll
+    for (int i = 0; i < kFreqs; ++i) {
+      const int j = tid + i * nt;
+      if (j < half) {
+        table[j] = turn_by(a, n.pos[i], frac[i]);
+      }
+    }
+  };
+  struct Round {
+    uint4 x[kVecs][2];
+  };
+  auto fetch = [&](long r, int h0, Round& n) {
+#pragma unroll
+    for (int u = 0; u < kVecs; ++u) {
+      const int h = h0 + u * hstep + hs;
+      if (h < heads) {
+        const __nv_bfloat16* p = piece_of<D>(a, r, h);
+        n.x[u][0] = *reinterpret_cast<const uint4*>(p + g0);
+        n.x[u][1] = *reinterpret_cast<const uint4*>(p + g1);
+      }
+    }
+  };
+  long r = blockIdx.x;
+  Ahead now;
+  Round next;
+  now.slot = a.slots[r];
+  fetch(r, 0, next);  // (a row that turns out to be skipped was read in vain)
+#pragma unroll
+  for (int i = 0; i < kFreqs; ++i) {
+    axis[i] = checked_axis(a, axis[i], tid + i * nt < half);
+    now.pos[i] = 0;
+    if (tid + i * nt < half) now.pos[i] = a.positions[(size_t)axis[i] * a.axis_stride + r];
+    frac[i] = turn_fraction(freq[i]);
+  }
+  if (now.slot < 0 || now.slot >= a.n_slots) {
+    settle(r, now);
+    if (r >= a.N) return;
+    fetch(r, 0, next);
+  }
+  turn_table(now, s_cs[0]);
+  for (int par = 0; r < a.N; par ^= 1) {
+    const long slot = now.slot;
+    const size_t page = (size_t)(slot / kBlockSize) * a.Hkv * kBlockSize + (size_t)(slot % kBlockSize);
+    long rn = r + gridDim.x;
+    look(rn, now);
+    __syncwarp();  // the row's table is there, the other one is free
+    float4 cs[4];     // this piece's eight pairs: (cos, sin, cos, sin)
+    if (rot) {
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+        cs[t] = *reinterpret_cast<const float4*>(&s_cs[par][8 * c + 2 * t]);
+    }
+    for (int h0 = 0; h0 < heads; h0 += kVecs * hstep) {
+      const Round x = next;
+      if (h0 + kVecs * hstep < heads) {
+        fetch(r, h0 + kVecs * hstep, next);
+      } else {
+        settle(rn, now);
+        if (rn < a.N) {
+          fetch(rn, 0, next);
+          turn_table(now, s_cs[par ^ 1]);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kVecs; ++u) {
+        if (h0 + u * hstep >= heads) break;  // the same for the whole CTA
+        const int h = h0 + u * hstep + hs;
+        finish<D>(a, x.x[u][0], x.x[u][1], h, h < heads, g0, g1, rot, cs, r, page);
+      }
+    }
+    r = rn;
+  }
+}
+
+// Few rows: a CTA for each, a piece or two per thread, every load the row needs
+// in flight at once.
+constexpr int kRowVecs = 2;
+template <int D>
+__global__ void __launch_bounds__(kMaxThreads, 2) row_kernel(Args a) {
+  griddep_entry();
+  constexpr int kLanes = D / 16;
+  __shared__ __align__(16) float2 s_cs[kMaxHalf];
+  const int tid = threadIdx.x, nt = blockDim.x;
+  const int half = a.rd >> 1;
+  const int heads = a.Hq + 2 * a.Hkv;
+  const int c = tid % kLanes, hs = tid / kLanes, hstep = nt / kLanes;
+  const bool rot = 16 * c < a.rd;
+  const int g0 = rot && !a.inter ? 8 * c : 16 * c;
+  const int g1 = rot && !a.inter ? half + 8 * c : 16 * c + 8;
+  const long r = blockIdx.x;
+  const long slot = a.slots[r];
+  float freq = 0.f;
+  int pos = 0;
+  if (tid < half) {
+    freq = a.inv_freq[tid];
+    const int axis = a.freq_axis ? checked_axis(a, a.freq_axis[tid], true) : 0;
+    pos = a.positions[(size_t)axis * a.axis_stride + r];
+  }
+  uint4 x[kRowVecs][2];
+  auto fetch = [&](int h0) {
+#pragma unroll
+    for (int u = 0; u < kRowVecs; ++u) {
+      const int h = h0 + u * hstep + hs;
+      x[u][0] = x[u][1] = make_uint4(0u, 0u, 0u, 0u);
+      if (h < heads) {
+        const __nv_bfloat16* p = piece_of<D>(a, r, h);
+        x[u][0] = *reinterpret_cast<const uint4*>(p + g0);
+        x[u][1] = *reinterpret_cast<const uint4*>(p + g1);
+      }
+    }
+  };
+  fetch(0);  // (a row that turns out to be skipped was read in vain)
+  if (slot < 0 || slot >= a.n_slots) {  // the same for the whole CTA
+    if (slot != -1 && tid == 0) flag(a.dev_status, SV_DEV_BAD_SLOT);
+    return;
+  }
+  if (tid < half) s_cs[tid] = turn_by(a, pos, turn_fraction(freq));
+  __syncthreads();
+  float4 cs[4];
+  if (rot) {
+#pragma unroll
+    for (int t = 0; t < 4; ++t) cs[t] = *reinterpret_cast<const float4*>(&s_cs[8 * c + 2 * t]);
+  }
+  const size_t page = (size_t)(slot / kBlockSize) * a.Hkv * kBlockSize + (size_t)(slot % kBlockSize);
+  for (int h0 = 0; h0 < heads; h0 += kRowVecs * hstep) {
+    if (h0 > 0) fetch(h0);
+#pragma unroll
+    for (int u = 0; u < kRowVecs; ++u) {
+      if (h0 + u * hstep >= heads) break;  // the same for the whole CTA
+      const int h = h0 + u * hstep + hs;
+      finish<D>(a, x[u][0], x[u][1], h, h < heads, g0, g1, rot, cs, r, page);
+    }
   }
 }
 
@@ -281,18 +432,25 @@ extern "C" sv_status sv_stage_qkv(const sv_paged_kv* kv, int32_t n_rows, const v
   a.Hq = n_q_heads;
   a.Hkv = kv->n_kv_heads;
   a.eps = eps;
-  const int nvec = (n_q_heads + 2 * kv->n_kv_heads) * (D / 8);
-  // threads: the fewest vectors each that keep the CTA at kMaxThreads, evenly
-  int per = 1;
-  while ((nvec + per - 1) / per > stg::kMaxThreads) ++per;
-  int threads = ((nvec + per - 1) / per + 31) / 32 * 32;
-  threads = max(threads, stg::kMaxHalf);  // a thread for every rotated pair
+  const int lanes = D / 16;
+  const long pieces = (long)(n_q_heads + 2 * kv->n_kv_heads) * lanes;
   const int nsm = num_sms();
   if (nsm < 1) return SV_ERR_CUDA;
-  const unsigned grid = (unsigned)min((long)n_rows, (long)nsm * (2048 / threads));
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (sv::launch(D == 64 ? stg::stage_kernel<64> : stg::stage_kernel<128>, grid, (unsigned)threads,
-                 0, s, a) != cudaSuccess)
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (n_rows >= (long)nsm * stg::kStreamRows) {
+    e = sv::launch(D == 64 ? stg::stream_kernel<64> : stg::stream_kernel<128>,
+                   (unsigned)min((long)n_rows, nsm * 32L), 32, 0, s, a);
+  } else {
+    // a thread for every piece while that leaves an SM's rows side by side
+    const long rows_per_sm = ((long)n_rows + nsm - 1) / nsm;
+    const long most = min((long)stg::kMaxThreads, 1024 / rows_per_sm / 32 * 32);
+    const unsigned threads =
+        (unsigned)max((long)stg::kMaxHalf, min(most, (pieces + 31) / 32 * 32));
+    e = sv::launch(D == 64 ? stg::row_kernel<64> : stg::row_kernel<128>, (unsigned)n_rows, threads,
+                   0, s, a);
+  }
+  if (e != cudaSuccess)
     return SV_ERR_CUDA;
   return SV_OK;
 }
