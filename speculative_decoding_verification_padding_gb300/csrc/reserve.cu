@@ -9,12 +9,15 @@
 // order) is free_list[free - 1 - k].
 //
 // Bound: latency.  A step moves a few KB; what costs is the chain offsets,
-// lengths -> table entries -> scan -> free list -> stores.  One CTA walks it
-// with every list spread flat over its threads (entries and rows, not
-// requests, so that one long request costs no more than many short ones),
-// the per-request state in shared memory.  Batches of more than kInlineRows
-// rows leave slots and positions to a second launch over all SMs.
-// Measured: see the figures at kInlineRows.
+// lengths -> table entries -> scan -> free list -> stores, and the search for
+// every row's request.  One CTA walks the chain with every list spread flat
+// over its threads (entries and rows, not requests, so that one long request
+// costs no more than many short ones), the per-request state in shared memory.
+// With more rows than threads, a cluster of up to eight CTAs walks it side by
+// side, each with the whole per-request state and a share of the rows: only
+// the first writes tables and counts, and what a row's check finds wrong is
+// told to all.  More rows than shared memory holds go to a second launch.
+// Measured: see the figures at kClusterRows.
 
 #include <limits.h>
 
@@ -37,18 +40,30 @@ struct Args {
   int32_t* dev_status;
   int R, N, max_rows, max_blocks, num_blocks, capacity;
   int inline_rows;  // this launch writes slots and positions too
+  int cluster;      // CTAs that share the rows
 };
 
-constexpr int kMaxRequests = 8192;  // four ints of shared memory each
-// Up to here the planning CTA writes the rows' slots and positions itself.
-constexpr int kInlineRows = 4096;
+constexpr int kMaxRequests = 8192;  // five ints of shared memory each
+// A CTA's share of the rows before another CTA joins its cluster.  Measured
+// with a copy of the tables before every call taken off: one chain 4.0 us, 256
+// chains of 5 rows 6.9, 512 of 2 to 9 (2816 rows) 8.0 (9.0 with twice the
+// share), 256 of 17 7.6 (17.6 in one CTA and a second launch), 2000 of 5 13.7
+// (27.6).
+constexpr int kClusterRows = 1024;
+constexpr int kMaxCluster = 8;
+constexpr size_t kMaxSmem = 200 * 1024;  // more: the rows go to a second launch
+// Chains without parents have nothing to check: from here on a second launch
+// over all SMs is faster (75000 rows 12.7 us against 17.9; 23000 rows 8.4 both).
+constexpr int kChainRows = 32768;
+constexpr int kRowUnroll = 2;    // rows of a thread side by side
 constexpr int kRowTile = 1024;  // rows per CTA of the second launch
 constexpr int kRowThreads = 256;
 
 // Shared memory: offsets [R + 1], entry prefix [R + 1], new blocks then start
-// rank [R], first new entry [R], parents [N] (rows handled inline).
-inline size_t plan_smem(int R, int N, bool rows) {
-  return sizeof(int) * (4 * (size_t)R + 2) + (rows ? (size_t)N : 0);
+// rank [R], first new entry [R], contexts [R]; for rows handled inline the
+// owners of this CTA's [share] and the parents of all [N].
+inline size_t plan_smem(int R, long share, long N) {
+  return sizeof(int) * (5 * (size_t)R + 2) + 2 * (size_t)((share + 1) & ~1L) + (size_t)N;
 }
 
 // The largest i in [0, n) with v[i] <= x (0 if there is none).
@@ -61,7 +76,9 @@ __device__ __forceinline__ int last_not_above(const int* v, int n, int x) {
   return lo;
 }
 
-// Exclusive prefix of v over the block's threads; *total is their sum.
+// Exclusive prefix of v over the block's threads; *total is their sum.  s_warp:
+// 32 words that no thread reads or writes from another scan without a barrier
+// between.
 __device__ __forceinline__ int block_scan(int v, int* s_warp, int* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int x = v;
@@ -70,7 +87,6 @@ __device__ __forceinline__ int block_scan(int v, int* s_warp, int* total) {
     const int y = __shfl_up_sync(0xffffffffu, x, o);
     if (lane >= o) x += y;
   }
-  __syncthreads();  // s_warp may still be read from the last scan
   if (lane == 31) s_warp[warp] = x;
   __syncthreads();
   int before = 0, sum = 0;
@@ -87,6 +103,11 @@ __device__ __forceinline__ int block_scan(int v, int* s_warp, int* total) {
   }
   *total = sum;
   return (warp ? before : 0) + x - v;
+}
+
+// The smaller of v and an int in the shared memory of any CTA of the cluster.
+__device__ __forceinline__ void dsmem_min(uint32_t at, int v) {
+  asm volatile("red.relaxed.cluster.shared::cluster.min.s32 [%0], %1;\n" ::"r"(at), "r"(v) : "memory");
 }
 
 // Parents as one byte: local indexes are below 128; anything else is -2.
@@ -114,8 +135,13 @@ __global__ void __launch_bounds__(1024) plan_kernel(Args a) {
   int* s_e0 = s_cu + R + 1;      // [R + 1] prefix of table entries looked at
   int* s_new = s_e0 + R + 1;     // [R] new blocks, then rank of the first (-1: refused)
   int* s_first = s_new + R;      // [R] first new entry (INT_MAX: none, -1: malformed)
-  int8_t* s_par = reinterpret_cast<int8_t*>(s_first + R);  // [N] with inline_rows
-  __shared__ int s_warp[32], s_popped, s_fc;
+  int* s_ctx = s_first + R;      // [R]
+  const int C = a.cluster, rank = C > 1 ? (int)cluster_rank() : 0;
+  const int share = a.inline_rows ? ((a.N + C - 1) / C + 1) & ~1 : 0;
+  const int row0 = rank * share, row1 = min(a.N, row0 + share);  // this CTA's rows
+  uint16_t* s_own = reinterpret_cast<uint16_t*>(s_ctx + R);  // [share] the row's request
+  int8_t* s_par = reinterpret_cast<int8_t*>(s_own + share);  // [N] with inline_rows
+  __shared__ int s_warp[4][32], s_popped, s_fc;  // a scan's two rounds alternate
   const int tid = threadIdx.x, nt = blockDim.x;
   if (tid == 0) {
     s_popped = 0;
@@ -126,8 +152,8 @@ __global__ void __launch_bounds__(1024) plan_kernel(Args a) {
     for (int r = tid; r < a.N; r += nt) s_par[r] = parent_byte(a.parent[r]);
 
   // ---- requests: offsets, lengths, how many table entries they span ----
-  int carry = 0;
-  for (int base = 0; base < R; base += nt) {
+  int carry = 0, turn = 0;
+  for (int base = 0; base < R; base += nt, turn ^= 1) {
     const int i = base + tid;
     int e = 0;
     if (i < R) {
@@ -136,76 +162,111 @@ __global__ void __launch_bounds__(1024) plan_kernel(Args a) {
       int finding = 0;
       if (rows < 1 || rows > a.max_rows || c0 < 0 || c1 > a.N) finding = SV_DEV_BAD_WINDOW;
       else if (ctx < 0 || ctx + rows > (long)a.max_blocks * kBlockSize) finding = SV_DEV_BAD_LENGTH;
-      if (finding) flag(a.dev_status, finding);
-      else e = (int)((ctx + rows + kBlockSize - 1) / kBlockSize - ctx / kBlockSize);
+      if (finding) {
+        if (rank == 0) flag(a.dev_status, finding);
+      } else e = (int)((ctx + rows + kBlockSize - 1) / kBlockSize - ctx / kBlockSize);
       s_cu[i] = (int)c0;
+      s_ctx[i] = (int)ctx;
       if (i == R - 1) s_cu[R] = (int)c1;
       s_new[i] = 0;
       s_first[i] = finding ? -1 : INT_MAX;
     }
     int total;
-    const int excl = block_scan(e, s_warp, &total);
+    const int excl = block_scan(e, s_warp[turn], &total);
     if (i < R) s_e0[i] = carry + excl;
     carry += total;
   }
   if (tid == 0) s_e0[R] = carry;
   const int E = carry;
-  __syncthreads();
+  // (every CTA's state is set up before another one may write to it)
+  if (C > 1) cluster_sync();
+  else __syncthreads();
 
   // ---- entries: which are new; rows: are the parents sound ----
   for (int x = tid; x < E; x += nt) {
     const int i = last_not_above(s_e0, R, x);
-    const int ctx = a.ctx[i];
+    const int ctx = s_ctx[i];
     const int t0 = ctx / kBlockSize, t = t0 + (x - s_e0[i]);
     const int id = a.tables[(size_t)i * a.max_blocks + t];
     // a block that holds committed tokens has to be there already
     if (id < -1 || id >= a.num_blocks || (id == -1 && t == t0 && ctx % kBlockSize)) {
-      flag(a.dev_status, SV_DEV_BAD_BLOCK_ID);
+      if (rank == 0) flag(a.dev_status, SV_DEV_BAD_BLOCK_ID);
       atomicMin(&s_first[i], -1);
     } else if (id == -1) {
       atomicAdd(&s_new[i], 1);
       atomicMin(&s_first[i], t);
     }
   }
-  if (a.parent && R > 0) {
-    for (int r = tid; r < a.N; r += nt) {
-      const int i = last_not_above(s_cu, R, r);
-      const int j = r - s_cu[i];
-      if (j < 0 || r >= s_cu[i + 1]) continue;
-      if (s_e0[i + 1] == s_e0[i]) continue;  // found malformed above
-      const int p = a.inline_rows ? s_par[r] : (int)parent_byte(a.parent[r]);
-      if (j == 0 ? p != -1 : (p < 0 || p >= j)) {
-        flag(a.dev_status, SV_DEV_BAD_PARENT);
-        atomicMin(&s_first[i], -1);
+  // (kRowUnroll rows of a thread side by side: a search is a chain of
+  // dependent reads)
+  if ((a.parent || a.inline_rows) && R > 0) {
+    const int from = a.inline_rows ? row0 : 0, to = a.inline_rows ? row1 : a.N;
+    for (int r0 = from + tid; r0 < to; r0 += kRowUnroll * nt) {
+      int own[kRowUnroll], p[kRowUnroll];
+#pragma unroll
+      for (int u = 0; u < kRowUnroll; ++u) {
+        const int r = r0 + u * nt;
+        p[u] = -2;
+        if (r < to && a.parent) p[u] = a.inline_rows ? s_par[r] : (int)parent_byte(a.parent[r]);
+        own[u] = 0;
+      }
+      // the largest i with s_cu[i] <= r, bit by bit from the top
+      for (int step = 32 - __clz(R); step > 0; --step) {
+#pragma unroll
+        for (int u = 0; u < kRowUnroll; ++u) {
+          const int at = own[u] + (1 << (step - 1));
+          if (at < R && s_cu[at] <= r0 + u * nt) own[u] = at;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kRowUnroll; ++u) {
+        const int r = r0 + u * nt;
+        if (r >= to) continue;
+        const int i = own[u], j = r - s_cu[i];
+        if (a.inline_rows) s_own[r - row0] = (uint16_t)i;
+        if (!a.parent || j < 0 || r >= s_cu[i + 1]) continue;
+        if (s_e0[i + 1] == s_e0[i]) continue;  // found malformed above
+        if (j == 0 ? p[u] != -1 : (p[u] < 0 || p[u] >= j)) {
+          flag(a.dev_status, SV_DEV_BAD_PARENT);
+          for (int c = 0; c < C; ++c) {  // in every CTA of the cluster
+            if (c == rank) atomicMin(&s_first[i], -1);
+            else dsmem_min(dsmem_addr(smem_u32(&s_first[i]), (uint32_t)c), -1);
+          }
+        }
       }
     }
   }
-  __syncthreads();
+  // (also: every CTA has looked at the table entries before the first writes new ones)
+  if (C > 1) cluster_sync();
+  else __syncthreads();
 
   // ---- requests: who is served ----
   const int fc = s_fc;
   carry = 0;
-  for (int base = 0; base < R; base += nt) {
+  turn = 0;
+  for (int base = 0; base < R; base += nt, turn ^= 1) {
     const int i = base + tid;
     int n = 0, first = -1;
     if (i < R) {
       n = s_new[i];
       first = s_first[i];
       // new entries end the range: none of them may lie before one in use
-      if (first >= 0 && n > 0 && first + n != a.ctx[i] / kBlockSize + s_e0[i + 1] - s_e0[i]) {
-        flag(a.dev_status, SV_DEV_BAD_BLOCK_ID);
+      if (first >= 0 && n > 0 && first + n != s_ctx[i] / kBlockSize + s_e0[i + 1] - s_e0[i]) {
+        if (rank == 0) flag(a.dev_status, SV_DEV_BAD_BLOCK_ID);
         s_first[i] = first = -1;
       }
       if (first < 0) n = 0;
     }
     int total;
-    const int start = carry + block_scan(n, s_warp, &total);
+    const int start = carry + block_scan(n, s_warp[2 + turn], &total);
     if (i < R) {
       const bool fits = n == 0 || start + n <= fc;
       const bool served = first >= 0 && fits;
-      if (!fits) flag(a.dev_status, SV_DEV_POOL_EMPTY);
       s_new[i] = served ? start : -1;
-      a.taken[i] = served ? n : -1;
+      if (rank == 0) {
+        if (!fits) flag(a.dev_status, SV_DEV_POOL_EMPTY);
+        a.taken[i] = served ? n : -1;
+      }
       if (served && n > 0) atomicMax(&s_popped, start + n);
     }
     carry += total;
@@ -213,40 +274,47 @@ __global__ void __launch_bounds__(1024) plan_kernel(Args a) {
   __syncthreads();
 
   // ---- entries: the new ones take their block ----
-  for (int x = tid; x < E; x += nt) {
+  for (int x = tid; rank == 0 && x < E; x += nt) {
     const int i = last_not_above(s_e0, R, x);
-    const int t = a.ctx[i] / kBlockSize + (x - s_e0[i]);
+    const int t = s_ctx[i] / kBlockSize + (x - s_e0[i]);
     const int start = s_new[i], first = s_first[i];
     if (start < 0 || t < first) continue;
     const int id = a.free_list[fc - 1 - (start + t - first)];
     if (id >= 0 && id < a.num_blocks) a.tables[(size_t)i * a.max_blocks + t] = id;
     else flag(a.dev_status, SV_DEV_BAD_BLOCK_ID);  // the entry stays -1
   }
-  if (tid == 0 && s_popped > 0) *a.free_count = fc - s_popped;
-  if (!a.inline_rows) return;
+  if (rank == 0 && tid == 0 && s_popped > 0) *a.free_count = fc - s_popped;
 
   // ---- rows: slot and position (ids straight from the free list) ----
-  for (int r = tid; r < a.N; r += nt) {
-    int slot = -1, pos = -1;
-    const int i = R > 0 ? last_not_above(s_cu, R, r) : 0;
-    const int j = R > 0 ? r - s_cu[i] : -1;
-    if (j >= 0 && r < s_cu[i + 1] && s_new[i] >= 0) {
-      const int ctx = a.ctx[i];
-      const int t = (ctx + j) / kBlockSize, first = s_first[i];
-      const int id = t < first ? a.tables[(size_t)i * a.max_blocks + t]
-                               : a.free_list[fc - 1 - (s_new[i] + t - first)];
-      if (id >= 0 && id < a.num_blocks) {
-        int depth = j;
-        if (a.parent) {
-          const int8_t* par = s_par + s_cu[i];
-          depth = depth_of(par, j);
-        }
-        slot = id * kBlockSize + (ctx + j) % kBlockSize;
-        pos = ctx + (a.pos_offset ? a.pos_offset[i] : 0) + depth;
-      }
+  if (!a.inline_rows) return;
+  for (int r0 = row0 + tid; r0 < row1; r0 += kRowUnroll * nt) {
+    int id[kRowUnroll], off[kRowUnroll];
+#pragma unroll
+    for (int u = 0; u < kRowUnroll; ++u) {  // every row's loads
+      const int r = r0 + u * nt;
+      id[u] = -1;
+      off[u] = 0;
+      if (r >= row1 || R == 0) continue;
+      const int i = s_own[r - row0], j = r - s_cu[i];
+      if (j < 0 || r >= s_cu[i + 1] || s_new[i] < 0) continue;
+      const int t = (s_ctx[i] + j) / kBlockSize, first = s_first[i];
+      id[u] = t < first ? a.tables[(size_t)i * a.max_blocks + t]
+                        : a.free_list[fc - 1 - (s_new[i] + t - first)];
+      if (a.pos_offset && a.positions) off[u] = a.pos_offset[i];
     }
-    a.slots[r] = slot;
-    if (a.positions) a.positions[r] = pos;
+#pragma unroll
+    for (int u = 0; u < kRowUnroll; ++u) {
+      const int r = r0 + u * nt;
+      if (r >= row1) continue;
+      int slot = -1, pos = -1;
+      if (id[u] >= 0 && id[u] < a.num_blocks) {
+        const int i = s_own[r - row0], j = r - s_cu[i], ctx = s_ctx[i];
+        slot = id[u] * kBlockSize + (ctx + j) % kBlockSize;
+        if (a.positions) pos = ctx + off[u] + (a.parent ? depth_of(s_par + s_cu[i], j) : j);
+      }
+      a.slots[r] = slot;
+      if (a.positions) a.positions[r] = pos;
+    }
   }
 }
 
@@ -329,20 +397,28 @@ extern "C" sv_status sv_reserve_kv(const sv_paged_kv* kv, const sv_batch* bt,
   a.max_blocks = kv->max_blocks_per_req;
   a.num_blocks = kv->num_blocks;
   a.capacity = pool->capacity;
-  a.inline_rows = a.N <= rsv::kInlineRows ? 1 : 0;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const size_t smem = rsv::plan_smem(a.R, a.N, a.inline_rows != 0);
+  a.cluster = 1;
+  while (a.cluster < rsv::kMaxCluster && a.N > (long)a.cluster * rsv::kClusterRows) a.cluster *= 2;
+  size_t smem = rsv::plan_smem(a.R, (a.N + a.cluster - 1) / a.cluster, a.N);
+  a.inline_rows = smem <= rsv::kMaxSmem && (a.parent || a.N <= rsv::kChainRows) ? 1 : 0;
+  if (!a.inline_rows) {
+    a.cluster = 1;
+    smem = rsv::plan_smem(a.R, 0, 0);
+  }
   if (smem > 48 * 1024) {
     static PerDevice smem_set;
-    if (smem_limit_once(smem_set, rsv::plan_kernel,
-                        rsv::plan_smem(rsv::kMaxRequests, rsv::kInlineRows, true)) != cudaSuccess)
+    if (smem_limit_once(smem_set, rsv::plan_kernel, rsv::kMaxSmem) != cudaSuccess)
       return SV_ERR_CUDA;
   }
   // one thread per row or request, up to a full CTA: few warps meet a
   // barrier sooner
   const int want = max(a.R, min(a.N, 1024));
   const unsigned threads = (unsigned)max(128, min(1024, (want + 31) / 32 * 32));
-  if (sv::launch(rsv::plan_kernel, 1, threads, smem, s, a) != cudaSuccess) return SV_ERR_CUDA;
+  const cudaError_t e =
+      a.cluster > 1 ? sv::launch_cluster(rsv::plan_kernel, (unsigned)a.cluster, threads, smem, s, a.cluster, a)
+                    : sv::launch(rsv::plan_kernel, 1, threads, smem, s, a);
+  if (e != cudaSuccess) return SV_ERR_CUDA;
   if (!a.inline_rows) {
     const unsigned grid = (unsigned)(((long)a.N + rsv::kRowTile - 1) / rsv::kRowTile);
     if (sv::launch(rsv::rows_kernel, grid, rsv::kRowThreads, 0, s, a) != cudaSuccess)
