@@ -229,7 +229,8 @@ sv_status sv_tree_attend(const sv_paged_kv* kv, const sv_batch* batch, const voi
  * A window starting at row 0 resets the request's state; a later window
  * continues it (requests already decided are skipped).
  * target_logits, draft_logits: fp32 [total_rows][vocab]; draft_logits may be
- * NULL when temperature == 0.
+ * NULL when temperature == 0.  A logit of -inf (a barred token) has
+ * probability 0; every row needs one that is finite.
  * ws: at least sv_accept_workspace() bytes, 256-byte aligned. */
 size_t sv_accept_workspace(const sv_batch* batch, int32_t vocab);
 sv_status sv_accept(const sv_batch* batch, const float* target_logits, const float* draft_logits,

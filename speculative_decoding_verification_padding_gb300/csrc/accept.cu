@@ -743,7 +743,7 @@ __global__ void __launch_bounds__(kStatThreads, 4) stats_kernel(Args a) {
             l *= ex2((m - x) * kLog2e);
             m = x;
           }
-          l += ex2((x - m) * kLog2e);
+          if (m != -INFINITY) l += ex2((x - m) * kLog2e);  // (-inf alone adds nothing)
         }
       }
     } else {
