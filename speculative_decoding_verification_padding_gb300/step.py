@@ -10,6 +10,10 @@ outputs and workspaces with torch, and enqueues the library calls of a step:
   budget    sv_select_budget -> sv_tree_attend -> sv_accept_commit,
             with the selected verify_len feeding the batch
 
+``EdgeStep`` runs a one-pass step with its two edges, from projections and raw
+logits: sv_reserve_kv -> sv_stage_qkv -> sv_tree_attend -> sv_shape_logits ->
+sv_accept_commit.
+
 ``HostPipeline`` runs such steps on inputs that arrive in pinned host memory,
 double-buffered so that the next step's upload overlaps this step's kernels.
 
@@ -19,6 +23,7 @@ Nothing here computes any part of the step; it only moves memory and calls.
 from __future__ import annotations
 
 import copy
+import dataclasses
 
 import numpy as np
 import torch
@@ -224,6 +229,74 @@ class DeviceStep:
             "done": self.done.cpu().numpy(),
             "dev_status": int(self.dev_status.item()),
         }
+
+
+def unstaged(w: Workload) -> Workload:
+    """The workload before its rows were staged: the blocks behind each
+    request's context are back in the pool."""
+    tables = w.block_tables.copy()
+    free = [int(b) for b in w.free_list[:w.free_count]]
+    for i, ctx in enumerate(w.cache_lens):
+        behind = tables[i, -(-int(ctx) // 16):]
+        free += [int(b) for b in behind if b >= 0]
+        behind[:] = -1
+    free_list = np.full_like(w.free_list, -1)
+    free_list[:len(free)] = free
+    return dataclasses.replace(w, block_tables=tables, free_list=free_list, free_count=len(free))
+
+
+class EdgeStep(DeviceStep):
+    """A one-pass step with its two edges.  ``q``, ``k``, ``v`` (bf16
+    [rows][heads][dim], views of one projection output will do) are turned
+    and staged into blocks that the step takes from the pool itself; the
+    workload's target and draft logits (fp32 or bf16) are shaped by ``rules``
+    before they are tested.  Without rules the logits are tested as they are.
+    """
+
+    def __init__(self, w: Workload, q, k, v, rotary=None, rules=None, q_weight=None,
+                 k_weight=None, eps: float = 1e-6, pos_offset=None, device="cuda"):
+        super().__init__(unstaged(w), device, mode="onepass")
+        self.qkv, self.rotary, self.rules = (q, k, v), rotary, rules
+        self.weights, self.eps, self.pos_offset = (q_weight, k_weight), eps, pos_offset
+        n, rows = w.n_req, w.total_rows
+        new = lambda m: torch.full((m,), -1, dtype=torch.int32, device=device)
+        self.slots, self.positions, self.taken = new(rows), new(rows), new(n)
+        self.raw = (self.target, self.draft)
+        if rules is not None:
+            self.target = torch.empty_like(self.target)
+            self.draft = None if self.draft is None else torch.empty_like(self.draft)
+
+    def reserve(self):
+        self._bound("reserve", self.batch, lambda: api.bind_reserve_kv(
+            self.kv, self.batch, self.pool, self.slots, self.positions, self.taken,
+            self.pos_offset, self.dev_status))()
+
+    def stage(self):
+        self._bound("stage", self.batch, lambda: api.bind_stage_qkv(
+            self.kv, *self.qkv, self.slots, None if self.rotary is None else self.positions,
+            self.rotary, self.q, *self.weights, self.eps, self.dev_status))()
+
+    def shape(self):
+        for name, raw, out in (("shape target", self.raw[0], self.target),
+                               ("shape draft", self.raw[1], self.draft)):
+            if raw is not None and self.rules is not None:
+                self._bound(name, self.batch, lambda: api.bind_shape_logits(
+                    self.batch, raw, self.rules, out, self.dev_status))()
+
+    def run(self, commit: bool = True, restore: bool = True):
+        if restore:
+            self.restore_cache_state()
+        self.reserve()
+        self.stage()
+        self.attend()
+        self.shape()
+        if commit:
+            self.accept_commit()
+        else:
+            self.accept()
+
+    def _twin(self):
+        raise NotImplementedError("an EdgeStep's inputs are its projections and raw logits")
 
 
 class HostPipeline:
