@@ -225,3 +225,41 @@ def test_reserve_and_commit_conserve_the_pool():
     held = tables[tables >= 0].tolist() + pool[:n].cpu().tolist()
     assert len(held) == len(set(held)) == c.blocks - 2
     assert (tables >= 0).sum() == (-(-(c.ctx + 1) // 16)).sum()
+
+
+def test_faults_found_anywhere_in_a_large_batch():
+    # the rows of 300 trees are shared by several CTAs: each finds some faults
+    rng = np.random.default_rng(13)
+    c = Case(rng.integers(15, 40, 300), rng.integers(0, 300, 300), "tree", seed=13)
+    bad = rng.choice(300, 40, replace=False)
+    for i in bad:
+        j = int(rng.integers(1, c.rows[i]))
+        c.parent[c.cu[i] + j] = rng.choice([j, -1, 127, 1 << 20])
+    ref = c.check(c.run(), err=edges.BAD_PARENT)
+    assert (ref["taken"][bad] == -1).all() and (ref["taken"] >= 0).sum() == 260
+
+
+def test_more_rows_than_shared_memory_holds():
+    rng = np.random.default_rng(14)
+    c = Case(rng.integers(120, 129, 1600), rng.integers(0, 100, 1600), "tree", seed=14, pad=77)
+    c.parent[c.cu[700] + 9] = 9
+    c.check(c.run(), err=edges.BAD_PARENT)
+    c = Case([40000, 1, 3001, 29], [0, 31, 7, 0], "prompt", pad=3)
+    c.check(c.run())
+
+
+def test_two_batches_at_once_on_two_streams():
+    cases = [_rng_case(200, 30, "tree", seed=20 + k) for k in range(2)]
+    for c in cases:
+        c.run()
+    streams = [torch.cuda.Stream() for _ in cases]
+    for _ in range(20):
+        for c, s in zip(cases, streams):
+            d = c.keep[2]
+            with torch.cuda.stream(s):
+                d["tables"].copy_(torch.from_numpy(c.tables), non_blocking=False)
+                d["count"].fill_(c.free)
+                c.call()
+    torch.cuda.synchronize()
+    for c in cases:
+        c.check(c.keep[2])

@@ -1,9 +1,10 @@
 """sv_shape_logits against the CPU oracle (fp64).
 
-Bound of a touched logit, from the arithmetic: a division or product, the
-product and sum of the penalties, their subtraction and the bias's addition
-round to fp32 once each, so six halves of a step, 6 * 2^-24 of the sum of the
-absolute values that are added up.  Untouched logits are equal to the input,
+Bound of a touched logit, from the arithmetic: the reciprocal of the repetition
+penalty and the product with it, the product and sum of the other penalties,
+the bias's addition to those and their addition to the logit round to fp32
+once each, so six halves of a step, 6 * 2^-24 of the sum of the absolute values
+that are added up.  Untouched logits are equal to the input,
 barred ones are -inf.
 """
 
@@ -330,6 +331,40 @@ def test_stream_and_graph_and_repeats():
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(c.out, first)
+
+
+def test_two_batches_at_once_on_two_streams():
+    cases = [Case([9] * 20, 9000, tree=True, bias=20, masks=0.5, few=True, seed=k) for k in range(2)]
+    calls = [c.bind() for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for call, s in zip(calls, streams):
+            call(s)
+    for c in cases:
+        c.check()
+
+
+def test_more_logits_than_32_bits_count():
+    # 2.2 billion logits: the last rows' offsets pass 2^31 and 2^32 bytes
+    V, N = 151936, 14500
+    g = torch.Generator("cuda").manual_seed(0)
+    x = torch.empty(N, V, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    out = torch.empty(N, V, device="cuda")
+    cu = torch.arange(0, N + 1, 5, dtype=torch.int32, device="cuda")
+    parent = (torch.arange(N, device="cuda") % 5 - 1).int()
+    R = N // 5
+    b = api.Batch(cu, parent, torch.full((N,), 7, dtype=torch.int32, device="cuda"), 5)
+    one = torch.ones(R, device="cuda")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    api.sv_shape_logits(b, x, api.LogitRules(presence=one, frequency=one), out, st)
+    assert st.item() == 0
+    j = torch.arange(N, device="cuda") % 5
+    want = x[:, 7].float() - (j + (j > 0)).float()  # the path's drafts are all token 7
+    assert ((out[:, 7] - want).abs() <= 2.0 ** -21 * (x[:, 7].float().abs() + 5)).all()
+    out[:, 7] = x[:, 7].float()
+    for r in range(0, N, 2900):
+        assert torch.equal(out[r:r + 2900], x[r:r + 2900].float())
 
 
 @pytest.mark.parametrize("over,words", [

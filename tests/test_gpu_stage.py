@@ -191,6 +191,39 @@ def test_shared_position_for_every_axis():
     c.check()
 
 
+def test_far_blocks_and_two_streams_at_once():
+    # cache slots whose element offsets pass 2^31, and two calls side by side
+    K, D, blocks = 8, 128, 140000
+    kc = torch.zeros(blocks, K, 16, D, dtype=torch.bfloat16, device="cuda")
+    vc = torch.zeros_like(kc)
+    c = Case(40, 8, K, D)
+    d = Case(40, 8, K, D, seed=1)
+    z = torch.zeros(1, 1, dtype=torch.int32, device="cuda")
+    calls = []
+    for k, case in enumerate((c, d)):
+        case.slots = (torch.arange(40) * 2 + k + (blocks - 5) * 16).int()
+        calls.append(case.bind(kv=api.PagedKV(kc, vc, z, z[0])))
+    torch.cuda.synchronize()
+    for call in calls:
+        call(torch.cuda.Stream())
+    torch.cuda.synchronize()
+    for case in (c, d):
+        small = {"kc": case.kc, "vc": case.vc}
+        at = case.slots.long().cuda()
+        for name, big in (("kc", kc), ("vc", vc)):
+            got = big[at // 16, :, at % 16]
+            # the same rows into a small cache, whose result test_head_layouts checks
+            assert (got.float().abs().sum((1, 2)) > 0).all()
+            small[name] = got
+        case.slots = torch.arange(40).int()
+        case.bind()()
+        torch.cuda.synchronize()
+        at = case.slots.long().cuda()
+        assert torch.equal(case.dev["kc"][at // 16, :, at % 16], small["kc"])
+        assert torch.equal(case.dev["vc"][at // 16, :, at % 16], small["vc"])
+    assert kc[: blocks - 5].abs().max() == 0
+
+
 def test_stream_and_graph():
     c = Case(21, 8, 2, 64)
     s = torch.cuda.Stream()
