@@ -191,6 +191,56 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) rules_kernel(Args a) {
   const T* src = static_cast<const T*>(a.logits) + (size_t)ra * a.stride + lo;
   float* dst = a.out + (size_t)ra * a.V + lo;
 
+  // This thread's touched entries, four bits a quad: sixteen bits for each
+  // place that a row can start at.
+  static_assert(kQuads == 4, "");
+  uint64_t hits4 = 0;
+  auto hits_at = [&](int head, int q) { return (unsigned)(hits4 >> (16 * head + 4 * q)) & 15u; };
+  // Each row is loaded (its mask's bits first) before the row before it is
+  // worked on.
+  using Quad = typename QuadOf<T>::type;
+  struct Row {
+    Quad x[kQuads];
+    unsigned let;  // permitted entries, four bits a quad; the top bit: the edge
+    float edge;    // !EVEN: one of the entries that no 16 bytes of the output hold
+  };
+  auto words_of = [&](int k) -> const unsigned* {
+    return ru.mask && sm.masked[k] >= 0 ? sm.words[k] : nullptr;
+  };
+  // entries [head, head + mid) of the row at d start on 16 bytes of the output
+  auto head_of = [&](const float* d) {
+    return EVEN ? 0 : min(n, (int)((0u - (unsigned)((uintptr_t)d >> 2)) & 3u));
+  };
+  auto fetch = [&](int k, const T* s, const float* d, Row& row) {
+    const unsigned* words = words_of(k);
+    const int head = head_of(d), end = EVEN ? n : head + ((n - head) & ~3);
+    row.let = 0xffffffffu;
+    if (words) {
+      row.let = 1u << 31;
+#pragma unroll
+      for (int q = 0; q < kQuads; ++q) {
+        const int o = head + 4 * (q * kThreads + tid);
+        if (o < end) row.let |= nibble(words, o) << (4 * q);
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < kQuads; ++q) {
+      const int o = head + 4 * (q * kThreads + tid);
+      bool want = o < end && (row.let >> (4 * q) & 15u);
+      if (a.in_place && !words) want = want && hits_at(head, q);
+      if (want) row.x[q].load(s + o, a.alike, a.logits_end);
+    }
+    if (!EVEN && tid < n - (end - head)) {
+      const int o = tid < head ? tid : end - head + tid;
+      const bool may = !words || (words[o >> 5] >> (o & 31) & 1u);
+      if (may) row.edge = load1(s + o);
+      else row.let &= ~(1u << 31);
+    }
+  };
+  // (in place, which entries to load is known only when the rules are)
+  const bool early = !a.in_place;
+  Row next;
+
   // ---- its rules in shared memory ----
   // What these need is loaded before the first barrier: the tree (one node a
   // thread), the rows' mask numbers, the head of the history.
@@ -344,6 +394,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) rules_kernel(Args a) {
       if (mine(v)) atomicMin(&s_first[v - lo], (unsigned)(t - b0));
     }
     __syncthreads();
+    if (early) fetch(0, src, dst, next);  // under what is left to do for the rules
     if (paths) {
       if (tid > 0 && tid < w.rows && mine(node_t)) {
         node_n = (int)(sm.cnt[node_t - lo] & ~kDraft);
@@ -404,10 +455,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) rules_kernel(Args a) {
     const float y = x * (x > 0.f ? inv : rho);
     return (seen ? y : x) + add;
   };
-  // This thread's touched entries, four bits a quad: sixteen bits for each
-  // place that a row can start at.
-  static_assert(kQuads == 4, "");
-  uint64_t hits4 = 0;
   if (rules) {
 #pragma unroll
     for (int e = 0; e < (EVEN ? 1 : 4); ++e)
@@ -417,53 +464,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) rules_kernel(Args a) {
         if (o < n) hits4 |= (uint64_t)nibble(sm.hit, o) << (16 * e + 4 * q);
       }
   }
-  auto hits_at = [&](int head, int q) { return (unsigned)(hits4 >> (16 * head + 4 * q)) & 15u; };
 
   // ---- the rows ----
-  // Each row is loaded (its mask's bits first) before the row before it is
-  // worked on.
-  using Quad = typename QuadOf<T>::type;
-  struct Row {
-    Quad x[kQuads];
-    unsigned let;  // permitted entries, four bits a quad; the top bit: the edge
-    float edge;    // !EVEN: one of the entries that no 16 bytes of the output hold
-  };
-  auto words_of = [&](int k) -> const unsigned* {
-    return ru.mask && sm.masked[k] >= 0 ? sm.words[k] : nullptr;
-  };
-  // entries [head, head + mid) of the row at d start on 16 bytes of the output
-  auto head_of = [&](const float* d) {
-    return EVEN ? 0 : min(n, (int)((0u - (unsigned)((uintptr_t)d >> 2)) & 3u));
-  };
-  auto fetch = [&](int k, const T* s, const float* d, Row& row) {
-    const unsigned* words = words_of(k);
-    const int head = head_of(d), end = EVEN ? n : head + ((n - head) & ~3);
-    row.let = 0xffffffffu;
-    if (words) {
-      row.let = 1u << 31;
-#pragma unroll
-      for (int q = 0; q < kQuads; ++q) {
-        const int o = head + 4 * (q * kThreads + tid);
-        if (o < end) row.let |= nibble(words, o) << (4 * q);
-      }
-    }
-#pragma unroll
-    for (int q = 0; q < kQuads; ++q) {
-      const int o = head + 4 * (q * kThreads + tid);
-      bool want = o < end && (row.let >> (4 * q) & 15u);
-      if (a.in_place && !words) want = want && hits_at(head, q);
-      if (want) row.x[q].load(s + o, a.alike, a.logits_end);
-    }
-    if (!EVEN && tid < n - (end - head)) {
-      const int o = tid < head ? tid : end - head + tid;
-      const bool may = !words || (words[o >> 5] >> (o & 31) & 1u);
-      if (may) row.edge = load1(s + o);
-      else row.let &= ~(1u << 31);
-    }
-  };
   bool added = false;  // some row's path is in the addends
-  Row next;
-  fetch(0, src, dst, next);
+  if (!(rules && early)) fetch(0, src, dst, next);
   for (int k = 0; k < rows; ++k, src += a.stride, dst += a.V) {
     Row row = next;
     if (k + 1 < rows) fetch(k + 1, src + a.stride, dst + a.V, next);
