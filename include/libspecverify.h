@@ -439,7 +439,8 @@ sv_status sv_adapt_gamma(int32_t n_req, const int32_t* accepted_len, const int32
  * i is served iff n_i == 0 or S_i <= *free_count: requests are served in
  * order, whole, and once one does not fit no later one takes a block.  New
  * block k of the call (k from 0, in (request, table index) order) is
- * free_list[*free_count - 1 - k]; *free_count drops by the blocks taken.
+ * free_list[*free_count - 1 - k]; *free_count (taken as 0 if it is negative, as
+ * the capacity if it is above it) drops by the blocks taken.
  * Outputs:
  *   kv->block_tables: the new entries of served requests;
  *   taken [n_req]: new blocks of the request, -1 if it was not served;
@@ -457,7 +458,8 @@ sv_status sv_adapt_gamma(int32_t n_req, const int32_t* accepted_len, const int32
  * batch->parent may be NULL here: every request is a chain, of any length
  * (a prompt); max_rows_per_req is then not limited to 128.  batch->tokens and
  * kv->k_cache / v_cache are not read.
- * Supported: block_size 16, n_req <= 8192, fewer than 2^27 blocks. */
+ * Supported: block_size 16, n_req <= 8192, fewer than 2^27 blocks, at most
+ * 2^30 rows. */
 sv_status sv_reserve_kv(const sv_paged_kv* kv, const sv_batch* batch, const sv_block_pool* pool,
                         const int32_t* pos_offset, int32_t* slots, int32_t* positions,
                         int32_t* taken, int32_t* dev_status, void* stream);
@@ -484,8 +486,8 @@ sv_status sv_reserve_kv(const sv_paged_kv* kv, const sv_batch* batch, const sv_b
  *   q_out: bf16 [n_rows][n_q_heads][head_dim]; it may be q itself, else
  *   it must not overlap q, k or v.
  * A row of slot -1 (padding, a request that was not served) is skipped: nothing
- * of it is read or written; any other slot outside the cache sets
- * SV_DEV_BAD_SLOT and is skipped too.  Two rows must not name one slot.  An
+ * of it is written; any other slot outside the cache sets SV_DEV_BAD_SLOT and
+ * is skipped too.  Two rows must not name one slot.  An
  * axis outside [0, n_axes) sets SV_DEV_BAD_PARAM and reads axis 0.
  * kv->block_tables and cache_lens are not read.
  * Supported: block_size 16, head_dim 64 or 128, rotary_dim a multiple of 16;
@@ -525,8 +527,8 @@ sv_status sv_stage_qkv(const sv_paged_kv* kv, int32_t n_rows, const void* q, int
  * Every part may be left out (NULL):
  *   history int32 [n_req][max_history], history_len, prompt_len (NULL: 0)
  *     [n_req]: read only with a penalty; tokens outside [0, vocab) are ignored;
- *   repetition (finite, > 0; 1 = none), frequency, presence (finite; 0 = none):
- *     fp32 [n_req];
+ *   repetition (2^-126 .. 2^126; 1 = none; the division is a product with its
+ *     reciprocal), frequency, presence (finite; 0 = none): fp32 [n_req];
  *   biases: entries bias_begin[i] .. bias_begin[i + 1] - 1 (of n_bias) of
  *     bias_token / bias_value are request i's; a token listed twice takes its
  *     first entry, one outside [0, vocab) is ignored;

@@ -371,7 +371,8 @@ extern "C" sv_status sv_reserve_kv(const sv_paged_kv* kv, const sv_batch* bt,
   if (kv->num_blocks < 0 || kv->max_blocks_per_req < 0 || pool->capacity < 0)
     return SV_ERR_INVALID_ARGUMENT;
   if (kv->block_size != kBlockSize || kv->num_blocks > INT_MAX / kBlockSize ||
-      kv->max_blocks_per_req > INT_MAX / kBlockSize || bt->n_req > rsv::kMaxRequests)
+      kv->max_blocks_per_req > INT_MAX / kBlockSize || bt->n_req > rsv::kMaxRequests ||
+      bt->total_rows > 1 << 30)
     return SV_ERR_UNSUPPORTED_SHAPE;
   if (bt->parent && bt->max_rows_per_req > kMaxRows) return SV_ERR_UNSUPPORTED_SHAPE;
   if (bt->n_req == 0 && bt->total_rows == 0) return SV_OK;

@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) rules_kernel(Args a) {
   int finding = 0;
   if (!w.ok)
     finding = SV_DEV_BAD_WINDOW;
-  else if (!(rho > 0.f && rho < INFINITY) || !(fabsf(freq) < INFINITY) ||
+  else if (!(rho >= 0x1p-126f && rho <= 0x1p126f) || !(fabsf(freq) < INFINITY) ||
            !(fabsf(pres) < INFINITY) || b0 < 0 || b1 < b0 || b1 > ru.n_bias)
     finding = SV_DEV_BAD_PARAM;
   else if (hlen < 0 || hlen > ru.max_history || plen < 0 || plen > hlen)
@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) rules_kernel(Args a) {
     sm.masked[tid] = m;
   }
   // (a negative token is a large offset)
-  auto mine = [&](int v) { return (unsigned)(v - lo) < (unsigned)n; };
+  auto mine = [&](int v) { return (unsigned)v - (unsigned)lo < (unsigned)n; };
   if (rules) {
     for (int o = tid; o < kSlice / 4; o += kThreads) {
       reinterpret_cast<uint4*>(sm.cnt)[o] = make_uint4(0u, 0u, 0u, 0u);
@@ -552,7 +552,7 @@ extern "C" sv_status sv_shape_logits(const sv_batch* bt, const void* logits, int
     return SV_ERR_INVALID_ARGUMENT;
   if (logits_type != SV_LOGITS_F32 && logits_type != SV_LOGITS_BF16)
     return SV_ERR_INVALID_ARGUMENT;
-  if (bt->max_rows_per_req > kMaxRows) return SV_ERR_UNSUPPORTED_SHAPE;
+  if (bt->max_rows_per_req > kMaxRows || vocab > 1 << 30) return SV_ERR_UNSUPPORTED_SHAPE;
   if (bt->total_rows > 1 && logits_stride < vocab) return SV_ERR_INVALID_ARGUMENT;
   const sv_logit_rules& ru = *rules;
   const bool pen = ru.repetition || ru.frequency || ru.presence;

@@ -34,6 +34,7 @@
 // rate; six rows of 48 heads: 3.0 us.
 
 #include <limits.h>
+#include <math.h>
 
 #include "sv_internal.cuh"
 
@@ -375,7 +376,7 @@ extern "C" sv_status sv_stage_qkv(const sv_paged_kv* kv, int32_t n_rows, const v
   stg::Args a{};
   if (rotary) {
     if (rotary->rotary_dim < 0 || rotary->rotary_dim > D || rotary->n_axes < 1 ||
-        !(rotary->scale == rotary->scale))
+        !(fabsf(rotary->scale) < INFINITY))
       return SV_ERR_INVALID_ARGUMENT;
     if (rotary->rotary_dim % 16) return SV_ERR_UNSUPPORTED_SHAPE;
     a.rd = rotary->rotary_dim;
@@ -388,7 +389,7 @@ extern "C" sv_status sv_stage_qkv(const sv_paged_kv* kv, int32_t n_rows, const v
       return SV_ERR_INVALID_ARGUMENT;
   }
   // the negations refuse NaN too
-  if ((q_weight || k_weight) && !(eps >= 0.f)) return SV_ERR_INVALID_ARGUMENT;
+  if ((q_weight || k_weight) && !(eps >= 0.f && eps < INFINITY)) return SV_ERR_INVALID_ARGUMENT;
   const int64_t qw = (int64_t)n_q_heads * D, kw = (int64_t)kv->n_kv_heads * D;
   if (n_rows > 1 && (q_stride < qw || k_stride < kw || v_stride < kw))
     return SV_ERR_INVALID_ARGUMENT;

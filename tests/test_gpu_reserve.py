@@ -263,3 +263,36 @@ def test_two_batches_at_once_on_two_streams():
     torch.cuda.synchronize()
     for c in cases:
         c.check(c.keep[2])
+
+
+def test_without_positions_and_status():
+    c = _rng_case(30, 20, "tree", seed=30)
+    ref = c.run()
+    fresh = c.run()
+    d = c.keep[2]
+    d["tables"].copy_(_i32(c.tables))
+    d["count"].fill_(c.free)
+    d["ctx"][3] = -5
+    d["positions"].fill_(-3)
+    pages, batch, _ = c.keep
+    api.sv_reserve_kv(api.PagedKV(pages, pages, d["tables"], d["ctx"]), batch, api.BlockPool(d["list"], d["count"]),
+                      d["slots"], None, d["taken"])
+    torch.cuda.synchronize()
+    assert d["status"].item() == 0 and (d["positions"] == -3).all() and d["taken"][3] == -1
+    assert (d["slots"][c.cu[3]:c.cu[4]] == -1).all() and torch.equal(d["slots"][:c.cu[3]], ref["slots"][:c.cu[3]])
+    del fresh
+
+
+@pytest.mark.parametrize("count", [-7, 1 << 30])
+def test_a_free_count_outside_the_list(count):
+    c = _rng_case(6, 20, "chain", seed=31)
+    c.list = np.arange(c.list.size, dtype=np.int32) % c.blocks
+    c.free = count
+    d = c.run()
+    c.free = 0 if count < 0 else c.list.size
+    e, ref = edges.reserve(c.cu, c.parent, c.ctx, c.tables, c.list, c.free, c.blocks, c.max_rows, c.total, c.offset)
+    assert d["status"].item() == e
+    for k in ("taken", "slots", "positions", "tables"):
+        assert np.array_equal(d[k].cpu().numpy(), ref[k]), k
+    taken = int(ref["taken"][ref["taken"] > 0].sum())
+    assert d["count"].item() == (c.free - taken if taken else count)

@@ -4,7 +4,9 @@ Bound of a touched logit, from the arithmetic: the reciprocal of the repetition
 penalty and the product with it, the product and sum of the other penalties,
 the bias's addition to those and their addition to the logit round to fp32
 once each, so six halves of a step, 6 * 2^-24 of the sum of the absolute values
-that are added up.  Untouched logits are equal to the input,
+that are added up.  Below 2^-126 fp32 has steps of 2^-149 whatever the value
+(a product of 1e-30 and 2^-126 is 0), so half a step there is 2^-150: six of
+those are added, which is what a subnormal result can be off by.  Untouched logits are equal to the input,
 barred ones are -inf.
 """
 
@@ -104,7 +106,7 @@ class Case:
         assert same[fixed & ((w == x) | np.isinf(w))].all()
         with np.errstate(invalid="ignore"):  # of equal infinities
             d = np.abs(np.where(np.isfinite(w), g - w, 0))
-        assert (d <= 6 * 2.0 ** -24 * np.where(np.isfinite(m), m, 0)).all()
+        assert (d <= 6 * 2.0 ** -24 * np.where(np.isfinite(m), m, 0) + 6 * 2.0 ** -150).all()
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
@@ -247,6 +249,29 @@ def test_mask_rows_by_position_and_out_of_range():
     c.check(status=edges.BAD_PARAM)
 
 
+@pytest.mark.parametrize("rho", [2.0 ** -126, 2.0 ** 126, 1e-3, 1e3])
+def test_the_repetition_penalty_over_its_range(rho):
+    c = Case([4, 4], 400, few=True, hist=(30, 50))
+    c.kw["repetition"][:] = rho
+    c.kw["frequency"][:] = c.kw["presence"][:] = 0
+    x = c.logits
+    x[:, :7] = torch.tensor([-2.0, 0.0, 1.0, 3e-38 if rho < 1 else 3.0, 2.0 ** -10, -0.0, -1e-30])
+    if rho < 1e-6:  # what overflows is infinite
+        x[:, [2, 4]] = 0.0
+    if rho > 1e6:
+        x[:, 0] = -1e-38
+    c.bind()()
+    c.check()
+
+
+def test_without_a_status_word_findings_are_dropped():
+    c = Case([3, 4, 5], 500)
+    c.kw["repetition"][1] = -1
+    c.bind(dev_status=None)()
+    torch.cuda.synchronize()
+    assert (c.out[3:7] == 55).all() and (c.out[:3] != 55).any() and c.status.item() == 0
+
+
 def test_windows_and_padding_rows():
     c = Case([5, 9, 1, 12], 1000, tree=False, masks=0.6, behind=6)
     c.windows = dict(row_begin=[1, 0, 1, 4], row_end=[3, 9, 1, 12], verify_len=[9, 3, 9, 6])
@@ -258,6 +283,8 @@ def test_windows_and_padding_rows():
 @pytest.mark.parametrize("spoil,status", [
     (lambda c: c.kw["repetition"].__setitem__(1, 0.0), edges.BAD_PARAM),
     (lambda c: c.kw["repetition"].__setitem__(1, -1.0), edges.BAD_PARAM),
+    (lambda c: c.kw["repetition"].__setitem__(1, 1e-39), edges.BAD_PARAM),
+    (lambda c: c.kw["repetition"].__setitem__(1, 2e38), edges.BAD_PARAM),
     (lambda c: c.kw["repetition"].__setitem__(1, np.nan), edges.BAD_PARAM),
     (lambda c: c.kw["repetition"].__setitem__(1, np.inf), edges.BAD_PARAM),
     (lambda c: c.kw["frequency"].__setitem__(1, np.nan), edges.BAD_PARAM),

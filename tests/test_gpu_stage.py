@@ -191,6 +191,24 @@ def test_shared_position_for_every_axis():
     c.check()
 
 
+def test_the_c_call_with_one_position_on_three_axes():
+    import ctypes
+    from speculative_decoding_verification_padding_gb300 import _native as N
+    c = Case(30, 4, 2, 64, axes=3)
+    c.pos[1:] = c.pos[0]
+    c.bind()
+    keep = [t.cuda() for t in (c.slots, c.pos[0], c.freq, c.axis, c.qw, c.kw)]
+    slots, pos, freq, axis, qw, kw = (t.data_ptr() for t in keep)
+    d = c.dev
+    kv = N.SvPagedKV(d["kc"].data_ptr(), d["vc"].data_ptr(), c.kc.shape[0], 16, 2, 64, None, 0, None)
+    rot = N.SvRotary(freq, 64, 0, 3, axis, 1.0)
+    step = c.q.stride(0)
+    assert N.lib().sv_stage_qkv(ctypes.byref(kv), 30, c.q.data_ptr(), step, c.k.data_ptr(), step, c.v.data_ptr(), step,
+                                4, slots, pos, 0, ctypes.byref(rot), qw, kw, c.eps, d["out"].data_ptr(), None,
+                                torch.cuda.current_stream().cuda_stream) == N.SV_OK
+    c.check()
+
+
 def test_far_blocks_and_two_streams_at_once():
     # cache slots whose element offsets pass 2^31, and two calls side by side
     K, D, blocks = 8, 128, 140000
