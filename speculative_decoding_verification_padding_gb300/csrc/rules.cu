@@ -204,6 +204,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) rules_kernel(Args a) {
   // place that a row can start at.
   static_assert(kQuads == 4, "");
   uint64_t hits4 = 0;
+  unsigned seen16 = 0;  // EVEN: its entries that the repetition penalty takes, paths apart
   auto hits_at = [&](int head, int q) { return (unsigned)(hits4 >> (16 * head + 4 * q)) & 15u; };
   // Each row is loaded (its mask's bits first) before the row before it is
   // worked on.
@@ -246,8 +247,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) rules_kernel(Args a) {
       else row.let &= ~(1u << 31);
     }
   };
-  // (in place, which entries to load is known only when the rules are)
-  const bool early = !a.in_place;
   Row next;
 
   // ---- its rules in shared memory ----
@@ -402,8 +401,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) rules_kernel(Args a) {
       const int v = ru.bias_token[t];
       if (mine(v)) atomicMin(&s_first[v - lo], (unsigned)(t - b0));
     }
-    __syncthreads();
-    if (early) fetch(0, src, dst, next);  // under what is left to do for the rules
+  }
+  __syncthreads();  // counts and mask bits are there
+  // The first row's loads go out under what is left to do for the rules, unless
+  // the rules say which entries to load.
+  const bool early = !a.in_place || words_of(0);
+  if (early) fetch(0, src, dst, next);
+  if (rules) {
     if (paths) {
       if (tid > 0 && tid < w.rows && mine(node_t)) {
         node_n = (int)(sm.cnt[node_t - lo] & ~kDraft);
@@ -413,34 +417,51 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) rules_kernel(Args a) {
       }
       __syncthreads();  // the counts become addends
     }
+    const bool maps = !EVEN || paths;  // bit maps for all to read, or only this thread's own bits
 #pragma unroll
     for (int q = 0; q < kQuads; ++q) {
       const int o = 4 * (q * kThreads + tid);
       const uint4 c = *reinterpret_cast<const uint4*>(sm.cnt + o);
       const uint32_t asked = *reinterpret_cast<const uint32_t*>(sm.asked + o);
-      const auto addend = [&](unsigned m) { return m ? -(freq * (float)m + pres) : 0.f; };
-      const unsigned m[4] = {c.x & ~kDraft, c.y & ~kDraft, c.z & ~kDraft, c.w & ~kDraft};
-      *reinterpret_cast<float4*>(sm.add + o) =
-          make_float4(addend(m[0]), addend(m[1]), addend(m[2]), addend(m[3]));
-      unsigned seen = (m[0] || (asked & 0xffu) ? 1u : 0u) | (m[1] || (asked & 0xff00u) ? 2u : 0u) |
-                      (m[2] || (asked & 0xff0000u) ? 4u : 0u) | (m[3] || (asked >> 24) ? 8u : 0u);
-      unsigned hit = seen | (c.x ? 1u : 0u) | (c.y ? 2u : 0u) | (c.z ? 4u : 0u) | (c.w ? 8u : 0u);
+      unsigned seen = 0, hit = 0;
+      if (c.x | c.y | c.z | c.w) {
+        const auto addend = [&](unsigned v) {
+          const unsigned m = v & ~kDraft;
+          return m ? -(freq * (float)m + pres) : 0.f;
+        };
+        *reinterpret_cast<float4*>(sm.add + o) =
+            make_float4(addend(c.x), addend(c.y), addend(c.z), addend(c.w));
+        seen = (c.x & ~kDraft ? 1u : 0u) | (c.y & ~kDraft ? 2u : 0u) | (c.z & ~kDraft ? 4u : 0u) |
+               (c.w & ~kDraft ? 8u : 0u);
+        hit = (c.x ? 1u : 0u) | (c.y ? 2u : 0u) | (c.z ? 4u : 0u) | (c.w ? 8u : 0u);
+      }
+      // the four bytes' marks as four bits
+      const unsigned marks = (asked * 0x10204080u) >> 28;
+      seen |= marks;
+      hit |= marks;
       if (b1 > b0) {
         const uint4 f = *reinterpret_cast<const uint4*>(s_first + o);
-        hit |= (f.x != ~0u ? 1u : 0u) | (f.y != ~0u ? 2u : 0u) | (f.z != ~0u ? 4u : 0u) |
-               (f.w != ~0u ? 8u : 0u);
+        if ((f.x & f.y & f.z & f.w) != ~0u)
+          hit |= (f.x != ~0u ? 1u : 0u) | (f.y != ~0u ? 2u : 0u) | (f.z != ~0u ? 4u : 0u) |
+                 (f.w != ~0u ? 8u : 0u);
       }
-      // eight lanes' nibbles make a word
-      seen <<= 4 * (lane & 7);
-      hit <<= 4 * (lane & 7);
+      if (EVEN) {
+        hits4 |= (uint64_t)hit << (4 * q);
+        seen16 |= seen << (4 * q);
+      }
+      if (maps) {
+        // eight lanes' nibbles make a word
+        seen <<= 4 * (lane & 7);
+        hit <<= 4 * (lane & 7);
 #pragma unroll
-      for (int d = 1; d < 8; d <<= 1) {
-        seen |= __shfl_xor_sync(0xffffffffu, seen, d);
-        hit |= __shfl_xor_sync(0xffffffffu, hit, d);
-      }
-      if ((lane & 7) == 0) {
-        sm.seen[o >> 5] = seen;
-        sm.hit[o >> 5] = hit;
+        for (int d = 1; d < 8; d <<= 1) {
+          seen |= __shfl_xor_sync(0xffffffffu, seen, d);
+          hit |= __shfl_xor_sync(0xffffffffu, hit, d);
+        }
+        if ((lane & 7) == 0) {
+          sm.seen[o >> 5] = seen;
+          sm.hit[o >> 5] = hit;
+        }
       }
     }
     if (tid == 0) sm.hit[kWords] = sm.seen[kWords] = 0;
@@ -454,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) rules_kernel(Args a) {
       }
     }
   }
-  __syncthreads();
+  if (rules) __syncthreads();
   auto on_path = [&](int k) {
     return (sm.path[k][0] | sm.path[k][1] | sm.path[k][2] | sm.path[k][3]) != 0;
   };
@@ -464,9 +485,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) rules_kernel(Args a) {
     const float y = x * (x > 0.f ? inv : rho);
     return (seen ? y : x) + add;
   };
-  if (rules) {
+  if (!EVEN && rules) {
 #pragma unroll
-    for (int e = 0; e < (EVEN ? 1 : 4); ++e)
+    for (int e = 0; e < 4; ++e)
 #pragma unroll
       for (int q = 0; q < kQuads; ++q) {
         const int o = e + 4 * (q * kThreads + tid);
@@ -476,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) rules_kernel(Args a) {
 
   // ---- the rows ----
   bool added = false;  // some row's path is in the addends
-  if (!(rules && early)) fetch(0, src, dst, next);
+  if (!early) fetch(0, src, dst, next);
   for (int k = 0; k < rows; ++k, src += a.stride, dst += a.V) {
     Row row = next;
     if (k + 1 < rows) fetch(k + 1, src + a.stride, dst + a.V, next);
@@ -511,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) rules_kernel(Args a) {
       float4 x = row.x[q].get(odd);
       if (__any_sync(0xffffffffu, hit & let)) {
         if (o < end) {
-          const unsigned seen = nibble(sm.seen, o);
+          const unsigned seen = EVEN && !paths ? seen16 >> (4 * q) : nibble(sm.seen, o);
           float4 d;
           if (EVEN) d = *reinterpret_cast<const float4*>(sm.add + o);
           else d = make_float4(sm.add[o], sm.add[o + 1], sm.add[o + 2], sm.add[o + 3]);
