@@ -197,6 +197,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) rules_kernel(Args a) {
   if (j0 >= j1) return;
   const int ra = w.cu + j0, rows = j1 - j0;
   const bool rules = pen || b1 > b0;
+  // In place, an unmasked row's untouched entries stay where they are, unless it
+  // is the only one: loading it before it is known which they are is faster then
+  // (256 single rows: 90 us against 103).
+  const bool lean = a.in_place && rows > 1;
   const T* src = static_cast<const T*>(a.logits) + (size_t)ra * a.stride + lo;
   float* dst = a.out + (size_t)ra * a.V + lo;
 
@@ -237,7 +241,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) rules_kernel(Args a) {
     for (int q = 0; q < kQuads; ++q) {
       const int o = head + 4 * (q * kThreads + tid);
       bool want = o < end && (row.let >> (4 * q) & 15u);
-      if (a.in_place && !words) want = want && hits_at(head, q);
+      if (lean && !words) want = want && hits_at(head, q);
       if (want) row.x[q].load(s + o, a.alike, a.logits_end);
     }
     if (!EVEN && tid < n - (end - head)) {
@@ -405,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) rules_kernel(Args a) {
   __syncthreads();  // counts and mask bits are there
   // The first row's loads go out under what is left to do for the rules, unless
   // the rules say which entries to load.
-  const bool early = !a.in_place || words_of(0);
+  const bool early = !lean || words_of(0);
   if (early) fetch(0, src, dst, next);
   if (rules) {
     if (paths) {
@@ -502,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) rules_kernel(Args a) {
     Row row = next;
     if (k + 1 < rows) fetch(k + 1, src + a.stride, dst + a.V, next);
     const unsigned* words = words_of(k);
-    const bool sparse = a.in_place && !words;  // only touched entries change
+    const bool sparse = lean && !words;  // only touched entries change
     const int head = head_of(dst), end = EVEN ? n : head + ((n - head) & ~3);
     const bool odd = sizeof(T) == 2 && !a.alike && ((uintptr_t)(src + head) & 2);
     if (paths) {
