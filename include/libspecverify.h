@@ -471,7 +471,8 @@ sv_status sv_reserve_kv(const sv_paged_kv* kv, const sv_batch* batch, const sv_b
  *   K page of s  = turn(norm(k[r][g], k_weight))     g < kv->n_kv_heads
  *   V page of s  = v[r][g]
  * norm(x, w) = x / sqrt(mean(x^2) + eps) * w over the head's head_dim
- *   elements; w NULL: x itself.  Weights: fp32 [head_dim], 16-byte aligned.
+ *   elements (below 2^60 in magnitude, so that their squares add up in fp32);
+ *   w NULL: x itself.  Weights: fp32 [head_dim], 16-byte aligned.
  * turn: the first rotary_dim elements form rotary_dim / 2 pairs (a, b),
  *   elements (j, j + rotary_dim / 2), or (2j, 2j + 1) if interleaved;
  *   (a, b) -> scale * (a cos t - b sin t, b cos t + a sin t) with

@@ -328,6 +328,15 @@ def test_in_place_and_apart_agree():
         assert torch.equal(first, c.out)
 
 
+@pytest.mark.parametrize("masks", [None, 0.5])
+@pytest.mark.parametrize("V", [4096, 9001])
+def test_single_rows_in_place(V, masks):
+    c = Case([1] * 40, V, bias=9, masks=masks, few=V < 5000)
+    x = c.logits.cuda()
+    c.bind(out=x, logits=x)()
+    c.check()
+
+
 def test_misaligned_rows_and_outputs():
     c = Case([5, 6], 4096, bias=9, masks=0.5)
     wide = torch.zeros(11 * 4096 + 4, device="cuda")
