@@ -103,7 +103,10 @@ class BoundCall:
     def __init__(self, name: str, args: tuple, device: torch.device, keep=None):
         self._f = getattr(N.lib(), name)
         self._name = name
-        self._args = args  # ctypes byref objects keep their structs alive
+        # Numbers become ctypes values once, not at every call; ctypes byref
+        # objects keep their structs alive.
+        self._args = tuple(t(a) if isinstance(a, (int, float)) else a
+                           for t, a in zip(N.PROTOTYPES[name][1], args))
         self._keep = keep  # what the call's tensors belong to, where the binder hands it over
         self._dev = device.index if device.index is not None else torch.cuda.current_device()
 
