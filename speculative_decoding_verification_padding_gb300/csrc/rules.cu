@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) rules_kernel(Args a) {
   static_assert(kQuads == 4, "");
   uint64_t hits4 = 0;
   unsigned seen16 = 0;  // EVEN: its entries that the repetition penalty takes, paths apart
-  auto hits_at = [&](int head, int q) { return (unsigned)(hits4 >> (16 * head + 4 * q)) & 15u; };
+  auto hits_at = [&](int head) { return (unsigned)(hits4 >> (EVEN ? 0 : 16 * head)) & 0xffffu; };
   // Each row is loaded (its mask's bits first) before the row before it is
   // worked on.
   using Quad = typename QuadOf<T>::type;
@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) rules_kernel(Args a) {
     for (int q = 0; q < kQuads; ++q) {
       const int o = head + 4 * (q * kThreads + tid);
       bool want = o < end && (row.let >> (4 * q) & 15u);
-      if (lean && !words) want = want && hits_at(head, q);
+      if (lean && !words) want = want && (hits_at(head) >> (4 * q) & 15u);
       if (want) row.x[q].load(s + o, a.alike, a.logits_end);
     }
     if (!EVEN && tid < n - (end - head)) {
@@ -486,8 +486,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) rules_kernel(Args a) {
   const float inv = 1.f / rho;
   // y of touched entry o with value x
   auto shaped = [&](float x, float add, bool seen) {
-    const float y = x * (x > 0.f ? inv : rho);
-    return (seen ? y : x) + add;
+    const float f = x > 0.f ? inv : rho;
+    return fmaf(x, seen ? f : 1.f, add);
   };
   if (!EVEN && rules) {
 #pragma unroll
@@ -528,11 +528,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) rules_kernel(Args a) {
         __syncthreads();
       }
     }
+    const unsigned hits = hits_at(head);
 #pragma unroll
     for (int q = 0; q < kQuads; ++q) {
       const int o = head + 4 * (q * kThreads + tid);
       const unsigned let = row.let >> (4 * q) & 15u;
-      const unsigned hit = hits_at(head, q);
+      const unsigned hit = hits >> (4 * q) & 15u;
       float4 x = row.x[q].get(odd);
       if (__any_sync(0xffffffffu, hit & let)) {
         if (o < end) {
@@ -546,10 +547,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) rules_kernel(Args a) {
           x.w = shaped(x.w, d.w, seen & 8u);
         }
       }
-      if (!(let & 1u)) x.x = -INFINITY;
-      if (!(let & 2u)) x.y = -INFINITY;
-      if (!(let & 4u)) x.z = -INFINITY;
-      if (!(let & 8u)) x.w = -INFINITY;
+      if (words) {
+        if (!(let & 1u)) x.x = -INFINITY;
+        if (!(let & 2u)) x.y = -INFINITY;
+        if (!(let & 4u)) x.z = -INFINITY;
+        if (!(let & 8u)) x.w = -INFINITY;
+      }
       if (o < end && !(sparse && !hit)) *reinterpret_cast<float4*>(dst + o) = x;
     }
     const int rest = n - (end - head);
