@@ -27,7 +27,7 @@
 // slices that hold one.
 //
 // Measured (1280 rows of 151936, histories of 3450 tokens on average, 300
-// biases, masks; floor 232 us at the copy rate): 272 us, 230 us without rules;
+// biases, masks; floor 232 us at the copy rate): 269 us, 230 us without rules;
 // 256 single rows of 128256 with 7750 tokens of history 89 us (floor 39).
 // The same work with rules applied to touched entries alone under branches:
 // 341; touched entries written over the copied rows: 439; rows passing through
@@ -47,7 +47,8 @@ constexpr int kSlice = 4096;    // vocabulary entries of a CTA
 constexpr int kWords = kSlice / 32;
 constexpr int kQuads = kSlice / (4 * kThreads);
 constexpr int kMaxChunk = 9;    // rows of a CTA at most: a root and eight drafts
-constexpr int kHistVecs = 2;    // vectors of four history tokens a thread has in flight
+constexpr int kHistVecs = 3;    // vectors of four history tokens a thread has in flight (two: 272 us, four:
+                                // 269 us but 256 single rows 97 instead of 89)
 
 struct Args {
   sv_batch bt;
