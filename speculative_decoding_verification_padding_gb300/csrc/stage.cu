@@ -60,10 +60,11 @@ struct Args {
 
 constexpr int kVecs = 3;          // pieces of a thread's round; two rounds are in flight
 constexpr int kMaxThreads = 512;
-// Rows per SM from which a warp takes whole rows (56 heads of 128: 2000 rows
-// 13.5 us in stream_kernel and 16.2 in row_kernel, 300 rows 8.5 and 4.5, 1280
-// rows 12.4 and 11.9).
-constexpr int kStreamRows = 12;
+// Rows per SM from which a warp takes whole rows.  stream_kernel / row_kernel,
+// 56 heads of 128: 400 rows 7.8 / 5.3 us, 1000 rows 9.1 / 9.1, 1500 rows 12.9 /
+// 12.6, 2200 rows 13.7 / 16.1; 18 heads of 64: 1500 rows 4.6 / 4.1, 2200 rows
+// 4.7 / 4.9.
+constexpr int kStreamRows = 10;
 constexpr int kMaxHalf = 64;      // rotated pairs of a head at most
 
 // f / (2 pi) modulo one turn, in units of 2^-64 of a turn.
