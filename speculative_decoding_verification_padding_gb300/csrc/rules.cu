@@ -13,7 +13,7 @@
 // Bound: HBM, 4 bytes written and 2 or 4 read per logit; a barred logit need
 // not be read, and in place an untouched one need not be moved.  Few tokens of
 // a row are touched by a penalty or bias, and they are the same for all rows
-// of a request but for their paths.  So a CTA takes kSlice entries of the
+// of a request but for their paths.  So a CTA takes a slice of the
 // vocabulary and some rows of one request and first boils the request's rules
 // down to shared memory: the history is counted (every CTA reads the whole
 // history from L2 and keeps what falls in its slice: no workspace, no global
@@ -28,7 +28,7 @@
 //
 // Measured (1280 rows of 151936, histories of 3450 tokens on average, 300
 // biases, masks; floor 232 us at the copy rate): 269 us, 230 us without rules;
-// 256 single rows of 128256 with 7750 tokens of history 89 us (floor 39).
+// 256 single rows of 128256 with 7750 tokens of history 78 us (floor 39).
 // The same work with rules applied to touched entries alone under branches:
 // 341; touched entries written over the copied rows: 439; rows passing through
 // a shared-memory ring of bulk copies: 437 to 528, with warps specialised: 416;
@@ -41,11 +41,18 @@ namespace sv {
 namespace rul {
 
 constexpr int kThreads = 256;
-constexpr int kCtasPerSm = 4;
+constexpr int kCtasPerSm = 4, kWideCtasPerSm = 3;
 constexpr int kWarps = kThreads / 32;
-constexpr int kSlice = 4096;    // vocabulary entries of a CTA
-constexpr int kWords = kSlice / 32;
-constexpr int kQuads = kSlice / (4 * kThreads);
+// Vocabulary entries of a CTA: four quads a thread, or eight where requests
+// have single rows.  Those need no registers for a next row, and half as many
+// CTAs read each history (256 rows of 128256, 7750 tokens: fp32 78 us against
+// 89, bf16 69 against 96; without a history bf16 35 against 41, fp32 with
+// biases alone 55 against 53).  With more rows the next one's loads are worth
+// more: 256 chains of five in bf16, each row loaded when its turn comes, 276 us
+// against 183.
+constexpr int kRowQuads = 4, kSingleQuads = 8;
+template <int kQuads>
+constexpr int kSliceOf = 4 * kThreads * kQuads;
 constexpr int kMaxChunk = 9;    // rows of a CTA at most: a root and eight drafts
 constexpr int kHistVecs = 3;    // vectors of four history tokens a thread has in flight (two: 272 us, four:
                                 // 269 us but 256 single rows 97 instead of 89)
@@ -63,7 +70,9 @@ struct Args {
   int alike;  // input rows lie in four entries as the output's do
 };
 
+template <int kQuads>
 struct Smem {
+  static constexpr int kSlice = kSliceOf<kQuads>, kWords = kSlice / 32;
   union {
     unsigned cnt[kSlice];      // first occurrences and kDraft,
     float add[kSlice];         // then the addend
@@ -76,11 +85,38 @@ struct Smem {
   unsigned mine[kMaxRows / 32];             // nodes whose token is in the slice
   unsigned path[kMaxChunk][kMaxRows / 32];  // of those, the nodes on the row's path
   int masked[kMaxChunk];                    // the row's mask row, -1: none
-  unsigned words[kMaxChunk][kWords + 1];    // that mask's bits of the slice
+  unsigned words[kQuads > kRowQuads ? 1 : kMaxChunk][kWords + 1];  // that mask's bits of the slice
 };
-// Behind it, with biases: the lowest list position of each token.
-constexpr size_t kBiasAt = (sizeof(Smem) + 15) / 16 * 16;
-constexpr size_t kBiasBytes = kSlice * sizeof(unsigned);
+// Behind it, with biases: the lowest list position of each token (in 16 bits
+// for wide slices: 32 would leave room for two CTAs instead of three, 94 us
+// instead of 78).
+template <int kQuads>
+struct FirstOf {
+  using type = unsigned;
+};
+template <>
+struct FirstOf<kSingleQuads> {
+  using type = unsigned short;
+};
+__device__ __forceinline__ void first_min(unsigned* at, unsigned v) { atomicMin(at, v); }
+__device__ __forceinline__ void first_min(unsigned short* at, unsigned v) {
+  unsigned short old = *at;
+  while (v < old) {  // *at falls with every turn but the last
+    const unsigned short was = atomicCAS(at, old, (unsigned short)v);
+    if (was == old) break;
+    old = was;
+  }
+}
+__device__ __forceinline__ void first_load(const unsigned* at, unsigned (&f)[4]) {
+  const uint4 v = *reinterpret_cast<const uint4*>(at);
+  f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w;
+}
+__device__ __forceinline__ void first_load(const unsigned short* at, unsigned (&f)[4]) {
+  const ushort4 v = *reinterpret_cast<const ushort4*>(at);
+  f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w;
+}
+template <int kQuads>
+constexpr size_t kBiasAt = (sizeof(Smem<kQuads>) + 15) / 16 * 16;
 
 constexpr unsigned kDraft = 0x80000000u;  // the token is some draft's
 
@@ -157,13 +193,19 @@ __device__ __forceinline__ unsigned nibble(const unsigned* bits, int o) {
   return b & 15u;
 }
 
-// EVEN: every row of the output starts on 16 bytes.
-template <typename T, bool EVEN>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) rules_kernel(Args a) {
+// EVEN: every row of the output starts on 16 bytes.  kQuads: kSingleQuads where
+// each request has one row at most, else kRowQuads.
+template <typename T, bool EVEN, int kQuads>
+__global__ void __launch_bounds__(kThreads, kQuads > kRowQuads ? kWideCtasPerSm : kCtasPerSm)
+    rules_kernel(Args a) {
   griddep_entry();
+  constexpr int kSlice = kSliceOf<kQuads>, kWords = kSlice / 32;
+  constexpr bool kSingle = kQuads > kRowQuads;
   extern __shared__ __align__(16) uint8_t s_raw[];
-  Smem& sm = *reinterpret_cast<Smem*>(s_raw);
-  unsigned* s_first = reinterpret_cast<unsigned*>(s_raw + kBiasAt);
+  Smem<kQuads>& sm = *reinterpret_cast<Smem<kQuads>*>(s_raw);
+  using First = typename FirstOf<kQuads>::type;
+  constexpr unsigned kNone = (First)~0u;
+  First* s_first = reinterpret_cast<First*>(s_raw + kBiasAt<kQuads>);
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   // slices in order: the lowest token ids are the most frequent ones, and
   // counting them takes longest: their slices start first
@@ -201,24 +243,28 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) rules_kernel(Args a) {
   const bool rules = pen || b1 > b0;
   // In place, an unmasked row's untouched entries stay where they are, unless it
   // is the only one: loading it before it is known which they are is faster then
-  // (256 single rows: 90 us against 103).
+  // (256 single rows of 4096 entries a CTA: 90 us against 103).
   const bool lean = a.in_place && rows > 1;
   const T* src = static_cast<const T*>(a.logits) + (size_t)ra * a.stride + lo;
   float* dst = a.out + (size_t)ra * a.V + lo;
 
   // This thread's touched entries, four bits a quad: sixteen bits for each
-  // place that a row can start at.
-  static_assert(kQuads == 4, "");
+  // place that a row can start at, or those of the one row.
+  constexpr bool kOne = EVEN || kSingle;
+  static_assert(4 * kQuads * (kOne ? 1 : 4) <= (kOne ? 32 : 64), "");
   uint64_t hits4 = 0;
-  unsigned seen16 = 0;  // EVEN: its entries that the repetition penalty takes, paths apart
-  auto hits_at = [&](int head) { return (unsigned)(hits4 >> (EVEN ? 0 : 16 * head)) & 0xffffu; };
+  unsigned seen_own = 0;  // EVEN: its entries that the repetition penalty takes, paths apart
+  auto hits_at = [&](int head) {
+    return kOne ? (unsigned)hits4 : (unsigned)(hits4 >> (16 * head)) & 0xffffu;
+  };
   // Each row is loaded (its mask's bits first) before the row before it is
   // worked on.
   using Quad = typename QuadOf<T>::type;
   struct Row {
     Quad x[kQuads];
-    unsigned let;  // permitted entries, four bits a quad; the top bit: the edge
+    unsigned let;  // permitted entries, four bits a quad
     float edge;    // !EVEN: one of the entries that no 16 bytes of the output hold
+    bool open;     // it is permitted
   };
   auto words_of = [&](int k) -> const unsigned* {
     return ru.mask && sm.masked[k] >= 0 ? sm.words[k] : nullptr;
@@ -231,8 +277,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) rules_kernel(Args a) {
     const unsigned* words = words_of(k);
     const int head = head_of(d), end = EVEN ? n : head + ((n - head) & ~3);
     row.let = 0xffffffffu;
+    row.open = true;
     if (words) {
-      row.let = 1u << 31;
+      row.let = 0u;
 #pragma unroll
       for (int q = 0; q < kQuads; ++q) {
         const int o = head + 4 * (q * kThreads + tid);
@@ -250,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) rules_kernel(Args a) {
       const int o = tid < head ? tid : end - head + tid;
       const bool may = !words || (words[o >> 5] >> (o & 31) & 1u);
       if (may) row.edge = load1(s + o);
-      else row.let &= ~(1u << 31);
+      else row.open = false;
     }
   };
   Row next;
@@ -301,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) rules_kernel(Args a) {
       reinterpret_cast<uint32_t*>(sm.asked)[o] = 0u;
     }
     if (b1 > b0)
-      for (int o = tid; o < kSlice / 4; o += kThreads)
+      for (int o = tid; o < kSlice * (int)sizeof(First) / 16; o += kThreads)
         reinterpret_cast<uint4*>(s_first)[o] =
             make_uint4(0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu);
     if (tid < kMaxRows) {
@@ -387,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) rules_kernel(Args a) {
         take(t, h[t]);
       }
       // the path of every row of this CTA, its nodes in the slice only
-      paths = (sm.mine[0] | sm.mine[1] | sm.mine[2] | sm.mine[3]) != 0;
+      paths = !kSingle && (sm.mine[0] | sm.mine[1] | sm.mine[2] | sm.mine[3]) != 0;
       if (paths) {
         if (tid > 0 && tid < w.rows && mine(node_t)) atomicOr(&sm.cnt[node_t - lo], kDraft);
         if (tid < rows) {
@@ -402,10 +449,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) rules_kernel(Args a) {
         }
       }
     }
-    if (mine(btok)) atomicMin(&s_first[btok - lo], (unsigned)tid);
+    if (mine(btok)) first_min(&s_first[btok - lo], (unsigned)tid);
     for (int t = b0 + kThreads + tid; t < b1; t += kThreads) {
       const int v = ru.bias_token[t];
-      if (mine(v)) atomicMin(&s_first[v - lo], (unsigned)(t - b0));
+      if (mine(v)) first_min(&s_first[v - lo], (unsigned)(t - b0));
     }
   }
   __syncthreads();  // counts and mask bits are there
@@ -418,8 +465,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) rules_kernel(Args a) {
       if (tid > 0 && tid < w.rows && mine(node_t)) {
         node_n = (int)(sm.cnt[node_t - lo] & ~kDraft);
         node_seen = node_n > 0 || sm.asked[node_t - lo];
-        const unsigned f = b1 > b0 ? s_first[node_t - lo] : 0xffffffffu;
-        if (f != 0xffffffffu) node_bias = ru.bias_value[b0 + (int)f];
+        const unsigned f = b1 > b0 ? s_first[node_t - lo] : kNone;
+        if (f != kNone) node_bias = ru.bias_value[b0 + (int)f];
       }
       __syncthreads();  // the counts become addends
     }
@@ -446,14 +493,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) rules_kernel(Args a) {
       seen |= marks;
       hit |= marks;
       if (b1 > b0) {
-        const uint4 f = *reinterpret_cast<const uint4*>(s_first + o);
-        if ((f.x & f.y & f.z & f.w) != ~0u)
-          hit |= (f.x != ~0u ? 1u : 0u) | (f.y != ~0u ? 2u : 0u) | (f.z != ~0u ? 4u : 0u) |
-                 (f.w != ~0u ? 8u : 0u);
+        unsigned f[4];
+        first_load(s_first + o, f);
+        if ((f[0] & f[1] & f[2] & f[3]) != kNone)
+          hit |= (f[0] != kNone ? 1u : 0u) | (f[1] != kNone ? 2u : 0u) | (f[2] != kNone ? 4u : 0u) |
+                 (f[3] != kNone ? 8u : 0u);
       }
       if (EVEN) {
         hits4 |= (uint64_t)hit << (4 * q);
-        seen16 |= seen << (4 * q);
+        seen_own |= seen << (4 * q);
       }
       if (maps) {
         // eight lanes' nibbles make a word
@@ -492,11 +540,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) rules_kernel(Args a) {
     return fmaf(x, seen ? f : 1.f, add);
   };
   if (!EVEN && rules) {
+    const int e0 = kSingle ? head_of(dst) : 0;
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
+    for (int e = 0; e < (kSingle ? 1 : 4); ++e)
 #pragma unroll
       for (int q = 0; q < kQuads; ++q) {
-        const int o = e + 4 * (q * kThreads + tid);
+        const int o = e0 + e + 4 * (q * kThreads + tid);
         if (o < n) hits4 |= (uint64_t)nibble(sm.hit, o) << (16 * e + 4 * q);
       }
   }
@@ -506,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) rules_kernel(Args a) {
   if (!early) fetch(0, src, dst, next);
   for (int k = 0; k < rows; ++k, src += a.stride, dst += a.V) {
     Row row = next;
-    if (k + 1 < rows) fetch(k + 1, src + a.stride, dst + a.V, next);
+    if (!kSingle && k + 1 < rows) fetch(k + 1, src + a.stride, dst + a.V, next);
     const unsigned* words = words_of(k);
     const bool sparse = lean && !words;  // only touched entries change
     const int head = head_of(dst), end = EVEN ? n : head + ((n - head) & ~3);
@@ -539,7 +588,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) rules_kernel(Args a) {
       float4 x = row.x[q].get(odd);
       if (__any_sync(0xffffffffu, hit & let)) {
         if (o < end) {
-          const unsigned seen = EVEN && !paths ? seen16 >> (4 * q) : nibble(sm.seen, o);
+          const unsigned seen = EVEN && !paths ? seen_own >> (4 * q) : nibble(sm.seen, o);
           float4 d;
           if (EVEN) d = *reinterpret_cast<const float4*>(sm.add + o);
           else d = make_float4(sm.add[o], sm.add[o + 1], sm.add[o + 2], sm.add[o + 3]);
@@ -562,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) rules_kernel(Args a) {
       const int o = tid < head ? tid : end - head + tid;
       float y = row.edge;
       if (rules) y = shaped(y, sm.add[o], sm.seen[o >> 5] >> (o & 31) & 1u);
-      if (!(row.let >> 31)) y = -INFINITY;
+      if (!row.open) y = -INFINITY;
       dst[o] = y;
     }
   }
@@ -621,12 +670,18 @@ extern "C" sv_status sv_shape_logits(const sv_batch* bt, const void* logits, int
   const bool even = (to & 15) == 0 && vocab % 4 == 0;
   const int nsm = num_sms();
   if (nsm < 1) return SV_ERR_CUDA;
-  const int slices = (vocab + rul::kSlice - 1) / rul::kSlice;
+  const long room = (long)nsm * rul::kCtasPerSm;
+  const int wide = rul::kSliceOf<rul::kSingleQuads>;
+  // Wide slices where they leave no place for a CTA empty.
+  const bool single = ((pen && a.ru.max_history > 0) || esz == 2) && bt->max_rows_per_req == 1 &&
+                      (!ru.bias_begin || ru.n_bias < 0xffff) &&
+                      (long)bt->n_req * ((vocab + wide - 1) / wide) >= room;
+  const int slice = single ? wide : rul::kSliceOf<rul::kRowQuads>;
+  const int slices = (vocab + slice - 1) / slice;
   // Rows of a CTA: all of a request's up to kMaxChunk, unless that leaves places
   // for CTAs empty: a CTA's rows follow one another, its rules cost a few rows'
   // time.  (Eight chains with histories of 8000: one row a CTA 24 us, three 15;
   // sixteen trees of 33 to 65 rows: seventeen a CTA 71 us, nine 60.)
-  const long room = (long)nsm * rul::kCtasPerSm;
   const long fair = ((long)bt->total_rows * slices + room - 1) / room;
   const int most = (int)max(1L, min((long)rul::kMaxChunk, fair));
   a.chunks = (bt->max_rows_per_req + most - 1) / most;
@@ -634,11 +689,24 @@ extern "C" sv_status sv_shape_logits(const sv_batch* bt, const void* logits, int
   const long units = (long)bt->n_req * a.chunks, ctas = units * slices;
   if (ctas > 0x7fffffffL) return SV_ERR_UNSUPPORTED_SHAPE;
   a.units = (int)units;
-  const size_t smem = rul::kBiasAt + (ru.bias_begin ? rul::kBiasBytes : 0);
-  void (*const kernel)(rul::Args) =
-      esz == 4 ? (even ? rul::rules_kernel<float, true> : rul::rules_kernel<float, false>)
-               : (even ? rul::rules_kernel<__nv_bfloat16, true>
-                       : rul::rules_kernel<__nv_bfloat16, false>);
+  const auto pick = [&](auto t) -> void (*)(rul::Args) {
+    using T = decltype(t);
+    if (single)
+      return even ? rul::rules_kernel<T, true, rul::kSingleQuads>
+                  : rul::rules_kernel<T, false, rul::kSingleQuads>;
+    return even ? rul::rules_kernel<T, true, rul::kRowQuads>
+                : rul::rules_kernel<T, false, rul::kRowQuads>;
+  };
+  const auto kernel = esz == 4 ? pick(0.f) : pick(__nv_bfloat16());
+  size_t smem = single ? rul::kBiasAt<rul::kSingleQuads> : rul::kBiasAt<rul::kRowQuads>;
+  if (ru.bias_begin) smem += slice * (single ? sizeof(unsigned short) : sizeof(unsigned));
+  if (single) {
+    static PerDevice limit[4];
+    if (smem_limit_once(limit[2 * (esz == 4) + even], kernel,
+                        rul::kBiasAt<rul::kSingleQuads> + wide * sizeof(unsigned short)) !=
+        cudaSuccess)
+      return SV_ERR_CUDA;
+  }
   if (sv::launch(kernel, (unsigned)ctas, rul::kThreads, smem, static_cast<cudaStream_t>(stream),
                  a) != cudaSuccess)
     return SV_ERR_CUDA;

@@ -337,6 +337,48 @@ def test_single_rows_in_place(V, masks):
     c.check()
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("R,V", [(620, 8192), (640, 5003), (310, 8196), (310, 8195), (160, 24581),
+                                 (100, 50257), (90, 50260)])
+@pytest.mark.parametrize("parts", ["pen", "pen bias mask", "bias mask"])
+def test_many_single_rows(R, V, dtype, parts):
+    c = Case([1] * R, V, dtype, pad=R % 3, hist=(0, 600), pen="pen" in parts,
+             bias=60 if "bias" in parts else 0, masks=0.3 if "mask" in parts else None, seed=V,
+             few=R == 310, behind=2)
+    c.bind()()
+    c.check()
+
+
+def test_many_single_rows_in_place_and_spoilt():
+    c = Case([1] * 640, 4003, bias=20, masks=0.5, hist=(0, 90))
+    c.bind()()
+    c.check()
+    first, x = c.out, c.x.contiguous().clone()
+    c.bind(out=x, logits=x)()
+    torch.cuda.synchronize()
+    assert torch.equal(first, x)
+    good = {k: v.copy() for k, v in c.kw.items()}
+    c.kw["history_len"][639] = 91
+    c.kw["repetition"][7] = 0.0
+    c.bind()()
+    c.kw = good
+    c.check(status=edges.BAD_LENGTH | edges.BAD_PARAM, rows=np.r_[0:7, 8:639])
+
+
+@pytest.mark.parametrize("n", [65533, 65534, 65535, 70000])
+def test_single_rows_with_long_lists_of_biases(n):
+    # a token's only entry may be the list's last, whatever the list's length
+    c = Case([1] * 620, 8000, hist=(0, 20))
+    token = c.rng.integers(0, 7000, n).astype(np.int32)
+    token[-1] = 7999
+    begin = np.full(621, n, np.int32)
+    begin[0] = 0
+    c.kw.update(bias_begin=begin, bias_token=token,
+                bias_value=c.rng.standard_normal(n).astype(np.float32))
+    c.bind()()
+    c.check()
+
+
 def test_misaligned_rows_and_outputs():
     c = Case([5, 6], 4096, bias=9, masks=0.5)
     wide = torch.zeros(11 * 4096 + 4, device="cuda")
