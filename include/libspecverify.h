@@ -459,7 +459,8 @@ sv_status sv_adapt_gamma(int32_t n_req, const int32_t* accepted_len, const int32
  * (a prompt); max_rows_per_req is then not limited to 128.  batch->tokens and
  * kv->k_cache / v_cache are not read.
  * Supported: block_size 16, n_req <= 8192, fewer than 2^27 blocks, at most
- * 2^30 rows. */
+ * 2^30 rows, n_req * min(max_blocks_per_req, max_rows_per_req / 16 + 2) below
+ * 2^31. */
 sv_status sv_reserve_kv(const sv_paged_kv* kv, const sv_batch* batch, const sv_block_pool* pool,
                         const int32_t* pos_offset, int32_t* slots, int32_t* positions,
                         int32_t* taken, int32_t* dev_status, void* stream);

@@ -375,6 +375,9 @@ extern "C" sv_status sv_reserve_kv(const sv_paged_kv* kv, const sv_batch* bt,
       bt->total_rows > 1 << 30)
     return SV_ERR_UNSUPPORTED_SHAPE;
   if (bt->parent && bt->max_rows_per_req > kMaxRows) return SV_ERR_UNSUPPORTED_SHAPE;
+  // the entries of all requests are numbered in 32 bits
+  const long span = min((long)kv->max_blocks_per_req, bt->max_rows_per_req / kBlockSize + 2L);
+  if (bt->n_req * span > INT_MAX) return SV_ERR_UNSUPPORTED_SHAPE;
   if (bt->n_req == 0 && bt->total_rows == 0) return SV_OK;
   if (!pool->free_list || !pool->free_count || (bt->total_rows > 0 && !slots))
     return SV_ERR_INVALID_ARGUMENT;

@@ -59,6 +59,19 @@ def test_reserve_refuses(lib):
     assert call(b=_batch(n_req=0, total_rows=0)) == N.SV_OK
 
 
+def test_reserve_refuses_what_its_counts_cannot_hold(lib):
+    # requests times the table entries that each may span: counted in 32 bits
+    # (offsets that overlap could reach it, whatever the number of rows)
+    def call(n_req, max_rows, entries):
+        kv, b = _kv(max_blocks_per_req=entries), _batch(n_req=n_req, max_rows_per_req=max_rows, parent=None,
+                                                        total_rows=1 << 30)
+        return lib.sv_reserve_kv(ctypes.byref(kv), ctypes.byref(b), ctypes.byref(N.SvBlockPool(A, A, 10)), None,
+                                 None, A, A, None, None)  # without slots it stops behind the check
+
+    assert call(8192, 1 << 30, 1 << 26) == call(32, 1 << 30, (1 << 27) - 1) == call(8192, 1 << 23, 1 << 19) == SHAPE
+    assert call(8192, 1 << 30, 1 << 17) == call(8192, 1 << 21, 1 << 26) == call(31, 1 << 30, (1 << 27) - 1) == BAD
+
+
 def test_stage_refuses(lib):
     half = N.SvRotary(A, 64, 0, 1, None, 1.0)
 
