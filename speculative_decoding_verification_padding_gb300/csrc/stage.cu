@@ -61,9 +61,9 @@ struct Args {
 constexpr int kVecs = 3;          // pieces of a thread's round; two rounds are in flight
 constexpr int kMaxThreads = 512;
 // Rows per SM from which a warp takes whole rows.  stream_kernel / row_kernel,
-// 56 heads of 128: 400 rows 7.8 / 5.3 us, 1000 rows 9.1 / 9.1, 1500 rows 12.9 /
-// 12.6, 2200 rows 13.7 / 16.1; 18 heads of 64: 1500 rows 4.6 / 4.1, 2200 rows
-// 4.7 / 4.9.
+// 56 heads of 128: 400 rows 7.8 / 5.2 us, 1000 rows 9.1 / 8.0, 1500 rows 12.9 /
+// 11.2, 1800 rows 13.3 / 14.7; 18 heads of 64: 1500 rows 4.6 / 3.6, 1800 rows
+// 4.6 / 4.8.
 constexpr int kStreamRows = 10;
 constexpr int kMaxHalf = 64;      // rotated pairs of a head at most
 
@@ -294,11 +294,28 @@ __global__ void __launch_bounds__(32) stream_kernel(Args a) {
   }
 }
 
-// Few rows: a CTA for each, a piece or two per thread, every load the row needs
-// in flight at once.
-constexpr int kRowVecs = 2;
+// Few rows: a CTA for each, every load the row needs in flight at once.  The
+// pieces come to shared memory by asynchronous copies, each to a place that
+// only the thread that asked for it reads, so no barrier stands between; a
+// thread works on its first while the others are on their way.  (Two pieces of
+// a thread at a time in registers: 1280 rows of 56 heads 11.8 us, so 10.2.)
+constexpr int kRowVecs = 8;                  // pieces of a thread in flight at most
+constexpr size_t kMaxRowSmem = 40 * 1024;
+// Waits until all but the last n of this thread's copies are there.
+__device__ __forceinline__ void wait_all_but(int n) {
+  switch (n) {
+    case 0: cp_async_wait<0>(); break;
+    case 1: cp_async_wait<1>(); break;
+    case 2: cp_async_wait<2>(); break;
+    case 3: cp_async_wait<3>(); break;
+    case 4: cp_async_wait<4>(); break;
+    case 5: cp_async_wait<5>(); break;
+    case 6: cp_async_wait<6>(); break;
+    default: cp_async_wait<7>(); break;
+  }
+}
 template <int D>
-__global__ void __launch_bounds__(kMaxThreads, 2) row_kernel(Args a) {
+__global__ void __launch_bounds__(kMaxThreads, 2) row_kernel(Args a, int vecs) {
   griddep_entry();
   constexpr int kLanes = D / 16;
   __shared__ __align__(16) float2 s_cs[kMaxHalf];
@@ -318,22 +335,25 @@ __global__ void __launch_bounds__(kMaxThreads, 2) row_kernel(Args a) {
     const int axis = a.freq_axis ? checked_axis(a, a.freq_axis[tid], true) : 0;
     pos = a.positions[(size_t)axis * a.axis_stride + r];
   }
-  uint4 x[kRowVecs][2];
+  extern __shared__ __align__(16) uint4 s_x[];  // [vecs][2][nt]
   auto fetch = [&](int h0) {
-#pragma unroll
-    for (int u = 0; u < kRowVecs; ++u) {
+    for (int u = 0; u < vecs; ++u) {
       const int h = h0 + u * hstep + hs;
-      x[u][0] = x[u][1] = make_uint4(0u, 0u, 0u, 0u);
+      uint4* to = s_x + (size_t)u * 2 * nt + tid;
       if (h < heads) {
         const __nv_bfloat16* p = piece_of<D>(a, r, h);
-        x[u][0] = *reinterpret_cast<const uint4*>(p + g0);
-        x[u][1] = *reinterpret_cast<const uint4*>(p + g1);
+        cp_async16(smem_u32(to), p + g0, 16);
+        cp_async16(smem_u32(to + nt), p + g1, 16);
+      } else {
+        to[0] = to[nt] = make_uint4(0u, 0u, 0u, 0u);
       }
+      cp_async_commit();
     }
   };
   fetch(0);  // (a row that turns out to be skipped was read in vain)
   if (slot < 0 || slot >= a.n_slots) {  // the same for the whole CTA
     if (slot != -1 && tid == 0) flag(a.dev_status, SV_DEV_BAD_SLOT);
+    cp_async_wait<0>();
     return;
   }
   if (tid < half) s_cs[tid] = turn_by(a, pos, turn_fraction(freq));
@@ -344,13 +364,14 @@ __global__ void __launch_bounds__(kMaxThreads, 2) row_kernel(Args a) {
     for (int t = 0; t < 4; ++t) cs[t] = *reinterpret_cast<const float4*>(&s_cs[8 * c + 2 * t]);
   }
   const size_t page = (size_t)(slot / kBlockSize) * a.Hkv * kBlockSize + (size_t)(slot % kBlockSize);
-  for (int h0 = 0; h0 < heads; h0 += kRowVecs * hstep) {
+  for (int h0 = 0; h0 < heads; h0 += vecs * hstep) {
     if (h0 > 0) fetch(h0);
-#pragma unroll
-    for (int u = 0; u < kRowVecs; ++u) {
+    for (int u = 0; u < vecs; ++u) {
       if (h0 + u * hstep >= heads) break;  // the same for the whole CTA
       const int h = h0 + u * hstep + hs;
-      finish<D>(a, x[u][0], x[u][1], h, h < heads, g0, g1, rot, cs, r, page);
+      wait_all_but(vecs - 1 - u);
+      const uint4* x = s_x + (size_t)u * 2 * nt + tid;
+      finish<D>(a, x[0], x[nt], h, h < heads, g0, g1, rot, cs, r, page);
     }
   }
 }
@@ -445,14 +466,16 @@ extern "C" sv_status sv_stage_qkv(const sv_paged_kv* kv, int32_t n_rows, const v
                    (unsigned)min((long)n_rows, nsm * 32L), 32, 0, s, a);
   } else {
     // a thread for every piece while that leaves an SM's rows side by side
-    // (1280 rows of 56 heads of 128, nine an SM: 96 threads 11.9 us, 160 13.7;
-    // 300 rows, two an SM: 448 threads 4.5 us)
+    // (1280 rows of 56 heads of 128, nine an SM: 96 threads 10.4 us, 64 13.0,
+    // 128 12.6; 300 rows, two an SM: 448 threads 4.1 us, 384 4.4)
     const long rows_per_sm = ((long)n_rows + nsm - 1) / nsm;
     const long most = min((long)stg::kMaxThreads, 1024 / rows_per_sm / 32 * 32);
     const unsigned threads =
         (unsigned)max((long)stg::kMaxHalf, min(most, (pieces + 31) / 32 * 32));
+    const long each = (pieces + threads - 1) / threads;
+    const int vecs = (int)max(1L, min(min(each, (long)stg::kRowVecs), (long)(stg::kMaxRowSmem / (32 * threads))));
     e = sv::launch(D == 64 ? stg::row_kernel<64> : stg::row_kernel<128>, (unsigned)n_rows, threads,
-                   0, s, a);
+                   (size_t)vecs * threads * 32, s, a, vecs);
   }
   if (e != cudaSuccess)
     return SV_ERR_CUDA;

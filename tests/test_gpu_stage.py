@@ -102,6 +102,14 @@ def test_head_layouts_and_rows(rows, heads, kv_heads, dim):
     c.check()
 
 
+@pytest.mark.parametrize("rows,heads,kv_heads,dim", [(3, 200, 8, 128), (150, 300, 40, 128), (2, 1000, 1, 64),
+                                                     (1300, 130, 3, 128), (1400, 90, 12, 64)])
+def test_rows_wider_than_a_block_holds_at_once(rows, heads, kv_heads, dim):
+    c = Case(rows, heads, kv_heads, dim, rotary=dim // 2, seed=heads)
+    c.bind()()
+    c.check()
+
+
 @pytest.mark.parametrize("dim,rotary", [(64, 0), (64, 16), (64, 48), (64, 64), (128, 0), (128, 32),
                                         (128, 80), (128, 96), (128, 128)])
 @pytest.mark.parametrize("interleaved", [False, True])
