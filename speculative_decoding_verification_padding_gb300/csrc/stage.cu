@@ -27,10 +27,11 @@
 // are read from shared memory once for all its heads.  (With 8 elements per
 // lane and shuffles for the partners, shared-memory and shuffle traffic
 // bounded the kernel at 43 % of HBM.)  A norm is two or three shuffles.
-// Many rows: each goes to a warp, which loads kVecs pieces per lane ahead of
-// the kVecs it works on, over the end of the row; the next row's sines are
-// computed under its last loads.  Few: a CTA for each, all its loads at once.
-// 20000 rows of 80 heads of 128: 133 us, 6.15 TB/s, 0.91 of the measured copy
+// Many rows: each (or each half of one) goes to a warp, which loads kVecs
+// pieces per lane ahead of the kVecs it works on, over the end of the row; the
+// next row's sines are computed under its last loads.  Few: a CTA for each, all
+// its loads at once.
+// 20000 rows of 80 heads of 128: 132 us, 6.20 TB/s, 0.91 of the measured copy
 // rate; six rows of 48 heads: 3.0 us.
 
 #include <limits.h>
@@ -60,11 +61,14 @@ struct Args {
 
 constexpr int kVecs = 3;          // pieces of a thread's round; two rounds are in flight
 constexpr int kMaxThreads = 512;
-// Rows per SM from which a warp takes whole rows.  stream_kernel / row_kernel,
-// 56 heads of 128: 400 rows 7.8 / 5.2 us, 1000 rows 9.1 / 8.0, 1500 rows 12.9 /
-// 11.2, 1800 rows 13.3 / 14.7; 18 heads of 64: 1500 rows 4.6 / 3.6, 1800 rows
-// 4.6 / 4.8.
-constexpr int kStreamRows = 10;
+constexpr int kStreamWarps = 16;  // warps of stream_kernel on an SM
+// A CTA takes a row as long as all rows are on the SMs at once, or there are no
+// more than kFewRows an SM; then a warp takes several in turn.  stream_kernel /
+// row_kernel: 56 heads of 128, 1000 rows 9.1 / 7.6 us, 1500 rows 12.9 / 10.6,
+// 1800 rows 13.3 / 13.4; 18 heads of 64, 4099 rows 8.0 / 6.5; rows too wide to be
+// there together, 160 heads of 128: 700 rows (five an SM) 15.1 / 15.0, 1000 rows
+// 22.0 / 23.9.
+constexpr int kFewRows = 4;
 constexpr int kMaxHalf = 64;      // rotated pairs of a head at most
 
 // f / (2 pi) modulo one turn, in units of 2^-64 of a turn.
@@ -172,8 +176,9 @@ __device__ __forceinline__ void finish(const Args& a, uint4 y0, uint4 y1, int h,
   }
 }
 
+// A warp's unit of work: a row (sh = 0) or half of one (sh = 1), `span` heads.
 template <int D>
-__global__ void __launch_bounds__(32) stream_kernel(Args a) {
+__global__ void __launch_bounds__(32) stream_kernel(Args a, int sh, int span) {
   griddep_entry();
   constexpr int kLanes = D / 16;  // lanes of a head
   __shared__ __align__(16) float2 s_cs[2][kMaxHalf];  // (cos, sin) of this row and the next
@@ -196,14 +201,16 @@ __global__ void __launch_bounds__(32) stream_kernel(Args a) {
     freq[i] = j < half ? a.inv_freq[j] : 0.f;
     axis[i] = j < half && a.freq_axis ? a.freq_axis[j] : 0;
   }
-  // Row r's slot and the positions its angles need, as loaded.
+  const long units = (long)a.N << sh;
+  // The slot of a unit's row and the positions its angles need, as loaded.
   struct Ahead {
     int slot;
     int pos[kFreqs];
   };
   unsigned long long frac[kFreqs];
-  auto look = [&](long r, Ahead& n) {
+  auto look = [&](long x, Ahead& n) {
     n.slot = -1;
+    const long r = x >> sh;
     if (r < a.N) {
       n.slot = a.slots[r];
 #pragma unroll
@@ -211,12 +218,12 @@ __global__ void __launch_bounds__(32) stream_kernel(Args a) {
         if (tid + i * nt < half) n.pos[i] = a.positions[(size_t)axis[i] * a.axis_stride + r];
     }
   };
-  // The first row from r on (in steps of the grid) that is not skipped.
-  auto settle = [&](long& r, Ahead& n) {
-    while (r < a.N && (n.slot < 0 || n.slot >= a.n_slots)) {  // the same for the whole CTA
+  // The first unit from x on (in steps of the grid) that is not skipped.
+  auto settle = [&](long& x, Ahead& n) {
+    while (x < units && (n.slot < 0 || n.slot >= a.n_slots)) {  // the same for the whole CTA
       if (n.slot != -1 && tid == 0) flag(a.dev_status, SV_DEV_BAD_SLOT);
-      r += gridDim.x;
-      look(r, n);
+      x += gridDim.x;
+      look(x, n);
     }
   };
   auto turn_table = [&](const Ahead& n, float2* table) {
@@ -228,43 +235,49 @@ __global__ void __launch_bounds__(32) stream_kernel(Args a) {
       }
     }
   };
+  auto from = [&](long x) { return sh ? ((int)x & 1) * span : 0; };  // its heads
+  auto upto = [&](long x) { return min(heads, from(x) + span); };
   struct Round {
     uint4 x[kVecs][2];
   };
-  auto fetch = [&](long r, int h0, Round& n) {
+  auto fetch = [&](long x, int h0, Round& n) {
+    const long r = x >> sh;
+    const int to = upto(x);
 #pragma unroll
     for (int u = 0; u < kVecs; ++u) {
       const int h = h0 + u * hstep + hs;
-      if (h < heads) {
+      if (h < to) {
         const __nv_bfloat16* p = piece_of<D>(a, r, h);
         n.x[u][0] = *reinterpret_cast<const uint4*>(p + g0);
         n.x[u][1] = *reinterpret_cast<const uint4*>(p + g1);
       }
     }
   };
-  long r = blockIdx.x;
+  long x = blockIdx.x;
   Ahead now;
   Round next;
-  now.slot = a.slots[r];
-  fetch(r, 0, next);  // (a row that turns out to be skipped was read in vain)
+  now.slot = a.slots[x >> sh];
+  fetch(x, from(x), next);  // (a row that turns out to be skipped was read in vain)
 #pragma unroll
   for (int i = 0; i < kFreqs; ++i) {
     axis[i] = checked_axis(a, axis[i], tid + i * nt < half);
     now.pos[i] = 0;
-    if (tid + i * nt < half) now.pos[i] = a.positions[(size_t)axis[i] * a.axis_stride + r];
+    if (tid + i * nt < half) now.pos[i] = a.positions[(size_t)axis[i] * a.axis_stride + (x >> sh)];
     frac[i] = turn_fraction(freq[i]);
   }
   if (now.slot < 0 || now.slot >= a.n_slots) {
-    settle(r, now);
-    if (r >= a.N) return;
-    fetch(r, 0, next);
+    settle(x, now);
+    if (x >= units) return;
+    fetch(x, from(x), next);
   }
   turn_table(now, s_cs[0]);
-  for (int par = 0; r < a.N; par ^= 1) {
+  for (int par = 0; x < units; par ^= 1) {
+    const long r = x >> sh;
+    const int end = upto(x);
     const long slot = now.slot;
     const size_t page = (size_t)(slot / kBlockSize) * a.Hkv * kBlockSize + (size_t)(slot % kBlockSize);
-    long rn = r + gridDim.x;
-    look(rn, now);
+    long xn = x + gridDim.x;
+    look(xn, now);
     __syncwarp();  // the row's table is there, the other one is free
     float4 cs[4];     // this piece's eight pairs: (cos, sin, cos, sin)
     if (rot) {
@@ -272,25 +285,25 @@ __global__ void __launch_bounds__(32) stream_kernel(Args a) {
       for (int t = 0; t < 4; ++t)
         cs[t] = *reinterpret_cast<const float4*>(&s_cs[par][8 * c + 2 * t]);
     }
-    for (int h0 = 0; h0 < heads; h0 += kVecs * hstep) {
-      const Round x = next;
-      if (h0 + kVecs * hstep < heads) {
-        fetch(r, h0 + kVecs * hstep, next);
+    for (int h0 = from(x); h0 < end; h0 += kVecs * hstep) {
+      const Round cur = next;
+      if (h0 + kVecs * hstep < end) {
+        fetch(x, h0 + kVecs * hstep, next);
       } else {
-        settle(rn, now);
-        if (rn < a.N) {
-          fetch(rn, 0, next);
+        settle(xn, now);
+        if (xn < units) {
+          fetch(xn, from(xn), next);
           turn_table(now, s_cs[par ^ 1]);
         }
       }
 #pragma unroll
       for (int u = 0; u < kVecs; ++u) {
-        if (h0 + u * hstep >= heads) break;  // the same for the whole CTA
+        if (h0 + u * hstep >= end) break;  // the same for the whole CTA
         const int h = h0 + u * hstep + hs;
-        finish<D>(a, x.x[u][0], x.x[u][1], h, h < heads, g0, g1, rot, cs, r, page);
+        finish<D>(a, cur.x[u][0], cur.x[u][1], h, h < end, g0, g1, rot, cs, r, page);
       }
     }
-    r = rn;
+    x = xn;
   }
 }
 
@@ -328,12 +341,17 @@ __global__ void __launch_bounds__(kMaxThreads, 2) row_kernel(Args a, int vecs) {
   const int g1 = rot && !a.inter ? half + 8 * c : 16 * c + 8;
   const long r = blockIdx.x;
   const long slot = a.slots[r];
-  float freq = 0.f;
-  int pos = 0;
-  if (tid < half) {
-    freq = a.inv_freq[tid];
-    const int axis = a.freq_axis ? checked_axis(a, a.freq_axis[tid], true) : 0;
-    pos = a.positions[(size_t)axis * a.axis_stride + r];
+  constexpr int kFreqs = kMaxHalf / 32;
+  float freq[kFreqs];
+  int pos[kFreqs];
+#pragma unroll
+  for (int i = 0; i < kFreqs; ++i) {
+    const int j = tid + i * nt;
+    if (j < half) {
+      freq[i] = a.inv_freq[j];
+      const int axis = a.freq_axis ? checked_axis(a, a.freq_axis[j], true) : 0;
+      pos[i] = a.positions[(size_t)axis * a.axis_stride + r];
+    }
   }
   extern __shared__ __align__(16) uint4 s_x[];  // [vecs][2][nt]
   auto fetch = [&](int h0) {
@@ -356,7 +374,11 @@ __global__ void __launch_bounds__(kMaxThreads, 2) row_kernel(Args a, int vecs) {
     cp_async_wait<0>();
     return;
   }
-  if (tid < half) s_cs[tid] = turn_by(a, pos, turn_fraction(freq));
+#pragma unroll
+  for (int i = 0; i < kFreqs; ++i) {
+    const int j = tid + i * nt;
+    if (j < half) s_cs[j] = turn_by(a, pos[i], turn_fraction(freq[i]));
+  }
   __syncthreads();
   float4 cs[4];
   if (rot) {
@@ -461,19 +483,32 @@ extern "C" sv_status sv_stage_qkv(const sv_paged_kv* kv, int32_t n_rows, const v
   if (nsm < 1) return SV_ERR_CUDA;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
-  if (n_rows >= (long)nsm * stg::kStreamRows) {
+  const long per_sm = ((long)n_rows + nsm - 1) / nsm;
+  // a CTA's own shared memory: its table and what the system takes
+  const bool resident = per_sm <= 32 && per_sm * (pieces * 32 + 1536) <= 227 * 1024L;
+  if (!resident && per_sm > stg::kFewRows) {
+    const int heads = n_q_heads + 2 * kv->n_kv_heads, round = stg::kVecs * (32 / lanes);
+    const int rounds = (heads + round - 1) / round;
+    // Halves of rows where the last wave would hold few whole ones (2600 rows of
+    // 80 heads 25.0 us against 26.9; of 160 heads 42.7 against 49.2).  Rows of
+    // one round are never halved: no half is empty.
+    const long wave = (long)nsm * stg::kStreamWarps;
+    const auto cost = [&](int parts, int each) {
+      return (n_rows * (long)parts + wave - 1) / wave * (2 * each + 1);
+    };
+    const int sh = cost(2, (rounds + 1) / 2) < cost(1, rounds) ? 1 : 0;
+    const int span = ((rounds + (1 << sh) - 1) >> sh) * round;
     e = sv::launch(D == 64 ? stg::stream_kernel<64> : stg::stream_kernel<128>,
-                   (unsigned)min((long)n_rows, nsm * 32L), 32, 0, s, a);
+                   (unsigned)min((long)n_rows << sh, 2 * wave), 32, 0, s, a, sh, span);
   } else {
     // a thread for every piece while that leaves an SM's rows side by side
     // (1280 rows of 56 heads of 128, nine an SM: 96 threads 10.4 us, 64 13.0,
     // 128 12.6; 300 rows, two an SM: 448 threads 4.1 us, 384 4.4)
-    const long rows_per_sm = ((long)n_rows + nsm - 1) / nsm;
-    const long most = min((long)stg::kMaxThreads, 1024 / rows_per_sm / 32 * 32);
-    const unsigned threads =
-        (unsigned)max((long)stg::kMaxHalf, min(most, (pieces + 31) / 32 * 32));
+    const long most = min((long)stg::kMaxThreads, 1024 / per_sm / 32 * 32);
+    const unsigned threads = (unsigned)max(32L, min(most, (pieces + 31) / 32 * 32));
     const long each = (pieces + threads - 1) / threads;
-    const int vecs = (int)max(1L, min(min(each, (long)stg::kRowVecs), (long)(stg::kMaxRowSmem / (32 * threads))));
+    const long room = (long)(stg::kMaxRowSmem / (32 * threads));
+    const int vecs = (int)max(1L, min(min(each, (long)stg::kRowVecs), room));
     e = sv::launch(D == 64 ? stg::row_kernel<64> : stg::row_kernel<128>, (unsigned)n_rows, threads,
                    (size_t)vecs * threads * 32, s, a, vecs);
   }
