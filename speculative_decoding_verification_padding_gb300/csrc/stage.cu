@@ -21,8 +21,8 @@
 // Bound: HBM for many rows (each element read once and written once), launch
 // and one load latency for few.  A piece is 16 elements of a head, two 16-byte
 // vectors chosen so that both elements of every pair are the same thread's (8
-// elements of the first half and their 8 partners of the second, or 16
-// neighbours), and it lies at the same place of every head a thread works on:
+// elements of the first half and their 8 partners of the second, or whole
+// pairs of neighbours), and it lies at the same place of every head a thread works on:
 // the rotation needs no exchange between lanes, and a row's sine and cosine
 // are read from shared memory once for all its heads.  (With 8 elements per
 // lane and shuffles for the partners, shared-memory and shuffle traffic
@@ -32,7 +32,7 @@
 // next row's sines are computed under its last loads.  Few: a CTA for each, all
 // its loads at once.
 // 20000 rows of 80 heads of 128: 132 us, 6.20 TB/s, 0.91 of the measured copy
-// rate; six rows of 48 heads: 3.0 us.
+// rate; six rows of 48 heads: 2.8 us.
 
 #include <limits.h>
 #include <math.h>
@@ -188,8 +188,12 @@ __global__ void __launch_bounds__(32) stream_kernel(Args a, int sh, int span) {
   const int heads = a.Hq + 2 * a.Hkv;
   const int c = tid % kLanes, hs = tid / kLanes, hstep = nt / kLanes;
   const bool rot = 16 * c < a.rd;  // rotary_dim is a multiple of 16: whole pieces
-  const int g0 = rot && !a.inter ? 8 * c : 16 * c;
-  const int g1 = rot && !a.inter ? half + 8 * c : 16 * c + 8;
+  // A piece's two vectors lie half of the rotated (or of the other) elements
+  // apart, whichever make a pair: neighbouring lanes read neighbouring vectors
+  // (20000 rows with a norm alone 137 us; two neighbours a lane 160).
+  const int g0 = rot ? 8 * c : a.rd + 8 * (c - a.rd / 16);
+  const int g1 = g0 + (rot ? half : (D - a.rd) >> 1);
+  const int t0 = (a.inter ? 4 : 8) * c, t1 = t0 + (a.inter ? half >> 1 : 4);  // their pairs
   // The frequencies this lane turns every row's position by, as loaded; what
   // they make is computed behind the first row's loads.
   constexpr int kFreqs = kMaxHalf / 32;
@@ -283,7 +287,7 @@ __global__ void __launch_bounds__(32) stream_kernel(Args a, int sh, int span) {
     if (rot) {
 #pragma unroll
       for (int t = 0; t < 4; ++t)
-        cs[t] = *reinterpret_cast<const float4*>(&s_cs[par][8 * c + 2 * t]);
+        cs[t] = *reinterpret_cast<const float4*>(&s_cs[par][(t < 2 ? t0 : t1) + 2 * (t & 1)]);
     }
     for (int h0 = from(x); h0 < end; h0 += kVecs * hstep) {
       const Round cur = next;
@@ -337,6 +341,7 @@ __global__ void __launch_bounds__(kMaxThreads, 2) row_kernel(Args a, int vecs) {
   const int heads = a.Hq + 2 * a.Hkv;
   const int c = tid % kLanes, hs = tid / kLanes, hstep = nt / kLanes;
   const bool rot = 16 * c < a.rd;
+  // (the places that stream_kernel takes cost 1 us of 10 here)
   const int g0 = rot && !a.inter ? 8 * c : 16 * c;
   const int g1 = rot && !a.inter ? half + 8 * c : 16 * c + 8;
   const long r = blockIdx.x;

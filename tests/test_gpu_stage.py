@@ -110,6 +110,15 @@ def test_rows_wider_than_a_block_holds_at_once(rows, heads, kv_heads, dim):
     c.check()
 
 
+@pytest.mark.parametrize("dim,rotary", [(64, 0), (64, 16), (64, 48), (64, 64), (128, 0), (128, 48), (128, 112),
+                                        (128, 128)])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_partial_rotation_of_many_rows(dim, rotary, interleaved):
+    c = Case(5001, 5, 2, dim, rotary, axes=3 if rotary else 1, interleaved=interleaved, skip=3, seed=rotary)
+    c.bind()()
+    c.check()
+
+
 @pytest.mark.parametrize("rows,heads,kv_heads,dim,skip", [
     (2600, 64, 8, 128, 0), (2600, 64, 8, 128, 2500), (2433, 21, 2, 128, 7), (4300, 33, 8, 64, 40), (4865, 3, 1, 64, 0),
     (4864, 4, 1, 64, 9), (5100, 10, 3, 64, 5000), (1700, 70, 1, 128, 100)])
