@@ -34,6 +34,9 @@
 // a shared-memory ring of bulk copies: 437 to 528, with warps specialised: 416;
 // the history counted by eight CTAs through distributed shared memory: 360
 // (the slice of the most frequent tokens takes 42 % of the remote updates).
+// 783 rows of 50257 in bf16 under masks that permit 48 tokens: 58.6 us; barred
+// entries written before the rules are prepared: 68.2; vectors that begin on
+// 128 instead of 16 bytes of the output: 63.5.
 
 #include "sv_internal.cuh"
 
