@@ -192,7 +192,9 @@ sv_status sv_tree_attend(const sv_paged_kv* kv, const sv_batch* batch, const voi
  *     in the window, accept x_j iff u(i, j) < min(1, p_{j-1}(x_j) /
  *     q_{j-1}(x_j)); at the first rejection emit a token drawn from
  *     normalize(max(0, p_{j-1} - q_{j-1})); if every draft up to lim_i - 1
- *     is accepted emit a token drawn from p_{lim_i - 1}.
+ *     is accepted emit a token drawn from p_{lim_i - 1}.  (q = 0 < p: the
+ *     ratio is 1.  p = q = 0, a token barred on both sides: it was not drawn
+ *     from this q, so it is rejected and the token drawn from p_{j-1}.)
  *   temperature > 0 (trees, one window over all rows; siblings drawn
  *     independently from the parent's q): from the root, children are tried
  *     in index order; child c (token x) is accepted iff u(i, c) <
@@ -201,7 +203,8 @@ sv_status sv_tree_attend(const sv_paged_kv* kv, const sv_batch* batch, const voi
  *     c_j q_n) / S(c_j), S(c) = sum_v max(0, p_n,v - c q_n,v), c_0 = 0,
  *     c_{j+1} = c_j + S(c_j).  On acceptance the walk moves to c; when every
  *     child is rejected the emitted token is drawn from p' (from p_n if S
- *     vanished); at a leaf it is drawn from p_leaf.  (Tree verification is
+ *     vanished); at a leaf it is drawn from p_leaf.  A child barred on both
+ *     sides (p_n = q_n = 0) is passed over, p' stays as it is.  (Tree verification is
  *     on the pages; this multi-candidate rejection rule is the plainest
  *     lossless reading.)
  *   temperature == 0 (chains and trees): keep the longest root-to-node path

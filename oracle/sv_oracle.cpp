@@ -453,7 +453,8 @@ struct AcceptArgs {
 // max(0, p_v - c q_v), with c_0 = 0 (S(0) = 1) and c_{j+1} = c_j + S(c_j):
 // max(0, max(0, p - c q) / S - q) = max(0, p - (c + S) q) / S.  If S reaches
 // 0 (p <= c q everywhere) the residual is undefined: the remaining siblings
-// are not tested and the token is drawn from p_n.  Uniforms: child c uses
+// are not tested and the token is drawn from p_n.  A sibling with p_n = q_n = 0
+// (barred on both sides) was not drawn from q_n and is passed over.  Uniforms: child c uses
 // accept_uniform(seed, i, c); the emitted token uses the race stream at
 // position (accepted nodes + 1), as for a chain.
 double residual_mass(const float* lp, const float* lq, int V, float T, const RowSoftmax& sp,
@@ -484,6 +485,7 @@ void tree_sample(const AcceptArgs& a, int i, const Window& w, int cu, int32_t* n
     for (int ch : kids) {
       const int x = a.tokens[cu + ch];
       const double p = prob(lp, x, a.T, sp), q = prob(lq, x, a.T, sq);
+      if (p == 0.0 && q == 0.0) continue;  // barred on both sides: not a draw from q_n
       const double pres = std::max(0.0, p - c * q) / S;
       const double ratio = q > 0.0 ? std::min(1.0, pres / q) : 1.0;
       const double u = accept_uniform(a.seed, i, ch);
@@ -624,6 +626,11 @@ int accept_one(const AcceptArgs& a, int i) {
       }
       double ratio = q > 0.0 ? std::min(1.0, p / q) : 1.0;
       double u = accept_uniform(a.seed, i, j);
+      if (p == 0.0 && q == 0.0) {  // barred on both sides: not a draw from q, nothing was tried
+        a.next_token[i] =
+            race_sample(lp, nullptr, a.V, a.T, sp[j - 1], nullptr, a.seed, i, j, &amb);
+        break;
+      }
       if (std::fabs(u - ratio) < 1e-6) amb = true;
       if (u < ratio) {
         a.accepted_len[i] = j;

@@ -290,16 +290,20 @@ __device__ __forceinline__ void two_sum(float a, float b, float& s, float& e) {
 // Everything stays in fp32: double precision runs at a small fraction of the
 // fp32 rate on this GPU, and the dependent fp64 chain of the former form
 // cost microseconds per decision.  q that would vanish in double (q below
-// the smallest denormal) gives ratio 1, as the definition's q > 0 test does.
+// the smallest denormal) gives ratio 1, as the definition's q > 0 test does,
+// unless p vanishes with it: such a token is barred on both sides.
 // p and q themselves (row statistics output) are formed in fp32.
 // p / q itself (unclamped), by the same exact exponent: +inf stands for a q
-// that vanishes in double, 0 for p = 0.
+// that vanishes in double, 0 for p = 0, kBarred for both.
+constexpr float kBarred = -1.f;
+constexpr float kVanishes = -745.13f;  // exp of anything below is 0 in double
 __device__ __forceinline__ float pq_ratio(float xp, float xq, float mp, float lp, float mq,
                                           float lq) {
   float s1, e1, s2, e2, h, l;
   two_sum(xq, -mq, s2, e2);
-  if (s2 - logf(lq) < -745.13f) return INFINITY;  // also xq = -inf
   two_sum(xp, -mp, s1, e1);
+  if (s2 - logf(lq) < kVanishes)  // also xq = -inf
+    return s1 - logf(lp) < kVanishes ? kBarred : INFINITY;
   if (s1 == -INFINITY) return 0.f;                // p = 0
   two_sum(s1, -s2, h, l);
   l = __fadd_rn(l, __fsub_rn(e1, e2));
@@ -584,6 +588,17 @@ __device__ int decide_request(const Args& a, int nch, int i, DecideSmem& sm, Com
     if (u < r_j) {
       len = j;
       if (lane == 0) nodes[j] = j;
+    } else if (r_j == kBarred) {
+      // not a draw from q, so its rejection takes nothing from p: the token
+      // comes from p itself (the residual would count q's mass as tried)
+      jb.mode = 2;
+      jb.row = cu + j - 1;
+      jb.pos = j;
+      jb.mp = sm.mp[j - 1];
+      jb.lp = sm.lp[j - 1];
+      jb.mq = 0.f;
+      jb.lq = 1.f;
+      break;
     } else {
       jb.mode = 1;
       jb.row = cu + j - 1;
@@ -1221,17 +1236,23 @@ __global__ void __launch_bounds__(NT) tree_kernel(Args a) {
         // from the exact exponent in fp32 (as on chains; fp64 runs at a
         // small fraction of the fp32 rate on this GPU) and 1 / S taken once
         // per pass.  q that vanishes gives ratio 1, as the definition's
-        // q > 0 test does; p = 0 gives 0.
+        // q > 0 test does; p = 0 gives 0.  A sibling barred on both sides is
+        // not a draw from q: it is passed over, p' stays as it is.
         const float r_pq = pq_ratio(s_xp[ch] / T, s_xq[ch] / T, s_st[0], s_st[1], s_st[2], s_st[3]);
-        const double ratio =
-            r_pq == INFINITY ? 1.0 : fmin(1.0, fmax(0.0, (double)r_pq - c) * inv_S);
-        const double u = (double)accept_u(a.seed, i, ch);
-        if (fabs(u - ratio) < 1e-6) amb = true;
-        s_dec = u < ratio ? 1 : 0;
+        if (r_pq == kBarred) {
+          s_dec = 2;
+        } else {
+          const double ratio =
+              r_pq == INFINITY ? 1.0 : fmin(1.0, fmax(0.0, (double)r_pq - c) * inv_S);
+          const double u = (double)accept_u(a.seed, i, ch);
+          if (fabs(u - ratio) < 1e-6) amb = true;
+          s_dec = u < ratio ? 1 : 0;
+        }
       }
       __syncthreads();
       const int dec = s_dec;
       __syncthreads();  // s_dec is rewritten by the next test
+      if (dec == 2) continue;
       if (dec) {
         if (tid == 0 && rank == 0) nodes[k + 1] = ch;
         ++k;
