@@ -105,3 +105,33 @@ def test_a_long_chain_barred_behind_its_first_warp():
     assert err == 0 and status.item() == 0
     assert al.item() == st.accepted_len[0] == 39
     assert nxt.item() == st.next_token[0] and np.isfinite(logits[39, nxt.item()])
+
+
+LOWEST = float(np.finfo(np.float32).min)
+
+
+def _grammar(w, seed, low, few=6):
+    """Masks that permit a few tokens of the vocabulary, most of the row's
+    drafted ones among them, as a grammar's do: everything else is at low."""
+    rng = np.random.default_rng(seed)
+    V = w.target_logits.shape[1]
+    for i in range(w.n_req):
+        c0, c1 = w.cu_rows[i], w.cu_rows[i + 1]
+        for r in range(c0, c1):
+            let = [w.tokens[c] for c in range(c0 + 1, c1) if w.parent[c] == r - c0 and rng.random() < 0.7]
+            let = np.union1d(let, rng.choice(V, few, replace=False)).astype(int)
+            for x in (w.target_logits[r], w.draft_logits[r]):
+                kept = x[let].copy()
+                x[:] = low
+                x[let] = kept
+            # drafts that p and q agree about
+            w.target_logits[r, let] = w.draft_logits[r, let] + rng.normal(0, 0.3, len(let))
+    return w
+
+
+@pytest.mark.parametrize("case", list(CASES))
+def test_masks_whose_quotient_is_below_the_range(case):
+    # the lowest fp32 over T = 0.7 is -inf
+    kw = dict(CASES[case])
+    w = _grammar(wl.make_workload(wl.config(kw.pop("name")), ctx_scale=0.01, temperature=0.7, **kw), 4, LOWEST)
+    _no_barred_token(w, *_check(w, 0.7))
