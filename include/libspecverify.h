@@ -232,8 +232,9 @@ sv_status sv_tree_attend(const sv_paged_kv* kv, const sv_batch* batch, const voi
  * A window starting at row 0 resets the request's state; a later window
  * continues it (requests already decided are skipped).
  * target_logits, draft_logits: fp32 [total_rows][vocab]; draft_logits may be
- * NULL when temperature == 0.  A logit of -inf (a barred token) has
- * probability 0; every row needs one that is finite.
+ * NULL when temperature == 0.  A barred token's logit of -inf or of the lowest
+ * fp32 values has probability 0; every row needs one logit that is not barred,
+ * and no logit's quotient by the temperature is above 2^126.
  * ws: at least sv_accept_workspace() bytes, 256-byte aligned. */
 size_t sv_accept_workspace(const sv_batch* batch, int32_t vocab);
 sv_status sv_accept(const sv_batch* batch, const float* target_logits, const float* draft_logits,

@@ -631,6 +631,7 @@ __device__ int decide_request(const Args& a, int nch, int i, DecideSmem& sm, Com
 }
 
 // ----------------------------------------------------------------- stats --
+constexpr float kMaxInLog2 = 0x1.6p127f;  // times log2 e it is below 2^128
 // Warp-granular: every warp owns one slice of one row at a time and reduces
 // it with shuffles into one partial (no warp waits for another); the
 // decision kernel merges the partials.
@@ -743,12 +744,19 @@ __global__ void __launch_bounds__(kStatThreads, 4) stats_kernel(Args a) {
             l *= ex2((m - mx) * kLog2e);
             m = mx;
           }
-          if (m != -INFINITY) {  // nothing but -inf so far adds nothing
+          if (fabsf(m) < kMaxInLog2) {
             const float mb = m * kLog2e;
 #pragma unroll
             for (int k = 0; k < kDepth; ++k)
               l += (ex2(fmaf(x[k].x, kLog2e, -mb)) + ex2(fmaf(x[k].y, kLog2e, -mb))) +
                    (ex2(fmaf(x[k].z, kLog2e, -mb)) + ex2(fmaf(x[k].w, kLog2e, -mb)));
+          } else if (m != -INFINITY) {
+            // nothing but masks of the type's lowest value so far: m log2 e is
+            // past the range (nothing but -inf adds nothing)
+#pragma unroll
+            for (int k = 0; k < kDepth; ++k)
+              l += (ex2((x[k].x - m) * kLog2e) + ex2((x[k].y - m) * kLog2e)) +
+                   (ex2((x[k].z - m) * kLog2e) + ex2((x[k].w - m) * kLog2e));
           }
         }
       } else {

@@ -135,3 +135,13 @@ def test_masks_whose_quotient_is_below_the_range(case):
     kw = dict(CASES[case])
     w = _grammar(wl.make_workload(wl.config(kw.pop("name")), ctx_scale=0.01, temperature=0.7, **kw), 4, LOWEST)
     _no_barred_token(w, *_check(w, 0.7))
+
+
+@pytest.mark.parametrize("T,low", [(1.0, LOWEST), (1.3, LOWEST), (0.7, 0.69 * LOWEST), (1.0, -np.inf), (0.7, -np.inf)])
+@pytest.mark.parametrize("case", list(CASES) + ["wide"])
+def test_masks_that_permit_a_few_tokens(case, T, low):
+    # whole spans of a row are barred, at -inf or at a value whose product with
+    # log2 e is past the range
+    kw = dict(CASES.get(case, dict(name="chain8b", vocab=128256, draft_sigma=0.3)))
+    w = _grammar(wl.make_workload(wl.config(kw.pop("name")), ctx_scale=0.01, temperature=T, **kw), 6, low)
+    _no_barred_token(w, *_check(w, T))
