@@ -52,6 +52,7 @@ constexpr int kMaxRequests = 8192;  // five ints of shared memory each
 constexpr int kClusterRows = 1024;
 constexpr int kMaxCluster = 8;
 constexpr size_t kMaxSmem = 200 * 1024;  // more: the rows go to a second launch
+constexpr size_t kFreeSmem = 47 * 1024;  // less may be had unasked: 48 KB with the kernel's own scan words
 // Chains without parents have nothing to check: from here on a second launch
 // over all SMs is faster (75000 rows 12.7 us against 17.9; 23000 rows 8.4 both).
 constexpr int kChainRows = 32768;
@@ -410,7 +411,7 @@ extern "C" sv_status sv_reserve_kv(const sv_paged_kv* kv, const sv_batch* bt,
     a.cluster = 1;
     smem = rsv::plan_smem(a.R, 0, 0);
   }
-  if (smem > 48 * 1024) {
+  if (smem > rsv::kFreeSmem) {
     static PerDevice smem_set;
     if (smem_limit_once(smem_set, rsv::plan_kernel, rsv::kMaxSmem) != cudaSuccess)
       return SV_ERR_CUDA;
