@@ -23,6 +23,8 @@
  *                     chunked step;
  *   sv_reserve_kv     blocks for a step's rows taken from the pool, their
  *                     cache slots and positions (sv_commit_kv's counterpart);
+ *   sv_slot_windows   row windows that keep requests without slots out of
+ *                     the rest of the step;
  *   sv_stage_qkv      head norms and rotation of the rows' Q and K, K and V
  *                     written into the cache pages sv_tree_attend reads;
  *   sv_shape_logits   penalties for repeated tokens, biases and grammar masks
@@ -455,8 +457,8 @@ sv_status sv_adapt_gamma(int32_t n_req, const int32_t* accepted_len, const int32
  *     slots is -1.  pos_offset (nullable): int32 [n_req].
  * Packed rows of no request (behind cu_rows[n_req]) get -1 in both.  A
  * request that is malformed (SV_DEV_BAD_WINDOW, BAD_LENGTH, BAD_BLOCK_ID,
- * BAD_PARENT) or does not fit (SV_DEV_POOL_EMPTY) is left as it was; a
- * free-list entry that is no block id is dropped with SV_DEV_BAD_BLOCK_ID
+ * BAD_PARENT) or does not fit (SV_DEV_POOL_EMPTY) is left as it was, and has to
+ * be kept out of the rest of the step (sv_slot_windows); a free-list entry that is no block id is dropped with SV_DEV_BAD_BLOCK_ID
  * (its table entry stays -1, its rows get slot -1).  Row windows and
  * verify_len are ignored, as the commit ignores them.
  * batch->parent may be NULL here: every request is a chain, of any length
@@ -468,6 +470,20 @@ sv_status sv_adapt_gamma(int32_t n_req, const int32_t* accepted_len, const int32
 sv_status sv_reserve_kv(const sv_paged_kv* kv, const sv_batch* batch, const sv_block_pool* pool,
                         const int32_t* pos_offset, int32_t* slots, int32_t* positions,
                         int32_t* taken, int32_t* dev_status, void* stream);
+
+/* Windows for the calls behind sv_reserve_kv: row_end[i] = lim_i (all verified
+ * rows of request i) where each of those rows has a slot inside the cache, else
+ * 0, an empty window.  As the batch's row_end (row_begin NULL) it keeps a
+ * request that was not served, whose rows are not staged, out of
+ * sv_tree_attend, sv_accept and sv_accept_commit: its cache length, blocks and
+ * outputs stay as they were, and the step can be tried again.  (Without it the
+ * request would be decided and committed over slots that were never written.
+ * sv_commit_kv takes no windows: there its accepted_len has to be -1.)
+ * A request whose offsets or verify_len are malformed gets 0 too.  The batch's
+ * own row windows are ignored.  slots: int32 [total_rows], -1 = none.
+ * Supported: block_size 16, max_rows_per_req <= 128. */
+sv_status sv_slot_windows(const sv_paged_kv* kv, const sv_batch* batch, const int32_t* slots,
+                          int32_t* row_end, void* stream);
 
 /* ----------------------------------------------------------------- stage --
  * Fills what sv_tree_attend reads from the rows' projections: for every row r

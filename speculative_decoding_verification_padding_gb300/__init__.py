@@ -8,13 +8,13 @@ draws the seeded synthetic inputs.
 
 from .api import (Batch, BlockPool, LogitRules, PagedKV, Rotary, sv_accept, sv_accept_workspace,
                   sv_chunk_windows, sv_commit_kv, sv_reserve_kv, sv_select_budget,
-                  sv_select_budget_workspace, sv_shape_logits, sv_stage_qkv, sv_tree_attend,
-                  sv_tree_attend_workspace, sv_verify_chunked, sv_verify_chunked_workspace,
-                  workspace)
+                  sv_select_budget_workspace, sv_shape_logits, sv_slot_windows, sv_stage_qkv,
+                  sv_tree_attend, sv_tree_attend_workspace, sv_verify_chunked,
+                  sv_verify_chunked_workspace, workspace)
 from ._native import SpecVerifyError
 
 __all__ = ["Batch", "BlockPool", "LogitRules", "PagedKV", "Rotary", "SpecVerifyError", "sv_accept",
            "sv_accept_workspace", "sv_chunk_windows", "sv_commit_kv", "sv_reserve_kv",
-           "sv_select_budget", "sv_select_budget_workspace", "sv_shape_logits", "sv_stage_qkv",
-           "sv_tree_attend", "sv_tree_attend_workspace", "sv_verify_chunked",
+           "sv_select_budget", "sv_select_budget_workspace", "sv_shape_logits", "sv_slot_windows",
+           "sv_stage_qkv", "sv_tree_attend", "sv_tree_attend_workspace", "sv_verify_chunked",
            "sv_verify_chunked_workspace", "workspace"]

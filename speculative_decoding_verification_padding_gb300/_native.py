@@ -98,6 +98,7 @@ PROTOTYPES = {
     "sv_select_chunk": (ctypes.c_int, [I32, P, P, P, ctypes.c_double, ctypes.c_double, U64, P, P,
                                        P, P, P]),
     "sv_reserve_kv": (ctypes.c_int, [P, P, P, P, P, P, P, P, P]),
+    "sv_slot_windows": (ctypes.c_int, [P, P, P, P, P]),
     "sv_stage_qkv": (ctypes.c_int, [P, I32, P, I64, P, I64, P, I64, I32, P, P, I64, P, P, P, F32, P,
                                     P, P]),
     "sv_shape_logits": (ctypes.c_int, [P, P, I32, I64, I32, P, P, P, P]),

@@ -587,6 +587,33 @@ def bind_reserve_kv(kv: PagedKV, batch: Batch, pool: BlockPool, slots: torch.Ten
                      (kv, batch, pool, slots, positions, taken, pos_offset, dev_status))
 
 
+def _slot_windows_args(kv, batch, slots, row_end):
+    _expect(slots, torch.int32, "slots")
+    _expect(row_end, torch.int32, "row_end")
+    _at_least(slots, batch.total_rows, "slots")
+    _at_least(row_end, batch.n_req, "row_end")
+    _at_least(batch.verify_len, batch.n_req, "verify_len")
+    dev = _one_device(batch.cu_rows, batch.verify_len, slots, row_end)
+    b, k = batch.c(), kv.c()
+    return (ctypes.byref(k), ctypes.byref(b), _ptr(slots), _ptr(row_end)), dev
+
+
+def sv_slot_windows(kv: PagedKV, batch: Batch, slots: torch.Tensor, row_end: torch.Tensor,
+                    stream=None):
+    """row_end [n_req]: all rows of a request whose rows all have cache slots, 0
+    for any other.  As the batch's row_end it keeps what was not served out of
+    the rest of the step."""
+    args, _ = _slot_windows_args(kv, batch, slots, row_end)
+    _call("sv_slot_windows", args, stream)
+
+
+def bind_slot_windows(kv: PagedKV, batch: Batch, slots: torch.Tensor,
+                      row_end: torch.Tensor) -> BoundCall:
+    """sv_slot_windows with its arguments marshalled once (see BoundCall)."""
+    args, dev = _slot_windows_args(kv, batch, slots, row_end)
+    return BoundCall("sv_slot_windows", args, dev, (kv, batch, slots, row_end))
+
+
 def _stage_args(kv, q, k, v, slots, positions, rotary, q_out, q_weight, k_weight, eps, dev_status):
     for name, t in (("q", q), ("k", k), ("v", v), ("q_out", q_out)):
         _expect(t, torch.bfloat16, name)

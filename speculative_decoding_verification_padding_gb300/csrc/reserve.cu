@@ -1,5 +1,6 @@
 // reserve.cu — sv_reserve_kv: the blocks, cache slots and positions of a
-// step's rows, built on the GPU from the requests' lengths.
+// step's rows, built on the GPU from the requests' lengths; sv_slot_windows:
+// the row windows that keep what was not served out of the step.
 //
 // The counterpart of sv_commit_kv's release: entries [ctx / 16,
 // ceil((ctx + rows) / 16)) of a request's table that are -1 are new.  With
@@ -356,6 +357,28 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(Args a) {
   }
 }
 
+// sv_slot_windows: a warp for each request looks at its rows' slots (four a
+// lane at most, all in flight).
+constexpr int kWindowWarps = 8;
+__global__ void __launch_bounds__(32 * kWindowWarps) slot_windows_kernel(sv_batch bt,
+                                                                         const int32_t* slots,
+                                                                         long n_slots,
+                                                                         int32_t* row_end) {
+  griddep_entry();
+  const int i = blockIdx.x * kWindowWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (i >= bt.n_req) return;
+  bt.row_begin = bt.row_end = nullptr;
+  const Window w = window_of(bt, i);
+  bool there = w.ok;
+  if (w.ok)
+    for (int j = lane; j < w.lim; j += 32) {
+      const int s = slots[w.cu + j];
+      there = there && s >= 0 && s < n_slots;
+    }
+  there = __all_sync(0xffffffffu, there);
+  if (lane == 0) row_end[i] = there ? w.lim : 0;
+}
+
 }  // namespace rsv
 }  // namespace sv
 
@@ -429,5 +452,23 @@ extern "C" sv_status sv_reserve_kv(const sv_paged_kv* kv, const sv_batch* bt,
     if (sv::launch(rsv::rows_kernel, grid, rsv::kRowThreads, 0, s, a) != cudaSuccess)
       return SV_ERR_CUDA;
   }
+  return SV_OK;
+}
+
+extern "C" sv_status sv_slot_windows(const sv_paged_kv* kv, const sv_batch* bt, const int32_t* slots,
+                                     int32_t* row_end, void* stream) {
+  SV_TRACE("sv_slot_windows");
+  if (!kv || !bt) return SV_ERR_INVALID_ARGUMENT;
+  if (bt->n_req < 0 || bt->total_rows < 0 || bt->max_rows_per_req < 1 || kv->num_blocks < 0)
+    return SV_ERR_INVALID_ARGUMENT;
+  if (kv->block_size != kBlockSize || bt->max_rows_per_req > kMaxRows)
+    return SV_ERR_UNSUPPORTED_SHAPE;
+  if (bt->n_req == 0) return SV_OK;
+  if (!bt->cu_rows || !row_end || (bt->total_rows > 0 && !slots)) return SV_ERR_INVALID_ARGUMENT;
+  const unsigned grid = ((unsigned)bt->n_req + rsv::kWindowWarps - 1) / rsv::kWindowWarps;
+  if (sv::launch(rsv::slot_windows_kernel, grid, 32 * rsv::kWindowWarps, 0,
+                 static_cast<cudaStream_t>(stream), *bt, slots, (long)kv->num_blocks * kBlockSize,
+                 row_end) != cudaSuccess)
+    return SV_ERR_CUDA;
   return SV_OK;
 }

@@ -11,8 +11,8 @@ outputs and workspaces with torch, and enqueues the library calls of a step:
             with the selected verify_len feeding the batch
 
 ``EdgeStep`` runs a one-pass step with its two edges, from projections and raw
-logits: sv_reserve_kv -> sv_stage_qkv -> sv_tree_attend -> sv_shape_logits ->
-sv_accept_commit.
+logits: sv_reserve_kv -> sv_slot_windows -> sv_stage_qkv -> sv_tree_attend ->
+sv_shape_logits -> sv_accept_commit.
 
 ``HostPipeline`` runs such steps on inputs that arrive in pinned host memory,
 double-buffered so that the next step's upload overlaps this step's kernels.
@@ -251,6 +251,10 @@ class EdgeStep(DeviceStep):
     and staged into blocks that the step takes from the pool itself; the
     workload's target and draft logits (fp32 or bf16) are shaped by ``rules``
     before they are tested.  Without rules the logits are tested as they are.
+
+    A request that gets no slots for its rows (the pool is short, its input is
+    malformed) takes no part in the rest of the step: ``row_end`` is 0 for it,
+    its cache, outputs and tokens stay as they were.
     """
 
     def __init__(self, w: Workload, q, k, v, rotary=None, rules=None, q_weight=None,
@@ -261,6 +265,8 @@ class EdgeStep(DeviceStep):
         n, rows = w.n_req, w.total_rows
         new = lambda m: torch.full((m,), -1, dtype=torch.int32, device=device)
         self.slots, self.positions, self.taken = new(rows), new(rows), new(n)
+        self.row_end = torch.zeros(n, dtype=torch.int32, device=device)
+        self.served = dataclasses.replace(self.batch, row_end=self.row_end)
         self.raw = (self.target, self.draft)
         if rules is not None:
             self.target = torch.empty_like(self.target)
@@ -270,6 +276,24 @@ class EdgeStep(DeviceStep):
         self._bound("reserve", self.batch, lambda: api.bind_reserve_kv(
             self.kv, self.batch, self.pool, self.slots, self.positions, self.taken,
             self.pos_offset, self.dev_status))()
+        self._bound("slot windows", self.batch, lambda: api.bind_slot_windows(
+            self.kv, self.batch, self.slots, self.row_end))()
+
+    def attend(self, batch=None):
+        super().attend(batch or self.served)
+
+    def accept(self, batch=None, row_stats=None):
+        super().accept(batch or self.served, row_stats)
+
+    def accept_commit(self, batch=None, row_stats=None):
+        super().accept_commit(batch or self.served, row_stats)
+
+    def commit(self, batch=None):
+        # sv_commit_kv takes no windows: a request that was kept out has no path
+        # (reported as SV_DEV_BAD_WINDOW, and left as it was)
+        path_len = self.accepted_len.masked_fill(self.row_end == 0, -1)
+        api.sv_commit_kv(self.kv, batch or self.batch, path_len, self.accepted_nodes, self.pool,
+                         self.dev_status)
 
     def stage(self):
         self._bound("stage", self.batch, lambda: api.bind_stage_qkv(
