@@ -546,7 +546,7 @@ sv_status sv_stage_qkv(const sv_paged_kv* kv, int32_t n_rows, const void* q, int
  * logits: SV_LOGITS_F32 or SV_LOGITS_BF16, row r at element r * logits_stride
  *   (a head's padded output will do); out may be the logits themselves (fp32,
  *   logits_stride == vocab), else the two must not overlap.
- * Every part may be left out (NULL):
+ * Every part may be left out (NULL; set the structure to zero first):
  *   history int32 [n_req][max_history], history_len, prompt_len (NULL: 0)
  *     [n_req]: read only with a penalty; tokens outside [0, vocab) are ignored;
  *   repetition (2^-126 .. 2^126; 1 = none; the division is a product with its
@@ -558,7 +558,10 @@ sv_status sv_stage_qkv(const sv_paged_kv* kv, int32_t n_rows, const void* q, int
  *     row's mask, -1 for none (NULL: mask r for row r).
  * A request with a parameter or range out of bounds (SV_DEV_BAD_PARAM,
  * BAD_LENGTH, BAD_WINDOW, BAD_PARENT) and rows outside the windows are left as
- * they were.  A mask row outside [0, n_masks) sets SV_DEV_BAD_PARAM, one that
+ * they were.  Such a request's logits are not to be tested: row_end (NULL: not
+ * asked for), int32 [n_req], is set to 0 for it and left alone for the others,
+ * so that what sv_slot_windows filled, or this batch's own row_end, keeps it
+ * out of sv_accept too.  A mask row outside [0, n_masks) sets SV_DEV_BAD_PARAM, one that
  * permits no token SV_DEV_EMPTY_MASK; such a mask is not applied.
  * No workspace; results do not depend on the order of anything. */
 #define SV_LOGITS_F32 0
@@ -579,6 +582,7 @@ typedef struct {
   int32_t mask_stride;       /* words per mask row, at least ceil(vocab / 32) */
   int32_t n_masks;
   const int32_t* mask_row;
+  int32_t* row_end;          /* out */
 } sv_logit_rules;
 sv_status sv_shape_logits(const sv_batch* batch, const void* logits, int32_t logits_type,
                           int64_t logits_stride, int32_t vocab, const sv_logit_rules* rules,

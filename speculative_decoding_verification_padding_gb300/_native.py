@@ -69,7 +69,7 @@ class SvLogitRules(ctypes.Structure):
     _fields_ = [("history", P), ("max_history", I32), ("history_len", P), ("prompt_len", P),
                 ("repetition", P), ("frequency", P), ("presence", P), ("bias_begin", P),
                 ("bias_token", P), ("bias_value", P), ("n_bias", I32), ("mask", P),
-                ("mask_stride", I32), ("n_masks", I32), ("mask_row", P)]
+                ("mask_stride", I32), ("n_masks", I32), ("mask_row", P), ("row_end", P)]
 
 
 # name -> (restype, argtypes), exactly the functions declared in the header

@@ -219,7 +219,8 @@ class LogitRules:
     mask: Optional[torch.Tensor] = None
     mask_row: Optional[torch.Tensor] = None
 
-    def c(self, n_req: int, total_rows: int) -> N.SvLogitRules:
+    def c(self, n_req: int, total_rows: int,
+          row_end: Optional[torch.Tensor] = None) -> N.SvLogitRules:
         for name in ("history", "history_len", "prompt_len", "bias_begin", "bias_token", "mask",
                      "mask_row"):
             _expect(getattr(self, name), torch.int32, name)
@@ -243,7 +244,7 @@ class LogitRules:
             _ptr(self.prompt_len), _ptr(self.repetition), _ptr(self.frequency),
             _ptr(self.presence), _ptr(self.bias_begin), _ptr(self.bias_token),
             _ptr(self.bias_value), n_bias, _ptr(mask), 0 if mask is None else mask.shape[1],
-            0 if mask is None else mask.shape[0], _ptr(self.mask_row))
+            0 if mask is None else mask.shape[0], _ptr(self.mask_row), _ptr(row_end))
 
 
 def workspace(nbytes: int, device=None) -> torch.Tensor:
@@ -686,9 +687,10 @@ def bind_stage_qkv(kv: PagedKV, q: torch.Tensor, k: torch.Tensor, v: torch.Tenso
 _LOGIT_TYPES = {torch.float32: N.SV_LOGITS_F32, torch.bfloat16: N.SV_LOGITS_BF16}
 
 
-def _shape_args(batch, logits, rules, out, dev_status):
+def _shape_args(batch, logits, rules, out, dev_status, row_end):
     _expect(out, torch.float32, "out")
     _expect(dev_status, torch.int32, "dev_status")
+    _expect(row_end, torch.int32, "row_end")
     if logits.dtype not in _LOGIT_TYPES:
         raise N.SpecVerifyError(f"logits must be float32 or bfloat16, got {logits.dtype}")
     n, rows = batch.n_req, batch.total_rows
@@ -696,26 +698,32 @@ def _shape_args(batch, logits, rules, out, dev_status):
         raise N.SpecVerifyError(f"logits and out must be [{rows}][vocab], got {list(logits.shape)} "
                                 f"and {list(out.shape)}")
     _at_least(batch.tokens, rows, "tokens")
+    _at_least(row_end, n, "row_end")
     for name in ("row_begin", "row_end", "verify_len"):
         _at_least(getattr(batch, name), n, name)
     dev = _one_device(batch.cu_rows, batch.parent, batch.tokens, batch.row_begin, batch.row_end,
-                      batch.verify_len, logits, out, dev_status, *vars(rules).values())
-    b, r = batch.c(), rules.c(n, rows)
+                      batch.verify_len, logits, out, dev_status, row_end, *vars(rules).values())
+    b, r = batch.c(), rules.c(n, rows, row_end)
     lp, stride = _rows_ptr(logits, "logits")
     return (ctypes.byref(b), lp, _LOGIT_TYPES[logits.dtype], stride, out.shape[1], ctypes.byref(r),
             _ptr(out), _ptr(dev_status)), dev
 
 
 def sv_shape_logits(batch: Batch, logits: torch.Tensor, rules: LogitRules, out: torch.Tensor,
-                    dev_status: Optional[torch.Tensor] = None, stream=None):
+                    dev_status: Optional[torch.Tensor] = None, stream=None,
+                    row_end: Optional[torch.Tensor] = None):
     """The logits [rows][vocab] (fp32 or bf16; rows may lie apart) under each
-    request's penalties, biases and masks, into out (fp32; may be logits)."""
-    args, _ = _shape_args(batch, logits, rules, out, dev_status)
+    request's penalties, biases and masks, into out (fp32; may be logits).
+    row_end [n_req] becomes 0 for a request whose rules are malformed, whose rows
+    are left as they were."""
+    args, _ = _shape_args(batch, logits, rules, out, dev_status, row_end)
     _call("sv_shape_logits", args, stream)
 
 
 def bind_shape_logits(batch: Batch, logits: torch.Tensor, rules: LogitRules, out: torch.Tensor,
-                      dev_status: Optional[torch.Tensor] = None) -> BoundCall:
+                      dev_status: Optional[torch.Tensor] = None,
+                      row_end: Optional[torch.Tensor] = None) -> BoundCall:
     """sv_shape_logits with its arguments marshalled once (see BoundCall)."""
-    args, dev = _shape_args(batch, logits, rules, out, dev_status)
-    return BoundCall("sv_shape_logits", args, dev, (batch, logits, rules, out, dev_status))
+    args, dev = _shape_args(batch, logits, rules, out, dev_status, row_end)
+    return BoundCall("sv_shape_logits", args, dev,
+                     (batch, logits, rules, out, dev_status, row_end))

@@ -236,8 +236,15 @@ __global__ void __launch_bounds__(kThreads, kQuads > kRowQuads ? kWideCtasPerSm 
     finding = SV_DEV_BAD_PARAM;
   else if (hlen < 0 || hlen > ru.max_history || plen < 0 || plen > hlen)
     finding = SV_DEV_BAD_LENGTH;
-  if (finding) {  // the request's rows are left as they were
-    if (tid == 0) flag(a.dev_status, finding);
+  // The request's rows are left as they were, and it is told apart from the
+  // others (every CTA of it comes to the same end).
+  auto refuse = [&](int why) {
+    if (tid != 0) return;
+    flag(a.dev_status, why);
+    if (ru.row_end) ru.row_end[i] = 0;
+  };
+  if (finding) {
+    refuse(finding);
     return;
   }
   const int j0 = w.b + chunk * a.chunk, j1 = min(w.e, j0 + a.chunk);  // this CTA's nodes
@@ -361,8 +368,8 @@ __global__ void __launch_bounds__(kThreads, kQuads > kRowQuads ? kWideCtasPerSm 
       if (lane == 0) sm.mine[wid] = m;
     }
   }
-  if (__syncthreads_or(bad)) {  // the request's rows are left as they were
-    if (tid == 0) flag(a.dev_status, SV_DEV_BAD_PARENT);
+  if (__syncthreads_or(bad)) {
+    refuse(SV_DEV_BAD_PARENT);
     return;
   }
   if (ru.mask) {

@@ -254,7 +254,8 @@ class EdgeStep(DeviceStep):
 
     A request that gets no slots for its rows (the pool is short, its input is
     malformed) takes no part in the rest of the step: ``row_end`` is 0 for it,
-    its cache, outputs and tokens stay as they were.
+    its cache, outputs and tokens stay as they were.  One whose rules are
+    malformed is attended, but neither decided nor committed.
     """
 
     def __init__(self, w: Workload, q, k, v, rotary=None, rules=None, q_weight=None,
@@ -305,7 +306,7 @@ class EdgeStep(DeviceStep):
                                ("shape draft", self.raw[1], self.draft)):
             if raw is not None and self.rules is not None:
                 self._bound(name, self.batch, lambda: api.bind_shape_logits(
-                    self.batch, raw, self.rules, out, self.dev_status))()
+                    self.batch, raw, self.rules, out, self.dev_status, self.row_end))()
 
     def run(self, commit: bool = True, restore: bool = True):
         if restore:
