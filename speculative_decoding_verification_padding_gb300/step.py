@@ -248,9 +248,10 @@ def unstaged(w: Workload) -> Workload:
 class EdgeStep(DeviceStep):
     """A one-pass step with its two edges.  ``q``, ``k``, ``v`` (bf16
     [rows][heads][dim], views of one projection output will do) are turned
-    and staged into blocks that the step takes from the pool itself; the
-    workload's target and draft logits (fp32 or bf16) are shaped by ``rules``
-    before they are tested.  Without rules the logits are tested as they are.
+    and staged into blocks that the step takes from the pool itself, at the
+    positions of the reservation (the same on every axis of ``rotary``); the
+    workload's target and draft logits (fp32) are shaped by ``rules`` before
+    they are tested.  Without rules the logits are tested as they are.
 
     A request that gets no slots for its rows (the pool is short, its input is
     malformed) takes no part in the rest of the step: ``row_end`` is 0 for it,
