@@ -321,6 +321,14 @@ class EdgeStep(DeviceStep):
         else:
             self.accept()
 
+    def inputs(self):
+        """The projections and raw logits in the place of the turned queries and
+        shaped logits: q, k, v, target logits, tokens, parents, row offsets, then
+        the draft logits (T > 0)."""
+        b, (target, draft) = self.batch, self.raw
+        t = [*self.qkv, target, b.tokens, b.parent, b.cu_rows]
+        return t if draft is None else t + [draft]
+
     def _twin(self):
         raise NotImplementedError("an EdgeStep's inputs are its projections and raw logits")
 
