@@ -236,15 +236,19 @@ class LogitRules:
         if mask is not None and mask.dim() != 2:
             raise N.SpecVerifyError(f"mask must be [n_masks][words], got {tuple(mask.shape)}")
         n_bias = 0
+        token, value = _ptr(self.bias_token), _ptr(self.bias_value)
         if self.bias_begin is not None and self.bias_token is not None:
             n_bias = self.bias_token.numel()
             _at_least(self.bias_value, n_bias, "bias_value")
+            if n_bias == 0 and self.bias_value is not None:
+                # an empty list has no address; none of it is read
+                token = value = _ptr(self.bias_begin)
         return N.SvLogitRules(
             _ptr(hist), 0 if hist is None else hist.shape[1], _ptr(self.history_len),
             _ptr(self.prompt_len), _ptr(self.repetition), _ptr(self.frequency),
-            _ptr(self.presence), _ptr(self.bias_begin), _ptr(self.bias_token),
-            _ptr(self.bias_value), n_bias, _ptr(mask), 0 if mask is None else mask.shape[1],
-            0 if mask is None else mask.shape[0], _ptr(self.mask_row), _ptr(row_end))
+            _ptr(self.presence), _ptr(self.bias_begin), token, value, n_bias, _ptr(mask),
+            0 if mask is None else mask.shape[1], 0 if mask is None else mask.shape[0],
+            _ptr(self.mask_row), _ptr(row_end))
 
 
 def workspace(nbytes: int, device=None) -> torch.Tensor:
