@@ -235,6 +235,11 @@ class LogitRules:
             raise N.SpecVerifyError(f"history must be [{n_req}][max_history], got {tuple(hist.shape)}")
         if mask is not None and mask.dim() != 2:
             raise N.SpecVerifyError(f"mask must be [n_masks][words], got {tuple(mask.shape)}")
+        if mask is not None and self.mask_row is None and mask.shape[0] < total_rows:
+            raise N.SpecVerifyError(f"mask has {mask.shape[0]} rows for {total_rows} rows without mask_row")
+        masks = _ptr(mask)
+        if mask is not None and mask.shape[0] == 0 and self.mask_row is not None:
+            masks = _ptr(self.mask_row)  # no address of its own; none of it is read
         n_bias = 0
         token, value = _ptr(self.bias_token), _ptr(self.bias_value)
         if self.bias_begin is not None and self.bias_token is not None:
@@ -246,7 +251,7 @@ class LogitRules:
         return N.SvLogitRules(
             _ptr(hist), 0 if hist is None else hist.shape[1], _ptr(self.history_len),
             _ptr(self.prompt_len), _ptr(self.repetition), _ptr(self.frequency),
-            _ptr(self.presence), _ptr(self.bias_begin), token, value, n_bias, _ptr(mask),
+            _ptr(self.presence), _ptr(self.bias_begin), token, value, n_bias, masks,
             0 if mask is None else mask.shape[1], 0 if mask is None else mask.shape[0],
             _ptr(self.mask_row), _ptr(row_end))
 

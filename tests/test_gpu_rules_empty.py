@@ -38,3 +38,15 @@ def test_offsets_into_an_empty_list_are_refused():
     assert torch.equal(out[:2], x[:2]) and (out[2] == 7).all()
     with pytest.raises(api.N.SpecVerifyError):  # a list without values
         api.sv_shape_logits(b, x, api.LogitRules(bias_begin=dev([0, 0, 0]), bias_token=none.int()), out, status)
+
+
+def test_rows_that_name_a_mask_there_is_not():
+    # no masks in this step: rows that want one are reported, the others pass
+    dev, b, x = _batch()
+    masks = torch.empty(0, 2, dtype=torch.int32, device="cuda")
+    for rows, want in (([-1, -1, -1], 0), ([-1, 0, -1], api.N.SV_DEV_BAD_PARAM)):
+        out, status = torch.full_like(x, 7), dev([0])
+        api.sv_shape_logits(b, x, api.LogitRules(mask=masks, mask_row=dev(rows)), out, status)
+        assert status.item() == want and torch.equal(out, x)
+    with pytest.raises(api.N.SpecVerifyError):  # a mask for every row, but there are none
+        api.sv_shape_logits(b, x, api.LogitRules(mask=masks), out, status)
