@@ -293,17 +293,22 @@ __device__ __forceinline__ void two_sum(float a, float b, float& s, float& e) {
 // the smallest denormal) gives ratio 1, as the definition's q > 0 test does,
 // unless p vanishes with it: such a token is barred on both sides.
 // p and q themselves (row statistics output) are formed in fp32.
+__device__ __forceinline__ bool vanishes(float x_minus_m, float l) {
+  return x_minus_m - logf(l) < -745.13f;
+}
+// Both vanish.
+__device__ __forceinline__ bool barred(float xp, float xq, float mp, float lp, float mq, float lq) {
+  return vanishes(__fsub_rn(xq, mq), lq) && vanishes(__fsub_rn(xp, mp), lp);
+}
+constexpr float kBarred = -1.f;  // a chain's ratio then
 // p / q itself (unclamped), by the same exact exponent: +inf stands for a q
-// that vanishes in double, 0 for p = 0, kBarred for both.
-constexpr float kBarred = -1.f;
-constexpr float kVanishes = -745.13f;  // exp of anything below is 0 in double
+// that vanishes in double, 0 for p = 0.
 __device__ __forceinline__ float pq_ratio(float xp, float xq, float mp, float lp, float mq,
                                           float lq) {
   float s1, e1, s2, e2, h, l;
   two_sum(xq, -mq, s2, e2);
+  if (vanishes(s2, lq)) return INFINITY;  // also xq = -inf
   two_sum(xp, -mp, s1, e1);
-  if (s2 - logf(lq) < kVanishes)  // also xq = -inf
-    return s1 - logf(lp) < kVanishes ? kBarred : INFINITY;
   if (s1 == -INFINITY) return 0.f;                // p = 0
   two_sum(s1, -s2, h, l);
   l = __fadd_rn(l, __fsub_rn(e1, e2));
@@ -315,6 +320,7 @@ __device__ __forceinline__ float accept_ratio(float xp, float xq, float mp, floa
     *p_out = __fdiv_rn(expf(__fsub_rn(xp, mp)), lp);
     *q_out = __fdiv_rn(expf(__fsub_rn(xq, mq)), lq);
   }
+  if (barred(xp, xq, mp, lp, mq, lq)) return kBarred;
   return fminf(1.f, pq_ratio(xp, xq, mp, lp, mq, lq));
 }
 
@@ -631,7 +637,6 @@ __device__ int decide_request(const Args& a, int nch, int i, DecideSmem& sm, Com
 }
 
 // ----------------------------------------------------------------- stats --
-constexpr float kMaxInLog2 = 0x1.6p127f;  // times log2 e it is below 2^128
 // Warp-granular: every warp owns one slice of one row at a time and reduces
 // it with shuffles into one partial (no warp waits for another); the
 // decision kernel merges the partials.
@@ -744,20 +749,13 @@ __global__ void __launch_bounds__(kStatThreads, 4) stats_kernel(Args a) {
             l *= ex2((m - mx) * kLog2e);
             m = mx;
           }
-          if (fabsf(m) < kMaxInLog2) {
-            const float mb = m * kLog2e;
+          // (a lane that has met nothing but barred entries, at -inf or the lowest
+          // values, adds 0 for them: no product past the range, no inf - inf)
+          const float mb = fmaxf(m * kLog2e, -3.402823466e38f);
 #pragma unroll
-            for (int k = 0; k < kDepth; ++k)
-              l += (ex2(fmaf(x[k].x, kLog2e, -mb)) + ex2(fmaf(x[k].y, kLog2e, -mb))) +
-                   (ex2(fmaf(x[k].z, kLog2e, -mb)) + ex2(fmaf(x[k].w, kLog2e, -mb)));
-          } else if (m != -INFINITY) {
-            // nothing but masks of the type's lowest value so far: m log2 e is
-            // past the range (nothing but -inf adds nothing)
-#pragma unroll
-            for (int k = 0; k < kDepth; ++k)
-              l += (ex2((x[k].x - m) * kLog2e) + ex2((x[k].y - m) * kLog2e)) +
-                   (ex2((x[k].z - m) * kLog2e) + ex2((x[k].w - m) * kLog2e));
-          }
+          for (int k = 0; k < kDepth; ++k)
+            l += (ex2(fmaf(x[k].x, kLog2e, -mb)) + ex2(fmaf(x[k].y, kLog2e, -mb))) +
+                 (ex2(fmaf(x[k].z, kLog2e, -mb)) + ex2(fmaf(x[k].w, kLog2e, -mb)));
         }
       } else {
         for (int v = lo + lane; v < hi; v += 32) {
@@ -1206,6 +1204,16 @@ __global__ void __launch_bounds__(NT) tree_kernel(Args a) {
     }
   }
   __syncthreads();
+  if (warp == 0) {
+    // A node barred on both sides is not a draw from q: it is nobody's child
+    // (only this warp reads the parents; passing over it in the walk itself cost
+    // a tree's call 1 us)
+    for (int r = lane + 1; r < rows; r += 32) {
+      const int p = s_par[r];
+      if (barred(s_xp[r] / T, s_xq[r] / T, s_mp[p], s_lp[p], s_mq[p], s_lq[p])) s_par[r] = -1;
+    }
+    __syncwarp();
+  }
   for (int step = 0; step < kMaxRows; ++step) {  // every move goes to a larger node
     if (warp == 0) {
       // children of n in index order, and the node's statistics
@@ -1244,23 +1252,17 @@ __global__ void __launch_bounds__(NT) tree_kernel(Args a) {
         // from the exact exponent in fp32 (as on chains; fp64 runs at a
         // small fraction of the fp32 rate on this GPU) and 1 / S taken once
         // per pass.  q that vanishes gives ratio 1, as the definition's
-        // q > 0 test does; p = 0 gives 0.  A sibling barred on both sides is
-        // not a draw from q: it is passed over, p' stays as it is.
+        // q > 0 test does; p = 0 gives 0.
         const float r_pq = pq_ratio(s_xp[ch] / T, s_xq[ch] / T, s_st[0], s_st[1], s_st[2], s_st[3]);
-        if (r_pq == kBarred) {
-          s_dec = 2;
-        } else {
-          const double ratio =
-              r_pq == INFINITY ? 1.0 : fmin(1.0, fmax(0.0, (double)r_pq - c) * inv_S);
-          const double u = (double)accept_u(a.seed, i, ch);
-          if (fabs(u - ratio) < 1e-6) amb = true;
-          s_dec = u < ratio ? 1 : 0;
-        }
+        const double ratio =
+            r_pq == INFINITY ? 1.0 : fmin(1.0, fmax(0.0, (double)r_pq - c) * inv_S);
+        const double u = (double)accept_u(a.seed, i, ch);
+        if (fabs(u - ratio) < 1e-6) amb = true;
+        s_dec = u < ratio ? 1 : 0;
       }
       __syncthreads();
       const int dec = s_dec;
       __syncthreads();  // s_dec is rewritten by the next test
-      if (dec == 2) continue;
       if (dec) {
         if (tid == 0 && rank == 0) nodes[k + 1] = ch;
         ++k;

@@ -145,13 +145,14 @@ __device__ __forceinline__ float pick_u(uint64_t seed, int i, int pos, int g) {
 // "Computation of elementary functions on the IBM RISC System/6000
 // processor" (IBM J. Res. Dev. 34(1), 1990).  Equal to the correctly rounded
 // quotient except in rare cases where it is one ulp away; used only where the
-// result feeds a normaliser, never a decision.  An infinite product (of a
-// masked logit, or of one so low that its quotient is below the range) has no
-// residual and stays as it is: correcting it would give inf - inf.
+// result feeds a normaliser, never a decision.  A product of -inf (of a masked
+// logit, or of one so low that its quotient is below the range) has a residual
+// of NaN or +inf: the minimum makes that a number, which leaves the -inf as it
+// is; any other residual is below it.
 __device__ __forceinline__ float div_by(float x, float d, float r) {
   const float q = x * r;
-  const float e = fmaf(-q, d, x);
-  return fabsf(q) < INFINITY ? fmaf(e, r, q) : q;
+  const float e = fminf(fmaf(-q, d, x), 3.402823466e38f);
+  return fmaf(e, r, q);
 }
 
 // 2^x by the hardware approximation (relative error below 2^-22; results
