@@ -145,3 +145,43 @@ def test_masks_that_permit_a_few_tokens(case, T, low):
     kw = dict(CASES.get(case, dict(name="chain8b", vocab=128256, draft_sigma=0.3)))
     w = _grammar(wl.make_workload(wl.config(kw.pop("name")), ctx_scale=0.01, temperature=T, **kw), 6, low)
     _no_barred_token(w, *_check(w, T))
+
+
+@pytest.mark.parametrize("share", [0.3, 1.0])
+@pytest.mark.parametrize("T", [0.7, 1.0])
+def test_barred_drafts_in_a_chunked_step(T, share):
+    w = wl.make_workload(wl.config("batch64"), n_req=24, ctx_scale=0.01, vocab=2048, temperature=T, draft_sigma=0.3)
+    w = _bar_drafts(w, 7, share)
+    s = DeviceStep(w, mode="chunked", chunk=2)
+    s.run()
+    res = s.results()
+    assert res["dev_status"] == 0
+    err, st = oracle.verify_chunked(w.batch(), w.kv(), w.q, w.cfg.n_q_heads, w.softmax_scale, w.target_logits,
+                                    w.draft_logits, T, w.seed, chunk=2)[:2]
+    assert err == 0
+    sure = (st.ambiguous == 0) & (res["ambiguous"] == 0)
+    assert sure.sum() >= len(sure) - 1
+    for k in ("accepted_len", "next_token"):
+        assert np.array_equal(res[k][sure], getattr(st, k)[sure]), k
+    _no_barred_token(w, res, sure)
+    assert np.array_equal(s.kv.cache_lens.cpu().numpy(), w.cache_lens + 1 + res["accepted_len"])
+
+
+def test_barred_drafts_under_a_budget():
+    # verified prefixes only: a barred draft behind the prefix is never looked at
+    w = wl.make_workload(wl.config("batch64"), n_req=24, ctx_scale=0.01, vocab=2048, temperature=0.7, draft_sigma=0.3)
+    w = _bar_drafts(w, 9, 0.5)
+    rng = np.random.default_rng(1)
+    keep = np.array([rng.integers(0, n) for n in np.diff(w.cu_rows)], np.int32)
+    s = DeviceStep(w, mode="onepass")
+    b = api.Batch(s.batch.cu_rows, s.batch.parent, s.batch.tokens, s.batch.max_rows,
+                  verify_len=torch.from_numpy(keep).cuda())
+    s.accept(b)
+    res = s.results()
+    err, st = oracle.accept(dict(w.batch(), verify_len=keep), w.target_logits, w.draft_logits, 0.7, w.seed)
+    assert err == 0 and res["dev_status"] == 0
+    sure = (st.ambiguous == 0) & (res["ambiguous"] == 0)
+    assert sure.sum() >= len(sure) - 1
+    for k in ("accepted_len", "next_token"):
+        assert np.array_equal(res[k][sure], getattr(st, k)[sure]), k
+    _no_barred_token(w, res, sure)
