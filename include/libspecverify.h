@@ -253,7 +253,7 @@ sv_status sv_accept(const sv_batch* batch, const float* target_logits, const flo
  * moves its K/V and sets its new length, and the last request to finish
  * appends every released block to the pool: no separate commit launches,
  * no second read of accepted_len / accepted_nodes.  One-pass calls only
- * (windows covering whole requests, as for sv_commit_kv).
+ * (windows covering whole requests; one with an empty window is left as it was).
  * ws: at least sv_accept_commit_workspace() bytes, 256-byte aligned. */
 size_t sv_accept_commit_workspace(const sv_batch* batch, int32_t vocab);
 sv_status sv_accept_commit(const sv_batch* batch, const float* target_logits,

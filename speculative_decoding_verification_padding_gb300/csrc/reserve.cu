@@ -358,7 +358,8 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(Args a) {
 }
 
 // sv_slot_windows: a warp for each request looks at its rows' slots (four a
-// lane at most, all in flight).
+// lane at most).  Launch and two dependent loads: 1.2 us for one request of six
+// rows, 1.3 for 256 of five, 1.8 for 8192 of five, in a graph of such calls.
 constexpr int kWindowWarps = 8;
 __global__ void __launch_bounds__(32 * kWindowWarps) slot_windows_kernel(sv_batch bt,
                                                                          const int32_t* slots,

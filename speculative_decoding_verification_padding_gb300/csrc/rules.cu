@@ -27,14 +27,14 @@
 // slices that hold one.
 //
 // Measured (1280 rows of 151936, histories of 3450 tokens on average, 300
-// biases, masks; floor 232 us at the copy rate): 269 us, 230 us without rules;
+// biases, masks; floor 232 us at the copy rate): 270 us, 230 us without rules;
 // 256 single rows of 128256 with 7750 tokens of history 78 us (floor 39).
 // The same work with rules applied to touched entries alone under branches:
 // 341; touched entries written over the copied rows: 439; rows passing through
 // a shared-memory ring of bulk copies: 437 to 528, with warps specialised: 416;
 // the history counted by eight CTAs through distributed shared memory: 360
 // (the slice of the most frequent tokens takes 42 % of the remote updates).
-// 783 rows of 50257 in bf16 under masks that permit 48 tokens: 58.6 us; barred
+// 783 rows of 50257 in bf16 under masks that permit 48 tokens: 58.9 us; barred
 // entries written before the rules are prepared: 68.2; vectors that begin on
 // 128 instead of 16 bytes of the output: 63.5.
 

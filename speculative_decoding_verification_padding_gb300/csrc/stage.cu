@@ -31,7 +31,7 @@
 // pieces per lane ahead of the kVecs it works on, over the end of the row; the
 // next row's sines are computed under its last loads.  Few: a CTA for each, all
 // its loads at once.
-// 20000 rows of 80 heads of 128: 132 us, 6.20 TB/s, 0.91 of the measured copy
+// 20000 rows of 80 heads of 128: 134 us, 6.12 TB/s, 0.90 of the measured copy
 // rate; six rows of 48 heads: 2.8 us.
 
 #include <limits.h>
