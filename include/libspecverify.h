@@ -478,7 +478,9 @@ sv_status sv_reserve_kv(const sv_paged_kv* kv, const sv_batch* batch, const sv_b
  * sv_tree_attend, sv_accept and sv_accept_commit: its cache length, blocks and
  * outputs stay as they were, and the step can be tried again.  (Without it the
  * request would be decided and committed over slots that were never written.
- * sv_commit_kv takes no windows: there its accepted_len has to be -1.)
+ * sv_commit_kv takes no windows: there its accepted_len has to be -1.
+ * sv_verify_chunked and sv_verify_chunked_commit use their own: there row_end -
+ * 1 as the batch's verify_len does it.  Both report it as SV_DEV_BAD_WINDOW.)
  * A request whose offsets or verify_len are malformed gets 0 too.  The batch's
  * own row windows are ignored.  slots: int32 [total_rows], -1 = none.
  * Supported: block_size 16, max_rows_per_req <= 128. */

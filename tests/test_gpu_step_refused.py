@@ -9,7 +9,8 @@ import torch
 import oracle
 from oracle import edges
 from speculative_decoding_verification_padding_gb300 import api, build
-from speculative_decoding_verification_padding_gb300.step import EdgeStep
+from speculative_decoding_verification_padding_gb300 import workloads as wl
+from speculative_decoding_verification_padding_gb300.step import DeviceStep
 from test_gpu_step_edges import _arr, _check_step, _edge_step, _state
 
 pytestmark = pytest.mark.gpu
@@ -179,6 +180,29 @@ def test_a_captured_step_sees_the_pool_of_each_replay():
         assert (len(out) > 0) == (count == 0)
         _check_kept_out(s, out, before)
         _check_served(s, served, before)
+
+
+def test_a_chunked_step_leaves_out_what_has_no_slots():
+    w = wl.make_workload(wl.config("batch64"), n_req=12, ctx_scale=0.01, vocab=1024, temperature=0.7)
+    s = DeviceStep(w, mode="chunked", chunk=2)
+    slots = torch.zeros(w.total_rows, dtype=torch.int32, device="cuda")
+    out = [2, 9, 11]
+    for i in out:
+        slots[int(w.cu_rows[i + 1]) - 1] = -1
+    row_end = torch.zeros(12, dtype=torch.int32, device="cuda")
+    api.sv_slot_windows(s.kv, s.batch, slots, row_end)
+    b = api.Batch(s.batch.cu_rows, s.batch.parent, s.batch.tokens, s.batch.max_rows, verify_len=row_end - 1)
+    s.batch = b
+    _prime(s)
+    before = _before(s)
+    s.run(restore=False)
+    torch.cuda.synchronize()
+    assert s.dev_status.item() == edges.BAD_WINDOW
+    for i in out:
+        assert _arr(s.kv.cache_lens)[i] == before["cache_lens"][i]
+        assert np.array_equal(_arr(s.kv.block_tables)[i], before["block_tables"][i])
+        assert _arr(s.next_token)[i] == RESULTS.index("next_token") + 1
+    _check_served(s, np.setdiff1d(np.arange(12), out), before)
 
 
 # ------------------------------------------------- sv_slot_windows alone --
