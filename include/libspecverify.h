@@ -28,7 +28,12 @@
  *   sv_stage_qkv      head norms and rotation of the rows' Q and K, K and V
  *                     written into the cache pages sv_tree_attend reads;
  *   sv_shape_logits   penalties for repeated tokens, biases and grammar masks
- *                     on the logits sv_accept reads.
+ *                     on the logits sv_accept reads;
+ *   sv_bound_pages, sv_score_pages, sv_select_pages, sv_page_attend
+ *                     attention of each draft row over the pages of a long
+ *                     context that a cheap score selects for it;
+ *   sv_prefix_attend  sv_tree_attend for requests that share a prefix, its
+ *                     pages read once for all of them.
  *
  * Sources (pages by title; section names glossed):
  *   [SwiftSpec] "SwiftSpec: 드래프터와 타깃을 서로 다른 GPU에 분리하고 비동기로
@@ -589,6 +594,103 @@ typedef struct {
 sv_status sv_shape_logits(const sv_batch* batch, const void* logits, int32_t logits_type,
                           int64_t logits_stride, int32_t vocab, const sv_logit_rules* rules,
                           float* out, int32_t* dev_status, void* stream);
+
+/* ----------------------------------------------------------- page choice --
+ * For requests with long contexts: which pages of the cache a draft row
+ * attends.  Complete pages of request i: t = 0 .. n_i - 1, n_i = cache_lens[i]
+ * / 16 (rounded down).  Every row chooses for itself, for each KV head, as it
+ * would if it were decoded alone: what is verified stays the distribution that
+ * a decoder without drafts samples from under the same choice.
+ *
+ * sv_bound_pages: bounds[b][g][0][d] = the least, [1][d] the greatest of the 16
+ * keys of the page in block b, KV head g, for the complete pages t >=
+ * from_len[i] / 16 of requests 0 .. n_req - 1 (from_len NULL: all).  Called
+ * after a commit with the lengths before it, it keeps the bounds of a cache up
+ * to date; pages that several requests share may be bounded by each of them.
+ * bounds: bf16 [num_blocks][n_kv_heads][2][head_dim]; other entries are left as
+ * they were.  Exact; keys that are NaN count for nothing.  kv->v_cache is not read.  Lengths
+ * that are negative or do not fit the table: SV_DEV_BAD_LENGTH, the request is
+ * skipped; a block outside the cache: SV_DEV_BAD_BLOCK_ID, the page is skipped.
+ * Supported: n_req <= 8192, n_req * max_blocks_per_req below 2^31. */
+sv_status sv_bound_pages(const sv_paged_kv* kv, int32_t n_req, const int32_t* from_len,
+                         void* bounds, int32_t* dev_status, void* stream);
+
+/* For row r of request i inside its window, KV head g and t < n_i:
+ *   scores[r][g][t] = max over query heads h of g of
+ *                     sum_d max(q[r][h][d] lo_d, q[r][h][d] hi_d)
+ * with (lo, hi) the page's bounds: at least the product of any of those queries
+ * with any key of the page.  fp32 sums of exact products.
+ * scores: fp32 [total_rows][n_kv_heads][max_pages]; other entries are left as
+ * they were.  q: bf16 [total_rows][n_q_heads][head_dim], 16-byte aligned.
+ * Requests whose pages are more than max_pages, or whose length does not fit
+ * the table, set SV_DEV_BAD_LENGTH and are skipped, malformed windows
+ * SV_DEV_BAD_WINDOW; a page whose block is outside the cache sets
+ * SV_DEV_BAD_BLOCK_ID and scores 0.  batch->parent and tokens, kv->k_cache and v_cache are
+ * not read.  Supported: n_req * n_kv_heads <= 65535. */
+sv_status sv_score_pages(const sv_paged_kv* kv, const sv_batch* batch, const void* q,
+                         int32_t n_q_heads, const void* bounds, float* scores, int32_t max_pages,
+                         int32_t* dev_status, void* stream);
+
+/* pages[r][g][0 .. n_keep - 1], for rows inside their windows: the pages the
+ * row attends, ascending, then -1.  All n_i pages if n_i <= n_keep; else the
+ * first n_first, the last n_last and those of greatest score (the lower page on
+ * ties; NaN below everything, -0 = +0), n_keep in all.
+ * scores as sv_score_pages leaves them; pages: int32
+ * [total_rows][n_kv_heads][n_keep].  Findings as there.
+ * Supported: n_keep 1 .. 1024, n_first + n_last <= n_keep, max_pages <= 49152.
+ * Of kv only n_kv_heads, max_blocks_per_req and cache_lens are read. */
+sv_status sv_select_pages(const sv_paged_kv* kv, const sv_batch* batch, const float* scores,
+                          int32_t max_pages, int32_t n_first, int32_t n_last, int32_t n_keep,
+                          int32_t* pages, int32_t* dev_status, void* stream);
+
+/* sv_tree_attend over the selected pages only: row r and KV head g attend the
+ * slots of the complete pages listed in pages[r][g], the slots behind the last
+ * complete page (16 n_i .. ctx_i - 1) and the staged slots of r's ancestors and
+ * of r itself.  A list ends at its first -1 or after n_keep pages; it has to
+ * ascend and stay below n_i: at the first page that does not it ends too, with
+ * SV_DEV_BAD_PARAM.  Pages of a request that several rows list are read once
+ * for all rows of a tile.  K and V of every listed page and every staged row
+ * have to be finite.  Everything else as sv_tree_attend (rows outside the
+ * windows are not written; a block outside the cache sets SV_DEV_BAD_BLOCK_ID
+ * and its slots are left out).  With every page listed the result is
+ * sv_tree_attend's up to rounding.
+ * Supported: n_keep 0 .. 1024, max_blocks_per_req <= 262144, otherwise as
+ * sv_tree_attend.  ws: sv_page_attend_workspace() bytes, 256-byte aligned. */
+size_t sv_page_attend_workspace(const sv_batch* batch, const sv_paged_kv* kv, int32_t n_q_heads,
+                                int32_t n_keep);
+sv_status sv_page_attend(const sv_paged_kv* kv, const sv_batch* batch, const void* q,
+                         int32_t n_q_heads, float softmax_scale, const int32_t* pages,
+                         int32_t n_keep, void* out, void* ws, size_t ws_bytes,
+                         int32_t* dev_status, void* stream);
+
+/* --------------------------------------------------------- shared prefix --
+ * sv_tree_attend for a batch whose requests share prefixes (a system prompt, a
+ * document): the shared pages are read once for all rows of a group, on
+ * tcgen05 tensor cores, each request's own pages as sv_tree_attend reads them,
+ * and the two parts joined in fp32.  Same keys, same result up to rounding.
+ * Group k = requests cu_groups[k] .. cu_groups[k + 1] - 1 (int32 [n_groups +
+ * 1], from 0 to n_req), which share their first prefix_len[k] slots (int32
+ * [n_groups]; a multiple of 16, 0: nothing).  The blocks of the prefix are read
+ * from the table of the group's first request, whatever its window; the other
+ * requests' entries there are not read.  A group of one request may have a
+ * prefix too (its context by the tensor cores).
+ * A request shorter than its group's prefix sets SV_DEV_BAD_LENGTH, a malformed
+ * group SV_DEV_BAD_PARAM; such requests are skipped.  K and V of attended pages
+ * and staged rows have to be finite.
+ * Supported: 1 <= n_groups <= n_req, q 16-byte aligned, otherwise as
+ * sv_tree_attend.  ws: sv_prefix_attend_workspace() bytes, 256-byte aligned
+ * (the workspace does not depend on the contents of the groups). */
+typedef struct {
+  int32_t n_groups;
+  const int32_t* cu_groups;
+  const int32_t* prefix_len;
+} sv_shared_prefix;
+size_t sv_prefix_attend_workspace(const sv_batch* batch, const sv_paged_kv* kv,
+                                  const sv_shared_prefix* prefix, int32_t n_q_heads);
+sv_status sv_prefix_attend(const sv_paged_kv* kv, const sv_batch* batch,
+                           const sv_shared_prefix* prefix, const void* q, int32_t n_q_heads,
+                           float softmax_scale, void* out, void* ws, size_t ws_bytes,
+                           int32_t* dev_status, void* stream);
 
 /* ------------------------------------------------------------ self test --
  * Every wait inside the library's kernels (on an mbarrier a TMA copy or a

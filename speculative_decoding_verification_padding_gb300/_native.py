@@ -65,6 +65,10 @@ class SvRotary(ctypes.Structure):
                 ("freq_axis", P), ("scale", F32)]
 
 
+class SvSharedPrefix(ctypes.Structure):
+    _fields_ = [("n_groups", I32), ("cu_groups", P), ("prefix_len", P)]
+
+
 class SvLogitRules(ctypes.Structure):
     _fields_ = [("history", P), ("max_history", I32), ("history_len", P), ("prompt_len", P),
                 ("repetition", P), ("frequency", P), ("presence", P), ("bias_begin", P),
@@ -102,6 +106,13 @@ PROTOTYPES = {
     "sv_stage_qkv": (ctypes.c_int, [P, I32, P, I64, P, I64, P, I64, I32, P, P, I64, P, P, P, F32, P,
                                     P, P]),
     "sv_shape_logits": (ctypes.c_int, [P, P, I32, I64, I32, P, P, P, P]),
+    "sv_bound_pages": (ctypes.c_int, [P, I32, P, P, P, P]),
+    "sv_score_pages": (ctypes.c_int, [P, P, P, I32, P, P, I32, P, P]),
+    "sv_select_pages": (ctypes.c_int, [P, P, P, I32, I32, I32, I32, P, P, P]),
+    "sv_page_attend_workspace": (SZ, [P, P, I32, I32]),
+    "sv_page_attend": (ctypes.c_int, [P, P, P, I32, F32, P, I32, P, P, SZ, P, P]),
+    "sv_prefix_attend_workspace": (SZ, [P, P, P, I32]),
+    "sv_prefix_attend": (ctypes.c_int, [P, P, P, P, I32, F32, P, P, SZ, P, P]),
     "sv_selftest_bounded_wait": (ctypes.c_int, [I32, P, P]),
 }
 

@@ -256,6 +256,24 @@ class LogitRules:
             _ptr(self.mask_row), _ptr(row_end))
 
 
+@dataclass
+class SharedPrefix:
+    """sv_shared_prefix: requests cu_groups[k] .. cu_groups[k + 1] - 1 share their
+    first prefix_len[k] cache slots (int32 device tensors)."""
+    cu_groups: torch.Tensor
+    prefix_len: torch.Tensor
+
+    @property
+    def n_groups(self):
+        return self.cu_groups.shape[0] - 1
+
+    def c(self) -> N.SvSharedPrefix:
+        _expect(self.cu_groups, torch.int32, "cu_groups")
+        _expect(self.prefix_len, torch.int32, "prefix_len")
+        _at_least(self.prefix_len, self.n_groups, "prefix_len")
+        return N.SvSharedPrefix(self.n_groups, _ptr(self.cu_groups), _ptr(self.prefix_len))
+
+
 def workspace(nbytes: int, device=None) -> torch.Tensor:
     """A 256-byte aligned device buffer of at least nbytes (torch allocations are)."""
     return torch.empty(max(1, nbytes), dtype=torch.uint8, device=device or "cuda")
@@ -736,3 +754,214 @@ def bind_shape_logits(batch: Batch, logits: torch.Tensor, rules: LogitRules, out
     args, dev = _shape_args(batch, logits, rules, out, dev_status, row_end)
     return BoundCall("sv_shape_logits", args, dev,
                      (batch, logits, rules, out, dev_status, row_end))
+
+
+# --------------------------------------------- less of a long cache is read --
+
+def _cache_shape(kv, what):
+    if kv.v_cache.shape != kv.k_cache.shape:
+        raise N.SpecVerifyError(f"{what}: k_cache and v_cache differ in shape")
+    return kv.k_cache.shape
+
+
+def _batch_fits(kv, batch):
+    n = batch.n_req
+    _at_least(batch.tokens, batch.total_rows, "tokens")
+    for name in ("row_begin", "row_end", "verify_len"):
+        _at_least(getattr(batch, name), n, name)
+    _at_least(kv.cache_lens, n, "cache_lens")
+    if kv.block_tables.shape[0] < n:
+        raise N.SpecVerifyError(f"block_tables has {kv.block_tables.shape[0]} rows for {n} requests")
+
+
+def _batch_tensors(batch):
+    return (batch.cu_rows, batch.parent, batch.row_begin, batch.row_end, batch.verify_len)
+
+
+def _queries(kv, batch, q):
+    """The query heads of q, [rows][heads][dim] for the batch and the cache."""
+    _expect(q, torch.bfloat16, "q")
+    d = kv.k_cache.shape[3]
+    if q.dim() != 3 or q.shape[0] != batch.total_rows or q.shape[2] != d:
+        raise N.SpecVerifyError(f"q must be [{batch.total_rows}][heads][{d}], got {list(q.shape)}")
+    return q.shape[1]
+
+
+def _bound_args(kv, bounds, from_len, dev_status):
+    _expect(bounds, torch.bfloat16, "bounds")
+    _expect(from_len, torch.int32, "from_len")
+    _expect(dev_status, torch.int32, "dev_status")
+    nb, hkv, _, d = _cache_shape(kv, "sv_bound_pages")
+    if tuple(bounds.shape) != (nb, hkv, 2, d):
+        raise N.SpecVerifyError(f"bounds must be {[nb, hkv, 2, d]}, got {list(bounds.shape)}")
+    n = kv.cache_lens.shape[0]
+    _at_least(from_len, n, "from_len")
+    if kv.block_tables.shape[0] < n:
+        raise N.SpecVerifyError(f"block_tables has {kv.block_tables.shape[0]} rows for {n} requests")
+    dev = _one_device(kv.k_cache, kv.block_tables, kv.cache_lens, bounds, from_len, dev_status)
+    k = kv.c()
+    return (ctypes.byref(k), n, _ptr(from_len), _ptr(bounds), _ptr(dev_status)), dev
+
+
+def sv_bound_pages(kv: PagedKV, bounds: torch.Tensor, from_len: Optional[torch.Tensor] = None,
+                   dev_status: Optional[torch.Tensor] = None, stream=None):
+    """Least and greatest key of the complete pages behind from_len (None: all) of
+    every request of kv.cache_lens, into bounds [blocks][kv heads][2][dim]."""
+    args, _ = _bound_args(kv, bounds, from_len, dev_status)
+    _call("sv_bound_pages", args, stream)
+
+
+def bind_bound_pages(kv: PagedKV, bounds: torch.Tensor, from_len: Optional[torch.Tensor] = None,
+                     dev_status: Optional[torch.Tensor] = None) -> BoundCall:
+    """sv_bound_pages with its arguments marshalled once (see BoundCall)."""
+    args, dev = _bound_args(kv, bounds, from_len, dev_status)
+    return BoundCall("sv_bound_pages", args, dev, (kv, bounds, from_len, dev_status))
+
+
+def _scores(kv, batch, scores):
+    _expect(scores, torch.float32, "scores")
+    want = (batch.total_rows, kv.k_cache.shape[1])
+    if scores.dim() != 3 or tuple(scores.shape[:2]) != want:
+        raise N.SpecVerifyError(f"scores must be [{want[0]}][{want[1]}][pages], got {list(scores.shape)}")
+    return scores.shape[2]
+
+
+def _score_args(kv, batch, q, bounds, scores, dev_status):
+    heads = _queries(kv, batch, q)
+    _expect(bounds, torch.bfloat16, "bounds")
+    _expect(dev_status, torch.int32, "dev_status")
+    nb, hkv, _, d = _cache_shape(kv, "sv_score_pages")
+    if tuple(bounds.shape) != (nb, hkv, 2, d):
+        raise N.SpecVerifyError(f"bounds must be {[nb, hkv, 2, d]}, got {list(bounds.shape)}")
+    max_pages = _scores(kv, batch, scores)
+    _batch_fits(kv, batch)
+    dev = _one_device(*_batch_tensors(batch), q, bounds, scores, kv.block_tables, kv.cache_lens,
+                      dev_status)
+    b, k = batch.c(), kv.c()
+    return (ctypes.byref(k), ctypes.byref(b), _ptr(q), heads, _ptr(bounds), _ptr(scores), max_pages,
+            _ptr(dev_status)), dev
+
+
+def sv_score_pages(kv: PagedKV, batch: Batch, q: torch.Tensor, bounds: torch.Tensor,
+                   scores: torch.Tensor, dev_status: Optional[torch.Tensor] = None, stream=None):
+    """An upper bound of the products of each row's queries with the keys of each
+    complete page, into scores [rows][kv heads][pages]."""
+    args, _ = _score_args(kv, batch, q, bounds, scores, dev_status)
+    _call("sv_score_pages", args, stream)
+
+
+def bind_score_pages(kv: PagedKV, batch: Batch, q: torch.Tensor, bounds: torch.Tensor,
+                     scores: torch.Tensor, dev_status: Optional[torch.Tensor] = None) -> BoundCall:
+    """sv_score_pages with its arguments marshalled once (see BoundCall)."""
+    args, dev = _score_args(kv, batch, q, bounds, scores, dev_status)
+    return BoundCall("sv_score_pages", args, dev, (kv, batch, q, bounds, scores, dev_status))
+
+
+def _pages(kv, batch, pages):
+    _expect(pages, torch.int32, "pages")
+    want = (batch.total_rows, kv.k_cache.shape[1])
+    if pages.dim() != 3 or tuple(pages.shape[:2]) != want:
+        raise N.SpecVerifyError(f"pages must be [{want[0]}][{want[1]}][n_keep], got {list(pages.shape)}")
+    return pages.shape[2]
+
+
+def _select_args(kv, batch, scores, pages, n_first, n_last, dev_status):
+    _expect(dev_status, torch.int32, "dev_status")
+    max_pages, n_keep = _scores(kv, batch, scores), _pages(kv, batch, pages)
+    _batch_fits(kv, batch)
+    dev = _one_device(*_batch_tensors(batch), scores, pages, kv.cache_lens, dev_status)
+    b, k = batch.c(), kv.c()
+    return (ctypes.byref(k), ctypes.byref(b), _ptr(scores), max_pages, int(n_first), int(n_last),
+            n_keep, _ptr(pages), _ptr(dev_status)), dev
+
+
+def sv_select_pages(kv: PagedKV, batch: Batch, scores: torch.Tensor, pages: torch.Tensor,
+                    n_first: int = 1, n_last: int = 4, dev_status: Optional[torch.Tensor] = None,
+                    stream=None):
+    """The pages each row attends, ascending, into pages [rows][kv heads][n_keep]:
+    the first n_first, the last n_last and those of greatest score."""
+    args, _ = _select_args(kv, batch, scores, pages, n_first, n_last, dev_status)
+    _call("sv_select_pages", args, stream)
+
+
+def bind_select_pages(kv: PagedKV, batch: Batch, scores: torch.Tensor, pages: torch.Tensor,
+                      n_first: int = 1, n_last: int = 4,
+                      dev_status: Optional[torch.Tensor] = None) -> BoundCall:
+    """sv_select_pages with its arguments marshalled once (see BoundCall)."""
+    args, dev = _select_args(kv, batch, scores, pages, n_first, n_last, dev_status)
+    return BoundCall("sv_select_pages", args, dev, (kv, batch, scores, pages, dev_status))
+
+
+def sv_page_attend_workspace(batch: Batch, kv: PagedKV, n_q_heads: int, n_keep: int) -> int:
+    b, k = batch.c(), kv.c()
+    return N.lib().sv_page_attend_workspace(ctypes.byref(b), ctypes.byref(k), n_q_heads, n_keep)
+
+
+def _attended(kv, batch, q, out, ws, dev_status, *others):
+    """Query heads, batch and cache structs and device of an attention call."""
+    heads = _queries(kv, batch, q)
+    _expect(out, torch.bfloat16, "out")
+    _expect(dev_status, torch.int32, "dev_status")
+    if out.shape != q.shape:
+        raise N.SpecVerifyError(f"out must be {list(q.shape)}, got {list(out.shape)}")
+    _cache_shape(kv, "attention")
+    _batch_fits(kv, batch)
+    dev = _one_device(*_batch_tensors(batch), q, out, ws, kv.k_cache, kv.v_cache, kv.block_tables,
+                      kv.cache_lens, dev_status, *others)
+    return heads, batch.c(), kv.c(), dev
+
+
+def _page_attend_args(kv, batch, q, softmax_scale, pages, out, ws, dev_status):
+    n_keep = _pages(kv, batch, pages)
+    heads, b, k, dev = _attended(kv, batch, q, out, ws, dev_status, pages)
+    return (ctypes.byref(k), ctypes.byref(b), _ptr(q), heads, float(softmax_scale), _ptr(pages),
+            n_keep, _ptr(out), _ptr(ws), ws.numel() * ws.element_size(), _ptr(dev_status)), dev
+
+
+def sv_page_attend(kv: PagedKV, batch: Batch, q: torch.Tensor, softmax_scale: float,
+                   pages: torch.Tensor, out: torch.Tensor, ws: torch.Tensor,
+                   dev_status: Optional[torch.Tensor] = None, stream=None):
+    """sv_tree_attend over the pages that sv_select_pages chose for each row and KV
+    head, the slots behind the last complete page and the staged ancestors."""
+    args, _ = _page_attend_args(kv, batch, q, softmax_scale, pages, out, ws, dev_status)
+    _call("sv_page_attend", args, stream)
+
+
+def bind_page_attend(kv: PagedKV, batch: Batch, q: torch.Tensor, softmax_scale: float,
+                     pages: torch.Tensor, out: torch.Tensor, ws: torch.Tensor,
+                     dev_status: Optional[torch.Tensor] = None) -> BoundCall:
+    """sv_page_attend with its arguments marshalled once (see BoundCall)."""
+    args, dev = _page_attend_args(kv, batch, q, softmax_scale, pages, out, ws, dev_status)
+    return BoundCall("sv_page_attend", args, dev, (kv, batch, q, pages, out, ws, dev_status))
+
+
+def sv_prefix_attend_workspace(batch: Batch, kv: PagedKV, shared: SharedPrefix,
+                               n_q_heads: int) -> int:
+    b, k, s = batch.c(), kv.c(), shared.c()
+    return N.lib().sv_prefix_attend_workspace(ctypes.byref(b), ctypes.byref(k), ctypes.byref(s),
+                                              n_q_heads)
+
+
+def _prefix_attend_args(kv, batch, shared, q, softmax_scale, out, ws, dev_status):
+    s = shared.c()
+    heads, b, k, dev = _attended(kv, batch, q, out, ws, dev_status, shared.cu_groups,
+                                 shared.prefix_len)
+    return (ctypes.byref(k), ctypes.byref(b), ctypes.byref(s), _ptr(q), heads, float(softmax_scale),
+            _ptr(out), _ptr(ws), ws.numel() * ws.element_size(), _ptr(dev_status)), dev
+
+
+def sv_prefix_attend(kv: PagedKV, batch: Batch, shared: SharedPrefix, q: torch.Tensor,
+                     softmax_scale: float, out: torch.Tensor, ws: torch.Tensor,
+                     dev_status: Optional[torch.Tensor] = None, stream=None):
+    """sv_tree_attend for requests that share prefixes, whose pages are read once
+    for all rows of a group, from the table of its first request."""
+    args, _ = _prefix_attend_args(kv, batch, shared, q, softmax_scale, out, ws, dev_status)
+    _call("sv_prefix_attend", args, stream)
+
+
+def bind_prefix_attend(kv: PagedKV, batch: Batch, shared: SharedPrefix, q: torch.Tensor,
+                       softmax_scale: float, out: torch.Tensor, ws: torch.Tensor,
+                       dev_status: Optional[torch.Tensor] = None) -> BoundCall:
+    """sv_prefix_attend with its arguments marshalled once (see BoundCall)."""
+    args, dev = _prefix_attend_args(kv, batch, shared, q, softmax_scale, out, ws, dev_status)
+    return BoundCall("sv_prefix_attend", args, dev, (kv, batch, shared, q, out, ws, dev_status))

@@ -1,0 +1,597 @@
+// prefix.cu — sv_prefix_attend: verification attention of a batch whose requests
+// share a prefix, the prefix's pages read once for all rows of a group.
+//
+// Sources: [SwiftSpec] mechanism 3 (one padding-free call for all draft rows),
+// [SSD] section details (PagedAttention: requests that share a prompt share its
+// pages); computing the shared part once is on none of the pages.
+//
+// softmax over (prefix, own keys) = the two parts' (max, sum, weighted values)
+// joined.  Launches:
+//   plan    (1 CTA) checks groups and requests, lists the active rows of every
+//           group, cuts them into prefix units and the requests' rows into tiles;
+//   prefix  (tcgen05) units of 256 virtual rows (rows of all requests of the
+//           group x GQA group) by a part of the prefix's pages: (max, sum, O);
+//   units, merge (sv_page_units.cuh) over each request's own pages.
+
+#include "sv_page_units.cuh"
+#include "sv_tcgen05.cuh"
+
+namespace sv {
+namespace pu {
+
+constexpr int kUnitPages = 1024;   // pages of a prefix unit at most (block ids in shared memory)
+constexpr int kStagePages = 8;     // pages of a prefix stage (128 tokens)
+
+__global__ void __launch_bounds__(1024) prefix_plan_kernel(const __grid_constant__ Args a, int nsm) {
+  griddep_entry();
+  __shared__ int s_warp[32], s_tiles, s_stages, s_rows, s_units, s_pages, s_np, s_groups_bad;
+  const int R = a.bt.n_req, G = a.n_groups, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) {
+    s_tiles = s_stages = s_rows = s_units = s_pages = 0;
+    if (a.bt.cu_rows[0] != 0 || a.bt.cu_rows[R] != a.bt.total_rows) flag(a.dev_status, SV_DEV_BAD_WINDOW);
+    s_groups_bad = a.cu_groups[0] != 0 || a.cu_groups[G] != R;
+  }
+  __syncthreads();
+  // groups that do not cut the requests into runs: nothing is attended
+  for (int k = tid; k < G; k += blockDim.x)
+    if (a.cu_groups[k] > a.cu_groups[k + 1]) s_groups_bad = 1;
+  __syncthreads();
+  if (s_groups_bad) {
+    if (tid == 0) {
+      flag(a.dev_status, SV_DEV_BAD_PARAM);
+      a.hdr->T = a.hdr->W = a.hdr->C = a.hdr->units = 0;
+    }
+    return;
+  }
+  for (int base = 0; base < R; base += blockDim.x) {
+    const int i = base + tid;
+    Window w{};
+    int ctx = 0, nt = 0, stages = 0, first = 0, grp = 0, rows = 0;
+    if (i < R && request_rows(a, i, w, ctx)) {
+      grp = find_segment(a.cu_groups, G, i);
+      const int p = a.prefix_len[grp];
+      if (p < 0 || p % kBlockSize != 0) {
+        flag(a.dev_status, SV_DEV_BAD_PARAM);
+      } else if (p > ctx) {
+        flag(a.dev_status, SV_DEV_BAD_LENGTH);
+      } else {
+        first = p / kBlockSize;
+        rows = w.e - w.b;
+        nt = (rows + a.rt - 1) / a.rt;
+        for (int k = 0; k < nt; ++k) {
+          const int last = min(w.b + (k + 1) * a.rt, w.e);
+          stages += ((ctx + last + kBlockSize - 1) / kBlockSize - first + 3) / 4;
+        }
+      }
+    }
+    const int at = block_scan(nt, s_warp, &s_tiles);
+    int stage = block_scan(stages, s_warp, &s_stages) * a.Hkv;
+    const int arow = block_scan(rows, s_warp, &s_rows);
+    if (i < R) a.aoff[i] = arow;
+    for (int k = 0; k < rows && arow + k < a.bt.total_rows; ++k) a.arows[arow + k] = w.cu + w.b + k;
+    for (int k = 0; k < nt && at + k < a.tiles_cap; ++k) {
+      Tile t{};
+      t.i = i;
+      t.cu = w.cu;
+      t.ctx = ctx;
+      t.r0 = w.b + k * a.rt;
+      t.nr = min(a.rt, w.e - t.r0);
+      t.rows = w.rows;
+      t.first = first;
+      t.ncomp = ctx / kBlockSize - first;
+      t.nent = (ctx + t.r0 + t.nr + kBlockSize - 1) / kBlockSize - first;
+      t.arow = arow + k * a.rt;
+      t.grp = grp;
+      a.tiles[at + k] = t;
+      for (int g = 0; g < a.Hkv; ++g, stage += (t.nent + 3) / 4)
+        a.off[(size_t)(at + k) * a.Hkv + g] = stage;
+    }
+  }
+  // (offsets that overlap could ask for more than there is; such a call is left out)
+  const bool fits = s_tiles <= a.tiles_cap && s_rows <= a.bt.total_rows;
+  if (!fits) {
+    if (tid == 0) {
+      flag(a.dev_status, SV_DEV_BAD_WINDOW);
+      a.hdr->T = a.hdr->W = a.hdr->C = a.hdr->units = 0;
+    }
+    return;
+  }
+  const int T = s_tiles, W = s_stages * a.Hkv;
+  if (tid == 0) {
+    a.hdr->T = T;
+    a.off[(size_t)T * a.Hkv] = W;
+    a.aoff[R] = s_rows;
+  }
+  __syncthreads();
+  deal_stages(a, T * a.Hkv, W);
+  // groups: first active row, active rows, pages
+  for (int k = tid; k < G; k += blockDim.x) {
+    const int x = a.aoff[a.cu_groups[k]], n = a.aoff[a.cu_groups[k + 1]] - x;
+    const int pages = n > 0 ? a.prefix_len[k] / kBlockSize : 0;  // checked by its requests
+    a.groups[k] = make_int4(x, n, pages, 0);
+    atomicMax(&s_pages, pages);
+  }
+  __syncthreads();
+  // Pages of a unit: of the ways to cut the longest prefix into np parts the one
+  // whose waves of units (one CTA an SM) take least, a unit costing its stages
+  // and about three more for its start and its rows' merge.
+  if (warp == 0) {
+    long best = -1;
+    int best_P = kStagePages;
+    const int least = (s_pages + kUnitPages - 1) / kUnitPages;
+    for (int k = lane; k < 64; k += 32) {
+      const int np = max(1, least) + k;
+      int P = (s_pages + np - 1) / np;
+      P = max(kStagePages, (P + kStagePages - 1) / kStagePages * kStagePages);
+      long units = 0;
+      for (int y = 0; y < G; ++y) {
+        const int4 gr = a.groups[y];
+        units += (long)((gr.y * a.group + kPrefixRows - 1) / kPrefixRows) * a.Hkv * ((gr.z + P - 1) / P);
+      }
+      const long cost = (units + nsm - 1) / nsm * (P / kStagePages + 3);
+      if (units <= a.punits_cap && (best < 0 || cost < best)) {
+        best = cost;
+        best_P = P;
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const long b = __shfl_xor_sync(0xffffffffu, best, o);
+      const int P = __shfl_xor_sync(0xffffffffu, best_P, o);
+      if (b >= 0 && (best < 0 || b < best || (b == best && P > best_P))) {
+        best = b;
+        best_P = P;
+      }
+    }
+    if (lane == 0) s_np = best_P;
+  }
+  __syncthreads();
+  const int P = s_np;
+  for (int base = 0; base < G; base += blockDim.x) {
+    const int k = base + tid;
+    int4 gr = make_int4(0, 0, 0, 0);
+    int np = 0, n = 0;
+    if (k < G) {
+      gr = a.groups[k];
+      np = (gr.z + P - 1) / P;
+      n = (gr.y * a.group + kPrefixRows - 1) / kPrefixRows * a.Hkv * np;
+    }
+    const int at = block_scan(n, s_warp, &s_units);
+    if (k < G) a.groups[k].w = at;
+  }
+  for (int k = warp; k < G; k += blockDim.x >> 5) {
+    const int4 gr = a.groups[k];
+    const int np = (gr.z + P - 1) / P;
+    const int n = (gr.y * a.group + kPrefixRows - 1) / kPrefixRows * a.Hkv * np;
+    for (int y = lane; y < n && gr.w + y < a.punits_cap; y += 32)
+      a.punits[gr.w + y] = make_int4(k, y / np % a.Hkv, y / np / a.Hkv, y % np);
+  }
+  if (tid == 0) {
+    a.hdr->np_pages = P;
+    a.hdr->units = min(s_units, a.punits_cap);
+  }
+}
+
+// ------------------------------------------------------------ tcgen05 --
+// One CTA takes two tiles of 128 virtual rows by a run of pages, 128 tokens a
+// stage: S = Q K^T and O += P V of a tile are tcgen05.mma of 128 x 128 (S) and
+// 128 x D (O), accumulators in tensor memory: S of the tiles in columns 0 .. 255,
+// O in 256 .. 511.
+//   warps 0-3, 4-7: the softmax of tile 0 and 1; thread t owns row t (TMEM lane
+//     t): S to registers, running max and sum, P (bf16) back over S; O is
+//     rescaled in place only where a row's max grows by more than 2^8;
+//   warps 8, 9: the copies of K and V (two slots each, refilled as soon as both
+//     tiles' products have read them); warp 8 owns the tensor memory;
+//   warp 10: issues the products, tile 0's PV and next QK^T while tile 1's
+//     softmax runs and the other way round.
+// A barrier's commit covers every product issued before it, so a tile's S of a
+// stage also says that its PV of the stage before has landed.  Every wait is
+// bounded; a CTA that gives up flags SV_DEV_TIMEOUT, lets copies and products
+// land and frees its tensor memory.
+namespace pfx {
+constexpr int kTok = 128;
+constexpr int kThreads = 352;
+constexpr uint32_t kCols = 512, kColO = 256;
+template <int D>
+struct Smem {
+  static constexpr int kHalf = kTok * 128;            // 64 elements of d of 128 rows
+  static constexpr int kTile = D / 64 * kHalf;        // Q of a tile; K or V of a stage
+  static constexpr int kBytes = 2 * kTile + 4 * kTile + 1024;
+  // one CTA an SM: two would ask for more tensor memory than there is
+  static constexpr int kAsk = kBytes > 120 * 1024 ? kBytes : 120 * 1024;
+};
+}  // namespace pfx
+
+template <int D>
+__global__ void __launch_bounds__(pfx::kThreads, 1)
+    prefix_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap tmK,
+                  const __grid_constant__ CUtensorMap tmV) {
+  griddep_entry();
+  using pfx::kTok;
+  using S = pfx::Smem<D>;
+  constexpr int kHalves = D / 64;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  __shared__ int s_tbl[kUnitPages];
+  __shared__ __align__(8) unsigned long long s_kfull[2], s_kfree[2], s_vfull[2], s_vfree[2],
+      s_sfull[2], s_pfull[2], s_odone[2], s_drain;
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort, s_bad;
+  __shared__ int s_issued[4];
+  const int u = blockIdx.x;
+  if (u >= a.hdr->units) return;
+  const int4 un = a.punits[u];
+  const int4 gr = a.groups[un.x];
+  const int P = a.hdr->np_pages, g = un.y, group = a.group;
+  const int v0 = un.z * kPrefixRows, vrows = min(kPrefixRows, gr.y * group - v0);
+  const int ntile = vrows > 128 ? 2 : 1;
+  const int p0 = un.w * P, np = min(P, gr.z - p0);
+  const int n_stage = (np + kStagePages - 1) / kStagePages;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  uint8_t* base_ptr = smem_raw + (base - smem_u32(smem_raw));
+  const uint32_t ring = base + 2 * S::kTile;  // K slots, then V slots
+
+  if (tid == 0) {
+    s_abort = 0;
+    s_bad = np % kStagePages != 0;
+    for (int k = 0; k < 4; ++k) s_issued[k] = -1;
+    for (int k = 0; k < 2; ++k) {
+      mbar_init(smem_u32(&s_kfull[k]), 1);
+      mbar_init(smem_u32(&s_kfree[k]), 1);
+      mbar_init(smem_u32(&s_vfull[k]), 1);
+      mbar_init(smem_u32(&s_vfree[k]), 1);
+      mbar_init(smem_u32(&s_sfull[k]), 1);
+      mbar_init(smem_u32(&s_pfull[k]), 128);
+      mbar_init(smem_u32(&s_odone[k]), 1);
+    }
+    mbar_init(smem_u32(&s_drain), 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
+  const int32_t* table = a.tables + (size_t)a.cu_groups[un.x] * a.max_blocks + p0;
+  for (int p = tid; p < n_stage * kStagePages; p += pfx::kThreads) {
+    int b = -1;
+    if (p < np) {
+      b = __ldg(table + p);
+      if (b < 0 || b >= a.num_blocks) {
+        flag(a.dev_status, SV_DEV_BAD_BLOCK_ID);
+        b = -1;
+        s_bad = 1;
+      }
+    }
+    s_tbl[p] = b;
+  }
+  if (warp == 8) {
+    tc5::tmem_alloc(smem_u32(&s_tmem), pfx::kCols);
+    tc5::tmem_relinquish();
+  }
+  // Q rows, K-major with the 128-byte swizzle, zeros past the unit's rows
+  const bool real = tid < vrows;
+  if (tid < 128 * ntile) {
+    const int v = v0 + min(tid, vrows - 1);
+    const int4* src = reinterpret_cast<const int4*>(
+        a.q + ((size_t)a.arows[gr.x + v / group] * a.Hq + g * group + v % group) * D);
+    const int t = tid & 127;
+#pragma unroll
+    for (int c = 0; c < D / 8; ++c) {
+      const int4 x = real ? __ldg(src + c) : make_int4(0, 0, 0, 0);
+      const uint32_t off = (uint32_t)((tid >> 7) * S::kTile + (c >> 3) * S::kHalf + t * 128 +
+                                      (((c & 7) ^ (t & 7)) << 4));
+      *reinterpret_cast<int4*>(base_ptr + off) = x;
+    }
+    fence_proxy_async_smem();
+  }
+  tc5::fence_before_sync();
+  __syncthreads();
+  tc5::fence_after_sync();
+  const uint32_t tmem = s_tmem;
+
+  if (warp == 8 || warp == 9) {
+    // --------------------------------------------------------- producers --
+    const int half = warp - 8;  // 0: K, 1: V
+    unsigned long long* freeb = half ? s_vfree : s_kfree;
+    unsigned long long* fullb = half ? s_vfull : s_kfull;
+    for (int st = 0; st < n_stage; ++st) {
+      const int slot = st & 1;
+      bool go = true;
+      if (st >= 2) go = mbar_wait_bounded(smem_u32(&freeb[slot]), (uint32_t)(((st - 2) >> 1) & 1));
+      if (!__all_sync(0xffffffffu, go)) {
+        s_abort = 1;
+        break;
+      }
+      if (__any_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&s_abort))) break;
+      const int b = lane < kStagePages ? s_tbl[st * kStagePages + lane] : -1;
+      const uint32_t bar = smem_u32(&fullb[slot]);
+      const int n = __popc(__ballot_sync(0xffffffffu, b >= 0));
+      if (lane == 0) {
+        mbar_arrive_expect_tx(bar, (uint32_t)(n * kHalves * 2048));
+        s_issued[2 * half + slot] = st;
+      }
+      __syncwarp();
+      if (b >= 0) {
+        const uint32_t dst = ring + (2 * half + slot) * S::kTile + lane * 2048;
+        const int y = (b * a.Hkv + g) * kBlockSize;
+#pragma unroll
+        for (int h = 0; h < kHalves; ++h)
+          tma_load_2d(dst + h * S::kHalf, half ? &tmV : &tmK, 64 * h, y, bar);
+      }
+    }
+  } else if (warp == 10) {
+    // --------------------------------------------------------- MMA issue --
+    if (lane == 0) {
+      constexpr uint32_t idesc_qk = tc5::idesc_bf16_f32(128, kTok, false);
+      constexpr uint32_t idesc_pv = tc5::idesc_bf16_f32(128, D, true);
+      auto qk = [&](int t, int st) {
+        const uint32_t sb = ring + (st & 1) * S::kTile;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const uint64_t ad = tc5::sw128_desc(base + t * S::kTile + (ks >> 2) * S::kHalf + (ks & 3) * 32, 16, 1024);
+          const uint64_t bd = tc5::sw128_desc(sb + (ks >> 2) * S::kHalf + (ks & 3) * 32, 16, 1024);
+          tc5::mma_bf16(tmem + (uint32_t)(t * kTok), ad, bd, idesc_qk, ks > 0 ? 1u : 0u);
+        }
+        tc5::commit(smem_u32(&s_sfull[t]));
+        if (t == ntile - 1) tc5::commit(smem_u32(&s_kfree[st & 1]));
+      };
+      auto pv = [&](int t, int st) {
+        const uint32_t sb = ring + (2 + (st & 1)) * S::kTile;
+#pragma unroll
+        for (int ks = 0; ks < kTok / 16; ++ks) {
+          const uint64_t bd = tc5::sw128_desc(sb + ks * 2048, S::kHalf, 1024);
+          tc5::mma_bf16_ts(tmem + pfx::kColO + (uint32_t)(t * 128), tmem + (uint32_t)(t * kTok) + ks * 8,
+                           bd, idesc_pv, (st > 0 || ks > 0) ? 1u : 0u);
+        }
+        tc5::commit(smem_u32(&s_odone[t]));
+        if (t == ntile - 1) tc5::commit(smem_u32(&s_vfree[st & 1]));
+      };
+      bool ok = mbar_wait_bounded(smem_u32(&s_kfull[0]), 0u);
+      if (ok) {
+        tc5::fence_after_sync();
+        for (int t = 0; t < ntile; ++t) qk(t, 0);
+      }
+      for (int st = 0; st < n_stage && ok; ++st) {
+        const uint32_t par = (uint32_t)((st >> 1) & 1);
+        for (int t = 0; t < ntile && ok; ++t) {
+          // P of the tile is there (and S has been read), V has landed
+          ok = mbar_wait_bounded(smem_u32(&s_pfull[t]), (uint32_t)(st & 1)) &&
+               mbar_wait_bounded(smem_u32(&s_vfull[st & 1]), par) &&
+               !*reinterpret_cast<volatile int*>(&s_abort);
+          if (!ok) break;
+          tc5::fence_after_sync();
+          pv(t, st);
+          if (st + 1 < n_stage) {
+            // the next S goes where P was: PV has to be through with it
+            ok = mbar_wait_bounded(smem_u32(&s_kfull[(st + 1) & 1]), (uint32_t)(((st + 1) >> 1) & 1)) &&
+                 mbar_wait_bounded(smem_u32(&s_odone[t]), (uint32_t)(st & 1));
+            if (!ok) break;
+            tc5::fence_after_sync();
+            qk(t, st + 1);
+          }
+        }
+      }
+      if (!ok) s_abort = 1;
+      // every product has landed before the CTA moves on
+      tc5::commit(smem_u32(&s_drain));
+      mbar_wait_bounded(smem_u32(&s_drain), 0);
+    }
+  } else if (warp < 4 * ntile) {
+    // ----------------------------------------------------- softmax, rows --
+    const int t = warp >> 2;
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + lane_base + (uint32_t)(t * kTok);
+    const uint32_t to = tmem + lane_base + pfx::kColO + (uint32_t)(t * 128);
+    const float sc = a.scale_log2;
+    float m_ref = -INFINITY, l = 0.f;
+    bool ok = true;
+    for (int st = 0; st < n_stage; ++st) {
+      const bool got = mbar_wait_bounded(smem_u32(&s_sfull[t]), (uint32_t)(st & 1));
+      if (!__all_sync(0xffffffffu, got)) {
+        ok = false;
+        break;
+      }
+      tc5::fence_after_sync();
+      uint32_t sa[64], sb[64];
+      tc5::tmem_ld_x64(ts, sa);
+      tc5::tmem_ld_x64(ts + 64, sb);
+      uint32_t pages = 0xffu;  // pages of the stage that are there
+      if (s_bad) {
+        pages = 0u;
+#pragma unroll
+        for (int p = 0; p < kStagePages; ++p)
+          if (s_tbl[st * kStagePages + p] >= 0) pages |= 1u << p;
+        if (pages != 0xffu) {
+#pragma unroll
+          for (int j = 0; j < 64; ++j) {
+            if (!((pages >> (j / 16)) & 1u)) sa[j] = __float_as_uint(-INFINITY);
+            if (!((pages >> (4 + j / 16)) & 1u)) sb[j] = __float_as_uint(-INFINITY);
+          }
+        }
+      }
+      float mx = -INFINITY, mx2 = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < 64; ++j) {
+        mx = fmaxf(mx, __uint_as_float(sa[j]));
+        mx2 = fmaxf(mx2, __uint_as_float(sb[j]));
+      }
+      mx = fmaxf(mx, mx2) * sc;
+      const bool grow = mx > m_ref + 8.f;
+      if (__any_sync(0xffffffffu, grow)) {
+        const float m_new = grow ? mx : m_ref;
+        const float alpha = grow ? ex2(m_ref - m_new) : 1.f;  // 0 while m_ref is -inf
+        if (st > 0) {
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            uint32_t ov[32];
+            tc5::tmem_ld_x32(to + c, ov);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) ov[k] = __float_as_uint(__uint_as_float(ov[k]) * alpha);
+            tc5::tmem_st_x32(to + c, ov);
+          }
+        }
+        l *= alpha;
+        m_ref = m_new;
+      }
+      const float mb = m_ref == -INFINITY ? 0.f : m_ref;
+      float r0 = 0.f, r1 = 0.f;
+      uint32_t pk[32];
+#pragma unroll
+      for (int j = 0; j < 64; j += 2) {
+        const float e0 = ex2(fmaf(__uint_as_float(sa[j]), sc, -mb));
+        const float e1 = ex2(fmaf(__uint_as_float(sa[j + 1]), sc, -mb));
+        r0 += e0;
+        r1 += e1;
+        pk[j / 2] = pack_bf16(e0, e1);
+      }
+      tc5::tmem_st_x32(ts, pk);
+#pragma unroll
+      for (int j = 0; j < 64; j += 2) {
+        const float e0 = ex2(fmaf(__uint_as_float(sb[j]), sc, -mb));
+        const float e1 = ex2(fmaf(__uint_as_float(sb[j + 1]), sc, -mb));
+        r0 += e0;
+        r1 += e1;
+        pk[j / 2] = pack_bf16(e0, e1);
+      }
+      tc5::tmem_st_x32(ts + 32, pk);
+      l += r0 + r1;
+      if (pages != 0xffu && t == 0) {
+        // rows of V that were not copied may hold anything: zeros, so that
+        // their weights of 0 add nothing (tile 1's PV follows tile 0's)
+        const bool gv = mbar_wait_bounded(smem_u32(&s_vfull[st & 1]), (uint32_t)((st >> 1) & 1));
+        if (!__all_sync(0xffffffffu, gv)) {
+          ok = false;
+          break;
+        }
+        uint8_t* vb = base_ptr + (ring - base) + (2 + (st & 1)) * S::kTile;
+        for (int x = tid; x < kTok * (D / 8); x += 128) {
+          const int row = x / (D / 8), c = x % (D / 8);
+          if (!((pages >> (row / 16)) & 1u))
+            *reinterpret_cast<int4*>(vb + (c >> 3) * S::kHalf + row * 128 + (((c & 7) ^ (row & 7)) << 4)) =
+                make_int4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+      }
+      tc5::fence_before_sync();
+      mbar_arrive(smem_u32(&s_pfull[t]));
+    }
+    if (ok) {
+      const bool g3 = mbar_wait_bounded(smem_u32(&s_drain), 0u);
+      if (!__all_sync(0xffffffffu, g3)) ok = false;
+    }
+    if (!ok) {
+      s_abort = 1;
+    } else {
+      tc5::fence_after_sync();
+      const size_t row = (size_t)u * kPrefixRows + tid;
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        uint32_t ov[32];
+        tc5::tmem_ld_x32(to + c, ov);
+        if (!real) continue;
+        float4* dst = reinterpret_cast<float4*>(a.po + row * D + c);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          dst[k] = make_float4(__uint_as_float(ov[4 * k]), __uint_as_float(ov[4 * k + 1]),
+                               __uint_as_float(ov[4 * k + 2]), __uint_as_float(ov[4 * k + 3]));
+      }
+      if (real) reinterpret_cast<float2*>(a.pml)[row] = make_float2(m_ref, l);
+    }
+  }
+
+  // every role is done with tensor memory and the ring
+  tc5::fence_before_sync();
+  __syncthreads();
+  tc5::fence_after_sync();
+  if (s_abort) {
+    // copies in flight land before the CTA leaves (bounded waits)
+    if (tid == 0) {
+      flag(a.dev_status, SV_DEV_TIMEOUT);
+      for (int k = 0; k < 4; ++k)
+        if (s_issued[k] >= 0)
+          mbar_wait_bounded(smem_u32(k < 2 ? &s_kfull[k] : &s_vfull[k - 2]),
+                            (uint32_t)((s_issued[k] >> 1) & 1));
+    }
+    __syncthreads();
+  }
+  if (warp == 8) tc5::tmem_dealloc(tmem, pfx::kCols);
+}
+
+inline Args prefix_args(const sv_paged_kv* kv, const sv_batch* bt, const sv_shared_prefix* sp,
+                        int32_t Hq, uint8_t* at, size_t& off) {
+  Args a = common_args(kv, bt, Hq, at, off);
+  a.n_groups = sp->n_groups;
+  a.cu_groups = sp->cu_groups;
+  a.prefix_len = sp->prefix_len;
+  a.arows = take<int>(at, off, bt->total_rows);
+  a.aoff = take<int>(at, off, bt->n_req + 1);
+  a.groups = take<int4>(at, off, sp->n_groups);
+  // the row tiles of all groups, by the parts that the longest table needs at
+  // least, and four waves of units to choose finer parts from
+  const long tiles = (long)bt->total_rows * a.group / kPrefixRows + sp->n_groups;
+  const long parts = std::max(1, (kv->max_blocks_per_req + kUnitPages - 1) / kUnitPages);
+  a.punits_cap = (int)(tiles * a.Hkv * parts + 4L * sizing_sms());
+  a.punits = take<int4>(at, off, a.punits_cap);
+  a.pml = take<float>(at, off, (size_t)a.punits_cap * kPrefixRows * 2);
+  a.po = take<float>(at, off, (size_t)a.punits_cap * kPrefixRows * kv->head_dim);
+  return a;
+}
+
+template <int D>
+sv_status prefix_attend(const Args& a, const void* k, const void* v, cudaStream_t stream) {
+  CUtensorMap tmK, tmV;
+  if (!attn::make_map(&tmK, k, a.num_blocks, a.Hkv, D) || !attn::make_map(&tmV, v, a.num_blocks, a.Hkv, D))
+    return SV_ERR_CUDA;
+  static PerDevice set;
+  if (smem_limit_once(set, prefix_kernel<D>, pfx::Smem<D>::kAsk) != cudaSuccess) return SV_ERR_CUDA;
+  const int threads = std::min(1024, std::max(128, (a.bt.n_req + 31) / 32 * 32));
+  if (sv::launch(prefix_plan_kernel, 1, threads, 0, stream, a, sizing_sms()) != cudaSuccess ||
+      sv::launch(prefix_kernel<D>, a.punits_cap, pfx::kThreads, pfx::Smem<D>::kAsk, stream, a, tmK, tmV) !=
+          cudaSuccess)
+    return SV_ERR_CUDA;
+  return launch_units<D, false>(a, tmK, tmV, stream);
+}
+
+inline sv_status check_prefix(const sv_paged_kv* kv, const sv_batch* bt, const sv_shared_prefix* sp,
+                              int32_t Hq) {
+  const sv_status st = check(kv, bt, Hq);
+  if (st != SV_OK) return st;
+  if (!sp) return SV_ERR_INVALID_ARGUMENT;
+  if (bt->n_req == 0) return SV_OK;
+  if (sp->n_groups < 1 || sp->n_groups > bt->n_req) return SV_ERR_INVALID_ARGUMENT;
+  return SV_OK;
+}
+
+}  // namespace pu
+}  // namespace sv
+
+using namespace sv;
+
+extern "C" size_t sv_prefix_attend_workspace(const sv_batch* bt, const sv_paged_kv* kv,
+                                             const sv_shared_prefix* prefix, int32_t n_q_heads) {
+  if (pu::check_prefix(kv, bt, prefix, n_q_heads) != SV_OK) return 0;
+  size_t off = 0;
+  (void)pu::prefix_args(kv, bt, prefix, n_q_heads, nullptr, off);
+  return off;
+}
+
+extern "C" sv_status sv_prefix_attend(const sv_paged_kv* kv, const sv_batch* bt,
+                                      const sv_shared_prefix* prefix, const void* q,
+                                      int32_t n_q_heads, float softmax_scale, void* out, void* ws,
+                                      size_t ws_bytes, int32_t* dev_status, void* stream) {
+  SV_TRACE("sv_prefix_attend");
+  const sv_status st = pu::check_prefix(kv, bt, prefix, n_q_heads);
+  if (st != SV_OK) return st;
+  if (bt->n_req == 0 || bt->total_rows == 0) return SV_OK;
+  if (!q || !out || !ws || !prefix->cu_groups || !prefix->prefix_len) return SV_ERR_INVALID_ARGUMENT;
+  if (((uintptr_t)q & 15) || ((uintptr_t)out & 3)) return SV_ERR_INVALID_ARGUMENT;
+  if ((uintptr_t)ws & 255) return SV_ERR_INVALID_ARGUMENT;
+  if (!(softmax_scale > 0.f)) return SV_ERR_INVALID_ARGUMENT;
+  size_t need = 0;
+  pu::Args a = pu::prefix_args(kv, bt, prefix, n_q_heads, static_cast<uint8_t*>(ws), need);
+  if (ws_bytes < need) return SV_ERR_WORKSPACE_TOO_SMALL;
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.out = static_cast<__nv_bfloat16*>(out);
+  a.scale_log2 = softmax_scale * 1.4426950408889634f;
+  a.dev_status = dev_status;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return kv->head_dim == 128 ? pu::prefix_attend<128>(a, kv->k_cache, kv->v_cache, s)
+                             : pu::prefix_attend<64>(a, kv->k_cache, kv->v_cache, s);
+}
