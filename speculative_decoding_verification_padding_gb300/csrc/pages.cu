@@ -148,23 +148,24 @@ struct ScoreArgs {
 };
 
 constexpr int kScoreThreads = 128;
-constexpr int kScoreTiles = 8;  // 16-row tiles of a CTA
+constexpr int kScoreTiles = 16;  // tiles of eight virtual rows of a CTA
 constexpr int kMaxPer = 256;
 
 // For a row's query head h and page t: sum_d max(q lo, q hi) = min(q, 0) . lo +
 // max(q, 0) . hi, a product of [q-, q+] with the 2 D contiguous elements [lo,
 // hi] of the page: exact bf16 factors, fp32 sums, on mma.sync m16n8k16 (16
-// virtual rows x 8 pages x 16 elements).  A 16-row tile holds 16 / g2 rows, its
-// g2 >= group slots the group's heads (some twice: the maximum over the slots
-// does not see that).  The k order of a product is free, so a lane takes 16
-// consecutive bytes of a page's bounds as the operands of two steps: the bounds
-// go from global memory to registers without a stop, 16 pages a warp at once.
-template <int D>
+// pages x 8 virtual rows x 16 elements).  Virtual row v is row v / g2, head slot
+// v % g2 of it, the group's heads in the first slots and again in the rest (the
+// maximum over the slots does not see that).  The pages are the product's rows:
+// the maximum over a row's slots is then one over four neighbouring lanes.  The k
+// order of a product is free, so a lane takes 16 consecutive bytes of a page's
+// bounds as the operands of two steps: the bounds go from global memory to
+// registers without a stop, 16 pages a warp at once.
+template <int D, int G2>
 __global__ void __launch_bounds__(kScoreThreads) score_kernel(ScoreArgs a) {
   griddep_entry();
-  constexpr int kSteps = 2 * D / 16;
-  constexpr int kPairs = kSteps / 2;  // 16-byte chunks a lane holds of a page
-  extern __shared__ __align__(16) uint4 s_q[];  // [tile][step][lane]
+  constexpr int kPairs = 2 * D / 32;  // 16-byte chunks a lane holds of a page, two steps each
+  extern __shared__ __align__(16) uint4 s_q[];  // [tile][pair of steps][lane]
   __shared__ int s_tbl[kMaxPer];
   const int i = blockIdx.z / a.Hkv, g = blockIdx.z % a.Hkv;
   const Window w = window_of(a.bt, i);
@@ -179,14 +180,14 @@ __global__ void __launch_bounds__(kScoreThreads) score_kernel(ScoreArgs a) {
     if (first) flag(a.dev_status, SV_DEV_BAD_LENGTH);
     return;
   }
-  const int per_tile = 16 / a.g2;  // rows of a tile
-  const int r0 = w.b + blockIdx.y * kScoreTiles * per_tile;
-  const int nr = min(w.e - r0, kScoreTiles * per_tile);
+  const int per_block = kScoreTiles * 8 / G2;  // rows of a CTA
+  const int r0 = w.b + blockIdx.y * per_block;
+  const int nr = min(w.e - r0, per_block);
   const int p0 = blockIdx.x * a.per, p1 = min(n, p0 + a.per);
   if (nr <= 0 || p0 >= p1) return;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int gq = lane >> 2, tq = lane & 3;
-  const int tiles = (nr + per_tile - 1) / per_tile;
+  const int tiles = (nr * G2 + 7) / 8;
   for (int p = p0 + tid; p < p1; p += kScoreThreads) {
     int b = __ldg(a.tables + (size_t)i * a.max_blocks + p);
     if (b < 0 || b >= a.num_blocks) {
@@ -195,74 +196,110 @@ __global__ void __launch_bounds__(kScoreThreads) score_kernel(ScoreArgs a) {
     }
     s_tbl[p - p0] = b;
   }
-  // [q-, q+] of the tiles' rows in the order the products take them
-  for (int x = tid; x < tiles * kPairs * 32; x += kScoreThreads) {
-    const int l = x & 31, c = (x >> 5) % kPairs, mt = (x >> 5) / kPairs;
-    const int chunk = c * 4 + (l & 3);
-    uint4 v[2];
+  // [q-, q+] of the rows in the order the products take them: the lower half of
+  // the pairs is q-, the upper q+, of the same chunk of q
+  for (int x = tid; x < tiles * (kPairs / 2) * 32; x += kScoreThreads) {
+    const int l = x & 31, c = (x >> 5) % (kPairs / 2), nt = (x >> 5) / (kPairs / 2);
+    const int v = nt * 8 + (l >> 2);
+    const int r = min(v / G2, nr - 1);
+    const int h = v % G2 < a.group ? v % G2 : v % G2 - a.group;  // G2 < 2 group
+    uint4 up = __ldg(reinterpret_cast<const uint4*>(
+                  a.q + ((size_t)(w.cu + r0 + r) * a.Hq + g * a.group + h) * D) + c * 4 + (l & 3));
+    uint4 down = up;
+    const __nv_bfloat162 z = __floats2bfloat162_rn(0.f, 0.f);
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int slot = (l >> 2) + 8 * k;
-      const int r = min(mt * per_tile + slot / a.g2, nr - 1), h = (slot % a.g2) % a.group;
-      const uint4* src = reinterpret_cast<const uint4*>(
-          a.q + ((size_t)(w.cu + r0 + r) * a.Hq + g * a.group + h) * D);
-      v[k] = __ldg(src + chunk % (D / 8));
-      const __nv_bfloat162 z = __floats2bfloat162_rn(0.f, 0.f);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        __nv_bfloat162& y = reinterpret_cast<__nv_bfloat162*>(&v[k])[e];
-        y = chunk < D / 8 ? __hmin2(y, z) : __hmax2(y, z);
-      }
+    for (int e = 0; e < 4; ++e) {
+      __nv_bfloat162& y = reinterpret_cast<__nv_bfloat162*>(&up)[e];
+      reinterpret_cast<__nv_bfloat162*>(&down)[e] = __hmin2(y, z);
+      y = __hmax2(y, z);
     }
-    s_q[(mt * kSteps + 2 * c) * 32 + l] = make_uint4(v[0].x, v[1].x, v[0].y, v[1].y);
-    s_q[(mt * kSteps + 2 * c + 1) * 32 + l] = make_uint4(v[0].z, v[1].z, v[0].w, v[1].w);
+    s_q[(nt * kPairs + c) * 32 + l] = down;
+    s_q[(nt * kPairs + kPairs / 2 + c) * 32 + l] = up;
   }
   __syncthreads();
+  float* out = a.scores + ((size_t)(w.cu + r0) * a.Hkv + g) * a.max_pages;
+  const size_t row_step = (size_t)a.Hkv * a.max_pages;
+  constexpr int kRows = 8 / (G2 < 8 ? G2 : 8);  // rows of a tile
   for (int p = p0 + warp * 16; p < p1; p += (kScoreThreads / 32) * 16) {
-    uint4 bd[2][kPairs];
+    uint4 bd[2][kPairs];  // pages p + gq and p + gq + 8
 #pragma unroll
-    for (int nt = 0; nt < 2; ++nt) {
-      const int page = p + nt * 8 + gq;
+    for (int k = 0; k < 2; ++k) {
+      const int page = p + k * 8 + gq;
       const int b = page < p1 ? s_tbl[page - p0] : -1;
       const uint4* src = reinterpret_cast<const uint4*>(
           a.bounds + ((size_t)max(b, 0) * a.Hkv + g) * 2 * D) + tq;
 #pragma unroll
-      for (int c = 0; c < kPairs; ++c) bd[nt][c] = b >= 0 ? __ldg(src + c * 4) : make_uint4(0, 0, 0, 0);
+      for (int c = 0; c < kPairs; ++c) bd[k][c] = b >= 0 ? __ldg(src + c * 4) : make_uint4(0, 0, 0, 0);
     }
-    for (int mt = 0; mt < tiles; ++mt) {
-      float acc[2][4] = {};
+    for (int nt = 0; nt < tiles; nt += 2) {
+      float acc[2][4] = {};  // pages gq, gq + 8 by virtual rows 2 tq, 2 tq + 1
+      const uint4* s0 = s_q + nt * kPairs * 32 + lane;
+      const uint4* s1 = s0 + (nt + 1 < tiles ? kPairs * 32 : 0);
 #pragma unroll
       for (int c = 0; c < kPairs; ++c) {
-        const uint4 x = s_q[(mt * kSteps + 2 * c) * 32 + lane];
-        const uint4 y = s_q[(mt * kSteps + 2 * c + 1) * 32 + lane];
-        const uint32_t ax[4] = {x.x, x.y, x.z, x.w}, ay[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-          mma16816(acc[nt], ax, bd[nt][c].x, bd[nt][c].y);
-          mma16816(acc[nt], ay, bd[nt][c].z, bd[nt][c].w);
-        }
+        const uint32_t ax[4] = {bd[0][c].x, bd[1][c].x, bd[0][c].y, bd[1][c].y};
+        const uint32_t ay[4] = {bd[0][c].z, bd[1][c].z, bd[0][c].w, bd[1][c].w};
+        const uint4 x = s0[c * 32], y = s1[c * 32];
+        mma16816(acc[0], ax, x.x, x.y);
+        mma16816(acc[1], ax, y.x, y.y);
+        mma16816(acc[0], ay, x.z, x.w);
+        mma16816(acc[1], ay, y.z, y.w);
       }
-      // the maximum over each row's g2 slots: lanes gq and gq + 8
+      if (G2 == 1) {  // every virtual row is a row
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt) {
-        if (a.g2 == 16)
+        for (int k = 0; k < 2; ++k)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) acc[nt][e] = acc[nt][e + 2] = fmaxf(acc[nt][e], acc[nt][e + 2]);
-        for (int o = 1; o < a.g2 && o < 8; o <<= 1)
+          for (int e = 0; e < 4; ++e) {
+            const int r = (nt + k) * 8 + 2 * tq + (e & 1), page = p + gq + (e >> 1) * 8;
+            if (r < nr && page < p1) out[r * row_step + page] = acc[k][e];
+          }
+        continue;
+      }
+      float lo[2], hi[2];  // pages gq, gq + 8
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            acc[nt][e] = fmaxf(acc[nt][e], __shfl_xor_sync(0xffffffffu, acc[nt][e], 4 * o));
-        if (gq % min(a.g2, 8) != 0) continue;
+      for (int k = 0; k < 2; ++k) {
+        lo[k] = fmaxf(acc[k][0], acc[k][1]);
+        hi[k] = fmaxf(acc[k][2], acc[k][3]);
+      }
+      if (G2 == 16) {  // both tiles are one row's
+        lo[0] = fmaxf(lo[0], lo[1]);
+        hi[0] = fmaxf(hi[0], hi[1]);
+      }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int slot = gq + (e >> 1) * 8;
-          const int r = mt * per_tile + slot / a.g2, page = p + nt * 8 + 2 * tq + (e & 1);
-          if (slot % a.g2 == 0 && r < nr && page < p1)
-            a.scores[((size_t)(w.cu + r0 + r) * a.Hkv + g) * a.max_pages + page] = acc[nt][e];
+      for (int k = 0; k < 2; ++k) {
+        if (G2 > 2) {
+          lo[k] = fmaxf(lo[k], __shfl_xor_sync(0xffffffffu, lo[k], 1));
+          hi[k] = fmaxf(hi[k], __shfl_xor_sync(0xffffffffu, hi[k], 1));
+        }
+        if (G2 > 4) {
+          lo[k] = fmaxf(lo[k], __shfl_xor_sync(0xffffffffu, lo[k], 2));
+          hi[k] = fmaxf(hi[k], __shfl_xor_sync(0xffffffffu, hi[k], 2));
+        }
+        // the lanes of a row: the first writes page gq, the second (where the row
+        // has one) page gq + 8
+        constexpr int own = G2 < 2 ? 1 : G2 < 8 ? G2 / 2 : 4;  // lanes of a row
+        const int r = G2 == 16 ? nt / 2 : (nt + k) * kRows + 2 * tq / (G2 < 8 ? G2 : 8), at = tq % own;
+        if (r >= nr || (G2 == 16 && k == 1)) continue;
+        if (own == 1) {
+          if (p + gq < p1) out[r * row_step + p + gq] = lo[k];
+          if (p + gq + 8 < p1) out[r * row_step + p + gq + 8] = hi[k];
+        } else if (at < 2 && p + gq + 8 * at < p1) {
+          out[r * row_step + p + gq + 8 * at] = at ? hi[k] : lo[k];
         }
       }
     }
   }
+}
+
+template <int G2>
+cudaError_t launch_score(const ScoreArgs& a, int dim, dim3 grid, size_t smem, cudaStream_t s) {
+  static PerDevice set128, set64;
+  const size_t most = (size_t)kScoreTiles * 8 * 32 * 16;  // of head_dim 128
+  cudaError_t e = dim == 128 ? smem_limit_once(set128, score_kernel<128, G2>, most)
+                             : smem_limit_once(set64, score_kernel<64, G2>, most);
+  if (e != cudaSuccess) return e;
+  return dim == 128 ? sv::launch(score_kernel<128, G2>, grid, kScoreThreads, smem, s, a)
+                    : sv::launch(score_kernel<64, G2>, grid, kScoreThreads, smem, s, a);
 }
 
 // ---------------------------------------------------------------- select --
@@ -276,8 +313,6 @@ struct SelectArgs {
   int Hkv, max_blocks, max_pages, n_first, n_last, n_keep;
 };
 
-constexpr int kSelectThreads = 256;
-
 // Whole numbers in the order of the scores: NaN below everything, -0 = +0.
 __device__ __forceinline__ uint32_t score_key(float x) {
   if (x != x) return 0u;
@@ -285,104 +320,223 @@ __device__ __forceinline__ uint32_t score_key(float x) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// One CTA a (row, KV head).  The n_keep-th greatest key is found digit by digit
-// (8 bits, from the highest) in counts of the keys that agree with the digits
-// found before; then the pages above it and the first of those equal to it are
-// written in order.
-__global__ void __launch_bounds__(kSelectThreads) select_kernel(SelectArgs a) {
-  griddep_entry();
-  extern __shared__ uint32_t s_key[];
-  __shared__ int s_hist[256];
-  __shared__ int s_warp[2][kSelectThreads / 32];
-  __shared__ uint32_t s_prefix;
-  __shared__ int s_need;
-  const int r = blockIdx.x, g = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (r >= a.bt.cu_rows[a.bt.n_req]) return;
-  const int i = find_segment(a.bt.cu_rows, a.bt.n_req, r);
+struct SelectRow {
+  int r, g, n;
+};
+
+// The row and KV head of a CTA; false if it has nothing to choose (every page is
+// kept, or the row is left as it is).
+__device__ __forceinline__ bool select_row(const SelectArgs& a, SelectRow& s) {
+  s.r = blockIdx.x;
+  s.g = blockIdx.y;
+  const int tid = threadIdx.x;
+  if (s.r >= a.bt.cu_rows[a.bt.n_req]) return false;
+  const int i = find_segment(a.bt.cu_rows, a.bt.n_req, s.r);
   const Window w = window_of(a.bt, i);
-  const int ctx = a.lens[i], n = ctx / kBlockSize;
+  const int ctx = a.lens[i];
+  s.n = ctx / kBlockSize;
   if (!w.ok) {
-    if (tid == 0 && g == 0) flag(a.dev_status, SV_DEV_BAD_WINDOW);
-    return;
+    if (tid == 0 && s.g == 0) flag(a.dev_status, SV_DEV_BAD_WINDOW);
+    return false;
   }
-  if (ctx < 0 || ctx > (long)a.max_blocks * kBlockSize || n > a.max_pages) {
-    if (tid == 0 && g == 0) flag(a.dev_status, SV_DEV_BAD_LENGTH);
-    return;
+  if (ctx < 0 || ctx > (long)a.max_blocks * kBlockSize || s.n > a.max_pages) {
+    if (tid == 0 && s.g == 0) flag(a.dev_status, SV_DEV_BAD_LENGTH);
+    return false;
   }
-  if (r < w.cu + w.b || r >= w.cu + w.e) return;
-  int32_t* out = a.pages + ((size_t)r * a.Hkv + g) * a.n_keep;
-  if (n <= a.n_keep) {
-    for (int t = tid; t < a.n_keep; t += kSelectThreads) out[t] = t < n ? t : -1;
-    return;
+  if (s.r < w.cu + w.b || s.r >= w.cu + w.e) return false;
+  if (s.n <= a.n_keep) {
+    int32_t* out = a.pages + ((size_t)s.r * a.Hkv + s.g) * a.n_keep;
+    for (int t = tid; t < a.n_keep; t += blockDim.x) out[t] = t < s.n ? t : -1;
+    return false;
   }
-  const float* s = a.scores + ((size_t)r * a.Hkv + g) * a.max_pages;
-  for (int t = tid; t < n; t += kSelectThreads)
-    s_key[t] = (t < a.n_first || t >= n - a.n_last) ? 0xffffffffu : score_key(__ldg(s + t));
-  if (tid == 0) {
-    s_prefix = 0u;
-    s_need = a.n_keep;
-  }
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    s_hist[tid] = 0;
-    __syncthreads();
-    const uint32_t above = shift == 24 ? 0u : 0xffffffffu << (shift + 8);
-    const uint32_t prefix = s_prefix;
-    for (int t = tid; t < n; t += kSelectThreads) {
-      const uint32_t k = s_key[t];
-      if ((k & above) == prefix) atomicAdd(&s_hist[(k >> shift) & 255], 1);
+  return true;
+}
+
+// The score a key stands for (0 is NaN's).
+__device__ __forceinline__ float key_score(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? k & 0x7fffffffu : ~k);
+}
+
+constexpr int kBins = 2048;
+constexpr int kCandidates = 512;
+
+// One CTA a (row, KV head), its keys in shared memory.  The n_keep-th greatest:
+// the keys between the least and the greatest are counted in kBins bins of equal
+// width (of the scores; of the keys where the scores' range is no number to
+// divide by), the bin that holds the one sought is found from the top, and its
+// few keys rank one another.  Where they are many the bin is cut again; equal
+// keys need no cut.  Then the pages above it and the first of those equal to it
+// are written in order.  Ranges of scores fill equal bins better than digits of
+// their bits: few additions meet in one word.
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS) select_kernel(SelectArgs a) {
+  griddep_entry();
+  constexpr int kWarps = THREADS / 32;
+  constexpr int kOwn = kBins / THREADS;  // bins a thread adds up
+  extern __shared__ uint32_t s_key[];
+  __shared__ uint32_t s_bin[kBins];
+  __shared__ uint32_t s_cand[kCandidates];
+  __shared__ uint32_t s_min[kWarps], s_max[kWarps], s_sum[kWarps];
+  __shared__ uint32_t s_kth;
+  __shared__ int s_found, s_before, s_count, s_above;
+  SelectRow sr;
+  if (!select_row(a, sr)) return;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = sr.n;
+  const float* s = a.scores + ((size_t)sr.r * a.Hkv + sr.g) * a.max_pages;
+  // the least and greatest of the keys that are chosen from
+  auto range = [&](uint32_t mn, uint32_t mx, uint32_t& lo, uint32_t& hi) {
+    mn = __reduce_min_sync(0xffffffffu, mn);
+    mx = __reduce_max_sync(0xffffffffu, mx);
+    if (lane == 0) {
+      s_min[warp] = mn;
+      s_max[warp] = mx;
     }
     __syncthreads();
-    if (warp == 0) {
-      // keys in the digits above lane's eight, from the highest digit down
-      int c[8], sum = 0;
+    lo = __reduce_min_sync(0xffffffffu, s_min[lane % kWarps]);
+    hi = __reduce_max_sync(0xffffffffu, s_max[lane % kWarps]);
+  };
+  uint32_t mn = 0xffffffffu, mx = 0u, lo, hi;
+#pragma unroll 4
+  for (int t = tid; t < n; t += THREADS) {
+    uint32_t k = 0xffffffffu;
+    if (t >= a.n_first && t < n - a.n_last) {
+      k = score_key(__ldg(s + t));
+      mn = min(mn, k);
+      mx = max(mx, k);
+    }
+    s_key[t] = k;
+  }
+  range(mn, mx, lo, hi);
+  int need = a.n_keep - a.n_first - a.n_last;  // keys still sought in lo .. hi
+  uint32_t kth = 0xffffffffu;                  // none: the pages that are always kept
+  if (need == 0) need = a.n_keep;
+  else
+    for (;;) {
+      if (lo == hi) {
+        kth = lo;
+        break;
+      }
+      const float xlo = key_score(lo), width = key_score(hi) - xlo;
+      const bool linear = lo > 0u && width > 1e-30f && width < 1e38f;
+      const float inv = linear ? (float)(kBins - 1) / width : 0.f;
+      const int shift = max(0, 32 - __clz(hi - lo) - 11);
+      auto bin = [&](uint32_t k) {  // never falls where k grows
+        return linear ? min(kBins - 1, (int)((key_score(k) - xlo) * inv)) : (int)((k - lo) >> shift);
+      };
 #pragma unroll
-      for (int k = 0; k < 8; ++k) sum += c[k] = s_hist[255 - (lane * 8 + k)];
-      int x = sum;
+      for (int k = 0; k < kOwn; ++k) s_bin[k * THREADS + tid] = 0u;
+      if (tid == 0) s_count = s_above = 0;
+      __syncthreads();
+      for (int t = tid; t < n; t += THREADS) {
+        const uint32_t k = s_key[t];
+        if (k >= lo && k <= hi) atomicAdd(&s_bin[bin(k)], 1u);
+      }
+      __syncthreads();
+      // thread tid adds up kOwn bins, the highest for thread 0
+      uint32_t c[kOwn], sum = 0;
+#pragma unroll
+      for (int k = 0; k < kOwn; ++k) sum += c[k] = s_bin[kBins - 1 - (tid * kOwn + k)];
+      uint32_t x = sum;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
         if (lane >= o) x += y;
       }
-      const int need = s_need;
-      __syncwarp();
-      int before = x - sum;
-      if (before < need && x >= need) {
+      if (lane == 31) s_sum[warp] = x;
+      __syncthreads();
+      uint32_t before = x - sum;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          if (before < need && before + c[k] >= need) {
-            s_prefix = prefix | ((uint32_t)(255 - (lane * 8 + k)) << shift);
-            s_need = need - before;
+      for (int y = 0; y < kWarps; ++y)
+        if (y < warp) before += s_sum[y];
+      if ((int)before < need && (int)(before + sum) >= need) {
+#pragma unroll
+        for (int k = 0; k < kOwn; ++k) {
+          if ((int)before < need && (int)(before + c[k]) >= need) {
+            s_found = kBins - 1 - (tid * kOwn + k);
+            s_before = (int)before;
           }
           before += c[k];
         }
       }
+      __syncthreads();
+      const int found = s_found;
+      need -= s_before;
+      const bool few = s_bin[found] <= (uint32_t)kCandidates;
+      mn = 0xffffffffu;
+      mx = 0u;
+      for (int t = tid; t < n; t += THREADS) {
+        const uint32_t k = s_key[t];
+        if (k < lo || k > hi || bin(k) != found) continue;
+        mn = min(mn, k);
+        mx = max(mx, k);
+        if (few) s_cand[atomicAdd(&s_count, 1)] = k;
+      }
+      if (!few) {
+        range(mn, mx, lo, hi);
+        continue;
+      }
+      __syncthreads();
+      // the key with fewer than `need` candidates above it and at least so many at
+      // or above it (equal ones find the same)
+      const int m = s_count;
+      for (int y = tid; y < m; y += THREADS) {
+        const uint32_t k = s_cand[y];
+        int up = 0, eq = 0;
+        for (int z = 0; z < m; ++z) {
+          up += s_cand[z] > k;
+          eq += s_cand[z] == k;
+        }
+        if (up < need && up + eq >= need) {
+          s_kth = k;
+          s_above = up;
+        }
+      }
+      __syncthreads();
+      kth = s_kth;
+      need -= s_above;
+      break;
     }
-    __syncthreads();
+  // places in order: pages above the threshold and equal to it are counted for
+  // every warp's 32 neighbours (high and low half of a word), then added up
+  const int chunks = (n + 31) / 32;  // at most 1536
+  __syncthreads();
+  for (int ch = warp; ch < chunks; ch += kWarps) {
+    const uint32_t k = ch * 32 + lane < n ? s_key[ch * 32 + lane] : 0u;
+    const unsigned bu = __ballot_sync(0xffffffffu, ch * 32 + lane < n && k > kth);
+    const unsigned be = __ballot_sync(0xffffffffu, ch * 32 + lane < n && k == kth);
+    if (lane == 0) s_bin[ch] = ((uint32_t)__popc(bu) << 16) | (uint32_t)__popc(be);
   }
-  const uint32_t kth = s_prefix;
-  const int need = s_need;  // of the pages whose key is kth, the first so many
-  int above = 0, equal = 0;  // written so far
-  for (int base = 0; base < n; base += kSelectThreads) {
-    const int t = base + tid;
+  __syncthreads();
+  uint32_t c[kOwn], sum = 0;
+#pragma unroll
+  for (int k = 0; k < kOwn; ++k) sum += c[k] = tid * kOwn + k < chunks ? s_bin[tid * kOwn + k] : 0u;
+  uint32_t x = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) s_sum[warp] = x;
+  __syncthreads();
+  uint32_t before = x - sum;
+#pragma unroll
+  for (int y = 0; y < kWarps; ++y)
+    if (y < warp) before += s_sum[y];
+#pragma unroll
+  for (int k = 0; k < kOwn; ++k) {
+    if (tid * kOwn + k < chunks) s_bin[tid * kOwn + k] = before;
+    before += c[k];
+  }
+  __syncthreads();
+  int32_t* out = a.pages + ((size_t)sr.r * a.Hkv + sr.g) * a.n_keep;
+  for (int ch = warp; ch < chunks; ch += kWarps) {
+    const int t = ch * 32 + lane;
     const uint32_t k = t < n ? s_key[t] : 0u;
-    const bool up = t < n && k > kth, eq = t < n && k == kth;
-    const unsigned bu = __ballot_sync(0xffffffffu, up), be = __ballot_sync(0xffffffffu, eq);
-    if (lane == 0) {
-      s_warp[0][warp] = __popc(bu);
-      s_warp[1][warp] = __popc(be);
-    }
-    __syncthreads();
-    int u = above, e = equal;
-    for (int x = 0; x < kSelectThreads / 32; ++x) {
-      if (x < warp) { u += s_warp[0][x]; e += s_warp[1][x]; }
-      above += s_warp[0][x];
-      equal += s_warp[1][x];
-    }
+    const bool u = t < n && k > kth, e = t < n && k == kth;
+    const unsigned bu = __ballot_sync(0xffffffffu, u), be = __ballot_sync(0xffffffffu, e);
     const unsigned below = (1u << lane) - 1u;
-    u += __popc(bu & below);
-    e += __popc(be & below);
-    if (up || (eq && e < need)) out[u + min(e, need)] = t;
-    __syncthreads();
+    const int pe = (int)(s_bin[ch] & 0xffffu) + __popc(be & below);
+    if (u || (e && pe < need)) out[(s_bin[ch] >> 16) + __popc(bu & below) + min(pe, need)] = t;
   }
 }
 
@@ -474,20 +628,21 @@ extern "C" sv_status sv_score_pages(const sv_paged_kv* kv, const sv_batch* bt, c
   if (nsm < 1) return SV_ERR_CUDA;
   const long units = (long)bt->n_req * kv->n_kv_heads * max_pages;
   a.per = units <= 64L * 8 * nsm ? 64 : pg::kMaxPer;
-  const int per_block = pg::kScoreTiles * (16 / a.g2);
+  const int per_block = pg::kScoreTiles * 8 / a.g2;
   const int most_rows = std::min(bt->max_rows_per_req, bt->total_rows);
   const dim3 grid((max_pages + a.per - 1) / a.per, (most_rows + per_block - 1) / per_block,
                   bt->n_req * kv->n_kv_heads);
-  const int tiles = std::min(pg::kScoreTiles, (most_rows + 16 / a.g2 - 1) / (16 / a.g2));
-  const size_t smem = (size_t)tiles * (2 * kv->head_dim / 16) * 32 * 16;
+  const int tiles = std::min(pg::kScoreTiles, (most_rows * a.g2 + 7) / 8);
+  const size_t smem = (size_t)tiles * (2 * kv->head_dim / 32) * 32 * 16;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  static PerDevice set128, set64;
-  if (smem_limit_once(set128, pg::score_kernel<128>, 65536) != cudaSuccess ||
-      smem_limit_once(set64, pg::score_kernel<64>, 65536) != cudaSuccess)
-    return SV_ERR_CUDA;
-  const cudaError_t e =
-      kv->head_dim == 128 ? sv::launch(pg::score_kernel<128>, grid, pg::kScoreThreads, smem, s, a)
-                          : sv::launch(pg::score_kernel<64>, grid, pg::kScoreThreads, smem, s, a);
+  cudaError_t e;
+  switch (a.g2) {
+    case 1: e = pg::launch_score<1>(a, kv->head_dim, grid, smem, s); break;
+    case 2: e = pg::launch_score<2>(a, kv->head_dim, grid, smem, s); break;
+    case 4: e = pg::launch_score<4>(a, kv->head_dim, grid, smem, s); break;
+    case 8: e = pg::launch_score<8>(a, kv->head_dim, grid, smem, s); break;
+    default: e = pg::launch_score<16>(a, kv->head_dim, grid, smem, s); break;
+  }
   return e == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
 
@@ -516,10 +671,17 @@ extern "C" sv_status sv_select_pages(const sv_paged_kv* kv, const sv_batch* bt, 
   a.n_first = n_first;
   a.n_last = n_last;
   a.n_keep = n_keep;
-  static PerDevice set;
-  if (smem_limit_once(set, pg::select_kernel, 49152 * 4) != cudaSuccess) return SV_ERR_CUDA;
-  const cudaError_t e =
-      sv::launch(pg::select_kernel, dim3(bt->total_rows, kv->n_kv_heads), pg::kSelectThreads,
-                 (size_t)max_pages * 4, static_cast<cudaStream_t>(stream), a);
+  const dim3 grid(bt->total_rows, kv->n_kv_heads);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  static PerDevice set_many, set_few;
+  if (smem_limit_once(set_many, pg::select_kernel<256>, 49152 * 4) != cudaSuccess ||
+      smem_limit_once(set_few, pg::select_kernel<1024>, 49152 * 4) != cudaSuccess)
+    return SV_ERR_CUDA;
+  const size_t smem = (size_t)std::max(max_pages, 1) * 4;
+  // few lists leave SMs idle: more threads for each
+  const bool few = (long)bt->total_rows * kv->n_kv_heads <= sizing_sms() || max_pages > 16384;
+  e = few ? sv::launch(pg::select_kernel<1024>, grid, 1024, smem, s, a)
+          : sv::launch(pg::select_kernel<256>, grid, 256, smem, s, a);
   return e == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
