@@ -148,24 +148,92 @@ struct ScoreArgs {
 };
 
 constexpr int kScoreThreads = 128;
-constexpr int kScoreTiles = 16;  // tiles of eight virtual rows of a CTA
+constexpr int kScoreTiles = 8;  // tiles of 16 virtual rows of a CTA
 constexpr int kMaxPer = 256;
+
+// MT tiles of 16 virtual rows (from row r0 on) by a warp's 16 pages from `page`
+// on: 2 MT chains of products side by side.  A thread has of each tile the slots
+// gq and gq + 8 by the pages 2 tq, 2 tq + 1 of two eights: v[eight * 4 + half * 2
+// + odd].  The maximum over a row's G2 slots is one over lanes: at each step a
+// lane keeps half of its values and hands the other half over, so that in the
+// end every value is in one lane only.
+template <int D, int G2, int MT>
+__device__ __forceinline__ void score_tiles(const uint4 (&bd)[2][2 * D / 32], const uint4* sq,
+                                            int r0, int nr, int page, int p1, int lane,
+                                            unsigned known, float* out, size_t row_step) {
+  constexpr int kPairs = 2 * D / 32;
+  const int gq = lane >> 2, tq = lane & 3;
+  float acc[MT][2][4] = {};
+#pragma unroll
+  for (int c = 0; c < kPairs; ++c) {
+#pragma unroll
+    for (int k = 0; k < MT; ++k) {
+      const uint4 x = sq[((k * kPairs + c) * 2) * 32], y = sq[((k * kPairs + c) * 2 + 1) * 32];
+      const uint32_t ax[4] = {x.x, x.y, x.z, x.w}, ay[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt) mma16816(acc[k][nt], ax, bd[nt][c].x, bd[nt][c].y);
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt) mma16816(acc[k][nt], ay, bd[nt][c].z, bd[nt][c].w);
+    }
+  }
+  const bool b0 = gq & 1, b1 = gq & 2, b2 = gq & 4;
+  auto halve = [&](float lo, float hi, bool up, int o) {
+    return fmaxf(up ? hi : lo, __shfl_xor_sync(0xffffffffu, up ? lo : hi, o));
+  };
+  auto put = [&](int r, int at, float v) {
+    if (r < nr && page + at < p1) out[r * row_step + page + at] = (known >> at) & 1u ? v : 0.f;
+  };
+#pragma unroll
+  for (int k = 0; k < MT; ++k) {
+    const int row = r0 + k * (16 / G2);
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = acc[k][j >> 2][j & 3];
+    if (G2 == 16) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) v[j] = halve(fmaxf(v[j], v[j + 2]), fmaxf(v[4 + j], v[6 + j]), b0, 4);
+      v[0] = halve(v[0], v[1], b1, 8);
+      v[0] = fmaxf(v[0], __shfl_xor_sync(0xffffffffu, v[0], 16));
+      if (!b2) put(row, b0 * 8 + 2 * tq + b1, v[0]);
+    } else if (G2 == 1) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) put(row + gq + (j & 2) * 4, (j & 4) * 2 + 2 * tq + (j & 1), v[j]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = halve(v[j], v[j + 4], b0, 4);  // v: half * 2 + odd
+      if (G2 == 2) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) put(row + (gq >> 1) + (j & 2) * 2, b0 * 8 + 2 * tq + (j & 1), v[j]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) v[j] = halve(v[j], v[j + 2], b1, 8);
+        if (G2 == 4) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) put(row + (gq >> 2) + 2 * b1, b0 * 8 + 2 * tq + j, v[j]);
+        } else {
+          put(row + b1, b0 * 8 + 2 * tq + b2, halve(v[0], v[1], b2, 16));
+        }
+      }
+    }
+  }
+}
 
 // For a row's query head h and page t: sum_d max(q lo, q hi) = min(q, 0) . lo +
 // max(q, 0) . hi, a product of [q-, q+] with the 2 D contiguous elements [lo,
 // hi] of the page: exact bf16 factors, fp32 sums, on mma.sync m16n8k16 (16
-// pages x 8 virtual rows x 16 elements).  Virtual row v is row v / g2, head slot
-// v % g2 of it, the group's heads in the first slots and again in the rest (the
-// maximum over the slots does not see that).  The pages are the product's rows:
-// the maximum over a row's slots is then one over four neighbouring lanes.  The k
-// order of a product is free, so a lane takes 16 consecutive bytes of a page's
-// bounds as the operands of two steps: the bounds go from global memory to
-// registers without a stop, 16 pages a warp at once.
+// virtual rows x 8 pages x 16 elements).  Virtual row v is row v / G2, head slot
+// v % G2 of it, the group's heads in the first slots and some again in the rest
+// (the maximum over the slots does not see that).  The k order of a product is
+// free, so a lane takes 16 consecutive bytes of a page's bounds as the operands
+// of two steps: the bounds go from global memory to registers without a stop, 16
+// pages a warp at once (eight at once, with the next eight on their way, read q
+// from shared memory twice as often: 73 us where this takes 55).
 template <int D, int G2>
 __global__ void __launch_bounds__(kScoreThreads) score_kernel(ScoreArgs a) {
   griddep_entry();
   constexpr int kPairs = 2 * D / 32;  // 16-byte chunks a lane holds of a page, two steps each
-  extern __shared__ __align__(16) uint4 s_q[];  // [tile][pair of steps][lane]
+  constexpr int kTileRows = 16 / G2;
+  extern __shared__ __align__(16) uint4 s_q[];  // [tile][step][lane]
   __shared__ int s_tbl[kMaxPer];
   const int i = blockIdx.z / a.Hkv, g = blockIdx.z % a.Hkv;
   const Window w = window_of(a.bt, i);
@@ -180,14 +248,13 @@ __global__ void __launch_bounds__(kScoreThreads) score_kernel(ScoreArgs a) {
     if (first) flag(a.dev_status, SV_DEV_BAD_LENGTH);
     return;
   }
-  const int per_block = kScoreTiles * 8 / G2;  // rows of a CTA
-  const int r0 = w.b + blockIdx.y * per_block;
-  const int nr = min(w.e - r0, per_block);
+  const int r0 = w.b + blockIdx.y * kScoreTiles * kTileRows;
+  const int nr = min(w.e - r0, kScoreTiles * kTileRows);
   const int p0 = blockIdx.x * a.per, p1 = min(n, p0 + a.per);
   if (nr <= 0 || p0 >= p1) return;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int gq = lane >> 2, tq = lane & 3;
-  const int tiles = (nr * G2 + 7) / 8;
+  const int tiles = (nr + kTileRows - 1) / kTileRows;
   for (int p = p0 + tid; p < p1; p += kScoreThreads) {
     int b = __ldg(a.tables + (size_t)i * a.max_blocks + p);
     if (b < 0 || b >= a.num_blocks) {
@@ -196,105 +263,60 @@ __global__ void __launch_bounds__(kScoreThreads) score_kernel(ScoreArgs a) {
     }
     s_tbl[p - p0] = b;
   }
-  // [q-, q+] of the rows in the order the products take them: the lower half of
-  // the pairs is q-, the upper q+, of the same chunk of q
+  // [q-, q+] of the tiles' rows in the order the products take them: the lower
+  // half of the steps is q-, the upper q+, of the same chunks of q
   for (int x = tid; x < tiles * (kPairs / 2) * 32; x += kScoreThreads) {
-    const int l = x & 31, c = (x >> 5) % (kPairs / 2), nt = (x >> 5) / (kPairs / 2);
-    const int v = nt * 8 + (l >> 2);
-    const int r = min(v / G2, nr - 1);
-    const int h = v % G2 < a.group ? v % G2 : v % G2 - a.group;  // G2 < 2 group
-    uint4 up = __ldg(reinterpret_cast<const uint4*>(
-                  a.q + ((size_t)(w.cu + r0 + r) * a.Hq + g * a.group + h) * D) + c * 4 + (l & 3));
-    uint4 down = up;
-    const __nv_bfloat162 z = __floats2bfloat162_rn(0.f, 0.f);
+    const int l = x & 31, c = (x >> 5) % (kPairs / 2), mt = (x >> 5) / (kPairs / 2);
+    uint4 dn[2], up[2];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      __nv_bfloat162& y = reinterpret_cast<__nv_bfloat162*>(&up)[e];
-      reinterpret_cast<__nv_bfloat162*>(&down)[e] = __hmin2(y, z);
-      y = __hmax2(y, z);
+    for (int k = 0; k < 2; ++k) {
+      const int slot = (l >> 2) + 8 * k, s = slot % G2;
+      const int r = min(mt * kTileRows + slot / G2, nr - 1), h = s < a.group ? s : s - a.group;
+      up[k] = __ldg(reinterpret_cast<const uint4*>(
+                  a.q + ((size_t)(w.cu + r0 + r) * a.Hq + g * a.group + h) * D) + c * 4 + (l & 3));
+      const __nv_bfloat162 z = __floats2bfloat162_rn(0.f, 0.f);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        __nv_bfloat162& y = reinterpret_cast<__nv_bfloat162*>(&up[k])[e];
+        reinterpret_cast<__nv_bfloat162*>(&dn[k])[e] = __hmin2(y, z);
+        y = __hmax2(y, z);
+      }
     }
-    s_q[(nt * kPairs + c) * 32 + l] = down;
-    s_q[(nt * kPairs + kPairs / 2 + c) * 32 + l] = up;
+    uint4* to = s_q + (mt * kPairs + c) * 64 + l;
+    to[0] = make_uint4(dn[0].x, dn[1].x, dn[0].y, dn[1].y);
+    to[32] = make_uint4(dn[0].z, dn[1].z, dn[0].w, dn[1].w);
+    to[kPairs * 32] = make_uint4(up[0].x, up[1].x, up[0].y, up[1].y);
+    to[kPairs * 32 + 32] = make_uint4(up[0].z, up[1].z, up[0].w, up[1].w);
   }
   __syncthreads();
   float* out = a.scores + ((size_t)(w.cu + r0) * a.Hkv + g) * a.max_pages;
   const size_t row_step = (size_t)a.Hkv * a.max_pages;
-  constexpr int kRows = 8 / (G2 < 8 ? G2 : 8);  // rows of a tile
   for (int p = p0 + warp * 16; p < p1; p += (kScoreThreads / 32) * 16) {
     uint4 bd[2][kPairs];  // pages p + gq and p + gq + 8
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      const int page = p + k * 8 + gq;
-      const int b = page < p1 ? s_tbl[page - p0] : -1;
+      const int b = s_tbl[min(p + k * 8 + gq, p1 - 1) - p0];
       const uint4* src = reinterpret_cast<const uint4*>(
           a.bounds + ((size_t)max(b, 0) * a.Hkv + g) * 2 * D) + tq;
 #pragma unroll
-      for (int c = 0; c < kPairs; ++c) bd[k][c] = b >= 0 ? __ldg(src + c * 4) : make_uint4(0, 0, 0, 0);
+      for (int c = 0; c < kPairs; ++c) bd[k][c] = __ldg(src + c * 4);
     }
-    for (int nt = 0; nt < tiles; nt += 2) {
-      float acc[2][4] = {};  // pages gq, gq + 8 by virtual rows 2 tq, 2 tq + 1
-      const uint4* s0 = s_q + nt * kPairs * 32 + lane;
-      const uint4* s1 = s0 + (nt + 1 < tiles ? kPairs * 32 : 0);
-#pragma unroll
-      for (int c = 0; c < kPairs; ++c) {
-        const uint32_t ax[4] = {bd[0][c].x, bd[1][c].x, bd[0][c].y, bd[1][c].y};
-        const uint32_t ay[4] = {bd[0][c].z, bd[1][c].z, bd[0][c].w, bd[1][c].w};
-        const uint4 x = s0[c * 32], y = s1[c * 32];
-        mma16816(acc[0], ax, x.x, x.y);
-        mma16816(acc[1], ax, y.x, y.y);
-        mma16816(acc[0], ay, x.z, x.w);
-        mma16816(acc[1], ay, y.z, y.w);
-      }
-      if (G2 == 1) {  // every virtual row is a row
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int r = (nt + k) * 8 + 2 * tq + (e & 1), page = p + gq + (e >> 1) * 8;
-            if (r < nr && page < p1) out[r * row_step + page] = acc[k][e];
-          }
-        continue;
-      }
-      float lo[2], hi[2];  // pages gq, gq + 8
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        lo[k] = fmaxf(acc[k][0], acc[k][1]);
-        hi[k] = fmaxf(acc[k][2], acc[k][3]);
-      }
-      if (G2 == 16) {  // both tiles are one row's
-        lo[0] = fmaxf(lo[0], lo[1]);
-        hi[0] = fmaxf(hi[0], hi[1]);
-      }
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        if (G2 > 2) {
-          lo[k] = fmaxf(lo[k], __shfl_xor_sync(0xffffffffu, lo[k], 1));
-          hi[k] = fmaxf(hi[k], __shfl_xor_sync(0xffffffffu, hi[k], 1));
-        }
-        if (G2 > 4) {
-          lo[k] = fmaxf(lo[k], __shfl_xor_sync(0xffffffffu, lo[k], 2));
-          hi[k] = fmaxf(hi[k], __shfl_xor_sync(0xffffffffu, hi[k], 2));
-        }
-        // the lanes of a row: the first writes page gq, the second (where the row
-        // has one) page gq + 8
-        constexpr int own = G2 < 2 ? 1 : G2 < 8 ? G2 / 2 : 4;  // lanes of a row
-        const int r = G2 == 16 ? nt / 2 : (nt + k) * kRows + 2 * tq / (G2 < 8 ? G2 : 8), at = tq % own;
-        if (r >= nr || (G2 == 16 && k == 1)) continue;
-        if (own == 1) {
-          if (p + gq < p1) out[r * row_step + p + gq] = lo[k];
-          if (p + gq + 8 < p1) out[r * row_step + p + gq + 8] = hi[k];
-        } else if (at < 2 && p + gq + 8 * at < p1) {
-          out[r * row_step + p + gq + 8 * at] = at ? hi[k] : lo[k];
-        }
-      }
-    }
+    // pages whose block is in the cache
+    const unsigned known = __ballot_sync(0xffffffffu, s_tbl[min(p + (lane & 15), p1 - 1) - p0] >= 0);
+    int mt = 0;
+    for (; mt + 2 <= tiles; mt += 2)
+      score_tiles<D, G2, 2>(bd, s_q + mt * kPairs * 64 + lane, mt * kTileRows, nr, p, p1, lane, known,
+                            out, row_step);
+    if (mt < tiles)
+      score_tiles<D, G2, 1>(bd, s_q + mt * kPairs * 64 + lane, mt * kTileRows, nr, p, p1, lane, known,
+                            out, row_step);
   }
 }
 
 template <int G2>
 cudaError_t launch_score(const ScoreArgs& a, int dim, dim3 grid, size_t smem, cudaStream_t s) {
   static PerDevice set128, set64;
-  const size_t most = (size_t)kScoreTiles * 8 * 32 * 16;  // of head_dim 128
+  const size_t most = (size_t)kScoreTiles * 16 * 32 * 16;  // of head_dim 128
   cudaError_t e = dim == 128 ? smem_limit_once(set128, score_kernel<128, G2>, most)
                              : smem_limit_once(set64, score_kernel<64, G2>, most);
   if (e != cudaSuccess) return e;
@@ -628,12 +650,12 @@ extern "C" sv_status sv_score_pages(const sv_paged_kv* kv, const sv_batch* bt, c
   if (nsm < 1) return SV_ERR_CUDA;
   const long units = (long)bt->n_req * kv->n_kv_heads * max_pages;
   a.per = units <= 64L * 8 * nsm ? 64 : pg::kMaxPer;
-  const int per_block = pg::kScoreTiles * 8 / a.g2;
+  const int per_block = pg::kScoreTiles * 16 / a.g2;
   const int most_rows = std::min(bt->max_rows_per_req, bt->total_rows);
   const dim3 grid((max_pages + a.per - 1) / a.per, (most_rows + per_block - 1) / per_block,
                   bt->n_req * kv->n_kv_heads);
-  const int tiles = std::min(pg::kScoreTiles, (most_rows * a.g2 + 7) / 8);
-  const size_t smem = (size_t)tiles * (2 * kv->head_dim / 32) * 32 * 16;
+  const int tiles = std::min(pg::kScoreTiles, (most_rows * a.g2 + 15) / 16);
+  const size_t smem = (size_t)tiles * (2 * kv->head_dim / 16) * 32 * 16;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   switch (a.g2) {
