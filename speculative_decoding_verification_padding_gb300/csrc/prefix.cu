@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(pfx::kThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ int s_tbl[kUnitPages];
   __shared__ __align__(8) unsigned long long s_kfull[2], s_kfree[2], s_vfull[2], s_vfree[2],
-      s_sfull[2], s_pfull[2], s_odone[2], s_drain;
+      s_sfull[2], s_pfull[2][2], s_odone[2], s_drain;
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort, s_bad;
   __shared__ int s_issued[4];
@@ -241,7 +241,8 @@ __global__ void __launch_bounds__(pfx::kThreads, 1)
       mbar_init(smem_u32(&s_vfull[k]), 1);
       mbar_init(smem_u32(&s_vfree[k]), 1);
       mbar_init(smem_u32(&s_sfull[k]), 1);
-      mbar_init(smem_u32(&s_pfull[k]), 128);
+      mbar_init(smem_u32(&s_pfull[k][0]), 128);
+      mbar_init(smem_u32(&s_pfull[k][1]), 128);
       mbar_init(smem_u32(&s_odone[k]), 1);
     }
     mbar_init(smem_u32(&s_drain), 1);
@@ -332,14 +333,17 @@ __global__ void __launch_bounds__(pfx::kThreads, 1)
         tc5::commit(smem_u32(&s_sfull[t]));
         if (t == ntile - 1) tc5::commit(smem_u32(&s_kfree[st & 1]));
       };
-      auto pv = [&](int t, int st) {
+      // the half h of a stage's tokens: 64
+      auto pv = [&](int t, int st, int h) {
         const uint32_t sb = ring + (2 + (st & 1)) * S::kTile;
 #pragma unroll
-        for (int ks = 0; ks < kTok / 16; ++ks) {
+        for (int k = 0; k < kTok / 32; ++k) {
+          const int ks = h * (kTok / 32) + k;
           const uint64_t bd = tc5::sw128_desc(sb + ks * 2048, S::kHalf, 1024);
           tc5::mma_bf16_ts(tmem + pfx::kColO + (uint32_t)(t * 128), tmem + (uint32_t)(t * kTok) + ks * 8,
                            bd, idesc_pv, (st > 0 || ks > 0) ? 1u : 0u);
         }
+        if (h == 0) return;
         tc5::commit(smem_u32(&s_odone[t]));
         if (t == ntile - 1) tc5::commit(smem_u32(&s_vfree[st & 1]));
       };
@@ -351,13 +355,17 @@ __global__ void __launch_bounds__(pfx::kThreads, 1)
       for (int st = 0; st < n_stage && ok; ++st) {
         const uint32_t par = (uint32_t)((st >> 1) & 1);
         for (int t = 0; t < ntile && ok; ++t) {
-          // P of the tile is there (and S has been read), V has landed
-          ok = mbar_wait_bounded(smem_u32(&s_pfull[t]), (uint32_t)(st & 1)) &&
+          // the first half of the tile's P is there (and S has been read), V has landed
+          ok = mbar_wait_bounded(smem_u32(&s_pfull[t][0]), (uint32_t)(st & 1)) &&
                mbar_wait_bounded(smem_u32(&s_vfull[st & 1]), par) &&
                !*reinterpret_cast<volatile int*>(&s_abort);
           if (!ok) break;
           tc5::fence_after_sync();
-          pv(t, st);
+          pv(t, st, 0);
+          ok = mbar_wait_bounded(smem_u32(&s_pfull[t][1]), (uint32_t)(st & 1));
+          if (!ok) break;
+          tc5::fence_after_sync();
+          pv(t, st, 1);
           if (st + 1 < n_stage) {
             // the next S goes where P was: PV has to be through with it
             ok = mbar_wait_bounded(smem_u32(&s_kfull[(st + 1) & 1]), (uint32_t)(((st + 1) >> 1) & 1)) &&
@@ -389,88 +397,82 @@ __global__ void __launch_bounds__(pfx::kThreads, 1)
         break;
       }
       tc5::fence_after_sync();
-      uint32_t sa[64], sb[64];
-      tc5::tmem_ld_x64(ts, sa);
-      tc5::tmem_ld_x64(ts + 64, sb);
-      uint32_t pages = 0xffu;  // pages of the stage that are there
+      uint32_t s[kTok];
+      tc5::tmem_ld_x128(ts, s);
       if (s_bad) {
-        pages = 0u;
+        uint32_t pages = 0u;  // pages of the stage that are there
 #pragma unroll
         for (int p = 0; p < kStagePages; ++p)
           if (s_tbl[st * kStagePages + p] >= 0) pages |= 1u << p;
         if (pages != 0xffu) {
 #pragma unroll
-          for (int j = 0; j < 64; ++j) {
-            if (!((pages >> (j / 16)) & 1u)) sa[j] = __float_as_uint(-INFINITY);
-            if (!((pages >> (4 + j / 16)) & 1u)) sb[j] = __float_as_uint(-INFINITY);
+          for (int j = 0; j < kTok; ++j)
+            if (!((pages >> (j / 16)) & 1u)) s[j] = __float_as_uint(-INFINITY);
+          if (t == 0) {
+            // rows of V that were not copied may hold anything: zeros, so that
+            // their weights of 0 add nothing (tile 1's PV follows tile 0's)
+            const bool gv = mbar_wait_bounded(smem_u32(&s_vfull[st & 1]), (uint32_t)((st >> 1) & 1));
+            if (!__all_sync(0xffffffffu, gv)) {
+              ok = false;
+              break;
+            }
+            uint8_t* vb = base_ptr + (ring - base) + (2 + (st & 1)) * S::kTile;
+            for (int x = tid; x < kTok * (D / 8); x += 128) {
+              const int row = x / (D / 8), c = x % (D / 8);
+              if (!((pages >> (row / 16)) & 1u))
+                *reinterpret_cast<int4*>(vb + (c >> 3) * S::kHalf + row * 128 + (((c & 7) ^ (row & 7)) << 4)) =
+                    make_int4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
           }
         }
       }
-      float mx = -INFINITY, mx2 = -INFINITY;
+      float mx4[4];
 #pragma unroll
-      for (int j = 0; j < 64; ++j) {
-        mx = fmaxf(mx, __uint_as_float(sa[j]));
-        mx2 = fmaxf(mx2, __uint_as_float(sb[j]));
-      }
-      mx = fmaxf(mx, mx2) * sc;
+      for (int k = 0; k < 4; ++k) mx4[k] = fmaxf(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1]));
+#pragma unroll
+      for (int j = 8; j < kTok; j += 8)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          mx4[k] = fmaxf(fmaxf(mx4[k], __uint_as_float(s[j + 2 * k])), __uint_as_float(s[j + 2 * k + 1]));
+      const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * sc;
       const bool grow = mx > m_ref + 8.f;
       if (__any_sync(0xffffffffu, grow)) {
         const float m_new = grow ? mx : m_ref;
         const float alpha = grow ? ex2(m_ref - m_new) : 1.f;  // 0 while m_ref is -inf
         if (st > 0) {
 #pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
-            uint32_t ov[32];
-            tc5::tmem_ld_x32(to + c, ov);
+          for (int c = 0; c < D; c += 16) {
+            uint32_t ov[16];
+            tc5::tmem_ld_x16(to + c, ov);
 #pragma unroll
-            for (int k = 0; k < 32; ++k) ov[k] = __float_as_uint(__uint_as_float(ov[k]) * alpha);
-            tc5::tmem_st_x32(to + c, ov);
+            for (int k = 0; k < 16; ++k) ov[k] = __float_as_uint(__uint_as_float(ov[k]) * alpha);
+            tc5::tmem_st_x16(to + c, ov);
           }
         }
         l *= alpha;
         m_ref = m_new;
       }
       const float mb = m_ref == -INFINITY ? 0.f : m_ref;
-      float r0 = 0.f, r1 = 0.f;
-      uint32_t pk[32];
+      const uint64_t sc2 = pair(sc, sc), mb2 = pair(-mb, -mb);
+      uint64_t sum[4] = {0, 0, 0, 0};
 #pragma unroll
-      for (int j = 0; j < 64; j += 2) {
-        const float e0 = ex2(fmaf(__uint_as_float(sa[j]), sc, -mb));
-        const float e1 = ex2(fmaf(__uint_as_float(sa[j + 1]), sc, -mb));
-        r0 += e0;
-        r1 += e1;
-        pk[j / 2] = pack_bf16(e0, e1);
-      }
-      tc5::tmem_st_x32(ts, pk);
+      for (int h = 0; h < 2; ++h) {
+        uint32_t pk[32];
 #pragma unroll
-      for (int j = 0; j < 64; j += 2) {
-        const float e0 = ex2(fmaf(__uint_as_float(sb[j]), sc, -mb));
-        const float e1 = ex2(fmaf(__uint_as_float(sb[j + 1]), sc, -mb));
-        r0 += e0;
-        r1 += e1;
-        pk[j / 2] = pack_bf16(e0, e1);
-      }
-      tc5::tmem_st_x32(ts + 32, pk);
-      l += r0 + r1;
-      if (pages != 0xffu && t == 0) {
-        // rows of V that were not copied may hold anything: zeros, so that
-        // their weights of 0 add nothing (tile 1's PV follows tile 0's)
-        const bool gv = mbar_wait_bounded(smem_u32(&s_vfull[st & 1]), (uint32_t)((st >> 1) & 1));
-        if (!__all_sync(0xffffffffu, gv)) {
-          ok = false;
-          break;
+        for (int j = 0; j < 32; ++j) {
+          const int e = h * 64 + 2 * j;
+          const float2 x = unpair(fma2(pair(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), sc2, mb2));
+          const float e0 = ex2(x.x), e1 = ex2(x.y);
+          sum[j & 3] = add2(sum[j & 3], pair(e0, e1));
+          pk[j] = pack_bf16(e0, e1);
         }
-        uint8_t* vb = base_ptr + (ring - base) + (2 + (st & 1)) * S::kTile;
-        for (int x = tid; x < kTok * (D / 8); x += 128) {
-          const int row = x / (D / 8), c = x % (D / 8);
-          if (!((pages >> (row / 16)) & 1u))
-            *reinterpret_cast<int4*>(vb + (c >> 3) * S::kHalf + row * 128 + (((c & 7) ^ (row & 7)) << 4)) =
-                make_int4(0, 0, 0, 0);
-        }
-        fence_proxy_async_smem();
+        tc5::tmem_st_x32(ts + h * 32, pk);
+        tc5::fence_before_sync();
+        mbar_arrive(smem_u32(&s_pfull[t][h]));
       }
-      tc5::fence_before_sync();
-      mbar_arrive(smem_u32(&s_pfull[t]));
+      const float2 r = unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
+      l += r.x + r.y;
     }
     if (ok) {
       const bool g3 = mbar_wait_bounded(smem_u32(&s_drain), 0u);
