@@ -182,15 +182,17 @@ __global__ void __launch_bounds__(1024) prefix_plan_kernel(const __grid_constant
 //     rescaled in place only where a row's max grows by more than 2^8;
 //   warps 8, 9: the copies of K and V (two slots each, refilled as soon as both
 //     tiles' products have read them); warp 8 owns the tensor memory;
-//   warp 10: issues the products, tile 0's PV and next QK^T while tile 1's
-//     softmax runs and the other way round.
+//   warps 10, 11: issue the products of tile 0 and 1, one tile's PV and next QK^T
+//     while the other's softmax runs.  (One thread that issued for both spent as
+//     long on its waits and on a full queue as the tensor cores on the products:
+//     343 us for 448 rows of 64 heads behind 24576 tokens, 2XX us so.)
 // A barrier's commit covers every product issued before it, so a tile's S of a
 // stage also says that its PV of the stage before has landed.  Every wait is
 // bounded; a CTA that gives up flags SV_DEV_TIMEOUT, lets copies and products
 // land and frees its tensor memory.
 namespace pfx {
 constexpr int kTok = 128;
-constexpr int kThreads = 352;
+constexpr int kThreads = 384;
 constexpr uint32_t kCols = 512, kColO = 256;
 template <int D>
 struct Smem {
@@ -213,7 +215,7 @@ __global__ void __launch_bounds__(pfx::kThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ int s_tbl[kUnitPages];
   __shared__ __align__(8) unsigned long long s_kfull[2], s_kfree[2], s_vfull[2], s_vfree[2],
-      s_sfull[2], s_pfull[2][2], s_odone[2], s_drain;
+      s_sfull[2], s_pfull[2][2], s_odone[2], s_drain[2], s_zero[2];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort, s_bad;
   __shared__ int s_issued[4];
@@ -237,15 +239,16 @@ __global__ void __launch_bounds__(pfx::kThreads, 1)
     for (int k = 0; k < 4; ++k) s_issued[k] = -1;
     for (int k = 0; k < 2; ++k) {
       mbar_init(smem_u32(&s_kfull[k]), 1);
-      mbar_init(smem_u32(&s_kfree[k]), 1);
+      mbar_init(smem_u32(&s_kfree[k]), ntile);
       mbar_init(smem_u32(&s_vfull[k]), 1);
-      mbar_init(smem_u32(&s_vfree[k]), 1);
+      mbar_init(smem_u32(&s_vfree[k]), ntile);
       mbar_init(smem_u32(&s_sfull[k]), 1);
       mbar_init(smem_u32(&s_pfull[k][0]), 128);
       mbar_init(smem_u32(&s_pfull[k][1]), 128);
       mbar_init(smem_u32(&s_odone[k]), 1);
+      mbar_init(smem_u32(&s_drain[k]), 1);
+      mbar_init(smem_u32(&s_zero[k]), 128);
     }
-    mbar_init(smem_u32(&s_drain), 1);
     fence_mbar_init();
   }
   __syncthreads();
@@ -317,69 +320,67 @@ __global__ void __launch_bounds__(pfx::kThreads, 1)
           tma_load_2d(dst + h * S::kHalf, half ? &tmV : &tmK, 64 * h, y, bar);
       }
     }
-  } else if (warp == 10) {
+  } else if (warp >= 10) {
     // --------------------------------------------------------- MMA issue --
-    if (lane == 0) {
+    const int t = warp - 10;
+    if (lane == 0 && t < ntile) {
       constexpr uint32_t idesc_qk = tc5::idesc_bf16_f32(128, kTok, false);
       constexpr uint32_t idesc_pv = tc5::idesc_bf16_f32(128, D, true);
-      auto qk = [&](int t, int st) {
+      const uint32_t ts = tmem + (uint32_t)(t * kTok), to = tmem + pfx::kColO + (uint32_t)(t * 128);
+      auto qk = [&](int st) {
         const uint32_t sb = ring + (st & 1) * S::kTile;
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
           const uint64_t ad = tc5::sw128_desc(base + t * S::kTile + (ks >> 2) * S::kHalf + (ks & 3) * 32, 16, 1024);
           const uint64_t bd = tc5::sw128_desc(sb + (ks >> 2) * S::kHalf + (ks & 3) * 32, 16, 1024);
-          tc5::mma_bf16(tmem + (uint32_t)(t * kTok), ad, bd, idesc_qk, ks > 0 ? 1u : 0u);
+          tc5::mma_bf16(ts, ad, bd, idesc_qk, ks > 0 ? 1u : 0u);
         }
         tc5::commit(smem_u32(&s_sfull[t]));
-        if (t == ntile - 1) tc5::commit(smem_u32(&s_kfree[st & 1]));
+        tc5::commit(smem_u32(&s_kfree[st & 1]));
       };
       // the half h of a stage's tokens: 64
-      auto pv = [&](int t, int st, int h) {
+      auto pv = [&](int st, int h) {
         const uint32_t sb = ring + (2 + (st & 1)) * S::kTile;
 #pragma unroll
         for (int k = 0; k < kTok / 32; ++k) {
           const int ks = h * (kTok / 32) + k;
           const uint64_t bd = tc5::sw128_desc(sb + ks * 2048, S::kHalf, 1024);
-          tc5::mma_bf16_ts(tmem + pfx::kColO + (uint32_t)(t * 128), tmem + (uint32_t)(t * kTok) + ks * 8,
-                           bd, idesc_pv, (st > 0 || ks > 0) ? 1u : 0u);
+          tc5::mma_bf16_ts(to, ts + ks * 8, bd, idesc_pv, (st > 0 || ks > 0) ? 1u : 0u);
         }
-        if (h == 0) return;
-        tc5::commit(smem_u32(&s_odone[t]));
-        if (t == ntile - 1) tc5::commit(smem_u32(&s_vfree[st & 1]));
       };
       bool ok = mbar_wait_bounded(smem_u32(&s_kfull[0]), 0u);
       if (ok) {
         tc5::fence_after_sync();
-        for (int t = 0; t < ntile; ++t) qk(t, 0);
+        qk(0);
       }
       for (int st = 0; st < n_stage && ok; ++st) {
-        const uint32_t par = (uint32_t)((st >> 1) & 1);
-        for (int t = 0; t < ntile && ok; ++t) {
-          // the first half of the tile's P is there (and S has been read), V has landed
-          ok = mbar_wait_bounded(smem_u32(&s_pfull[t][0]), (uint32_t)(st & 1)) &&
-               mbar_wait_bounded(smem_u32(&s_vfull[st & 1]), par) &&
-               !*reinterpret_cast<volatile int*>(&s_abort);
+        // V has landed, the first half of P is there (and S has been read)
+        ok = mbar_wait_bounded(smem_u32(&s_vfull[st & 1]), (uint32_t)((st >> 1) & 1)) &&
+             mbar_wait_bounded(smem_u32(&s_pfull[t][0]), (uint32_t)(st & 1)) &&
+             !*reinterpret_cast<volatile int*>(&s_abort);
+        if (!ok) break;
+        tc5::fence_after_sync();
+        pv(st, 0);
+        const bool more = st + 1 < n_stage;
+        ok = (!more || mbar_wait_bounded(smem_u32(&s_kfull[(st + 1) & 1]), (uint32_t)(((st + 1) >> 1) & 1))) &&
+             mbar_wait_bounded(smem_u32(&s_pfull[t][1]), (uint32_t)(st & 1));
+        if (!ok) break;
+        tc5::fence_after_sync();
+        pv(st, 1);
+        tc5::commit(smem_u32(&s_odone[t]));
+        tc5::commit(smem_u32(&s_vfree[st & 1]));
+        if (more) {
+          // the next S goes where P was: PV has to be through with it
+          ok = mbar_wait_bounded(smem_u32(&s_odone[t]), (uint32_t)(st & 1));
           if (!ok) break;
           tc5::fence_after_sync();
-          pv(t, st, 0);
-          ok = mbar_wait_bounded(smem_u32(&s_pfull[t][1]), (uint32_t)(st & 1));
-          if (!ok) break;
-          tc5::fence_after_sync();
-          pv(t, st, 1);
-          if (st + 1 < n_stage) {
-            // the next S goes where P was: PV has to be through with it
-            ok = mbar_wait_bounded(smem_u32(&s_kfull[(st + 1) & 1]), (uint32_t)(((st + 1) >> 1) & 1)) &&
-                 mbar_wait_bounded(smem_u32(&s_odone[t]), (uint32_t)(st & 1));
-            if (!ok) break;
-            tc5::fence_after_sync();
-            qk(t, st + 1);
-          }
+          qk(st + 1);
         }
       }
       if (!ok) s_abort = 1;
-      // every product has landed before the CTA moves on
-      tc5::commit(smem_u32(&s_drain));
-      mbar_wait_bounded(smem_u32(&s_drain), 0);
+      // every product of the tile has landed before the CTA moves on
+      tc5::commit(smem_u32(&s_drain[t]));
+      mbar_wait_bounded(smem_u32(&s_drain[t]), 0);
     }
   } else if (warp < 4 * ntile) {
     // ----------------------------------------------------- softmax, rows --
@@ -389,6 +390,7 @@ __global__ void __launch_bounds__(pfx::kThreads, 1)
     const uint32_t to = tmem + lane_base + pfx::kColO + (uint32_t)(t * 128);
     const float sc = a.scale_log2;
     float m_ref = -INFINITY, l = 0.f;
+    uint32_t zeroed = 0u;  // parity of the incomplete stages so far in each V slot
     bool ok = true;
     for (int st = 0; st < n_stage; ++st) {
       const bool got = mbar_wait_bounded(smem_u32(&s_sfull[t]), (uint32_t)(st & 1));
@@ -408,14 +410,18 @@ __global__ void __launch_bounds__(pfx::kThreads, 1)
 #pragma unroll
           for (int j = 0; j < kTok; ++j)
             if (!((pages >> (j / 16)) & 1u)) s[j] = __float_as_uint(-INFINITY);
+          // rows of V that were not copied may hold anything: tile 0's warps make
+          // them zeros, so that their weights of 0 add nothing; tile 1 waits for it
+          // (a barrier a slot: tile 0 gets to a slot's next stage after tile 1's PV)
+          const int slot = st & 1;
+          const bool gv = t == 0 ? mbar_wait_bounded(smem_u32(&s_vfull[slot]), (uint32_t)((st >> 1) & 1))
+                                 : mbar_wait_bounded(smem_u32(&s_zero[slot]), (zeroed >> slot) & 1u);
+          if (!__all_sync(0xffffffffu, gv)) {
+            ok = false;
+            break;
+          }
+          zeroed ^= 1u << slot;
           if (t == 0) {
-            // rows of V that were not copied may hold anything: zeros, so that
-            // their weights of 0 add nothing (tile 1's PV follows tile 0's)
-            const bool gv = mbar_wait_bounded(smem_u32(&s_vfull[st & 1]), (uint32_t)((st >> 1) & 1));
-            if (!__all_sync(0xffffffffu, gv)) {
-              ok = false;
-              break;
-            }
             uint8_t* vb = base_ptr + (ring - base) + (2 + (st & 1)) * S::kTile;
             for (int x = tid; x < kTok * (D / 8); x += 128) {
               const int row = x / (D / 8), c = x % (D / 8);
@@ -424,6 +430,7 @@ __global__ void __launch_bounds__(pfx::kThreads, 1)
                     make_int4(0, 0, 0, 0);
             }
             fence_proxy_async_smem();
+            mbar_arrive(smem_u32(&s_zero[slot]));
           }
         }
       }
@@ -475,7 +482,7 @@ __global__ void __launch_bounds__(pfx::kThreads, 1)
       l += r.x + r.y;
     }
     if (ok) {
-      const bool g3 = mbar_wait_bounded(smem_u32(&s_drain), 0u);
+      const bool g3 = mbar_wait_bounded(smem_u32(&s_drain[t]), 0u);
       if (!__all_sync(0xffffffffu, g3)) ok = false;
     }
     if (!ok) {
