@@ -175,25 +175,28 @@ __global__ void __launch_bounds__(1024) prefix_plan_kernel(const __grid_constant
 // ------------------------------------------------------------ tcgen05 --
 // One CTA takes two tiles of 128 virtual rows by a run of pages, 128 tokens a
 // stage: S = Q K^T and O += P V of a tile are tcgen05.mma of 128 x 128 (S) and
-// 128 x D (O), accumulators in tensor memory: S of the tiles in columns 0 .. 255,
-// O in 256 .. 511.
+// 128 x D (O).  Tensor memory: S in columns 0 .. 127, of one tile and then the
+// other, P (bf16) of the tiles in 128 .. 191 and 192 .. 255, O in 256 .. 511.
 //   warps 0-3, 4-7: the softmax of tile 0 and 1; thread t owns row t (TMEM lane
-//     t): S to registers, running max and sum, P (bf16) back over S; O is
-//     rescaled in place only where a row's max grows by more than 2^8;
+//     t): S to registers, which frees it for the other tile, running max and sum,
+//     P in two halves; O is rescaled in place only where a row's max grows by
+//     more than 2^8;
 //   warps 8, 9: the copies of K and V (two slots each, refilled as soon as both
 //     tiles' products have read them); warp 8 owns the tensor memory;
-//   warps 10, 11: issue the products of tile 0 and 1, one tile's PV and next QK^T
-//     while the other's softmax runs.  (One thread that issued for both spent as
-//     long on its waits and on a full queue as the tensor cores on the products:
-//     343 us for 448 rows of 64 heads behind 24576 tokens, 2XX us so.)
-// A barrier's commit covers every product issued before it, so a tile's S of a
-// stage also says that its PV of the stage before has landed.  Every wait is
-// bounded; a CTA that gives up flags SV_DEV_TIMEOUT, lets copies and products
-// land and frees its tensor memory.
+//   warps 10, 11: issue the products of tile 0 and 1, the next stage's QK^T as
+//     soon as the other tile's softmax has read S, before PV of this stage.
+// (Measured for 448 rows of 64 heads behind 24576 tokens: one thread that issued
+// for both tiles spent as long on waits and a full queue as the tensor cores on
+// the products, 343 us; a thread a tile with S and P of each tile in the same
+// columns, where the next QK^T waits for PV and both tiles fall into step, 307 us;
+// columns as they are, QK^T behind PV, 290 us; QK^T before PV 263 us; with two
+// waits at once and one commit a product, 243 us: 1.49 PFLOP/s.)
+// Every wait is bounded; a CTA that gives up flags SV_DEV_TIMEOUT, lets copies and
+// products land and frees its tensor memory.
 namespace pfx {
 constexpr int kTok = 128;
 constexpr int kThreads = 384;
-constexpr uint32_t kCols = 512, kColO = 256;
+constexpr uint32_t kCols = 512, kColP = 128, kColO = 256;
 template <int D>
 struct Smem {
   static constexpr int kHalf = kTok * 128;            // 64 elements of d of 128 rows
@@ -214,8 +217,10 @@ __global__ void __launch_bounds__(pfx::kThreads, 1)
   constexpr int kHalves = D / 64;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ int s_tbl[kUnitPages];
-  __shared__ __align__(8) unsigned long long s_kfull[2], s_kfree[2], s_vfull[2], s_vfree[2],
-      s_sfull[2], s_pfull[2][2], s_odone[2], s_drain[2], s_zero[2];
+  // of a slot: K, V landed; of a tile and slot: S ready (K read), PV done (V read);
+  // of a tile: S read by its softmax, P written, every product landed
+  __shared__ __align__(8) unsigned long long s_kfull[2], s_vfull[2], s_sfull[2][2], s_odone[2][2],
+      s_sread[2], s_pfull[2], s_drain[2], s_zero[2];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort, s_bad;
   __shared__ int s_issued[4];
@@ -239,13 +244,13 @@ __global__ void __launch_bounds__(pfx::kThreads, 1)
     for (int k = 0; k < 4; ++k) s_issued[k] = -1;
     for (int k = 0; k < 2; ++k) {
       mbar_init(smem_u32(&s_kfull[k]), 1);
-      mbar_init(smem_u32(&s_kfree[k]), ntile);
       mbar_init(smem_u32(&s_vfull[k]), 1);
-      mbar_init(smem_u32(&s_vfree[k]), ntile);
-      mbar_init(smem_u32(&s_sfull[k]), 1);
-      mbar_init(smem_u32(&s_pfull[k][0]), 128);
-      mbar_init(smem_u32(&s_pfull[k][1]), 128);
-      mbar_init(smem_u32(&s_odone[k]), 1);
+      for (int j = 0; j < 2; ++j) {
+        mbar_init(smem_u32(&s_sfull[k][j]), 1);
+        mbar_init(smem_u32(&s_odone[k][j]), 1);
+      }
+      mbar_init(smem_u32(&s_sread[k]), 128);
+      mbar_init(smem_u32(&s_pfull[k]), 128);
       mbar_init(smem_u32(&s_drain[k]), 1);
       mbar_init(smem_u32(&s_zero[k]), 128);
     }
@@ -293,12 +298,15 @@ __global__ void __launch_bounds__(pfx::kThreads, 1)
   if (warp == 8 || warp == 9) {
     // --------------------------------------------------------- producers --
     const int half = warp - 8;  // 0: K, 1: V
-    unsigned long long* freeb = half ? s_vfree : s_kfree;
+    // a slot is free once both tiles' products have read it
+    unsigned long long (*freeb)[2] = half ? s_odone : s_sfull;
     unsigned long long* fullb = half ? s_vfull : s_kfull;
     for (int st = 0; st < n_stage; ++st) {
       const int slot = st & 1;
       bool go = true;
-      if (st >= 2) go = mbar_wait_bounded(smem_u32(&freeb[slot]), (uint32_t)(((st - 2) >> 1) & 1));
+      if (st >= 2)
+        for (int t = 0; t < ntile; ++t)
+          go = go && mbar_wait_bounded(smem_u32(&freeb[t][slot]), (uint32_t)(((st - 2) >> 1) & 1));
       if (!__all_sync(0xffffffffu, go)) {
         s_abort = 1;
         break;
@@ -326,56 +334,44 @@ __global__ void __launch_bounds__(pfx::kThreads, 1)
     if (lane == 0 && t < ntile) {
       constexpr uint32_t idesc_qk = tc5::idesc_bf16_f32(128, kTok, false);
       constexpr uint32_t idesc_pv = tc5::idesc_bf16_f32(128, D, true);
-      const uint32_t ts = tmem + (uint32_t)(t * kTok), to = tmem + pfx::kColO + (uint32_t)(t * 128);
-      auto qk = [&](int st) {
-        const uint32_t sb = ring + (st & 1) * S::kTile;
+      const uint32_t tp = tmem + pfx::kColP + (uint32_t)(t * 64), to = tmem + pfx::kColO + (uint32_t)(t * 128);
+      // descriptors of slot 0, first step: the address field counts 16 bytes
+      const uint64_t qd = tc5::sw128_desc(base + t * S::kTile, 16, 1024);
+      const uint64_t kd = tc5::sw128_desc(ring, 16, 1024);
+      const uint64_t vd = tc5::sw128_desc(ring + 2 * S::kTile, S::kHalf, 1024);
+      auto qk = [&](int st) -> bool {
+        // K has landed, and the softmax has read the S that was there: tile 1's of
+        // the stage before (tile 0's, if it is alone), tile 0's of this stage
+        const uint32_t kf = smem_u32(&s_kfull[st & 1]), kp = (uint32_t)((st >> 1) & 1);
+        const uint32_t sr = smem_u32(&s_sread[t == 1 ? 0 : ntile - 1]);
+        if (!(t == 0 && st == 0 ? mbar_wait_bounded(kf, kp)
+                                : mbar_wait2_bounded(kf, kp, sr, (uint32_t)((t == 1 ? st : st - 1) & 1))))
+          return false;
+        tc5::fence_after_sync();
+        const uint64_t bd = kd + (uint64_t)((st & 1) * (S::kTile >> 4));
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
-          const uint64_t ad = tc5::sw128_desc(base + t * S::kTile + (ks >> 2) * S::kHalf + (ks & 3) * 32, 16, 1024);
-          const uint64_t bd = tc5::sw128_desc(sb + (ks >> 2) * S::kHalf + (ks & 3) * 32, 16, 1024);
-          tc5::mma_bf16(ts, ad, bd, idesc_qk, ks > 0 ? 1u : 0u);
+          const uint64_t o = (uint64_t)(((ks >> 2) * S::kHalf + (ks & 3) * 32) >> 4);
+          tc5::mma_bf16(tmem, qd + o, bd + o, idesc_qk, ks > 0 ? 1u : 0u);
         }
-        tc5::commit(smem_u32(&s_sfull[t]));
-        tc5::commit(smem_u32(&s_kfree[st & 1]));
+        tc5::commit(smem_u32(&s_sfull[t][st & 1]));
+        return true;
       };
-      // the half h of a stage's tokens: 64
-      auto pv = [&](int st, int h) {
-        const uint32_t sb = ring + (2 + (st & 1)) * S::kTile;
-#pragma unroll
-        for (int k = 0; k < kTok / 32; ++k) {
-          const int ks = h * (kTok / 32) + k;
-          const uint64_t bd = tc5::sw128_desc(sb + ks * 2048, S::kHalf, 1024);
-          tc5::mma_bf16_ts(to, ts + ks * 8, bd, idesc_pv, (st > 0 || ks > 0) ? 1u : 0u);
-        }
-      };
-      bool ok = mbar_wait_bounded(smem_u32(&s_kfull[0]), 0u);
-      if (ok) {
-        tc5::fence_after_sync();
-        qk(0);
-      }
+      bool ok = qk(0);
       for (int st = 0; st < n_stage && ok; ++st) {
-        // V has landed, the first half of P is there (and S has been read)
-        ok = mbar_wait_bounded(smem_u32(&s_vfull[st & 1]), (uint32_t)((st >> 1) & 1)) &&
-             mbar_wait_bounded(smem_u32(&s_pfull[t][0]), (uint32_t)(st & 1)) &&
+        if (st + 1 < n_stage && !(ok = qk(st + 1))) break;
+        // V has landed, P is there
+        ok = mbar_wait2_bounded(smem_u32(&s_vfull[st & 1]), (uint32_t)((st >> 1) & 1),
+                                smem_u32(&s_pfull[t]), (uint32_t)(st & 1)) &&
              !*reinterpret_cast<volatile int*>(&s_abort);
         if (!ok) break;
         tc5::fence_after_sync();
-        pv(st, 0);
-        const bool more = st + 1 < n_stage;
-        ok = (!more || mbar_wait_bounded(smem_u32(&s_kfull[(st + 1) & 1]), (uint32_t)(((st + 1) >> 1) & 1))) &&
-             mbar_wait_bounded(smem_u32(&s_pfull[t][1]), (uint32_t)(st & 1));
-        if (!ok) break;
-        tc5::fence_after_sync();
-        pv(st, 1);
-        tc5::commit(smem_u32(&s_odone[t]));
-        tc5::commit(smem_u32(&s_vfree[st & 1]));
-        if (more) {
-          // the next S goes where P was: PV has to be through with it
-          ok = mbar_wait_bounded(smem_u32(&s_odone[t]), (uint32_t)(st & 1));
-          if (!ok) break;
-          tc5::fence_after_sync();
-          qk(st + 1);
-        }
+        const uint64_t bd = vd + (uint64_t)((st & 1) * (S::kTile >> 4));
+#pragma unroll
+        for (int ks = 0; ks < kTok / 16; ++ks)
+          tc5::mma_bf16_ts(to, tp + ks * 8, bd + (uint64_t)(ks * 2048 >> 4), idesc_pv,
+                           (st > 0 || ks > 0) ? 1u : 0u);
+        tc5::commit(smem_u32(&s_odone[t][st & 1]));
       }
       if (!ok) s_abort = 1;
       // every product of the tile has landed before the CTA moves on
@@ -386,14 +382,21 @@ __global__ void __launch_bounds__(pfx::kThreads, 1)
     // ----------------------------------------------------- softmax, rows --
     const int t = warp >> 2;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t ts = tmem + lane_base + (uint32_t)(t * kTok);
+    const uint32_t ts = tmem + lane_base, tp = ts + pfx::kColP + (uint32_t)(t * 64);
     const uint32_t to = tmem + lane_base + pfx::kColO + (uint32_t)(t * 128);
     const float sc = a.scale_log2;
     float m_ref = -INFINITY, l = 0.f;
+    // PV of the stage before has landed: O may be rescaled, P overwritten
+    auto pv_done = [&](int st) -> bool {
+      const bool got = st == 0 || mbar_wait_bounded(smem_u32(&s_odone[t][(st - 1) & 1]), (uint32_t)(((st - 1) >> 1) & 1));
+      if (!__all_sync(0xffffffffu, got)) return false;
+      tc5::fence_after_sync();
+      return true;
+    };
     uint32_t zeroed = 0u;  // parity of the incomplete stages so far in each V slot
     bool ok = true;
     for (int st = 0; st < n_stage; ++st) {
-      const bool got = mbar_wait_bounded(smem_u32(&s_sfull[t]), (uint32_t)(st & 1));
+      const bool got = mbar_wait_bounded(smem_u32(&s_sfull[t][st & 1]), (uint32_t)((st >> 1) & 1));
       if (!__all_sync(0xffffffffu, got)) {
         ok = false;
         break;
@@ -401,6 +404,8 @@ __global__ void __launch_bounds__(pfx::kThreads, 1)
       tc5::fence_after_sync();
       uint32_t s[kTok];
       tc5::tmem_ld_x128(ts, s);
+      tc5::fence_before_sync();
+      mbar_arrive(smem_u32(&s_sread[t]));
       if (s_bad) {
         uint32_t pages = 0u;  // pages of the stage that are there
 #pragma unroll
@@ -447,6 +452,10 @@ __global__ void __launch_bounds__(pfx::kThreads, 1)
       if (__any_sync(0xffffffffu, grow)) {
         const float m_new = grow ? mx : m_ref;
         const float alpha = grow ? ex2(m_ref - m_new) : 1.f;  // 0 while m_ref is -inf
+        if (!pv_done(st)) {
+          ok = false;
+          break;
+        }
         if (st > 0) {
 #pragma unroll 1
           for (int c = 0; c < D; c += 16) {
@@ -474,10 +483,15 @@ __global__ void __launch_bounds__(pfx::kThreads, 1)
           sum[j & 3] = add2(sum[j & 3], pair(e0, e1));
           pk[j] = pack_bf16(e0, e1);
         }
-        tc5::tmem_st_x32(ts + h * 32, pk);
-        tc5::fence_before_sync();
-        mbar_arrive(smem_u32(&s_pfull[t][h]));
+        if (h == 0 && !pv_done(st)) {
+          ok = false;
+          break;
+        }
+        tc5::tmem_st_x32(tp + h * 32, pk);
       }
+      if (!ok) break;
+      tc5::fence_before_sync();
+      mbar_arrive(smem_u32(&s_pfull[t]));
       const float2 r = unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
       l += r.x + r.y;
     }

@@ -323,6 +323,16 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity,
     if (mbar_try_wait(bar, parity)) return true;
   return false;
 }
+// Both phases at once: the second is asked for while the first answer is on its
+// way (an answer takes a while when the tensor cores read shared memory).
+__device__ __forceinline__ bool mbar_wait2_bounded(uint32_t bar0, uint32_t parity0, uint32_t bar1,
+                                                   uint32_t parity1) {
+  for (int it = 0; it < kWaitLimit; ++it) {
+    const bool a = mbar_try_wait(bar0, parity0), b = mbar_try_wait(bar1, parity1);
+    if (a && b) return true;
+  }
+  return false;
+}
 // The same wait for a thread with nothing else to do: each try may suspend it
 // for up to 50 us while the phase is incomplete, instead of spinning; at
 // most 40000 tries (2 s) before it gives up.
