@@ -20,7 +20,6 @@ namespace sv {
 namespace pu {
 
 constexpr int kUnitPages = 1024;   // pages of a prefix unit at most (block ids in shared memory)
-constexpr int kStagePages = 8;     // pages of a prefix stage (128 tokens)
 
 __global__ void __launch_bounds__(1024) prefix_plan_kernel(const __grid_constant__ Args a, int nsm) {
   griddep_entry();
@@ -60,7 +59,7 @@ __global__ void __launch_bounds__(1024) prefix_plan_kernel(const __grid_constant
         nt = (rows + a.rt - 1) / a.rt;
         for (int k = 0; k < nt; ++k) {
           const int last = min(w.b + (k + 1) * a.rt, w.e);
-          stages += ((ctx + last + kBlockSize - 1) / kBlockSize - first + 3) / 4;
+          stages += ((ctx + last + kBlockSize - 1) / kBlockSize - first + kStagePages - 1) / kStagePages;
         }
       }
     }
@@ -83,7 +82,7 @@ __global__ void __launch_bounds__(1024) prefix_plan_kernel(const __grid_constant
       t.arow = arow + k * a.rt;
       t.grp = grp;
       a.tiles[at + k] = t;
-      for (int g = 0; g < a.Hkv; ++g, stage += (t.nent + 3) / 4)
+      for (int g = 0; g < a.Hkv; ++g, stage += (t.nent + kStagePages - 1) / kStagePages)
         a.off[(size_t)(at + k) * a.Hkv + g] = stage;
     }
   }
@@ -194,7 +193,6 @@ __global__ void __launch_bounds__(1024) prefix_plan_kernel(const __grid_constant
 // Every wait is bounded; a CTA that gives up flags SV_DEV_TIMEOUT, lets copies and
 // products land and frees its tensor memory.
 namespace pfx {
-constexpr int kTok = 128;
 constexpr int kThreads = 384;
 constexpr uint32_t kCols = 512, kColP = 128, kColO = 256;
 template <int D>
@@ -212,7 +210,6 @@ __global__ void __launch_bounds__(pfx::kThreads, 1)
     prefix_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap tmK,
                   const __grid_constant__ CUtensorMap tmV) {
   griddep_entry();
-  using pfx::kTok;
   using S = pfx::Smem<D>;
   constexpr int kHalves = D / 64;
   extern __shared__ __align__(1024) uint8_t smem_raw[];

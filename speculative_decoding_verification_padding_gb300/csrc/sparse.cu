@@ -7,10 +7,10 @@
 //
 // Launches:
 //   plan   (1 CTA) checks the requests and cuts their rows into tiles of up to
-//          64 virtual rows;
+//          128 virtual rows;
 //   build  (1 CTA a (tile, KV head)) the union of the rows' page lists as block
-//          ids with a mask of the rows that see each, in page order: a page that
-//          several rows of a tile chose is read once.  The last CTA deals the
+//          ids, in page order, with a bit a row and entry for who sees it: a page
+//          that several rows of a tile chose is read once.  The last CTA deals the
 //          lists' stages out;
 //   units, merge (sv_page_units.cuh).
 
@@ -106,15 +106,14 @@ __global__ void __launch_bounds__(kBuildThreads) build_kernel(const __grid_const
   __syncthreads();
   const int U = s_carry;
   int* blk = a.blk + (size_t)x * a.cap;
-  unsigned long long* mask = a.mask + (size_t)x * a.cap;
+  uint32_t* see = a.see + (size_t)x * a.rt * (a.cap / 32);
   const int32_t* table = a.tables + (size_t)tl.i * a.max_blocks;
   for (int y = tid; y < words; y += kBuildThreads) {
     uint32_t bits = s_bits[y];
-    for (int pos = (int)s_before[y]; bits; bits &= bits - 1, ++pos) {
+    for (int pos = (int)s_before[y]; bits; bits &= bits - 1, ++pos)
       blk[pos] = __ldg(table + y * 32 + __ffs(bits) - 1);
-      mask[pos] = 0ull;
-    }
   }
+  for (int y = tid; y < tl.nr * (a.cap / 32); y += kBuildThreads) see[y] = 0u;
   const int ntail = (tl.ctx + tl.r0 + tl.nr + kBlockSize - 1) / kBlockSize - n;
   for (int k = tid; k < ntail; k += kBuildThreads) blk[U + k] = __ldg(table + n + k);
   __syncthreads();
@@ -123,7 +122,7 @@ __global__ void __launch_bounds__(kBuildThreads) build_kernel(const __grid_const
     for (int k = lane; k < s_len[r]; k += 32) {
       const int v = __ldg(list + k);
       const int pos = (int)s_before[v >> 5] + __popc(s_bits[v >> 5] & ((1u << (v & 31)) - 1u));
-      atomicOr(mask + pos, 1ull << r);
+      atomicOr(see + (size_t)r * (a.cap / 32) + (pos >> 5), 1u << (pos & 31));
     }
   }
   if (tid == 0) {
@@ -137,7 +136,7 @@ __global__ void __launch_bounds__(kBuildThreads) build_kernel(const __grid_const
   // every list is known: their first stages, and the CTAs' shares
   for (int base = 0; base < lists; base += kBuildThreads) {
     const int y = base + tid;
-    const int v = y < lists ? (__ldcg(a.cnt + 2 * y + 1) + 3) / 4 : 0;
+    const int v = y < lists ? (__ldcg(a.cnt + 2 * y + 1) + kStagePages - 1) / kStagePages : 0;
     const int at = block_scan(v, s_warp, &s_carry);
     if (y < lists) a.off[y] = at;
   }
@@ -152,10 +151,10 @@ inline Args page_args(const sv_paged_kv* kv, const sv_batch* bt, int32_t Hq, int
   a.n_keep = n_keep;
   // the rows' pages, and a tail of at most (15 + 128 + 15) / 16 pages
   const long most = std::min((long)kv->max_blocks_per_req, (long)a.rt * n_keep) + 9;
-  a.cap = (int)((most + 3) / 4 * 4);
+  a.cap = (int)((most + 31) / 32 * 32);
   const size_t lists = (size_t)a.tiles_cap * a.Hkv;
   a.blk = take<int>(at, off, lists * a.cap);
-  a.mask = take<unsigned long long>(at, off, lists * a.cap);
+  a.see = take<uint32_t>(at, off, lists * a.rt * (a.cap / 32));
   a.cnt = take<int>(at, off, lists * 2);
   return a;
 }
@@ -205,7 +204,7 @@ extern "C" sv_status sv_page_attend(const sv_paged_kv* kv, const sv_batch* bt, c
   if (st != SV_OK) return st;
   if (bt->n_req == 0 || bt->total_rows == 0) return SV_OK;
   if (!q || !out || !ws || (n_keep > 0 && !pages)) return SV_ERR_INVALID_ARGUMENT;
-  if (((uintptr_t)q | (uintptr_t)out) & 3) return SV_ERR_INVALID_ARGUMENT;
+  if (((uintptr_t)q & 15) || ((uintptr_t)out & 3)) return SV_ERR_INVALID_ARGUMENT;
   if ((uintptr_t)ws & 255) return SV_ERR_INVALID_ARGUMENT;
   if (!(softmax_scale > 0.f)) return SV_ERR_INVALID_ARGUMENT;
   size_t need = 0;

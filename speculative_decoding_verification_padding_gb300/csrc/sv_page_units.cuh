@@ -1,32 +1,31 @@
 // sv_page_units.cuh — attention of tiles of draft rows over lists of pages, and
 // the merge of its parts: what sv_page_attend and sv_prefix_attend share.
 //
-// A tile is up to 64 virtual rows (query rows x GQA group) of one request.  For
+// A tile is up to 128 virtual rows (query rows x GQA group) of one request.  For
 // every (tile, KV head) there is a list of cache pages: complete pages of the
-// context first, of which each row sees all or none of the slots (a bit of the
-// page's row mask), then the tail, the pages from the one that holds slot ctx
-// on, whose slots a row sees up to the context's end and where its ancestors
-// lie.  The lists are cut into stages of four pages; all stages of a call, in
-// (tile, KV head) order, are dealt out evenly to C CTAs, so that a CTA's share
-// is one run of stages over one or several lists.  A list that lies in one
-// CTA's share is written to the output there; the parts of the others meet in
-// merge_kernel.  Part c of list x has the slot c + x: the runs and the lists
-// both only move on, so no two parts share a slot and C + lists slots do.
+// context first, of which each row sees all or none of the slots, then the tail,
+// the pages from the one that holds slot ctx on, whose slots a row sees up to the
+// context's end and where its ancestors lie.  The lists are cut into stages of
+// eight pages; all stages of a call, in (tile, KV head) order, are dealt out
+// evenly to C CTAs, so that a CTA's share is one run of stages over one or several
+// lists.  A list that lies in one CTA's share is written to the output there; the
+// parts of the others meet in merge_kernel.  Part c of list x has the slot c + x:
+// the runs and the lists both only move on, so no two parts share a slot and C +
+// lists slots do.
 #pragma once
 
 #include <algorithm>
 
 #include "sv_attend_common.cuh"
 #include "sv_internal.cuh"
+#include "sv_tcgen05.cuh"
 
 namespace sv {
 namespace pu {
 
-constexpr int kTB = 64;         // tokens of a stage (four pages)
-constexpr int kStages = 3;      // TMA ring depth
-constexpr int kThreads = 128;   // four warps
-constexpr int kTileRows = 64;   // virtual rows of a tile
-constexpr int kIds = 8;         // stages whose block ids and masks wait in shared memory
+constexpr int kTok = 128;        // tokens of a stage
+constexpr int kStagePages = 8;   // pages of a stage
+constexpr int kTileRows = 128;   // virtual rows of a tile
 
 struct __align__(16) Tile {
   int i, cu, ctx, r0;      // request, its first packed row, context, first local row
@@ -68,9 +67,9 @@ struct Args {
   // page lists (sv_page_attend)
   const int32_t* pages;
   int n_keep;
-  int cap;            // entries of a list, a multiple of four
+  int cap;            // entries of a list, a multiple of 32
   int* blk;           // [lists][cap]
-  unsigned long long* mask;  // [lists][cap]
+  uint32_t* see;      // [lists][rt][cap / 32] pages a row sees, a bit an entry
   int* cnt;           // [lists][2] complete pages, all entries
   // shared prefix (sv_prefix_attend)
   int n_groups;
@@ -160,102 +159,6 @@ __device__ __forceinline__ int block_scan(int v, int* s_warp, int* carry) {
 
 // ------------------------------------------------------------------ units --
 
-template <int D>
-struct Frag {
-  float o[D / 8][4];
-  float m_a, m_b, l_a, l_b;
-};
-
-// NT * 8 tokens from stage row s0 on for this warp's two rows; bit t of vis_*
-// says whether the row sees token t of the stage.
-template <int D, int NT>
-__device__ __forceinline__ void slice_compute(Frag<D>& f, const uint32_t (&qf)[D / 16][4],
-                                              uint32_t kbase, uint32_t vbase, int s0,
-                                              unsigned long long vis_a, unsigned long long vis_b,
-                                              float scale_log2, int lane) {
-  using SL = attn::StageLayout<D>;
-  const int tq = lane & 3;
-  float sc[NT][4];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
-#pragma unroll
-    for (int ks = 0; ks < D / 16; ks += 2) {
-      const int trow = s0 + nt * 8 + (lane & 7);
-      const int chunk = 2 * ks + (lane >> 3);
-      uint32_t r[4];
-      ldsm_x4(r, kbase + SL::off(trow, chunk));
-      mma16816(sc[nt], qf[ks], r[0], r[1]);
-      mma16816(sc[nt], qf[ks + 1], r[2], r[3]);
-    }
-  }
-  constexpr uint32_t kAll = NT == 4 ? 0xffffffffu : (1u << (NT * 8 & 31)) - 1u;
-  const uint32_t va = (uint32_t)(vis_a >> s0) & kAll, vb = (uint32_t)(vis_b >> s0) & kAll;
-  const bool need_mask = __any_sync(0xffffffffu, va != kAll || vb != kAll);
-  float mx_a = -INFINITY, mx_b = -INFINITY;
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      float v = sc[nt][e] * scale_log2;
-      if (need_mask && !(((e < 2 ? va : vb) >> (nt * 8 + 2 * tq + (e & 1))) & 1u)) v = -INFINITY;
-      sc[nt][e] = v;
-      if (e < 2) mx_a = fmaxf(mx_a, v); else mx_b = fmaxf(mx_b, v);
-    }
-  }
-  mx_a = fmaxf(mx_a, __shfl_xor_sync(0xffffffffu, mx_a, 1));
-  mx_a = fmaxf(mx_a, __shfl_xor_sync(0xffffffffu, mx_a, 2));
-  mx_b = fmaxf(mx_b, __shfl_xor_sync(0xffffffffu, mx_b, 1));
-  mx_b = fmaxf(mx_b, __shfl_xor_sync(0xffffffffu, mx_b, 2));
-  const float nm_a = fmaxf(f.m_a, mx_a), nm_b = fmaxf(f.m_b, mx_b);
-  const float base_a = nm_a == -INFINITY ? 0.f : nm_a;
-  const float base_b = nm_b == -INFINITY ? 0.f : nm_b;
-  const float al_a = ex2(f.m_a - base_a), al_b = ex2(f.m_b - base_b);
-  f.m_a = nm_a;
-  f.m_b = nm_b;
-  float ps_a = 0.f, ps_b = 0.f;
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    sc[nt][0] = ex2(sc[nt][0] - base_a);
-    sc[nt][1] = ex2(sc[nt][1] - base_a);
-    sc[nt][2] = ex2(sc[nt][2] - base_b);
-    sc[nt][3] = ex2(sc[nt][3] - base_b);
-    ps_a += sc[nt][0] + sc[nt][1];
-    ps_b += sc[nt][2] + sc[nt][3];
-  }
-  f.l_a = f.l_a * al_a + ps_a;
-  f.l_b = f.l_b * al_b + ps_b;
-  // a row's factor is 1 once its maximum has settled: O is then left alone
-  if (__any_sync(0xffffffffu, al_a != 1.f || al_b != 1.f)) {
-#pragma unroll
-    for (int dn = 0; dn < D / 8; ++dn) {
-      f.o[dn][0] *= al_a;
-      f.o[dn][1] *= al_a;
-      f.o[dn][2] *= al_b;
-      f.o[dn][3] *= al_b;
-    }
-  }
-  // P is rounded to bf16 for the tensor cores (2^-9 of each weight at most, in
-  // the sum of many; the normaliser keeps fp32)
-#pragma unroll
-  for (int kk = 0; kk < NT / 2; ++kk) {
-    uint32_t pa[4];
-    pa[0] = pack_bf16(sc[2 * kk][0], sc[2 * kk][1]);
-    pa[1] = pack_bf16(sc[2 * kk][2], sc[2 * kk][3]);
-    pa[2] = pack_bf16(sc[2 * kk + 1][0], sc[2 * kk + 1][1]);
-    pa[3] = pack_bf16(sc[2 * kk + 1][2], sc[2 * kk + 1][3]);
-#pragma unroll
-    for (int dn = 0; dn < D / 8; dn += 2) {
-      const int trow = s0 + 16 * kk + (lane & 7) + ((lane >> 3) & 1) * 8;
-      const int chunk = dn + (lane >> 4);
-      uint32_t r[4];
-      ldsm_x4_t(r, vbase + SL::off(trow, chunk));
-      mma16816(f.o[dn], pa, r[0], r[1]);
-      mma16816(f.o[dn + 1], pa, r[2], r[3]);
-    }
-  }
-}
-
 // Slots m0 .. m0 + 15 relative to the context's end that a row sees: those
 // before it, and its ancestors-or-self (bits of mk1:mk0).
 __device__ __forceinline__ uint32_t tail_visible(int m0, unsigned long long mk0,
@@ -267,304 +170,526 @@ __device__ __forceinline__ uint32_t tail_visible(int m0, unsigned long long mk0,
   return ((uint32_t)(mk0 << -m0) | ((1u << -m0) - 1u)) & 0xffffu;
 }
 
+// One CTA an SM works through its share as one sequence of stages, n = 0, 1, ...
+// over all its lists (L = 0, 1, ...), so that the copies and products of a list
+// begin while the one before is still being finished:
+//   warps 0-3: the softmax; thread t owns row t of the tile (TMEM lane t): S to
+//     registers, what the row does not see masked, running max and sum, P (bf16)
+//     back over S; O is rescaled only where a row's max grows by more than 2^8; at
+//     a list's end O to the output or to a part;
+//   warp 4: the copies of Q and K, warp 5 of V (two slots each);
+//   warp 6: one thread issues S = Q K^T (128 x 128) and O += P V (128 x D) as
+//     tcgen05.mma, QK^T of the next stage before PV of this one;
+//   warp 7: reads the lists ahead (a ring of kLists records in shared memory).
+// Tensor memory: S of two stages in columns 0 .. 255, O of two lists in 256 .. 511.
+// Bound by the pages' bytes: a stage of 64 KB (head_dim 128) is 1.5 us of one SM's
+// share of HBM, its products 0.7 us, its softmax 0.6 us.
+// Every wait is bounded; a CTA that gives up flags SV_DEV_TIMEOUT, lets copies and
+// products land and frees its tensor memory.
+namespace unit {
+constexpr int kThreads = 256;
+constexpr int kLists = 4;
+constexpr uint32_t kCols = 512, kColO = 256;
+template <int D>
+struct Smem {
+  static constexpr int kHalf = kTok * 128;         // 64 elements of d of 128 rows
+  static constexpr int kTile = D / 64 * kHalf;     // Q of a list; K or V of a stage
+  static constexpr int kBytes = 6 * kTile + 1024;  // two each
+  // one CTA an SM: two would ask for more tensor memory than there is
+  static constexpr int kAsk = kBytes > 120 * 1024 ? kBytes : 120 * 1024;
+};
+// A list's part in the share.
+struct Rec {
+  int x, g, n_stage, e_first;   // n_stage 0: the end
+  int i, row0, nr, ctx;         // request; first packed row of the tile, its rows
+  int first, ncomp, nent, lim;  // staged rows up to which slots are written
+  int whole, bad, r0, grp;      // all of the list; some block outside the cache
+};
+}  // namespace unit
+
 template <int D, bool SPARSE>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(unit::kThreads, 1)
     unit_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap tmK,
-                const __grid_constant__ CUtensorMap tmV) {
+                const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmQ) {
   griddep_entry();
-  using SL = attn::StageLayout<D>;
+  using unit::kLists;
+  using unit::Rec;
+  using S = unit::Smem<D>;
+  constexpr int kHalves = D / 64;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
+  __shared__ Rec s_rec[kLists];
+  __shared__ ulonglong2 s_anc[kLists][kTileRows];  // ancestors-or-self of the tile's rows
+  __shared__ int s_ids[kLists][kStagePages];       // blocks of a list's first stage
   __shared__ int s_par[kMaxRows];
-  __shared__ unsigned long long s_anc[kTileRows][2];
-  __shared__ int s_id[kIds][4];
-  __shared__ unsigned long long s_row[kIds][4];  // rows that see the page
-  __shared__ __align__(8) unsigned long long s_full[kStages];
+  // records there / free; K, V landed; S ready (K read), PV done (V read), P written
+  // of a stage's slot; Q landed, O read of a list's
+  __shared__ __align__(8) unsigned long long s_lfull[kLists], s_lfree[kLists], s_kfull[2], s_vfull[2],
+      s_sfull[2], s_odone[2], s_pfull[2], s_qfull[2], s_ofree[2], s_drain;
+  __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
+  __shared__ int s_issued[6];  // phases begun of s_kfull, s_vfull, s_qfull
   const int W = a.hdr->W, C = a.hdr->C;
   const int c = blockIdx.x;
   if (c >= C) return;
-  const int s_end = share_start(c + 1, W, C);
-  int s_at = share_start(c, W, C);
-  int x = a.start[c];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int gq = lane >> 2, tq = lane & 3;
-  const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  uint8_t* ring_ptr = smem_raw + (ring - smem_u32(smem_raw));
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  uint8_t* base_ptr = smem_raw + (base - smem_u32(smem_raw));
+  const uint32_t ring = base + 2 * S::kTile;  // Q of two lists, then K slots, V slots
   if (tid == 0) {
     s_abort = 0;
-    for (int k = 0; k < kStages; ++k) mbar_init(smem_u32(&s_full[k]), 4);
+    for (int k = 0; k < 6; ++k) s_issued[k] = 0;
+    for (int k = 0; k < kLists; ++k) {
+      mbar_init(smem_u32(&s_lfull[k]), 1);
+      mbar_init(smem_u32(&s_lfree[k]), 7);  // four softmax warps, two producers, the issuing thread
+    }
+    for (int k = 0; k < 2; ++k) {
+      mbar_init(smem_u32(&s_kfull[k]), 1);
+      mbar_init(smem_u32(&s_vfull[k]), 1);
+      mbar_init(smem_u32(&s_sfull[k]), 1);
+      mbar_init(smem_u32(&s_odone[k]), 1);
+      mbar_init(smem_u32(&s_pfull[k]), 128);
+      mbar_init(smem_u32(&s_qfull[k]), 1);
+      mbar_init(smem_u32(&s_ofree[k]), 128);
+    }
+    mbar_init(smem_u32(&s_drain), 1);
     fence_mbar_init();
   }
-  int it = 0;  // stages issued to the ring by earlier lists of this share
-  for (; s_at < s_end; ++x) {
-    const int off0 = a.off[x], off1 = a.off[x + 1];
-    const int e_first = 4 * (s_at - off0);  // first entry of the list in this share
-    const int n_stage = min(s_end, off1) - s_at;
-    if (n_stage <= 0) continue;  // an empty list
-    const bool whole = s_at == off0 && s_at + n_stage == off1;
-    s_at += n_stage;
-    const int g = x % a.Hkv;
-    const Tile tl = a.tiles[x / a.Hkv];
-    const int ncomp = SPARSE ? a.cnt[2 * x] : tl.ncomp;
-    const int nent = SPARSE ? a.cnt[2 * x + 1] : tl.nent;
-    const int group = a.group, Mu = tl.nr * group;
-    const int tail0 = tl.ctx / kBlockSize * kBlockSize - tl.ctx;  // first tail slot
-    const int lim = tl.r0 + tl.nr;  // staged rows that may be attended
-    const bool tail = min(nent, e_first + 4 * n_stage) > ncomp;
+  if (warp == 4) {
+    tc5::tmem_alloc(smem_u32(&s_tmem), unit::kCols);
+    tc5::tmem_relinquish();
+  }
+  tc5::fence_before_sync();
+  __syncthreads();
+  tc5::fence_after_sync();
+  const uint32_t tmem = s_tmem;
+  auto gone = [&] { return *reinterpret_cast<volatile int*>(&s_abort) != 0; };
+  // the record of list L, by a whole warp (or by one thread); null: gave up
+  auto list_at = [&](int L) -> const Rec* {
+    if (!mbar_wait_bounded(smem_u32(&s_lfull[L % kLists]), (uint32_t)((L / kLists) & 1))) return nullptr;
+    return &s_rec[L % kLists];
+  };
+  auto list_done = [&](int L) { mbar_arrive(smem_u32(&s_lfree[L % kLists])); };
+  // block of entry e of a list, -1 past its end or outside the cache
+  auto block_of = [&](const Rec& r, int e) {
+    if (e >= r.nent) return -1;
+    const int b = SPARSE ? __ldg(a.blk + (size_t)r.x * a.cap + e)
+                         : __ldg(a.tables + (size_t)r.i * a.max_blocks + r.first + e);
+    return b >= 0 && b < a.num_blocks ? b : -1;
+  };
 
-    // block ids (and row masks) of stage st, entry p: thread p loads them
-    auto entry_id = [&](int st) {
-      const int e = e_first + 4 * st + (tid & 3);
-      int b = -1;
-      if (st < n_stage && e < nent) {
-        b = SPARSE ? __ldg(a.blk + (size_t)x * a.cap + e)
-                   : __ldg(a.tables + (size_t)tl.i * a.max_blocks + tl.first + e);
-        if (b < 0 || b >= a.num_blocks) {
-          flag(a.dev_status, SV_DEV_BAD_BLOCK_ID);
-          b = -1;
+  if (warp == 7) {
+    // ------------------------------------------------------- lists ahead --
+    const int s_end = share_start(c + 1, W, C);
+    int s_at = share_start(c, W, C), x = a.start[c], L = 0;
+    bool ok = true;
+    for (;; ++x) {
+      Rec r{};
+      if (s_at < s_end) {
+        const int off0 = a.off[x], off1 = a.off[x + 1];
+        r.n_stage = min(s_end, off1) - s_at;
+        if (r.n_stage <= 0) continue;  // an empty list
+        const Tile tl = a.tiles[x / a.Hkv];
+        r.x = x;
+        r.g = x % a.Hkv;
+        r.e_first = kStagePages * (s_at - off0);
+        r.whole = s_at == off0 && s_at + r.n_stage == off1;
+        r.i = tl.i;
+        r.row0 = tl.cu + tl.r0;
+        r.nr = tl.nr;
+        r.ctx = tl.ctx;
+        r.first = tl.first;
+        r.ncomp = SPARSE ? a.cnt[2 * x] : tl.ncomp;
+        r.nent = SPARSE ? a.cnt[2 * x + 1] : tl.nent;
+        r.lim = tl.r0 + tl.nr;
+        r.r0 = tl.r0;
+        r.grp = tl.grp;
+        s_at += r.n_stage;
+        if (L >= kLists &&
+            !mbar_wait_bounded(smem_u32(&s_lfree[L % kLists]), (uint32_t)((L / kLists - 1) & 1)))
+          ok = false;
+        if (!__all_sync(0xffffffffu, ok) || __any_sync(0xffffffffu, gone())) {
+          ok = false;
+          break;
         }
-      }
-      return b;
-    };
-    auto entry_rows = [&](int st) {
-      const int e = e_first + 4 * st + (tid & 3);
-      if (!SPARSE || st >= n_stage || e >= ncomp) return ~0ull;
-      return __ldg(a.mask + (size_t)x * a.cap + e);
-    };
-    __syncthreads();  // the list before is done with the shared arrays
-    if (tid < 4 * kStages) {
-      s_id[tid >> 2][tid & 3] = entry_id(tid >> 2);
-      s_row[tid >> 2][tid & 3] = entry_rows(tid >> 2);
-    }
-    if (tail)
-      for (int j = tid; j < tl.rows; j += kThreads) s_par[j] = a.bt.parent[tl.cu + j];
-    fence_proxy_async_smem();  // the ring held parts of the list before
-    __syncthreads();
-    // lane 0 of warp p copies page p of a stage and announces its bytes
-    auto issue = [&](int st) {
-      if (lane != 0 || st >= n_stage) return;
-      const int slot = (it + st) % kStages;
-      const uint32_t bar = smem_u32(&s_full[slot]);
-      const uint32_t kdst = ring + slot * SL::kStageBytes;
-      const int b = s_id[st % kIds][warp];
-      mbar_arrive_expect_tx(bar, b >= 0 ? 2u * SL::kHalves * SL::kBoxBytes : 0u);
-      if (b < 0) return;
-      const int y = (b * a.Hkv + g) * kBlockSize;
-#pragma unroll
-      for (int h = 0; h < SL::kHalves; ++h) {
-        const uint32_t o = (uint32_t)((warp * SL::kHalves + h) * SL::kBoxBytes);
-        tma_load_2d(kdst + o, &tmK, 64 * h, y, bar);
-        tma_load_2d(kdst + SL::kTensorBytes + o, &tmV, 64 * h, y, bar);
-      }
-    };
-#pragma unroll
-    for (int st = 0; st < kStages - 1; ++st) issue(st);
-    if (tail) {
-      for (int t = tid; t < tl.nr; t += kThreads) {
-        unsigned long long lo = 0ull, hi = 0ull;
-        int m = tl.r0 + t;
-        for (int steps = 0; m >= 0 && steps <= kMaxRows; ++steps) {  // parents were checked
-          if (m < 64) lo |= 1ull << m; else hi |= 1ull << (m - 64);
-          m = s_par[m];
+        const int e_end = min(r.nent, r.e_first + r.n_stage * kStagePages);
+        bool bad = false;
+        for (int e = r.e_first + lane; e < e_end; e += 32) {
+          const int b = block_of(r, e);
+          bad |= b < 0;
+          if (e < r.e_first + kStagePages) s_ids[L % kLists][e - r.e_first] = b;
         }
-        s_anc[t][0] = lo;
-        s_anc[t][1] = hi;
-      }
-      __syncthreads();
-    }
-
-    // m-tile mt and token slice ts of TS of this warp
-    const int MT = (Mu + 15) >> 4;
-    const int TS = MT == 1 ? 4 : MT == 2 ? 2 : 1;
-    const int mt = MT == 3 ? warp : warp % MT;
-    const int ts = MT == 3 ? 0 : warp / MT;
-    const bool active = mt < MT;
-    const int vl_a = mt * 16 + gq, vl_b = vl_a + 8;
-    const bool real_a = active && vl_a < Mu, real_b = active && vl_b < Mu;
-    const int lr_a = real_a ? vl_a / group : 0, lr_b = real_b ? vl_b / group : 0;
-    const size_t qrow_a = (size_t)(tl.cu + tl.r0 + lr_a) * a.Hq + g * group + (real_a ? vl_a % group : 0);
-    const size_t qrow_b = (size_t)(tl.cu + tl.r0 + lr_b) * a.Hq + g * group + (real_b ? vl_b % group : 0);
-    unsigned long long ka0 = 0, ka1 = 0, kb0 = 0, kb1 = 0;
-    if (tail) {
-      ka0 = s_anc[lr_a][0]; ka1 = s_anc[lr_a][1];
-      kb0 = s_anc[lr_b][0]; kb1 = s_anc[lr_b][1];
-    }
-    uint32_t qf[D / 16][4];
-    {
-      const uint32_t* qa = reinterpret_cast<const uint32_t*>(a.q + qrow_a * D);
-      const uint32_t* qb = reinterpret_cast<const uint32_t*>(a.q + qrow_b * D);
-#pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks) {
-        qf[ks][0] = real_a ? __ldg(qa + ks * 8 + tq) : 0u;
-        qf[ks][1] = real_b ? __ldg(qb + ks * 8 + tq) : 0u;
-        qf[ks][2] = real_a ? __ldg(qa + ks * 8 + 4 + tq) : 0u;
-        qf[ks][3] = real_b ? __ldg(qb + ks * 8 + 4 + tq) : 0u;
-      }
-    }
-    Frag<D> f;
-#pragma unroll
-    for (int dn = 0; dn < D / 8; ++dn) f.o[dn][0] = f.o[dn][1] = f.o[dn][2] = f.o[dn][3] = 0.f;
-    f.m_a = f.m_b = -INFINITY;
-    f.l_a = f.l_b = 0.f;
-
-    int issued = min(kStages - 1, n_stage), abort_at = -1;
-    for (int st = 0; st < n_stage; ++st) {
-      issue(st + kStages - 1);
-      if (st + kStages - 1 < n_stage) issued = st + kStages;
-      // ids of the stage after those in flight: loaded now, stored at the end
-      int id_next = -1;
-      unsigned long long row_next = ~0ull;
-      if (tid < 4) {
-        id_next = entry_id(st + kStages);
-        row_next = entry_rows(st + kStages);
-      }
-      const int slot = (it + st) % kStages;
-      unsigned long long vis_a = 0ull, vis_b = 0ull;
-      int valid = 0;  // sixteens of slots of the stage that hold something, 5 bits each
-      const int e0 = e_first + 4 * st;
-#pragma unroll
-      for (int p = 0; p < 4; ++p) {
-        unsigned long long wa = 0ull, wb = 0ull;
-        int n = 0;
-        if (s_id[st % kIds][p] >= 0) {
-          if (e0 + p < ncomp) {
-            n = 16;
-            wa = wb = 0xffffull;
-            if (SPARSE) {
-              const unsigned long long rows = s_row[st % kIds][p];
-              wa = (rows >> lr_a) & 1ull ? 0xffffull : 0ull;
-              wb = (rows >> lr_b) & 1ull ? 0xffffull : 0ull;
+        for (int e = e_end + lane; e < r.e_first + kStagePages; e += 32)
+          s_ids[L % kLists][e - r.e_first] = -1;
+        if (bad) flag(a.dev_status, SV_DEV_BAD_BLOCK_ID);
+        r.bad = __any_sync(0xffffffffu, bad);
+        if (e_end > r.ncomp) {  // the tail is among it
+          for (int j = lane; j < tl.rows; j += 32) s_par[j] = a.bt.parent[tl.cu + j];
+          __syncwarp();
+          for (int t = lane; t < tl.nr; t += 32) {
+            unsigned long long lo = 0ull, hi = 0ull;
+            int m = tl.r0 + t;
+            for (int steps = 0; m >= 0 && steps <= kMaxRows; ++steps) {  // parents were checked
+              if (m < 64) lo |= 1ull << m; else hi |= 1ull << (m - 64);
+              m = s_par[m];
             }
-          } else {
-            const int m0 = tail0 + (e0 + p - ncomp) * kBlockSize;
-            n = max(0, min(16, lim - m0));
-            wa = tail_visible(m0, ka0, ka1);
-            wb = tail_visible(m0, kb0, kb1);
+            s_anc[L % kLists][t] = make_ulonglong2(lo, hi);
           }
         }
-        vis_a |= wa << (16 * p);
-        vis_b |= wb << (16 * p);
-        valid |= n << (8 * p);
-      }
-      // rows of no query take what their neighbours need no mask for
-      if (!real_a) vis_a = ~0ull;
-      if (!real_b) vis_b = ~0ull;
-      // a wait that gives up marks the CTA; all threads stop after the barrier
-      if (!mbar_wait_bounded(smem_u32(&s_full[slot]), (uint32_t)(((it + st) / kStages) & 1))) s_abort = 1;
-      const uint32_t kbase = ring + slot * SL::kStageBytes;
-      const uint32_t vbase = kbase + SL::kTensorBytes;
-      if (valid != 0x10101010) {
-        // slots that nothing was written to may hold anything: V = 0 there, so
-        // that their weights of 0 add nothing
-        for (int y = tid; y < kTB * (D / 8); y += kThreads) {
-          const int t = y / (D / 8), ch = y % (D / 8);
-          if ((t & 15) >= ((valid >> (8 * (t >> 4))) & 31))
-            *reinterpret_cast<int4*>(ring_ptr + (vbase - ring) + SL::off(t, ch)) = make_int4(0, 0, 0, 0);
-        }
-        fence_proxy_async_smem();  // before later copies into the slot
-        __syncthreads();
-      }
-      if (active) {
-        if (TS == 4) {
-          slice_compute<D, 2>(f, qf, kbase, vbase, ts * 16, vis_a, vis_b, a.scale_log2, lane);
-        } else if (TS == 2) {
-          slice_compute<D, 4>(f, qf, kbase, vbase, ts * 32, vis_a, vis_b, a.scale_log2, lane);
-        } else {
-          slice_compute<D, 4>(f, qf, kbase, vbase, 0, vis_a, vis_b, a.scale_log2, lane);
-          slice_compute<D, 4>(f, qf, kbase, vbase, 32, vis_a, vis_b, a.scale_log2, lane);
-        }
-      }
-      if (tid < 4) {
-        s_id[(st + kStages) % kIds][tid] = id_next;
-        s_row[(st + kStages) % kIds][tid] = row_next;
-      }
-      __syncthreads();  // the slot is free
-      if (s_abort) {
-        abort_at = st;
-        if (tid == 0) flag(a.dev_status, SV_DEV_TIMEOUT);
+      } else if (L >= kLists &&
+                 !mbar_wait_bounded(smem_u32(&s_lfree[L % kLists]), (uint32_t)((L / kLists - 1) & 1))) {
+        ok = false;
         break;
       }
-    }
-    if (abort_at >= 0) {
-      // copies in flight land before the CTA leaves (bounded waits)
-      if (tid == 0)
-        for (int st = abort_at; st < issued; ++st)
-          mbar_wait_bounded(smem_u32(&s_full[(it + st) % kStages]),
-                            (uint32_t)(((it + st) / kStages) & 1));
-      __syncthreads();
-      return;
-    }
-    it += n_stage;
-
-    // warps that shared an m-tile meet through shared memory (the ring is idle)
-    float* xch = reinterpret_cast<float*>(ring_ptr);
-    constexpr int kFragFloats = D / 2 + 4;
-    if (TS > 1) {
-      if (active && ts > 0) {
-        float* dst = xch + ((size_t)warp * kFragFloats) * 32 + lane;
-#pragma unroll
-        for (int dn = 0; dn < D / 8; ++dn)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) dst[(dn * 4 + e) * 32] = f.o[dn][e];
-        dst[(D / 2 + 0) * 32] = f.m_a;
-        dst[(D / 2 + 1) * 32] = f.m_b;
-        dst[(D / 2 + 2) * 32] = f.l_a;
-        dst[(D / 2 + 3) * 32] = f.l_b;
+      __syncwarp();
+      if (lane == 0) {
+        s_rec[L % kLists] = r;
+        mbar_arrive(smem_u32(&s_lfull[L % kLists]));
       }
-      __syncthreads();
-      if (active && ts == 0) {
-        for (int t = 1; t < TS; ++t) {
-          const float* src = xch + ((size_t)(warp + t * MT) * kFragFloats) * 32 + lane;
-          const float m2a = src[(D / 2 + 0) * 32], m2b = src[(D / 2 + 1) * 32];
-          const float l2a = src[(D / 2 + 2) * 32], l2b = src[(D / 2 + 3) * 32];
-          const float na = fmaxf(f.m_a, m2a), nb = fmaxf(f.m_b, m2b);
-          const float ba = na == -INFINITY ? 0.f : na, bb = nb == -INFINITY ? 0.f : nb;
-          const float s1a = exp2f(f.m_a - ba), s2a = exp2f(m2a - ba);
-          const float s1b = exp2f(f.m_b - bb), s2b = exp2f(m2b - bb);
+      ++L;
+      if (r.n_stage == 0) break;
+    }
+    if (!ok) s_abort = 1;
+  } else if (warp == 4 || warp == 5) {
+    // --------------------------------------------------------- producers --
+    const bool isV = warp == 5;
+    bool ok = true;
+    int n = 0;
+    for (int L = 0; ok; ++L) {
+      const Rec* rp = list_at(L);
+      if (!__all_sync(0xffffffffu, rp != nullptr)) {
+        ok = false;
+        break;
+      }
+      const Rec r = *rp;
+      if (r.n_stage == 0) break;
+      int b = lane < kStagePages ? s_ids[L % kLists][lane] : -1;
+      __syncwarp();
+      if (lane == 0) list_done(L);
+      for (int st = 0; st < r.n_stage; ++st, ++n) {
+        // blocks of the next stage on their way
+        const int e1 = r.e_first + (st + 1) * kStagePages + lane;
+        const int b1 = st + 1 < r.n_stage && lane < kStagePages ? block_of(r, e1) : -1;
+        const int slot = n & 1;
+        // the slot is free once the products of stage n - 2 have read it
+        bool go = n < 2 || mbar_wait_bounded(smem_u32(isV ? &s_odone[slot] : &s_sfull[slot]),
+                                             (uint32_t)(((n - 2) >> 1) & 1));
+        if (!__all_sync(0xffffffffu, go) || __any_sync(0xffffffffu, gone())) {
+          ok = false;
+          break;
+        }
+        if (!isV && st == 0 && lane == 0) {
+          // Q of the list: its buffer's last reader was a list before stage n - 2
+          const uint32_t bar = smem_u32(&s_qfull[L & 1]), dst = base + (L & 1) * S::kTile;
+          mbar_arrive_expect_tx(bar, (uint32_t)(kHalves * a.rt * a.group * 128));
+          s_issued[4 + (L & 1)] += 1;
 #pragma unroll
-          for (int dn = 0; dn < D / 8; ++dn) {
-            f.o[dn][0] = f.o[dn][0] * s1a + src[(dn * 4 + 0) * 32] * s2a;
-            f.o[dn][1] = f.o[dn][1] * s1a + src[(dn * 4 + 1) * 32] * s2a;
-            f.o[dn][2] = f.o[dn][2] * s1b + src[(dn * 4 + 2) * 32] * s2b;
-            f.o[dn][3] = f.o[dn][3] * s1b + src[(dn * 4 + 3) * 32] * s2b;
+          for (int h = 0; h < kHalves; ++h)
+            tma_load_3d(dst + h * S::kHalf, &tmQ, 64 * h, r.g * a.group, r.row0, bar);
+        }
+        const uint32_t bar = smem_u32(isV ? &s_vfull[slot] : &s_kfull[slot]);
+        const int cnt = __popc(__ballot_sync(0xffffffffu, b >= 0));
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bar, (uint32_t)(cnt * kHalves * 2048));
+          s_issued[2 * isV + slot] += 1;
+        }
+        __syncwarp();
+        if (b >= 0) {
+          const uint32_t dst = ring + (2 * isV + slot) * S::kTile + lane * 2048;
+          const int y = (b * a.Hkv + r.g) * kBlockSize;
+#pragma unroll
+          for (int h = 0; h < kHalves; ++h)
+            tma_load_2d(dst + h * S::kHalf, isV ? &tmV : &tmK, 64 * h, y, bar);
+        }
+        b = b1;
+      }
+    }
+    if (!ok) s_abort = 1;
+  } else if (warp == 6) {
+    // --------------------------------------------------------- MMA issue --
+    if (lane == 0) {
+      constexpr uint32_t idesc_qk = tc5::idesc_bf16_f32(128, kTok, false);
+      constexpr uint32_t idesc_pv = tc5::idesc_bf16_f32(128, D, true);
+      const uint64_t qd = tc5::sw128_desc(base, 16, 1024);
+      const uint64_t kd = tc5::sw128_desc(ring, 16, 1024);
+      const uint64_t vd = tc5::sw128_desc(ring + 2 * S::kTile, S::kHalf, 1024);
+      bool ok = true;
+      // the lists of the next QK^T and of the next PV: PV follows a stage behind
+      int Lq = 0, sq = 0, nq = 0, n_q = 0, Lp = 0, sp = 0, np = 0;
+      const Rec* rq = list_at(0);
+      ok = rq != nullptr;
+      if (ok) nq = np = rq->n_stage;
+      auto qk = [&]() -> bool {  // stage n_q
+        const int n = n_q, slot = n & 1;
+        if (sq == 0 && !mbar_wait_bounded(smem_u32(&s_qfull[Lq & 1]), (uint32_t)((Lq >> 1) & 1))) return false;
+        // K has landed; PV of stage n - 2 is through with its P, where S goes
+        const uint32_t kf = smem_u32(&s_kfull[slot]), kp = (uint32_t)((n >> 1) & 1);
+        if (!(n < 2 ? mbar_wait_bounded(kf, kp)
+                    : mbar_wait2_bounded(kf, kp, smem_u32(&s_odone[slot]), (uint32_t)(((n - 2) >> 1) & 1))))
+          return false;
+        tc5::fence_after_sync();
+        const uint64_t ad = qd + (uint64_t)((Lq & 1) * (S::kTile >> 4));
+        const uint64_t bd = kd + (uint64_t)(slot * (S::kTile >> 4));
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const uint64_t o = (uint64_t)(((ks >> 2) * S::kHalf + (ks & 3) * 32) >> 4);
+          tc5::mma_bf16(tmem + (uint32_t)(slot * kTok), ad + o, bd + o, idesc_qk, ks > 0 ? 1u : 0u);
+        }
+        tc5::commit(smem_u32(&s_sfull[slot]));
+        ++n_q;
+        if (++sq == nq) {
+          ++Lq;
+          sq = 0;
+          const Rec* r = list_at(Lq);
+          if (!r) return false;
+          nq = r->n_stage;
+        }
+        return true;
+      };
+      if (ok && nq > 0) ok = qk();
+      for (int n = 0; ok && np > 0; ++n) {
+        if (nq > 0 && !(ok = qk())) break;
+        const int slot = n & 1;
+        // V has landed, P is there; at a list's first stage O of the list two before
+        // has been read
+        ok = mbar_wait2_bounded(smem_u32(&s_vfull[slot]), (uint32_t)((n >> 1) & 1),
+                                smem_u32(&s_pfull[slot]), (uint32_t)((n >> 1) & 1)) &&
+             (sp > 0 || Lp < 2 ||
+              mbar_wait_bounded(smem_u32(&s_ofree[Lp & 1]), (uint32_t)(((Lp >> 1) - 1) & 1))) &&
+             !gone();
+        if (!ok) break;
+        tc5::fence_after_sync();
+        const uint64_t bd = vd + (uint64_t)(slot * (S::kTile >> 4));
+        const uint32_t to = tmem + unit::kColO + (uint32_t)((Lp & 1) * 128);
+#pragma unroll
+        for (int ks = 0; ks < kTok / 16; ++ks)
+          tc5::mma_bf16_ts(to, tmem + (uint32_t)(slot * kTok) + ks * 8, bd + (uint64_t)(ks * 2048 >> 4),
+                           idesc_pv, (sp > 0 || ks > 0) ? 1u : 0u);
+        tc5::commit(smem_u32(&s_odone[slot]));
+        if (++sp == np) {
+          list_done(Lp);
+          ++Lp;
+          sp = 0;
+          const Rec* r = list_at(Lp);
+          if (!r) {
+            ok = false;
+            break;
           }
-          f.l_a = f.l_a * s1a + l2a * s2a;
-          f.l_b = f.l_b * s1b + l2b * s2b;
-          f.m_a = na;
-          f.m_b = nb;
+          np = r->n_stage;
         }
       }
+      if (!ok) s_abort = 1;
+      // every product has landed before the CTA moves on
+      tc5::commit(smem_u32(&s_drain));
+      mbar_wait_bounded(smem_u32(&s_drain), 0);
     }
-    if (!active || ts != 0) continue;
-    f.l_a += __shfl_xor_sync(0xffffffffu, f.l_a, 1);
-    f.l_a += __shfl_xor_sync(0xffffffffu, f.l_a, 2);
-    f.l_b += __shfl_xor_sync(0xffffffffu, f.l_b, 1);
-    f.l_b += __shfl_xor_sync(0xffffffffu, f.l_b, 2);
-    if (whole && (SPARSE || a.groups[tl.grp].z == 0)) {
-      const float inv_a = f.l_a > 0.f ? 1.f / f.l_a : 0.f;
-      const float inv_b = f.l_b > 0.f ? 1.f / f.l_b : 0.f;
-      uint32_t* oa = reinterpret_cast<uint32_t*>(a.out + qrow_a * D);
-      uint32_t* ob = reinterpret_cast<uint32_t*>(a.out + qrow_b * D);
-#pragma unroll
-      for (int dn = 0; dn < D / 8; ++dn) {
-        if (real_a) oa[dn * 4 + tq] = pack_bf16(f.o[dn][0] * inv_a, f.o[dn][1] * inv_a);
-        if (real_b) ob[dn * 4 + tq] = pack_bf16(f.o[dn][2] * inv_b, f.o[dn][3] * inv_b);
+  } else {
+    // ----------------------------------------------------- softmax, rows --
+    const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
+    const float sc = a.scale_log2;
+    const uint64_t sc2 = pair(sc, sc);
+    const int group = a.group;
+    bool ok = true;
+    int n = 0;
+    for (int L = 0; ok; ++L) {
+      const Rec* rp = list_at(L);
+      if (!__all_sync(0xffffffffu, rp != nullptr)) {
+        ok = false;
+        break;
       }
-      continue;
-    }
-    const size_t part = (size_t)(c + x) * a.tile_vr;
-    if (tq == 0) {
-      if (real_a) reinterpret_cast<float2*>(a.ml)[part + vl_a] = make_float2(f.m_a, f.l_a);
-      if (real_b) reinterpret_cast<float2*>(a.ml)[part + vl_b] = make_float2(f.m_b, f.l_b);
-    }
+      const Rec r = *rp;
+      if (r.n_stage == 0) break;
+      const int vrows = r.nr * group;
+      const bool real = tid < vrows;
+      const int lr = real ? tid / group : 0, head = r.g * group + (real ? tid % group : 0);
+      const bool some = warp * 32 < vrows;  // rows in this warp at all
+      ulonglong2 anc = make_ulonglong2(0ull, 0ull);
+      const int e_end = min(r.nent, r.e_first + r.n_stage * kStagePages);
+      if (e_end > r.ncomp) anc = s_anc[L % kLists][lr];
+      __syncwarp();
+      if (lane == 0) list_done(L);
+      const uint32_t* see = SPARSE ? a.see + ((size_t)r.x * a.rt + lr) * (a.cap / 32) : nullptr;
+      uint32_t bits = SPARSE ? __ldg(see + (r.e_first >> 5)) : 0u, bits1 = 0u;
+      const int tail0 = r.ctx / kBlockSize * kBlockSize - r.ctx;  // first tail slot
+      const uint32_t to = tmem + lane_base + unit::kColO + (uint32_t)((L & 1) * 128);
+      float m_ref = -INFINITY, l = 0.f;
+      for (int st = 0; st < r.n_stage; ++st, ++n) {
+        const int slot = n & 1;
+        const int e0 = r.e_first + st * kStagePages;
+        if (SPARSE && (e0 & 31) == 0 && st > 0) bits = bits1;
+        if (SPARSE && (e0 & 31) == 24 && st + 1 < r.n_stage) bits1 = __ldg(see + (e0 >> 5) + 1);
+        const uint32_t vis = SPARSE ? bits >> (e0 & 31) : 0xffu;  // pages of the stage the row sees
+        const bool got = mbar_wait_bounded(smem_u32(&s_sfull[slot]), (uint32_t)((n >> 1) & 1));
+        if (!__all_sync(0xffffffffu, got)) {
+          ok = false;
+          break;
+        }
+        const bool odd = r.bad || e0 + kStagePages > r.ncomp;  // not all complete and there
+        if (odd) {
+          // rows of V that nothing was written to may hold anything: zeros, so that
+          // their weights of 0 add nothing
+          const bool gv = mbar_wait_bounded(smem_u32(&s_vfull[slot]), (uint32_t)((n >> 1) & 1));
+          if (!__all_sync(0xffffffffu, gv)) {
+            ok = false;
+            break;
+          }
+          uint8_t* vb = base_ptr + (ring - base) + (2 + slot) * S::kTile;
+#pragma unroll 1
+          for (int p = 0; p < kStagePages; ++p) {
+            int have = 0;
+            if (block_of(r, e0 + p) >= 0)
+              have = e0 + p < r.ncomp ? 16
+                                      : max(0, min(16, r.lim - tail0 - (e0 + p - r.ncomp) * kBlockSize));
+            for (int y = tid; y < (16 - have) * (D / 8); y += 128) {
+              const int t = p * 16 + have + y / (D / 8), ch = y % (D / 8);
+              *reinterpret_cast<int4*>(vb + (ch >> 3) * S::kHalf + t * 128 + (((ch & 7) ^ (t & 7)) << 4)) =
+                  make_int4(0, 0, 0, 0);
+            }
+          }
+          fence_proxy_async_smem();
+        }
+        tc5::fence_after_sync();
+        if (some) {
+          const uint32_t ts = tmem + lane_base + (uint32_t)(slot * kTok);
+          uint32_t s[kTok];
+          tc5::tmem_ld_x128(ts, s);
+          uint32_t pages = vis;  // pages of which the row sees something
+          if (odd) {
+            pages = 0u;
 #pragma unroll
-    for (int dn = 0; dn < D / 8; ++dn) {
-      if (real_a)
-        *reinterpret_cast<float2*>(a.o + (part + vl_a) * D + dn * 8 + 2 * tq) = make_float2(f.o[dn][0], f.o[dn][1]);
-      if (real_b)
-        *reinterpret_cast<float2*>(a.o + (part + vl_b) * D + dn * 8 + 2 * tq) = make_float2(f.o[dn][2], f.o[dn][3]);
+            for (int p = 0; p < kStagePages; ++p) {
+              uint32_t w = 0u;
+              if (block_of(r, e0 + p) >= 0)
+                w = e0 + p < r.ncomp ? ((vis >> p) & 1u ? 0xffffu : 0u)
+                                     : tail_visible(tail0 + (e0 + p - r.ncomp) * kBlockSize, anc.x, anc.y);
+#pragma unroll
+              for (int k = 0; k < 16; ++k)
+                if (!((w >> k) & 1u)) s[16 * p + k] = __float_as_uint(-INFINITY);
+              if (w) pages |= 1u << p;
+            }
+          }
+          float mx = -INFINITY;
+#pragma unroll
+          for (int p = 0; p < kStagePages; ++p) {
+            float m2[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const uint32_t* q = s + 16 * p + 8 * k;
+              m2[k] = fmaxf(fmaxf(fmaxf(__uint_as_float(q[0]), __uint_as_float(q[1])), __uint_as_float(q[2])),
+                            fmaxf(__uint_as_float(q[3]), __uint_as_float(q[4])));
+              m2[k] = fmaxf(fmaxf(m2[k], __uint_as_float(q[5])), fmaxf(__uint_as_float(q[6]), __uint_as_float(q[7])));
+            }
+            if ((pages >> p) & 1u) mx = fmaxf(fmaxf(mx, m2[0]), m2[1]);
+          }
+          mx *= sc;
+          const bool grow = mx > m_ref + 8.f;
+          if (__any_sync(0xffffffffu, grow)) {
+            const float m_new = grow ? mx : m_ref;
+            const float alpha = grow ? ex2(m_ref - m_new) : 1.f;  // 0 while m_ref is -inf
+            if (st > 0) {
+              const bool g2 = mbar_wait_bounded(smem_u32(&s_odone[(n - 1) & 1]), (uint32_t)(((n - 1) >> 1) & 1));
+              if (!__all_sync(0xffffffffu, g2)) {
+                ok = false;
+                break;
+              }
+              tc5::fence_after_sync();
+#pragma unroll 1
+              for (int k = 0; k < D; k += 16) {
+                uint32_t ov[16];
+                tc5::tmem_ld_x16(to + k, ov);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) ov[j] = __float_as_uint(__uint_as_float(ov[j]) * alpha);
+                tc5::tmem_st_x16(to + k, ov);
+              }
+            }
+            l *= alpha;
+            m_ref = m_new;
+          }
+          const float mb = m_ref == -INFINITY ? 0.f : m_ref;
+          uint64_t sum[4] = {0, 0, 0, 0};
+          // P is rounded to bf16 for the tensor cores (2^-8 of each weight at most, in
+          // a sum of many; the normaliser keeps fp32); a page that the row does not
+          // see gets its -inf with the maximum's subtraction
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t pk[32];
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+              const float off = (pages >> (4 * h + p)) & 1u ? -mb : -INFINITY;
+              const uint64_t off2 = pair(off, off);
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const int e = h * 64 + 16 * p + 2 * k;
+                const float2 x = unpair(fma2(pair(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), sc2, off2));
+                const float w0 = ex2(x.x), w1 = ex2(x.y);
+                sum[k & 3] = add2(sum[k & 3], pair(w0, w1));
+                pk[8 * p + k] = pack_bf16(w0, w1);
+              }
+            }
+            tc5::tmem_st_x32(ts + h * 32, pk);
+          }
+          const float2 z = unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
+          l += z.x + z.y;
+        }
+        tc5::fence_before_sync();
+        mbar_arrive(smem_u32(&s_pfull[slot]));
+      }
+      if (!ok) break;
+      // the list's last PV has landed: O, normalised, to the output or to a part
+      {
+        const bool g3 = mbar_wait_bounded(smem_u32(&s_odone[(n - 1) & 1]), (uint32_t)(((n - 1) >> 1) & 1));
+        if (!__all_sync(0xffffffffu, g3)) {
+          ok = false;
+          break;
+        }
+        tc5::fence_after_sync();
+      }
+      if (some) {
+        const size_t row = (size_t)(r.row0 + lr) * a.Hq + head;
+        const bool out = r.whole && (SPARSE || a.groups[r.grp].z == 0);
+        const size_t part = (size_t)(c + r.x) * a.tile_vr + tid;
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll 1
+        for (int k = 0; k < D; k += 32) {
+          uint32_t ov[32];
+          tc5::tmem_ld_x32(to + k, ov);
+          if (!real) continue;
+          if (out) {
+            uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + row * D + k);
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              dst[j] = pack_bf16(__uint_as_float(ov[2 * j]) * inv, __uint_as_float(ov[2 * j + 1]) * inv);
+          } else {
+            float4* dst = reinterpret_cast<float4*>(a.o + part * D + k);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              dst[j] = make_float4(__uint_as_float(ov[4 * j]), __uint_as_float(ov[4 * j + 1]),
+                                   __uint_as_float(ov[4 * j + 2]), __uint_as_float(ov[4 * j + 3]));
+          }
+        }
+        if (real && !out) reinterpret_cast<float2*>(a.ml)[part] = make_float2(m_ref, l);
+      }
+      tc5::fence_before_sync();
+      mbar_arrive(smem_u32(&s_ofree[L & 1]));
     }
+    if (!ok) s_abort = 1;
   }
+
+  // every role is done with tensor memory and the ring
+  tc5::fence_before_sync();
+  __syncthreads();
+  tc5::fence_after_sync();
+  if (s_abort) {
+    // copies in flight land before the CTA leaves (bounded waits)
+    if (tid == 0) {
+      flag(a.dev_status, SV_DEV_TIMEOUT);
+      for (int k = 0; k < 6; ++k)
+        if (s_issued[k] > 0)
+          mbar_wait_bounded(smem_u32(k < 2 ? &s_kfull[k] : k < 4 ? &s_vfull[k - 2] : &s_qfull[k - 4]),
+                            (uint32_t)((s_issued[k] - 1) & 1));
+    }
+    __syncthreads();
+  }
+  if (warp == 4) tc5::tmem_dealloc(tmem, unit::kCols);
 }
 
 // ------------------------------------------------------------------ merge --
@@ -714,7 +839,7 @@ inline Args common_args(const sv_paged_kv* kv, const sv_batch* bt, int32_t Hq, u
   a.tile_vr = a.rt * a.group;
   // ceil(rows / rt) tiles a request
   a.tiles_cap = bt->total_rows / a.rt + bt->n_req;
-  a.ctas = 2 * sizing_sms();
+  a.ctas = sizing_sms();
   const size_t lists = (size_t)a.tiles_cap * a.Hkv, slots = lists + a.ctas;
   a.hdr = take<Header>(at, off, 1);
   a.tiles = take<Tile>(at, off, a.tiles_cap);
@@ -725,13 +850,29 @@ inline Args common_args(const sv_paged_kv* kv, const sv_batch* bt, int32_t Hq, u
   return a;
 }
 
+// The query rows as boxes of a tile: 64 elements x the heads of a KV head's group
+// x the tile's rows.
+inline bool make_q_map(CUtensorMap* map, const Args& a, int D) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = attn::encode_fn();
+  if (!enc) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)a.Hq, (cuuint64_t)a.bt.total_rows};
+  const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)a.Hq * D * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)a.group, (cuuint32_t)a.rt};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<__nv_bfloat16*>(a.q), dims, strides,
+             box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int D, bool SPARSE>
 inline sv_status launch_units(const Args& a, const CUtensorMap& tmK, const CUtensorMap& tmV,
                               cudaStream_t stream) {
-  constexpr size_t smem = (size_t)kStages * attn::StageLayout<D>::kStageBytes + 1024;
+  CUtensorMap tmQ;
+  if (!make_q_map(&tmQ, a, D)) return SV_ERR_CUDA;
   static PerDevice set;
-  if (smem_limit_once(set, unit_kernel<D, SPARSE>, smem) != cudaSuccess) return SV_ERR_CUDA;
-  if (sv::launch(unit_kernel<D, SPARSE>, a.ctas, kThreads, smem, stream, a, tmK, tmV) != cudaSuccess)
+  if (smem_limit_once(set, unit_kernel<D, SPARSE>, unit::Smem<D>::kAsk) != cudaSuccess) return SV_ERR_CUDA;
+  if (sv::launch(unit_kernel<D, SPARSE>, a.ctas, unit::kThreads, unit::Smem<D>::kAsk, stream, a, tmK, tmV,
+                 tmQ) != cudaSuccess)
     return SV_ERR_CUDA;
   if (sv::launch(merge_kernel<D, SPARSE>, a.tiles_cap * a.Hkv, kMergeThreads, 0, stream, a) !=
       cudaSuccess)
