@@ -13,6 +13,8 @@
 //           group x GQA group) by a part of the prefix's pages: (max, sum, O);
 //   units, merge (sv_page_units.cuh) over each request's own pages.
 
+#include <limits.h>
+
 #include "sv_page_units.cuh"
 #include "sv_tcgen05.cuh"
 
@@ -21,9 +23,10 @@ namespace pu {
 
 constexpr int kUnitPages = 1024;   // pages of a prefix unit at most (block ids in shared memory)
 
-__global__ void __launch_bounds__(1024) prefix_plan_kernel(const __grid_constant__ Args a, int nsm) {
+__global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_constant__ Args a, int nsm) {
   griddep_entry();
-  __shared__ int s_warp[32], s_tiles, s_stages, s_rows, s_units, s_pages, s_np, s_groups_bad;
+  __shared__ int s_warp[32], s_tiles, s_stages, s_rows, s_units, s_pages, s_groups_bad;
+  __shared__ long s_cost[64];
   const int R = a.bt.n_req, G = a.n_groups, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
     s_tiles = s_stages = s_rows = s_units = s_pages = 0;
@@ -34,7 +37,7 @@ __global__ void __launch_bounds__(1024) prefix_plan_kernel(const __grid_constant
   // groups that do not cut the requests into runs: nothing is attended
   for (int k = tid; k < G; k += blockDim.x)
     if (a.cu_groups[k] > a.cu_groups[k + 1]) s_groups_bad = 1;
-  __syncthreads();
+  check_requests(a);
   if (s_groups_bad) {
     if (tid == 0) {
       flag(a.dev_status, SV_DEV_BAD_PARAM);
@@ -44,51 +47,36 @@ __global__ void __launch_bounds__(1024) prefix_plan_kernel(const __grid_constant
   }
   for (int base = 0; base < R; base += blockDim.x) {
     const int i = base + tid;
-    Window w{};
-    int ctx = 0, nt = 0, stages = 0, first = 0, grp = 0, rows = 0;
-    if (i < R && request_rows(a, i, w, ctx)) {
-      grp = find_segment(a.cu_groups, G, i);
-      const int p = a.prefix_len[grp];
+    Req r{};
+    int nt = 0, stages = 0;
+    if (i < R) {
+      r = a.req[i];
+      r.grp = find_segment(a.cu_groups, G, i);
+      const int p = a.prefix_len[r.grp];
       if (p < 0 || p % kBlockSize != 0) {
-        flag(a.dev_status, SV_DEV_BAD_PARAM);
-      } else if (p > ctx) {
-        flag(a.dev_status, SV_DEV_BAD_LENGTH);
-      } else {
-        first = p / kBlockSize;
-        rows = w.e - w.b;
-        nt = (rows + a.rt - 1) / a.rt;
-        for (int k = 0; k < nt; ++k) {
-          const int last = min(w.b + (k + 1) * a.rt, w.e);
-          stages += ((ctx + last + kBlockSize - 1) / kBlockSize - first + kStagePages - 1) / kStagePages;
-        }
+        if (r.e > r.b) flag(a.dev_status, SV_DEV_BAD_PARAM);
+        r.e = r.b;
+      } else if (p > r.ctx) {
+        if (r.e > r.b) flag(a.dev_status, SV_DEV_BAD_LENGTH);
+        r.e = r.b;
+      }
+      r.first = p / kBlockSize;
+      nt = (r.e - r.b + a.rt - 1) / a.rt;
+      for (int k = 0; k < nt; ++k) {
+        const int last = min(r.b + (k + 1) * a.rt, r.e);
+        stages += ((r.ctx + last + kBlockSize - 1) / kBlockSize - r.first + kStagePages - 1) / kStagePages;
       }
     }
-    const int at = block_scan(nt, s_warp, &s_tiles);
-    int stage = block_scan(stages, s_warp, &s_stages) * a.Hkv;
-    const int arow = block_scan(rows, s_warp, &s_rows);
-    if (i < R) a.aoff[i] = arow;
-    for (int k = 0; k < rows && arow + k < a.bt.total_rows; ++k) a.arows[arow + k] = w.cu + w.b + k;
-    for (int k = 0; k < nt && at + k < a.tiles_cap; ++k) {
-      Tile t{};
-      t.i = i;
-      t.cu = w.cu;
-      t.ctx = ctx;
-      t.r0 = w.b + k * a.rt;
-      t.nr = min(a.rt, w.e - t.r0);
-      t.rows = w.rows;
-      t.first = first;
-      t.ncomp = ctx / kBlockSize - first;
-      t.nent = (ctx + t.r0 + t.nr + kBlockSize - 1) / kBlockSize - first;
-      t.arow = arow + k * a.rt;
-      t.grp = grp;
-      a.tiles[at + k] = t;
-      for (int g = 0; g < a.Hkv; ++g, stage += (t.nent + kStagePages - 1) / kStagePages)
-        a.off[(size_t)(at + k) * a.Hkv + g] = stage;
+    r.tile = block_scan(nt, s_warp, &s_tiles);
+    r.stage = block_scan(stages, s_warp, &s_stages);
+    r.arow = block_scan(r.e - r.b, s_warp, &s_rows);
+    if (i < R) {
+      a.req[i] = r;
+      a.aoff[i] = r.arow;
     }
   }
   // (offsets that overlap could ask for more than there is; such a call is left out)
-  const bool fits = s_tiles <= a.tiles_cap && s_rows <= a.bt.total_rows;
-  if (!fits) {
+  if (s_tiles > a.tiles_cap || s_rows > a.bt.total_rows) {
     if (tid == 0) {
       flag(a.dev_status, SV_DEV_BAD_WINDOW);
       a.hdr->T = a.hdr->W = a.hdr->C = a.hdr->units = 0;
@@ -102,7 +90,19 @@ __global__ void __launch_bounds__(1024) prefix_plan_kernel(const __grid_constant
     a.aoff[R] = s_rows;
   }
   __syncthreads();
-  deal_stages(a, T * a.Hkv, W);
+  write_tiles(a);
+  // first stages of the lists, the active rows
+  for (int i = warp; i < R; i += blockDim.x >> 5) {
+    const Req r = a.req[i];
+    for (int k = lane; k < r.e - r.b; k += 32) a.arows[r.arow + k] = r.cu + r.b + k;
+    int stage = r.stage * a.Hkv;
+    for (int k = 0, b = r.b; b < r.e; ++k, b += a.rt) {
+      const int n = ((r.ctx + min(b + a.rt, r.e) + kBlockSize - 1) / kBlockSize - r.first + kStagePages - 1) /
+                    kStagePages;
+      for (int g = lane; g < a.Hkv; g += 32) a.off[(size_t)(r.tile + k) * a.Hkv + g] = stage + g * n;
+      stage += a.Hkv * n;
+    }
+  }
   // groups: first active row, active rows, pages
   for (int k = tid; k < G; k += blockDim.x) {
     const int x = a.aoff[a.cu_groups[k]], n = a.aoff[a.cu_groups[k + 1]] - x;
@@ -111,41 +111,31 @@ __global__ void __launch_bounds__(1024) prefix_plan_kernel(const __grid_constant
     atomicMax(&s_pages, pages);
   }
   __syncthreads();
+  deal_stages(a, T * a.Hkv, W);
   // Pages of a unit: of the ways to cut the longest prefix into np parts the one
   // whose waves of units (one CTA an SM) take least, a unit costing its stages
   // and about three more for its start and its rows' merge.
-  if (warp == 0) {
-    long best = -1;
-    int best_P = kStagePages;
-    const int least = (s_pages + kUnitPages - 1) / kUnitPages;
-    for (int k = lane; k < 64; k += 32) {
-      const int np = max(1, least) + k;
-      int P = (s_pages + np - 1) / np;
-      P = max(kStagePages, (P + kStagePages - 1) / kStagePages * kStagePages);
-      long units = 0;
-      for (int y = 0; y < G; ++y) {
-        const int4 gr = a.groups[y];
-        units += (long)((gr.y * a.group + kPrefixRows - 1) / kPrefixRows) * a.Hkv * ((gr.z + P - 1) / P);
-      }
-      const long cost = (units + nsm - 1) / nsm * (P / kStagePages + 3);
-      if (units <= a.punits_cap && (best < 0 || cost < best)) {
-        best = cost;
-        best_P = P;
-      }
+  const int least = max(1, (s_pages + kUnitPages - 1) / kUnitPages);
+  auto unit_pages = [&](int k) {  // of the k-th way: least + k parts
+    const int P = (s_pages + least + k - 1) / (least + k);
+    return max(kStagePages, (P + kStagePages - 1) / kStagePages * kStagePages);
+  };
+  for (int k = warp; k < 64; k += blockDim.x >> 5) {
+    const int P = unit_pages(k);
+    int units = 0;
+    for (int y = lane; y < G; y += 32) {
+      const int4 gr = a.groups[y];
+      units += (gr.y * a.group + kPrefixRows - 1) / kPrefixRows * a.Hkv * ((gr.z + P - 1) / P);
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const long b = __shfl_xor_sync(0xffffffffu, best, o);
-      const int P = __shfl_xor_sync(0xffffffffu, best_P, o);
-      if (b >= 0 && (best < 0 || b < best || (b == best && P > best_P))) {
-        best = b;
-        best_P = P;
-      }
-    }
-    if (lane == 0) s_np = best_P;
+    units = __reduce_add_sync(0xffffffffu, units);
+    if (lane == 0)
+      s_cost[k] = units <= a.punits_cap ? (long)((units + nsm - 1) / nsm) * (P / kStagePages + 3) : LONG_MAX;
   }
   __syncthreads();
-  const int P = s_np;
+  int best = 0;  // the fewest parts on ties
+  for (int k = 1; k < 64; ++k)
+    if (s_cost[k] < s_cost[best]) best = k;
+  const int P = unit_pages(best);
   for (int base = 0; base < G; base += blockDim.x) {
     const int k = base + tid;
     int4 gr = make_int4(0, 0, 0, 0);
@@ -561,8 +551,7 @@ sv_status prefix_attend(const Args& a, const void* k, const void* v, cudaStream_
     return SV_ERR_CUDA;
   static PerDevice set;
   if (smem_limit_once(set, prefix_kernel<D>, pfx::Smem<D>::kAsk) != cudaSuccess) return SV_ERR_CUDA;
-  const int threads = std::min(1024, std::max(128, (a.bt.n_req + 31) / 32 * 32));
-  if (sv::launch(prefix_plan_kernel, 1, threads, 0, stream, a, sizing_sms()) != cudaSuccess ||
+  if (sv::launch(prefix_plan_kernel, 1, kPlanThreads, 0, stream, a, sizing_sms()) != cudaSuccess ||
       sv::launch(prefix_kernel<D>, a.punits_cap, pfx::kThreads, pfx::Smem<D>::kAsk, stream, a, tmK, tmV) !=
           cudaSuccess)
     return SV_ERR_CUDA;

@@ -22,7 +22,7 @@ namespace pu {
 constexpr int kMaxTable = 1 << 18;  // table entries a request may have (bits in shared memory)
 constexpr int kBuildThreads = 256;
 
-__global__ void __launch_bounds__(1024) page_plan_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const __grid_constant__ Args a) {
   griddep_entry();
   __shared__ int s_warp[32], s_tiles;
   const int R = a.bt.n_req, tid = threadIdx.x;
@@ -30,32 +30,24 @@ __global__ void __launch_bounds__(1024) page_plan_kernel(const __grid_constant__
     s_tiles = 0;
     if (a.bt.cu_rows[0] != 0 || a.bt.cu_rows[R] != a.bt.total_rows) flag(a.dev_status, SV_DEV_BAD_WINDOW);
   }
-  __syncthreads();
+  check_requests(a);
   for (int base = 0; base < R; base += blockDim.x) {
     const int i = base + tid;
-    Window w{};
-    int ctx = 0, nt = 0;
-    if (i < R && request_rows(a, i, w, ctx)) nt = (w.e - w.b + a.rt - 1) / a.rt;
+    const int nt = i < R ? (a.req[i].e - a.req[i].b + a.rt - 1) / a.rt : 0;
     const int at = block_scan(nt, s_warp, &s_tiles);
-    for (int k = 0; k < nt && at + k < a.tiles_cap; ++k) {
-      Tile t{};
-      t.i = i;
-      t.cu = w.cu;
-      t.ctx = ctx;
-      t.r0 = w.b + k * a.rt;
-      t.nr = min(a.rt, w.e - t.r0);
-      t.rows = w.rows;
-      a.tiles[at + k] = t;
-    }
+    if (i < R) a.req[i].tile = at;
   }
+  // (offsets that overlap could ask for more tiles than there are; such a call is left out)
+  const bool fits = s_tiles <= a.tiles_cap;
   if (tid == 0) {
-    // (offsets that overlap could ask for more tiles than there are; such a call is left out)
-    if (s_tiles > a.tiles_cap) flag(a.dev_status, SV_DEV_BAD_WINDOW);
-    a.hdr->T = s_tiles <= a.tiles_cap ? s_tiles : 0;
+    if (!fits) flag(a.dev_status, SV_DEV_BAD_WINDOW);
+    a.hdr->T = fits ? s_tiles : 0;
     a.hdr->W = 0;
     a.hdr->C = 0;
     a.hdr->ticket = 0;
   }
+  __syncthreads();
+  if (fits) write_tiles(a);
 }
 
 __global__ void __launch_bounds__(kBuildThreads) build_kernel(const __grid_constant__ Args a) {
@@ -167,8 +159,7 @@ sv_status page_attend(const Args& a, const void* k, const void* v, cudaStream_t 
   const size_t words = ((size_t)a.max_blocks + 31) / 32;
   static PerDevice set;
   if (smem_limit_once(set, build_kernel, kMaxTable / 32 * 8) != cudaSuccess) return SV_ERR_CUDA;
-  const int threads = std::min(1024, std::max(128, (a.bt.n_req + 31) / 32 * 32));
-  if (sv::launch(page_plan_kernel, 1, threads, 0, stream, a) != cudaSuccess ||
+  if (sv::launch(page_plan_kernel, 1, kPlanThreads, 0, stream, a) != cudaSuccess ||
       sv::launch(build_kernel, a.tiles_cap * a.Hkv, kBuildThreads, words * 8, stream, a) != cudaSuccess)
     return SV_ERR_CUDA;
   return launch_units<D, true>(a, tmK, tmV, stream);

@@ -26,6 +26,7 @@ namespace pu {
 constexpr int kTok = 128;        // tokens of a stage
 constexpr int kStagePages = 8;   // pages of a stage
 constexpr int kTileRows = 128;   // virtual rows of a tile
+constexpr int kPlanThreads = 1024;
 
 struct __align__(16) Tile {
   int i, cu, ctx, r0;      // request, its first packed row, context, first local row
@@ -45,6 +46,7 @@ struct Header {
   int pad[58];
 };
 
+struct Req;
 struct Args {
   sv_batch bt;
   int num_blocks, Hkv, max_blocks;
@@ -59,6 +61,7 @@ struct Args {
   float scale_log2;
   int32_t* dev_status;
   Header* hdr;
+  Req* req;           // [n_req]
   Tile* tiles;
   int* off;           // [lists + 1] first stage of each list
   int* start;         // [ctas] list of each CTA's first stage
@@ -109,31 +112,72 @@ __device__ __forceinline__ void deal_stages(const Args& a, int lists, int W) {
   }
 }
 
-// A request's window, parents and length; false (and reported) if it cannot be
-// attended.
-__device__ __forceinline__ bool request_rows(const Args& a, int i, Window& w, int& ctx) {
-  w = window_of(a.bt, i);
-  ctx = a.lens[i];
-  bool bad = false;
-  if (w.ok)
-    for (int j0 = 0; j0 < w.rows; j0 += 8) {  // eight loads in flight, then the checks
-      int pp[8];
+// What the plan keeps of a request.
+struct Req {
+  int cu, rows, b, e;  // e = b: left out
+  int ctx, first, grp, tile;  // prefix pages, group (prefix calls); first tile
+  int stage, arow;     // first stage of the request's lists of one KV head, first active row
+};
+
+// Window, parents and length of every request into a.req, by all threads of the
+// block: a warp a request, all of a request's loads in flight at once.  Requests
+// that cannot be attended are reported and left out.
+__device__ __forceinline__ void check_requests(const Args& a) {
+  const int lane = threadIdx.x & 31;
+  for (int i = threadIdx.x >> 5; i < a.bt.n_req; i += blockDim.x >> 5) {
+    const Window w = window_of(a.bt, i);
+    const int ctx = a.lens[i];
+    bool bad = false;
+    if (w.ok) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) pp[k] = j0 + k < w.rows ? a.bt.parent[w.cu + j0 + k] : 0;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int j = j0 + k;
-        if (j < w.rows) bad |= (j == 0) ? (pp[k] != -1) : (pp[k] < 0 || pp[k] >= j);
+      for (int k = 0; k < kMaxRows / 32; ++k) {
+        const int j = lane + 32 * k;
+        if (j < w.rows) {
+          const int p = a.bt.parent[w.cu + j];
+          bad |= j == 0 ? p != -1 : (p < 0 || p >= j);
+        }
       }
     }
-  if (!w.ok) flag(a.dev_status, SV_DEV_BAD_WINDOW);
-  if (bad) flag(a.dev_status, SV_DEV_BAD_PARENT);
-  if (!w.ok || bad) return false;
-  if (ctx < 0 || (long)ctx + w.rows > (long)a.max_blocks * kBlockSize) {
-    flag(a.dev_status, SV_DEV_BAD_LENGTH);
-    return false;
+    bad = __any_sync(0xffffffffu, bad);
+    if (lane != 0) continue;
+    const bool fits = ctx >= 0 && (long)ctx + w.rows <= (long)a.max_blocks * kBlockSize;
+    if (!w.ok) flag(a.dev_status, SV_DEV_BAD_WINDOW);
+    else if (bad) flag(a.dev_status, SV_DEV_BAD_PARENT);
+    else if (!fits) flag(a.dev_status, SV_DEV_BAD_LENGTH);
+    Req r{};
+    r.cu = w.cu;
+    r.rows = w.rows;
+    r.b = w.b;
+    r.e = w.ok && !bad && fits ? max(w.b, w.e) : w.b;  // (a window behind the verified rows is empty)
+    r.ctx = ctx;
+    a.req[i] = r;
   }
-  return true;
+  __syncthreads();
+}
+
+// The tiles of every request (tile: its first), by all threads of the block: a warp
+// a request.
+__device__ __forceinline__ void write_tiles(const Args& a) {
+  const int lane = threadIdx.x & 31;
+  for (int i = threadIdx.x >> 5; i < a.bt.n_req; i += blockDim.x >> 5) {
+    const Req r = a.req[i];
+    const int nt = (r.e - r.b + a.rt - 1) / a.rt;
+    for (int k = lane; k < nt; k += 32) {
+      Tile t{};
+      t.i = i;
+      t.cu = r.cu;
+      t.ctx = r.ctx;
+      t.r0 = r.b + k * a.rt;
+      t.nr = min(a.rt, r.e - t.r0);
+      t.rows = r.rows;
+      t.first = r.first;
+      t.ncomp = r.ctx / kBlockSize - r.first;
+      t.nent = (r.ctx + t.r0 + t.nr + kBlockSize - 1) / kBlockSize - r.first;
+      t.arow = r.arow + k * a.rt;
+      t.grp = r.grp;
+      a.tiles[r.tile + k] = t;
+    }
+  }
 }
 
 // Exclusive scan over the block's threads of v, on top of *carry (shared),
@@ -524,7 +568,10 @@ __global__ void __launch_bounds__(unit::kThreads, 1)
           break;
         }
         const bool odd = r.bad || e0 + kStagePages > r.ncomp;  // not all complete and there
+        uint32_t there = 0xffu;
         if (odd) {
+          there = e0 + kStagePages <= r.nent ? 0xffu : (1u << (r.nent - e0)) - 1u;
+          if (r.bad) there &= __ballot_sync(0xffffffffu, lane < kStagePages && block_of(r, e0 + lane) >= 0);
           // rows of V that nothing was written to may hold anything: zeros, so that
           // their weights of 0 add nothing
           const bool gv = mbar_wait_bounded(smem_u32(&s_vfull[slot]), (uint32_t)((n >> 1) & 1));
@@ -536,7 +583,7 @@ __global__ void __launch_bounds__(unit::kThreads, 1)
 #pragma unroll 1
           for (int p = 0; p < kStagePages; ++p) {
             int have = 0;
-            if (block_of(r, e0 + p) >= 0)
+            if ((there >> p) & 1u)
               have = e0 + p < r.ncomp ? 16
                                       : max(0, min(16, r.lim - tail0 - (e0 + p - r.ncomp) * kBlockSize));
             for (int y = tid; y < (16 - have) * (D / 8); y += 128) {
@@ -558,7 +605,7 @@ __global__ void __launch_bounds__(unit::kThreads, 1)
 #pragma unroll
             for (int p = 0; p < kStagePages; ++p) {
               uint32_t w = 0u;
-              if (block_of(r, e0 + p) >= 0)
+              if ((there >> p) & 1u)
                 w = e0 + p < r.ncomp ? ((vis >> p) & 1u ? 0xffffu : 0u)
                                      : tail_visible(tail0 + (e0 + p - r.ncomp) * kBlockSize, anc.x, anc.y);
 #pragma unroll
@@ -694,16 +741,17 @@ __global__ void __launch_bounds__(unit::kThreads, 1)
 
 // ------------------------------------------------------------------ merge --
 
-// One CTA a list: the parts of its rows -- of the CTAs that shared it and, in
-// prefix calls, of the prefix units of the row's group -- in one online pass.
-// SL neighbouring lanes share four columns of a row, lane s of them the parts
-// s, s + SL, ..., kLoads of them in flight at once; shuffles join the lanes.
+// One CTA a list (gridDim.y share its rows where lists are few), a warp a row: the
+// parts of the row -- of the CTAs that shared its list and, in prefix calls, of the
+// prefix units of its group -- in one online pass, kLoads of them in flight; a lane
+// has four columns (D / 4 lanes; with 64 columns half a warp takes each second
+// part and the halves join).
 constexpr int kMergeThreads = 256;
 constexpr int kPrefixRows = 256;  // virtual rows of a prefix unit
 template <int D, bool SPARSE>
 __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_constant__ Args a) {
   griddep_entry();
-  constexpr int kQuads = D / 4, kLoads = 8;
+  constexpr int kLanes = D / 4, kStep = 32 / kLanes, kLoads = 8;
   const int x = blockIdx.x;
   const int T = a.hdr->T, W = a.hdr->W, C = a.hdr->C;
   if (x >= T * a.Hkv) return;
@@ -720,54 +768,49 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_const
   }
   const int n = ns + np;
   if (n == 1) return;  // written by the CTA that had it whole
-  int SL = 1;
-  while (SL < 32 && SL * kLoads < n) SL <<= 1;
-  const int items = tl.nr * group * kQuads * SL;
-  for (int x0 = 0; x0 < items; x0 += kMergeThreads) {
-    const int y = x0 + threadIdx.x;
-    const bool live = y < items;
-    const int sl = y % SL, qd = y / SL;
-    const int vr = qd / kQuads, c4 = qd % kQuads;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int c4 = lane % kLanes, sub = lane / kLanes;
+  for (int vr = blockIdx.y * (kMergeThreads / 32) + warp; vr < tl.nr * group;
+       vr += gridDim.y * (kMergeThreads / 32)) {
+    size_t prow = 0;
+    if (!SPARSE && np > 0) {
+      const int v = (tl.arow - grp.x) * group + vr;  // among the group's virtual rows
+      prow = ((size_t)(grp.w + (v / kPrefixRows * a.Hkv + g) * np)) * kPrefixRows + v % kPrefixRows;
+    }
     float Mx = -INFINITY, L = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (live) {
-      size_t prow = 0;
-      if (!SPARSE && np > 0) {
-        const int v = (tl.arow - grp.x) * group + vr;  // among the group's virtual rows
-        prow = ((size_t)(grp.w + (v / kPrefixRows * a.Hkv + g) * np)) * kPrefixRows + v % kPrefixRows;
+    for (int k0 = sub; k0 < n; k0 += kLoads * kStep) {
+      float2 ml2[kLoads];
+      float4 o4[kLoads];
+#pragma unroll
+      for (int k = 0; k < kLoads; ++k) {
+        const int s = min(k0 + k * kStep, n - 1);
+        const float* ml = a.ml;
+        const float* o = a.o;
+        size_t row = (size_t)(c0 + s + x) * a.tile_vr + vr;
+        if (!SPARSE && s >= ns) {
+          ml = a.pml;
+          o = a.po;
+          row = prow + (size_t)(s - ns) * kPrefixRows;
+        }
+        ml2[k] = __ldcg(reinterpret_cast<const float2*>(ml) + row);
+        o4[k] = __ldcg(reinterpret_cast<const float4*>(o + row * D) + c4);
       }
-      for (int k0 = sl; k0 < n; k0 += kLoads * SL) {
-        float2 ml2[kLoads];
-        float4 o4[kLoads];
 #pragma unroll
-        for (int k = 0; k < kLoads; ++k) {
-          const int s = min(k0 + k * SL, n - 1);
-          const float* ml = a.ml;
-          const float* o = a.o;
-          size_t row = (size_t)(c0 + s + x) * a.tile_vr + vr;
-          if (!SPARSE && s >= ns) {
-            ml = a.pml;
-            o = a.po;
-            row = prow + (size_t)(s - ns) * kPrefixRows;
-          }
-          ml2[k] = __ldcg(reinterpret_cast<const float2*>(ml) + row);
-          o4[k] = __ldcg(reinterpret_cast<const float4*>(o + row * D) + c4);
-        }
-#pragma unroll
-        for (int k = 0; k < kLoads; ++k) {
-          const float nm = fmaxf(Mx, ml2[k].x);
-          if (k0 + k * SL >= n || nm == -INFINITY) continue;
-          const float s_old = exp2f(Mx - nm), s_new = exp2f(ml2[k].x - nm);
-          L = L * s_old + ml2[k].y * s_new;
-          acc.x = acc.x * s_old + o4[k].x * s_new;
-          acc.y = acc.y * s_old + o4[k].y * s_new;
-          acc.z = acc.z * s_old + o4[k].z * s_new;
-          acc.w = acc.w * s_old + o4[k].w * s_new;
-          Mx = nm;
-        }
+      for (int k = 0; k < kLoads; ++k) {
+        const float nm = fmaxf(Mx, ml2[k].x);
+        if (k0 + k * kStep >= n || nm == -INFINITY) continue;
+        const float s_old = exp2f(Mx - nm), s_new = exp2f(ml2[k].x - nm);
+        L = L * s_old + ml2[k].y * s_new;
+        acc.x = acc.x * s_old + o4[k].x * s_new;
+        acc.y = acc.y * s_old + o4[k].y * s_new;
+        acc.z = acc.z * s_old + o4[k].z * s_new;
+        acc.w = acc.w * s_old + o4[k].w * s_new;
+        Mx = nm;
       }
     }
-    for (int o = SL >> 1; o > 0; o >>= 1) {
+#pragma unroll
+    for (int o = kLanes; o < 32; o <<= 1) {
       const float m2 = __shfl_xor_sync(0xffffffffu, Mx, o);
       const float l2 = __shfl_xor_sync(0xffffffffu, L, o);
       float4 a2;
@@ -786,7 +829,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_const
         Mx = nm;
       }
     }
-    if (!live || sl != 0) continue;
+    if (sub != 0) continue;
     const float inv = L > 0.f ? 1.f / L : 0.f;
     const size_t row = (size_t)(tl.cu + tl.r0 + vr / group) * a.Hq + g * group + vr % group;
     uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + row * D + c4 * 4);
@@ -842,6 +885,7 @@ inline Args common_args(const sv_paged_kv* kv, const sv_batch* bt, int32_t Hq, u
   a.ctas = sizing_sms();
   const size_t lists = (size_t)a.tiles_cap * a.Hkv, slots = lists + a.ctas;
   a.hdr = take<Header>(at, off, 1);
+  a.req = take<Req>(at, off, bt->n_req);
   a.tiles = take<Tile>(at, off, a.tiles_cap);
   a.off = take<int>(at, off, lists + 1);
   a.start = take<int>(at, off, a.ctas);
@@ -874,8 +918,11 @@ inline sv_status launch_units(const Args& a, const CUtensorMap& tmK, const CUten
   if (sv::launch(unit_kernel<D, SPARSE>, a.ctas, unit::kThreads, unit::Smem<D>::kAsk, stream, a, tmK, tmV,
                  tmQ) != cudaSuccess)
     return SV_ERR_CUDA;
-  if (sv::launch(merge_kernel<D, SPARSE>, a.tiles_cap * a.Hkv, kMergeThreads, 0, stream, a) !=
-      cudaSuccess)
+  // few lists leave SMs idle: several CTAs share a list's rows
+  const int lists = a.tiles_cap * a.Hkv;
+  const int most = (a.tile_vr + kMergeThreads / 32 - 1) / (kMergeThreads / 32);
+  const int parts = std::max(1, std::min(most, 4 * sizing_sms() / lists));
+  if (sv::launch(merge_kernel<D, SPARSE>, dim3(lists, parts), kMergeThreads, 0, stream, a) != cudaSuccess)
     return SV_ERR_CUDA;
   return SV_OK;
 }

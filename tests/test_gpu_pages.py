@@ -67,9 +67,9 @@ class Setup:
         for name, v in (("row_begin", begin), ("row_end", end), ("verify_len", verify)):
             if v is not None:
                 setattr(self.batch, name, self.i32(v))
-        self.windows = [(b if begin is None else begin[i],
-                         min(m if end is None else end[i], m if verify is None else verify[i] + 1))
-                        for i, (b, m) in enumerate(self.windows)]
+        begin = begin or [0] * len(self.rows)
+        self.windows = [(b, max(b, min(m if end is None else end[i], m if verify is None else verify[i] + 1)))
+                        for i, (b, m) in enumerate(zip(begin, self.rows))]
 
     def numpy(self):
         return f64(self.k), f64(self.v), f64(self.q)
@@ -317,8 +317,8 @@ def test_page_attention_with_all_or_no_pages(keep):
 
 
 def test_page_attention_in_windows():
-    s = Setup([400, 300, 200, 100], [4, 30, 6, 8], 8, 2, 128)
-    s.window(begin=[1, 0, 2, 3], end=[4, 25, 2, 8], verify=[9, 22, 9, 5])
+    s = Setup([400, 300, 200, 100, 77], [4, 30, 6, 8, 9], 8, 2, 128)
+    s.window(begin=[1, 0, 2, 3, 5], end=[4, 25, 2, 8, 9], verify=[9, 22, 9, 5, 3])  # the last begins behind its rows
     pages = s.lists(6)
     got = attended(s, s.i32(pages))
     assert s.status.item() == 0

@@ -80,8 +80,8 @@ def test_prefix_lengths_around_a_stage(pages):
 
 
 def test_prefix_in_windows():
-    s = Shared([(256, [10, 20, 30]), (64, [5, 6])], [4, 12, 6, 8, 3], 8, 2, 128)
-    s.window(begin=[4, 0, 2, 3, 0], end=[4, 11, 6, 8, 3], verify=[9, 7, 9, 5, 0])
+    s = Shared([(256, [10, 20, 30]), (64, [5, 6, 7])], [4, 12, 6, 8, 3, 9], 8, 2, 128)
+    s.window(begin=[4, 0, 2, 3, 0, 5], end=[4, 11, 6, 8, 3, 9], verify=[9, 7, 9, 5, 0, 3])
     s.check(s.run())
     assert s.status.item() == 0
 
