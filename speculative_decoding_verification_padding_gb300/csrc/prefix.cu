@@ -13,23 +13,20 @@
 //           group x GQA group) by a part of the prefix's pages: (max, sum, O);
 //   units, merge (sv_page_units.cuh) over each request's own pages.
 
-#include <limits.h>
-
 #include "sv_page_units.cuh"
 #include "sv_tcgen05.cuh"
 
 namespace sv {
 namespace pu {
 
-constexpr int kUnitPages = 1024;   // pages of a prefix unit at most (block ids in shared memory)
-
-__global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_constant__ Args a, int nsm) {
+__global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_constant__ Args a) {
   griddep_entry();
-  __shared__ int s_warp[32], s_tiles, s_stages, s_rows, s_units, s_pages, s_groups_bad;
-  __shared__ long s_cost[64];
+  __shared__ int s_warp[32], s_tiles, s_stages, s_rows, s_lists, s_pstages, s_groups_bad;
+  extern __shared__ __align__(16) uint8_t s_mem[];
   const int R = a.bt.n_req, G = a.n_groups, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  Req* req = R <= kPlanRequests ? reinterpret_cast<Req*>(s_mem) : a.req;
   if (tid == 0) {
-    s_tiles = s_stages = s_rows = s_units = s_pages = 0;
+    s_tiles = s_stages = s_rows = s_lists = s_pstages = 0;
     if (a.bt.cu_rows[0] != 0 || a.bt.cu_rows[R] != a.bt.total_rows) flag(a.dev_status, SV_DEV_BAD_WINDOW);
     s_groups_bad = a.cu_groups[0] != 0 || a.cu_groups[G] != R;
   }
@@ -37,11 +34,11 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
   // groups that do not cut the requests into runs: nothing is attended
   for (int k = tid; k < G; k += blockDim.x)
     if (a.cu_groups[k] > a.cu_groups[k + 1]) s_groups_bad = 1;
-  check_requests(a);
+  check_requests(a, req);
   if (s_groups_bad) {
     if (tid == 0) {
       flag(a.dev_status, SV_DEV_BAD_PARAM);
-      a.hdr->T = a.hdr->W = a.hdr->C = a.hdr->units = 0;
+      a.hdr->T = a.hdr->W = a.hdr->C = a.hdr->Wp = a.hdr->Cp = 0;
     }
     return;
   }
@@ -50,7 +47,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
     Req r{};
     int nt = 0, stages = 0;
     if (i < R) {
-      r = a.req[i];
+      r = req[i];
       r.grp = find_segment(a.cu_groups, G, i);
       const int p = a.prefix_len[r.grp];
       if (p < 0 || p % kBlockSize != 0) {
@@ -71,7 +68,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
     r.stage = block_scan(stages, s_warp, &s_stages);
     r.arow = block_scan(r.e - r.b, s_warp, &s_rows);
     if (i < R) {
-      a.req[i] = r;
+      req[i] = r;
       a.aoff[i] = r.arow;
     }
   }
@@ -79,91 +76,68 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
   if (s_tiles > a.tiles_cap || s_rows > a.bt.total_rows) {
     if (tid == 0) {
       flag(a.dev_status, SV_DEV_BAD_WINDOW);
-      a.hdr->T = a.hdr->W = a.hdr->C = a.hdr->units = 0;
+      a.hdr->T = a.hdr->W = a.hdr->C = a.hdr->Wp = a.hdr->Cp = 0;
     }
     return;
   }
   const int T = s_tiles, W = s_stages * a.Hkv;
+  const int C = min(a.ctas, W);
   if (tid == 0) {
     a.hdr->T = T;
+    a.hdr->W = W;
+    a.hdr->C = C;
     a.off[(size_t)T * a.Hkv] = W;
     a.aoff[R] = s_rows;
   }
   __syncthreads();
-  write_tiles(a);
+  write_tiles(a, req);
   // first stages of the lists, the active rows
   for (int i = warp; i < R; i += blockDim.x >> 5) {
-    const Req r = a.req[i];
+    const Req r = req[i];
     for (int k = lane; k < r.e - r.b; k += 32) a.arows[r.arow + k] = r.cu + r.b + k;
     int stage = r.stage * a.Hkv;
     for (int k = 0, b = r.b; b < r.e; ++k, b += a.rt) {
       const int n = ((r.ctx + min(b + a.rt, r.e) + kBlockSize - 1) / kBlockSize - r.first + kStagePages - 1) /
                     kStagePages;
-      for (int g = lane; g < a.Hkv; g += 32) a.off[(size_t)(r.tile + k) * a.Hkv + g] = stage + g * n;
+      for (int g = lane; g < a.Hkv; g += 32) {
+        const int x = (r.tile + k) * a.Hkv + g;
+        a.off[x] = stage + g * n;
+        deal_list(a, x, stage + g * n, stage + (g + 1) * n, W, C);
+      }
       stage += a.Hkv * n;
     }
   }
-  // groups: first active row, active rows, pages
-  for (int k = tid; k < G; k += blockDim.x) {
-    const int x = a.aoff[a.cu_groups[k]], n = a.aoff[a.cu_groups[k + 1]] - x;
-    const int pages = n > 0 ? a.prefix_len[k] / kBlockSize : 0;  // checked by its requests
-    a.groups[k] = make_int4(x, n, pages, 0);
-    atomicMax(&s_pages, pages);
-  }
-  __syncthreads();
-  deal_stages(a, T * a.Hkv, W);
-  // Pages of a unit: of the ways to cut the longest prefix into np parts the one
-  // whose waves of units (one CTA an SM) take least, a unit costing its stages
-  // and about three more for its start and its rows' merge.
-  const int least = max(1, (s_pages + kUnitPages - 1) / kUnitPages);
-  auto unit_pages = [&](int k) {  // of the k-th way: least + k parts
-    const int P = (s_pages + least + k - 1) / (least + k);
-    return max(kStagePages, (P + kStagePages - 1) / kStagePages * kStagePages);
-  };
-  for (int k = warp; k < 64; k += blockDim.x >> 5) {
-    const int P = unit_pages(k);
-    int units = 0;
-    for (int y = lane; y < G; y += 32) {
-      const int4 gr = a.groups[y];
-      units += (gr.y * a.group + kPrefixRows - 1) / kPrefixRows * a.Hkv * ((gr.z + P - 1) / P);
-    }
-    units = __reduce_add_sync(0xffffffffu, units);
-    if (lane == 0)
-      s_cost[k] = units <= a.punits_cap ? (long)((units + nsm - 1) / nsm) * (P / kStagePages + 3) : LONG_MAX;
-  }
-  __syncthreads();
-  int best = 0;  // the fewest parts on ties
-  for (int k = 1; k < 64; ++k)
-    if (s_cost[k] < s_cost[best]) best = k;
-  const int P = unit_pages(best);
+  // groups: first active row, active rows, pages; their lists, one a 256-row tile
+  // and KV head, and the lists' stages
   for (int base = 0; base < G; base += blockDim.x) {
     const int k = base + tid;
     int4 gr = make_int4(0, 0, 0, 0);
-    int np = 0, n = 0;
+    int n = 0, sp = 0;
     if (k < G) {
-      gr = a.groups[k];
-      np = (gr.z + P - 1) / P;
-      n = (gr.y * a.group + kPrefixRows - 1) / kPrefixRows * a.Hkv * np;
+      gr.x = a.aoff[a.cu_groups[k]];
+      gr.y = a.aoff[a.cu_groups[k + 1]] - gr.x;
+      gr.z = gr.y > 0 ? a.prefix_len[k] / kBlockSize : 0;  // checked by its requests
+      n = gr.z > 0 ? (gr.y * a.group + kPrefixRows - 1) / kPrefixRows * a.Hkv : 0;
+      sp = (gr.z + kStagePages - 1) / kStagePages;
     }
-    const int at = block_scan(n, s_warp, &s_units);
-    if (k < G) a.groups[k].w = at;
-  }
-  for (int k = warp; k < G; k += blockDim.x >> 5) {
-    const int4 gr = a.groups[k];
-    const int np = (gr.z + P - 1) / P;
-    const int n = (gr.y * a.group + kPrefixRows - 1) / kPrefixRows * a.Hkv * np;
-    for (int y = lane; y < n && gr.w + y < a.punits_cap; y += 32)
-      a.punits[gr.w + y] = make_int4(k, y / np % a.Hkv, y / np / a.Hkv, y % np);
+    gr.w = block_scan(n, s_warp, &s_lists);
+    const int stage = block_scan(n * sp, s_warp, &s_pstages);
+    if (k < G) {
+      a.groups[k] = gr;
+      a.gstage[k] = stage;
+    }
   }
   if (tid == 0) {
-    a.hdr->np_pages = P;
-    a.hdr->units = min(s_units, a.punits_cap);
+    a.gstage[G] = s_pstages;
+    a.hdr->Wp = s_pstages;
+    a.hdr->Cp = min(a.ctas, s_pstages);
   }
 }
 
 // ------------------------------------------------------------ tcgen05 --
-// One CTA takes two tiles of 128 virtual rows by a run of pages, 128 tokens a
-// stage: S = Q K^T and O += P V of a tile are tcgen05.mma of 128 x 128 (S) and
+// A list is two tiles of 128 virtual rows of a group by its prefix, 128 tokens a
+// stage; all stages are dealt out evenly to one CTA an SM (as those of the page
+// lists), which works through its share list by list: S = Q K^T and O += P V of a tile are tcgen05.mma of 128 x 128 (S) and
 // 128 x D (O).  Tensor memory: S in columns 0 .. 127, of one tile and then the
 // other, P (bf16) of the tiles in 128 .. 191 and 192 .. 255, O in 256 .. 511.
 //   warps 0-3, 4-7: the softmax of tile 0 and 1; thread t owns row t (TMEM lane
@@ -203,7 +177,6 @@ __global__ void __launch_bounds__(pfx::kThreads, 1)
   using S = pfx::Smem<D>;
   constexpr int kHalves = D / 64;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  __shared__ int s_tbl[kUnitPages];
   // of a slot: K, V landed; of a tile and slot: S ready (K read), PV done (V read);
   // of a tile: S read by its softmax, P written, every product landed
   __shared__ __align__(8) unsigned long long s_kfull[2], s_vfull[2], s_sfull[2][2], s_odone[2][2],
@@ -211,24 +184,53 @@ __global__ void __launch_bounds__(pfx::kThreads, 1)
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort, s_bad;
   __shared__ int s_issued[4];
-  const int u = blockIdx.x;
-  if (u >= a.hdr->units) return;
-  const int4 un = a.punits[u];
-  const int4 gr = a.groups[un.x];
-  const int P = a.hdr->np_pages, g = un.y, group = a.group;
-  const int v0 = un.z * kPrefixRows, vrows = min(kPrefixRows, gr.y * group - v0);
-  const int ntile = vrows > 128 ? 2 : 1;
-  const int p0 = un.w * P, np = min(P, gr.z - p0);
-  const int n_stage = (np + kStagePages - 1) / kStagePages;
+  const int Wp = a.hdr->Wp, Cp = a.hdr->Cp, c = blockIdx.x;
+  if (c >= Cp) return;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* base_ptr = smem_raw + (base - smem_u32(smem_raw));
   const uint32_t ring = base + 2 * S::kTile;  // K slots, then V slots
+  const int s_end = share_start(c + 1, Wp, Cp);
+  int s_at = share_start(c, Wp, Cp);
+  int k = 0;  // the group of the share's first stage (groups without stages are passed over)
+  for (int hi = a.n_groups - 1; k < hi;) {
+    const int mid = (k + hi + 1) >> 1;
+    if (a.gstage[mid] <= s_at) k = mid; else hi = mid - 1;
+  }
+  if (tid == 0) s_abort = 0;
+  if (warp == 8) {
+    tc5::tmem_alloc(smem_u32(&s_tmem), pfx::kCols);
+    tc5::tmem_relinquish();
+  }
+  for (bool again = false; s_at < s_end; again = true) {
+  while (s_at >= a.gstage[k + 1]) ++k;
+  const int4 gr = a.groups[k];
+  const int group = a.group, sp = (gr.z + kStagePages - 1) / kStagePages;
+  const int list = (s_at - a.gstage[k]) / sp, st0 = (s_at - a.gstage[k]) % sp, g = list % a.Hkv;
+  const int n_stage = min(sp - st0, s_end - s_at);
+  const int v0 = list / a.Hkv * kPrefixRows, vrows = min(kPrefixRows, gr.y * group - v0);
+  const int ntile = vrows > 128 ? 2 : 1;
+  const int np = min(n_stage * kStagePages, gr.z - st0 * kStagePages);
+  const size_t slot_id = (size_t)(c + gr.w + list);
+  s_at += n_stage;
+  const int32_t* table = a.tables + (size_t)a.cu_groups[k] * a.max_blocks + st0 * kStagePages;
+  // block of page p of the run, -1 past its end or outside the cache
+  auto block_of = [&](int p) {
+    if (p >= np) return -1;
+    const int b = __ldg(table + p);
+    return b >= 0 && b < a.num_blocks ? b : -1;
+  };
+
 
   if (tid == 0) {
-    s_abort = 0;
     s_bad = np % kStagePages != 0;
     for (int k = 0; k < 4; ++k) s_issued[k] = -1;
+    if (again)
+      for (int k = 0; k < 2; ++k) {
+        for (unsigned long long* b : {&s_kfull[k], &s_vfull[k], &s_sfull[k][0], &s_sfull[k][1], &s_odone[k][0],
+                                      &s_odone[k][1], &s_sread[k], &s_pfull[k], &s_drain[k], &s_zero[k]})
+          mbar_inval(smem_u32(b));
+      }
     for (int k = 0; k < 2; ++k) {
       mbar_init(smem_u32(&s_kfull[k]), 1);
       mbar_init(smem_u32(&s_vfull[k]), 1);
@@ -244,23 +246,11 @@ __global__ void __launch_bounds__(pfx::kThreads, 1)
     fence_mbar_init();
   }
   __syncthreads();
-  const int32_t* table = a.tables + (size_t)a.cu_groups[un.x] * a.max_blocks + p0;
-  for (int p = tid; p < n_stage * kStagePages; p += pfx::kThreads) {
-    int b = -1;
-    if (p < np) {
-      b = __ldg(table + p);
-      if (b < 0 || b >= a.num_blocks) {
-        flag(a.dev_status, SV_DEV_BAD_BLOCK_ID);
-        b = -1;
-        s_bad = 1;
-      }
+  for (int p = tid; p < np; p += pfx::kThreads)
+    if (block_of(p) < 0) {
+      flag(a.dev_status, SV_DEV_BAD_BLOCK_ID);
+      s_bad = 1;
     }
-    s_tbl[p] = b;
-  }
-  if (warp == 8) {
-    tc5::tmem_alloc(smem_u32(&s_tmem), pfx::kCols);
-    tc5::tmem_relinquish();
-  }
   // Q rows, K-major with the 128-byte swizzle, zeros past the unit's rows
   const bool real = tid < vrows;
   if (tid < 128 * ntile) {
@@ -288,6 +278,7 @@ __global__ void __launch_bounds__(pfx::kThreads, 1)
     // a slot is free once both tiles' products have read it
     unsigned long long (*freeb)[2] = half ? s_odone : s_sfull;
     unsigned long long* fullb = half ? s_vfull : s_kfull;
+    int next = lane < kStagePages ? block_of(lane) : -1;
     for (int st = 0; st < n_stage; ++st) {
       const int slot = st & 1;
       bool go = true;
@@ -299,7 +290,8 @@ __global__ void __launch_bounds__(pfx::kThreads, 1)
         break;
       }
       if (__any_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&s_abort))) break;
-      const int b = lane < kStagePages ? s_tbl[st * kStagePages + lane] : -1;
+      const int b = next;
+      next = lane < kStagePages ? block_of((st + 1) * kStagePages + lane) : -1;
       const uint32_t bar = smem_u32(&fullb[slot]);
       const int n = __popc(__ballot_sync(0xffffffffu, b >= 0));
       if (lane == 0) {
@@ -394,10 +386,8 @@ __global__ void __launch_bounds__(pfx::kThreads, 1)
       tc5::fence_before_sync();
       mbar_arrive(smem_u32(&s_sread[t]));
       if (s_bad) {
-        uint32_t pages = 0u;  // pages of the stage that are there
-#pragma unroll
-        for (int p = 0; p < kStagePages; ++p)
-          if (s_tbl[st * kStagePages + p] >= 0) pages |= 1u << p;
+        // pages of the stage that are there
+        const uint32_t pages = __ballot_sync(0xffffffffu, lane < kStagePages && block_of(st * kStagePages + lane) >= 0);
         if (pages != 0xffu) {
 #pragma unroll
           for (int j = 0; j < kTok; ++j)
@@ -490,19 +480,18 @@ __global__ void __launch_bounds__(pfx::kThreads, 1)
       s_abort = 1;
     } else {
       tc5::fence_after_sync();
-      const size_t row = (size_t)u * kPrefixRows + tid;
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
         uint32_t ov[32];
         tc5::tmem_ld_x32(to + c, ov);
         if (!real) continue;
-        float4* dst = reinterpret_cast<float4*>(a.po + row * D + c);
+        float4* dst = reinterpret_cast<float4*>(a.po) + (slot_id * (D / 4) + c / 4) * kPrefixRows + tid;
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-          dst[k] = make_float4(__uint_as_float(ov[4 * k]), __uint_as_float(ov[4 * k + 1]),
-                               __uint_as_float(ov[4 * k + 2]), __uint_as_float(ov[4 * k + 3]));
+          dst[k * kPrefixRows] = make_float4(__uint_as_float(ov[4 * k]), __uint_as_float(ov[4 * k + 1]),
+                                             __uint_as_float(ov[4 * k + 2]), __uint_as_float(ov[4 * k + 3]));
       }
-      if (real) reinterpret_cast<float2*>(a.pml)[row] = make_float2(m_ref, l);
+      if (real) reinterpret_cast<float2*>(a.pml)[slot_id * kPrefixRows + tid] = make_float2(m_ref, l);
     }
   }
 
@@ -510,6 +499,8 @@ __global__ void __launch_bounds__(pfx::kThreads, 1)
   tc5::fence_before_sync();
   __syncthreads();
   tc5::fence_after_sync();
+  if (s_abort) break;
+  }
   if (s_abort) {
     // copies in flight land before the CTA leaves (bounded waits)
     if (tid == 0) {
@@ -521,7 +512,7 @@ __global__ void __launch_bounds__(pfx::kThreads, 1)
     }
     __syncthreads();
   }
-  if (warp == 8) tc5::tmem_dealloc(tmem, pfx::kCols);
+  if (warp == 8) tc5::tmem_dealloc(s_tmem, pfx::kCols);
 }
 
 inline Args prefix_args(const sv_paged_kv* kv, const sv_batch* bt, const sv_shared_prefix* sp,
@@ -533,14 +524,11 @@ inline Args prefix_args(const sv_paged_kv* kv, const sv_batch* bt, const sv_shar
   a.arows = take<int>(at, off, bt->total_rows);
   a.aoff = take<int>(at, off, bt->n_req + 1);
   a.groups = take<int4>(at, off, sp->n_groups);
-  // the row tiles of all groups, by the parts that the longest table needs at
-  // least, and four waves of units to choose finer parts from
-  const long tiles = (long)bt->total_rows * a.group / kPrefixRows + sp->n_groups;
-  const long parts = std::max(1, (kv->max_blocks_per_req + kUnitPages - 1) / kUnitPages);
-  a.punits_cap = (int)(tiles * a.Hkv * parts + 4L * sizing_sms());
-  a.punits = take<int4>(at, off, a.punits_cap);
-  a.pml = take<float>(at, off, (size_t)a.punits_cap * kPrefixRows * 2);
-  a.po = take<float>(at, off, (size_t)a.punits_cap * kPrefixRows * kv->head_dim);
+  a.gstage = take<int>(at, off, sp->n_groups + 1);
+  // the row tiles of all groups
+  a.plists = (int)(((long)bt->total_rows * a.group / kPrefixRows + sp->n_groups) * a.Hkv);
+  a.pml = take<float>(at, off, (size_t)(a.plists + a.ctas) * kPrefixRows * 2);
+  a.po = take<float>(at, off, (size_t)(a.plists + a.ctas) * kPrefixRows * kv->head_dim);
   return a;
 }
 
@@ -551,9 +539,8 @@ sv_status prefix_attend(const Args& a, const void* k, const void* v, cudaStream_
     return SV_ERR_CUDA;
   static PerDevice set;
   if (smem_limit_once(set, prefix_kernel<D>, pfx::Smem<D>::kAsk) != cudaSuccess) return SV_ERR_CUDA;
-  if (sv::launch(prefix_plan_kernel, 1, kPlanThreads, 0, stream, a, sizing_sms()) != cudaSuccess ||
-      sv::launch(prefix_kernel<D>, a.punits_cap, pfx::kThreads, pfx::Smem<D>::kAsk, stream, a, tmK, tmV) !=
-          cudaSuccess)
+  if (sv::launch(prefix_plan_kernel, 1, kPlanThreads, plan_smem(a), stream, a) != cudaSuccess ||
+      sv::launch(prefix_kernel<D>, a.ctas, pfx::kThreads, pfx::Smem<D>::kAsk, stream, a, tmK, tmV) != cudaSuccess)
     return SV_ERR_CUDA;
   return launch_units<D, false>(a, tmK, tmV, stream);
 }
@@ -590,7 +577,7 @@ extern "C" sv_status sv_prefix_attend(const sv_paged_kv* kv, const sv_batch* bt,
   if (st != SV_OK) return st;
   if (bt->n_req == 0 || bt->total_rows == 0) return SV_OK;
   if (!q || !out || !ws || !prefix->cu_groups || !prefix->prefix_len) return SV_ERR_INVALID_ARGUMENT;
-  if (((uintptr_t)q & 15) || ((uintptr_t)out & 3)) return SV_ERR_INVALID_ARGUMENT;
+  if (((uintptr_t)q | (uintptr_t)out) & 15) return SV_ERR_INVALID_ARGUMENT;
   if ((uintptr_t)ws & 255) return SV_ERR_INVALID_ARGUMENT;
   if (!(softmax_scale > 0.f)) return SV_ERR_INVALID_ARGUMENT;
   size_t need = 0;

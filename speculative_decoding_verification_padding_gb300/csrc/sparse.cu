@@ -25,17 +25,19 @@ constexpr int kBuildThreads = 256;
 __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const __grid_constant__ Args a) {
   griddep_entry();
   __shared__ int s_warp[32], s_tiles;
+  extern __shared__ __align__(16) uint8_t s_mem[];
   const int R = a.bt.n_req, tid = threadIdx.x;
+  Req* req = R <= kPlanRequests ? reinterpret_cast<Req*>(s_mem) : a.req;
   if (tid == 0) {
     s_tiles = 0;
     if (a.bt.cu_rows[0] != 0 || a.bt.cu_rows[R] != a.bt.total_rows) flag(a.dev_status, SV_DEV_BAD_WINDOW);
   }
-  check_requests(a);
+  check_requests(a, req);
   for (int base = 0; base < R; base += blockDim.x) {
     const int i = base + tid;
-    const int nt = i < R ? (a.req[i].e - a.req[i].b + a.rt - 1) / a.rt : 0;
+    const int nt = i < R ? (req[i].e - req[i].b + a.rt - 1) / a.rt : 0;
     const int at = block_scan(nt, s_warp, &s_tiles);
-    if (i < R) a.req[i].tile = at;
+    if (i < R) req[i].tile = at;
   }
   // (offsets that overlap could ask for more tiles than there are; such a call is left out)
   const bool fits = s_tiles <= a.tiles_cap;
@@ -47,7 +49,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const __grid_co
     a.hdr->ticket = 0;
   }
   __syncthreads();
-  if (fits) write_tiles(a);
+  if (fits) write_tiles(a, req);
 }
 
 __global__ void __launch_bounds__(kBuildThreads) build_kernel(const __grid_constant__ Args a) {
@@ -133,8 +135,14 @@ __global__ void __launch_bounds__(kBuildThreads) build_kernel(const __grid_const
     if (y < lists) a.off[y] = at;
   }
   __syncthreads();
-  if (tid == 0) a.off[lists] = s_carry;
-  deal_stages(a, lists, s_carry);
+  const int W = s_carry, C = min(a.ctas, W);
+  if (tid == 0) {
+    a.off[lists] = W;
+    a.hdr->W = W;
+    a.hdr->C = C;
+  }
+  __syncthreads();
+  for (int y = tid; y < lists; y += kBuildThreads) deal_list(a, y, a.off[y], a.off[y + 1], W, C);
 }
 
 inline Args page_args(const sv_paged_kv* kv, const sv_batch* bt, int32_t Hq, int32_t n_keep,
@@ -159,7 +167,7 @@ sv_status page_attend(const Args& a, const void* k, const void* v, cudaStream_t 
   const size_t words = ((size_t)a.max_blocks + 31) / 32;
   static PerDevice set;
   if (smem_limit_once(set, build_kernel, kMaxTable / 32 * 8) != cudaSuccess) return SV_ERR_CUDA;
-  if (sv::launch(page_plan_kernel, 1, kPlanThreads, 0, stream, a) != cudaSuccess ||
+  if (sv::launch(page_plan_kernel, 1, kPlanThreads, plan_smem(a), stream, a) != cudaSuccess ||
       sv::launch(build_kernel, a.tiles_cap * a.Hkv, kBuildThreads, words * 8, stream, a) != cudaSuccess)
     return SV_ERR_CUDA;
   return launch_units<D, true>(a, tmK, tmV, stream);
@@ -195,7 +203,7 @@ extern "C" sv_status sv_page_attend(const sv_paged_kv* kv, const sv_batch* bt, c
   if (st != SV_OK) return st;
   if (bt->n_req == 0 || bt->total_rows == 0) return SV_OK;
   if (!q || !out || !ws || (n_keep > 0 && !pages)) return SV_ERR_INVALID_ARGUMENT;
-  if (((uintptr_t)q & 15) || ((uintptr_t)out & 3)) return SV_ERR_INVALID_ARGUMENT;
+  if (((uintptr_t)q | (uintptr_t)out) & 15) return SV_ERR_INVALID_ARGUMENT;
   if ((uintptr_t)ws & 255) return SV_ERR_INVALID_ARGUMENT;
   if (!(softmax_scale > 0.f)) return SV_ERR_INVALID_ARGUMENT;
   size_t need = 0;

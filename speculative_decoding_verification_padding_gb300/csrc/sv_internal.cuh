@@ -287,6 +287,10 @@ __device__ __forceinline__ float4 dsmem_ld4(uint32_t a) {
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;\n" ::"r"(bar), "r"(count) : "memory");
 }
+// The barrier's word may be initialised anew afterwards.
+__device__ __forceinline__ void mbar_inval(uint32_t bar) {
+  asm volatile("mbarrier.inval.shared::cta.b64 [%0];\n" ::"r"(bar) : "memory");
+}
 // Order this thread's earlier generic-proxy shared-memory accesses before
 // later asynchronous-proxy (TMA) accesses to the same addresses.
 __device__ __forceinline__ void fence_proxy_async_smem() {

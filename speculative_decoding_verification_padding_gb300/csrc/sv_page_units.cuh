@@ -41,8 +41,8 @@ struct Header {
   int W;       // stages of all lists
   int C;       // CTAs that share them (at most W)
   int ticket;
-  int np_pages;  // pages of a prefix unit
-  int units;     // prefix units
+  int Wp;      // stages of all prefix lists
+  int Cp;      // CTAs that share them
   int pad[58];
 };
 
@@ -66,7 +66,7 @@ struct Args {
   int* off;           // [lists + 1] first stage of each list
   int* start;         // [ctas] list of each CTA's first stage
   float* ml;          // [slots][tile_vr][2]
-  float* o;           // [slots][tile_vr][D]
+  float* o;           // [slots][D / 4][tile_vr][4]: neighbouring rows in neighbouring lanes
   // page lists (sv_page_attend)
   const int32_t* pages;
   int n_keep;
@@ -80,11 +80,11 @@ struct Args {
   const int32_t* prefix_len;
   int* arows;         // [total_rows] packed rows of the active rows
   int* aoff;          // [n_req + 1] first active row of each request
-  int4* groups;       // [n_groups] first active row, active rows, pages, first unit
-  int4* punits;       // group, KV head, row tile, split
-  int punits_cap;
-  float* pml;
-  float* po;
+  int4* groups;       // [n_groups] first active row, active rows, pages, first prefix list
+  int* gstage;        // [n_groups + 1] first stage of each group's prefix lists
+  int plists;         // prefix lists at most: 256-row tiles x KV heads
+  float* pml;         // [plists + ctas][kPrefixRows][2]
+  float* po;          // [plists + ctas][D / 4][kPrefixRows][4]
 };
 
 // Stage s of W belongs to the CTA c of C <= W with start(c) <= s < start(c + 1).
@@ -93,23 +93,12 @@ __device__ __forceinline__ int share_of(int s, int W, int C) { return (int)((((l
 
 // ------------------------------------------------------------------ lists --
 
-// The list of each CTA's first stage, from the lists' first stages off[0 ..
-// lists] (global memory, written by this block before a barrier).
-__device__ __forceinline__ void deal_stages(const Args& a, int lists, int W) {
-  const int C = min(a.ctas, W);
-  for (int c = threadIdx.x; c < C; c += blockDim.x) {
-    const int s = share_start(c, W, C);
-    int lo = 0, hi = lists - 1;
-    while (lo < hi) {  // the last list that starts at or before s; empty lists are passed over
-      const int mid = (lo + hi + 1) >> 1;
-      if (a.off[mid] <= s) lo = mid; else hi = mid - 1;
-    }
-    a.start[c] = lo;
-  }
-  if (threadIdx.x == 0) {
-    a.hdr->W = W;
-    a.hdr->C = C;
-  }
+// List x has the stages off0 .. off1 - 1 of W: it is the first list of the CTAs
+// whose share begins there (C = min(a.ctas, W) of them).
+__device__ __forceinline__ void deal_list(const Args& a, int x, int off0, int off1, int W, int C) {
+  if (off0 >= off1) return;
+  // the least c with floor(c W / C) >= off0
+  for (int c = (int)(((long)off0 * C + W - 1) / W); c < C && share_start(c, W, C) < off1; ++c) a.start[c] = x;
 }
 
 // What the plan keeps of a request.
@@ -119,10 +108,13 @@ struct Req {
   int stage, arow;     // first stage of the request's lists of one KV head, first active row
 };
 
-// Window, parents and length of every request into a.req, by all threads of the
+// Requests whose records the plan keeps in shared memory; more go to the workspace.
+constexpr int kPlanRequests = 512;
+
+// Window, parents and length of every request into req, by all threads of the
 // block: a warp a request, all of a request's loads in flight at once.  Requests
 // that cannot be attended are reported and left out.
-__device__ __forceinline__ void check_requests(const Args& a) {
+__device__ __forceinline__ void check_requests(const Args& a, Req* req) {
   const int lane = threadIdx.x & 31;
   for (int i = threadIdx.x >> 5; i < a.bt.n_req; i += blockDim.x >> 5) {
     const Window w = window_of(a.bt, i);
@@ -150,17 +142,17 @@ __device__ __forceinline__ void check_requests(const Args& a) {
     r.b = w.b;
     r.e = w.ok && !bad && fits ? max(w.b, w.e) : w.b;  // (a window behind the verified rows is empty)
     r.ctx = ctx;
-    a.req[i] = r;
+    req[i] = r;
   }
   __syncthreads();
 }
 
 // The tiles of every request (tile: its first), by all threads of the block: a warp
 // a request.
-__device__ __forceinline__ void write_tiles(const Args& a) {
+__device__ __forceinline__ void write_tiles(const Args& a, const Req* req) {
   const int lane = threadIdx.x & 31;
   for (int i = threadIdx.x >> 5; i < a.bt.n_req; i += blockDim.x >> 5) {
-    const Req r = a.req[i];
+    const Req r = req[i];
     const int nt = (r.e - r.b + a.rt - 1) / a.rt;
     for (int k = lane; k < nt; k += 32) {
       Tile t{};
@@ -580,18 +572,18 @@ __global__ void __launch_bounds__(unit::kThreads, 1)
             break;
           }
           uint8_t* vb = base_ptr + (ring - base) + (2 + slot) * S::kTile;
-#pragma unroll 1
-          for (int p = 0; p < kStagePages; ++p) {
-            int have = 0;
-            if ((there >> p) & 1u)
-              have = e0 + p < r.ncomp ? 16
-                                      : max(0, min(16, r.lim - tail0 - (e0 + p - r.ncomp) * kBlockSize));
-            for (int y = tid; y < (16 - have) * (D / 8); y += 128) {
-              const int t = p * 16 + have + y / (D / 8), ch = y % (D / 8);
+          auto zero = [&](int t0, int t1) {  // rows t0 .. t1 - 1 of V
+            for (int y = tid; y < (t1 - t0) * (D / 8); y += 128) {
+              const int t = t0 + y / (D / 8), ch = y % (D / 8);
               *reinterpret_cast<int4*>(vb + (ch >> 3) * S::kHalf + t * 128 + (((ch & 7) ^ (t & 7)) << 4)) =
                   make_int4(0, 0, 0, 0);
             }
-          }
+          };
+          // behind the last staged slot, and (where a block is missing) whole pages
+          zero(min(kTok, max(0, (r.ncomp - e0) * kBlockSize + r.lim - tail0)), kTok);
+          if (r.bad)
+            for (int p = 0; p < kStagePages; ++p)
+              if (!((there >> p) & 1u)) zero(16 * p, 16 * p + 16);
           fence_proxy_async_smem();
         }
         tc5::fence_after_sync();
@@ -601,17 +593,16 @@ __global__ void __launch_bounds__(unit::kThreads, 1)
           tc5::tmem_ld_x128(ts, s);
           uint32_t pages = vis;  // pages of which the row sees something
           if (odd) {
-            pages = 0u;
 #pragma unroll
             for (int p = 0; p < kStagePages; ++p) {
-              uint32_t w = 0u;
-              if ((there >> p) & 1u)
-                w = e0 + p < r.ncomp ? ((vis >> p) & 1u ? 0xffffu : 0u)
-                                     : tail_visible(tail0 + (e0 + p - r.ncomp) * kBlockSize, anc.x, anc.y);
+              if (e0 + p < r.ncomp && ((there >> p) & 1u)) continue;  // the same for all rows
+              const uint32_t w = (there >> p) & 1u
+                                     ? tail_visible(tail0 + (e0 + p - r.ncomp) * kBlockSize, anc.x, anc.y)
+                                     : 0u;
 #pragma unroll
               for (int k = 0; k < 16; ++k)
                 if (!((w >> k) & 1u)) s[16 * p + k] = __float_as_uint(-INFINITY);
-              if (w) pages |= 1u << p;
+              pages = w ? pages | 1u << p : pages & ~(1u << p);
             }
           }
           float mx = -INFINITY;
@@ -701,16 +692,22 @@ __global__ void __launch_bounds__(unit::kThreads, 1)
           tc5::tmem_ld_x32(to + k, ov);
           if (!real) continue;
           if (out) {
-            uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + row * D + k);
+            uint4* dst = reinterpret_cast<uint4*>(a.out + row * D + k);
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-              dst[j] = pack_bf16(__uint_as_float(ov[2 * j]) * inv, __uint_as_float(ov[2 * j + 1]) * inv);
+            for (int j = 0; j < 4; ++j) {
+              uint32_t w[4];
+#pragma unroll
+              for (int z = 0; z < 4; ++z)
+                w[z] = pack_bf16(__uint_as_float(ov[8 * j + 2 * z]) * inv, __uint_as_float(ov[8 * j + 2 * z + 1]) * inv);
+              dst[j] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
           } else {
-            float4* dst = reinterpret_cast<float4*>(a.o + part * D + k);
+            float4* dst = reinterpret_cast<float4*>(a.o) + ((size_t)(c + r.x) * (D / 4) + k / 4) * a.tile_vr + tid;
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-              dst[j] = make_float4(__uint_as_float(ov[4 * j]), __uint_as_float(ov[4 * j + 1]),
-                                   __uint_as_float(ov[4 * j + 2]), __uint_as_float(ov[4 * j + 3]));
+              dst[(size_t)j * a.tile_vr] =
+                  make_float4(__uint_as_float(ov[4 * j]), __uint_as_float(ov[4 * j + 1]),
+                              __uint_as_float(ov[4 * j + 2]), __uint_as_float(ov[4 * j + 3]));
           }
         }
         if (real && !out) reinterpret_cast<float2*>(a.ml)[part] = make_float2(m_ref, l);
@@ -741,101 +738,85 @@ __global__ void __launch_bounds__(unit::kThreads, 1)
 
 // ------------------------------------------------------------------ merge --
 
-// One CTA a list (gridDim.y share its rows where lists are few), a warp a row: the
-// parts of the row -- of the CTAs that shared its list and, in prefix calls, of the
-// prefix units of its group -- in one online pass, kLoads of them in flight; a lane
-// has four columns (D / 4 lanes; with 64 columns half a warp takes each second
-// part and the halves join).
+// One CTA takes 32 rows of a list, a lane a row, a warp D / 8 columns: the parts of
+// the row -- of the CTAs that shared its list and, in prefix calls, those that
+// shared its group's prefix -- in one online pass, two of them in flight.
 constexpr int kMergeThreads = 256;
-constexpr int kPrefixRows = 256;  // virtual rows of a prefix unit
+constexpr int kPrefixRows = 256;  // virtual rows of a prefix list
 template <int D, bool SPARSE>
 __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_constant__ Args a) {
   griddep_entry();
-  constexpr int kLanes = D / 4, kStep = 32 / kLanes, kLoads = 8;
+  constexpr int kQuads = D / 32;  // of a warp
   const int x = blockIdx.x;
-  const int T = a.hdr->T, W = a.hdr->W, C = a.hdr->C;
-  if (x >= T * a.Hkv) return;
+  const Header h = *a.hdr;
+  if (x >= h.T * a.Hkv) return;
   const int off0 = a.off[x], off1 = a.off[x + 1];
-  if (off0 == off1) return;
   const Tile tl = a.tiles[x / a.Hkv];
+  if (off0 == off1) return;
   const int g = x % a.Hkv, group = a.group;
-  const int c0 = share_of(off0, W, C), ns = share_of(off1 - 1, W, C) - c0 + 1;
-  int np = 0;
-  int4 grp = make_int4(0, 0, 0, 0);
+  const int lane = threadIdx.x & 31, c4 = (threadIdx.x >> 5) * kQuads;
+  const int vr = blockIdx.y * 32 + lane, vrows = tl.nr * group;
+  if ((int)blockIdx.y * 32 >= vrows) return;
+  const int c0 = share_of(off0, h.W, h.C), ns = share_of(off1 - 1, h.W, h.C) - c0 + 1;
+  const int vs = min(vr, vrows - 1);
+  int np = 0, p0 = 0, pv = 0;
   if (!SPARSE) {
-    grp = a.groups[tl.grp];
-    np = grp.z > 0 ? (grp.z + a.hdr->np_pages - 1) / a.hdr->np_pages : 0;
+    const int4 grp = a.groups[tl.grp];
+    if (grp.z > 0) {
+      const int v = (tl.arow - grp.x) * group + vs;  // among the group's virtual rows
+      const int list = v / kPrefixRows * a.Hkv + g, sp = (grp.z + kStagePages - 1) / kStagePages;
+      const int s0 = a.gstage[tl.grp] + list * sp;
+      const int cp = share_of(s0, h.Wp, h.Cp);
+      np = share_of(s0 + sp - 1, h.Wp, h.Cp) - cp + 1;
+      p0 = cp + grp.w + list;
+      pv = v % kPrefixRows;
+    }
   }
-  const int n = ns + np;
-  if (n == 1) return;  // written by the CTA that had it whole
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int c4 = lane % kLanes, sub = lane / kLanes;
-  for (int vr = blockIdx.y * (kMergeThreads / 32) + warp; vr < tl.nr * group;
-       vr += gridDim.y * (kMergeThreads / 32)) {
-    size_t prow = 0;
-    if (!SPARSE && np > 0) {
-      const int v = (tl.arow - grp.x) * group + vr;  // among the group's virtual rows
-      prow = ((size_t)(grp.w + (v / kPrefixRows * a.Hkv + g) * np)) * kPrefixRows + v % kPrefixRows;
-    }
-    float Mx = -INFINITY, L = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k0 = sub; k0 < n; k0 += kLoads * kStep) {
-      float2 ml2[kLoads];
-      float4 o4[kLoads];
+  const int n = ns + np;  // (rows of a block may lie in two prefix lists)
+  if (SPARSE ? n == 1 : np == 0 && ns == 1) return;  // written by the CTA that had it whole
+  float Mx = -INFINITY, L = 0.f;
+  float4 acc[kQuads];
 #pragma unroll
-      for (int k = 0; k < kLoads; ++k) {
-        const int s = min(k0 + k * kStep, n - 1);
-        const float* ml = a.ml;
-        const float* o = a.o;
-        size_t row = (size_t)(c0 + s + x) * a.tile_vr + vr;
-        if (!SPARSE && s >= ns) {
-          ml = a.pml;
-          o = a.po;
-          row = prow + (size_t)(s - ns) * kPrefixRows;
-        }
-        ml2[k] = __ldcg(reinterpret_cast<const float2*>(ml) + row);
-        o4[k] = __ldcg(reinterpret_cast<const float4*>(o + row * D) + c4);
-      }
+  for (int j = 0; j < kQuads; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k0 = 0; k0 < n; k0 += 2) {
+    float2 ml2[2];
+    float4 o4[2][kQuads];
 #pragma unroll
-      for (int k = 0; k < kLoads; ++k) {
-        const float nm = fmaxf(Mx, ml2[k].x);
-        if (k0 + k * kStep >= n || nm == -INFINITY) continue;
-        const float s_old = exp2f(Mx - nm), s_new = exp2f(ml2[k].x - nm);
-        L = L * s_old + ml2[k].y * s_new;
-        acc.x = acc.x * s_old + o4[k].x * s_new;
-        acc.y = acc.y * s_old + o4[k].y * s_new;
-        acc.z = acc.z * s_old + o4[k].z * s_new;
-        acc.w = acc.w * s_old + o4[k].w * s_new;
-        Mx = nm;
-      }
+    for (int k = 0; k < 2; ++k) {
+      const int s = min(k0 + k, n - 1);
+      const bool own = SPARSE || s < ns;
+      const size_t slot = own ? (size_t)(c0 + s + x) : (size_t)(p0 + s - ns);
+      const int rows = own ? a.tile_vr : kPrefixRows, row = own ? vs : pv;
+      ml2[k] = __ldcg(reinterpret_cast<const float2*>(own ? a.ml : a.pml) + slot * rows + row);
+      const float4* o = reinterpret_cast<const float4*>(own ? a.o : a.po) + (slot * (D / 4) + c4) * rows + row;
+#pragma unroll
+      for (int j = 0; j < kQuads; ++j) o4[k][j] = __ldcg(o + (size_t)j * rows);
     }
 #pragma unroll
-    for (int o = kLanes; o < 32; o <<= 1) {
-      const float m2 = __shfl_xor_sync(0xffffffffu, Mx, o);
-      const float l2 = __shfl_xor_sync(0xffffffffu, L, o);
-      float4 a2;
-      a2.x = __shfl_xor_sync(0xffffffffu, acc.x, o);
-      a2.y = __shfl_xor_sync(0xffffffffu, acc.y, o);
-      a2.z = __shfl_xor_sync(0xffffffffu, acc.z, o);
-      a2.w = __shfl_xor_sync(0xffffffffu, acc.w, o);
-      const float nm = fmaxf(Mx, m2);
-      if (nm != -INFINITY) {
-        const float s_old = exp2f(Mx - nm), s_new = exp2f(m2 - nm);
-        L = L * s_old + l2 * s_new;
-        acc.x = acc.x * s_old + a2.x * s_new;
-        acc.y = acc.y * s_old + a2.y * s_new;
-        acc.z = acc.z * s_old + a2.z * s_new;
-        acc.w = acc.w * s_old + a2.w * s_new;
-        Mx = nm;
+    for (int k = 0; k < 2; ++k) {
+      const float nm = fmaxf(Mx, ml2[k].x);
+      if (k0 + k >= n || nm == -INFINITY) continue;
+      const float s_old = exp2f(Mx - nm), s_new = exp2f(ml2[k].x - nm);
+      L = L * s_old + ml2[k].y * s_new;
+#pragma unroll
+      for (int j = 0; j < kQuads; ++j) {
+        acc[j].x = acc[j].x * s_old + o4[k][j].x * s_new;
+        acc[j].y = acc[j].y * s_old + o4[k][j].y * s_new;
+        acc[j].z = acc[j].z * s_old + o4[k][j].z * s_new;
+        acc[j].w = acc[j].w * s_old + o4[k][j].w * s_new;
       }
+      Mx = nm;
     }
-    if (sub != 0) continue;
-    const float inv = L > 0.f ? 1.f / L : 0.f;
-    const size_t row = (size_t)(tl.cu + tl.r0 + vr / group) * a.Hq + g * group + vr % group;
-    uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + row * D + c4 * 4);
-    dst[0] = pack_bf16(acc.x * inv, acc.y * inv);
-    dst[1] = pack_bf16(acc.z * inv, acc.w * inv);
   }
+  if (vr >= vrows) return;
+  const float inv = L > 0.f ? 1.f / L : 0.f;
+  const size_t row = (size_t)(tl.cu + tl.r0 + vr / group) * a.Hq + g * group + vr % group;
+  uint4* dst = reinterpret_cast<uint4*>(a.out + row * D + c4 * 4);
+#pragma unroll
+  for (int j = 0; j < kQuads; j += 2)
+    dst[j / 2] = make_uint4(pack_bf16(acc[j].x * inv, acc[j].y * inv), pack_bf16(acc[j].z * inv, acc[j].w * inv),
+                            pack_bf16(acc[j + 1].x * inv, acc[j + 1].y * inv),
+                            pack_bf16(acc[j + 1].z * inv, acc[j + 1].w * inv));
 }
 
 // ------------------------------------------------------------- host side --
@@ -894,6 +875,10 @@ inline Args common_args(const sv_paged_kv* kv, const sv_batch* bt, int32_t Hq, u
   return a;
 }
 
+inline size_t plan_smem(const Args& a) {
+  return a.bt.n_req <= kPlanRequests ? sizeof(Req) * (size_t)a.bt.n_req : 0;
+}
+
 // The query rows as boxes of a tile: 64 elements x the heads of a KV head's group
 // x the tile's rows.
 inline bool make_q_map(CUtensorMap* map, const Args& a, int D) {
@@ -918,12 +903,8 @@ inline sv_status launch_units(const Args& a, const CUtensorMap& tmK, const CUten
   if (sv::launch(unit_kernel<D, SPARSE>, a.ctas, unit::kThreads, unit::Smem<D>::kAsk, stream, a, tmK, tmV,
                  tmQ) != cudaSuccess)
     return SV_ERR_CUDA;
-  // few lists leave SMs idle: several CTAs share a list's rows
-  const int lists = a.tiles_cap * a.Hkv;
-  const int most = (a.tile_vr + kMergeThreads / 32 - 1) / (kMergeThreads / 32);
-  const int parts = std::max(1, std::min(most, 4 * sizing_sms() / lists));
-  if (sv::launch(merge_kernel<D, SPARSE>, dim3(lists, parts), kMergeThreads, 0, stream, a) != cudaSuccess)
-    return SV_ERR_CUDA;
+  const dim3 grid(a.tiles_cap * a.Hkv, (a.tile_vr + 31) / 32);
+  if (sv::launch(merge_kernel<D, SPARSE>, grid, kMergeThreads, 0, stream, a) != cudaSuccess) return SV_ERR_CUDA;
   return SV_OK;
 }
 
