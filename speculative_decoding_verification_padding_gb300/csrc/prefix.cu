@@ -127,10 +127,28 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
       a.gstage[k] = stage;
     }
   }
+  const int Wp = s_pstages, Cp = min(a.ctas, Wp);
   if (tid == 0) {
-    a.gstage[G] = s_pstages;
-    a.hdr->Wp = s_pstages;
-    a.hdr->Cp = min(a.ctas, s_pstages);
+    a.gstage[G] = Wp;
+    a.hdr->Wp = Wp;
+    a.hdr->Cp = Cp;
+  }
+  __syncthreads();
+  for (int c = tid; c < Cp; c += blockDim.x) {
+    const int s = share_start(c, Wp, Cp);
+    PStart ps;
+    ps.k = 0;  // the last group whose stages begin at or before s
+    for (int hi = G - 1; ps.k < hi;) {
+      const int mid = (ps.k + hi + 1) >> 1;
+      if (a.gstage[mid] <= s) ps.k = mid; else hi = mid - 1;
+    }
+    ps.gr = a.groups[ps.k];
+    const int sp = (ps.gr.z + kStagePages - 1) / kStagePages;
+    ps.list = (s - a.gstage[ps.k]) / sp;
+    ps.st0 = (s - a.gstage[ps.k]) % sp;
+    ps.leader = a.cu_groups[ps.k];
+    ps.lists = (ps.gr.y * a.group + kPrefixRows - 1) / kPrefixRows * a.Hkv;
+    a.pstart[c] = ps;
   }
 }
 
@@ -173,47 +191,61 @@ template <int D>
 __global__ void __launch_bounds__(pfx::kThreads, 1)
     prefix_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap tmK,
                   const __grid_constant__ CUtensorMap tmV) {
-  griddep_entry();
   using S = pfx::Smem<D>;
   constexpr int kHalves = D / 64;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   // of a slot: K, V landed; of a tile and slot: S ready (K read), PV done (V read);
   // of a tile: S read by its softmax, P written, every product landed
   __shared__ __align__(8) unsigned long long s_kfull[2], s_vfull[2], s_sfull[2][2], s_odone[2][2],
-      s_sread[2], s_pfull[2], s_drain[2], s_zero[2];
+      s_sread[2], s_pfull[2], s_qfull[2], s_drain[2], s_zero[2];
   __shared__ uint32_t s_tmem;
-  __shared__ int s_abort, s_bad;
+  __shared__ int s_abort;
   __shared__ int s_issued[4];
-  const int Wp = a.hdr->Wp, Cp = a.hdr->Cp, c = blockIdx.x;
-  if (c >= Cp) return;
+  const int c = blockIdx.x;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* base_ptr = smem_raw + (base - smem_u32(smem_raw));
   const uint32_t ring = base + 2 * S::kTile;  // K slots, then V slots
-  const int s_end = share_start(c + 1, Wp, Cp);
-  int s_at = share_start(c, Wp, Cp);
-  int k = 0;  // the group of the share's first stage (groups without stages are passed over)
-  for (int hi = a.n_groups - 1; k < hi;) {
-    const int mid = (k + hi + 1) >> 1;
-    if (a.gstage[mid] <= s_at) k = mid; else hi = mid - 1;
-  }
+  const int group = a.group;
+  // nothing that earlier kernels write is read before griddep_entry()
   if (tid == 0) s_abort = 0;
   if (warp == 8) {
+    if (lane == 0) {
+      prefetch_map(&tmK);
+      prefetch_map(&tmV);
+    }
+    __syncwarp();
     tc5::tmem_alloc(smem_u32(&s_tmem), pfx::kCols);
     tc5::tmem_relinquish();
   }
+  griddep_entry();
+  const int Wp = a.hdr->Wp, Cp = a.hdr->Cp;
+  PStart ps = a.pstart[c];  // (there are a.ctas of them)
+  if (c >= Cp) {
+    __syncthreads();
+    if (warp == 8) tc5::tmem_dealloc(s_tmem, pfx::kCols);
+    return;
+  }
+  const int s_end = share_start(c + 1, Wp, Cp);
+  int s_at = share_start(c, Wp, Cp);
   for (bool again = false; s_at < s_end; again = true) {
-  while (s_at >= a.gstage[k + 1]) ++k;
-  const int4 gr = a.groups[k];
-  const int group = a.group, sp = (gr.z + kStagePages - 1) / kStagePages;
-  const int list = (s_at - a.gstage[k]) / sp, st0 = (s_at - a.gstage[k]) % sp, g = list % a.Hkv;
+  if (again && ++ps.list == ps.lists) {  // the next group that has stages
+    while (s_at >= a.gstage[ps.k + 1]) ++ps.k;
+    ps.gr = a.groups[ps.k];
+    ps.leader = a.cu_groups[ps.k];
+    ps.list = 0;
+    ps.lists = (ps.gr.y * group + kPrefixRows - 1) / kPrefixRows * a.Hkv;
+  }
+  if (again) ps.st0 = 0;
+  const int4 gr = ps.gr;
+  const int list = ps.list, st0 = ps.st0, g = list % a.Hkv, sp = (gr.z + kStagePages - 1) / kStagePages;
   const int n_stage = min(sp - st0, s_end - s_at);
   const int v0 = list / a.Hkv * kPrefixRows, vrows = min(kPrefixRows, gr.y * group - v0);
   const int ntile = vrows > 128 ? 2 : 1;
   const int np = min(n_stage * kStagePages, gr.z - st0 * kStagePages);
   const size_t slot_id = (size_t)(c + gr.w + list);
   s_at += n_stage;
-  const int32_t* table = a.tables + (size_t)a.cu_groups[k] * a.max_blocks + st0 * kStagePages;
+  const int32_t* table = a.tables + (size_t)ps.leader * a.max_blocks + st0 * kStagePages;
   // block of page p of the run, -1 past its end or outside the cache
   auto block_of = [&](int p) {
     if (p >= np) return -1;
@@ -221,14 +253,13 @@ __global__ void __launch_bounds__(pfx::kThreads, 1)
     return b >= 0 && b < a.num_blocks ? b : -1;
   };
 
-
   if (tid == 0) {
-    s_bad = np % kStagePages != 0;
     for (int k = 0; k < 4; ++k) s_issued[k] = -1;
     if (again)
       for (int k = 0; k < 2; ++k) {
         for (unsigned long long* b : {&s_kfull[k], &s_vfull[k], &s_sfull[k][0], &s_sfull[k][1], &s_odone[k][0],
-                                      &s_odone[k][1], &s_sread[k], &s_pfull[k], &s_drain[k], &s_zero[k]})
+                                      &s_odone[k][1], &s_sread[k], &s_pfull[k], &s_qfull[k], &s_drain[k],
+                                      &s_zero[k]})
           mbar_inval(smem_u32(b));
       }
     for (int k = 0; k < 2; ++k) {
@@ -240,38 +271,18 @@ __global__ void __launch_bounds__(pfx::kThreads, 1)
       }
       mbar_init(smem_u32(&s_sread[k]), 128);
       mbar_init(smem_u32(&s_pfull[k]), 128);
+      mbar_init(smem_u32(&s_qfull[k]), 128);
       mbar_init(smem_u32(&s_drain[k]), 1);
       mbar_init(smem_u32(&s_zero[k]), 128);
     }
     fence_mbar_init();
-  }
-  __syncthreads();
-  for (int p = tid; p < np; p += pfx::kThreads)
-    if (block_of(p) < 0) {
-      flag(a.dev_status, SV_DEV_BAD_BLOCK_ID);
-      s_bad = 1;
-    }
-  // Q rows, K-major with the 128-byte swizzle, zeros past the unit's rows
-  const bool real = tid < vrows;
-  if (tid < 128 * ntile) {
-    const int v = v0 + min(tid, vrows - 1);
-    const int4* src = reinterpret_cast<const int4*>(
-        a.q + ((size_t)a.arows[gr.x + v / group] * a.Hq + g * group + v % group) * D);
-    const int t = tid & 127;
-#pragma unroll
-    for (int c = 0; c < D / 8; ++c) {
-      const int4 x = real ? __ldg(src + c) : make_int4(0, 0, 0, 0);
-      const uint32_t off = (uint32_t)((tid >> 7) * S::kTile + (c >> 3) * S::kHalf + t * 128 +
-                                      (((c & 7) ^ (t & 7)) << 4));
-      *reinterpret_cast<int4*>(base_ptr + off) = x;
-    }
-    fence_proxy_async_smem();
   }
   tc5::fence_before_sync();
   __syncthreads();
   tc5::fence_after_sync();
   const uint32_t tmem = s_tmem;
 
+  const bool real = tid < vrows;
   if (warp == 8 || warp == 9) {
     // --------------------------------------------------------- producers --
     const int half = warp - 8;  // 0: K, 1: V
@@ -292,6 +303,8 @@ __global__ void __launch_bounds__(pfx::kThreads, 1)
       if (__any_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&s_abort))) break;
       const int b = next;
       next = lane < kStagePages ? block_of((st + 1) * kStagePages + lane) : -1;
+      if (half == 0 && lane < kStagePages && st * kStagePages + lane < np && b < 0)
+        flag(a.dev_status, SV_DEV_BAD_BLOCK_ID);
       const uint32_t bar = smem_u32(&fullb[slot]);
       const int n = __popc(__ballot_sync(0xffffffffu, b >= 0));
       if (lane == 0) {
@@ -336,7 +349,7 @@ __global__ void __launch_bounds__(pfx::kThreads, 1)
         tc5::commit(smem_u32(&s_sfull[t][st & 1]));
         return true;
       };
-      bool ok = qk(0);
+      bool ok = mbar_wait_bounded(smem_u32(&s_qfull[t]), 0u) && qk(0);
       for (int st = 0; st < n_stage && ok; ++st) {
         if (st + 1 < n_stage && !(ok = qk(st + 1))) break;
         // V has landed, P is there
@@ -364,6 +377,25 @@ __global__ void __launch_bounds__(pfx::kThreads, 1)
     const uint32_t ts = tmem + lane_base, tp = ts + pfx::kColP + (uint32_t)(t * 64);
     const uint32_t to = tmem + lane_base + pfx::kColO + (uint32_t)(t * 128);
     const float sc = a.scale_log2;
+    {
+      // Q row, K-major with the 128-byte swizzle, zeros past the list's rows
+      const int v = v0 + min(tid, vrows - 1), row = tid & 127;
+      const int4* src = reinterpret_cast<const int4*>(
+          a.q + ((size_t)a.arows[gr.x + v / group] * a.Hq + g * group + v % group) * D);
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c) {
+        const int4 x = real ? __ldg(src + c) : make_int4(0, 0, 0, 0);
+        const uint32_t off = (uint32_t)(t * S::kTile + (c >> 3) * S::kHalf + row * 128 + (((c & 7) ^ (row & 7)) << 4));
+        *reinterpret_cast<int4*>(base_ptr + off) = x;
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(smem_u32(&s_qfull[t]));
+    }
+    // pages of the next stage that are there
+    auto there = [&](int st) {
+      return __ballot_sync(0xffffffffu, lane < kStagePages && block_of(st * kStagePages + lane) >= 0);
+    };
+    uint32_t pages1 = there(0);
     float m_ref = -INFINITY, l = 0.f;
     // PV of the stage before has landed: O may be rescaled, P overwritten
     auto pv_done = [&](int st) -> bool {
@@ -375,6 +407,8 @@ __global__ void __launch_bounds__(pfx::kThreads, 1)
     uint32_t zeroed = 0u;  // parity of the incomplete stages so far in each V slot
     bool ok = true;
     for (int st = 0; st < n_stage; ++st) {
+      const uint32_t pages = pages1;
+      pages1 = there(st + 1);
       const bool got = mbar_wait_bounded(smem_u32(&s_sfull[t][st & 1]), (uint32_t)((st >> 1) & 1));
       if (!__all_sync(0xffffffffu, got)) {
         ok = false;
@@ -385,9 +419,7 @@ __global__ void __launch_bounds__(pfx::kThreads, 1)
       tc5::tmem_ld_x128(ts, s);
       tc5::fence_before_sync();
       mbar_arrive(smem_u32(&s_sread[t]));
-      if (s_bad) {
-        // pages of the stage that are there
-        const uint32_t pages = __ballot_sync(0xffffffffu, lane < kStagePages && block_of(st * kStagePages + lane) >= 0);
+      {
         if (pages != 0xffu) {
 #pragma unroll
           for (int j = 0; j < kTok; ++j)
@@ -525,6 +557,7 @@ inline Args prefix_args(const sv_paged_kv* kv, const sv_batch* bt, const sv_shar
   a.aoff = take<int>(at, off, bt->n_req + 1);
   a.groups = take<int4>(at, off, sp->n_groups);
   a.gstage = take<int>(at, off, sp->n_groups + 1);
+  a.pstart = take<PStart>(at, off, a.ctas);
   // the row tiles of all groups
   a.plists = (int)(((long)bt->total_rows * a.group / kPrefixRows + sp->n_groups) * a.Hkv);
   a.pml = take<float>(at, off, (size_t)(a.plists + a.ctas) * kPrefixRows * 2);

@@ -353,6 +353,10 @@ __device__ __forceinline__ bool mbar_wait_sleep_bounded(uint32_t bar, uint32_t p
   }
   return false;
 }
+// Fetches a tensor map before its first use.
+__device__ __forceinline__ void prefetch_map(const void* tmap) {
+  asm volatile("prefetch.tensormap [%0];\n" ::"l"(tmap) : "memory");
+}
 // 2-D tiled TMA load of one box into shared memory, completing on `bar`.
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* tmap, int x, int y,
                                             uint32_t bar) {

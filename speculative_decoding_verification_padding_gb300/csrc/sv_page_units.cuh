@@ -46,6 +46,13 @@ struct Header {
   int pad[58];
 };
 
+// Where a CTA's share of the prefix stages begins: group, list of the group and
+// stage of the list; the group's lists, record and first request.
+struct __align__(16) PStart {
+  int4 gr;
+  int k, list, st0, lists, leader, pad[3];
+};
+
 struct Req;
 struct Args {
   sv_batch bt;
@@ -82,6 +89,7 @@ struct Args {
   int* aoff;          // [n_req + 1] first active row of each request
   int4* groups;       // [n_groups] first active row, active rows, pages, first prefix list
   int* gstage;        // [n_groups + 1] first stage of each group's prefix lists
+  PStart* pstart;     // [ctas]
   int plists;         // prefix lists at most: 256-row tiles x KV heads
   float* pml;         // [plists + ctas][kPrefixRows][2]
   float* po;          // [plists + ctas][D / 4][kPrefixRows][4]
@@ -247,7 +255,6 @@ template <int D, bool SPARSE>
 __global__ void __launch_bounds__(unit::kThreads, 1)
     unit_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap tmK,
                 const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmQ) {
-  griddep_entry();
   using unit::kLists;
   using unit::Rec;
   using S = unit::Smem<D>;
@@ -264,13 +271,12 @@ __global__ void __launch_bounds__(unit::kThreads, 1)
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   __shared__ int s_issued[6];  // phases begun of s_kfull, s_vfull, s_qfull
-  const int W = a.hdr->W, C = a.hdr->C;
   const int c = blockIdx.x;
-  if (c >= C) return;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* base_ptr = smem_raw + (base - smem_u32(smem_raw));
   const uint32_t ring = base + 2 * S::kTile;  // Q of two lists, then K slots, V slots
+  // nothing that earlier kernels write is read before griddep_entry()
   if (tid == 0) {
     s_abort = 0;
     for (int k = 0; k < 6; ++k) s_issued[k] = 0;
@@ -291,6 +297,12 @@ __global__ void __launch_bounds__(unit::kThreads, 1)
     fence_mbar_init();
   }
   if (warp == 4) {
+    if (lane == 0) {
+      prefetch_map(&tmK);
+      prefetch_map(&tmV);
+      prefetch_map(&tmQ);
+    }
+    __syncwarp();
     tc5::tmem_alloc(smem_u32(&s_tmem), unit::kCols);
     tc5::tmem_relinquish();
   }
@@ -298,6 +310,12 @@ __global__ void __launch_bounds__(unit::kThreads, 1)
   __syncthreads();
   tc5::fence_after_sync();
   const uint32_t tmem = s_tmem;
+  griddep_entry();
+  const int W = a.hdr->W, C = a.hdr->C, x_start = a.start[c];
+  if (c >= C) {
+    if (warp == 4) tc5::tmem_dealloc(tmem, unit::kCols);
+    return;
+  }
   auto gone = [&] { return *reinterpret_cast<volatile int*>(&s_abort) != 0; };
   // the record of list L, by a whole warp (or by one thread); null: gave up
   auto list_at = [&](int L) -> const Rec* {
@@ -316,15 +334,17 @@ __global__ void __launch_bounds__(unit::kThreads, 1)
   if (warp == 7) {
     // ------------------------------------------------------- lists ahead --
     const int s_end = share_start(c + 1, W, C);
-    int s_at = share_start(c, W, C), x = a.start[c], L = 0;
+    int s_at = share_start(c, W, C), x = x_start, L = 0;
     bool ok = true;
     for (;; ++x) {
       Rec r{};
       if (s_at < s_end) {
         const int off0 = a.off[x], off1 = a.off[x + 1];
+        const Tile tl = a.tiles[x / a.Hkv];
+        r.ncomp = SPARSE ? a.cnt[2 * x] : tl.ncomp;
+        r.nent = SPARSE ? a.cnt[2 * x + 1] : tl.nent;
         r.n_stage = min(s_end, off1) - s_at;
         if (r.n_stage <= 0) continue;  // an empty list
-        const Tile tl = a.tiles[x / a.Hkv];
         r.x = x;
         r.g = x % a.Hkv;
         r.e_first = kStagePages * (s_at - off0);
@@ -334,12 +354,17 @@ __global__ void __launch_bounds__(unit::kThreads, 1)
         r.nr = tl.nr;
         r.ctx = tl.ctx;
         r.first = tl.first;
-        r.ncomp = SPARSE ? a.cnt[2 * x] : tl.ncomp;
-        r.nent = SPARSE ? a.cnt[2 * x + 1] : tl.nent;
         r.lim = tl.r0 + tl.nr;
         r.r0 = tl.r0;
         r.grp = tl.grp;
         s_at += r.n_stage;
+        const int e_end = min(r.nent, r.e_first + r.n_stage * kStagePages);
+        const bool tail = e_end > r.ncomp;  // the tail is among it
+        int par[kMaxRows / 32];
+#pragma unroll
+        for (int k = 0; k < kMaxRows / 32; ++k)
+          par[k] = tail && lane + 32 * k < tl.rows ? a.bt.parent[tl.cu + lane + 32 * k] : -1;
+        const int b0 = block_of(r, r.e_first + lane);
         if (L >= kLists &&
             !mbar_wait_bounded(smem_u32(&s_lfree[L % kLists]), (uint32_t)((L / kLists - 1) & 1)))
           ok = false;
@@ -347,19 +372,14 @@ __global__ void __launch_bounds__(unit::kThreads, 1)
           ok = false;
           break;
         }
-        const int e_end = min(r.nent, r.e_first + r.n_stage * kStagePages);
-        bool bad = false;
-        for (int e = r.e_first + lane; e < e_end; e += 32) {
-          const int b = block_of(r, e);
-          bad |= b < 0;
-          if (e < r.e_first + kStagePages) s_ids[L % kLists][e - r.e_first] = b;
-        }
-        for (int e = e_end + lane; e < r.e_first + kStagePages; e += 32)
-          s_ids[L % kLists][e - r.e_first] = -1;
+        if (lane < kStagePages) s_ids[L % kLists][lane] = b0;
+        bool bad = r.e_first + lane < e_end && b0 < 0;
+        for (int e = r.e_first + 32 + lane; e < e_end; e += 32) bad |= block_of(r, e) < 0;
         if (bad) flag(a.dev_status, SV_DEV_BAD_BLOCK_ID);
         r.bad = __any_sync(0xffffffffu, bad);
-        if (e_end > r.ncomp) {  // the tail is among it
-          for (int j = lane; j < tl.rows; j += 32) s_par[j] = a.bt.parent[tl.cu + j];
+        if (tail) {
+#pragma unroll
+          for (int k = 0; k < kMaxRows / 32; ++k) s_par[lane + 32 * k] = par[k];
           __syncwarp();
           for (int t = lane; t < tl.nr; t += 32) {
             unsigned long long lo = 0ull, hi = 0ull;
@@ -740,25 +760,31 @@ __global__ void __launch_bounds__(unit::kThreads, 1)
 
 // One CTA takes 32 rows of a list, a lane a row, a warp D / 8 columns: the parts of
 // the row -- of the CTAs that shared its list and, in prefix calls, those that
-// shared its group's prefix -- in one online pass, two of them in flight.
+// shared its group's prefix -- in one online pass, kLoads of them in flight.  Where
+// there are at most 16 rows, `slices` lanes share a row, each with every so many-th
+// part, and join by shuffles.
 constexpr int kMergeThreads = 256;
 constexpr int kPrefixRows = 256;  // virtual rows of a prefix list
 template <int D, bool SPARSE>
 __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_constant__ Args a) {
   griddep_entry();
   constexpr int kQuads = D / 32;  // of a warp
+  constexpr int kLoads = 4;
   const int x = blockIdx.x;
-  const Header h = *a.hdr;
-  if (x >= h.T * a.Hkv) return;
+  const int T = a.hdr->T, W = a.hdr->W, C = a.hdr->C, Wp = a.hdr->Wp, Cp = a.hdr->Cp;
+  if (x >= T * a.Hkv) return;
   const int off0 = a.off[x], off1 = a.off[x + 1];
   const Tile tl = a.tiles[x / a.Hkv];
   if (off0 == off1) return;
   const int g = x % a.Hkv, group = a.group;
+  const int vr0 = blockIdx.y * 32, vrows = tl.nr * group;
+  if (vr0 >= vrows) return;
   const int lane = threadIdx.x & 31, c4 = (threadIdx.x >> 5) * kQuads;
-  const int vr = blockIdx.y * 32 + lane, vrows = tl.nr * group;
-  if ((int)blockIdx.y * 32 >= vrows) return;
-  const int c0 = share_of(off0, h.W, h.C), ns = share_of(off1 - 1, h.W, h.C) - c0 + 1;
-  const int vs = min(vr, vrows - 1);
+  int rows2 = 1;  // rows of the block, rounded up to a power of two
+  while (rows2 < 32 && rows2 < vrows - vr0) rows2 *= 2;
+  const int slices = 32 / rows2, slice = lane / rows2;
+  const int vr = vr0 + lane % rows2, vs = min(vr, vrows - 1);
+  const int c0 = share_of(off0, W, C), ns = share_of(off1 - 1, W, C) - c0 + 1;
   int np = 0, p0 = 0, pv = 0;
   if (!SPARSE) {
     const int4 grp = a.groups[tl.grp];
@@ -766,8 +792,8 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_const
       const int v = (tl.arow - grp.x) * group + vs;  // among the group's virtual rows
       const int list = v / kPrefixRows * a.Hkv + g, sp = (grp.z + kStagePages - 1) / kStagePages;
       const int s0 = a.gstage[tl.grp] + list * sp;
-      const int cp = share_of(s0, h.Wp, h.Cp);
-      np = share_of(s0 + sp - 1, h.Wp, h.Cp) - cp + 1;
+      const int cp = share_of(s0, Wp, Cp);
+      np = share_of(s0 + sp - 1, Wp, Cp) - cp + 1;
       p0 = cp + grp.w + list;
       pv = v % kPrefixRows;
     }
@@ -778,12 +804,27 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_const
   float4 acc[kQuads];
 #pragma unroll
   for (int j = 0; j < kQuads; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int k0 = 0; k0 < n; k0 += 2) {
-    float2 ml2[2];
-    float4 o4[2][kQuads];
+  auto join = [&](float m2, float l2, const float4 (&o2)[kQuads]) {
+    const float nm = fmaxf(Mx, m2);
+    if (nm == -INFINITY) return;
+    const float s_old = exp2f(Mx - nm), s_new = exp2f(m2 - nm);
+    L = L * s_old + l2 * s_new;
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int s = min(k0 + k, n - 1);
+    for (int j = 0; j < kQuads; ++j) {
+      acc[j].x = acc[j].x * s_old + o2[j].x * s_new;
+      acc[j].y = acc[j].y * s_old + o2[j].y * s_new;
+      acc[j].z = acc[j].z * s_old + o2[j].z * s_new;
+      acc[j].w = acc[j].w * s_old + o2[j].w * s_new;
+    }
+    Mx = nm;
+  };
+  for (int k0 = slice; k0 < n; k0 += kLoads * slices) {
+    float2 ml2[kLoads];
+    float4 o4[kLoads][kQuads];
+#pragma unroll
+    for (int k = 0; k < kLoads; ++k) {
+      const int s = k0 + k * slices;
+      if (s >= n) break;
       const bool own = SPARSE || s < ns;
       const size_t slot = own ? (size_t)(c0 + s + x) : (size_t)(p0 + s - ns);
       const int rows = own ? a.tile_vr : kPrefixRows, row = own ? vs : pv;
@@ -793,22 +834,25 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_const
       for (int j = 0; j < kQuads; ++j) o4[k][j] = __ldcg(o + (size_t)j * rows);
     }
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const float nm = fmaxf(Mx, ml2[k].x);
-      if (k0 + k >= n || nm == -INFINITY) continue;
-      const float s_old = exp2f(Mx - nm), s_new = exp2f(ml2[k].x - nm);
-      L = L * s_old + ml2[k].y * s_new;
-#pragma unroll
-      for (int j = 0; j < kQuads; ++j) {
-        acc[j].x = acc[j].x * s_old + o4[k][j].x * s_new;
-        acc[j].y = acc[j].y * s_old + o4[k][j].y * s_new;
-        acc[j].z = acc[j].z * s_old + o4[k][j].z * s_new;
-        acc[j].w = acc[j].w * s_old + o4[k][j].w * s_new;
-      }
-      Mx = nm;
+    for (int k = 0; k < kLoads; ++k) {
+      if (k0 + k * slices >= n) break;
+      join(ml2[k].x, ml2[k].y, o4[k]);
     }
   }
-  if (vr >= vrows) return;
+  __syncwarp();
+  for (int o = rows2; o < 32; o <<= 1) {
+    const float m2 = __shfl_xor_sync(0xffffffffu, Mx, o), l2 = __shfl_xor_sync(0xffffffffu, L, o);
+    float4 o2[kQuads];
+#pragma unroll
+    for (int j = 0; j < kQuads; ++j) {
+      o2[j].x = __shfl_xor_sync(0xffffffffu, acc[j].x, o);
+      o2[j].y = __shfl_xor_sync(0xffffffffu, acc[j].y, o);
+      o2[j].z = __shfl_xor_sync(0xffffffffu, acc[j].z, o);
+      o2[j].w = __shfl_xor_sync(0xffffffffu, acc[j].w, o);
+    }
+    join(m2, l2, o2);
+  }
+  if (vr >= vrows || slice != 0) return;
   const float inv = L > 0.f ? 1.f / L : 0.f;
   const size_t row = (size_t)(tl.cu + tl.r0 + vr / group) * a.Hq + g * group + vr % group;
   uint4* dst = reinterpret_cast<uint4*>(a.out + row * D + c4 * 4);
