@@ -19,22 +19,77 @@
 namespace sv {
 namespace pu {
 
+constexpr int kPlanThreads = 1024;
+// Requests and groups whose records the plan keeps in shared memory; with more of
+// them they are in the workspace.
+constexpr int kPlanRequests = 512, kPlanGroups = 256;
+
+struct PlanSmem {
+  Req req[kPlanRequests];
+  int4 groups[kPlanGroups];
+  int cu_groups[kPlanGroups + 1], prefix_len[kPlanGroups], gstage[kPlanGroups + 1];
+};
+
 __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_constant__ Args a) {
   griddep_entry();
-  __shared__ int s_warp[32], s_tiles, s_stages, s_rows, s_lists, s_pstages, s_groups_bad;
   extern __shared__ __align__(16) uint8_t s_mem[];
+  __shared__ int s_tiles, s_stages, s_rows, s_groups_bad;
+  PlanSmem& sm = *reinterpret_cast<PlanSmem*>(s_mem);
   const int R = a.bt.n_req, G = a.n_groups, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  Req* req = R <= kPlanRequests ? reinterpret_cast<Req*>(s_mem) : a.req;
-  if (tid == 0) {
-    s_tiles = s_stages = s_rows = s_lists = s_pstages = 0;
-    if (a.bt.cu_rows[0] != 0 || a.bt.cu_rows[R] != a.bt.total_rows) flag(a.dev_status, SV_DEV_BAD_WINDOW);
-    s_groups_bad = a.cu_groups[0] != 0 || a.cu_groups[G] != R;
-  }
+  const bool small = R <= kPlanRequests && G <= kPlanGroups;  // in shared memory
+  Req* req = small ? sm.req : a.req;
+  int4* groups = small ? sm.groups : a.groups;
+  int* gstage = small ? sm.gstage : a.gstage;
+  const int32_t* cu_groups = small ? sm.cu_groups : a.cu_groups;
+  const int32_t* prefix_len = small ? sm.prefix_len : a.prefix_len;
+  if (tid == 0) s_groups_bad = 0;
   __syncthreads();
   // groups that do not cut the requests into runs: nothing is attended
-  for (int k = tid; k < G; k += blockDim.x)
-    if (a.cu_groups[k] > a.cu_groups[k + 1]) s_groups_bad = 1;
-  check_requests(a, req);
+  for (int k = tid; k <= G; k += blockDim.x) {
+    const int v = a.cu_groups[k], next = k < G ? a.cu_groups[k + 1] : R;
+    if (small) sm.cu_groups[k] = v;
+    if (small && k < G) sm.prefix_len[k] = a.prefix_len[k];
+    if ((k == 0 && v != 0) || (k < G ? v > next : v != R)) s_groups_bad = 1;
+  }
+  // windows, parents and lengths, 16 lanes a request; what cannot be attended is
+  // reported and left out
+  constexpr int kLanes = 16;
+  for (int i0 = 0; i0 < R; i0 += kPlanThreads / kLanes) {
+    const int i = i0 + tid / kLanes, l = tid % kLanes;
+    Window w{};
+    int ctx = 0;
+    bool bad = false;
+    if (i < R) {
+      w = window_of(a.bt, i);
+      ctx = a.lens[i];
+      if (w.ok) {
+#pragma unroll
+        for (int k = 0; k < kMaxRows / kLanes; ++k) {
+          const int j = l + kLanes * k;
+          if (j < w.rows) {
+            const int p = a.bt.parent[w.cu + j];
+            bad |= j == 0 ? p != -1 : (p < 0 || p >= j);
+          }
+        }
+      }
+    }
+    bad = (__ballot_sync(0xffffffffu, bad) >> (lane & 16)) & 0xffffu;
+    if (i >= R || l != 0) continue;
+    const bool fits = ctx >= 0 && (long)ctx + w.rows <= (long)a.max_blocks * kBlockSize;
+    if (!w.ok) flag(a.dev_status, SV_DEV_BAD_WINDOW);
+    else if (bad) flag(a.dev_status, SV_DEV_BAD_PARENT);
+    else if (!fits) flag(a.dev_status, SV_DEV_BAD_LENGTH);
+    Req r{};
+    r.cu = w.cu;
+    r.rows = w.rows;
+    r.b = w.b;
+    r.e = w.ok && !bad && fits ? max(w.b, w.e) : w.b;  // (a window behind the verified rows is empty)
+    r.ctx = ctx;
+    req[i] = r;
+  }
+  if (tid == 0 && (a.bt.cu_rows[0] != 0 || a.bt.cu_rows[R] != a.bt.total_rows))
+    flag(a.dev_status, SV_DEV_BAD_WINDOW);
+  __syncthreads();
   if (s_groups_bad) {
     if (tid == 0) {
       flag(a.dev_status, SV_DEV_BAD_PARAM);
@@ -42,36 +97,69 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
     }
     return;
   }
-  for (int base = 0; base < R; base += blockDim.x) {
-    const int i = base + tid;
-    Req r{};
-    int nt = 0, stages = 0;
-    if (i < R) {
-      r = req[i];
-      r.grp = find_segment(a.cu_groups, G, i);
-      const int p = a.prefix_len[r.grp];
-      if (p < 0 || p % kBlockSize != 0) {
-        if (r.e > r.b) flag(a.dev_status, SV_DEV_BAD_PARAM);
-        r.e = r.b;
-      } else if (p > r.ctx) {
-        if (r.e > r.b) flag(a.dev_status, SV_DEV_BAD_LENGTH);
-        r.e = r.b;
-      }
-      r.first = p / kBlockSize;
-      nt = (r.e - r.b + a.rt - 1) / a.rt;
-      for (int k = 0; k < nt; ++k) {
-        const int last = min(r.b + (k + 1) * a.rt, r.e);
-        stages += ((r.ctx + last + kBlockSize - 1) / kBlockSize - r.first + kStagePages - 1) / kStagePages;
-      }
+  // the request's group, tiles and stages
+  auto stages_of = [&](const Req& r, int k) {  // of its tile k
+    return ((r.ctx + min(r.b + (k + 1) * a.rt, r.e) + kBlockSize - 1) / kBlockSize - r.first + kStagePages - 1) /
+           kStagePages;
+  };
+  for (int i = tid; i < R; i += blockDim.x) {
+    Req r = req[i];
+    int lo = 0;
+    for (int hi = G - 1; lo < hi;) {  // the last group that begins at or before i
+      const int mid = (lo + hi + 1) >> 1;
+      if (cu_groups[mid] <= i) lo = mid; else hi = mid - 1;
     }
-    r.tile = block_scan(nt, s_warp, &s_tiles);
-    r.stage = block_scan(stages, s_warp, &s_stages);
-    r.arow = block_scan(r.e - r.b, s_warp, &s_rows);
-    if (i < R) {
-      req[i] = r;
-      a.aoff[i] = r.arow;
+    const int p = prefix_len[lo];
+    if (r.e > r.b && (p < 0 || p % kBlockSize != 0 || p > r.ctx)) {
+      flag(a.dev_status, p < 0 || p % kBlockSize != 0 ? SV_DEV_BAD_PARAM : SV_DEV_BAD_LENGTH);
+      r.e = r.b;
+    }
+    r.grp = lo;
+    r.first = p / kBlockSize;
+    const int nt = (r.e - r.b + a.rt - 1) / a.rt;
+    r.tile = nt;  // counts, for now
+    r.stage = 0;
+    for (int k = 0; k < nt; ++k) r.stage += stages_of(r, k);
+    r.arow = r.e - r.b;
+    req[i] = r;
+  }
+  __syncthreads();
+  // offsets of all three, by one warp, a run of requests a lane
+  if (warp == 0) {
+    const int per = (R + 31) / 32, i0 = min(R, lane * per), i1 = min(R, i0 + per);
+    int c[3] = {0, 0, 0}, at[3];
+    for (int i = i0; i < i1; ++i) {
+      c[0] += req[i].tile;
+      c[1] += req[i].stage;
+      c[2] += req[i].arow;
+    }
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      int x = c[k];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      at[k] = x - c[k];
+      c[k] = __shfl_sync(0xffffffffu, x, 31);
+    }
+    for (int i = i0; i < i1; ++i) {
+      const int t = req[i].tile, s = req[i].stage, n = req[i].arow;
+      req[i].tile = at[0];
+      req[i].stage = at[1];
+      req[i].arow = at[2];
+      at[0] += t;
+      at[1] += s;
+      at[2] += n;
+    }
+    if (lane == 0) {
+      s_tiles = c[0];
+      s_stages = c[1];
+      s_rows = c[2];
     }
   }
+  __syncthreads();
   // (offsets that overlap could ask for more than there is; such a call is left out)
   if (s_tiles > a.tiles_cap || s_rows > a.bt.total_rows) {
     if (tid == 0) {
@@ -80,73 +168,99 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
     }
     return;
   }
-  const int T = s_tiles, W = s_stages * a.Hkv;
-  const int C = min(a.ctas, W);
-  if (tid == 0) {
-    a.hdr->T = T;
-    a.hdr->W = W;
-    a.hdr->C = C;
-    a.off[(size_t)T * a.Hkv] = W;
-    a.aoff[R] = s_rows;
-  }
-  __syncthreads();
-  write_tiles(a, req);
-  // first stages of the lists, the active rows
-  for (int i = warp; i < R; i += blockDim.x >> 5) {
-    const Req r = req[i];
-    for (int k = lane; k < r.e - r.b; k += 32) a.arows[r.arow + k] = r.cu + r.b + k;
-    int stage = r.stage * a.Hkv;
-    for (int k = 0, b = r.b; b < r.e; ++k, b += a.rt) {
-      const int n = ((r.ctx + min(b + a.rt, r.e) + kBlockSize - 1) / kBlockSize - r.first + kStagePages - 1) /
-                    kStagePages;
-      for (int g = lane; g < a.Hkv; g += 32) {
-        const int x = (r.tile + k) * a.Hkv + g;
-        a.off[x] = stage + g * n;
-        deal_list(a, x, stage + g * n, stage + (g + 1) * n, W, C);
-      }
-      stage += a.Hkv * n;
+  const int W = s_stages * a.Hkv, C = min(a.ctas, W);
+  if (warp > 0) {
+    // tiles, first stages of their lists, active rows: a warp a request
+    if (tid == 32) {
+      a.hdr->T = s_tiles;
+      a.hdr->W = W;
+      a.hdr->C = C;
+      a.off[(size_t)s_tiles * a.Hkv] = W;
     }
+    for (int i = warp - 1; i < R; i += kPlanThreads / 32 - 1) {
+      const Req r = req[i];
+      for (int k = lane; k < r.e - r.b; k += 32) a.arows[r.arow + k] = r.cu + r.b + k;
+      int stage = r.stage * a.Hkv;
+      for (int k = 0, b = r.b; b < r.e; ++k, b += a.rt) {
+        const int n = stages_of(r, k);
+        for (int g = lane; g < a.Hkv; g += 32) {
+          const int x = (r.tile + k) * a.Hkv + g;
+          a.off[x] = stage + g * n;
+          deal_list(a, x, stage + g * n, stage + (g + 1) * n, W, C);
+        }
+        stage += a.Hkv * n;
+        if (lane == 0) {
+          Tile t{};
+          t.i = i;
+          t.cu = r.cu;
+          t.ctx = r.ctx;
+          t.r0 = b;
+          t.nr = min(a.rt, r.e - b);
+          t.rows = r.rows;
+          t.first = r.first;
+          t.ncomp = r.ctx / kBlockSize - r.first;
+          t.nent = (r.ctx + b + t.nr + kBlockSize - 1) / kBlockSize - r.first;
+          t.arow = r.arow + k * a.rt;
+          t.grp = r.grp;
+          a.tiles[r.tile + k] = t;
+        }
+      }
+    }
+    return;
   }
   // groups: first active row, active rows, pages; their lists, one a 256-row tile
   // and KV head, and the lists' stages
-  for (int base = 0; base < G; base += blockDim.x) {
-    const int k = base + tid;
+  auto arow = [&](int i) { return i < R ? req[i].arow : s_rows; };
+  int lists = 0, stages = 0;
+  for (int base = 0; base < G; base += 32) {
+    const int k = base + lane;
     int4 gr = make_int4(0, 0, 0, 0);
-    int n = 0, sp = 0;
+    int n = 0, s = 0;
     if (k < G) {
-      gr.x = a.aoff[a.cu_groups[k]];
-      gr.y = a.aoff[a.cu_groups[k + 1]] - gr.x;
-      gr.z = gr.y > 0 ? a.prefix_len[k] / kBlockSize : 0;  // checked by its requests
+      gr.x = arow(cu_groups[k]);
+      gr.y = arow(cu_groups[k + 1]) - gr.x;
+      gr.z = gr.y > 0 ? prefix_len[k] / kBlockSize : 0;  // checked by its requests
       n = gr.z > 0 ? (gr.y * a.group + kPrefixRows - 1) / kPrefixRows * a.Hkv : 0;
-      sp = (gr.z + kStagePages - 1) / kStagePages;
+      s = n * ((gr.z + kStagePages - 1) / kStagePages);
     }
-    gr.w = block_scan(n, s_warp, &s_lists);
-    const int stage = block_scan(n * sp, s_warp, &s_pstages);
+    int x = n, y = s;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, x, o), v = __shfl_up_sync(0xffffffffu, y, o);
+      if (lane >= o) { x += u; y += v; }
+    }
+    gr.w = lists + x - n;
     if (k < G) {
-      a.groups[k] = gr;
-      a.gstage[k] = stage;
+      groups[k] = gr;
+      gstage[k] = stages + y - s;
+      if (small) {
+        a.groups[k] = gr;
+        a.gstage[k] = stages + y - s;
+      }
     }
+    lists += __shfl_sync(0xffffffffu, x, 31);
+    stages += __shfl_sync(0xffffffffu, y, 31);
   }
-  const int Wp = s_pstages, Cp = min(a.ctas, Wp);
-  if (tid == 0) {
+  const int Wp = stages, Cp = min(a.ctas, Wp);
+  if (lane == 0) {
     a.gstage[G] = Wp;
     a.hdr->Wp = Wp;
     a.hdr->Cp = Cp;
   }
-  __syncthreads();
-  for (int c = tid; c < Cp; c += blockDim.x) {
+  __syncwarp();
+  for (int c = lane; c < Cp; c += 32) {
     const int s = share_start(c, Wp, Cp);
     PStart ps;
     ps.k = 0;  // the last group whose stages begin at or before s
     for (int hi = G - 1; ps.k < hi;) {
       const int mid = (ps.k + hi + 1) >> 1;
-      if (a.gstage[mid] <= s) ps.k = mid; else hi = mid - 1;
+      if (gstage[mid] <= s) ps.k = mid; else hi = mid - 1;
     }
-    ps.gr = a.groups[ps.k];
+    ps.gr = groups[ps.k];
     const int sp = (ps.gr.z + kStagePages - 1) / kStagePages;
-    ps.list = (s - a.gstage[ps.k]) / sp;
-    ps.st0 = (s - a.gstage[ps.k]) % sp;
-    ps.leader = a.cu_groups[ps.k];
+    ps.list = (s - gstage[ps.k]) / sp;
+    ps.st0 = (s - gstage[ps.k]) % sp;
+    ps.leader = cu_groups[ps.k];
     ps.lists = (ps.gr.y * a.group + kPrefixRows - 1) / kPrefixRows * a.Hkv;
     a.pstart[c] = ps;
   }
@@ -554,7 +668,7 @@ inline Args prefix_args(const sv_paged_kv* kv, const sv_batch* bt, const sv_shar
   a.cu_groups = sp->cu_groups;
   a.prefix_len = sp->prefix_len;
   a.arows = take<int>(at, off, bt->total_rows);
-  a.aoff = take<int>(at, off, bt->n_req + 1);
+  a.req = take<Req>(at, off, bt->n_req);
   a.groups = take<int4>(at, off, sp->n_groups);
   a.gstage = take<int>(at, off, sp->n_groups + 1);
   a.pstart = take<PStart>(at, off, a.ctas);
@@ -572,7 +686,7 @@ sv_status prefix_attend(const Args& a, const void* k, const void* v, cudaStream_
     return SV_ERR_CUDA;
   static PerDevice set;
   if (smem_limit_once(set, prefix_kernel<D>, pfx::Smem<D>::kAsk) != cudaSuccess) return SV_ERR_CUDA;
-  if (sv::launch(prefix_plan_kernel, 1, kPlanThreads, plan_smem(a), stream, a) != cudaSuccess ||
+  if (sv::launch(prefix_plan_kernel, 1, kPlanThreads, sizeof(PlanSmem), stream, a) != cudaSuccess ||
       sv::launch(prefix_kernel<D>, a.ctas, pfx::kThreads, pfx::Smem<D>::kAsk, stream, a, tmK, tmV) != cudaSuccess)
     return SV_ERR_CUDA;
   return launch_units<D, false>(a, tmK, tmV, stream);

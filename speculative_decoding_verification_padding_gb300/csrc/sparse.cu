@@ -6,12 +6,10 @@
 // is on none of the pages and fixed in the header.
 //
 // Launches:
-//   plan   (1 CTA) checks the requests and cuts their rows into tiles of up to
-//          128 virtual rows;
-//   build  (1 CTA a (tile, KV head)) the union of the rows' page lists as block
-//          ids, in page order, with a bit a row and entry for who sees it: a page
-//          that several rows of a tile chose is read once.  The last CTA deals the
-//          lists' stages out;
+//   build  (1 CTA a (tile, KV head)) checks the requests, cuts their rows into tiles
+//          of up to 128 virtual rows and makes each list: the union of the rows'
+//          page lists as block ids, in page order, with a bit a row and entry for
+//          who sees it -- a page that several rows of a tile chose is read once;
 //   units, merge (sv_page_units.cuh).
 
 #include "sv_page_units.cuh"
@@ -22,75 +20,96 @@ namespace pu {
 constexpr int kMaxTable = 1 << 18;  // table entries a request may have (bits in shared memory)
 constexpr int kBuildThreads = 256;
 
-__global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const __grid_constant__ Args a) {
-  griddep_entry();
-  __shared__ int s_warp[32], s_tiles;
-  extern __shared__ __align__(16) uint8_t s_mem[];
-  const int R = a.bt.n_req, tid = threadIdx.x;
-  Req* req = R <= kPlanRequests ? reinterpret_cast<Req*>(s_mem) : a.req;
-  if (tid == 0) {
-    s_tiles = 0;
-    if (a.bt.cu_rows[0] != 0 || a.bt.cu_rows[R] != a.bt.total_rows) flag(a.dev_status, SV_DEV_BAD_WINDOW);
-  }
-  check_requests(a, req);
-  for (int base = 0; base < R; base += blockDim.x) {
-    const int i = base + tid;
-    const int nt = i < R ? (req[i].e - req[i].b + a.rt - 1) / a.rt : 0;
-    const int at = block_scan(nt, s_warp, &s_tiles);
-    if (i < R) req[i].tile = at;
-  }
-  // (offsets that overlap could ask for more tiles than there are; such a call is left out)
-  const bool fits = s_tiles <= a.tiles_cap;
-  if (tid == 0) {
-    if (!fits) flag(a.dev_status, SV_DEV_BAD_WINDOW);
-    a.hdr->T = fits ? s_tiles : 0;
-    a.hdr->W = 0;
-    a.hdr->C = 0;
-    a.hdr->ticket = 0;
-  }
-  __syncthreads();
-  if (fits) write_tiles(a, req);
-}
-
 __global__ void __launch_bounds__(kBuildThreads) build_kernel(const __grid_constant__ Args a) {
   griddep_entry();
   extern __shared__ uint32_t s_bits[];  // one bit a page, then the bits before each word
-  __shared__ int s_warp[32], s_carry, s_last;
+  __shared__ int s_warp[32], s_carry, s_req, s_k;
   __shared__ int s_len[kTileRows];
-  const int x = blockIdx.x;
-  const int lists = a.hdr->T * a.Hkv;
-  if (x >= lists) return;
-  const Tile tl = a.tiles[x / a.Hkv];
-  const int g = x % a.Hkv;
+  const int x = blockIdx.x, tile = x / a.Hkv, g = x % a.Hkv, R = a.bt.n_req;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int n = tl.ctx / kBlockSize, words = (n + 31) / 32;
+  // the request that holds the tile, and how many tiles there are
+  if (tid == 0) {
+    s_carry = 0;
+    if (x == 0 && (a.bt.cu_rows[0] != 0 || a.bt.cu_rows[R] != a.bt.total_rows))
+      flag(a.dev_status, SV_DEV_BAD_WINDOW);
+  }
+  for (int base = 0; base < R; base += kBuildThreads) {
+    const int i = base + tid;
+    int nt = 0;
+    if (i < R) {
+      const Window w = window_of(a.bt, i);
+      if (w.ok) nt = (max(w.b, w.e) - w.b + a.rt - 1) / a.rt;
+      else if (x == 0) flag(a.dev_status, SV_DEV_BAD_WINDOW);
+    }
+    const int at = block_scan(nt, s_warp, &s_carry);
+    if (at <= tile && tile < at + nt) {
+      s_req = i;
+      s_k = tile - at;
+    }
+  }
+  __syncthreads();
+  // (offsets that overlap could ask for more tiles than there are; such a call is left out)
+  const int T = s_carry <= a.tiles_cap ? s_carry : 0;
+  if (x == 0 && tid == 0) {
+    if (s_carry > a.tiles_cap) flag(a.dev_status, SV_DEV_BAD_WINDOW);
+    a.hdr->T = T;
+  }
+  if (tile >= T) return;
+  const int i = s_req, ctx = a.lens[i];
+  const Window w = window_of(a.bt, i);
+  const int r0 = w.b + s_k * a.rt, nr = min(a.rt, w.e - r0), n = max(ctx, 0) / kBlockSize;
+  bool bad = false;
+  if (tid < w.rows) {
+    const int p = a.bt.parent[w.cu + tid];
+    bad = tid == 0 ? p != -1 : (p < 0 || p >= tid);
+  }
+  const bool fits = ctx >= 0 && (long)ctx + w.rows <= (long)a.max_blocks * kBlockSize;
+  const int words = fits ? (n + 31) / 32 : 0;
   uint32_t* s_before = s_bits + words;
   for (int y = tid; y < words; y += kBuildThreads) s_bits[y] = 0u;
+  if (tid < nr) s_len[tid] = a.n_keep;
   if (tid == 0) s_carry = 0;
-  __syncthreads();
-  const int32_t* rows = a.pages + ((size_t)(tl.cu + tl.r0) * a.Hkv + g) * a.n_keep;
-  const size_t row_step = (size_t)a.Hkv * a.n_keep;
-  // a row's list ends where its pages stop to ascend
-  for (int r = warp; r < tl.nr; r += kBuildThreads / 32) {
-    const int32_t* list = rows + r * row_step;
-    int last = -1, len = 0;
-    for (int k0 = 0; k0 < a.n_keep; k0 += 32) {
-      const int k = k0 + lane;
-      const int v = k < a.n_keep ? __ldg(list + k) : -1;
-      int prev = __shfl_up_sync(0xffffffffu, v, 1);
-      if (lane == 0) prev = last;
-      const unsigned bad = __ballot_sync(0xffffffffu, v <= prev || v >= n);
-      const int good = bad ? __ffs(bad) - 1 : 32;
-      if (lane < good) atomicOr(&s_bits[v >> 5], 1u << (v & 31));
-      len += good;
-      if (bad) {
-        if (lane == good && v != -1) flag(a.dev_status, SV_DEV_BAD_PARAM);
-        break;
-      }
-      last = __shfl_sync(0xffffffffu, v, 31);
+  if (__syncthreads_or(bad) || !fits) {
+    // an empty list
+    if (tid == 0) {
+      a.cnt[2 * x] = a.cnt[2 * x + 1] = 0;
+      if (g == 0 && s_k == 0) flag(a.dev_status, fits ? SV_DEV_BAD_PARENT : SV_DEV_BAD_LENGTH);
     }
-    if (lane == 0) s_len[r] = len;
+    return;
   }
+  if (g == 0 && tid == 0) {
+    Tile t{};
+    t.i = i;
+    t.cu = w.cu;
+    t.ctx = ctx;
+    t.r0 = r0;
+    t.nr = nr;
+    t.rows = w.rows;
+    a.tiles[tile] = t;
+  }
+  uint32_t* see = a.see + (size_t)x * a.rt * (a.cap / 32);
+  for (int y = tid; y < nr * (a.cap / 32); y += kBuildThreads) see[y] = 0u;
+  // a warp takes 32 entries of a row at once
+  const int32_t* rows = a.pages + ((size_t)(w.cu + r0) * a.Hkv + g) * a.n_keep;
+  const size_t row_step = (size_t)a.Hkv * a.n_keep;
+  const int chunks = (a.n_keep + 31) / 32;
+  auto entries = [&](auto&& f) {
+    for (int y = warp; y < nr * chunks; y += kBuildThreads / 32) {
+      const int r = y / chunks, k = y % chunks * 32 + lane;
+      if (k < a.n_keep) f(r, k, rows + r * row_step);
+    }
+  };
+  // a row's list ends where its pages stop to ascend
+  entries([&](int r, int k, const int32_t* list) {
+    const int v = __ldg(list + k), prev = k ? __ldg(list + k - 1) : -1;
+    if (v <= prev || v >= n) atomicMin(&s_len[r], k);
+  });
+  __syncthreads();
+  entries([&](int r, int k, const int32_t* list) {
+    const int v = __ldg(list + k);
+    if (k < s_len[r]) atomicOr(&s_bits[v >> 5], 1u << (v & 31));
+    else if (k == s_len[r] && v != -1) flag(a.dev_status, SV_DEV_BAD_PARAM);
+  });
   __syncthreads();
   for (int base = 0; base < words; base += kBuildThreads) {
     const int y = base + tid;
@@ -100,49 +119,20 @@ __global__ void __launch_bounds__(kBuildThreads) build_kernel(const __grid_const
   __syncthreads();
   const int U = s_carry;
   int* blk = a.blk + (size_t)x * a.cap;
-  uint32_t* see = a.see + (size_t)x * a.rt * (a.cap / 32);
-  const int32_t* table = a.tables + (size_t)tl.i * a.max_blocks;
-  for (int y = tid; y < words; y += kBuildThreads) {
-    uint32_t bits = s_bits[y];
-    for (int pos = (int)s_before[y]; bits; bits &= bits - 1, ++pos)
-      blk[pos] = __ldg(table + y * 32 + __ffs(bits) - 1);
-  }
-  for (int y = tid; y < tl.nr * (a.cap / 32); y += kBuildThreads) see[y] = 0u;
-  const int ntail = (tl.ctx + tl.r0 + tl.nr + kBlockSize - 1) / kBlockSize - n;
-  for (int k = tid; k < ntail; k += kBuildThreads) blk[U + k] = __ldg(table + n + k);
-  __syncthreads();
-  for (int r = warp; r < tl.nr; r += kBuildThreads / 32) {
-    const int32_t* list = rows + r * row_step;
-    for (int k = lane; k < s_len[r]; k += 32) {
-      const int v = __ldg(list + k);
-      const int pos = (int)s_before[v >> 5] + __popc(s_bits[v >> 5] & ((1u << (v & 31)) - 1u));
-      atomicOr(see + (size_t)r * (a.cap / 32) + (pos >> 5), 1u << (pos & 31));
-    }
-  }
+  const int32_t* table = a.tables + (size_t)i * a.max_blocks;
+  entries([&](int r, int k, const int32_t* list) {
+    if (k >= s_len[r]) return;
+    const int v = __ldg(list + k);
+    const int pos = (int)s_before[v >> 5] + __popc(s_bits[v >> 5] & ((1u << (v & 31)) - 1u));
+    blk[pos] = __ldg(table + v);  // the same from every row that lists it
+    atomicOr(see + (size_t)r * (a.cap / 32) + (pos >> 5), 1u << (pos & 31));
+  });
+  const int ntail = (ctx + r0 + nr + kBlockSize - 1) / kBlockSize - n;
+  if (tid < ntail) blk[U + tid] = __ldg(table + n + tid);
   if (tid == 0) {
     a.cnt[2 * x] = U;
     a.cnt[2 * x + 1] = U + ntail;
-    s_last = ticket_add(&a.hdr->ticket, 1) == lists - 1;
-    s_carry = 0;
   }
-  __syncthreads();
-  if (!s_last) return;
-  // every list is known: their first stages, and the CTAs' shares
-  for (int base = 0; base < lists; base += kBuildThreads) {
-    const int y = base + tid;
-    const int v = y < lists ? (__ldcg(a.cnt + 2 * y + 1) + kStagePages - 1) / kStagePages : 0;
-    const int at = block_scan(v, s_warp, &s_carry);
-    if (y < lists) a.off[y] = at;
-  }
-  __syncthreads();
-  const int W = s_carry, C = min(a.ctas, W);
-  if (tid == 0) {
-    a.off[lists] = W;
-    a.hdr->W = W;
-    a.hdr->C = C;
-  }
-  __syncthreads();
-  for (int y = tid; y < lists; y += kBuildThreads) deal_list(a, y, a.off[y], a.off[y + 1], W, C);
 }
 
 inline Args page_args(const sv_paged_kv* kv, const sv_batch* bt, int32_t Hq, int32_t n_keep,
@@ -167,8 +157,7 @@ sv_status page_attend(const Args& a, const void* k, const void* v, cudaStream_t 
   const size_t words = ((size_t)a.max_blocks + 31) / 32;
   static PerDevice set;
   if (smem_limit_once(set, build_kernel, kMaxTable / 32 * 8) != cudaSuccess) return SV_ERR_CUDA;
-  if (sv::launch(page_plan_kernel, 1, kPlanThreads, plan_smem(a), stream, a) != cudaSuccess ||
-      sv::launch(build_kernel, a.tiles_cap * a.Hkv, kBuildThreads, words * 8, stream, a) != cudaSuccess)
+  if (sv::launch(build_kernel, a.tiles_cap * a.Hkv, kBuildThreads, words * 8, stream, a) != cudaSuccess)
     return SV_ERR_CUDA;
   return launch_units<D, true>(a, tmK, tmV, stream);
 }

@@ -26,7 +26,6 @@ namespace pu {
 constexpr int kTok = 128;        // tokens of a stage
 constexpr int kStagePages = 8;   // pages of a stage
 constexpr int kTileRows = 128;   // virtual rows of a tile
-constexpr int kPlanThreads = 1024;
 
 struct __align__(16) Tile {
   int i, cu, ctx, r0;      // request, its first packed row, context, first local row
@@ -40,7 +39,7 @@ struct Header {
   int T;       // tiles
   int W;       // stages of all lists
   int C;       // CTAs that share them (at most W)
-  int ticket;
+  int pad0;
   int Wp;      // stages of all prefix lists
   int Cp;      // CTAs that share them
   int pad[58];
@@ -68,10 +67,9 @@ struct Args {
   float scale_log2;
   int32_t* dev_status;
   Header* hdr;
-  Req* req;           // [n_req]
   Tile* tiles;
   int* off;           // [lists + 1] first stage of each list
-  int* start;         // [ctas] list of each CTA's first stage
+  int* start;         // [ctas] list of each CTA's first stage (prefix calls)
   float* ml;          // [slots][tile_vr][2]
   float* o;           // [slots][D / 4][tile_vr][4]: neighbouring rows in neighbouring lanes
   // page lists (sv_page_attend)
@@ -86,7 +84,7 @@ struct Args {
   const int32_t* cu_groups;
   const int32_t* prefix_len;
   int* arows;         // [total_rows] packed rows of the active rows
-  int* aoff;          // [n_req + 1] first active row of each request
+  Req* req;           // [n_req]
   int4* groups;       // [n_groups] first active row, active rows, pages, first prefix list
   int* gstage;        // [n_groups + 1] first stage of each group's prefix lists
   PStart* pstart;     // [ctas]
@@ -109,76 +107,12 @@ __device__ __forceinline__ void deal_list(const Args& a, int x, int off0, int of
   for (int c = (int)(((long)off0 * C + W - 1) / W); c < C && share_start(c, W, C) < off1; ++c) a.start[c] = x;
 }
 
-// What the plan keeps of a request.
+// What the plan of a prefix call keeps of a request.
 struct Req {
   int cu, rows, b, e;  // e = b: left out
-  int ctx, first, grp, tile;  // prefix pages, group (prefix calls); first tile
+  int ctx, first, grp, tile;  // prefix pages, group, first tile
   int stage, arow;     // first stage of the request's lists of one KV head, first active row
 };
-
-// Requests whose records the plan keeps in shared memory; more go to the workspace.
-constexpr int kPlanRequests = 512;
-
-// Window, parents and length of every request into req, by all threads of the
-// block: a warp a request, all of a request's loads in flight at once.  Requests
-// that cannot be attended are reported and left out.
-__device__ __forceinline__ void check_requests(const Args& a, Req* req) {
-  const int lane = threadIdx.x & 31;
-  for (int i = threadIdx.x >> 5; i < a.bt.n_req; i += blockDim.x >> 5) {
-    const Window w = window_of(a.bt, i);
-    const int ctx = a.lens[i];
-    bool bad = false;
-    if (w.ok) {
-#pragma unroll
-      for (int k = 0; k < kMaxRows / 32; ++k) {
-        const int j = lane + 32 * k;
-        if (j < w.rows) {
-          const int p = a.bt.parent[w.cu + j];
-          bad |= j == 0 ? p != -1 : (p < 0 || p >= j);
-        }
-      }
-    }
-    bad = __any_sync(0xffffffffu, bad);
-    if (lane != 0) continue;
-    const bool fits = ctx >= 0 && (long)ctx + w.rows <= (long)a.max_blocks * kBlockSize;
-    if (!w.ok) flag(a.dev_status, SV_DEV_BAD_WINDOW);
-    else if (bad) flag(a.dev_status, SV_DEV_BAD_PARENT);
-    else if (!fits) flag(a.dev_status, SV_DEV_BAD_LENGTH);
-    Req r{};
-    r.cu = w.cu;
-    r.rows = w.rows;
-    r.b = w.b;
-    r.e = w.ok && !bad && fits ? max(w.b, w.e) : w.b;  // (a window behind the verified rows is empty)
-    r.ctx = ctx;
-    req[i] = r;
-  }
-  __syncthreads();
-}
-
-// The tiles of every request (tile: its first), by all threads of the block: a warp
-// a request.
-__device__ __forceinline__ void write_tiles(const Args& a, const Req* req) {
-  const int lane = threadIdx.x & 31;
-  for (int i = threadIdx.x >> 5; i < a.bt.n_req; i += blockDim.x >> 5) {
-    const Req r = req[i];
-    const int nt = (r.e - r.b + a.rt - 1) / a.rt;
-    for (int k = lane; k < nt; k += 32) {
-      Tile t{};
-      t.i = i;
-      t.cu = r.cu;
-      t.ctx = r.ctx;
-      t.r0 = r.b + k * a.rt;
-      t.nr = min(a.rt, r.e - t.r0);
-      t.rows = r.rows;
-      t.first = r.first;
-      t.ncomp = r.ctx / kBlockSize - r.first;
-      t.nent = (r.ctx + t.r0 + t.nr + kBlockSize - 1) / kBlockSize - r.first;
-      t.arow = r.arow + k * a.rt;
-      t.grp = r.grp;
-      a.tiles[r.tile + k] = t;
-    }
-  }
-}
 
 // Exclusive scan over the block's threads of v, on top of *carry (shared),
 // which moves on by the total.
@@ -264,6 +198,7 @@ __global__ void __launch_bounds__(unit::kThreads, 1)
   __shared__ ulonglong2 s_anc[kLists][kTileRows];  // ancestors-or-self of the tile's rows
   __shared__ int s_ids[kLists][kStagePages];       // blocks of a list's first stage
   __shared__ int s_par[kMaxRows];
+  __shared__ int s_scan[32], s_carry, s_first[2];
   // records there / free; K, V landed; S ready (K read), PV done (V read), P written
   // of a stage's slot; Q landed, O read of a list's
   __shared__ __align__(8) unsigned long long s_lfull[kLists], s_lfree[kLists], s_kfull[2], s_vfull[2],
@@ -311,7 +246,42 @@ __global__ void __launch_bounds__(unit::kThreads, 1)
   tc5::fence_after_sync();
   const uint32_t tmem = s_tmem;
   griddep_entry();
-  const int W = a.hdr->W, C = a.hdr->C, x_start = a.start[c];
+  int W, C, x_start, off_start;
+  if (SPARSE) {
+    // A run of lists a thread: the stages before it, and of all of them
+    const int lists = a.hdr->T * a.Hkv, per = (lists + unit::kThreads - 1) / unit::kThreads;
+    const int y0 = min(lists, tid * per), y1 = min(lists, y0 + per);
+    auto stages = [&](int y) { return (a.cnt[2 * y + 1] + kStagePages - 1) / kStagePages; };
+    int sum = 0;
+    for (int y = y0; y < y1; ++y) sum += stages(y);
+    if (tid == 0) s_carry = 0;
+    int at = block_scan(sum, s_scan, &s_carry);
+    W = s_carry;
+    C = min(a.ctas, W);
+    const int s0 = c < C ? share_start(c, W, C) : -1;
+    for (int y = y0; y < y1; ++y) {
+      if (c == 0) a.off[y] = at;  // for the merge
+      const int n = stages(y);
+      if (at <= s0 && s0 < at + n) {
+        s_first[0] = y;
+        s_first[1] = at;
+      }
+      at += n;
+    }
+    if (c == 0 && tid == 0) {
+      a.off[lists] = W;
+      a.hdr->W = W;
+      a.hdr->C = C;
+    }
+    __syncthreads();
+    x_start = s_first[0];
+    off_start = s_first[1];
+  } else {
+    W = a.hdr->W;
+    C = a.hdr->C;
+    x_start = a.start[c];
+    off_start = 0;
+  }
   if (c >= C) {
     if (warp == 4) tc5::tmem_dealloc(tmem, unit::kCols);
     return;
@@ -334,15 +304,16 @@ __global__ void __launch_bounds__(unit::kThreads, 1)
   if (warp == 7) {
     // ------------------------------------------------------- lists ahead --
     const int s_end = share_start(c + 1, W, C);
-    int s_at = share_start(c, W, C), x = x_start, L = 0;
+    int s_at = share_start(c, W, C), x = x_start, off1 = off_start, L = 0;
     bool ok = true;
     for (;; ++x) {
       Rec r{};
       if (s_at < s_end) {
-        const int off0 = a.off[x], off1 = a.off[x + 1];
         const Tile tl = a.tiles[x / a.Hkv];
         r.ncomp = SPARSE ? a.cnt[2 * x] : tl.ncomp;
         r.nent = SPARSE ? a.cnt[2 * x + 1] : tl.nent;
+        const int off0 = SPARSE ? off1 : a.off[x];
+        off1 = off0 + (r.nent + kStagePages - 1) / kStagePages;
         r.n_stage = min(s_end, off1) - s_at;
         if (r.n_stage <= 0) continue;  // an empty list
         r.x = x;
@@ -910,17 +881,12 @@ inline Args common_args(const sv_paged_kv* kv, const sv_batch* bt, int32_t Hq, u
   a.ctas = sizing_sms();
   const size_t lists = (size_t)a.tiles_cap * a.Hkv, slots = lists + a.ctas;
   a.hdr = take<Header>(at, off, 1);
-  a.req = take<Req>(at, off, bt->n_req);
   a.tiles = take<Tile>(at, off, a.tiles_cap);
   a.off = take<int>(at, off, lists + 1);
   a.start = take<int>(at, off, a.ctas);
   a.ml = take<float>(at, off, slots * a.tile_vr * 2);
   a.o = take<float>(at, off, slots * a.tile_vr * kv->head_dim);
   return a;
-}
-
-inline size_t plan_smem(const Args& a) {
-  return a.bt.n_req <= kPlanRequests ? sizeof(Req) * (size_t)a.bt.n_req : 0;
 }
 
 // The query rows as boxes of a tile: 64 elements x the heads of a KV head's group
