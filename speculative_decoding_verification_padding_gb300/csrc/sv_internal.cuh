@@ -386,6 +386,18 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
       : "memory");
 }
 
+// Registers of a thread, for all warps of a warpgroup (four warps from a multiple of
+// four on): what some give back others may take, up to what the block was launched
+// with.
+template <int N>
+__device__ __forceinline__ void reg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void reg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N));
+}
+
 // --------------------------------------------- programmatic dependent launch --
 // Every kernel of the library starts with griddep_entry(): it waits until the
 // previous grid in the stream has completed and its writes are visible

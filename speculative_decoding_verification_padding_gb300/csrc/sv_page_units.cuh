@@ -137,35 +137,45 @@ __device__ __forceinline__ int block_scan(int v, int* s_warp, int* carry) {
 
 // ------------------------------------------------------------------ units --
 
-// Slots m0 .. m0 + 15 relative to the context's end that a row sees: those
-// before it, and its ancestors-or-self (bits of mk1:mk0).
+// Bits m0 .. m0 + 31 of what a row sees behind the context's end: ones before it
+// (m0 < 0), then its ancestors-or-self (bits of mk1:mk0).
 __device__ __forceinline__ uint32_t tail_visible(int m0, unsigned long long mk0,
                                                  unsigned long long mk1) {
   if (m0 >= 128) return 0u;
-  if (m0 >= 64) return (uint32_t)(mk1 >> (m0 - 64)) & 0xffffu;
-  if (m0 >= 0) return (uint32_t)((mk0 >> m0) | (m0 ? mk1 << (64 - m0) : 0ull)) & 0xffffu;
-  if (m0 <= -16) return 0xffffu;
-  return ((uint32_t)(mk0 << -m0) | ((1u << -m0) - 1u)) & 0xffffu;
+  if (m0 <= -32) return 0xffffffffu;
+  if (m0 < 0) return ((uint32_t)mk0 << -m0) | ((1u << -m0) - 1u);
+  const int w = m0 >> 5;
+  const uint32_t a[5] = {(uint32_t)mk0, (uint32_t)(mk0 >> 32), (uint32_t)mk1, (uint32_t)(mk1 >> 32), 0u};
+  uint32_t lo = a[3], hi = 0u;
+#pragma unroll
+  for (int k = 0; k < 3; ++k)
+    if (w == k) {
+      lo = a[k];
+      hi = a[k + 1];
+    }
+  return __funnelshift_r(lo, hi, m0 & 31);
 }
 
 // One CTA an SM works through its share as one sequence of stages, n = 0, 1, ...
 // over all its lists (L = 0, 1, ...), so that the copies and products of a list
 // begin while the one before is still being finished:
-//   warps 0-3: the softmax; thread t owns row t of the tile (TMEM lane t): S to
-//     registers, what the row does not see masked, running max and sum, P (bf16)
-//     back over S; O is rescaled only where a row's max grows by more than 2^8; at
-//     a list's end O to the output or to a part;
-//   warp 4: the copies of Q and K, warp 5 of V (two slots each);
-//   warp 6: one thread issues S = Q K^T (128 x 128) and O += P V (128 x D) as
+//   warps 0-3, 4-7: the softmax of every other list; thread t owns row t of the tile
+//     (TMEM lane t): S to registers, what the row does not see masked, running max
+//     and sum, P (bf16) back over S; O is rescaled only where a row's max grows by
+//     more than 2^8; at a list's end O to the output or to a part, while the other
+//     warps begin the next list (one set of warps for all lists: 57 us for the own
+//     pages of 64 requests, 3 stages a list, where this takes 51);
+//   warp 8: the copies of Q and K, warp 9 of V (two slots each);
+//   warp 10: one thread issues S = Q K^T (128 x 128) and O += P V (128 x D) as
 //     tcgen05.mma, QK^T of the next stage before PV of this one;
-//   warp 7: reads the lists ahead (a ring of kLists records in shared memory).
+//   warp 11: reads the lists ahead (a ring of kLists records in shared memory).
 // Tensor memory: S of two stages in columns 0 .. 255, O of two lists in 256 .. 511.
 // Bound by the pages' bytes: a stage of 64 KB (head_dim 128) is 1.5 us of one SM's
 // share of HBM, its products 0.7 us, its softmax 0.6 us.
 // Every wait is bounded; a CTA that gives up flags SV_DEV_TIMEOUT, lets copies and
 // products land and frees its tensor memory.
 namespace unit {
-constexpr int kThreads = 256;
+constexpr int kThreads = 384;
 constexpr int kLists = 4;
 constexpr uint32_t kCols = 512, kColO = 256;
 template <int D>
@@ -199,10 +209,12 @@ __global__ void __launch_bounds__(unit::kThreads, 1)
   __shared__ int s_ids[kLists][kStagePages];       // blocks of a list's first stage
   __shared__ int s_par[kMaxRows];
   __shared__ int s_scan[32], s_carry, s_first[2];
-  // records there / free; K, V landed; S ready (K read), PV done (V read), P written
-  // of a stage's slot; Q landed, O read of a list's
+  // records there / free; K, V landed, PV done (V read), P written of a stage's slot;
+  // S ready (K read) of a set of softmax warps and slot: a set counts its own stages
+  // there, as a wait for a phase must not begin before the one before is over; Q
+  // landed, O complete, O read of a list
   __shared__ __align__(8) unsigned long long s_lfull[kLists], s_lfree[kLists], s_kfull[2], s_vfull[2],
-      s_sfull[2], s_odone[2], s_pfull[2], s_qfull[2], s_ofree[2], s_drain;
+      s_sfull[2][2], s_odone[2], s_pfull[2], s_qfull[2], s_olast[2], s_ofree[2], s_drain;
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   __shared__ int s_issued[6];  // phases begun of s_kfull, s_vfull, s_qfull
@@ -217,21 +229,23 @@ __global__ void __launch_bounds__(unit::kThreads, 1)
     for (int k = 0; k < 6; ++k) s_issued[k] = 0;
     for (int k = 0; k < kLists; ++k) {
       mbar_init(smem_u32(&s_lfull[k]), 1);
-      mbar_init(smem_u32(&s_lfree[k]), 7);  // four softmax warps, two producers, the issuing thread
+      mbar_init(smem_u32(&s_lfree[k]), 11);  // eight softmax warps, two producers, the issuing thread
     }
     for (int k = 0; k < 2; ++k) {
       mbar_init(smem_u32(&s_kfull[k]), 1);
       mbar_init(smem_u32(&s_vfull[k]), 1);
-      mbar_init(smem_u32(&s_sfull[k]), 1);
+      mbar_init(smem_u32(&s_sfull[k][0]), 1);
+      mbar_init(smem_u32(&s_sfull[k][1]), 1);
       mbar_init(smem_u32(&s_odone[k]), 1);
       mbar_init(smem_u32(&s_pfull[k]), 128);
       mbar_init(smem_u32(&s_qfull[k]), 1);
+      mbar_init(smem_u32(&s_olast[k]), 1);
       mbar_init(smem_u32(&s_ofree[k]), 128);
     }
     mbar_init(smem_u32(&s_drain), 1);
     fence_mbar_init();
   }
-  if (warp == 4) {
+  if (warp == 8) {
     if (lane == 0) {
       prefetch_map(&tmK);
       prefetch_map(&tmV);
@@ -283,7 +297,7 @@ __global__ void __launch_bounds__(unit::kThreads, 1)
     off_start = 0;
   }
   if (c >= C) {
-    if (warp == 4) tc5::tmem_dealloc(tmem, unit::kCols);
+    if (warp == 8) tc5::tmem_dealloc(tmem, unit::kCols);
     return;
   }
   auto gone = [&] { return *reinterpret_cast<volatile int*>(&s_abort) != 0; };
@@ -301,7 +315,7 @@ __global__ void __launch_bounds__(unit::kThreads, 1)
     return b >= 0 && b < a.num_blocks ? b : -1;
   };
 
-  if (warp == 7) {
+  if (warp == 11) {
     // ------------------------------------------------------- lists ahead --
     const int s_end = share_start(c + 1, W, C);
     int s_at = share_start(c, W, C), x = x_start, off1 = off_start, L = 0;
@@ -376,11 +390,12 @@ __global__ void __launch_bounds__(unit::kThreads, 1)
       if (r.n_stage == 0) break;
     }
     if (!ok) s_abort = 1;
-  } else if (warp == 4 || warp == 5) {
+  } else if (warp == 8 || warp == 9) {
     // --------------------------------------------------------- producers --
-    const bool isV = warp == 5;
+    const bool isV = warp == 9;
     bool ok = true;
     int n = 0;
+    uint32_t held = 0u, phase = 0u, count = 0u;  // bits of the slots, of the sets and slots
     for (int L = 0; ok; ++L) {
       const Rec* rp = list_at(L);
       if (!__all_sync(0xffffffffu, rp != nullptr)) {
@@ -398,8 +413,14 @@ __global__ void __launch_bounds__(unit::kThreads, 1)
         const int b1 = st + 1 < r.n_stage && lane < kStagePages ? block_of(r, e1) : -1;
         const int slot = n & 1;
         // the slot is free once the products of stage n - 2 have read it
-        bool go = n < 2 || mbar_wait_bounded(smem_u32(isV ? &s_odone[slot] : &s_sfull[slot]),
-                                             (uint32_t)(((n - 2) >> 1) & 1));
+        bool go = n < 2 || (isV ? mbar_wait_bounded(smem_u32(&s_odone[slot]), (uint32_t)(((n - 2) >> 1) & 1))
+                                : mbar_wait_bounded(smem_u32(&s_sfull[(held >> slot) & 1][slot]),
+                                                    (phase >> slot) & 1u));
+        // the set and phase that will free the slot again
+        const int set = L & 1;
+        held = (held & ~(1u << slot)) | (uint32_t)set << slot;
+        phase = (phase & ~(1u << slot)) | ((count >> (2 * set + slot)) & 1u) << slot;
+        count ^= 1u << (2 * set + slot);
         if (!__all_sync(0xffffffffu, go) || __any_sync(0xffffffffu, gone())) {
           ok = false;
           break;
@@ -431,7 +452,7 @@ __global__ void __launch_bounds__(unit::kThreads, 1)
       }
     }
     if (!ok) s_abort = 1;
-  } else if (warp == 6) {
+  } else if (warp == 10) {
     // --------------------------------------------------------- MMA issue --
     if (lane == 0) {
       constexpr uint32_t idesc_qk = tc5::idesc_bf16_f32(128, kTok, false);
@@ -461,7 +482,7 @@ __global__ void __launch_bounds__(unit::kThreads, 1)
           const uint64_t o = (uint64_t)(((ks >> 2) * S::kHalf + (ks & 3) * 32) >> 4);
           tc5::mma_bf16(tmem + (uint32_t)(slot * kTok), ad + o, bd + o, idesc_qk, ks > 0 ? 1u : 0u);
         }
-        tc5::commit(smem_u32(&s_sfull[slot]));
+        tc5::commit(smem_u32(&s_sfull[Lq & 1][slot]));
         ++n_q;
         if (++sq == nq) {
           ++Lq;
@@ -493,6 +514,8 @@ __global__ void __launch_bounds__(unit::kThreads, 1)
                            idesc_pv, (sp > 0 || ks > 0) ? 1u : 0u);
         tc5::commit(smem_u32(&s_odone[slot]));
         if (++sp == np) {
+          // (the next lists may run on before this one's O is read: a barrier of its own)
+          tc5::commit(smem_u32(&s_olast[Lp & 1]));
           list_done(Lp);
           ++Lp;
           sp = 0;
@@ -511,12 +534,14 @@ __global__ void __launch_bounds__(unit::kThreads, 1)
     }
   } else {
     // ----------------------------------------------------- softmax, rows --
-    const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
+    const int row_t = tid & 127;  // this thread's row
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const float sc = a.scale_log2;
     const uint64_t sc2 = pair(sc, sc);
     const int group = a.group;
     bool ok = true;
     int n = 0;
+    uint32_t count = 0u;  // parity of this set's stages so far in each slot
     for (int L = 0; ok; ++L) {
       const Rec* rp = list_at(L);
       if (!__all_sync(0xffffffffu, rp != nullptr)) {
@@ -525,10 +550,16 @@ __global__ void __launch_bounds__(unit::kThreads, 1)
       }
       const Rec r = *rp;
       if (r.n_stage == 0) break;
+      if ((L & 1) != warp >> 2) {  // the other warps' list
+        __syncwarp();
+        if (lane == 0) list_done(L);
+        n += r.n_stage;
+        continue;
+      }
       const int vrows = r.nr * group;
-      const bool real = tid < vrows;
-      const int lr = real ? tid / group : 0, head = r.g * group + (real ? tid % group : 0);
-      const bool some = warp * 32 < vrows;  // rows in this warp at all
+      const bool real = row_t < vrows;
+      const int lr = real ? row_t / group : 0, head = r.g * group + (real ? row_t % group : 0);
+      const bool some = (warp & 3) * 32 < vrows;  // rows in this warp at all
       ulonglong2 anc = make_ulonglong2(0ull, 0ull);
       const int e_end = min(r.nent, r.e_first + r.n_stage * kStagePages);
       if (e_end > r.ncomp) anc = s_anc[L % kLists][lr];
@@ -545,7 +576,8 @@ __global__ void __launch_bounds__(unit::kThreads, 1)
         if (SPARSE && (e0 & 31) == 0 && st > 0) bits = bits1;
         if (SPARSE && (e0 & 31) == 24 && st + 1 < r.n_stage) bits1 = __ldg(see + (e0 >> 5) + 1);
         const uint32_t vis = SPARSE ? bits >> (e0 & 31) : 0xffu;  // pages of the stage the row sees
-        const bool got = mbar_wait_bounded(smem_u32(&s_sfull[slot]), (uint32_t)((n >> 1) & 1));
+        const bool got = mbar_wait_bounded(smem_u32(&s_sfull[L & 1][slot]), (count >> slot) & 1u);
+        count ^= 1u << slot;
         if (!__all_sync(0xffffffffu, got)) {
           ok = false;
           break;
@@ -555,61 +587,59 @@ __global__ void __launch_bounds__(unit::kThreads, 1)
         if (odd) {
           there = e0 + kStagePages <= r.nent ? 0xffu : (1u << (r.nent - e0)) - 1u;
           if (r.bad) there &= __ballot_sync(0xffffffffu, lane < kStagePages && block_of(r, e0 + lane) >= 0);
-          // rows of V that nothing was written to may hold anything: zeros, so that
-          // their weights of 0 add nothing
-          const bool gv = mbar_wait_bounded(smem_u32(&s_vfull[slot]), (uint32_t)((n >> 1) & 1));
-          if (!__all_sync(0xffffffffu, gv)) {
-            ok = false;
-            break;
-          }
-          uint8_t* vb = base_ptr + (ring - base) + (2 + slot) * S::kTile;
-          auto zero = [&](int t0, int t1) {  // rows t0 .. t1 - 1 of V
-            for (int y = tid; y < (t1 - t0) * (D / 8); y += 128) {
-              const int t = t0 + y / (D / 8), ch = y % (D / 8);
-              *reinterpret_cast<int4*>(vb + (ch >> 3) * S::kHalf + t * 128 + (((ch & 7) ^ (t & 7)) << 4)) =
-                  make_int4(0, 0, 0, 0);
-            }
-          };
-          // behind the last staged slot, and (where a block is missing) whole pages
-          zero(min(kTok, max(0, (r.ncomp - e0) * kBlockSize + r.lim - tail0)), kTok);
-          if (r.bad)
-            for (int p = 0; p < kStagePages; ++p)
-              if (!((there >> p) & 1u)) zero(16 * p, 16 * p + 16);
-          fence_proxy_async_smem();
         }
         tc5::fence_after_sync();
         if (some) {
           const uint32_t ts = tmem + lane_base + (uint32_t)(slot * kTok);
-          uint32_t s[kTok];
-          tc5::tmem_ld_x128(ts, s);
-          uint32_t pages = vis;  // pages of which the row sees something
-          if (odd) {
+          // In an odd stage: the tokens of quarter q (32 tokens) that the row sees.
+          const int m0 = tail0 + (e0 - r.ncomp) * kBlockSize;  // slot of the stage's first token
+          auto seen = [&](int q) {
+            const uint32_t w = tail_visible(m0 + 32 * q, anc.x, anc.y);
+            uint32_t x = 0u;
 #pragma unroll
-            for (int p = 0; p < kStagePages; ++p) {
-              if (e0 + p < r.ncomp && ((there >> p) & 1u)) continue;  // the same for all rows
-              const uint32_t w = (there >> p) & 1u
-                                     ? tail_visible(tail0 + (e0 + p - r.ncomp) * kBlockSize, anc.x, anc.y)
-                                     : 0u;
+            for (int h = 0; h < 2; ++h) {
+              const int p = 2 * q + h;
+              const uint32_t whole = (vis >> p) & 1u ? 0xffffu : 0u;
+              const uint32_t y = e0 + p < r.ncomp ? whole : (w >> (16 * h)) & 0xffffu;
+              x |= ((there >> p) & 1u ? y : 0u) << (16 * h);
+            }
+            return x;
+          };
+          // S is read twice, for the maxima and for P: its 128 values would not leave
+          // two sets of softmax warps registers enough
+          float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          if (!odd) {
+            uint32_t s[2][32];
+            tc5::tmem_ld_x32_begin(ts, s[0]);
 #pragma unroll
-              for (int k = 0; k < 16; ++k)
-                if (!((w >> k) & 1u)) s[16 * p + k] = __float_as_uint(-INFINITY);
-              pages = w ? pages | 1u << p : pages & ~(1u << p);
+            for (int q = 0; q < 4; ++q) {
+              tc5::tmem_ld_wait(s[q & 1]);
+              if (q < 3) tc5::tmem_ld_x32_begin(ts + 32 * (q + 1), s[(q + 1) & 1]);
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                float m2[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                  const uint32_t* v = s[q & 1] + 16 * h + 8 * k;
+                  m2[k] = fmaxf(fmaxf(fmaxf(__uint_as_float(v[0]), __uint_as_float(v[1])), __uint_as_float(v[2])),
+                                fmaxf(__uint_as_float(v[3]), __uint_as_float(v[4])));
+                  m2[k] = fmaxf(fmaxf(m2[k], __uint_as_float(v[5])), fmaxf(__uint_as_float(v[6]), __uint_as_float(v[7])));
+                }
+                if ((vis >> (2 * q + h)) & 1u) mx4[q] = fmaxf(fmaxf(mx4[q], m2[0]), m2[1]);
+              }
+            }
+          } else {
+#pragma unroll 1
+            for (int q = 0; q < 4; ++q) {
+              uint32_t s[32];
+              tc5::tmem_ld_x32(ts + 32 * q, s);
+              const uint32_t w = seen(q);
+#pragma unroll
+              for (int k = 0; k < 32; ++k)
+                if (w & (1u << k)) mx4[k & 3] = fmaxf(mx4[k & 3], __uint_as_float(s[k]));
             }
           }
-          float mx = -INFINITY;
-#pragma unroll
-          for (int p = 0; p < kStagePages; ++p) {
-            float m2[2];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const uint32_t* q = s + 16 * p + 8 * k;
-              m2[k] = fmaxf(fmaxf(fmaxf(__uint_as_float(q[0]), __uint_as_float(q[1])), __uint_as_float(q[2])),
-                            fmaxf(__uint_as_float(q[3]), __uint_as_float(q[4])));
-              m2[k] = fmaxf(fmaxf(m2[k], __uint_as_float(q[5])), fmaxf(__uint_as_float(q[6]), __uint_as_float(q[7])));
-            }
-            if ((pages >> p) & 1u) mx = fmaxf(fmaxf(mx, m2[0]), m2[1]);
-          }
-          mx *= sc;
+          const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * sc;
           const bool grow = mx > m_ref + 8.f;
           if (__any_sync(0xffffffffu, grow)) {
             const float m_new = grow ? mx : m_ref;
@@ -637,45 +667,82 @@ __global__ void __launch_bounds__(unit::kThreads, 1)
           uint64_t sum[4] = {0, 0, 0, 0};
           // P is rounded to bf16 for the tensor cores (2^-8 of each weight at most, in
           // a sum of many; the normaliser keeps fp32); a page that the row does not
-          // see gets its -inf with the maximum's subtraction
+          // see gets its -inf with the maximum's subtraction.  P of a quarter goes
+          // over columns of S that have been read.
+          auto weights = [&](const uint32_t (&s)[32], int q, float off0, float off1) {
+            uint32_t pk[16];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t pk[32];
-#pragma unroll
-            for (int p = 0; p < 4; ++p) {
-              const float off = (pages >> (4 * h + p)) & 1u ? -mb : -INFINITY;
-              const uint64_t off2 = pair(off, off);
-#pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                const int e = h * 64 + 16 * p + 2 * k;
-                const float2 x = unpair(fma2(pair(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), sc2, off2));
-                const float w0 = ex2(x.x), w1 = ex2(x.y);
-                sum[k & 3] = add2(sum[k & 3], pair(w0, w1));
-                pk[8 * p + k] = pack_bf16(w0, w1);
-              }
+            for (int k = 0; k < 16; ++k) {
+              const float off = k < 8 ? off0 : off1;
+              const float2 x = unpair(fma2(pair(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), sc2,
+                                           pair(off, off)));
+              const float w0 = ex2(x.x), w1 = ex2(x.y);
+              sum[k & 3] = add2(sum[k & 3], pair(w0, w1));
+              pk[k] = pack_bf16(w0, w1);
             }
-            tc5::tmem_st_x32(ts + h * 32, pk);
+            tc5::tmem_st_x16(ts + 16 * q, pk);
+          };
+          if (!odd) {
+            uint32_t s[2][32];
+            tc5::tmem_ld_x32_begin(ts, s[0]);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              tc5::tmem_ld_wait(s[q & 1]);
+              if (q < 3) tc5::tmem_ld_x32_begin(ts + 32 * (q + 1), s[(q + 1) & 1]);
+              weights(s[q & 1], q, (vis >> (2 * q)) & 1u ? -mb : -INFINITY, (vis >> (2 * q + 1)) & 1u ? -mb : -INFINITY);
+            }
+          } else {
+#pragma unroll 1
+            for (int q = 0; q < 4; ++q) {
+              uint32_t s[32];
+              tc5::tmem_ld_x32(ts + 32 * q, s);
+              const uint32_t w = seen(q);
+#pragma unroll
+              for (int k = 0; k < 32; ++k)
+                if (!(w & (1u << k))) s[k] = __float_as_uint(-INFINITY);
+              weights(s, q, -mb, -mb);
+            }
           }
           const float2 z = unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
           l += z.x + z.y;
+        }
+        if (odd) {
+          // rows of V that nothing was written to may hold anything: zeros, so that
+          // their weights of 0 add nothing
+          const bool gv = mbar_wait_bounded(smem_u32(&s_vfull[slot]), (uint32_t)((n >> 1) & 1));
+          if (!__all_sync(0xffffffffu, gv)) {
+            ok = false;
+            break;
+          }
+          uint8_t* vb = base_ptr + (ring - base) + (2 + slot) * S::kTile;
+          auto zero = [&](int t0, int t1) {  // rows t0 .. t1 - 1 of V
+            for (int y = row_t; y < (t1 - t0) * (D / 8); y += 128) {
+              const int t = t0 + y / (D / 8), ch = y % (D / 8);
+              *reinterpret_cast<int4*>(vb + (ch >> 3) * S::kHalf + t * 128 + (((ch & 7) ^ (t & 7)) << 4)) =
+                  make_int4(0, 0, 0, 0);
+            }
+          };
+          // behind the last staged slot, and (where a block is missing) whole pages
+          zero(min(kTok, max(0, (r.ncomp - e0) * kBlockSize + r.lim - tail0)), kTok);
+          if (r.bad)
+            for (int p = 0; p < kStagePages; ++p)
+              if (!((there >> p) & 1u)) zero(16 * p, 16 * p + 16);
+          fence_proxy_async_smem();
         }
         tc5::fence_before_sync();
         mbar_arrive(smem_u32(&s_pfull[slot]));
       }
       if (!ok) break;
       // the list's last PV has landed: O, normalised, to the output or to a part
-      {
-        const bool g3 = mbar_wait_bounded(smem_u32(&s_odone[(n - 1) & 1]), (uint32_t)(((n - 1) >> 1) & 1));
-        if (!__all_sync(0xffffffffu, g3)) {
-          ok = false;
-          break;
-        }
-        tc5::fence_after_sync();
+      const bool last = mbar_wait_bounded(smem_u32(&s_olast[L & 1]), (uint32_t)((L >> 1) & 1));
+      if (!__all_sync(0xffffffffu, last)) {
+        ok = false;
+        break;
       }
+      tc5::fence_after_sync();
       if (some) {
-        const size_t row = (size_t)(r.row0 + lr) * a.Hq + head;
         const bool out = r.whole && (SPARSE || a.groups[r.grp].z == 0);
-        const size_t part = (size_t)(c + r.x) * a.tile_vr + tid;
+        const size_t row = (size_t)(r.row0 + lr) * a.Hq + head, part = (size_t)(c + r.x);
         const float inv = l > 0.f ? 1.f / l : 0.f;
 #pragma unroll 1
         for (int k = 0; k < D; k += 32) {
@@ -693,7 +760,7 @@ __global__ void __launch_bounds__(unit::kThreads, 1)
               dst[j] = make_uint4(w[0], w[1], w[2], w[3]);
             }
           } else {
-            float4* dst = reinterpret_cast<float4*>(a.o) + ((size_t)(c + r.x) * (D / 4) + k / 4) * a.tile_vr + tid;
+            float4* dst = reinterpret_cast<float4*>(a.o) + (part * (D / 4) + k / 4) * a.tile_vr + row_t;
 #pragma unroll
             for (int j = 0; j < 8; ++j)
               dst[(size_t)j * a.tile_vr] =
@@ -701,7 +768,7 @@ __global__ void __launch_bounds__(unit::kThreads, 1)
                               __uint_as_float(ov[4 * j + 2]), __uint_as_float(ov[4 * j + 3]));
           }
         }
-        if (real && !out) reinterpret_cast<float2*>(a.ml)[part] = make_float2(m_ref, l);
+        if (real && !out) reinterpret_cast<float2*>(a.ml)[part * a.tile_vr + row_t] = make_float2(m_ref, l);
       }
       tc5::fence_before_sync();
       mbar_arrive(smem_u32(&s_ofree[L & 1]));
@@ -724,7 +791,7 @@ __global__ void __launch_bounds__(unit::kThreads, 1)
     }
     __syncthreads();
   }
-  if (warp == 4) tc5::tmem_dealloc(tmem, unit::kCols);
+  if (warp == 8) tc5::tmem_dealloc(tmem, unit::kCols);
 }
 
 // ------------------------------------------------------------------ merge --
