@@ -349,11 +349,18 @@ struct SelectRow {
 // The row and KV head of a CTA; false if it has nothing to choose (every page is
 // kept, or the row is left as it is).
 __device__ __forceinline__ bool select_row(const SelectArgs& a, SelectRow& s) {
+  __shared__ int s_req;
   s.r = blockIdx.x;
   s.g = blockIdx.y;
   const int tid = threadIdx.x;
-  if (s.r >= a.bt.cu_rows[a.bt.n_req]) return false;
-  const int i = find_segment(a.bt.cu_rows, a.bt.n_req, s.r);
+  // the request that owns the row, asked of all of them at once
+  if (tid == 0) s_req = -1;
+  __syncthreads();
+  for (int i = tid; i < a.bt.n_req; i += blockDim.x)
+    if (a.bt.cu_rows[i] <= s.r && s.r < a.bt.cu_rows[i + 1]) s_req = i;
+  __syncthreads();
+  const int i = s_req;
+  if (i < 0) return false;
   const Window w = window_of(a.bt, i);
   const int ctx = a.lens[i];
   s.n = ctx / kBlockSize;
@@ -379,24 +386,24 @@ __device__ __forceinline__ float key_score(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? k & 0x7fffffffu : ~k);
 }
 
-constexpr int kBins = 2048;
 constexpr int kCandidates = 512;
+constexpr int kMaxSelect = 49152;  // pages
 
-// One CTA a (row, KV head), its keys in shared memory.  The n_keep-th greatest:
-// the keys between the least and the greatest are counted in kBins bins of equal
+// One CTA a (row, KV head), its scores read from L1 in each pass (kept in shared
+// memory they left room for half as many CTAs).  The n_keep-th greatest:
+// the keys between the least and the greatest are counted in BINS bins of equal
 // width (of the scores; of the keys where the scores' range is no number to
 // divide by), the bin that holds the one sought is found from the top, and its
 // few keys rank one another.  Where they are many the bin is cut again; equal
-// keys need no cut.  Then the pages above it and the first of those equal to it
-// are written in order.  Ranges of scores fill equal bins better than digits of
-// their bits: few additions meet in one word.
-template <int THREADS>
+// keys need no cut.  Then a bit a page, of those above it and of the first of
+// those equal to it, is turned into the list.  Ranges of scores fill equal bins
+// better than digits of their bits: few additions meet in one word.
+template <int THREADS, int BINS>
 __global__ void __launch_bounds__(THREADS) select_kernel(SelectArgs a) {
   griddep_entry();
   constexpr int kWarps = THREADS / 32;
-  constexpr int kOwn = kBins / THREADS;  // bins a thread adds up
-  extern __shared__ uint32_t s_key[];
-  __shared__ uint32_t s_bin[kBins];
+  constexpr int kOwn = BINS / THREADS;  // bins a thread adds up
+  __shared__ uint32_t s_bin[BINS];
   __shared__ uint32_t s_cand[kCandidates];
   __shared__ uint32_t s_min[kWarps], s_max[kWarps], s_sum[kWarps];
   __shared__ uint32_t s_kth;
@@ -417,16 +424,29 @@ __global__ void __launch_bounds__(THREADS) select_kernel(SelectArgs a) {
     lo = __reduce_min_sync(0xffffffffu, s_min[lane % kWarps]);
     hi = __reduce_max_sync(0xffffffffu, s_max[lane % kWarps]);
   };
+  // before this thread's x of the block's, in the threads' order
+  auto scan = [&](uint32_t x) {
+    uint32_t y = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t z = __shfl_up_sync(0xffffffffu, y, o);
+      if (lane >= o) y += z;
+    }
+    if (lane == 31) s_sum[warp] = y;
+    __syncthreads();
+    uint32_t before = y - x;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w)
+      if (w < warp) before += s_sum[w];
+    return before;
+  };
+  const int t_first = a.n_first, t_last = n - a.n_last;  // the pages chosen from
   uint32_t mn = 0xffffffffu, mx = 0u, lo, hi;
 #pragma unroll 4
-  for (int t = tid; t < n; t += THREADS) {
-    uint32_t k = 0xffffffffu;
-    if (t >= a.n_first && t < n - a.n_last) {
-      k = score_key(__ldg(s + t));
-      mn = min(mn, k);
-      mx = max(mx, k);
-    }
-    s_key[t] = k;
+  for (int t = t_first + tid; t < t_last; t += THREADS) {
+    const uint32_t k = score_key(__ldg(s + t));
+    mn = min(mn, k);
+    mx = max(mx, k);
   }
   range(mn, mx, lo, hi);
   int need = a.n_keep - a.n_first - a.n_last;  // keys still sought in lo .. hi
@@ -440,41 +460,31 @@ __global__ void __launch_bounds__(THREADS) select_kernel(SelectArgs a) {
       }
       const float xlo = key_score(lo), width = key_score(hi) - xlo;
       const bool linear = lo > 0u && width > 1e-30f && width < 1e38f;
-      const float inv = linear ? (float)(kBins - 1) / width : 0.f;
-      const int shift = max(0, 32 - __clz(hi - lo) - 11);
+      const float inv = linear ? (float)(BINS - 1) / width : 0.f;
+      const int shift = max(0, 32 - __clz(hi - lo) - (31 - __clz(BINS)));
       auto bin = [&](uint32_t k) {  // never falls where k grows
-        return linear ? min(kBins - 1, (int)((key_score(k) - xlo) * inv)) : (int)((k - lo) >> shift);
+        return linear ? min(BINS - 1, (int)((key_score(k) - xlo) * inv)) : (int)((k - lo) >> shift);
       };
 #pragma unroll
       for (int k = 0; k < kOwn; ++k) s_bin[k * THREADS + tid] = 0u;
       if (tid == 0) s_count = s_above = 0;
       __syncthreads();
-      for (int t = tid; t < n; t += THREADS) {
-        const uint32_t k = s_key[t];
+#pragma unroll 4
+      for (int t = t_first + tid; t < t_last; t += THREADS) {
+        const uint32_t k = score_key(__ldg(s + t));
         if (k >= lo && k <= hi) atomicAdd(&s_bin[bin(k)], 1u);
       }
       __syncthreads();
       // thread tid adds up kOwn bins, the highest for thread 0
       uint32_t c[kOwn], sum = 0;
 #pragma unroll
-      for (int k = 0; k < kOwn; ++k) sum += c[k] = s_bin[kBins - 1 - (tid * kOwn + k)];
-      uint32_t x = sum;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-      }
-      if (lane == 31) s_sum[warp] = x;
-      __syncthreads();
-      uint32_t before = x - sum;
-#pragma unroll
-      for (int y = 0; y < kWarps; ++y)
-        if (y < warp) before += s_sum[y];
+      for (int k = 0; k < kOwn; ++k) sum += c[k] = s_bin[BINS - 1 - (tid * kOwn + k)];
+      uint32_t before = scan(sum);
       if ((int)before < need && (int)(before + sum) >= need) {
 #pragma unroll
         for (int k = 0; k < kOwn; ++k) {
           if ((int)before < need && (int)(before + c[k]) >= need) {
-            s_found = kBins - 1 - (tid * kOwn + k);
+            s_found = BINS - 1 - (tid * kOwn + k);
             s_before = (int)before;
           }
           before += c[k];
@@ -486,14 +496,17 @@ __global__ void __launch_bounds__(THREADS) select_kernel(SelectArgs a) {
       const bool few = s_bin[found] <= (uint32_t)kCandidates;
       mn = 0xffffffffu;
       mx = 0u;
-      for (int t = tid; t < n; t += THREADS) {
-        const uint32_t k = s_key[t];
-        if (k < lo || k > hi || bin(k) != found) continue;
-        mn = min(mn, k);
-        mx = max(mx, k);
-        if (few) s_cand[atomicAdd(&s_count, 1)] = k;
+#pragma unroll 4
+      for (int t = t_first + tid; t < t_last; t += THREADS) {
+        const uint32_t k = score_key(__ldg(s + t));
+        if (k >= lo && k <= hi && bin(k) == found) {
+          mn = min(mn, k);
+          mx = max(mx, k);
+          if (few) s_cand[atomicAdd(&s_count, 1)] = k;
+        }
       }
       if (!few) {
+        __syncwarp();
         range(mn, mx, lo, hi);
         continue;
       }
@@ -518,47 +531,51 @@ __global__ void __launch_bounds__(THREADS) select_kernel(SelectArgs a) {
       need -= s_above;
       break;
     }
-  // places in order: pages above the threshold and equal to it are counted for
-  // every warp's 32 neighbours (high and low half of a word), then added up
-  const int chunks = (n + 31) / 32;  // at most 1536
-  __syncthreads();
-  for (int ch = warp; ch < chunks; ch += kWarps) {
-    const uint32_t k = ch * 32 + lane < n ? s_key[ch * 32 + lane] : 0u;
-    const unsigned bu = __ballot_sync(0xffffffffu, ch * 32 + lane < n && k > kth);
-    const unsigned be = __ballot_sync(0xffffffffu, ch * 32 + lane < n && k == kth);
-    if (lane == 0) s_bin[ch] = ((uint32_t)__popc(bu) << 16) | (uint32_t)__popc(be);
-  }
-  __syncthreads();
-  uint32_t c[kOwn], sum = 0;
-#pragma unroll
-  for (int k = 0; k < kOwn; ++k) sum += c[k] = tid * kOwn + k < chunks ? s_bin[tid * kOwn + k] : 0u;
-  uint32_t x = sum;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
-  }
-  if (lane == 31) s_sum[warp] = x;
-  __syncthreads();
-  uint32_t before = x - sum;
-#pragma unroll
-  for (int y = 0; y < kWarps; ++y)
-    if (y < warp) before += s_sum[y];
-#pragma unroll
-  for (int k = 0; k < kOwn; ++k) {
-    if (tid * kOwn + k < chunks) s_bin[tid * kOwn + k] = before;
-    before += c[k];
-  }
-  __syncthreads();
+  // A bit a page: above the threshold, and the first `need` of those equal to it.
+  // A word at a time, in the order of the pages, BINS / 2 words at once.
   int32_t* out = a.pages + ((size_t)sr.r * a.Hkv + sr.g) * a.n_keep;
-  for (int ch = warp; ch < chunks; ch += kWarps) {
-    const int t = ch * 32 + lane;
-    const uint32_t k = t < n ? s_key[t] : 0u;
-    const bool u = t < n && k > kth, e = t < n && k == kth;
-    const unsigned bu = __ballot_sync(0xffffffffu, u), be = __ballot_sync(0xffffffffu, e);
-    const unsigned below = (1u << lane) - 1u;
-    const int pe = (int)(s_bin[ch] & 0xffffu) + __popc(be & below);
-    if (u || (e && pe < need)) out[(s_bin[ch] >> 16) + __popc(bu & below) + min(pe, need)] = t;
+  uint32_t* s_eq = s_bin + BINS / 2;
+  const int words = (n + 31) / 32;
+  uint32_t written = 0, equal = 0;  // before these words
+  for (int w0 = 0; w0 < words; w0 += BINS / 2) {
+    const int nw = min(words - w0, BINS / 2);
+    __syncthreads();
+    for (int w = warp; w < nw; w += kWarps) {
+      const int t = (w0 + w) * 32 + lane;
+      const uint32_t k = t < t_first || t >= t_last ? 0xffffffffu : score_key(__ldg(s + t));
+      const unsigned bu = __ballot_sync(0xffffffffu, t < n && k > kth);
+      const unsigned be = __ballot_sync(0xffffffffu, t < n && k == kth);
+      if (lane == 0) {
+        s_bin[w] = bu;
+        s_eq[w] = be;
+      }
+    }
+    __syncthreads();
+    const int per = (nw + THREADS - 1) / THREADS, b0 = min(nw, tid * per), b1 = min(nw, b0 + per);
+    uint32_t sum = 0;  // pages above (high half) and equal (low half) in this thread's words
+    for (int w = b0; w < b1; ++w) sum += ((uint32_t)__popc(s_bin[w]) << 16) + (uint32_t)__popc(s_eq[w]);
+    const uint32_t before = scan(sum);
+    uint32_t up = written + (before >> 16), eq = equal + (before & 0xffffu);
+    for (int w = b0; w < b1; ++w) {
+      const uint32_t above = s_bin[w];
+      uint32_t e = s_eq[w];
+      const int left = need - (int)eq;  // equal ones still to be taken
+      uint32_t take = above;
+      if (left >= __popc(e)) take |= e;
+      else
+        for (int k = 0; k < left; ++k, e &= e - 1) take |= e & (0u - e);
+      uint32_t pos = up + min(eq, (uint32_t)need);
+      up += __popc(above);
+      eq += __popc(s_eq[w]);
+      for (; take; take &= take - 1) out[pos++] = (w0 + w) * 32 + __ffs(take) - 1;
+    }
+    if (w0 + BINS / 2 < words) {  // more words: what came before them
+      uint32_t all = 0;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) all += s_sum[w];
+      written += all >> 16;
+      equal += all & 0xffffu;
+    }
   }
 }
 
@@ -678,7 +695,7 @@ extern "C" sv_status sv_select_pages(const sv_paged_kv* kv, const sv_batch* bt, 
   if (st != SV_OK) return st;
   if (max_pages < 0 || n_first < 0 || n_last < 0 || n_keep < 1 || (long)n_first + n_last > n_keep)
     return SV_ERR_INVALID_ARGUMENT;
-  if (n_keep > 1024 || max_pages > 49152 || kv->n_kv_heads > 65535) return SV_ERR_UNSUPPORTED_SHAPE;
+  if (n_keep > 1024 || max_pages > pg::kMaxSelect || kv->n_kv_heads > 65535) return SV_ERR_UNSUPPORTED_SHAPE;
   if (bt->n_req == 0 || bt->total_rows == 0) return SV_OK;
   if ((max_pages > 0 && !scores) || !pages || !kv->cache_lens) return SV_ERR_INVALID_ARGUMENT;
   pg::SelectArgs a;
@@ -696,14 +713,11 @@ extern "C" sv_status sv_select_pages(const sv_paged_kv* kv, const sv_batch* bt, 
   const dim3 grid(bt->total_rows, kv->n_kv_heads);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
-  static PerDevice set_many, set_few;
-  if (smem_limit_once(set_many, pg::select_kernel<256>, 49152 * 4) != cudaSuccess ||
-      smem_limit_once(set_few, pg::select_kernel<1024>, 49152 * 4) != cudaSuccess)
-    return SV_ERR_CUDA;
-  const size_t smem = (size_t)std::max(max_pages, 1) * 4;
-  // few lists leave SMs idle: more threads for each
-  const bool few = (long)bt->total_rows * kv->n_kv_heads <= sizing_sms() || max_pages > 16384;
-  e = few ? sv::launch(pg::select_kernel<1024>, grid, 1024, smem, s, a)
-          : sv::launch(pg::select_kernel<256>, grid, 256, smem, s, a);
+  // few lists leave SMs idle: more threads for each (350 rows of 8 heads with 62 to
+  // 6250 pages: 128 threads a list 40 us, 256 29 us, 512 43 us)
+  if ((long)bt->total_rows * kv->n_kv_heads <= sizing_sms())
+    e = sv::launch(pg::select_kernel<1024, 2048>, grid, 1024, 0, s, a);
+  else
+    e = sv::launch(pg::select_kernel<256, 512>, grid, 256, 0, s, a);
   return e == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
