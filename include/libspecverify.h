@@ -655,7 +655,7 @@ sv_status sv_select_pages(const sv_paged_kv* kv, const sv_batch* batch, const fl
  * and its slots are left out).  With every page listed the result is
  * sv_tree_attend's up to rounding.
  * Supported: n_keep 0 .. 1024, max_blocks_per_req <= 262144, q and out 16-byte
- * aligned, otherwise as sv_tree_attend.  ws: sv_page_attend_workspace() bytes, 256-byte aligned. */
+ * aligned and apart, otherwise as sv_tree_attend.  ws: sv_page_attend_workspace() bytes, 256-byte aligned. */
 size_t sv_page_attend_workspace(const sv_batch* batch, const sv_paged_kv* kv, int32_t n_q_heads,
                                 int32_t n_keep);
 sv_status sv_page_attend(const sv_paged_kv* kv, const sv_batch* batch, const void* q,
@@ -677,8 +677,8 @@ sv_status sv_page_attend(const sv_paged_kv* kv, const sv_batch* batch, const voi
  * A request shorter than its group's prefix sets SV_DEV_BAD_LENGTH, a malformed
  * group SV_DEV_BAD_PARAM; such requests are skipped.  K and V of attended pages
  * and staged rows have to be finite.
- * Supported: 1 <= n_groups <= n_req, q and out 16-byte aligned, otherwise as
- * sv_tree_attend.  ws: sv_prefix_attend_workspace() bytes, 256-byte aligned
+ * Supported: 1 <= n_groups <= n_req, q and out 16-byte aligned and apart,
+ * otherwise as sv_tree_attend.  ws: sv_prefix_attend_workspace() bytes, 256-byte aligned
  * (the workspace does not depend on the contents of the groups). */
 typedef struct {
   int32_t n_groups;

@@ -357,7 +357,7 @@ __device__ __forceinline__ bool select_row(const SelectArgs& a, SelectRow& s) {
   if (tid == 0) s_req = -1;
   __syncthreads();
   for (int i = tid; i < a.bt.n_req; i += blockDim.x)
-    if (a.bt.cu_rows[i] <= s.r && s.r < a.bt.cu_rows[i + 1]) s_req = i;
+    if (a.bt.cu_rows[i] <= s.r && s.r < a.bt.cu_rows[i + 1]) atomicMax(&s_req, i);
   __syncthreads();
   const int i = s_req;
   if (i < 0) return false;

@@ -673,7 +673,7 @@ inline Args prefix_args(const sv_paged_kv* kv, const sv_batch* bt, const sv_shar
   a.gstage = take<int>(at, off, sp->n_groups + 1);
   a.pstart = take<PStart>(at, off, a.ctas);
   // the row tiles of all groups
-  a.plists = (int)(((long)bt->total_rows * a.group / kPrefixRows + sp->n_groups) * a.Hkv);
+  a.plists = (int)std::min(((long)bt->total_rows * a.group / kPrefixRows + sp->n_groups) * a.Hkv, (long)INT32_MAX);
   a.pml = take<float>(at, off, (size_t)(a.plists + a.ctas) * kPrefixRows * 2);
   a.po = take<float>(at, off, (size_t)(a.plists + a.ctas) * kPrefixRows * kv->head_dim);
   return a;
@@ -711,8 +711,8 @@ extern "C" size_t sv_prefix_attend_workspace(const sv_batch* bt, const sv_paged_
                                              const sv_shared_prefix* prefix, int32_t n_q_heads) {
   if (pu::check_prefix(kv, bt, prefix, n_q_heads) != SV_OK) return 0;
   size_t off = 0;
-  (void)pu::prefix_args(kv, bt, prefix, n_q_heads, nullptr, off);
-  return off;
+  const pu::Args a = pu::prefix_args(kv, bt, prefix, n_q_heads, nullptr, off);
+  return pu::counts_fit((long)a.tiles_cap * a.Hkv, a.max_blocks) && pu::counts_fit(a.plists, a.max_blocks) ? off : 0;
 }
 
 extern "C" sv_status sv_prefix_attend(const sv_paged_kv* kv, const sv_batch* bt,
@@ -729,6 +729,9 @@ extern "C" sv_status sv_prefix_attend(const sv_paged_kv* kv, const sv_batch* bt,
   if (!(softmax_scale > 0.f)) return SV_ERR_INVALID_ARGUMENT;
   size_t need = 0;
   pu::Args a = pu::prefix_args(kv, bt, prefix, n_q_heads, static_cast<uint8_t*>(ws), need);
+  if (!pu::counts_fit((long)a.tiles_cap * a.Hkv, a.max_blocks) || !pu::counts_fit(a.plists, a.max_blocks))
+    return SV_ERR_UNSUPPORTED_SHAPE;
+  if (pu::overlap(q, out, bt, n_q_heads, kv->head_dim)) return SV_ERR_INVALID_ARGUMENT;
   if (ws_bytes < need) return SV_ERR_WORKSPACE_TOO_SMALL;
   a.q = static_cast<const __nv_bfloat16*>(q);
   a.out = static_cast<__nv_bfloat16*>(out);

@@ -179,8 +179,8 @@ extern "C" size_t sv_page_attend_workspace(const sv_batch* bt, const sv_paged_kv
                                            int32_t n_q_heads, int32_t n_keep) {
   if (pu::check_pages(kv, bt, n_q_heads, n_keep) != SV_OK) return 0;
   size_t off = 0;
-  (void)pu::page_args(kv, bt, n_q_heads, n_keep, nullptr, off);
-  return off;
+  const pu::Args a = pu::page_args(kv, bt, n_q_heads, n_keep, nullptr, off);
+  return pu::counts_fit((long)a.tiles_cap * a.Hkv, a.max_blocks) ? off : 0;
 }
 
 extern "C" sv_status sv_page_attend(const sv_paged_kv* kv, const sv_batch* bt, const void* q,
@@ -197,6 +197,8 @@ extern "C" sv_status sv_page_attend(const sv_paged_kv* kv, const sv_batch* bt, c
   if (!(softmax_scale > 0.f)) return SV_ERR_INVALID_ARGUMENT;
   size_t need = 0;
   pu::Args a = pu::page_args(kv, bt, n_q_heads, n_keep, static_cast<uint8_t*>(ws), need);
+  if (!pu::counts_fit((long)a.tiles_cap * a.Hkv, a.max_blocks)) return SV_ERR_UNSUPPORTED_SHAPE;
+  if (pu::overlap(q, out, bt, n_q_heads, kv->head_dim)) return SV_ERR_INVALID_ARGUMENT;
   if (ws_bytes < need) return SV_ERR_WORKSPACE_TOO_SMALL;
   a.q = static_cast<const __nv_bfloat16*>(q);
   a.out = static_cast<__nv_bfloat16*>(out);

@@ -921,6 +921,17 @@ inline sv_status check(const sv_paged_kv* kv, const sv_batch* bt, int32_t Hq) {
   return SV_OK;
 }
 
+// Lists and their stages are counted in 32 bits.
+inline bool counts_fit(long lists, int max_blocks) {
+  return lists < INT32_MAX && lists * (max_blocks / kStagePages + 3L) < INT32_MAX;
+}
+
+// Whether the rows of q and out (bf16) share memory.
+inline bool overlap(const void* q, const void* out, const sv_batch* bt, int32_t Hq, int D) {
+  const uintptr_t n = (uintptr_t)bt->total_rows * Hq * D * 2, x = (uintptr_t)q, y = (uintptr_t)out;
+  return x < y + n && y < x + n;
+}
+
 // The part of the arguments and of the workspace that both calls have; `at`
 // is the workspace's address or null, `off` moves on by what is taken.
 template <class T>
@@ -944,7 +955,7 @@ inline Args common_args(const sv_paged_kv* kv, const sv_batch* bt, int32_t Hq, u
   a.rt = std::min(kTileRows / a.group, most);
   a.tile_vr = a.rt * a.group;
   // ceil(rows / rt) tiles a request
-  a.tiles_cap = bt->total_rows / a.rt + bt->n_req;
+  a.tiles_cap = (int)std::min((long)bt->total_rows / a.rt + bt->n_req, (long)INT32_MAX);
   a.ctas = sizing_sms();
   const size_t lists = (size_t)a.tiles_cap * a.Hkv, slots = lists + a.ctas;
   a.hdr = take<Header>(at, off, 1);

@@ -10,6 +10,12 @@ outputs and workspaces with torch, and enqueues the library calls of a step:
   budget    sv_select_budget -> sv_tree_attend -> sv_accept_commit,
             with the selected verify_len feeding the batch
 
+Steps over long contexts read less of the cache: with a ``PageChoice`` each draft
+row attends the pages that a score selects for it (sv_score_pages ->
+sv_select_pages -> sv_page_attend in the place of sv_tree_attend, and
+sv_bound_pages behind the commit); with an ``api.SharedPrefix`` the prefixes that
+requests share are read once (sv_prefix_attend).
+
 ``EdgeStep`` runs a one-pass step with its two edges, from projections and raw
 logits: sv_reserve_kv -> sv_slot_windows -> sv_stage_qkv -> sv_tree_attend ->
 sv_shape_logits -> sv_accept_commit.
@@ -32,8 +38,18 @@ from . import api
 from .workloads import Workload
 
 
+@dataclasses.dataclass(frozen=True)
+class PageChoice:
+    """How many pages of a long context a row attends: n_keep for each KV head, the
+    first n_first and the last n_last always, the others by score."""
+    n_keep: int
+    n_first: int = 1
+    n_last: int = 4
+
+
 class DeviceStep:
-    def __init__(self, w: Workload, device="cuda", mode: str | None = None, chunk: int | None = None):
+    def __init__(self, w: Workload, device="cuda", mode: str | None = None, chunk: int | None = None,
+                 choice: PageChoice | None = None, shared: api.SharedPrefix | None = None):
         self.w = w
         self.device = device
         cfg = w.cfg
@@ -92,6 +108,22 @@ class DeviceStep:
                  api.sv_accept_workspace(self.batch, self.V),
                  api.sv_accept_commit_workspace(self.batch, self.V),
                  api.sv_verify_chunked_workspace(self.batch, self.kv, self.Hq, self.V))
+        self.choice, self.shared = choice, shared
+        if (choice is not None or shared is not None) and self.mode == "chunked":
+            raise ValueError("a chunked step attends the whole context")
+        if choice is not None and shared is not None:
+            raise ValueError("a step has a page choice or a shared prefix, not both")
+        if choice is not None:
+            nb, hkv, bs, d = self.kv.k_cache.shape
+            pages = self.kv.block_tables.shape[1]
+            self.bounds = torch.zeros((nb, hkv, 2, d), dtype=torch.bfloat16, device=dev)
+            self.scores = torch.zeros((rows, hkv, pages), dtype=torch.float32, device=dev)
+            self.pages = torch.full((rows, hkv, choice.n_keep), -1, dtype=torch.int32, device=dev)
+            self.bounded = torch.zeros_like(self.kv.cache_lens)  # lengths whose pages have bounds
+            api.sv_bound_pages(self.kv, self.bounds, None, self.dev_status)
+            ws = max(ws, api.sv_page_attend_workspace(self.batch, self.kv, self.Hq, choice.n_keep))
+        if shared is not None:
+            ws = max(ws, api.sv_prefix_attend_workspace(self.batch, self.kv, shared, self.Hq))
         self.ws = api.workspace(ws, dev)
 
     # ---------------------------------------------------------------------
@@ -110,8 +142,29 @@ class DeviceStep:
 
     def attend(self, batch=None):
         b = batch or self.batch
-        self._bound("attend", b, lambda: api.bind_tree_attend(
-            self.kv, b, self.q, self.Hq, self.scale, self.out, self.ws, self.dev_status))()
+        if self.choice is not None:
+            self.choose(b)
+            self._bound("attend", b, lambda: api.bind_page_attend(
+                self.kv, b, self.q, self.scale, self.pages, self.out, self.ws, self.dev_status))()
+        elif self.shared is not None:
+            self._bound("attend", b, lambda: api.bind_prefix_attend(
+                self.kv, b, self.shared, self.q, self.scale, self.out, self.ws, self.dev_status))()
+        else:
+            self._bound("attend", b, lambda: api.bind_tree_attend(
+                self.kv, b, self.q, self.Hq, self.scale, self.out, self.ws, self.dev_status))()
+
+    def choose(self, batch=None):
+        """The pages that each row attends, by its queries and the pages' bounds."""
+        b, c = batch or self.batch, self.choice
+        self._bound("score pages", b, lambda: api.bind_score_pages(
+            self.kv, b, self.q, self.bounds, self.scores, self.dev_status))()
+        self._bound("select pages", b, lambda: api.bind_select_pages(
+            self.kv, b, self.scores, self.pages, c.n_first, c.n_last, self.dev_status))()
+
+    def bound_pages(self):
+        """Bounds of the pages that were filled since ``bounded`` was set."""
+        self._bound("bound pages", self.batch, lambda: api.bind_bound_pages(
+            self.kv, self.bounds, self.bounded, self.dev_status))()
 
     def accept(self, batch=None, row_stats=None):
         b = batch or self.batch
@@ -163,6 +216,8 @@ class DeviceStep:
         """Enqueue one whole step of this workload's mode on the current stream."""
         if restore:
             self.restore_cache_state()
+        if self.choice is not None:
+            self.bounded.copy_(self.kv.cache_lens)
         if self.mode == "onepass":
             self.attend()
             if commit:
@@ -183,6 +238,8 @@ class DeviceStep:
                 self.accept(self.batch_sel)
         else:
             raise ValueError(self.mode)
+        if self.choice is not None and commit:
+            self.bound_pages()
 
     def inputs(self):
         """The device tensors a step reads that a caller feeds from the host each
@@ -260,8 +317,9 @@ class EdgeStep(DeviceStep):
     """
 
     def __init__(self, w: Workload, q, k, v, rotary=None, rules=None, q_weight=None,
-                 k_weight=None, eps: float = 1e-6, pos_offset=None, device="cuda"):
-        super().__init__(unstaged(w), device, mode="onepass")
+                 k_weight=None, eps: float = 1e-6, pos_offset=None, device="cuda",
+                 choice: PageChoice | None = None, shared: api.SharedPrefix | None = None):
+        super().__init__(unstaged(w), device, mode="onepass", choice=choice, shared=shared)
         self.qkv, self.rotary, self.rules = (q, k, v), rotary, rules
         self.weights, self.eps, self.pos_offset = (q_weight, k_weight), eps, pos_offset
         n, rows = w.n_req, w.total_rows
@@ -312,12 +370,16 @@ class EdgeStep(DeviceStep):
     def run(self, commit: bool = True, restore: bool = True):
         if restore:
             self.restore_cache_state()
+        if self.choice is not None:
+            self.bounded.copy_(self.kv.cache_lens)
         self.reserve()
         self.stage()
         self.attend()
         self.shape()
         if commit:
             self.accept_commit()
+            if self.choice is not None:
+                self.bound_pages()
         else:
             self.accept()
 
