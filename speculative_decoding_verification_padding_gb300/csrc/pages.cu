@@ -441,19 +441,26 @@ __global__ void __launch_bounds__(THREADS) select_kernel(SelectArgs a) {
     return before;
   };
   const int t_first = a.n_first, t_last = n - a.n_last;  // the pages chosen from
-  uint32_t mn = 0xffffffffu, mx = 0u, lo, hi;
+  uint32_t mn, mx, lo, hi;
+  {
+    float least = INFINITY, most = -INFINITY;
+    bool nan = false;
 #pragma unroll 4
-  for (int t = t_first + tid; t < t_last; t += THREADS) {
-    const uint32_t k = score_key(__ldg(s + t));
-    mn = min(mn, k);
-    mx = max(mx, k);
+    for (int t = t_first + tid; t < t_last; t += THREADS) {
+      const float x = __ldg(s + t);
+      least = fminf(least, x);
+      most = fmaxf(most, x);
+      nan |= x != x;
+    }
+    mn = nan ? 0u : score_key(least);
+    mx = score_key(most);
   }
   range(mn, mx, lo, hi);
   int need = a.n_keep - a.n_first - a.n_last;  // keys still sought in lo .. hi
   uint32_t kth = 0xffffffffu;                  // none: the pages that are always kept
   if (need == 0) need = a.n_keep;
   else
-    for (;;) {
+    for (bool all = true;; all = false) {
       if (lo == hi) {
         kth = lo;
         break;
@@ -461,18 +468,24 @@ __global__ void __launch_bounds__(THREADS) select_kernel(SelectArgs a) {
       const float xlo = key_score(lo), width = key_score(hi) - xlo;
       const bool linear = lo > 0u && width > 1e-30f && width < 1e38f;
       const float inv = linear ? (float)(BINS - 1) / width : 0.f;
+      const bool plain = all && linear;  // the first cut, of numbers: no keys needed
       const int shift = max(0, 32 - __clz(hi - lo) - (31 - __clz(BINS)));
       auto bin = [&](uint32_t k) {  // never falls where k grows
         return linear ? min(BINS - 1, (int)((key_score(k) - xlo) * inv)) : (int)((k - lo) >> shift);
       };
+      auto plain_bin = [&](float x) { return min(BINS - 1u, __float2uint_rz(fmaf(x, inv, -xlo * inv))); };
 #pragma unroll
       for (int k = 0; k < kOwn; ++k) s_bin[k * THREADS + tid] = 0u;
       if (tid == 0) s_count = s_above = 0;
       __syncthreads();
+      if (plain) {
 #pragma unroll 4
-      for (int t = t_first + tid; t < t_last; t += THREADS) {
-        const uint32_t k = score_key(__ldg(s + t));
-        if (k >= lo && k <= hi) atomicAdd(&s_bin[bin(k)], 1u);
+        for (int t = t_first + tid; t < t_last; t += THREADS) atomicAdd(&s_bin[plain_bin(__ldg(s + t))], 1u);
+      } else {
+        for (int t = t_first + tid; t < t_last; t += THREADS) {
+          const uint32_t k = score_key(__ldg(s + t));
+          if (k >= lo && k <= hi) atomicAdd(&s_bin[bin(k)], 1u);
+        }
       }
       __syncthreads();
       // thread tid adds up kOwn bins, the highest for thread 0
@@ -496,13 +509,21 @@ __global__ void __launch_bounds__(THREADS) select_kernel(SelectArgs a) {
       const bool few = s_bin[found] <= (uint32_t)kCandidates;
       mn = 0xffffffffu;
       mx = 0u;
+      auto candidate = [&](uint32_t k) {
+        mn = min(mn, k);
+        mx = max(mx, k);
+        if (few) s_cand[atomicAdd(&s_count, 1)] = k;
+      };
+      if (plain) {
 #pragma unroll 4
-      for (int t = t_first + tid; t < t_last; t += THREADS) {
-        const uint32_t k = score_key(__ldg(s + t));
-        if (k >= lo && k <= hi && bin(k) == found) {
-          mn = min(mn, k);
-          mx = max(mx, k);
-          if (few) s_cand[atomicAdd(&s_count, 1)] = k;
+        for (int t = t_first + tid; t < t_last; t += THREADS) {
+          const float x = __ldg(s + t);
+          if ((int)plain_bin(x) == found) candidate(score_key(x));
+        }
+      } else {
+        for (int t = t_first + tid; t < t_last; t += THREADS) {
+          const uint32_t k = score_key(__ldg(s + t));
+          if (k >= lo && k <= hi && bin(k) == found) candidate(k);
         }
       }
       if (!few) {
@@ -536,15 +557,26 @@ __global__ void __launch_bounds__(THREADS) select_kernel(SelectArgs a) {
   int32_t* out = a.pages + ((size_t)sr.r * a.Hkv + sr.g) * a.n_keep;
   uint32_t* s_eq = s_bin + BINS / 2;
   const int words = (n + 31) / 32;
+  // a threshold between the infinities is compared as a number
+  const float xth = key_score(kth);
+  const bool numbers = kth > 0x007fffffu && kth < 0xff800000u;
   uint32_t written = 0, equal = 0;  // before these words
   for (int w0 = 0; w0 < words; w0 += BINS / 2) {
     const int nw = min(words - w0, BINS / 2);
     __syncthreads();
     for (int w = warp; w < nw; w += kWarps) {
       const int t = (w0 + w) * 32 + lane;
-      const uint32_t k = t < t_first || t >= t_last ? 0xffffffffu : score_key(__ldg(s + t));
-      const unsigned bu = __ballot_sync(0xffffffffu, t < n && k > kth);
-      const unsigned be = __ballot_sync(0xffffffffu, t < n && k == kth);
+      bool up, eq;
+      if (numbers) {  // NaN is neither
+        const float x = t >= t_first && t < t_last ? __ldg(s + t) : t < n ? INFINITY : -INFINITY;
+        up = x > xth;
+        eq = x == xth;
+      } else {
+        const uint32_t k = t < t_first || t >= t_last ? 0xffffffffu : score_key(__ldg(s + t));
+        up = t < n && k > kth;
+        eq = t < n && k == kth;
+      }
+      const unsigned bu = __ballot_sync(0xffffffffu, up), be = __ballot_sync(0xffffffffu, eq);
       if (lane == 0) {
         s_bin[w] = bu;
         s_eq[w] = be;
