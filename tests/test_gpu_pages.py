@@ -169,7 +169,8 @@ def test_bounds_findings():
 @pytest.mark.parametrize("heads,kv_heads,dim", [(8, 8, 128), (6, 3, 64), (6, 2, 128), (8, 2, 64), (10, 2, 128),
                                                 (14, 2, 64), (8, 1, 128), (9, 1, 64), (32, 2, 128)])
 @pytest.mark.parametrize("shape", ["one", "ragged", "tree"])
-def test_scores(heads, kv_heads, dim, shape):
+@pytest.mark.parametrize("wide", [False, True])  # room for many pages: larger parts a CTA
+def test_scores(heads, kv_heads, dim, shape, wide):
     ctx, rows = {"one": ([300], [1]), "ragged": ([0, 15, 16, 1300, 257], [3, 2, 9, 1, 20]),
                  "tree": ([200, 90], [70, 33])}[shape]
     s = Setup(ctx, rows, heads, kv_heads, dim, tree=shape == "tree")
@@ -177,8 +178,21 @@ def test_scores(heads, kv_heads, dim, shape):
         s.window(begin=[0, 1, 2, 0, 0], end=[3, 2, 9, 1, 20], verify=[5, 5, 5, 0, 18])
     b = torch.empty(s.blocks, kv_heads, 2, dim, dtype=torch.bfloat16, device="cuda").fill_(float("nan"))
     api.sv_bound_pages(s.kv, b)
-    pages = max(ctx) // 16 + 2
-    out = torch.full((int(s.cu[-1]), kv_heads, pages), 7.0, device="cuda")
+    pages = 80000 // (len(ctx) * kv_heads) if wide else max(ctx) // 16 + 2
+    check_scores(s, b, torch.full((int(s.cu[-1]), kv_heads, pages), 7.0, device="cuda"), ctx, dim)
+
+
+@pytest.mark.parametrize("heads,kv_heads,dim,rows", [(10, 2, 128, [3, 1, 9]), (8, 2, 64, [1, 40, 2]), (32, 2, 128, [9, 1, 1])])
+@pytest.mark.parametrize("ctx", [[8191, 17000, 8208], [40, 2048 * 16 + 3, 0]])
+def test_scores_of_long_contexts(heads, kv_heads, dim, rows, ctx):
+    # several tiles a CTA and several CTAs a request
+    s = Setup(ctx, rows, heads, kv_heads, dim)
+    b = torch.empty(s.blocks, kv_heads, 2, dim, dtype=torch.bfloat16, device="cuda").fill_(float("nan"))
+    api.sv_bound_pages(s.kv, b)
+    check_scores(s, b, torch.full((int(s.cu[-1]), kv_heads, 14001), 7.0, device="cuda"), ctx, dim)
+
+
+def check_scores(s, b, out, ctx, dim):
     api.sv_score_pages(s.kv, s.batch, s.q, b, out, s.status)
     assert s.status.item() == 0
     bnd, q, got = f64(b), f64(s.q), out.cpu().double().numpy()
@@ -204,10 +218,15 @@ def test_scores_bound_every_product():
     assert (x.amax((2, 4)) <= out.double() + 1e-3).all()
 
 
-def test_scores_findings():
+@pytest.mark.parametrize("wide", [False, True])
+def test_scores_findings(wide):
     s = Setup([100, 64, 48], [2, 2, 2])
     b = torch.ones(s.blocks, 2, 2, 128, dtype=torch.bfloat16, device="cuda")
     out = torch.full((6, 2, 4), 7.0, device="cuda")
+    if wide:  # a length above the room of many pages
+        s.kv.cache_lens[0] = 15000 * 16
+        s.kv.block_tables = torch.nn.functional.pad(s.kv.block_tables, (0, 15010 - s.kv.block_tables.shape[1]), value=-1)
+        out = torch.full((6, 2, 14000), 7.0, device="cuda")
     s.kv.block_tables[2, 1] = -1
     api.sv_score_pages(s.kv, s.batch, s.q, b, out, s.status)  # request 0 has 6 pages, room for 4
     assert s.status.item() == N.SV_DEV_BAD_LENGTH | N.SV_DEV_BAD_BLOCK_ID
