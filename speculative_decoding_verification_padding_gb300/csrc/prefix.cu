@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
       gr.y = arow(cu_groups[k + 1]) - gr.x;
       gr.z = gr.y > 0 ? prefix_len[k] / kBlockSize : 0;  // checked by its requests
       n = gr.z > 0 ? (gr.y * a.group + kPrefixRows - 1) / kPrefixRows * a.Hkv : 0;
-      s = n * ((gr.z + kStagePages - 1) / kStagePages);
+      s = n * ((gr.z + kStagePages - 1) / kStagePages + kListStart);
     }
     int x = n, y = s;
 #pragma unroll
@@ -257,9 +257,9 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
       if (gstage[mid] <= s) ps.k = mid; else hi = mid - 1;
     }
     ps.gr = groups[ps.k];
-    const int sp = (ps.gr.z + kStagePages - 1) / kStagePages;
+    const int sp = (ps.gr.z + kStagePages - 1) / kStagePages + kListStart;
     ps.list = (s - gstage[ps.k]) / sp;
-    ps.st0 = (s - gstage[ps.k]) % sp;
+    ps.st0 = (s - gstage[ps.k]) % sp - kListStart;
     ps.leader = cu_groups[ps.k];
     ps.lists = (ps.gr.y * a.group + kPrefixRows - 1) / kPrefixRows * a.Hkv;
     a.pstart[c] = ps;
@@ -342,23 +342,25 @@ __global__ void __launch_bounds__(pfx::kThreads, 1)
   }
   const int s_end = share_start(c + 1, Wp, Cp);
   int s_at = share_start(c, Wp, Cp);
-  for (bool again = false; s_at < s_end; again = true) {
-  if (again && ++ps.list == ps.lists) {  // the next group that has stages
+  bool again = false, listed = false;  // a list was worked on, a list was looked at
+  for (; s_at < s_end; listed = true) {
+  if (listed && ++ps.list == ps.lists) {  // the next group that has stages
     while (s_at >= a.gstage[ps.k + 1]) ++ps.k;
     ps.gr = a.groups[ps.k];
     ps.leader = a.cu_groups[ps.k];
     ps.list = 0;
     ps.lists = (ps.gr.y * group + kPrefixRows - 1) / kPrefixRows * a.Hkv;
   }
-  if (again) ps.st0 = 0;
+  if (listed) ps.st0 = -kListStart;
   const int4 gr = ps.gr;
-  const int list = ps.list, st0 = ps.st0, g = list % a.Hkv, sp = (gr.z + kStagePages - 1) / kStagePages;
-  const int n_stage = min(sp - st0, s_end - s_at);
+  const int list = ps.list, g = list % a.Hkv, sp = (gr.z + kStagePages - 1) / kStagePages;
+  const int st0 = max(0, ps.st0), n_stage = min(sp, ps.st0 + s_end - s_at) - st0;
+  s_at += max(0, n_stage) + st0 - ps.st0;
+  if (n_stage <= 0) break;  // the share ends in the list's start
   const int v0 = list / a.Hkv * kPrefixRows, vrows = min(kPrefixRows, gr.y * group - v0);
   const int ntile = vrows > 128 ? 2 : 1;
   const int np = min(n_stage * kStagePages, gr.z - st0 * kStagePages);
   const size_t slot_id = (size_t)(c + gr.w + list);
-  s_at += n_stage;
   const int32_t* table = a.tables + (size_t)ps.leader * a.max_blocks + st0 * kStagePages;
   // block of page p of the run, -1 past its end or outside the cache
   auto block_of = [&](int p) {
@@ -391,6 +393,7 @@ __global__ void __launch_bounds__(pfx::kThreads, 1)
     }
     fence_mbar_init();
   }
+  again = true;
   tc5::fence_before_sync();
   __syncthreads();
   tc5::fence_after_sync();
@@ -647,6 +650,7 @@ __global__ void __launch_bounds__(pfx::kThreads, 1)
   tc5::fence_after_sync();
   if (s_abort) break;
   }
+  if (!again) __syncthreads();  // the tensor memory's address
   if (s_abort) {
     // copies in flight land before the CTA leaves (bounded waits)
     if (tid == 0) {

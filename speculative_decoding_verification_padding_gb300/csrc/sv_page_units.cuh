@@ -26,6 +26,10 @@ namespace pu {
 constexpr int kTok = 128;        // tokens of a stage
 constexpr int kStagePages = 8;   // pages of a stage
 constexpr int kTileRows = 128;   // virtual rows of a tile
+// Beginning a prefix list (its Q, the first copies, nothing yet to overlap with, and
+// writing out the one before) takes a CTA as long as about four stages: a list
+// counts so many more, before its own, when the stages are dealt out.
+constexpr int kListStart = 4;
 
 struct __align__(16) Tile {
   int i, cu, ctx, r0;      // request, its first packed row, context, first local row
@@ -40,13 +44,14 @@ struct Header {
   int W;       // stages of all lists
   int C;       // CTAs that share them (at most W)
   int pad0;
-  int Wp;      // stages of all prefix lists
+  int Wp;      // stages of all prefix lists, their starts included
   int Cp;      // CTAs that share them
   int pad[58];
 };
 
 // Where a CTA's share of the prefix stages begins: group, list of the group and
-// stage of the list; the group's lists, record and first request.
+// stage of the list (negative: in its start); the group's lists, record and first
+// request.
 struct __align__(16) PStart {
   int4 gr;
   int k, list, st0, lists, leader, pad[3];
@@ -86,7 +91,7 @@ struct Args {
   int* arows;         // [total_rows] packed rows of the active rows
   Req* req;           // [n_req]
   int4* groups;       // [n_groups] first active row, active rows, pages, first prefix list
-  int* gstage;        // [n_groups + 1] first stage of each group's prefix lists
+  int* gstage;        // [n_groups + 1] first stage of each group's prefix lists, starts included
   PStart* pstart;     // [ctas]
   int plists;         // prefix lists at most: 256-row tiles x KV heads
   float* pml;         // [plists + ctas][kPrefixRows][2]
@@ -829,7 +834,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_const
     if (grp.z > 0) {
       const int v = (tl.arow - grp.x) * group + vs;  // among the group's virtual rows
       const int list = v / kPrefixRows * a.Hkv + g, sp = (grp.z + kStagePages - 1) / kStagePages;
-      const int s0 = a.gstage[tl.grp] + list * sp;
+      const int s0 = a.gstage[tl.grp] + list * (sp + kListStart) + kListStart;
       const int cp = share_of(s0, Wp, Cp);
       np = share_of(s0 + sp - 1, Wp, Cp) - cp + 1;
       p0 = cp + grp.w + list;
@@ -921,9 +926,9 @@ inline sv_status check(const sv_paged_kv* kv, const sv_batch* bt, int32_t Hq) {
   return SV_OK;
 }
 
-// Lists and their stages are counted in 32 bits.
+// Lists and their stages, starts included, are counted in 32 bits.
 inline bool counts_fit(long lists, int max_blocks) {
-  return lists < INT32_MAX && lists * (max_blocks / kStagePages + 3L) < INT32_MAX;
+  return lists < INT32_MAX && lists * (max_blocks / kStagePages + 3L + kListStart) < INT32_MAX;
 }
 
 // Whether the rows of q and out (bf16) share memory.
