@@ -8,10 +8,12 @@
 // softmax over (prefix, own keys) = the two parts' (max, sum, weighted values)
 // joined.  Launches:
 //   plan    (1 CTA) checks groups and requests, lists the active rows of every
-//           group, cuts them into prefix units and the requests' rows into tiles;
-//   prefix  (tcgen05) units of 256 virtual rows (rows of all requests of the
-//           group x GQA group) by a part of the prefix's pages: (max, sum, O);
-//   units, merge (sv_page_units.cuh) over each request's own pages.
+//           group, cuts them into prefix lists and the requests' rows into tiles,
+//           divides the CTAs between the two and deals out both;
+//   prefix  (tcgen05, one CTA an SM) some CTAs the prefix lists -- 256 virtual rows
+//           (rows of all requests of the group x GQA group) by the prefix's pages:
+//           (max, sum, O) -- and the others the tiles' own pages (unit_share);
+//   merge   (sv_page_units.cuh) a row's parts of both.
 
 #include "sv_page_units.cuh"
 #include "sv_tcgen05.cuh"
@@ -33,7 +35,7 @@ struct PlanSmem {
 __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_constant__ Args a) {
   griddep_entry();
   extern __shared__ __align__(16) uint8_t s_mem[];
-  __shared__ int s_tiles, s_stages, s_rows, s_groups_bad;
+  __shared__ int s_tiles, s_stages, s_rows, s_pstages, s_groups_bad;
   PlanSmem& sm = *reinterpret_cast<PlanSmem*>(s_mem);
   const int R = a.bt.n_req, G = a.n_groups, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const bool small = R <= kPlanRequests && G <= kPlanGroups;  // in shared memory
@@ -153,10 +155,46 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
       at[1] += s;
       at[2] += n;
     }
+    __syncwarp();
+    const int rows = c[2];
+    // groups: first active row, active rows, pages; their lists, one a 256-row tile
+    // and KV head, and the lists' stages
+    auto arow = [&](int i) { return i < R ? req[i].arow : rows; };
+    int lists = 0, stages = 0;
+    for (int base = 0; base < G; base += 32) {
+      const int k = base + lane;
+      int4 gr = make_int4(0, 0, 0, 0);
+      int n = 0, s = 0;
+      if (k < G) {
+        gr.x = arow(cu_groups[k]);
+        gr.y = arow(cu_groups[k + 1]) - gr.x;
+        gr.z = gr.y > 0 ? prefix_len[k] / kBlockSize : 0;  // checked by its requests
+        n = gr.z > 0 ? (gr.y * a.group + kPrefixRows - 1) / kPrefixRows * a.Hkv : 0;
+        s = n * ((gr.z + kStagePages - 1) / kStagePages + kListStart);
+      }
+      int x = n, y = s;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, x, o), v = __shfl_up_sync(0xffffffffu, y, o);
+        if (lane >= o) { x += u; y += v; }
+      }
+      gr.w = lists + x - n;
+      if (k < G) {
+        groups[k] = gr;
+        gstage[k] = stages + y - s;
+        if (small) {
+          a.groups[k] = gr;
+          a.gstage[k] = stages + y - s;
+        }
+      }
+      lists += __shfl_sync(0xffffffffu, x, 31);
+      stages += __shfl_sync(0xffffffffu, y, 31);
+    }
     if (lane == 0) {
       s_tiles = c[0];
       s_stages = c[1];
-      s_rows = c[2];
+      s_rows = rows;
+      s_pstages = stages;
     }
   }
   __syncthreads();
@@ -168,7 +206,19 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
     }
     return;
   }
-  const int W = s_stages * a.Hkv, C = min(a.ctas, W);
+  // The CTAs that take prefix stages and those that take the requests' own: both at
+  // once, as one is bound by the tensor cores and the other by memory (448 rows of 64
+  // heads behind 24576 tokens, 1050 tokens of their own: 303 us, one after the other
+  // 327).  An own stage counts three quarters of a prefix stage and an own list's
+  // start a whole one, so that both kinds end at the same time (243 and 242 us; four
+  // requests 7.5 and 7.2, three groups of draft trees 24 and 27).
+  const int W = s_stages * a.Hkv, Wp = s_pstages;
+  int Cp = min(a.ctas, Wp), C = min(a.ctas, W);
+  if (Wp > 0 && W > 0) {
+    const long wp = 4L * Wp, all = wp + 3L * W + 4L * s_tiles * a.Hkv;
+    Cp = min(Wp, max(1, min(a.ctas - 1, (int)((a.ctas * wp + all / 2) / all))));
+    C = min(W, max(1, a.ctas - Cp));
+  }
   if (warp > 0) {
     // tiles, first stages of their lists, active rows: a warp a request
     if (tid == 32) {
@@ -208,40 +258,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
     }
     return;
   }
-  // groups: first active row, active rows, pages; their lists, one a 256-row tile
-  // and KV head, and the lists' stages
-  auto arow = [&](int i) { return i < R ? req[i].arow : s_rows; };
-  int lists = 0, stages = 0;
-  for (int base = 0; base < G; base += 32) {
-    const int k = base + lane;
-    int4 gr = make_int4(0, 0, 0, 0);
-    int n = 0, s = 0;
-    if (k < G) {
-      gr.x = arow(cu_groups[k]);
-      gr.y = arow(cu_groups[k + 1]) - gr.x;
-      gr.z = gr.y > 0 ? prefix_len[k] / kBlockSize : 0;  // checked by its requests
-      n = gr.z > 0 ? (gr.y * a.group + kPrefixRows - 1) / kPrefixRows * a.Hkv : 0;
-      s = n * ((gr.z + kStagePages - 1) / kStagePages + kListStart);
-    }
-    int x = n, y = s;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int u = __shfl_up_sync(0xffffffffu, x, o), v = __shfl_up_sync(0xffffffffu, y, o);
-      if (lane >= o) { x += u; y += v; }
-    }
-    gr.w = lists + x - n;
-    if (k < G) {
-      groups[k] = gr;
-      gstage[k] = stages + y - s;
-      if (small) {
-        a.groups[k] = gr;
-        a.gstage[k] = stages + y - s;
-      }
-    }
-    lists += __shfl_sync(0xffffffffu, x, 31);
-    stages += __shfl_sync(0xffffffffu, y, 31);
-  }
-  const int Wp = stages, Cp = min(a.ctas, Wp);
+  // where each CTA's share of the prefix stages ends
   if (lane == 0) {
     a.gstage[G] = Wp;
     a.hdr->Wp = Wp;
@@ -249,8 +266,8 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
   }
   __syncwarp();
   for (int c = lane; c < Cp; c += 32) {
-    const int s = share_start(c, Wp, Cp);
-    PStart ps;
+    const int s = share_start(c + 1, Wp, Cp) - 1;
+    PEnd ps{};
     ps.k = 0;  // the last group whose stages begin at or before s
     for (int hi = G - 1; ps.k < hi;) {
       const int mid = (ps.k + hi + 1) >> 1;
@@ -259,19 +276,23 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
     ps.gr = groups[ps.k];
     const int sp = (ps.gr.z + kStagePages - 1) / kStagePages + kListStart;
     ps.list = (s - gstage[ps.k]) / sp;
-    ps.st0 = (s - gstage[ps.k]) % sp - kListStart;
+    ps.at = (s - gstage[ps.k]) % sp;
     ps.leader = cu_groups[ps.k];
-    ps.lists = (ps.gr.y * a.group + kPrefixRows - 1) / kPrefixRows * a.Hkv;
-    a.pstart[c] = ps;
+    a.pend[c] = ps;
   }
 }
 
 // ------------------------------------------------------------ tcgen05 --
 // A list is two tiles of 128 virtual rows of a group by its prefix, 128 tokens a
-// stage; all stages are dealt out evenly to one CTA an SM (as those of the page
-// lists), which works through its share list by list: S = Q K^T and O += P V of a tile are tcgen05.mma of 128 x 128 (S) and
-// 128 x D (O).  Tensor memory: S in columns 0 .. 127, of one tile and then the
-// other, P (bf16) of the tiles in 128 .. 191 and 192 .. 255, O in 256 .. 511.
+// stage; all stages are dealt out evenly to the CTAs.  S = Q K^T and O += P V of a
+// tile are tcgen05.mma of 128 x 128 (S) and 128 x D (O).  Tensor memory: S in
+// columns 0 .. 127, of one tile and then the other, P (bf16) of the tiles in 128 ..
+// 191 and 192 .. 255, O in 256 .. 511.
+//   A CTA takes the lists of its share from the last to the first.  The last begins
+// at stage 0 of the prefix and the first goes on to the prefix's end, so that all
+// CTAs move through the prefix together and what one has read is still in L2 for the
+// others (first list first, the CTAs were spread over the whole prefix: 1.22 GB from
+// HBM for 448 rows of 64 heads behind 24576 tokens, now 0.29, own pages included).
 //   warps 0-3, 4-7: the softmax of tile 0 and 1; thread t owns row t (TMEM lane
 //     t): S to registers, which frees it for the other tile, running max and sum,
 //     P in two halves; O is rescaled in place only where a row's max grows by
@@ -304,7 +325,7 @@ struct Smem {
 template <int D>
 __global__ void __launch_bounds__(pfx::kThreads, 1)
     prefix_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap tmK,
-                  const __grid_constant__ CUtensorMap tmV) {
+                  const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmQ) {
   using S = pfx::Smem<D>;
   constexpr int kHalves = D / 64;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -315,6 +336,7 @@ __global__ void __launch_bounds__(pfx::kThreads, 1)
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   __shared__ int s_issued[4];
+  __shared__ __align__(16) unit::Shared s_unit;
   const int c = blockIdx.x;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -322,49 +344,69 @@ __global__ void __launch_bounds__(pfx::kThreads, 1)
   const uint32_t ring = base + 2 * S::kTile;  // K slots, then V slots
   const int group = a.group;
   // nothing that earlier kernels write is read before griddep_entry()
-  if (tid == 0) s_abort = 0;
+  if (tid == 0) {
+    s_abort = 0;
+    unit::init(s_unit);
+  }
   if (warp == 8) {
     if (lane == 0) {
       prefetch_map(&tmK);
       prefetch_map(&tmV);
+      prefetch_map(&tmQ);
     }
     __syncwarp();
     tc5::tmem_alloc(smem_u32(&s_tmem), pfx::kCols);
     tc5::tmem_relinquish();
   }
+  tc5::fence_before_sync();
+  __syncthreads();
+  tc5::fence_after_sync();
+  const uint32_t tmem = s_tmem;
   griddep_entry();
   const int Wp = a.hdr->Wp, Cp = a.hdr->Cp;
-  PStart ps = a.pstart[c];  // (there are a.ctas of them)
   if (c >= Cp) {
-    __syncthreads();
-    if (warp == 8) tc5::tmem_dealloc(s_tmem, pfx::kCols);
+    const int W = a.hdr->W, C = a.hdr->C, x_start = a.start[c - Cp];  // (there are a.ctas of them)
+    if (c - Cp < C)
+      unit_share<D, false>(a, tmK, tmV, tmQ, s_unit, base_ptr, tmem, c - Cp, W, C, x_start, 0);
+    if (warp == 8) tc5::tmem_dealloc(tmem, pfx::kCols);
     return;
   }
-  const int s_end = share_start(c + 1, Wp, Cp);
-  int s_at = share_start(c, Wp, Cp);
-  bool again = false, listed = false;  // a list was worked on, a list was looked at
-  for (; s_at < s_end; listed = true) {
-  if (listed && ++ps.list == ps.lists) {  // the next group that has stages
-    while (s_at >= a.gstage[ps.k + 1]) ++ps.k;
-    ps.gr = a.groups[ps.k];
-    ps.leader = a.cu_groups[ps.k];
-    ps.list = 0;
-    ps.lists = (ps.gr.y * group + kPrefixRows - 1) / kPrefixRows * a.Hkv;
-  }
-  if (listed) ps.st0 = -kListStart;
+  PEnd ps = a.pend[c];
+  const int s_begin = share_start(c, Wp, Cp);
+  int s_end = share_start(c + 1, Wp, Cp), phase = 0;
+  bool again = false;  // a list was worked on
+  while (s_end > s_begin) {
   const int4 gr = ps.gr;
   const int list = ps.list, g = list % a.Hkv, sp = (gr.z + kStagePages - 1) / kStagePages;
-  const int st0 = max(0, ps.st0), n_stage = min(sp, ps.st0 + s_end - s_at) - st0;
-  s_at += max(0, n_stage) + st0 - ps.st0;
-  if (n_stage <= 0) break;  // the share ends in the list's start
+  const int s_list = s_end - 1 - ps.at;  // where the list's start and stages begin
+  const int st0 = max(s_begin - s_list - kListStart, 0), n_stage = s_end - s_list - kListStart - st0;
+  const int* table = a.tables + (size_t)ps.leader * a.max_blocks + st0 * kStagePages;
+  // on to the list before
+  s_end = s_list;
+  --ps.list;
+  ps.at = sp + kListStart - 1;
+  if (ps.list < 0 && s_end > s_begin) {  // of the group before that has stages
+    do --ps.k;
+    while (a.gstage[ps.k] >= s_end);
+    ps.gr = a.groups[ps.k];
+    ps.leader = a.cu_groups[ps.k];
+    ps.list = (ps.gr.y * group + kPrefixRows - 1) / kPrefixRows * a.Hkv - 1;
+    ps.at = (ps.gr.z + kStagePages - 1) / kStagePages + kListStart - 1;
+  }
+  if (n_stage <= 0) continue;  // the share ends in the list's start
+  // stage st of this part is its stage (st + turn) mod n_stage: whole lists go on
+  // from the stage where the list before ended
+  const int turn = n_stage == sp ? phase % sp : 0;
+  phase += n_stage;
   const int v0 = list / a.Hkv * kPrefixRows, vrows = min(kPrefixRows, gr.y * group - v0);
   const int ntile = vrows > 128 ? 2 : 1;
   const int np = min(n_stage * kStagePages, gr.z - st0 * kStagePages);
   const size_t slot_id = (size_t)(c + gr.w + list);
-  const int32_t* table = a.tables + (size_t)ps.leader * a.max_blocks + st0 * kStagePages;
-  // block of page p of the run, -1 past its end or outside the cache
-  auto block_of = [&](int p) {
-    if (p >= np) return -1;
+  // block of page `lane` of stage st of the part, -1 past its end or outside the cache
+  auto page_of = [&](int st) { return (st + turn - (st + turn >= n_stage ? n_stage : 0)) * kStagePages + lane; };
+  auto block_of = [&](int st) {
+    const int p = page_of(st);
+    if (lane >= kStagePages || st >= n_stage || p >= np) return -1;
     const int b = __ldg(table + p);
     return b >= 0 && b < a.num_blocks ? b : -1;
   };
@@ -397,7 +439,6 @@ __global__ void __launch_bounds__(pfx::kThreads, 1)
   tc5::fence_before_sync();
   __syncthreads();
   tc5::fence_after_sync();
-  const uint32_t tmem = s_tmem;
 
   const bool real = tid < vrows;
   if (warp == 8 || warp == 9) {
@@ -406,7 +447,7 @@ __global__ void __launch_bounds__(pfx::kThreads, 1)
     // a slot is free once both tiles' products have read it
     unsigned long long (*freeb)[2] = half ? s_odone : s_sfull;
     unsigned long long* fullb = half ? s_vfull : s_kfull;
-    int next = lane < kStagePages ? block_of(lane) : -1;
+    int next = block_of(0);
     for (int st = 0; st < n_stage; ++st) {
       const int slot = st & 1;
       bool go = true;
@@ -419,8 +460,8 @@ __global__ void __launch_bounds__(pfx::kThreads, 1)
       }
       if (__any_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&s_abort))) break;
       const int b = next;
-      next = lane < kStagePages ? block_of((st + 1) * kStagePages + lane) : -1;
-      if (half == 0 && lane < kStagePages && st * kStagePages + lane < np && b < 0)
+      next = block_of(st + 1);
+      if (half == 0 && lane < kStagePages && b < 0 && page_of(st) < np)
         flag(a.dev_status, SV_DEV_BAD_BLOCK_ID);
       const uint32_t bar = smem_u32(&fullb[slot]);
       const int n = __popc(__ballot_sync(0xffffffffu, b >= 0));
@@ -510,7 +551,7 @@ __global__ void __launch_bounds__(pfx::kThreads, 1)
     }
     // pages of the next stage that are there
     auto there = [&](int st) {
-      return __ballot_sync(0xffffffffu, lane < kStagePages && block_of(st * kStagePages + lane) >= 0);
+      return __ballot_sync(0xffffffffu, block_of(st) >= 0);
     };
     uint32_t pages1 = there(0);
     float m_ref = -INFINITY, l = 0.f;
@@ -650,7 +691,6 @@ __global__ void __launch_bounds__(pfx::kThreads, 1)
   tc5::fence_after_sync();
   if (s_abort) break;
   }
-  if (!again) __syncthreads();  // the tensor memory's address
   if (s_abort) {
     // copies in flight land before the CTA leaves (bounded waits)
     if (tid == 0) {
@@ -662,7 +702,7 @@ __global__ void __launch_bounds__(pfx::kThreads, 1)
     }
     __syncthreads();
   }
-  if (warp == 8) tc5::tmem_dealloc(s_tmem, pfx::kCols);
+  if (warp == 8) tc5::tmem_dealloc(tmem, pfx::kCols);
 }
 
 inline Args prefix_args(const sv_paged_kv* kv, const sv_batch* bt, const sv_shared_prefix* sp,
@@ -675,7 +715,7 @@ inline Args prefix_args(const sv_paged_kv* kv, const sv_batch* bt, const sv_shar
   a.req = take<Req>(at, off, bt->n_req);
   a.groups = take<int4>(at, off, sp->n_groups);
   a.gstage = take<int>(at, off, sp->n_groups + 1);
-  a.pstart = take<PStart>(at, off, a.ctas);
+  a.pend = take<PEnd>(at, off, a.ctas);
   // the row tiles of all groups
   a.plists = (int)std::min(((long)bt->total_rows * a.group / kPrefixRows + sp->n_groups) * a.Hkv, (long)INT32_MAX);
   a.pml = take<float>(at, off, (size_t)(a.plists + a.ctas) * kPrefixRows * 2);
@@ -685,15 +725,18 @@ inline Args prefix_args(const sv_paged_kv* kv, const sv_batch* bt, const sv_shar
 
 template <int D>
 sv_status prefix_attend(const Args& a, const void* k, const void* v, cudaStream_t stream) {
-  CUtensorMap tmK, tmV;
-  if (!attn::make_map(&tmK, k, a.num_blocks, a.Hkv, D) || !attn::make_map(&tmV, v, a.num_blocks, a.Hkv, D))
+  CUtensorMap tmK, tmV, tmQ;
+  if (!attn::make_map(&tmK, k, a.num_blocks, a.Hkv, D) || !attn::make_map(&tmV, v, a.num_blocks, a.Hkv, D) ||
+      !make_q_map(&tmQ, a, D))
     return SV_ERR_CUDA;
   static PerDevice set;
   if (smem_limit_once(set, prefix_kernel<D>, pfx::Smem<D>::kAsk) != cudaSuccess) return SV_ERR_CUDA;
   if (sv::launch(prefix_plan_kernel, 1, kPlanThreads, sizeof(PlanSmem), stream, a) != cudaSuccess ||
-      sv::launch(prefix_kernel<D>, a.ctas, pfx::kThreads, pfx::Smem<D>::kAsk, stream, a, tmK, tmV) != cudaSuccess)
+      sv::launch(prefix_kernel<D>, a.ctas, pfx::kThreads, pfx::Smem<D>::kAsk, stream, a, tmK, tmV, tmQ) !=
+          cudaSuccess ||
+      launch_merge<D, false>(a, stream) != cudaSuccess)
     return SV_ERR_CUDA;
-  return launch_units<D, false>(a, tmK, tmV, stream);
+  return SV_OK;
 }
 
 inline sv_status check_prefix(const sv_paged_kv* kv, const sv_batch* bt, const sv_shared_prefix* sp,

@@ -135,6 +135,63 @@ __global__ void __launch_bounds__(kBuildThreads) build_kernel(const __grid_const
   }
 }
 
+template <int D>
+__global__ void __launch_bounds__(unit::kThreads, 1)
+    page_unit_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap tmK,
+                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmQ) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  __shared__ __align__(16) unit::Shared sh;
+  __shared__ int s_scan[32], s_carry, s_first[2];
+  __shared__ uint32_t s_tmem;
+  const int c = blockIdx.x, tid = threadIdx.x, warp = tid >> 5;
+  // nothing that earlier kernels write is read before griddep_entry()
+  if (tid == 0) unit::init(sh);
+  if (warp == 8) {
+    if ((tid & 31) == 0) {
+      prefetch_map(&tmK);
+      prefetch_map(&tmV);
+      prefetch_map(&tmQ);
+    }
+    __syncwarp();
+    tc5::tmem_alloc(smem_u32(&s_tmem), unit::kCols);
+    tc5::tmem_relinquish();
+  }
+  tc5::fence_before_sync();
+  __syncthreads();
+  tc5::fence_after_sync();
+  const uint32_t tmem = s_tmem;
+  griddep_entry();
+  // A run of lists a thread: the stages before it, and of all of them
+  const int lists = a.hdr->T * a.Hkv, per = (lists + unit::kThreads - 1) / unit::kThreads;
+  const int y0 = min(lists, tid * per), y1 = min(lists, y0 + per);
+  auto stages = [&](int y) { return (a.cnt[2 * y + 1] + kStagePages - 1) / kStagePages; };
+  int sum = 0;
+  for (int y = y0; y < y1; ++y) sum += stages(y);
+  if (tid == 0) s_carry = 0;
+  int at = block_scan(sum, s_scan, &s_carry);
+  const int W = s_carry, C = min(a.ctas, W);
+  const int s0 = c < C ? share_start(c, W, C) : -1;
+  for (int y = y0; y < y1; ++y) {
+    if (c == 0) a.off[y] = at;  // for the merge
+    const int n = stages(y);
+    if (at <= s0 && s0 < at + n) {
+      s_first[0] = y;
+      s_first[1] = at;
+    }
+    at += n;
+  }
+  if (c == 0 && tid == 0) {
+    a.off[lists] = W;
+    a.hdr->W = W;
+    a.hdr->C = C;
+  }
+  __syncthreads();
+  if (c < C)
+    unit_share<D, true>(a, tmK, tmV, tmQ, sh, smem_raw + ((1024 - smem_u32(smem_raw)) & 1023), tmem, c, W, C,
+                        s_first[0], s_first[1]);
+  if (warp == 8) tc5::tmem_dealloc(tmem, unit::kCols);
+}
+
 inline Args page_args(const sv_paged_kv* kv, const sv_batch* bt, int32_t Hq, int32_t n_keep,
                       uint8_t* at, size_t& off) {
   Args a = common_args(kv, bt, Hq, at, off);
@@ -151,15 +208,21 @@ inline Args page_args(const sv_paged_kv* kv, const sv_batch* bt, int32_t Hq, int
 
 template <int D>
 sv_status page_attend(const Args& a, const void* k, const void* v, cudaStream_t stream) {
-  CUtensorMap tmK, tmV;
-  if (!attn::make_map(&tmK, k, a.num_blocks, a.Hkv, D) || !attn::make_map(&tmV, v, a.num_blocks, a.Hkv, D))
+  CUtensorMap tmK, tmV, tmQ;
+  if (!attn::make_map(&tmK, k, a.num_blocks, a.Hkv, D) || !attn::make_map(&tmV, v, a.num_blocks, a.Hkv, D) ||
+      !make_q_map(&tmQ, a, D))
     return SV_ERR_CUDA;
   const size_t words = ((size_t)a.max_blocks + 31) / 32;
-  static PerDevice set;
-  if (smem_limit_once(set, build_kernel, kMaxTable / 32 * 8) != cudaSuccess) return SV_ERR_CUDA;
-  if (sv::launch(build_kernel, a.tiles_cap * a.Hkv, kBuildThreads, words * 8, stream, a) != cudaSuccess)
+  static PerDevice set_build, set_unit;
+  if (smem_limit_once(set_build, build_kernel, kMaxTable / 32 * 8) != cudaSuccess ||
+      smem_limit_once(set_unit, page_unit_kernel<D>, unit::Smem<D>::kAsk) != cudaSuccess)
     return SV_ERR_CUDA;
-  return launch_units<D, true>(a, tmK, tmV, stream);
+  if (sv::launch(build_kernel, a.tiles_cap * a.Hkv, kBuildThreads, words * 8, stream, a) != cudaSuccess ||
+      sv::launch(page_unit_kernel<D>, a.ctas, unit::kThreads, unit::Smem<D>::kAsk, stream, a, tmK, tmV, tmQ) !=
+          cudaSuccess ||
+      launch_merge<D, true>(a, stream) != cudaSuccess)
+    return SV_ERR_CUDA;
+  return SV_OK;
 }
 
 inline sv_status check_pages(const sv_paged_kv* kv, const sv_batch* bt, int32_t Hq, int32_t n_keep) {

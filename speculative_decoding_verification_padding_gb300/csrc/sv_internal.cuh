@@ -323,6 +323,7 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
 constexpr int kWaitLimit = 1 << 20;  // try_wait rounds before a wait gives up
 __device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity,
                                                   int limit = kWaitLimit) {
+#pragma unroll 1  // (unrolled, the waits of a kernel of many roles were a third of its code)
   for (int it = 0; it < limit; ++it)
     if (mbar_try_wait(bar, parity)) return true;
   return false;
@@ -331,6 +332,7 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity,
 // way (an answer takes a while when the tensor cores read shared memory).
 __device__ __forceinline__ bool mbar_wait2_bounded(uint32_t bar0, uint32_t parity0, uint32_t bar1,
                                                    uint32_t parity1) {
+#pragma unroll 1
   for (int it = 0; it < kWaitLimit; ++it) {
     const bool a = mbar_try_wait(bar0, parity0), b = mbar_try_wait(bar1, parity1);
     if (a && b) return true;
@@ -384,18 +386,6 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
       "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n"
       ::"r"(dst), "l"(src), "r"(bytes), "r"(bar)
       : "memory");
-}
-
-// Registers of a thread, for all warps of a warpgroup (four warps from a multiple of
-// four on): what some give back others may take, up to what the block was launched
-// with.
-template <int N>
-__device__ __forceinline__ void reg_dec() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void reg_inc() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N));
 }
 
 // --------------------------------------------- programmatic dependent launch --

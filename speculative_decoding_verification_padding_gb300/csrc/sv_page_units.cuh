@@ -28,7 +28,8 @@ constexpr int kStagePages = 8;   // pages of a stage
 constexpr int kTileRows = 128;   // virtual rows of a tile
 // Beginning a prefix list (its Q, the first copies, nothing yet to overlap with, and
 // writing out the one before) takes a CTA as long as about four stages: a list
-// counts so many more, before its own, when the stages are dealt out.
+// counts so many more, before its own, when the stages are dealt out (30 draft trees
+// behind three prompts: 57.5 us without, 51.7 with two, 50.6 with four and with six).
 constexpr int kListStart = 4;
 
 struct __align__(16) Tile {
@@ -43,18 +44,17 @@ struct Header {
   int T;       // tiles
   int W;       // stages of all lists
   int C;       // CTAs that share them (at most W)
-  int pad0;
   int Wp;      // stages of all prefix lists, their starts included
   int Cp;      // CTAs that share them
-  int pad[58];
+  int pad[59];
 };
 
-// Where a CTA's share of the prefix stages begins: group, list of the group and
-// stage of the list (negative: in its start); the group's lists, record and first
-// request.
-struct __align__(16) PStart {
+// The last stage of a CTA's share of the prefix stages: the group's record, the
+// group, the list among the group's, the stage behind the list's start (kListStart
+// counted, at), the group's first request.
+struct __align__(16) PEnd {
   int4 gr;
-  int k, list, st0, lists, leader, pad[3];
+  int k, list, at, leader;
 };
 
 struct Req;
@@ -92,7 +92,7 @@ struct Args {
   Req* req;           // [n_req]
   int4* groups;       // [n_groups] first active row, active rows, pages, first prefix list
   int* gstage;        // [n_groups + 1] first stage of each group's prefix lists, starts included
-  PStart* pstart;     // [ctas]
+  PEnd* pend;         // [ctas]
   int plists;         // prefix lists at most: 256-row tiles x KV heads
   float* pml;         // [plists + ctas][kPrefixRows][2]
   float* po;          // [plists + ctas][D / 4][kPrefixRows][4]
@@ -169,14 +169,16 @@ __device__ __forceinline__ uint32_t tail_visible(int m0, unsigned long long mk0,
 //     and sum, P (bf16) back over S; O is rescaled only where a row's max grows by
 //     more than 2^8; at a list's end O to the output or to a part, while the other
 //     warps begin the next list (one set of warps for all lists: 57 us for the own
-//     pages of 64 requests, 3 stages a list, where this takes 51);
+//     pages of 64 requests, five stages a list, where two take 51);
 //   warp 8: the copies of Q and K, warp 9 of V (two slots each);
 //   warp 10: one thread issues S = Q K^T (128 x 128) and O += P V (128 x D) as
 //     tcgen05.mma, QK^T of the next stage before PV of this one;
 //   warp 11: reads the lists ahead (a ring of kLists records in shared memory).
 // Tensor memory: S of two stages in columns 0 .. 255, O of two lists in 256 .. 511.
-// Bound by the pages' bytes: a stage of 64 KB (head_dim 128) is 1.5 us of one SM's
-// share of HBM, its products 0.7 us, its softmax 0.6 us.
+// Bound by the pages' bytes where all SMs do this: a stage of 64 KB (head_dim 128) is
+// 1.5 us of one SM's share of HBM, its products 0.7 us, its softmax 0.6 us (the own
+// choices of 48 chains: 97 us, 6.25 TB/s); an SM among others that do not read as
+// much takes 1.1 us.
 // Every wait is bounded; a CTA that gives up flags SV_DEV_TIMEOUT, lets copies and
 // products land and frees its tensor memory.
 namespace unit {
@@ -198,120 +200,65 @@ struct Rec {
   int first, ncomp, nent, lim;  // staged rows up to which slots are written
   int whole, bad, r0, grp;      // all of the list; some block outside the cache
 };
-}  // namespace unit
-
-template <int D, bool SPARSE>
-__global__ void __launch_bounds__(unit::kThreads, 1)
-    unit_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap tmK,
-                const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmQ) {
-  using unit::kLists;
-  using unit::Rec;
-  using S = unit::Smem<D>;
-  constexpr int kHalves = D / 64;
-  extern __shared__ __align__(1024) uint8_t smem_raw[];
-  __shared__ Rec s_rec[kLists];
-  __shared__ ulonglong2 s_anc[kLists][kTileRows];  // ancestors-or-self of the tile's rows
-  __shared__ int s_ids[kLists][kStagePages];       // blocks of a list's first stage
-  __shared__ int s_par[kMaxRows];
-  __shared__ int s_scan[32], s_carry, s_first[2];
+struct Shared {
+  Rec rec[kLists];
+  ulonglong2 anc[kLists][kTileRows];  // ancestors-or-self of the tile's rows
+  int ids[kLists][kStagePages];       // blocks of a list's first stage
+  int par[kMaxRows];
   // records there / free; K, V landed, PV done (V read), P written of a stage's slot;
   // S ready (K read) of a set of softmax warps and slot: a set counts its own stages
   // there, as a wait for a phase must not begin before the one before is over; Q
   // landed, O complete, O read of a list
-  __shared__ __align__(8) unsigned long long s_lfull[kLists], s_lfree[kLists], s_kfull[2], s_vfull[2],
-      s_sfull[2][2], s_odone[2], s_pfull[2], s_qfull[2], s_olast[2], s_ofree[2], s_drain;
-  __shared__ uint32_t s_tmem;
-  __shared__ int s_abort;
-  __shared__ int s_issued[6];  // phases begun of s_kfull, s_vfull, s_qfull
-  const int c = blockIdx.x;
+  unsigned long long lfull[kLists], lfree[kLists], kfull[2], vfull[2], sfull[2][2], odone[2], pfull[2],
+      qfull[2], olast[2], ofree[2], drain;
+  int abort;
+  int issued[6];  // phases begun of kfull, vfull, qfull
+};
+
+// By one thread, before the CTA's first barrier.
+__device__ __forceinline__ void init(Shared& sh) {
+  sh.abort = 0;
+  for (int k = 0; k < 6; ++k) sh.issued[k] = 0;
+  for (int k = 0; k < kLists; ++k) {
+    mbar_init(smem_u32(&sh.lfull[k]), 1);
+    mbar_init(smem_u32(&sh.lfree[k]), 11);  // eight softmax warps, two producers, the issuing thread
+  }
+  for (int k = 0; k < 2; ++k) {
+    mbar_init(smem_u32(&sh.kfull[k]), 1);
+    mbar_init(smem_u32(&sh.vfull[k]), 1);
+    mbar_init(smem_u32(&sh.sfull[k][0]), 1);
+    mbar_init(smem_u32(&sh.sfull[k][1]), 1);
+    mbar_init(smem_u32(&sh.odone[k]), 1);
+    mbar_init(smem_u32(&sh.pfull[k]), 128);
+    mbar_init(smem_u32(&sh.qfull[k]), 1);
+    mbar_init(smem_u32(&sh.olast[k]), 1);
+    mbar_init(smem_u32(&sh.ofree[k]), 128);
+  }
+  mbar_init(smem_u32(&sh.drain), 1);
+  fence_mbar_init();
+}
+}  // namespace unit
+
+// The work of CTA c of C: its share of W stages, the first of them of list x_start,
+// whose stages begin at off_start.  Q of two lists, then K slots and V slots from
+// `base` on (1024-byte aligned).
+template <int D, bool SPARSE>
+__device__ __forceinline__ void unit_share(const Args& a, const CUtensorMap& tmK, const CUtensorMap& tmV,
+                                           const CUtensorMap& tmQ, unit::Shared& sh, uint8_t* base_ptr,
+                                           uint32_t tmem, int c, int W, int C, int x_start, int off_start) {
+  using unit::kLists;
+  using unit::Rec;
+  using S = unit::Smem<D>;
+  constexpr int kHalves = D / 64;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  uint8_t* base_ptr = smem_raw + (base - smem_u32(smem_raw));
-  const uint32_t ring = base + 2 * S::kTile;  // Q of two lists, then K slots, V slots
-  // nothing that earlier kernels write is read before griddep_entry()
-  if (tid == 0) {
-    s_abort = 0;
-    for (int k = 0; k < 6; ++k) s_issued[k] = 0;
-    for (int k = 0; k < kLists; ++k) {
-      mbar_init(smem_u32(&s_lfull[k]), 1);
-      mbar_init(smem_u32(&s_lfree[k]), 11);  // eight softmax warps, two producers, the issuing thread
-    }
-    for (int k = 0; k < 2; ++k) {
-      mbar_init(smem_u32(&s_kfull[k]), 1);
-      mbar_init(smem_u32(&s_vfull[k]), 1);
-      mbar_init(smem_u32(&s_sfull[k][0]), 1);
-      mbar_init(smem_u32(&s_sfull[k][1]), 1);
-      mbar_init(smem_u32(&s_odone[k]), 1);
-      mbar_init(smem_u32(&s_pfull[k]), 128);
-      mbar_init(smem_u32(&s_qfull[k]), 1);
-      mbar_init(smem_u32(&s_olast[k]), 1);
-      mbar_init(smem_u32(&s_ofree[k]), 128);
-    }
-    mbar_init(smem_u32(&s_drain), 1);
-    fence_mbar_init();
-  }
-  if (warp == 8) {
-    if (lane == 0) {
-      prefetch_map(&tmK);
-      prefetch_map(&tmV);
-      prefetch_map(&tmQ);
-    }
-    __syncwarp();
-    tc5::tmem_alloc(smem_u32(&s_tmem), unit::kCols);
-    tc5::tmem_relinquish();
-  }
-  tc5::fence_before_sync();
-  __syncthreads();
-  tc5::fence_after_sync();
-  const uint32_t tmem = s_tmem;
-  griddep_entry();
-  int W, C, x_start, off_start;
-  if (SPARSE) {
-    // A run of lists a thread: the stages before it, and of all of them
-    const int lists = a.hdr->T * a.Hkv, per = (lists + unit::kThreads - 1) / unit::kThreads;
-    const int y0 = min(lists, tid * per), y1 = min(lists, y0 + per);
-    auto stages = [&](int y) { return (a.cnt[2 * y + 1] + kStagePages - 1) / kStagePages; };
-    int sum = 0;
-    for (int y = y0; y < y1; ++y) sum += stages(y);
-    if (tid == 0) s_carry = 0;
-    int at = block_scan(sum, s_scan, &s_carry);
-    W = s_carry;
-    C = min(a.ctas, W);
-    const int s0 = c < C ? share_start(c, W, C) : -1;
-    for (int y = y0; y < y1; ++y) {
-      if (c == 0) a.off[y] = at;  // for the merge
-      const int n = stages(y);
-      if (at <= s0 && s0 < at + n) {
-        s_first[0] = y;
-        s_first[1] = at;
-      }
-      at += n;
-    }
-    if (c == 0 && tid == 0) {
-      a.off[lists] = W;
-      a.hdr->W = W;
-      a.hdr->C = C;
-    }
-    __syncthreads();
-    x_start = s_first[0];
-    off_start = s_first[1];
-  } else {
-    W = a.hdr->W;
-    C = a.hdr->C;
-    x_start = a.start[c];
-    off_start = 0;
-  }
-  if (c >= C) {
-    if (warp == 8) tc5::tmem_dealloc(tmem, unit::kCols);
-    return;
-  }
-  auto gone = [&] { return *reinterpret_cast<volatile int*>(&s_abort) != 0; };
+  const uint32_t base = smem_u32(base_ptr), ring = base + 2 * S::kTile;
+  auto gone = [&] { return *reinterpret_cast<volatile int*>(&sh.abort) != 0; };
   // the record of list L, by a whole warp (or by one thread); null: gave up
   auto list_at = [&](int L) -> const Rec* {
-    if (!mbar_wait_bounded(smem_u32(&s_lfull[L % kLists]), (uint32_t)((L / kLists) & 1))) return nullptr;
-    return &s_rec[L % kLists];
+    if (!mbar_wait_bounded(smem_u32(&sh.lfull[L % kLists]), (uint32_t)((L / kLists) & 1))) return nullptr;
+    return &sh.rec[L % kLists];
   };
-  auto list_done = [&](int L) { mbar_arrive(smem_u32(&s_lfree[L % kLists])); };
+  auto list_done = [&](int L) { mbar_arrive(smem_u32(&sh.lfree[L % kLists])); };
   // block of entry e of a list, -1 past its end or outside the cache
   auto block_of = [&](const Rec& r, int e) {
     if (e >= r.nent) return -1;
@@ -356,45 +303,45 @@ __global__ void __launch_bounds__(unit::kThreads, 1)
           par[k] = tail && lane + 32 * k < tl.rows ? a.bt.parent[tl.cu + lane + 32 * k] : -1;
         const int b0 = block_of(r, r.e_first + lane);
         if (L >= kLists &&
-            !mbar_wait_bounded(smem_u32(&s_lfree[L % kLists]), (uint32_t)((L / kLists - 1) & 1)))
+            !mbar_wait_bounded(smem_u32(&sh.lfree[L % kLists]), (uint32_t)((L / kLists - 1) & 1)))
           ok = false;
         if (!__all_sync(0xffffffffu, ok) || __any_sync(0xffffffffu, gone())) {
           ok = false;
           break;
         }
-        if (lane < kStagePages) s_ids[L % kLists][lane] = b0;
+        if (lane < kStagePages) sh.ids[L % kLists][lane] = b0;
         bool bad = r.e_first + lane < e_end && b0 < 0;
         for (int e = r.e_first + 32 + lane; e < e_end; e += 32) bad |= block_of(r, e) < 0;
         if (bad) flag(a.dev_status, SV_DEV_BAD_BLOCK_ID);
         r.bad = __any_sync(0xffffffffu, bad);
         if (tail) {
 #pragma unroll
-          for (int k = 0; k < kMaxRows / 32; ++k) s_par[lane + 32 * k] = par[k];
+          for (int k = 0; k < kMaxRows / 32; ++k) sh.par[lane + 32 * k] = par[k];
           __syncwarp();
           for (int t = lane; t < tl.nr; t += 32) {
             unsigned long long lo = 0ull, hi = 0ull;
             int m = tl.r0 + t;
             for (int steps = 0; m >= 0 && steps <= kMaxRows; ++steps) {  // parents were checked
               if (m < 64) lo |= 1ull << m; else hi |= 1ull << (m - 64);
-              m = s_par[m];
+              m = sh.par[m];
             }
-            s_anc[L % kLists][t] = make_ulonglong2(lo, hi);
+            sh.anc[L % kLists][t] = make_ulonglong2(lo, hi);
           }
         }
       } else if (L >= kLists &&
-                 !mbar_wait_bounded(smem_u32(&s_lfree[L % kLists]), (uint32_t)((L / kLists - 1) & 1))) {
+                 !mbar_wait_bounded(smem_u32(&sh.lfree[L % kLists]), (uint32_t)((L / kLists - 1) & 1))) {
         ok = false;
         break;
       }
       __syncwarp();
       if (lane == 0) {
-        s_rec[L % kLists] = r;
-        mbar_arrive(smem_u32(&s_lfull[L % kLists]));
+        sh.rec[L % kLists] = r;
+        mbar_arrive(smem_u32(&sh.lfull[L % kLists]));
       }
       ++L;
       if (r.n_stage == 0) break;
     }
-    if (!ok) s_abort = 1;
+    if (!ok) sh.abort = 1;
   } else if (warp == 8 || warp == 9) {
     // --------------------------------------------------------- producers --
     const bool isV = warp == 9;
@@ -409,7 +356,7 @@ __global__ void __launch_bounds__(unit::kThreads, 1)
       }
       const Rec r = *rp;
       if (r.n_stage == 0) break;
-      int b = lane < kStagePages ? s_ids[L % kLists][lane] : -1;
+      int b = lane < kStagePages ? sh.ids[L % kLists][lane] : -1;
       __syncwarp();
       if (lane == 0) list_done(L);
       for (int st = 0; st < r.n_stage; ++st, ++n) {
@@ -418,8 +365,8 @@ __global__ void __launch_bounds__(unit::kThreads, 1)
         const int b1 = st + 1 < r.n_stage && lane < kStagePages ? block_of(r, e1) : -1;
         const int slot = n & 1;
         // the slot is free once the products of stage n - 2 have read it
-        bool go = n < 2 || (isV ? mbar_wait_bounded(smem_u32(&s_odone[slot]), (uint32_t)(((n - 2) >> 1) & 1))
-                                : mbar_wait_bounded(smem_u32(&s_sfull[(held >> slot) & 1][slot]),
+        bool go = n < 2 || (isV ? mbar_wait_bounded(smem_u32(&sh.odone[slot]), (uint32_t)(((n - 2) >> 1) & 1))
+                                : mbar_wait_bounded(smem_u32(&sh.sfull[(held >> slot) & 1][slot]),
                                                     (phase >> slot) & 1u));
         // the set and phase that will free the slot again
         const int set = L & 1;
@@ -432,18 +379,18 @@ __global__ void __launch_bounds__(unit::kThreads, 1)
         }
         if (!isV && st == 0 && lane == 0) {
           // Q of the list: its buffer's last reader was a list before stage n - 2
-          const uint32_t bar = smem_u32(&s_qfull[L & 1]), dst = base + (L & 1) * S::kTile;
+          const uint32_t bar = smem_u32(&sh.qfull[L & 1]), dst = base + (L & 1) * S::kTile;
           mbar_arrive_expect_tx(bar, (uint32_t)(kHalves * a.rt * a.group * 128));
-          s_issued[4 + (L & 1)] += 1;
+          sh.issued[4 + (L & 1)] += 1;
 #pragma unroll
           for (int h = 0; h < kHalves; ++h)
             tma_load_3d(dst + h * S::kHalf, &tmQ, 64 * h, r.g * a.group, r.row0, bar);
         }
-        const uint32_t bar = smem_u32(isV ? &s_vfull[slot] : &s_kfull[slot]);
+        const uint32_t bar = smem_u32(isV ? &sh.vfull[slot] : &sh.kfull[slot]);
         const int cnt = __popc(__ballot_sync(0xffffffffu, b >= 0));
         if (lane == 0) {
           mbar_arrive_expect_tx(bar, (uint32_t)(cnt * kHalves * 2048));
-          s_issued[2 * isV + slot] += 1;
+          sh.issued[2 * isV + slot] += 1;
         }
         __syncwarp();
         if (b >= 0) {
@@ -456,7 +403,7 @@ __global__ void __launch_bounds__(unit::kThreads, 1)
         b = b1;
       }
     }
-    if (!ok) s_abort = 1;
+    if (!ok) sh.abort = 1;
   } else if (warp == 10) {
     // --------------------------------------------------------- MMA issue --
     if (lane == 0) {
@@ -473,11 +420,11 @@ __global__ void __launch_bounds__(unit::kThreads, 1)
       if (ok) nq = np = rq->n_stage;
       auto qk = [&]() -> bool {  // stage n_q
         const int n = n_q, slot = n & 1;
-        if (sq == 0 && !mbar_wait_bounded(smem_u32(&s_qfull[Lq & 1]), (uint32_t)((Lq >> 1) & 1))) return false;
+        if (sq == 0 && !mbar_wait_bounded(smem_u32(&sh.qfull[Lq & 1]), (uint32_t)((Lq >> 1) & 1))) return false;
         // K has landed; PV of stage n - 2 is through with its P, where S goes
-        const uint32_t kf = smem_u32(&s_kfull[slot]), kp = (uint32_t)((n >> 1) & 1);
+        const uint32_t kf = smem_u32(&sh.kfull[slot]), kp = (uint32_t)((n >> 1) & 1);
         if (!(n < 2 ? mbar_wait_bounded(kf, kp)
-                    : mbar_wait2_bounded(kf, kp, smem_u32(&s_odone[slot]), (uint32_t)(((n - 2) >> 1) & 1))))
+                    : mbar_wait2_bounded(kf, kp, smem_u32(&sh.odone[slot]), (uint32_t)(((n - 2) >> 1) & 1))))
           return false;
         tc5::fence_after_sync();
         const uint64_t ad = qd + (uint64_t)((Lq & 1) * (S::kTile >> 4));
@@ -487,7 +434,7 @@ __global__ void __launch_bounds__(unit::kThreads, 1)
           const uint64_t o = (uint64_t)(((ks >> 2) * S::kHalf + (ks & 3) * 32) >> 4);
           tc5::mma_bf16(tmem + (uint32_t)(slot * kTok), ad + o, bd + o, idesc_qk, ks > 0 ? 1u : 0u);
         }
-        tc5::commit(smem_u32(&s_sfull[Lq & 1][slot]));
+        tc5::commit(smem_u32(&sh.sfull[Lq & 1][slot]));
         ++n_q;
         if (++sq == nq) {
           ++Lq;
@@ -504,10 +451,10 @@ __global__ void __launch_bounds__(unit::kThreads, 1)
         const int slot = n & 1;
         // V has landed, P is there; at a list's first stage O of the list two before
         // has been read
-        ok = mbar_wait2_bounded(smem_u32(&s_vfull[slot]), (uint32_t)((n >> 1) & 1),
-                                smem_u32(&s_pfull[slot]), (uint32_t)((n >> 1) & 1)) &&
+        ok = mbar_wait2_bounded(smem_u32(&sh.vfull[slot]), (uint32_t)((n >> 1) & 1),
+                                smem_u32(&sh.pfull[slot]), (uint32_t)((n >> 1) & 1)) &&
              (sp > 0 || Lp < 2 ||
-              mbar_wait_bounded(smem_u32(&s_ofree[Lp & 1]), (uint32_t)(((Lp >> 1) - 1) & 1))) &&
+              mbar_wait_bounded(smem_u32(&sh.ofree[Lp & 1]), (uint32_t)(((Lp >> 1) - 1) & 1))) &&
              !gone();
         if (!ok) break;
         tc5::fence_after_sync();
@@ -517,10 +464,10 @@ __global__ void __launch_bounds__(unit::kThreads, 1)
         for (int ks = 0; ks < kTok / 16; ++ks)
           tc5::mma_bf16_ts(to, tmem + (uint32_t)(slot * kTok) + ks * 8, bd + (uint64_t)(ks * 2048 >> 4),
                            idesc_pv, (sp > 0 || ks > 0) ? 1u : 0u);
-        tc5::commit(smem_u32(&s_odone[slot]));
+        tc5::commit(smem_u32(&sh.odone[slot]));
         if (++sp == np) {
           // (the next lists may run on before this one's O is read: a barrier of its own)
-          tc5::commit(smem_u32(&s_olast[Lp & 1]));
+          tc5::commit(smem_u32(&sh.olast[Lp & 1]));
           list_done(Lp);
           ++Lp;
           sp = 0;
@@ -532,10 +479,10 @@ __global__ void __launch_bounds__(unit::kThreads, 1)
           np = r->n_stage;
         }
       }
-      if (!ok) s_abort = 1;
+      if (!ok) sh.abort = 1;
       // every product has landed before the CTA moves on
-      tc5::commit(smem_u32(&s_drain));
-      mbar_wait_bounded(smem_u32(&s_drain), 0);
+      tc5::commit(smem_u32(&sh.drain));
+      mbar_wait_bounded(smem_u32(&sh.drain), 0);
     }
   } else {
     // ----------------------------------------------------- softmax, rows --
@@ -567,7 +514,7 @@ __global__ void __launch_bounds__(unit::kThreads, 1)
       const bool some = (warp & 3) * 32 < vrows;  // rows in this warp at all
       ulonglong2 anc = make_ulonglong2(0ull, 0ull);
       const int e_end = min(r.nent, r.e_first + r.n_stage * kStagePages);
-      if (e_end > r.ncomp) anc = s_anc[L % kLists][lr];
+      if (e_end > r.ncomp) anc = sh.anc[L % kLists][lr];
       __syncwarp();
       if (lane == 0) list_done(L);
       const uint32_t* see = SPARSE ? a.see + ((size_t)r.x * a.rt + lr) * (a.cap / 32) : nullptr;
@@ -581,7 +528,7 @@ __global__ void __launch_bounds__(unit::kThreads, 1)
         if (SPARSE && (e0 & 31) == 0 && st > 0) bits = bits1;
         if (SPARSE && (e0 & 31) == 24 && st + 1 < r.n_stage) bits1 = __ldg(see + (e0 >> 5) + 1);
         const uint32_t vis = SPARSE ? bits >> (e0 & 31) : 0xffu;  // pages of the stage the row sees
-        const bool got = mbar_wait_bounded(smem_u32(&s_sfull[L & 1][slot]), (count >> slot) & 1u);
+        const bool got = mbar_wait_bounded(smem_u32(&sh.sfull[L & 1][slot]), (count >> slot) & 1u);
         count ^= 1u << slot;
         if (!__all_sync(0xffffffffu, got)) {
           ok = false;
@@ -650,7 +597,7 @@ __global__ void __launch_bounds__(unit::kThreads, 1)
             const float m_new = grow ? mx : m_ref;
             const float alpha = grow ? ex2(m_ref - m_new) : 1.f;  // 0 while m_ref is -inf
             if (st > 0) {
-              const bool g2 = mbar_wait_bounded(smem_u32(&s_odone[(n - 1) & 1]), (uint32_t)(((n - 1) >> 1) & 1));
+              const bool g2 = mbar_wait_bounded(smem_u32(&sh.odone[(n - 1) & 1]), (uint32_t)(((n - 1) >> 1) & 1));
               if (!__all_sync(0xffffffffu, g2)) {
                 ok = false;
                 break;
@@ -714,13 +661,14 @@ __global__ void __launch_bounds__(unit::kThreads, 1)
         if (odd) {
           // rows of V that nothing was written to may hold anything: zeros, so that
           // their weights of 0 add nothing
-          const bool gv = mbar_wait_bounded(smem_u32(&s_vfull[slot]), (uint32_t)((n >> 1) & 1));
+          const bool gv = mbar_wait_bounded(smem_u32(&sh.vfull[slot]), (uint32_t)((n >> 1) & 1));
           if (!__all_sync(0xffffffffu, gv)) {
             ok = false;
             break;
           }
           uint8_t* vb = base_ptr + (ring - base) + (2 + slot) * S::kTile;
           auto zero = [&](int t0, int t1) {  // rows t0 .. t1 - 1 of V
+#pragma unroll 1
             for (int y = row_t; y < (t1 - t0) * (D / 8); y += 128) {
               const int t = t0 + y / (D / 8), ch = y % (D / 8);
               *reinterpret_cast<int4*>(vb + (ch >> 3) * S::kHalf + t * 128 + (((ch & 7) ^ (t & 7)) << 4)) =
@@ -729,17 +677,17 @@ __global__ void __launch_bounds__(unit::kThreads, 1)
           };
           // behind the last staged slot, and (where a block is missing) whole pages
           zero(min(kTok, max(0, (r.ncomp - e0) * kBlockSize + r.lim - tail0)), kTok);
-          if (r.bad)
-            for (int p = 0; p < kStagePages; ++p)
-              if (!((there >> p) & 1u)) zero(16 * p, 16 * p + 16);
+#pragma unroll 1
+          for (int p = 0; p < (r.bad ? kStagePages : 0); ++p)
+            if (!((there >> p) & 1u)) zero(16 * p, 16 * p + 16);
           fence_proxy_async_smem();
         }
         tc5::fence_before_sync();
-        mbar_arrive(smem_u32(&s_pfull[slot]));
+        mbar_arrive(smem_u32(&sh.pfull[slot]));
       }
       if (!ok) break;
       // the list's last PV has landed: O, normalised, to the output or to a part
-      const bool last = mbar_wait_bounded(smem_u32(&s_olast[L & 1]), (uint32_t)((L >> 1) & 1));
+      const bool last = mbar_wait_bounded(smem_u32(&sh.olast[L & 1]), (uint32_t)((L >> 1) & 1));
       if (!__all_sync(0xffffffffu, last)) {
         ok = false;
         break;
@@ -776,27 +724,26 @@ __global__ void __launch_bounds__(unit::kThreads, 1)
         if (real && !out) reinterpret_cast<float2*>(a.ml)[part * a.tile_vr + row_t] = make_float2(m_ref, l);
       }
       tc5::fence_before_sync();
-      mbar_arrive(smem_u32(&s_ofree[L & 1]));
+      mbar_arrive(smem_u32(&sh.ofree[L & 1]));
     }
-    if (!ok) s_abort = 1;
+    if (!ok) sh.abort = 1;
   }
 
   // every role is done with tensor memory and the ring
   tc5::fence_before_sync();
   __syncthreads();
   tc5::fence_after_sync();
-  if (s_abort) {
+  if (sh.abort) {
     // copies in flight land before the CTA leaves (bounded waits)
     if (tid == 0) {
       flag(a.dev_status, SV_DEV_TIMEOUT);
       for (int k = 0; k < 6; ++k)
-        if (s_issued[k] > 0)
-          mbar_wait_bounded(smem_u32(k < 2 ? &s_kfull[k] : k < 4 ? &s_vfull[k - 2] : &s_qfull[k - 4]),
-                            (uint32_t)((s_issued[k] - 1) & 1));
+        if (sh.issued[k] > 0)
+          mbar_wait_bounded(smem_u32(k < 2 ? &sh.kfull[k] : k < 4 ? &sh.vfull[k - 2] : &sh.qfull[k - 4]),
+                            (uint32_t)((sh.issued[k] - 1) & 1));
     }
     __syncthreads();
   }
-  if (warp == 8) tc5::tmem_dealloc(tmem, unit::kCols);
 }
 
 // ------------------------------------------------------------------ merge --
@@ -815,10 +762,9 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_const
   constexpr int kLoads = 4;
   const int x = blockIdx.x;
   const int T = a.hdr->T, W = a.hdr->W, C = a.hdr->C, Wp = a.hdr->Wp, Cp = a.hdr->Cp;
-  if (x >= T * a.Hkv) return;
-  const int off0 = a.off[x], off1 = a.off[x + 1];
+  const int off0 = a.off[x], off1 = a.off[x + 1];  // (anything past the last list)
   const Tile tl = a.tiles[x / a.Hkv];
-  if (off0 == off1) return;
+  if (x >= T * a.Hkv || off0 == off1) return;
   const int g = x % a.Hkv, group = a.group;
   const int vr0 = blockIdx.y * 32, vrows = tl.nr * group;
   if (vr0 >= vrows) return;
@@ -987,18 +933,9 @@ inline bool make_q_map(CUtensorMap* map, const Args& a, int D) {
 }
 
 template <int D, bool SPARSE>
-inline sv_status launch_units(const Args& a, const CUtensorMap& tmK, const CUtensorMap& tmV,
-                              cudaStream_t stream) {
-  CUtensorMap tmQ;
-  if (!make_q_map(&tmQ, a, D)) return SV_ERR_CUDA;
-  static PerDevice set;
-  if (smem_limit_once(set, unit_kernel<D, SPARSE>, unit::Smem<D>::kAsk) != cudaSuccess) return SV_ERR_CUDA;
-  if (sv::launch(unit_kernel<D, SPARSE>, a.ctas, unit::kThreads, unit::Smem<D>::kAsk, stream, a, tmK, tmV,
-                 tmQ) != cudaSuccess)
-    return SV_ERR_CUDA;
+inline cudaError_t launch_merge(const Args& a, cudaStream_t stream) {
   const dim3 grid(a.tiles_cap * a.Hkv, (a.tile_vr + 31) / 32);
-  if (sv::launch(merge_kernel<D, SPARSE>, grid, kMergeThreads, 0, stream, a) != cudaSuccess) return SV_ERR_CUDA;
-  return SV_OK;
+  return sv::launch(merge_kernel<D, SPARSE>, grid, kMergeThreads, 0, stream, a);
 }
 
 }  // namespace pu
