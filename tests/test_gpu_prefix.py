@@ -28,7 +28,8 @@ class Shared(Setup):
         for p, own in groups:
             a, b = cu[-1], cu[-1] + len(own)
             cu.append(b)
-            self.np_tables[a + 1:b, :p // 16] = self.np_tables[a, :p // 16]
+            if own:
+                self.np_tables[a + 1:b, :p // 16] = self.np_tables[a, :p // 16]
             first.append(p)
         given = self.np_tables.copy()
         for (p, _), a, b in zip(groups, cu, cu[1:]):
@@ -165,4 +166,33 @@ def test_prefix_in_a_graph_and_on_another_stream():
     out.fill_(7.0)
     graph.replay()
     s.check(out)
+    assert s.status.item() == 0
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("missing", [None, 24, 7])
+def test_prefix_shares_of_several_lists(dim, missing):
+    # about three lists a CTA: whole lists begin where the one before stopped, so
+    # that the last, incomplete stage (of one page) comes in their midst
+    s = Shared([(400, [3] * 30), (208, [0, 20] * 10), (0, [9])], [40] * 30 + [38] * 20 + [3], 32, 8, dim, seed=dim)
+    if missing is not None:
+        s.kv.block_tables[0, missing] = -1
+    got = s.run()
+    assert s.status.item() == (0 if missing is None else N.SV_DEV_BAD_BLOCK_ID)
+    check_attend(s, got, lambda i, r, g: [t for t in range(s.ctx[i]) if i >= 30 or t // 16 != missing])
+    assert torch.equal(s.run().view(torch.int16), got.view(torch.int16))
+
+
+@pytest.mark.parametrize("n", [1, 40, 300])
+def test_prefix_groups_of_one_and_of_none(n):
+    # groups without requests, without rows and without a prefix among others
+    rng = np.random.default_rng(n)
+    groups = [(16 * int(rng.integers(0, 12)), rng.integers(0, 40, int(rng.integers(0, 5))).tolist()) for _ in range(n)]
+    groups += [(144, [5, 0]), (32, []), (16, [1])]
+    total = sum(len(own) for _, own in groups)
+    rows = rng.integers(1, 4, total).tolist()
+    s = Shared(groups, rows, 4, 2, 64, seed=n)
+    keep = rng.random(total) > 0.3
+    s.window(begin=[0] * total, end=[r if k else 0 for r, k in zip(rows, keep)], verify=rows)
+    s.check(s.run())
     assert s.status.item() == 0
