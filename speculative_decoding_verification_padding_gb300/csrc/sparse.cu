@@ -19,11 +19,18 @@ namespace pu {
 
 constexpr int kMaxTable = 1 << 18;  // table entries a request may have (bits in shared memory)
 constexpr int kBuildThreads = 256;
+// Entries of the rows' lists that a thread keeps in registers: the first of a tile,
+// kHeld x 256 of them; of longer lists it reads the rest again for each step.
+constexpr int kHeld = 6;
 
+// Bound by latency, a chain of loads and barriers: what a step needs is asked for as
+// soon as its address is known (48 chains of 4000 .. 60000 tokens, 128 pages a row and
+// head: 5.2 us after the wait; each step with its own loads, 8.2).
 __global__ void __launch_bounds__(kBuildThreads) build_kernel(const __grid_constant__ Args a) {
   griddep_entry();
   extern __shared__ uint32_t s_bits[];  // one bit a page, then the bits before each word
-  __shared__ int s_warp[32], s_carry, s_req, s_k;
+  __shared__ int s_warp[32], s_carry, s_req, s_k, s_ctx;
+  __shared__ Window s_win;
   __shared__ int s_len[kTileRows];
   const int x = blockIdx.x, tile = x / a.Hkv, g = x % a.Hkv, R = a.bt.n_req;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -35,9 +42,11 @@ __global__ void __launch_bounds__(kBuildThreads) build_kernel(const __grid_const
   }
   for (int base = 0; base < R; base += kBuildThreads) {
     const int i = base + tid;
-    int nt = 0;
+    Window w{};
+    int nt = 0, ctx = 0;
     if (i < R) {
-      const Window w = window_of(a.bt, i);
+      w = window_of(a.bt, i);
+      ctx = a.lens[i];
       if (w.ok) nt = (max(w.b, w.e) - w.b + a.rt - 1) / a.rt;
       else if (x == 0) flag(a.dev_status, SV_DEV_BAD_WINDOW);
     }
@@ -45,6 +54,8 @@ __global__ void __launch_bounds__(kBuildThreads) build_kernel(const __grid_const
     if (at <= tile && tile < at + nt) {
       s_req = i;
       s_k = tile - at;
+      s_win = w;
+      s_ctx = ctx;
     }
   }
   __syncthreads();
@@ -55,9 +66,33 @@ __global__ void __launch_bounds__(kBuildThreads) build_kernel(const __grid_const
     a.hdr->T = T;
   }
   if (tile >= T) return;
-  const int i = s_req, ctx = a.lens[i];
-  const Window w = window_of(a.bt, i);
+  const int i = s_req, ctx = s_ctx;
+  const Window w = s_win;
   const int r0 = w.b + s_k * a.rt, nr = min(a.rt, w.e - r0), n = max(ctx, 0) / kBlockSize;
+  // a warp takes 32 entries of a row at once
+  constexpr int kWarps = kBuildThreads / 32;
+  const int32_t* rows = a.pages + ((size_t)(w.cu + r0) * a.Hkv + g) * a.n_keep;
+  const int32_t* table = a.tables + (size_t)i * a.max_blocks;
+  const size_t row_step = (size_t)a.Hkv * a.n_keep;
+  const int chunks = (a.n_keep + 31) / 32, runs = nr * chunks;
+  struct Entry {
+    int r, k, page, prev, block;
+  };
+  auto read = [&](int y) {  // (page and the one before it, where there are any)
+    Entry e{0, a.n_keep, -1, -1, -1};
+    if (y < runs) {
+      e.r = y / chunks;
+      e.k = (y - e.r * chunks) * 32 + lane;
+      const int32_t* list = rows + e.r * row_step + e.k;
+      if (e.k < a.n_keep) e.page = __ldg(list);
+      if (e.k < a.n_keep && e.k > 0) e.prev = __ldg(list - 1);
+    }
+    return e;
+  };
+  auto block_of = [&](int page) { return page >= 0 && page < a.max_blocks ? __ldg(table + page) : -1; };
+  Entry held[kHeld];
+#pragma unroll
+  for (int q = 0; q < kHeld; ++q) held[q] = read(warp + q * kWarps);
   bool bad = false;
   if (tid < w.rows) {
     const int p = a.bt.parent[w.cu + tid];
@@ -67,6 +102,8 @@ __global__ void __launch_bounds__(kBuildThreads) build_kernel(const __grid_const
   const int words = fits ? (n + 31) / 32 : 0;
   uint32_t* s_before = s_bits + words;
   for (int y = tid; y < words; y += kBuildThreads) s_bits[y] = 0u;
+  uint32_t* see = a.see + (size_t)x * a.rt * (a.cap / 32);
+  for (int y = tid; y < nr * (a.cap / 32); y += kBuildThreads) see[y] = 0u;
   if (tid < nr) s_len[tid] = a.n_keep;
   if (tid == 0) s_carry = 0;
   if (__syncthreads_or(bad) || !fits) {
@@ -87,28 +124,30 @@ __global__ void __launch_bounds__(kBuildThreads) build_kernel(const __grid_const
     t.rows = w.rows;
     a.tiles[tile] = t;
   }
-  uint32_t* see = a.see + (size_t)x * a.rt * (a.cap / 32);
-  for (int y = tid; y < nr * (a.cap / 32); y += kBuildThreads) see[y] = 0u;
-  // a warp takes 32 entries of a row at once
-  const int32_t* rows = a.pages + ((size_t)(w.cu + r0) * a.Hkv + g) * a.n_keep;
-  const size_t row_step = (size_t)a.Hkv * a.n_keep;
-  const int chunks = (a.n_keep + 31) / 32;
+  const int ntail = (ctx + r0 + nr + kBlockSize - 1) / kBlockSize - n;
+  const int tail_block = tid < ntail ? __ldg(table + n + tid) : -1;
+#pragma unroll
+  for (int q = 0; q < kHeld; ++q) held[q].block = block_of(held[q].page);
   auto entries = [&](auto&& f) {
-    for (int y = warp; y < nr * chunks; y += kBuildThreads / 32) {
-      const int r = y / chunks, k = y % chunks * 32 + lane;
-      if (k < a.n_keep) f(r, k, rows + r * row_step);
+#pragma unroll
+    for (int q = 0; q < kHeld; ++q)
+      if (held[q].k < a.n_keep) f(held[q]);
+    for (int y = warp + kHeld * kWarps; y < runs; y += kWarps) {
+      Entry e = read(y);
+      if (e.k < a.n_keep) {
+        e.block = block_of(e.page);
+        f(e);
+      }
     }
   };
   // a row's list ends where its pages stop to ascend
-  entries([&](int r, int k, const int32_t* list) {
-    const int v = __ldg(list + k), prev = k ? __ldg(list + k - 1) : -1;
-    if (v <= prev || v >= n) atomicMin(&s_len[r], k);
+  entries([&](const Entry& e) {
+    if (e.page <= e.prev || e.page >= n) atomicMin(&s_len[e.r], e.k);
   });
   __syncthreads();
-  entries([&](int r, int k, const int32_t* list) {
-    const int v = __ldg(list + k);
-    if (k < s_len[r]) atomicOr(&s_bits[v >> 5], 1u << (v & 31));
-    else if (k == s_len[r] && v != -1) flag(a.dev_status, SV_DEV_BAD_PARAM);
+  entries([&](const Entry& e) {
+    if (e.k < s_len[e.r]) atomicOr(&s_bits[e.page >> 5], 1u << (e.page & 31));
+    else if (e.k == s_len[e.r] && e.page != -1) flag(a.dev_status, SV_DEV_BAD_PARAM);
   });
   __syncthreads();
   for (int base = 0; base < words; base += kBuildThreads) {
@@ -119,16 +158,13 @@ __global__ void __launch_bounds__(kBuildThreads) build_kernel(const __grid_const
   __syncthreads();
   const int U = s_carry;
   int* blk = a.blk + (size_t)x * a.cap;
-  const int32_t* table = a.tables + (size_t)i * a.max_blocks;
-  entries([&](int r, int k, const int32_t* list) {
-    if (k >= s_len[r]) return;
-    const int v = __ldg(list + k);
-    const int pos = (int)s_before[v >> 5] + __popc(s_bits[v >> 5] & ((1u << (v & 31)) - 1u));
-    blk[pos] = __ldg(table + v);  // the same from every row that lists it
-    atomicOr(see + (size_t)r * (a.cap / 32) + (pos >> 5), 1u << (pos & 31));
+  entries([&](const Entry& e) {
+    if (e.k >= s_len[e.r]) return;
+    const int v = e.page, pos = (int)s_before[v >> 5] + __popc(s_bits[v >> 5] & ((1u << (v & 31)) - 1u));
+    blk[pos] = e.block;  // the same from every row that lists it
+    atomicOr(see + (size_t)e.r * (a.cap / 32) + (pos >> 5), 1u << (pos & 31));
   });
-  const int ntail = (ctx + r0 + nr + kBlockSize - 1) / kBlockSize - n;
-  if (tid < ntail) blk[U + tid] = __ldg(table + n + tid);
+  if (tid < ntail) blk[U + tid] = tail_block;
   if (tid == 0) {
     a.cnt[2 * x] = U;
     a.cnt[2 * x + 1] = U + ntail;
