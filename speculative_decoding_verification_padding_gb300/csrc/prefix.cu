@@ -45,14 +45,9 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
   const int32_t* cu_groups = small ? sm.cu_groups : a.cu_groups;
   const int32_t* prefix_len = small ? sm.prefix_len : a.prefix_len;
   if (tid == 0) s_groups_bad = 0;
-  __syncthreads();
-  // groups that do not cut the requests into runs: nothing is attended
-  for (int k = tid; k <= G; k += blockDim.x) {
-    const int v = a.cu_groups[k], next = k < G ? a.cu_groups[k + 1] : R;
-    if (small) sm.cu_groups[k] = v;
-    if (small && k < G) sm.prefix_len[k] = a.prefix_len[k];
-    if ((k == 0 && v != 0) || (k < G ? v > next : v != R)) s_groups_bad = 1;
-  }
+  // (asked for ahead of what the requests' rows are read for)
+  const int k0 = min(tid, G), cu0 = a.cu_groups[k0], cu1 = a.cu_groups[min(k0 + 1, G)],
+            len0 = a.prefix_len[min(k0, G - 1)];
   // windows, parents and lengths, 16 lanes a request; what cannot be attended is
   // reported and left out
   constexpr int kLanes = 16;
@@ -91,6 +86,17 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
   }
   if (tid == 0 && (a.bt.cu_rows[0] != 0 || a.bt.cu_rows[R] != a.bt.total_rows))
     flag(a.dev_status, SV_DEV_BAD_WINDOW);
+  // groups that do not cut the requests into runs: nothing is attended
+  auto check = [&](int k, int v, int next) {
+    if ((k == 0 && v != 0) || (k < G ? v > next : v != R)) s_groups_bad = 1;
+  };
+  __syncthreads();
+  if (tid <= G) check(tid, cu0, cu1);
+  for (int k = tid + kPlanThreads; k <= G; k += kPlanThreads) check(k, a.cu_groups[k], a.cu_groups[min(k + 1, G)]);
+  if (small && tid <= G) {
+    sm.cu_groups[tid] = cu0;
+    if (tid < G) sm.prefix_len[tid] = len0;
+  }
   __syncthreads();
   if (s_groups_bad) {
     if (tid == 0) {
@@ -99,6 +105,16 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
     }
     return;
   }
+  // The last entry at or before v of a table that does not descend (entries of none
+  // are as the one behind them).
+  auto last_at = [&](int n, int v, auto&& at) {
+    int lo = 0;
+    for (int hi = n - 1; lo < hi;) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (at(mid) <= v) lo = mid; else hi = mid - 1;
+    }
+    return lo;
+  };
   // the request's group, tiles and stages
   auto stages_of = [&](const Req& r, int k) {  // of its tile k
     return ((r.ctx + min(r.b + (k + 1) * a.rt, r.e) + kBlockSize - 1) / kBlockSize - r.first + kStagePages - 1) /
@@ -106,12 +122,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
   };
   for (int i = tid; i < R; i += blockDim.x) {
     Req r = req[i];
-    int lo = 0;
-    for (int hi = G - 1; lo < hi;) {  // the last group that begins at or before i
-      const int mid = (lo + hi + 1) >> 1;
-      if (cu_groups[mid] <= i) lo = mid; else hi = mid - 1;
-    }
-    const int p = prefix_len[lo];
+    const int lo = last_at(G, i, [&](int k) { return cu_groups[k]; }), p = prefix_len[lo];
     if (r.e > r.b && (p < 0 || p % kBlockSize != 0 || p > r.ctx)) {
       flag(a.dev_status, p < 0 || p % kBlockSize != 0 ? SV_DEV_BAD_PARAM : SV_DEV_BAD_LENGTH);
       r.e = r.b;
@@ -219,66 +230,70 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
     Cp = min(Wp, max(1, min(a.ctas - 1, (int)((a.ctas * wp + all / 2) / all))));
     C = min(W, max(1, a.ctas - Cp));
   }
-  if (warp > 0) {
-    // tiles, first stages of their lists, active rows: a warp a request
-    if (tid == 32) {
-      a.hdr->T = s_tiles;
-      a.hdr->W = W;
-      a.hdr->C = C;
-      a.off[(size_t)s_tiles * a.Hkv] = W;
-    }
-    for (int i = warp - 1; i < R; i += kPlanThreads / 32 - 1) {
-      const Req r = req[i];
-      for (int k = lane; k < r.e - r.b; k += 32) a.arows[r.arow + k] = r.cu + r.b + k;
-      int stage = r.stage * a.Hkv;
-      for (int k = 0, b = r.b; b < r.e; ++k, b += a.rt) {
-        const int n = stages_of(r, k);
-        for (int g = lane; g < a.Hkv; g += 32) {
-          const int x = (r.tile + k) * a.Hkv + g;
-          a.off[x] = stage + g * n;
-          deal_list(a, x, stage + g * n, stage + (g + 1) * n, W, C);
-        }
-        stage += a.Hkv * n;
-        if (lane == 0) {
-          Tile t{};
-          t.i = i;
-          t.cu = r.cu;
-          t.ctx = r.ctx;
-          t.r0 = b;
-          t.nr = min(a.rt, r.e - b);
-          t.rows = r.rows;
-          t.first = r.first;
-          t.ncomp = r.ctx / kBlockSize - r.first;
-          t.nent = (r.ctx + b + t.nr + kBlockSize - 1) / kBlockSize - r.first;
-          t.arow = r.arow + k * a.rt;
-          t.grp = r.grp;
-          a.tiles[r.tile + k] = t;
-        }
-      }
-    }
-    return;
-  }
-  // where each CTA's share of the prefix stages ends
-  if (lane == 0) {
-    a.gstage[G] = Wp;
+  if (tid == 0) {
+    a.hdr->T = s_tiles;
+    a.hdr->W = W;
+    a.hdr->C = C;
     a.hdr->Wp = Wp;
     a.hdr->Cp = Cp;
+    a.off[(size_t)s_tiles * a.Hkv] = W;
+    a.gstage[G] = Wp;
   }
-  __syncwarp();
-  for (int c = lane; c < Cp; c += 32) {
+  // Each table from a thread of its own on, as most are short.
+  auto from = [&](int first) { return (tid - first) & (kPlanThreads - 1); };
+  // the list of the first stage of each CTA's share of the own stages
+  for (int c = tid; c < C; c += kPlanThreads) {
+    int s = share_start(c, W, C), k = 0;
+    const int sh = s / a.Hkv;
+    const Req r = req[last_at(R, sh, [&](int i) { return req[i].stage; })];
+    s -= r.stage * a.Hkv;
+    int n = stages_of(r, 0);
+    while (s >= n * a.Hkv) {
+      s -= n * a.Hkv;
+      n = stages_of(r, ++k);
+    }
+    a.start[c] = (r.tile + k) * a.Hkv + s / n;
+  }
+  // the last stage of each CTA's share of the prefix stages
+  for (int c = from(160); c < Cp; c += kPlanThreads) {
     const int s = share_start(c + 1, Wp, Cp) - 1;
     PEnd ps{};
-    ps.k = 0;  // the last group whose stages begin at or before s
-    for (int hi = G - 1; ps.k < hi;) {
-      const int mid = (ps.k + hi + 1) >> 1;
-      if (gstage[mid] <= s) ps.k = mid; else hi = mid - 1;
-    }
+    ps.k = last_at(G, s, [&](int k) { return gstage[k]; });
     ps.gr = groups[ps.k];
     const int sp = (ps.gr.z + kStagePages - 1) / kStagePages + kListStart;
     ps.list = (s - gstage[ps.k]) / sp;
-    ps.at = (s - gstage[ps.k]) % sp;
+    ps.at = (s - gstage[ps.k]) - ps.list * sp;
     ps.leader = cu_groups[ps.k];
     a.pend[c] = ps;
+  }
+  // active rows
+  for (int y = from(320); y < s_rows; y += kPlanThreads) {
+    const Req r = req[last_at(R, y, [&](int i) { return req[i].arow; })];
+    a.arows[y] = r.cu + r.b + y - r.arow;
+  }
+  // tiles and the first stages of their lists
+  for (int x = from(512); x < s_tiles * a.Hkv; x += kPlanThreads) {
+    const int tile = x / a.Hkv, g = x - tile * a.Hkv;
+    const int i = last_at(R, tile, [&](int j) { return req[j].tile; });
+    const Req r = req[i];
+    const int k = tile - r.tile;
+    int before = 0;
+    for (int j = 0; j < k; ++j) before += stages_of(r, j);
+    a.off[x] = (r.stage + before) * a.Hkv + g * stages_of(r, k);
+    if (g != 0) continue;
+    Tile t{};
+    t.i = i;
+    t.cu = r.cu;
+    t.ctx = r.ctx;
+    t.r0 = r.b + k * a.rt;
+    t.nr = min(a.rt, r.e - t.r0);
+    t.rows = r.rows;
+    t.first = r.first;
+    t.ncomp = r.ctx / kBlockSize - r.first;
+    t.nent = (r.ctx + t.r0 + t.nr + kBlockSize - 1) / kBlockSize - r.first;
+    t.arow = r.arow + k * a.rt;
+    t.grp = r.grp;
+    a.tiles[tile] = t;
   }
 }
 

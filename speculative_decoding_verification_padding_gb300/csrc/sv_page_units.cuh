@@ -104,14 +104,6 @@ __device__ __forceinline__ int share_of(int s, int W, int C) { return (int)((((l
 
 // ------------------------------------------------------------------ lists --
 
-// List x has the stages off0 .. off1 - 1 of W: it is the first list of the CTAs
-// whose share begins there (C = min(a.ctas, W) of them).
-__device__ __forceinline__ void deal_list(const Args& a, int x, int off0, int off1, int W, int C) {
-  if (off0 >= off1) return;
-  // the least c with floor(c W / C) >= off0
-  for (int c = (int)(((long)off0 * C + W - 1) / W); c < C && share_start(c, W, C) < off1; ++c) a.start[c] = x;
-}
-
 // What the plan of a prefix call keeps of a request.
 struct Req {
   int cu, rows, b, e;  // e = b: left out
