@@ -219,8 +219,8 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
   }
   // The CTAs that take prefix stages and those that take the requests' own: both at
   // once, as one is bound by the tensor cores and the other by memory (448 rows of 64
-  // heads behind 24576 tokens, 1050 tokens of their own: 303 us, one after the other
-  // 327).  An own stage counts three quarters of a prefix stage and an own list's
+  // heads behind 24576 tokens, 100 .. 2000 tokens of a request's own: 303 us, one after
+  // the other 327).  An own stage counts three quarters of a prefix stage and an own list's
   // start a whole one, so that both kinds end at the same time (243 and 242 us; four
   // requests 7.5 and 7.2, three groups of draft trees 24 and 27).
   const int W = s_stages * a.Hkv, Wp = s_pstages;

@@ -744,7 +744,9 @@ __device__ __forceinline__ void unit_share(const Args& a, const CUtensorMap& tmK
 // the row -- of the CTAs that shared its list and, in prefix calls, those that
 // shared its group's prefix -- in one online pass, kLoads of them in flight.  Where
 // there are at most 16 rows, `slices` lanes share a row, each with every so many-th
-// part, and join by shuffles.
+// part, and join by shuffles.  Bound by latency: 8 us for the lists of 48 chains, 20
+// for 28672 virtual rows with three parts each (with two parts in flight and 3 CTAs an
+// SM, or 4, a call of few rows takes 24 and 32 us where it takes 22).
 constexpr int kMergeThreads = 256;
 constexpr int kPrefixRows = 256;  // virtual rows of a prefix list
 template <int D, bool SPARSE>
@@ -858,6 +860,7 @@ inline sv_status check(const sv_paged_kv* kv, const sv_batch* bt, int32_t Hq) {
   if (kv->num_blocks < 0 || kv->max_blocks_per_req < 0) return SV_ERR_INVALID_ARGUMENT;
   // rows of the cache are counted in 32 bits by the copies
   if ((long)kv->num_blocks * kv->n_kv_heads >= (1L << 31) / kBlockSize) return SV_ERR_UNSUPPORTED_SHAPE;
+  if (bt->n_req > 0 && kv->num_blocks < 1) return SV_ERR_INVALID_ARGUMENT;
   if (bt->n_req > 0 && (!kv->k_cache || !kv->v_cache || !kv->block_tables || !kv->cache_lens))
     return SV_ERR_INVALID_ARGUMENT;
   if (((uintptr_t)kv->k_cache | (uintptr_t)kv->v_cache) & 15) return SV_ERR_INVALID_ARGUMENT;
@@ -899,7 +902,7 @@ inline Args common_args(const sv_paged_kv* kv, const sv_batch* bt, int32_t Hq, u
   a.tile_vr = a.rt * a.group;
   // ceil(rows / rt) tiles a request
   a.tiles_cap = (int)std::min((long)bt->total_rows / a.rt + bt->n_req, (long)INT32_MAX);
-  a.ctas = sizing_sms();
+  a.ctas = std::max(2, sizing_sms());  // (a prefix call has CTAs of two kinds)
   const size_t lists = (size_t)a.tiles_cap * a.Hkv, slots = lists + a.ctas;
   a.hdr = take<Header>(at, off, 1);
   a.tiles = take<Tile>(at, off, a.tiles_cap);

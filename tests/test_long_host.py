@@ -205,3 +205,12 @@ def test_plain_attention_is_a_softmax():
     out, mag = plain.attend_row(np.zeros((2, 8)), k, v, table, 0, [0, 17, 33], 0.5)
     assert np.allclose(out, np.mean([v[3, 0, 0], v[1, 0, 1], v[0, 0, 1]], 0)) and (mag >= np.abs(out)).all()
     assert plain.path([-1, 0, 0, 2, 3], 4) == [4, 3, 2, 0]
+
+
+def test_attention_needs_a_cache(lib):
+    shared = N.SvSharedPrefix(1, A, A)
+    none = kv(num_blocks=0)
+    assert lib.sv_page_attend_workspace(ref(batch()), ref(none), 8, 3) == 0
+    assert lib.sv_prefix_attend_workspace(ref(batch()), ref(none), ref(shared), 8) == 0
+    assert lib.sv_page_attend(ref(none), ref(batch()), A, 8, 0.1, A, 3, OUT, A, 1 << 40, None, None) == INV
+    assert lib.sv_prefix_attend(ref(none), ref(batch()), ref(shared), A, 8, 0.1, OUT, A, 1 << 40, None, None) == INV
