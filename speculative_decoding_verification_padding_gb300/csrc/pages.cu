@@ -149,21 +149,21 @@ struct ScoreArgs {
 
 constexpr int kScoreThreads = 128;
 constexpr int kScoreTiles = 8;  // tiles of 16 virtual rows of a CTA
-constexpr int kMaxPer = 256;
+constexpr int kMaxPer = 512;
 
-// MT tiles of 16 virtual rows (from row r0 on) by a warp's 16 pages from `page`
-// on: 2 MT chains of products side by side.  A thread has of each tile the slots
-// gq and gq + 8 by the pages 2 tq, 2 tq + 1 of two eights: v[eight * 4 + half * 2
-// + odd].  The maximum over a row's G2 slots is one over lanes: at each step a
+// MT tiles of 16 virtual rows (from row r0 on) by a warp's 8 E pages from `page`
+// on: E MT chains of products side by side.  A thread has of each tile the slots
+// gq and gq + 8 by the pages 2 tq, 2 tq + 1 of each eight, taken in pairs of eights:
+// v[eight * 4 + half * 2 + odd].  The maximum over a row's G2 slots is one over lanes: at each step a
 // lane keeps half of its values and hands the other half over, so that in the
 // end every value is in one lane only.
-template <int D, int G2, int MT>
-__device__ __forceinline__ void score_tiles(const uint4 (&bd)[2][2 * D / 32], const uint4* sq,
+template <int D, int G2, int MT, int E>
+__device__ __forceinline__ void score_tiles(const uint4 (&bd)[E][2 * D / 32], const uint4* sq,
                                             int r0, int nr, int page, int p1, int lane,
                                             unsigned known, float* out, size_t row_step) {
   constexpr int kPairs = 2 * D / 32;
   const int gq = lane >> 2, tq = lane & 3;
-  float acc[MT][2][4] = {};
+  float acc[MT][E][4] = {};
 #pragma unroll
   for (int c = 0; c < kPairs; ++c) {
 #pragma unroll
@@ -171,24 +171,25 @@ __device__ __forceinline__ void score_tiles(const uint4 (&bd)[2][2 * D / 32], co
       const uint4 x = sq[((k * kPairs + c) * 2) * 32], y = sq[((k * kPairs + c) * 2 + 1) * 32];
       const uint32_t ax[4] = {x.x, x.y, x.z, x.w}, ay[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt) mma16816(acc[k][nt], ax, bd[nt][c].x, bd[nt][c].y);
+      for (int nt = 0; nt < E; ++nt) mma16816(acc[k][nt], ax, bd[nt][c].x, bd[nt][c].y);
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt) mma16816(acc[k][nt], ay, bd[nt][c].z, bd[nt][c].w);
+      for (int nt = 0; nt < E; ++nt) mma16816(acc[k][nt], ay, bd[nt][c].z, bd[nt][c].w);
     }
   }
   const bool b0 = gq & 1, b1 = gq & 2, b2 = gq & 4;
   auto halve = [&](float lo, float hi, bool up, int o) {
     return fmaxf(up ? hi : lo, __shfl_xor_sync(0xffffffffu, up ? lo : hi, o));
   };
-  auto put = [&](int r, int at, float v) {
+  auto put_at = [&](int r, int at, float v) {
     if (r < nr && page + at < p1) out[r * row_step + page + at] = (known >> at) & 1u ? v : 0.f;
   };
 #pragma unroll
-  for (int k = 0; k < MT; ++k) {
-    const int row = r0 + k * (16 / G2);
+  for (int ke = 0; ke < MT * E / 2; ++ke) {
+    const int k = ke / (E / 2), pr = ke % (E / 2), row = r0 + k * (16 / G2);
+    auto put = [&](int r, int at, float v) { put_at(r, 16 * pr + at, v); };
     float v[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = acc[k][j >> 2][j & 3];
+    for (int j = 0; j < 8; ++j) v[j] = acc[k][2 * pr + (j >> 2)][j & 3];
     if (G2 == 16) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) v[j] = halve(fmaxf(v[j], v[j + 2]), fmaxf(v[4 + j], v[6 + j]), b0, 4);
@@ -225,13 +226,13 @@ __device__ __forceinline__ void score_tiles(const uint4 (&bd)[2][2 * D / 32], co
 // v % G2 of it, the group's heads in the first slots and some again in the rest
 // (the maximum over the slots does not see that).  The k order of a product is
 // free, so a lane takes 16 consecutive bytes of a page's bounds as the operands
-// of two steps: the bounds go from global memory to registers without a stop, 16
-// pages a warp at once (eight at once, with the next eight on their way, read q
-// from shared memory twice as often: 73 us where this takes 54, for 264 rows of 40
-// heads by 48 contexts of 2000 .. 60000 tokens: 4.1 TB/s; bound by the shared-memory
-// and L1 traffic of the operands).
-template <int D, int G2>
-__global__ void __launch_bounds__(kScoreThreads) score_kernel(ScoreArgs a) {
+// of two steps: the bounds go from global memory to registers without a stop, 8 E
+// pages a warp at once.  Bound by the shared-memory and L1 traffic of the operands:
+// q is read again for every 8 E pages (264 rows of 40 heads by 48 contexts of 2000 ..
+// 60000 tokens: E = 1 73 us, 2 54, 4 49, 4.5 TB/s; small calls take E = 2, whose
+// pages are spread over more warps).
+template <int D, int G2, int E>
+__global__ void __launch_bounds__(kScoreThreads, E == 4 ? 3 : 4) score_kernel(ScoreArgs a) {
   griddep_entry();
   constexpr int kPairs = 2 * D / 32;  // 16-byte chunks a lane holds of a page, two steps each
   constexpr int kTileRows = 16 / G2;
@@ -293,10 +294,11 @@ __global__ void __launch_bounds__(kScoreThreads) score_kernel(ScoreArgs a) {
   __syncthreads();
   float* out = a.scores + ((size_t)(w.cu + r0) * a.Hkv + g) * a.max_pages;
   const size_t row_step = (size_t)a.Hkv * a.max_pages;
-  for (int p = p0 + warp * 16; p < p1; p += (kScoreThreads / 32) * 16) {
-    uint4 bd[2][kPairs];  // pages p + gq and p + gq + 8
+  constexpr int kPages = 8 * E;  // of a warp at once
+  for (int p = p0 + warp * kPages; p < p1; p += (kScoreThreads / 32) * kPages) {
+    uint4 bd[E][kPairs];  // pages p + gq, p + gq + 8, ...
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
+    for (int k = 0; k < E; ++k) {
       const int b = s_tbl[min(p + k * 8 + gq, p1 - 1) - p0];
       const uint4* src = reinterpret_cast<const uint4*>(
           a.bounds + ((size_t)max(b, 0) * a.Hkv + g) * 2 * D) + tq;
@@ -304,26 +306,30 @@ __global__ void __launch_bounds__(kScoreThreads) score_kernel(ScoreArgs a) {
       for (int c = 0; c < kPairs; ++c) bd[k][c] = __ldg(src + c * 4);
     }
     // pages whose block is in the cache
-    const unsigned known = __ballot_sync(0xffffffffu, s_tbl[min(p + (lane & 15), p1 - 1) - p0] >= 0);
+    const unsigned known = __ballot_sync(0xffffffffu, s_tbl[min(p + lane % kPages, p1 - 1) - p0] >= 0);
+    constexpr int MT = E == 4 ? 1 : 2;
     int mt = 0;
-    for (; mt + 2 <= tiles; mt += 2)
-      score_tiles<D, G2, 2>(bd, s_q + mt * kPairs * 64 + lane, mt * kTileRows, nr, p, p1, lane, known,
-                            out, row_step);
+    for (; mt + MT <= tiles; mt += MT)
+      score_tiles<D, G2, MT, E>(bd, s_q + mt * kPairs * 64 + lane, mt * kTileRows, nr, p, p1, lane, known,
+                                out, row_step);
     if (mt < tiles)
-      score_tiles<D, G2, 1>(bd, s_q + mt * kPairs * 64 + lane, mt * kTileRows, nr, p, p1, lane, known,
-                            out, row_step);
+      score_tiles<D, G2, 1, E>(bd, s_q + mt * kPairs * 64 + lane, mt * kTileRows, nr, p, p1, lane, known,
+                               out, row_step);
   }
 }
 
+template <int D, int G2, int E>
+cudaError_t launch_score(const ScoreArgs& a, dim3 grid, size_t smem, cudaStream_t s) {
+  static PerDevice set;
+  const size_t most = (size_t)kScoreTiles * (2 * D / 16) * 32 * 16;
+  const cudaError_t e = smem_limit_once(set, score_kernel<D, G2, E>, most);
+  return e == cudaSuccess ? sv::launch(score_kernel<D, G2, E>, grid, kScoreThreads, smem, s, a) : e;
+}
 template <int G2>
 cudaError_t launch_score(const ScoreArgs& a, int dim, dim3 grid, size_t smem, cudaStream_t s) {
-  static PerDevice set128, set64;
-  const size_t most = (size_t)kScoreTiles * 16 * 32 * 16;  // of head_dim 128
-  cudaError_t e = dim == 128 ? smem_limit_once(set128, score_kernel<128, G2>, most)
-                             : smem_limit_once(set64, score_kernel<64, G2>, most);
-  if (e != cudaSuccess) return e;
-  return dim == 128 ? sv::launch(score_kernel<128, G2>, grid, kScoreThreads, smem, s, a)
-                    : sv::launch(score_kernel<64, G2>, grid, kScoreThreads, smem, s, a);
+  if (a.per >= 256)
+    return dim == 128 ? launch_score<128, G2, 4>(a, grid, smem, s) : launch_score<64, G2, 4>(a, grid, smem, s);
+  return dim == 128 ? launch_score<128, G2, 2>(a, grid, smem, s) : launch_score<64, G2, 2>(a, grid, smem, s);
 }
 
 // ---------------------------------------------------------------- select --
@@ -701,7 +707,10 @@ extern "C" sv_status sv_score_pages(const sv_paged_kv* kv, const sv_batch* bt, c
   const int nsm = num_sms();
   if (nsm < 1) return SV_ERR_CUDA;
   const long units = (long)bt->n_req * kv->n_kv_heads * max_pages;
-  a.per = units <= 64L * 8 * nsm ? 64 : pg::kMaxPer;
+  // enough CTAs for the SMs first, then as many pages as pay for a CTA's start (512: 49
+  // us in the case above, 256 51, 128 60, 1024 56)
+  a.per = 64;
+  while (a.per < pg::kMaxPer && units > 8L * nsm * a.per) a.per *= 2;
   const int per_block = pg::kScoreTiles * 16 / a.g2;
   const int most_rows = std::min(bt->max_rows_per_req, bt->total_rows);
   const dim3 grid((max_pages + a.per - 1) / a.per, (most_rows + per_block - 1) / per_block,
