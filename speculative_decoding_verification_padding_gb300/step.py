@@ -41,7 +41,9 @@ from .workloads import Workload
 @dataclasses.dataclass(frozen=True)
 class PageChoice:
     """How many pages of a long context a row attends: n_keep for each KV head, the
-    first n_first and the last n_last always, the others by score."""
+    first n_first and the last n_last always, the others by score.  A step bounds the
+    pages that its commit fills; whoever fills the cache between steps (an admitted
+    prompt) calls api.sv_bound_pages with the step's ``bounds``."""
     n_keep: int
     n_first: int = 1
     n_last: int = 4

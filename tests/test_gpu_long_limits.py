@@ -7,7 +7,7 @@ import torch
 
 from oracle import pages as plain
 from speculative_decoding_verification_padding_gb300 import api, build
-from test_gpu_pages import Setup, attended, check_attend, f64, listed
+from test_gpu_pages import Setup, attended, check_attend, check_scores, f64, listed
 from test_gpu_prefix import Shared
 
 pytestmark = pytest.mark.gpu
@@ -93,6 +93,17 @@ def test_scores_of_65528_lists():
     x = torch.maximum(q.double() * bnd[:, :, 0].double(), q.double() * bnd[:, :, 1].double())
     # 2 D exact products added one by one in fp32
     assert ((out[:, :, 0].double() - x.sum(2)).abs() <= 128 * 2.0 ** -23 * x.abs().sum(2)).all()
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("group", [1, 2, 3, 4, 5, 7, 8, 11, 16])
+@pytest.mark.parametrize("room", [30000, 60000])  # pages a CTA: 256, 512
+def test_scores_of_large_calls(group, dim, room):
+    ctx, rows = [9000, 40, 4200, 500], [2, 3, 1, 19]
+    s = Setup(ctx, rows, 2 * group, 2, dim, seed=group)
+    b = torch.empty(s.blocks, 2, 2, dim, dtype=torch.bfloat16, device="cuda").fill_(float("nan"))
+    api.sv_bound_pages(s.kv, b)
+    check_scores(s, b, torch.full((25, 2, room), 7.0, device="cuda"), ctx, dim)
 
 
 def test_offsets_past_32_bits():
