@@ -668,6 +668,8 @@ sv_status sv_page_attend(const sv_paged_kv* kv, const sv_batch* batch, const voi
  * document): the shared pages are read once for all rows of a group, on
  * tcgen05 tensor cores, each request's own pages as sv_tree_attend reads them,
  * and the two parts joined in fp32.  Same keys, same result up to rounding.
+ * (Where sizes say that it costs more -- short prefixes, requests whose rows
+ * fill tiles by themselves -- a request reads the prefix with its own pages.)
  * Group k = requests cu_groups[k] .. cu_groups[k + 1] - 1 (int32 [n_groups +
  * 1], from 0 to n_req), which share their first prefix_len[k] slots (int32
  * [n_groups]; a multiple of 16, 0: nothing).  The blocks of the prefix are read

@@ -32,10 +32,32 @@ struct PlanSmem {
   int cu_groups[kPlanGroups + 1], prefix_len[kPlanGroups], gstage[kPlanGroups + 1];
 };
 
+// The time that `rows` virtual rows of a group take on one SM for a prefix of
+// `stages` stages, in quarters of an own stage (one tile by 128 tokens, however few
+// rows the tile has): a stage of a prefix list takes 5 with two tiles and 3 with one,
+// of head_dim 64 (half the copies and products, the same softmax) 4 and 2.5.
+__device__ __forceinline__ long prefix_cost(const Args& a, long rows, int stages) {
+  const long tiles = (rows + 127) / 128;
+  return (a.dim == 128 ? 5 * tiles + 1 : 3 * tiles + 2) * (stages + kListStart) / 2;
+}
+
+// Whether a request's rows go with its group's prefix lists (n requests about like it
+// in the group), or its own lists read the prefix's pages too.  A row in two parts
+// writes and reads both.  Where all own stages are few the SMs are there for them.
+// (27 trees of 83 rows, 16 heads a KV head, behind 16 .. 832 tokens: 98 us, 174 with
+// prefix lists; 62 chains of 2 rows behind 16 tokens 24 and 33; 64 chains behind 24576
+// tokens are 3.4 times the work without the lists.)
+__device__ __forceinline__ bool shared_pays(const Args& a, int n, int vrows, int tiles, int stages) {
+  if ((long)a.bt.n_req * tiles * a.Hkv * stages <= 6L * a.ctas) return false;
+  const long rows = (long)n * vrows;
+  return 4L * stages * tiles * n > prefix_cost(a, rows, stages) + rows * (5 * a.dim / 64) / 64;
+}
+
 __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_constant__ Args a) {
   griddep_entry();
   extern __shared__ __align__(16) uint8_t s_mem[];
   __shared__ int s_tiles, s_stages, s_rows, s_pstages, s_groups_bad;
+  __shared__ long s_pcost;
   PlanSmem& sm = *reinterpret_cast<PlanSmem*>(s_mem);
   const int R = a.bt.n_req, G = a.n_groups, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const bool small = R <= kPlanRequests && G <= kPlanGroups;  // in shared memory
@@ -127,13 +149,16 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
       flag(a.dev_status, p < 0 || p % kBlockSize != 0 ? SV_DEV_BAD_PARAM : SV_DEV_BAD_LENGTH);
       r.e = r.b;
     }
+    const int nt = (r.e - r.b + a.rt - 1) / a.rt, pages = r.e > r.b ? p / kBlockSize : 0;
+    const bool share = pages > 0 && shared_pays(a, cu_groups[lo + 1] - cu_groups[lo], (r.e - r.b) * a.group, nt,
+                                                (pages + kStagePages - 1) / kStagePages);
     r.grp = lo;
-    r.first = p / kBlockSize;
-    const int nt = (r.e - r.b + a.rt - 1) / a.rt;
+    r.first = share ? pages : 0;
+    r.pre = pages - r.first;
     r.tile = nt;  // counts, for now
     r.stage = 0;
     for (int k = 0; k < nt; ++k) r.stage += stages_of(r, k);
-    r.arow = r.e - r.b;
+    r.arow = share ? r.e - r.b : 0;
     req[i] = r;
   }
   __syncthreads();
@@ -168,10 +193,11 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
     }
     __syncwarp();
     const int rows = c[2];
-    // groups: first active row, active rows, pages; their lists, one a 256-row tile
+    // groups: first row, rows, pages; their lists, one a 256-row tile
     // and KV head, and the lists' stages
     auto arow = [&](int i) { return i < R ? req[i].arow : rows; };
     int lists = 0, stages = 0;
+    long cost = 0;
     for (int base = 0; base < G; base += 32) {
       const int k = base + lane;
       int4 gr = make_int4(0, 0, 0, 0);
@@ -182,6 +208,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
         gr.z = gr.y > 0 ? prefix_len[k] / kBlockSize : 0;  // checked by its requests
         n = gr.z > 0 ? (gr.y * a.group + kPrefixRows - 1) / kPrefixRows * a.Hkv : 0;
         s = n * ((gr.z + kStagePages - 1) / kStagePages + kListStart);
+        if (n > 0) cost += a.Hkv * prefix_cost(a, (long)gr.y * a.group, (gr.z + kStagePages - 1) / kStagePages);
       }
       int x = n, y = s;
 #pragma unroll
@@ -201,7 +228,10 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
       lists += __shfl_sync(0xffffffffu, x, 31);
       stages += __shfl_sync(0xffffffffu, y, 31);
     }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) cost += __shfl_xor_sync(0xffffffffu, cost, o);
     if (lane == 0) {
+      s_pcost = cost;
       s_tiles = c[0];
       s_stages = c[1];
       s_rows = rows;
@@ -220,14 +250,13 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
   // The CTAs that take prefix stages and those that take the requests' own: both at
   // once, as one is bound by the tensor cores and the other by memory (448 rows of 64
   // heads behind 24576 tokens, 100 .. 2000 tokens of a request's own: 303 us, one after
-  // the other 327).  An own stage counts three quarters of a prefix stage and an own list's
-  // start a whole one, so that both kinds end at the same time (243 and 242 us; four
-  // requests 7.5 and 7.2, three groups of draft trees 24 and 27).
+  // the other 327).  Divided by what both take, an own list's start 5, so that both
+  // kinds end at the same time.
   const int W = s_stages * a.Hkv, Wp = s_pstages;
   int Cp = min(a.ctas, Wp), C = min(a.ctas, W);
   if (Wp > 0 && W > 0) {
-    const long wp = 4L * Wp, all = wp + 3L * W + 4L * s_tiles * a.Hkv;
-    Cp = min(Wp, max(1, min(a.ctas - 1, (int)((a.ctas * wp + all / 2) / all))));
+    const long all = s_pcost + 4L * W + 5L * s_tiles * a.Hkv;
+    Cp = min(Wp, max(1, min(a.ctas - 1, (int)((a.ctas * s_pcost + all / 2) / all))));
     C = min(W, max(1, a.ctas - Cp));
   }
   if (tid == 0) {
@@ -266,7 +295,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
     ps.leader = cu_groups[ps.k];
     a.pend[c] = ps;
   }
-  // active rows
+  // rows of the prefix lists
   for (int y = from(320); y < s_rows; y += kPlanThreads) {
     const Req r = req[last_at(R, y, [&](int i) { return req[i].arow; })];
     a.arows[y] = r.cu + r.b + y - r.arow;
@@ -293,6 +322,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
     t.nent = (r.ctx + t.r0 + t.nr + kBlockSize - 1) / kBlockSize - r.first;
     t.arow = r.arow + k * a.rt;
     t.grp = r.grp;
+    t.pre = r.pre;
     a.tiles[tile] = t;
   }
 }

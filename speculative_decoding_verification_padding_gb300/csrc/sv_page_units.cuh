@@ -36,8 +36,9 @@ struct __align__(16) Tile {
   int i, cu, ctx, r0;      // request, its first packed row, context, first local row
   int nr, rows, first, ncomp;  // rows of the tile and of the request; first table
                                // entry and complete pages of its list (prefix calls)
-  int nent, arow, grp, pad;    // entries of the list; the tile's first row among all
-                               // active rows, its group (prefix calls)
+  int nent, arow, grp, pre;    // entries of the list; the tile's first row among those
+                               // of the prefix lists, its group, and the entries that
+                               // are read from its group's first request (prefix calls)
 };
 
 struct Header {
@@ -65,7 +66,7 @@ struct Args {
   const int32_t* lens;
   const __nv_bfloat16* q;
   __nv_bfloat16* out;
-  int Hq, group;
+  int Hq, group, dim;
   int rt;             // rows of a tile
   int tile_vr;        // virtual rows of a part: rt * group, at most what a request has
   int tiles_cap, ctas;
@@ -88,9 +89,9 @@ struct Args {
   int n_groups;
   const int32_t* cu_groups;
   const int32_t* prefix_len;
-  int* arows;         // [total_rows] packed rows of the active rows
+  int* arows;         // [total_rows] packed rows of the prefix lists' rows
   Req* req;           // [n_req]
-  int4* groups;       // [n_groups] first active row, active rows, pages, first prefix list
+  int4* groups;       // [n_groups] first of these rows, rows, pages, first prefix list
   int* gstage;        // [n_groups + 1] first stage of each group's prefix lists, starts included
   PEnd* pend;         // [ctas]
   int plists;         // prefix lists at most: 256-row tiles x KV heads
@@ -108,7 +109,9 @@ __device__ __forceinline__ int share_of(int s, int W, int C) { return (int)((((l
 struct Req {
   int cu, rows, b, e;  // e = b: left out
   int ctx, first, grp, tile;  // prefix pages, group, first tile
-  int stage, arow;     // first stage of the request's lists of one KV head, first active row
+  int stage, arow;     // first stage of the request's lists of one KV head, its first row
+                       // among those of the prefix lists
+  int pre, pad;        // pages of the prefix that its own lists read
 };
 
 // Exclusive scan over the block's threads of v, on top of *carry (shared),
@@ -189,8 +192,9 @@ struct Smem {
 struct Rec {
   int x, g, n_stage, e_first;   // n_stage 0: the end
   int i, row0, nr, ctx;         // request; first packed row of the tile, its rows
-  int first, ncomp, nent, lim;  // staged rows up to which slots are written
-  int whole, bad, r0, grp;      // all of the list; some block outside the cache
+  int first, ncomp, nent, r0;   // table entry and entries of the list; first local row
+  int whole, bad, pre, lead;    // all of the list; some block outside the cache; entries
+                                // read from another request
 };
 struct Shared {
   Rec rec[kLists];
@@ -255,7 +259,7 @@ __device__ __forceinline__ void unit_share(const Args& a, const CUtensorMap& tmK
   auto block_of = [&](const Rec& r, int e) {
     if (e >= r.nent) return -1;
     const int b = SPARSE ? __ldg(a.blk + (size_t)r.x * a.cap + e)
-                         : __ldg(a.tables + (size_t)r.i * a.max_blocks + r.first + e);
+                         : __ldg(a.tables + (size_t)(e < r.pre ? r.lead : r.i) * a.max_blocks + r.first + e);
     return b >= 0 && b < a.num_blocks ? b : -1;
   };
 
@@ -283,9 +287,9 @@ __device__ __forceinline__ void unit_share(const Args& a, const CUtensorMap& tmK
         r.nr = tl.nr;
         r.ctx = tl.ctx;
         r.first = tl.first;
-        r.lim = tl.r0 + tl.nr;
         r.r0 = tl.r0;
-        r.grp = tl.grp;
+        r.pre = SPARSE ? 0 : tl.pre;
+        r.lead = r.pre > 0 ? a.cu_groups[tl.grp] : 0;
         s_at += r.n_stage;
         const int e_end = min(r.nent, r.e_first + r.n_stage * kStagePages);
         const bool tail = e_end > r.ncomp;  // the tail is among it
@@ -668,7 +672,7 @@ __device__ __forceinline__ void unit_share(const Args& a, const CUtensorMap& tmK
             }
           };
           // behind the last staged slot, and (where a block is missing) whole pages
-          zero(min(kTok, max(0, (r.ncomp - e0) * kBlockSize + r.lim - tail0)), kTok);
+          zero(min(kTok, max(0, (r.ncomp - e0) * kBlockSize + r.r0 + r.nr - tail0)), kTok);
 #pragma unroll 1
           for (int p = 0; p < (r.bad ? kStagePages : 0); ++p)
             if (!((there >> p) & 1u)) zero(16 * p, 16 * p + 16);
@@ -686,7 +690,7 @@ __device__ __forceinline__ void unit_share(const Args& a, const CUtensorMap& tmK
       }
       tc5::fence_after_sync();
       if (some) {
-        const bool out = r.whole && (SPARSE || a.groups[r.grp].z == 0);
+        const bool out = r.whole && (SPARSE || r.first == 0);
         const size_t row = (size_t)(r.row0 + lr) * a.Hq + head, part = (size_t)(c + r.x);
         const float inv = l > 0.f ? 1.f / l : 0.f;
 #pragma unroll 1
@@ -770,8 +774,8 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_const
   const int c0 = share_of(off0, W, C), ns = share_of(off1 - 1, W, C) - c0 + 1;
   int np = 0, p0 = 0, pv = 0;
   if (!SPARSE) {
-    const int4 grp = a.groups[tl.grp];
-    if (grp.z > 0) {
+    if (tl.first > 0) {
+      const int4 grp = a.groups[tl.grp];
       const int v = (tl.arow - grp.x) * group + vs;  // among the group's virtual rows
       const int list = v / kPrefixRows * a.Hkv + g, sp = (grp.z + kStagePages - 1) / kStagePages;
       const int s0 = a.gstage[tl.grp] + list * (sp + kListStart) + kListStart;
@@ -897,6 +901,7 @@ inline Args common_args(const sv_paged_kv* kv, const sv_batch* bt, int32_t Hq, u
   a.lens = kv->cache_lens;
   a.Hq = Hq;
   a.group = Hq / kv->n_kv_heads;
+  a.dim = kv->head_dim;
   const int most = std::max(1, std::min(bt->max_rows_per_req, bt->total_rows));
   a.rt = std::min(kTileRows / a.group, most);
   a.tile_vr = a.rt * a.group;
