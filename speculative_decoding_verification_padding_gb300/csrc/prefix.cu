@@ -7,9 +7,9 @@
 //
 // softmax over (prefix, own keys) = the two parts' (max, sum, weighted values)
 // joined.  Launches:
-//   plan    (1 CTA) checks groups and requests, lists the active rows of every
-//           group, cuts them into prefix lists and the requests' rows into tiles,
-//           divides the CTAs between the two and deals out both;
+//   plan    (1 CTA) checks groups and requests, decides which requests share, lists
+//           their rows by group, cuts them into prefix lists and all requests' rows
+//           into tiles, divides the CTAs between the two and deals out both;
 //   prefix  (tcgen05, one CTA an SM) some CTAs the prefix lists -- 256 virtual rows
 //           (rows of all requests of the group x GQA group) by the prefix's pages:
 //           (max, sum, O) -- and the others the tiles' own pages (unit_share);
