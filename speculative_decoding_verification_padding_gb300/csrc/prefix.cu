@@ -44,9 +44,11 @@ __device__ __forceinline__ long prefix_cost(const Args& a, long rows, int stages
 // Whether a request's rows go with its group's prefix lists (n requests about like it
 // in the group), or its own lists read the prefix's pages too.  A row in two parts
 // writes and reads both.  Where all own stages are few the SMs are there for them.
-// (27 trees of 83 rows, 16 heads a KV head, behind 16 .. 832 tokens: 98 us, 174 with
-// prefix lists; 62 chains of 2 rows behind 16 tokens 24 and 33; 64 chains behind 24576
-// tokens are 3.4 times the work without the lists.)
+// (27 trees of 83 rows, 16 heads a KV head, behind 16 .. 832 tokens: 98 us with own
+// lists only, 174 with prefix lists; 62 chains of 2 rows behind 16 tokens 24 and 33; 64
+// chains of 7 rows behind 24576 tokens 748 and 293; 30 trees of 41 rows, 7 heads a KV
+// head, behind 809, 2024 and 5060 tokens 43.8 and 42.8, by the rule 41.8; 4 chains behind
+// 2048 tokens 21.8 and 21.9.)
 __device__ __forceinline__ bool shared_pays(const Args& a, int n, int vrows, int tiles, int stages) {
   if ((long)a.bt.n_req * tiles * a.Hkv * stages <= 6L * a.ctas) return false;
   const long rows = (long)n * vrows;
