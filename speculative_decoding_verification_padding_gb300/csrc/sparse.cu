@@ -29,14 +29,15 @@ constexpr int kHeld = 6;
 __global__ void __launch_bounds__(kBuildThreads) build_kernel(const __grid_constant__ Args a) {
   griddep_entry();
   extern __shared__ uint32_t s_bits[];  // one bit a page, then the bits before each word
-  __shared__ int s_warp[32], s_carry, s_req, s_k, s_ctx;
+  // (the two scans have a total each: one may still be read when the other begins)
+  __shared__ int s_warp[32], s_ntiles, s_npages, s_req, s_k, s_ctx;
   __shared__ Window s_win;
   __shared__ int s_len[kTileRows];
   const int x = blockIdx.x, tile = x / a.Hkv, g = x % a.Hkv, R = a.bt.n_req;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   // the request that holds the tile, and how many tiles there are
   if (tid == 0) {
-    s_carry = 0;
+    s_ntiles = s_npages = 0;
     if (x == 0 && (a.bt.cu_rows[0] != 0 || a.bt.cu_rows[R] != a.bt.total_rows))
       flag(a.dev_status, SV_DEV_BAD_WINDOW);
   }
@@ -50,7 +51,7 @@ __global__ void __launch_bounds__(kBuildThreads) build_kernel(const __grid_const
       if (w.ok) nt = (max(w.b, w.e) - w.b + a.rt - 1) / a.rt;
       else if (x == 0) flag(a.dev_status, SV_DEV_BAD_WINDOW);
     }
-    const int at = block_scan(nt, s_warp, &s_carry);
+    const int at = block_scan(nt, s_warp, &s_ntiles);
     if (at <= tile && tile < at + nt) {
       s_req = i;
       s_k = tile - at;
@@ -60,9 +61,9 @@ __global__ void __launch_bounds__(kBuildThreads) build_kernel(const __grid_const
   }
   __syncthreads();
   // (offsets that overlap could ask for more tiles than there are; such a call is left out)
-  const int T = s_carry <= a.tiles_cap ? s_carry : 0;
+  const int T = s_ntiles <= a.tiles_cap ? s_ntiles : 0;
   if (x == 0 && tid == 0) {
-    if (s_carry > a.tiles_cap) flag(a.dev_status, SV_DEV_BAD_WINDOW);
+    if (s_ntiles > a.tiles_cap) flag(a.dev_status, SV_DEV_BAD_WINDOW);
     a.hdr->T = T;
   }
   if (tile >= T) return;
@@ -105,7 +106,6 @@ __global__ void __launch_bounds__(kBuildThreads) build_kernel(const __grid_const
   uint32_t* see = a.see + (size_t)x * a.rt * (a.cap / 32);
   for (int y = tid; y < nr * (a.cap / 32); y += kBuildThreads) see[y] = 0u;
   if (tid < nr) s_len[tid] = a.n_keep;
-  if (tid == 0) s_carry = 0;
   if (__syncthreads_or(bad) || !fits) {
     // an empty list
     if (tid == 0) {
@@ -152,11 +152,11 @@ __global__ void __launch_bounds__(kBuildThreads) build_kernel(const __grid_const
   __syncthreads();
   for (int base = 0; base < words; base += kBuildThreads) {
     const int y = base + tid;
-    const int before = block_scan(y < words ? __popc(s_bits[y]) : 0, s_warp, &s_carry);
+    const int before = block_scan(y < words ? __popc(s_bits[y]) : 0, s_warp, &s_npages);
     if (y < words) s_before[y] = (uint32_t)before;
   }
   __syncthreads();
-  const int U = s_carry;
+  const int U = s_npages;
   int* blk = a.blk + (size_t)x * a.cap;
   entries([&](const Entry& e) {
     if (e.k >= s_len[e.r]) return;
