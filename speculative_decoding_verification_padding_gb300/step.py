@@ -42,8 +42,9 @@ from .workloads import Workload
 class PageChoice:
     """How many pages of a long context a row attends: n_keep for each KV head, the
     first n_first and the last n_last always, the others by score.  A step bounds the
-    pages that its commit fills; whoever fills the cache between steps (an admitted
-    prompt) calls api.sv_bound_pages with the step's ``bounds``."""
+    pages that its commit fills (run, accept_commit, commit); whoever fills the cache
+    between steps (an admitted prompt) calls api.sv_bound_pages with the step's
+    ``bounds``."""
     n_keep: int
     n_first: int = 1
     n_last: int = 4
@@ -121,7 +122,7 @@ class DeviceStep:
             self.bounds = torch.zeros((nb, hkv, 2, d), dtype=torch.bfloat16, device=dev)
             self.scores = torch.zeros((rows, hkv, pages), dtype=torch.float32, device=dev)
             self.pages = torch.full((rows, hkv, choice.n_keep), -1, dtype=torch.int32, device=dev)
-            self.bounded = torch.zeros_like(self.kv.cache_lens)  # lengths whose pages have bounds
+            self.bounded = self.kv.cache_lens.clone()  # lengths before the last commit
             api.sv_bound_pages(self.kv, self.bounds, None, self.dev_status)
             ws = max(ws, api.sv_page_attend_workspace(self.batch, self.kv, self.Hq, choice.n_keep))
         if shared is not None:
@@ -164,9 +165,18 @@ class DeviceStep:
             self.kv, b, self.scores, self.pages, c.n_first, c.n_last, self.dev_status))()
 
     def bound_pages(self):
-        """Bounds of the pages that were filled since ``bounded`` was set."""
+        """Bounds of the pages behind the lengths ``bounded``."""
         self._bound("bound pages", self.batch, lambda: api.bind_bound_pages(
             self.kv, self.bounds, self.bounded, self.dev_status))()
+
+    def _committed(self, call):
+        """A call that commits; with a page choice the pages that it fills get their
+        bounds behind it."""
+        if self.choice is not None:
+            self.bounded.copy_(self.kv.cache_lens)
+        call()
+        if self.choice is not None:
+            self.bound_pages()
 
     def accept(self, batch=None, row_stats=None):
         b = batch or self.batch
@@ -183,15 +193,15 @@ class DeviceStep:
     def accept_commit(self, batch=None, row_stats=None):
         b = batch or self.batch
         if row_stats is not None:
-            api.sv_accept_commit(b, self.target, self.draft, self.V, self.T, self.w.seed,
-                                 self.accepted_len, self.accepted_nodes, self.next_token,
-                                 self.ambiguous, self.done, row_stats, self.kv, self.pool,
-                                 self.ws, self.dev_status)
+            self._committed(lambda: api.sv_accept_commit(
+                b, self.target, self.draft, self.V, self.T, self.w.seed, self.accepted_len,
+                self.accepted_nodes, self.next_token, self.ambiguous, self.done, row_stats,
+                self.kv, self.pool, self.ws, self.dev_status))
             return
-        self._bound("accept_commit", b, lambda: api.bind_accept_commit(
+        self._committed(self._bound("accept_commit", b, lambda: api.bind_accept_commit(
             b, self.target, self.draft, self.V, self.T, self.w.seed, self.accepted_len,
             self.accepted_nodes, self.next_token, self.ambiguous, self.done, None, self.kv,
-            self.pool, self.ws, self.dev_status))()
+            self.pool, self.ws, self.dev_status)))
 
     def chunked(self):
         api.sv_verify_chunked(self.kv, self.batch, self.q, self.Hq, self.scale, self.out,
@@ -211,15 +221,14 @@ class DeviceStep:
             self.dev_status))()
 
     def commit(self, batch=None):
-        api.sv_commit_kv(self.kv, batch or self.batch, self.accepted_len, self.accepted_nodes,
-                         self.pool, self.dev_status)
+        self._committed(lambda: api.sv_commit_kv(
+            self.kv, batch or self.batch, self.accepted_len, self.accepted_nodes, self.pool,
+            self.dev_status))
 
     def run(self, commit: bool = True, restore: bool = True):
         """Enqueue one whole step of this workload's mode on the current stream."""
         if restore:
             self.restore_cache_state()
-        if self.choice is not None:
-            self.bounded.copy_(self.kv.cache_lens)
         if self.mode == "onepass":
             self.attend()
             if commit:
@@ -240,8 +249,6 @@ class DeviceStep:
                 self.accept(self.batch_sel)
         else:
             raise ValueError(self.mode)
-        if self.choice is not None and commit:
-            self.bound_pages()
 
     def inputs(self):
         """The device tensors a step reads that a caller feeds from the host each
@@ -354,8 +361,9 @@ class EdgeStep(DeviceStep):
         # sv_commit_kv takes no windows: a request that was kept out has no path
         # (reported as SV_DEV_BAD_WINDOW, and left as it was)
         path_len = self.accepted_len.masked_fill(self.row_end == 0, -1)
-        api.sv_commit_kv(self.kv, batch or self.batch, path_len, self.accepted_nodes, self.pool,
-                         self.dev_status)
+        self._committed(lambda: api.sv_commit_kv(
+            self.kv, batch or self.batch, path_len, self.accepted_nodes, self.pool,
+            self.dev_status))
 
     def stage(self):
         self._bound("stage", self.batch, lambda: api.bind_stage_qkv(
@@ -372,16 +380,12 @@ class EdgeStep(DeviceStep):
     def run(self, commit: bool = True, restore: bool = True):
         if restore:
             self.restore_cache_state()
-        if self.choice is not None:
-            self.bounded.copy_(self.kv.cache_lens)
         self.reserve()
         self.stage()
         self.attend()
         self.shape()
         if commit:
             self.accept_commit()
-            if self.choice is not None:
-                self.bound_pages()
         else:
             self.accept()
 
