@@ -618,8 +618,11 @@ sv_status sv_bound_pages(const sv_paged_kv* kv, int32_t n_req, const int32_t* fr
 /* For row r of request i inside its window, KV head g and t < n_i:
  *   scores[r][g][t] = max over query heads h of g of
  *                     sum_d max(q[r][h][d] lo_d, q[r][h][d] hi_d)
- * with (lo, hi) the page's bounds: at least the product of any of those queries
- * with any key of the page.  fp32 sums of exact products.
+ * with (lo, hi) the page's bounds: up to the rounding of the sum (2^-23 of the
+ * terms' magnitudes an addition), at least the product of any of those queries
+ * with any key of the page.  fp32 sums of exact products; a term is 0 where q is,
+ * and a head whose sum is no number (infinities of both signs, a dimension whose
+ * keys are all NaN) counts for nothing: NaN if no head has one.
  * scores: fp32 [total_rows][n_kv_heads][max_pages]; other entries are left as
  * they were.  q: bf16 [total_rows][n_q_heads][head_dim], 16-byte aligned.
  * Requests whose pages are more than max_pages, or whose length does not fit

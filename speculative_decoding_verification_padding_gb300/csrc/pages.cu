@@ -151,16 +151,23 @@ constexpr int kScoreThreads = 128;
 constexpr int kScoreTiles = 8;  // tiles of 16 virtual rows of a CTA
 constexpr int kMaxPer = 512;
 
+// The greater of two, NaN where one is.
+__device__ __forceinline__ float max_nan(float x, float y) {
+  float z;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(z) : "f"(x), "f"(y));
+  return z;
+}
+
 // MT tiles of 16 virtual rows (from row r0 on) by a warp's 8 E pages from `page`
 // on: E MT chains of products side by side.  A thread has of each tile the slots
 // gq and gq + 8 by the pages 2 tq, 2 tq + 1 of each eight, taken in pairs of eights:
 // v[eight * 4 + half * 2 + odd].  The maximum over a row's G2 slots is one over lanes: at each step a
 // lane keeps half of its values and hands the other half over, so that in the
-// end every value is in one lane only.
+// end every value is in one lane only.  `worst` becomes NaN where a sum is.
 template <int D, int G2, int MT, int E>
 __device__ __forceinline__ void score_tiles(const uint4 (&bd)[E][2 * D / 32], const uint4* sq,
                                             int r0, int nr, int page, int p1, int lane,
-                                            unsigned known, float* out, size_t row_step) {
+                                            unsigned known, float* out, size_t row_step, float& worst) {
   constexpr int kPairs = 2 * D / 32;
   const int gq = lane >> 2, tq = lane & 3;
   float acc[MT][E][4] = {};
@@ -178,9 +185,10 @@ __device__ __forceinline__ void score_tiles(const uint4 (&bd)[E][2 * D / 32], co
   }
   const bool b0 = gq & 1, b1 = gq & 2, b2 = gq & 4;
   auto halve = [&](float lo, float hi, bool up, int o) {
-    return fmaxf(up ? hi : lo, __shfl_xor_sync(0xffffffffu, up ? lo : hi, o));
+    return max_nan(up ? hi : lo, __shfl_xor_sync(0xffffffffu, up ? lo : hi, o));
   };
   auto put_at = [&](int r, int at, float v) {
+    worst = max_nan(worst, v);
     if (r < nr && page + at < p1) out[r * row_step + page + at] = (known >> at) & 1u ? v : 0.f;
   };
 #pragma unroll
@@ -192,9 +200,9 @@ __device__ __forceinline__ void score_tiles(const uint4 (&bd)[E][2 * D / 32], co
     for (int j = 0; j < 8; ++j) v[j] = acc[k][2 * pr + (j >> 2)][j & 3];
     if (G2 == 16) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j) v[j] = halve(fmaxf(v[j], v[j + 2]), fmaxf(v[4 + j], v[6 + j]), b0, 4);
+      for (int j = 0; j < 2; ++j) v[j] = halve(max_nan(v[j], v[j + 2]), max_nan(v[4 + j], v[6 + j]), b0, 4);
       v[0] = halve(v[0], v[1], b1, 8);
-      v[0] = fmaxf(v[0], __shfl_xor_sync(0xffffffffu, v[0], 16));
+      v[0] = max_nan(v[0], __shfl_xor_sync(0xffffffffu, v[0], 16));
       if (!b2) put(row, b0 * 8 + 2 * tq + b1, v[0]);
     } else if (G2 == 1) {
 #pragma unroll
@@ -219,12 +227,47 @@ __device__ __forceinline__ void score_tiles(const uint4 (&bd)[E][2 * D / 32], co
   }
 }
 
+// The scores of a CTA that are NaN once more, term by term: where a bound is infinite
+// [q-, q+] . [lo, hi] has products 0 x infinity.  A head that still has no number counts
+// for nothing.
+template <int D>
+__device__ __noinline__ void score_again(const ScoreArgs& a, const int* s_tbl) {
+  const int i = blockIdx.z / a.Hkv, g = blockIdx.z % a.Hkv;
+  const Window w = window_of(a.bt, i);
+  const int rows = kScoreTiles * (16 / a.g2), r0 = w.b + blockIdx.y * rows, nr = min(w.e - r0, rows);
+  const int p0 = blockIdx.x * a.per, p1 = min(a.lens[i] / kBlockSize, p0 + a.per);
+  for (int p = p0 + (int)threadIdx.x; p < p1; p += kScoreThreads) {
+    const int b = s_tbl[p - p0];
+    if (b < 0) continue;
+    const __nv_bfloat16* lo = a.bounds + ((size_t)b * a.Hkv + g) * 2 * D;
+    for (int r = w.cu + r0; r < w.cu + r0 + nr; ++r) {
+      float& out = a.scores[((size_t)r * a.Hkv + g) * a.max_pages + p];
+      float best = out;
+      if (best == best) continue;
+      for (int h = 0; h < a.group; ++h) {
+        const __nv_bfloat16* q = a.q + ((size_t)r * a.Hq + g * a.group + h) * D;
+        float sum = 0.f;
+        for (int d = 0; d < D; ++d) {
+          const float x = __bfloat162float(q[d]);
+          if (x > 0.f) sum += x * __bfloat162float(lo[D + d]);
+          else if (x < 0.f) sum += x * __bfloat162float(lo[d]);
+        }
+        best = fmaxf(best, sum);
+      }
+      out = best;
+    }
+  }
+}
+
 // For a row's query head h and page t: sum_d max(q lo, q hi) = min(q, 0) . lo +
 // max(q, 0) . hi, a product of [q-, q+] with the 2 D contiguous elements [lo,
 // hi] of the page: exact bf16 factors, fp32 sums, on mma.sync m16n8k16 (16
 // virtual rows x 8 pages x 16 elements).  Virtual row v is row v / G2, head slot
 // v % G2 of it, the group's heads in the first slots and some again in the rest
-// (the maximum over the slots does not see that).  The k order of a product is
+// (the maximum over the slots does not see that).  Where a bound is infinite 0 x infinity
+// makes the sum NaN: a CTA that meets NaN takes those again, term by term (noticing it
+// costs 1 %; with the second form inside the loop, or what it saw kept in a register,
+// 6 to 15 %).  The k order of a product is
 // free, so a lane takes 16 consecutive bytes of a page's bounds as the operands
 // of two steps: the bounds go from global memory to registers without a stop, 8 E
 // pages a warp at once.  Bound by the shared-memory and L1 traffic of the operands:
@@ -238,6 +281,8 @@ __global__ void __launch_bounds__(kScoreThreads, E == 4 ? 3 : 4) score_kernel(Sc
   constexpr int kTileRows = 16 / G2;
   extern __shared__ __align__(16) uint4 s_q[];  // [tile][step][lane]
   __shared__ int s_tbl[kMaxPer];
+  __shared__ int s_odd[kScoreThreads / 32];
+  if (threadIdx.x < kScoreThreads / 32) s_odd[threadIdx.x] = 0;
   const int i = blockIdx.z / a.Hkv, g = blockIdx.z % a.Hkv;
   const Window w = window_of(a.bt, i);
   const int ctx = a.lens[i];
@@ -309,13 +354,17 @@ __global__ void __launch_bounds__(kScoreThreads, E == 4 ? 3 : 4) score_kernel(Sc
     const unsigned known = __ballot_sync(0xffffffffu, s_tbl[min(p + lane % kPages, p1 - 1) - p0] >= 0);
     constexpr int MT = E == 4 ? 1 : 2;
     int mt = 0;
+    float worst = 0.f;
     for (; mt + MT <= tiles; mt += MT)
       score_tiles<D, G2, MT, E>(bd, s_q + mt * kPairs * 64 + lane, mt * kTileRows, nr, p, p1, lane, known,
-                                out, row_step);
+                                out, row_step, worst);
     if (mt < tiles)
       score_tiles<D, G2, 1, E>(bd, s_q + mt * kPairs * 64 + lane, mt * kTileRows, nr, p, p1, lane, known,
-                               out, row_step);
+                               out, row_step, worst);
+    if (worst != worst) s_odd[warp] = 1;
   }
+  __syncthreads();
+  if (s_odd[0] | s_odd[1] | s_odd[2] | s_odd[3]) score_again<D>(a, s_tbl);
 }
 
 template <int D, int G2, int E>
