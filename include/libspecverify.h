@@ -598,9 +598,15 @@ sv_status sv_shape_logits(const sv_batch* batch, const void* logits, int32_t log
 /* ----------------------------------------------------------- page choice --
  * For requests with long contexts: which pages of the cache a draft row
  * attends.  Complete pages of request i: t = 0 .. n_i - 1, n_i = cache_lens[i]
- * / 16 (rounded down).  Every row chooses for itself, for each KV head, as it
- * would if it were decoded alone: what is verified stays the distribution that
- * a decoder without drafts samples from under the same choice.
+ * / 16 (rounded down).  Every row chooses for itself, for each KV head, by its
+ * own queries among these; the open page and the row's ancestors it sees beside
+ * them.  A row of depth j (a root's is 0) with cache_lens[i] % 16 + j < 16
+ * attends what it would if its path were committed and it were decoded alone
+ * under the same choice.  The path of any other row completes d = (cache_lens[i]
+ * % 16 + j) / 16 pages, which do not count among n_keep and n_last: the row
+ * attends all that it would alone and up to d pages more, and the distribution
+ * that is verified for it is the one over these keys, not that of a decoder
+ * without drafts.
  *
  * sv_bound_pages: bounds[b][g][0][d] = the least, [1][d] the greatest of the 16
  * keys of the page in block b, KV head g, for the complete pages t >=

@@ -44,7 +44,8 @@ class PageChoice:
     first n_first and the last n_last always, the others by score.  A step bounds the
     pages that its commit fills (run, accept_commit, commit); whoever fills the cache
     between steps (an admitted prompt) calls api.sv_bound_pages with the step's
-    ``bounds``."""
+    ``bounds``.  Pages that a row's own path completes come on top: from there on a row
+    attends somewhat more than it would if it were decoded alone."""
     n_keep: int
     n_first: int = 1
     n_last: int = 4
