@@ -790,7 +790,7 @@ inline sv_status check_prefix(const sv_paged_kv* kv, const sv_batch* bt, const s
                               int32_t Hq) {
   const sv_status st = check(kv, bt, Hq);
   if (st != SV_OK) return st;
-  if (!sp) return SV_ERR_INVALID_ARGUMENT;
+  if (!sp || sp->n_groups < 0) return SV_ERR_INVALID_ARGUMENT;
   if (bt->n_req == 0) return SV_OK;
   if (sp->n_groups < 1 || sp->n_groups > bt->n_req) return SV_ERR_INVALID_ARGUMENT;
   return SV_OK;
