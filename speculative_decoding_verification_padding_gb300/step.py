@@ -50,6 +50,13 @@ class PageChoice:
     n_first: int = 1
     n_last: int = 4
 
+    def __post_init__(self):
+        if not 1 <= self.n_keep <= 1024:
+            raise ValueError(f"n_keep must be 1 .. 1024, got {self.n_keep}")
+        if self.n_first < 0 or self.n_last < 0 or self.n_first + self.n_last > self.n_keep:
+            raise ValueError(f"n_first and n_last must be 0 or more and n_keep together at most, got "
+                             f"{self.n_first} and {self.n_last} of {self.n_keep}")
+
 
 class DeviceStep:
     def __init__(self, w: Workload, device="cuda", mode: str | None = None, chunk: int | None = None,
@@ -120,6 +127,8 @@ class DeviceStep:
         if choice is not None:
             nb, hkv, bs, d = self.kv.k_cache.shape
             pages = self.kv.block_tables.shape[1]
+            if pages > 49152:
+                raise ValueError(f"a page choice takes tables of up to 49152 blocks, got {pages}")
             self.bounds = torch.zeros((nb, hkv, 2, d), dtype=torch.bfloat16, device=dev)
             self.scores = torch.zeros((rows, hkv, pages), dtype=torch.float32, device=dev)
             self.pages = torch.full((rows, hkv, choice.n_keep), -1, dtype=torch.int32, device=dev)
