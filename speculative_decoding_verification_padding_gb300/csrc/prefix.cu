@@ -570,6 +570,11 @@ __global__ void __launch_bounds__(pfx::kThreads, 1)
                            (st > 0 || ks > 0) ? 1u : 0u);
         tc5::commit(smem_u32(&s_odone[t][st & 1]));
       }
+      // The last PV's barrier has its arrival before the next list sets it up anew (of the
+      // others the softmax waits for each phase; nothing says that two commits arrive in
+      // their order, so the one below does not stand for it).
+      if (ok)
+        ok = mbar_wait_bounded(smem_u32(&s_odone[t][(n_stage - 1) & 1]), (uint32_t)(((n_stage - 1) >> 1) & 1));
       if (!ok) s_abort = 1;
       // every product of the tile has landed before the CTA moves on
       tc5::commit(smem_u32(&s_drain[t]));
