@@ -762,7 +762,7 @@ extern "C" sv_status sv_score_pages(const sv_paged_kv* kv, const sv_batch* bt, c
   while (a.per < pg::kMaxPer && units > 8L * nsm * a.per) a.per *= 2;
   const int per_block = pg::kScoreTiles * 16 / a.g2;
   const int most_rows = std::min(bt->max_rows_per_req, bt->total_rows);
-  const dim3 grid((max_pages + a.per - 1) / a.per, (most_rows + per_block - 1) / per_block,
+  const dim3 grid((max_pages - 1) / a.per + 1, (most_rows + per_block - 1) / per_block,
                   bt->n_req * kv->n_kv_heads);
   const int tiles = std::min(pg::kScoreTiles, (most_rows * a.g2 + 15) / 16);
   const size_t smem = (size_t)tiles * (2 * kv->head_dim / 16) * 32 * 16;
