@@ -220,10 +220,10 @@ class DeviceStep:
                               self.ambiguous, self.done, self.ws, self.dev_status)
 
     def chunked_commit(self):
-        self._bound("chunked_commit", self.batch, lambda: api.bind_verify_chunked_commit(
+        self._committed(self._bound("chunked_commit", self.batch, lambda: api.bind_verify_chunked_commit(
             self.kv, self.batch, self.q, self.Hq, self.scale, self.out, self.target, self.draft,
             self.V, self.T, self.w.seed, self.chunk, self.accepted_len, self.accepted_nodes,
-            self.next_token, self.ambiguous, self.done, self.pool, self.ws, self.dev_status))()
+            self.next_token, self.ambiguous, self.done, self.pool, self.ws, self.dev_status)))
 
     def select(self):
         self._bound("select", self.batch, lambda: api.bind_select_budget(

@@ -102,3 +102,14 @@ def test_a_captured_commit():
     _forget(s)
     graph.replay()
     _check(s, before)
+
+
+def test_a_chunked_commit_in_between():
+    # a step built for one pass offers the chunked call too (over the whole context)
+    s = DeviceStep(_workload("batch64"), mode="onepass", choice=PageChoice(6, 1, 2))
+    _forget(s)
+    s.restore_cache_state()
+    before = _lens(s)
+    s.chunked_commit()
+    _check(s, before)
+    assert s.results()["dev_status"] == 0
