@@ -6,7 +6,10 @@
 //   sv_select_pages  the pages of greatest score.
 //
 // Source: [SSD] section details (PagedAttention: the page is the unit of the
-// cache); the selection itself is on none of the pages and fixed in the header.
+// cache).  The selection itself is on none of the pages and fixed in the header; that a
+// page's products are bounded by its keys' least and greatest elements is the published
+// method of Tang et al., "Quest: Query-Aware Sparsity for Efficient Long-Context LLM
+// Inference" (ICML 2024).
 
 #include <algorithm>
 
@@ -270,10 +273,12 @@ __device__ __noinline__ void score_again(const ScoreArgs& a, const int* s_tbl) {
 // 6 to 15 %).  The k order of a product is
 // free, so a lane takes 16 consecutive bytes of a page's bounds as the operands
 // of two steps: the bounds go from global memory to registers without a stop, 8 E
-// pages a warp at once.  Bound by the shared-memory and L1 traffic of the operands:
-// q is read again for every 8 E pages (264 rows of 40 heads by 48 contexts of 2000 ..
-// 60000 tokens: E = 1 73 us, 2 54, 4 49, 4.5 TB/s; small calls take E = 2, whose
-// pages are spread over more warps).
+// pages a warp at once.  q is read again from shared memory for every 8 E pages (264
+// rows of 40 heads by 48 contexts of 2000 .. 60000 tokens: E = 1 73 us, 2 54, 4 51, 4.3
+// TB/s; small calls take E = 2, whose pages are spread over more warps).  No unit is
+// full there: HBM 57 %, in an SM's active cycles the load and store path 61 %, half of
+// it shared memory, the products 41 %; 12 warps an SM do not hide the loads (4.5 of 11
+// cycles an instruction), and the SMs are active 81 % of the time.
 template <int D, int G2, int E>
 __global__ void __launch_bounds__(kScoreThreads, E == 4 ? 3 : 4) score_kernel(ScoreArgs a) {
   griddep_entry();
@@ -444,7 +449,7 @@ __device__ __forceinline__ float key_score(uint32_t k) {
 }
 
 constexpr int kCandidates = 512;
-constexpr int kMaxSelect = 49152;  // pages
+constexpr int kMaxSelect = 49152;  // pages (the call's limit; nothing here is sized by it)
 
 // One CTA a (row, KV head), its scores read from L1 in each pass (kept in shared
 // memory they left room for half as many CTAs).  The n_keep-th greatest:

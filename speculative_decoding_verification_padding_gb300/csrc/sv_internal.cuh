@@ -320,7 +320,7 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 // Spin on a phase with an iteration limit; false means the limit was hit.
-constexpr int kWaitLimit = 1 << 20;  // try_wait rounds before a wait gives up
+constexpr int kWaitLimit = 1 << 20;  // try_wait rounds before a wait gives up: 4 s, at 3.8 us each
 __device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity,
                                                   int limit = kWaitLimit) {
 #pragma unroll 1  // (unrolled, the waits of a kernel of many roles were a third of its code)
@@ -389,10 +389,11 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 }
 
 // --------------------------------------------- programmatic dependent launch --
-// Every kernel of the library starts with griddep_entry(): it waits until the
-// previous grid in the stream has completed and its writes are visible
-// (nothing is read or written before that), then lets the next grid begin
-// launching, so that launch latency overlaps the tail of this grid.
+// Every kernel of the library calls griddep_entry() before it reads or writes any
+// memory of the caller: it waits until the previous grid in the stream has completed
+// and its writes are visible, then lets the next grid begin launching, so that launch
+// latency overlaps the tail of this grid.  Most call it first; page_unit_kernel and
+// prefix_kernel take their tensor memory and set up their barriers before it.
 __device__ __forceinline__ void griddep_entry() {
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
